@@ -99,7 +99,9 @@ def draw(rng):
                           kv, d, rng.choice([0, 0, rng.randint(0, longest // 4)]))
     fp32 = rng.random() < 0.15
     d = rng.choice([32, 64]) if fp32 else d
-    longest = _spread(rng, 1, 700 if fp32 else 20001 if kind == "attn" else 8192)
+    # (a training batch in which no query sees a second key would have zero dq and dk)
+    fewest = 1 if kind == "attn" else 16
+    longest = _spread(rng, fewest, 700 if fp32 else 20001 if kind == "attn" else 8192)
     pairs = 4e7 if fp32 else 8 * 20001**2 if kind == "attn" else 16 * 8192**2
     batch = max(1, min(_spread(rng, 1, 64), int(pairs * 64 / (heads * longest**2 * d))))
     while heads * longest**2 * d > pairs * 64:
@@ -107,7 +109,7 @@ def draw(rng):
     bidir = rng.random() < 0.25
     return attn_case(kind, batch, longest, rng.randint((longest + 1) // 2, longest), heads, kv, d,
                      special=rng.choice([0, 16, 64]), cand=rng.choice([0, 1, rng.randint(0, longest // 8 + 1)]),
-                     window=0 if bidir or rng.random() < 0.6 else _spread(rng, 1, 512), bidir=bidir,
+                     window=0 if bidir or rng.random() < 0.6 else _spread(rng, 1 if kind == "attn" else 4, 512), bidir=bidir,
                      rope=rng.random() < 0.7, dtype="fp32" if fp32 else "bf16")
 
 
