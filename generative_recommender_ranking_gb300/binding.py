@@ -191,6 +191,25 @@ def rec_attn_plan_query_pruned(params: RecAttnParams, keep_user_queries: int, of
     return Plan(h.value, B, int(off_h[-1]) if B > 0 else 0, (offsets_dev, timestamps_dev, types_dev))
 
 
+def rec_attn_plan_grouped(params: RecAttnParams, num_kv_heads: int, offsets_host, offsets_dev, timestamps_dev,
+                          types_dev, keep_user_queries: int = -1, stream=None) -> Plan:
+    """rec_attn_plan (keep_user_queries >= 0: rec_attn_plan_query_pruned) for query heads
+    that share num_kv_heads key/value heads: k, v, dk, dv of every call on the plan are
+    [T, num_kv_heads, d]."""
+    L = lib()
+    vp = ctypes.c_void_p
+    L.rec_attn_plan_grouped.argtypes = [ctypes.POINTER(RecAttnParams), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                        vp, vp, vp, vp, vp, ctypes.POINTER(vp)]
+    L.rec_attn_plan_grouped.restype = ctypes.c_int
+    off_h = np.ascontiguousarray(np.asarray(offsets_host, dtype=np.int64))
+    B = len(off_h) - 1
+    h = vp()
+    _check("rec_attn_plan_grouped", L.rec_attn_plan_grouped(
+        ctypes.byref(params), int(num_kv_heads), int(keep_user_queries), B, _ptr(off_h), _ptr(offsets_dev),
+        _ptr(timestamps_dev), _ptr(types_dev), _stream(stream), ctypes.byref(h)))
+    return Plan(h.value, B, int(off_h[-1]) if B > 0 else 0, (offsets_dev, timestamps_dev, types_dev))
+
+
 def rec_attn_query_keep(hist_len: int, n_min: int, layer: int, n_layers: int) -> int:
     """LazFormer Eq. 22 per-layer query budget (host-only)."""
     return int(lib().rec_attn_query_keep(int(hist_len), int(n_min), int(layer), int(n_layers)))
@@ -280,6 +299,63 @@ def rec_attn_compress(offsets_host, hist_begin, hist_len, segments, x, timestamp
     _check("rec_attn_compress", code)
 
 
+def _rows(fn: str, x, **others):
+    """(dtype, rows, width) of a contiguous [rows, width] tensor; the others must match it."""
+    import torch
+    dtypes = {torch.bfloat16: BF16, torch.float32: FP32}
+    ok = x.dim() == 2 and x.dtype in dtypes and x.is_contiguous()
+    for o in others.values():
+        ok = ok and o.dtype == x.dtype and o.shape == x.shape and o.device == x.device and o.is_contiguous()
+    if not ok:
+        raise RecAttnError(fn, ERR_INVALID_ARG)
+    return dtypes[x.dtype], x.shape[0], x.shape[1]
+
+
+def _gains(fn: str, x, types, **gains):
+    """The gains and their gradients: contiguous float32 [4 (by type) or 1, width]."""
+    import torch
+    groups = 4 if types is not None else 1
+    shape = (groups, x.shape[1])
+    ok = types is None or (types.dtype == torch.int8 and types.shape == (x.shape[0],) and types.is_contiguous()
+                           and types.device == x.device)
+    for g in gains.values():
+        ok = ok and (g is None or (g.dtype == torch.float32 and tuple(g.shape) == shape and g.is_contiguous()
+                                   and g.device == x.device))
+    if not ok:
+        raise RecAttnError(fn, ERR_INVALID_ARG)
+    return groups
+
+
+def rec_attn_layernorm_fwd(x, weight, bias, y, types=None, eps: float = 1e-5, stream=None) -> None:
+    """Layer norm of rows x [rows, width] (bf16 or float32) into y; weight and bias float32
+    [1, width], or [4, width] with types int8 [rows]: a gain and bias per token type."""
+    L = lib()
+    vp, i64 = ctypes.c_void_p, ctypes.c_int64
+    L.rec_attn_layernorm_fwd.argtypes = [ctypes.c_int32, i64, i64, ctypes.c_int32, vp, vp, vp, vp, ctypes.c_float, vp, vp]
+    L.rec_attn_layernorm_fwd.restype = ctypes.c_int
+    dtype, rows, width = _rows("rec_attn_layernorm_fwd", x, y=y)
+    groups = _gains("rec_attn_layernorm_fwd", x, types, weight=weight, bias=bias)
+    _check("rec_attn_layernorm_fwd", L.rec_attn_layernorm_fwd(dtype, rows, width, groups, _ptr(x), _ptr(types),
+                                                              _ptr(weight), _ptr(bias), float(eps), _ptr(y),
+                                                              _stream(stream)))
+
+
+def rec_attn_layernorm_bwd(x, weight, dy, dx, dweight=None, dbias=None, types=None, eps: float = 1e-5,
+                           stream=None) -> None:
+    """Gradients of rec_attn_layernorm_fwd for the upstream gradient dy: dx, and dweight and
+    dbias (float32, shaped as weight; None: not wanted), overwritten."""
+    L = lib()
+    vp, i64 = ctypes.c_void_p, ctypes.c_int64
+    L.rec_attn_layernorm_bwd.argtypes = [ctypes.c_int32, i64, i64, ctypes.c_int32, vp, vp, vp, ctypes.c_float, vp, vp,
+                                         vp, vp, vp]
+    L.rec_attn_layernorm_bwd.restype = ctypes.c_int
+    dtype, rows, width = _rows("rec_attn_layernorm_bwd", x, dy=dy, dx=dx)
+    groups = _gains("rec_attn_layernorm_bwd", x, types, weight=weight, dweight=dweight, dbias=dbias)
+    _check("rec_attn_layernorm_bwd", L.rec_attn_layernorm_bwd(dtype, rows, width, groups, _ptr(x), _ptr(types),
+                                                              _ptr(weight), float(eps), _ptr(dy), _ptr(dx),
+                                                              _ptr(dweight), _ptr(dbias), _stream(stream)))
+
+
 def rec_attn_fwd_compress(plan: Plan, q, k, v, hist_begin, hist_len, segments, x_out, t_out, ty_out,
                           stream=None) -> None:
     """Attention forward whose output is written already history-compressed
@@ -354,6 +430,23 @@ def rec_attn_cache_create(params: RecAttnParams, hist_offsets_host, hist_t, hist
     _check("rec_attn_cache_create", L.rec_attn_cache_create(
         ctypes.byref(params), len(off) - 1, _ptr(off), _ptr(hist_t), _ptr(hist_types), _ptr(k_hist), _ptr(v_hist),
         int(max_cands), _stream(stream), ctypes.byref(h)))
+    return KVCache(h.value, len(off) - 1, int(max_cands))
+
+
+def rec_attn_cache_create_grouped(params: RecAttnParams, num_kv_heads: int, hist_offsets_host, hist_t, hist_types,
+                                  k_hist, v_hist, max_cands: int, stream=None) -> KVCache:
+    """rec_attn_cache_create for query heads that share num_kv_heads key/value heads:
+    k_hist, v_hist [Th, num_kv_heads, d], and the candidates' keys and values alike."""
+    L = lib()
+    vp = ctypes.c_void_p
+    L.rec_attn_cache_create_grouped.argtypes = [ctypes.POINTER(RecAttnParams), ctypes.c_int32, ctypes.c_int32, vp, vp,
+                                                vp, vp, vp, ctypes.c_int32, vp, ctypes.POINTER(vp)]
+    L.rec_attn_cache_create_grouped.restype = ctypes.c_int
+    off = np.ascontiguousarray(np.asarray(hist_offsets_host, dtype=np.int64))
+    h = vp()
+    _check("rec_attn_cache_create_grouped", L.rec_attn_cache_create_grouped(
+        ctypes.byref(params), int(num_kv_heads), len(off) - 1, _ptr(off), _ptr(hist_t), _ptr(hist_types),
+        _ptr(k_hist), _ptr(v_hist), int(max_cands), _stream(stream), ctypes.byref(h)))
     return KVCache(h.value, len(off) - 1, int(max_cands))
 
 

@@ -24,6 +24,7 @@ using namespace recattn;
 
 struct rec_attn_plan_s {
   rec_attn_params p;
+  int32_t kv_heads = 0;  // key/value heads; p.num_heads / kv_heads query heads share one
   int device = 0;
   int num_sms = 0;
   int32_t batch = 0;
@@ -206,13 +207,15 @@ REC_ATTN_API const char* rec_attn_status_string(rec_attn_status s) {
 
 namespace {
 
-rec_attn_status plan_impl(const rec_attn_params* params, int32_t keep_user_queries, int32_t batch,
+// kv_heads: key/value heads (params->num_heads: one per query head).
+rec_attn_status plan_impl(const rec_attn_params* params, int32_t kv_heads, int32_t keep_user_queries, int32_t batch,
                           const int64_t* offsets_host, const int64_t* offsets_dev, const int64_t* timestamps_dev,
                           const int8_t* types_dev, void* stream, rec_attn_plan_t** plan_out) {
   if (!plan_out) return REC_ATTN_ERR_INVALID_ARG;
   *plan_out = nullptr;
   rec_attn_status st = check_params(params);
   if (st != REC_ATTN_OK) return st;
+  if (kv_heads < 1 || params->num_heads % kv_heads != 0) return REC_ATTN_ERR_INVALID_ARG;
   if (batch < 0 || (batch > 0 && !offsets_host)) return REC_ATTN_ERR_INVALID_ARG;
   std::vector<ReqMeta> meta((size_t)batch);
   long long NT = 0, NC = 0, T = 0;
@@ -239,6 +242,7 @@ rec_attn_status plan_impl(const rec_attn_params* params, int32_t keep_user_queri
   rec_attn_plan_s* plan = new (std::nothrow) rec_attn_plan_s();
   if (!plan) return REC_ATTN_ERR_OOM;
   plan->p = *params;
+  plan->kv_heads = kv_heads;
   if (plan->p.softmax_scale == 0.f) plan->p.softmax_scale = 1.f / std::sqrt((float)params->head_dim);
   plan->batch = batch;
   plan->T = T; plan->NT = NT; plan->NC = NC;
@@ -269,9 +273,10 @@ rec_attn_status plan_impl(const rec_attn_params* params, int32_t keep_user_queri
 
   // workspace layout
   const size_t elem = params->dtype == REC_ATTN_BF16 ? 2 : 4;
-  const size_t qk_bytes = (size_t)T * params->num_heads * params->head_dim * elem;
-  const WsLayout lay = ws_layout(batch, NT, NC, params->num_heads, params->use_rope ? qk_bytes : 0,
-                                 mask_capacity(NT, NC));
+  const size_t row_bytes = (size_t)T * params->head_dim * elem;  // one head's rows
+  const WsLayout lay = ws_layout(batch, NT, NC, params->num_heads,
+                                 params->use_rope ? row_bytes * params->num_heads : 0,
+                                 params->use_rope ? row_bytes * kv_heads : 0, mask_capacity(NT, NC));
   plan->ws_bytes = lay.total;
 
   cudaMemPool_t pool;
@@ -331,7 +336,8 @@ REC_ATTN_API rec_attn_status rec_attn_plan(const rec_attn_params* params, int32_
                                            const int64_t* offsets_host, const int64_t* offsets_dev,
                                            const int64_t* timestamps_dev, const int8_t* types_dev, void* stream,
                                            rec_attn_plan_t** plan_out) {
-  return plan_impl(params, -1, batch, offsets_host, offsets_dev, timestamps_dev, types_dev, stream, plan_out);
+  return plan_impl(params, params ? params->num_heads : 0, -1, batch, offsets_host, offsets_dev, timestamps_dev,
+                   types_dev, stream, plan_out);
 }
 
 REC_ATTN_API rec_attn_status rec_attn_plan_query_pruned(const rec_attn_params* params, int32_t keep_user_queries,
@@ -341,8 +347,19 @@ REC_ATTN_API rec_attn_status rec_attn_plan_query_pruned(const rec_attn_params* p
                                                         rec_attn_plan_t** plan_out) {
   if (plan_out) *plan_out = nullptr;
   if (keep_user_queries < -1) return REC_ATTN_ERR_INVALID_ARG;
-  return plan_impl(params, keep_user_queries, batch, offsets_host, offsets_dev, timestamps_dev, types_dev, stream,
-                   plan_out);
+  return plan_impl(params, params ? params->num_heads : 0, keep_user_queries, batch, offsets_host, offsets_dev,
+                   timestamps_dev, types_dev, stream, plan_out);
+}
+
+REC_ATTN_API rec_attn_status rec_attn_plan_grouped(const rec_attn_params* params, int32_t num_kv_heads,
+                                                   int32_t keep_user_queries, int32_t batch,
+                                                   const int64_t* offsets_host, const int64_t* offsets_dev,
+                                                   const int64_t* timestamps_dev, const int8_t* types_dev,
+                                                   void* stream, rec_attn_plan_t** plan_out) {
+  if (plan_out) *plan_out = nullptr;
+  if (keep_user_queries < -1) return REC_ATTN_ERR_INVALID_ARG;
+  return plan_impl(params, num_kv_heads, keep_user_queries, batch, offsets_host, offsets_dev, timestamps_dev,
+                   types_dev, stream, plan_out);
 }
 
 REC_ATTN_API int64_t rec_attn_query_keep(int64_t hist_len, int64_t n_min, int32_t layer, int32_t n_layers) {
@@ -357,6 +374,37 @@ REC_ATTN_API int64_t rec_attn_query_keep(int64_t hist_len, int64_t n_min, int32_
 }
 
 namespace {
+
+// Bytes of the plan's [T][H][d] (Q, O) and [T][kv heads][d] (K, V) tensors.
+size_t q_bytes(const rec_attn_plan_s* plan) {
+  return (size_t)plan->T * plan->p.num_heads * plan->p.head_dim * (plan->p.dtype == REC_ATTN_BF16 ? 2 : 4);
+}
+size_t kv_bytes(const rec_attn_plan_s* plan) { return q_bytes(plan) / (plan->p.num_heads / plan->kv_heads); }
+
+// The prologue's arguments for the plan's rows (Q' and K' into the plan's buffers).
+RopeArgs rope_args(const rec_attn_plan_s* plan, const void* q, const void* k) {
+  RopeArgs ra;
+  ra.meta = plan->pd.meta; ra.tile_req = plan->pd.treq; ra.batch = plan->batch; ra.t = plan->t;
+  ra.ty = plan->ty; ra.skip_user_q = 0;
+  ra.q = q; ra.k = k; ra.qr = plan->qrot; ra.kr = plan->krot;
+  ra.heads = plan->p.num_heads; ra.kv_heads = plan->kv_heads; ra.head_dim = plan->p.head_dim;
+  std::memcpy(ra.omega, plan->omega, sizeof ra.omega);  // all zero without the RoPE
+  return ra;
+}
+
+// Q'/K' buffers for a plan made without the RoPE, on its first fused call.
+cudaError_t make_qk_extra(rec_attn_plan_s* plan, cudaStream_t st) {
+  if (!plan->qk_extra) {
+    const size_t rows_q = ws_up(q_bytes(plan));
+    cudaMemPool_t pool;
+    cudaError_t e = pool_for(plan->device, &pool);
+    if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&plan->qk_extra, rows_q + ws_up(kv_bytes(plan)), pool, st);
+    if (e != cudaSuccess) { plan->qk_extra = nullptr; return e; }
+    plan->krot = static_cast<char*>(plan->qk_extra) + rows_q;
+  }
+  plan->qrot = plan->qk_extra;
+  return cudaSuccess;
+}
 
 // The forward of rec_attn_fwd and rec_attn_fwd_fused (f == nullptr: no fused step).
 // cmp: the history compression epilogue (the output goes to cmp->x_out, checked by the
@@ -378,9 +426,8 @@ rec_attn_status fwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
     for (const void* x : ptrs)
       if (reinterpret_cast<uintptr_t>(x) & 15u) return REC_ATTN_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(lse) & 3u) return REC_ATTN_ERR_INVALID_ARG;
-    const size_t elem = p.dtype == REC_ATTN_BF16 ? 2 : 4;
-    const size_t bytes = (size_t)T * p.num_heads * p.head_dim * elem;
-    if (overlaps(out, bytes, q, bytes) || overlaps(out, bytes, k, bytes) || overlaps(out, bytes, v, bytes))
+    const size_t bytes = q_bytes(plan), kvb = kv_bytes(plan);
+    if (overlaps(out, bytes, q, bytes) || overlaps(out, bytes, k, kvb) || overlaps(out, bytes, v, kvb))
       return REC_ATTN_ERR_INVALID_ARG;
     if (lse && (overlaps(lse, (size_t)T * p.num_heads * 4, out, bytes)))
       return REC_ATTN_ERR_INVALID_ARG;
@@ -409,16 +456,8 @@ rec_attn_status fwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   if (fuse_qk) {
     // fused QK-RMSNorm / gates, then the rotation (if the plan has one), into Q'/K'
     if (!plan->qrot) {
-      if (!plan->qk_extra) {
-        const size_t elem = p.dtype == REC_ATTN_BF16 ? 2 : 4;
-        const size_t qk_bytes = ((size_t)T * p.num_heads * p.head_dim * elem + 255) & ~(size_t)255;
-        cudaMemPool_t pool;
-        e = pool_for(plan->device, &pool);
-        if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&plan->qk_extra, 2 * qk_bytes, pool, st);
-        if (e != cudaSuccess) { plan->qk_extra = nullptr; return from_cuda(e); }
-        plan->krot = static_cast<char*>(plan->qk_extra) + qk_bytes;
-      }
-      plan->qrot = plan->qk_extra;
+      e = make_qk_extra(plan, st);
+      if (e != cudaSuccess) return from_cuda(e);
     }
     e = cudaStreamWaitEvent(st, plan->ev_meta, 0);
     if (e == cudaSuccess && plan->timing) {
@@ -426,12 +465,7 @@ rec_attn_status fwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
       e = cudaEventRecord(plan->ev[0], st);
     }
     if (e != cudaSuccess) return from_cuda(e);
-    RopeArgs ra;
-    ra.meta = plan->pd.meta; ra.tile_req = plan->pd.treq; ra.batch = plan->batch; ra.t = plan->t;
-    ra.ty = plan->ty; ra.skip_user_q = 0;
-    ra.q = q; ra.k = k; ra.qr = plan->qrot; ra.kr = plan->krot;
-    ra.heads = p.num_heads; ra.head_dim = p.head_dim;
-    std::memcpy(ra.omega, plan->omega, sizeof ra.omega);  // all zero without the RoPE
+    const RopeArgs ra = rope_args(plan, q, k);
     FusedArgs fa;
     fa.q_norm_w = f->q_norm_weight; fa.k_norm_w = f->k_norm_weight; fa.eps = f->norm_eps;
     fa.q_gate = f->q_gate; fa.k_gate = f->k_gate;
@@ -446,12 +480,7 @@ rec_attn_status fwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
       e = cudaEventRecord(plan->ev[0], st);
     }
     if (e != cudaSuccess) return from_cuda(e);
-    RopeArgs ra;
-    ra.meta = plan->pd.meta; ra.tile_req = plan->pd.treq; ra.batch = plan->batch; ra.t = plan->t;
-    ra.ty = plan->ty; ra.skip_user_q = 0;
-    ra.q = q; ra.k = k; ra.qr = plan->qrot; ra.kr = plan->krot;
-    ra.heads = p.num_heads; ra.head_dim = p.head_dim;
-    std::memcpy(ra.omega, plan->omega, sizeof ra.omega);
+    RopeArgs ra = rope_args(plan, q, k);
     ra.skip_user_q = plan->mask.keep_user == 0 ? 1 : 0;  // target attention: no user token queries
     e = launch_rope(ra, p.dtype, plan->NT, st);
     if (e == cudaSuccess && plan->timing) e = cudaEventRecord(plan->ev[1], st);
@@ -476,7 +505,8 @@ rec_attn_status fwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   a.kslot = plan->pd.kslot; a.mtab = plan->pd.mtab;
   a.q = qs; a.k = ks; a.v = v; a.out = out; a.lse = lse; a.status = plan->pd.status;
   a.out_gate = f ? f->out_gate : nullptr;
-  a.n_items = plan->NT * p.num_heads; a.heads = p.num_heads; a.scale = p.softmax_scale; a.mask = plan->mask;
+  a.n_items = plan->NT * p.num_heads; a.heads = p.num_heads; a.group = p.num_heads / plan->kv_heads;
+  a.scale = p.softmax_scale; a.mask = plan->mask;
   if (cmp) a.cmp = *cmp;
   a.long_items = long_items(p, plan->batch, plan->NT);
   if (p.dtype == REC_ATTN_FP32) {
@@ -484,9 +514,9 @@ rec_attn_status fwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
     return finish_timing(plan, st, e);
   }
   const void* srcs[3] = {qs, ks, v};
-  const long long cols = (long long)p.num_heads * p.head_dim;
   for (int i = 0; i < 3; ++i) {
     if (plan->map_src[i] != srcs[i]) {
+      const long long cols = (long long)(i == 0 ? p.num_heads : plan->kv_heads) * p.head_dim;
       if (!encode_map(&plan->maps[i], srcs[i], T, cols)) { plan->map_src[i] = nullptr; return REC_ATTN_ERR_CUDA; }
       plan->map_src[i] = srcs[i];
     }
@@ -531,16 +561,16 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
     for (const void* x : ptrs)
       if (!x || (reinterpret_cast<uintptr_t>(x) & 15u)) return REC_ATTN_ERR_INVALID_ARG;
     if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u)) return REC_ATTN_ERR_INVALID_ARG;
-    const size_t elem = p.dtype == REC_ATTN_BF16 ? 2 : 4;
-    const size_t bytes = (size_t)T * p.num_heads * p.head_dim * elem;
+    const size_t bytes = q_bytes(plan), kvb = kv_bytes(plan);
     const void* ins[6] = {q, k, v, out, dout, lse};
-    const size_t in_bytes[6] = {bytes, bytes, bytes, bytes, bytes, (size_t)T * p.num_heads * 4};
+    const size_t in_bytes[6] = {bytes, kvb, kvb, bytes, bytes, (size_t)T * p.num_heads * 4};
     void* outs[3] = {dq, dk, dv};
+    const size_t out_bytes[3] = {bytes, kvb, kvb};
     for (int o = 0; o < 3; ++o) {
       for (int i = 0; i < 6; ++i)
-        if (overlaps(outs[o], bytes, ins[i], in_bytes[i])) return REC_ATTN_ERR_INVALID_ARG;
+        if (overlaps(outs[o], out_bytes[o], ins[i], in_bytes[i])) return REC_ATTN_ERR_INVALID_ARG;
       for (int o2 = o + 1; o2 < 3; ++o2)
-        if (overlaps(outs[o], bytes, outs[o2], bytes)) return REC_ATTN_ERR_INVALID_ARG;
+        if (overlaps(outs[o], out_bytes[o], outs[o2], out_bytes[o2])) return REC_ATTN_ERR_INVALID_ARG;
     }
   }
   int dev = -1;
@@ -551,14 +581,18 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   plan->stream = st;
   if (T == 0) return REC_ATTN_OK;
   const bool tc = p.dtype == REC_ATTN_BF16;
-  const long long n_items = plan->NT * p.num_heads;
-  // bf16 workspace: descriptors [2][n_items] | row constants [H][NT][128] | lists [NC] |
-  // their mask-table slots [NC] | the mask table's columns [mcap][128][4]
-  const size_t off_rowc = (size_t)2 * n_items * sizeof(BwdItemDesc);
+  const long long n_items = plan->NT * p.num_heads, n_kv_items = plan->NT * plan->kv_heads;
+  const int group = p.num_heads / plan->kv_heads;
+  // bf16 workspace: descriptors [n_items], [n_kv_items] | row constants [H][NT][128] | lists [NC] |
+  // their mask-table slots [NC] | the mask table's columns [mcap][128][4] | with shared heads
+  // the dK/dV items' order [n_kv_items]
+  const size_t off_rowc = (size_t)(n_items + n_kv_items) * sizeof(BwdItemDesc);
   const size_t off_ql = off_rowc + (size_t)plan->NT * p.num_heads * kTile * sizeof(float2);
   const size_t off_qs = off_ql + (((size_t)plan->NC * sizeof(uint32_t) + 15) & ~(size_t)15);
   const size_t off_ct = off_qs + (((size_t)plan->NC * sizeof(int) + 15) & ~(size_t)15);
-  const size_t ws_bytes = tc ? off_ct + (size_t)plan->pd.mcap * kTile * 16 : (size_t)T * p.num_heads * sizeof(float);
+  const size_t off_ki = off_ct + (size_t)plan->pd.mcap * kTile * 16;
+  const size_t ws_bytes = tc ? off_ki + (group > 1 ? (size_t)n_kv_items * sizeof(int) : 0)
+                             : (size_t)T * p.num_heads * sizeof(float);
   if (!plan->bwd_ws) {
     cudaMemPool_t pool;
     e = pool_for(plan->device, &pool);
@@ -570,37 +604,19 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   const void* ks = k;
   if (fa) {  // the fused steps and the rotation again, into the plan's Q'/K' buffers
     if (!plan->qrot) {
-      if (!plan->qk_extra) {
-        const size_t elem = p.dtype == REC_ATTN_BF16 ? 2 : 4;
-        const size_t qk_bytes = ((size_t)T * p.num_heads * p.head_dim * elem + 255) & ~(size_t)255;
-        cudaMemPool_t pool;
-        e = pool_for(plan->device, &pool);
-        if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&plan->qk_extra, 2 * qk_bytes, pool, st);
-        if (e != cudaSuccess) { plan->qk_extra = nullptr; return from_cuda(e); }
-        plan->krot = static_cast<char*>(plan->qk_extra) + qk_bytes;
-      }
-      plan->qrot = plan->qk_extra;
+      e = make_qk_extra(plan, st);
+      if (e != cudaSuccess) return from_cuda(e);
     }
     e = cudaStreamWaitEvent(st, plan->ev_meta, 0);
     if (e != cudaSuccess) return from_cuda(e);
-    RopeArgs ra;
-    ra.meta = plan->pd.meta; ra.tile_req = plan->pd.treq; ra.batch = plan->batch; ra.t = plan->t;
-    ra.ty = plan->ty; ra.skip_user_q = 0;
-    ra.q = q; ra.k = k; ra.qr = plan->qrot; ra.kr = plan->krot;
-    ra.heads = p.num_heads; ra.head_dim = p.head_dim;
-    std::memcpy(ra.omega, plan->omega, sizeof ra.omega);  // all zero without the RoPE
+    const RopeArgs ra = rope_args(plan, q, k);
     e = launch_rope_fused(ra, *fa, p.dtype, plan->NT, st);
     if (e != cudaSuccess) return from_cuda(e);
     qs = plan->qrot; ks = plan->krot;
   } else if (p.use_rope) {  // Q' and K' again, into the plan's workspace
     e = cudaStreamWaitEvent(st, plan->ev_meta, 0);
     if (e != cudaSuccess) return from_cuda(e);
-    RopeArgs ra;
-    ra.meta = plan->pd.meta; ra.tile_req = plan->pd.treq; ra.batch = plan->batch; ra.t = plan->t;
-    ra.ty = plan->ty; ra.skip_user_q = 0;
-    ra.q = q; ra.k = k; ra.qr = plan->qrot; ra.kr = plan->krot;
-    ra.heads = p.num_heads; ra.head_dim = p.head_dim;
-    std::memcpy(ra.omega, plan->omega, sizeof ra.omega);
+    const RopeArgs ra = rope_args(plan, q, k);
     e = launch_rope(ra, p.dtype, plan->NT, st);
     if (e != cudaSuccess) return from_cuda(e);
     qs = plan->qrot; ks = plan->krot;
@@ -611,7 +627,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   a.meta = plan->pd.meta; a.batch = plan->batch; a.kcount = plan->pd.kcount; a.klist = plan->pd.klist;
   a.qkeep = plan->pd.qkeep;
   a.items = plan->pd.items; a.qreq = plan->pd.qreq; a.krec = plan->pd.krec;
-  a.n_items = plan->NT * p.num_heads;
+  a.n_items = n_items; a.n_kv_items = n_kv_items;
   a.status = plan->pd.status;
   a.counters = plan->pd.counters;
   a.cls = plan->pd.cls; a.t = plan->t; a.ty = plan->ty;
@@ -625,7 +641,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   a.qslot = tc ? reinterpret_cast<const int*>(bws + off_qs) : nullptr;
   a.ctab = tc ? reinterpret_cast<const uint32_t*>(bws + off_ct) : nullptr;
   a.dq = dq; a.dk = dk; a.dv = dv;
-  a.rows = T * p.num_heads; a.heads = p.num_heads; a.scale = p.softmax_scale;
+  a.rows = T * p.num_heads; a.heads = p.num_heads; a.group = group; a.scale = p.softmax_scale;
   a.rotate = p.use_rope; a.mask = plan->mask;
   std::memcpy(a.omega, plan->omega, sizeof a.omega);
   if (!tc) {
@@ -636,7 +652,8 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   if (!plan->bwd_sched) {  // the plan's masks never change: its backward schedule is built once
     BwdSchedArgs sa;
     sa.meta = plan->pd.meta; sa.qreq = plan->pd.qreq; sa.items = plan->pd.items; sa.kcount = plan->pd.kcount;
-    sa.cls = plan->pd.cls; sa.t = plan->t; sa.n_tiles = plan->NT; sa.n_items = n_items; sa.heads = p.num_heads;
+    sa.cls = plan->pd.cls; sa.t = plan->t; sa.n_tiles = plan->NT; sa.n_items = n_items; sa.n_kv_items = n_kv_items;
+    sa.heads = p.num_heads; sa.group = group; sa.kv_items = reinterpret_cast<int*>(bws + off_ki);
     sa.desc = reinterpret_cast<BwdItemDesc*>(bws);
     sa.qlist = reinterpret_cast<uint32_t*>(bws + off_ql);
     sa.pslot = plan->pd.pslot; sa.qslot = reinterpret_cast<int*>(bws + off_qs);
@@ -648,9 +665,9 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   }
   CUtensorMap maps[4];  // Q', K', V, the attention's dO
   const void* srcs[4] = {qs, ks, v, dout_attn};
-  const long long cols = (long long)p.num_heads * p.head_dim;
+  const int map_heads[4] = {p.num_heads, plan->kv_heads, plan->kv_heads, p.num_heads};
   for (int i = 0; i < 4; ++i)
-    if (!encode_map(&maps[i], srcs[i], T, cols)) return REC_ATTN_ERR_CUDA;
+    if (!encode_map(&maps[i], srcs[i], T, (long long)map_heads[i] * p.head_dim)) return REC_ATTN_ERR_CUDA;
   return from_cuda(launch_attn_bwd_tc(a, maps, p.head_dim, plan->num_sms, st));
 }
 
@@ -676,8 +693,7 @@ REC_ATTN_API rec_attn_status rec_attn_bwd_fused(rec_attn_plan_t* plan, const voi
       (fused->out_gate && !grads->dout_gate) || (fused->q_norm_weight && !grads->dq_norm_weight) ||
       (fused->k_norm_weight && !grads->dk_norm_weight))
     return REC_ATTN_ERR_INVALID_ARG;
-  const size_t elem = p.dtype == REC_ATTN_BF16 ? 2 : 4;
-  const size_t bytes = (size_t)T * p.num_heads * p.head_dim * elem;
+  const size_t bytes = q_bytes(plan), kvb = kv_bytes(plan);
   if (T > 0) {
     const void* al16[6] = {fused->q_gate, fused->k_gate, fused->out_gate, grads->dq_gate, grads->dk_gate,
                            grads->dout_gate};
@@ -687,10 +703,13 @@ REC_ATTN_API rec_attn_status rec_attn_bwd_fused(rec_attn_plan_t* plan, const voi
     for (const void* x : al4)
       if (reinterpret_cast<uintptr_t>(x) & 3u) return REC_ATTN_ERR_INVALID_ARG;
     void* gouts[3] = {grads->dq_gate, grads->dk_gate, grads->dout_gate};
+    const size_t gout_bytes[3] = {bytes, kvb, bytes};
     const void* gins[8] = {q, k, v, out, dout, fused->q_gate, fused->k_gate, fused->out_gate};
-    for (void* g : gouts)
-      for (const void* x : gins)
-        if (g && x && overlaps(g, bytes, x, bytes)) return REC_ATTN_ERR_INVALID_ARG;
+    const size_t gin_bytes[8] = {bytes, kvb, kvb, bytes, bytes, bytes, kvb, bytes};
+    for (int o = 0; o < 3; ++o)
+      for (int i = 0; i < 8; ++i)
+        if (gouts[o] && gins[i] && overlaps(gouts[o], gout_bytes[o], gins[i], gin_bytes[i]))
+          return REC_ATTN_ERR_INVALID_ARG;
   }
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -727,7 +746,7 @@ REC_ATTN_API rec_attn_status rec_attn_bwd_fused(rec_attn_plan_t* plan, const voi
   for (int side = 0; side < 2 && e == cudaSuccess && s == REC_ATTN_OK; ++side) {
     if (!(side == 0 ? qside : kside)) continue;
     NormGateArgs na{};
-    na.rows = T; na.heads = p.num_heads; na.head_dim = p.head_dim; na.eps = fused->norm_eps;
+    na.rows = T; na.heads = side == 0 ? p.num_heads : plan->kv_heads; na.head_dim = p.head_dim; na.eps = fused->norm_eps;
     na.a = side == 0 ? q : k;
     na.w = side == 0 ? fused->q_norm_weight : fused->k_norm_weight;
     na.gate = side == 0 ? fused->q_gate : fused->k_gate;
@@ -735,7 +754,7 @@ REC_ATTN_API rec_attn_status rec_attn_bwd_fused(rec_attn_plan_t* plan, const voi
     na.da = side == 0 ? dq : dk;
     na.dgate = side == 0 ? grads->dq_gate : grads->dk_gate;
     na.dw = side == 0 ? grads->dq_norm_weight : grads->dk_norm_weight;
-    if (na.dw) e = cudaMemsetAsync(na.dw, 0, sizeof(float) * (size_t)p.num_heads * p.head_dim, st);
+    if (na.dw) e = cudaMemsetAsync(na.dw, 0, sizeof(float) * (size_t)na.heads * p.head_dim, st);
     if (e == cudaSuccess) e = launch_bwd_norm_gate(na, p.dtype, st);
   }
   if (scratch) {
@@ -847,6 +866,102 @@ REC_ATTN_API rec_attn_status rec_attn_compress(int32_t batch, const int64_t* off
   return from_cuda(e != cudaSuccess ? e : e2);
 }
 
+namespace {
+
+constexpr int kMaxNormWidth = 16384;
+
+bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// The checks both directions of the layer norm share.
+rec_attn_status check_norm(int32_t dtype, int64_t rows, int64_t width, int32_t groups, const void* types, float eps) {
+  if (dtype != REC_ATTN_BF16 && dtype != REC_ATTN_FP32) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows < 0 || width < 1 || (width * (dtype == REC_ATTN_BF16 ? 2 : 4)) % 16 != 0) return REC_ATTN_ERR_INVALID_ARG;
+  if (!(std::isfinite(eps) && eps >= 0.f)) return REC_ATTN_ERR_INVALID_ARG;
+  if ((groups != 1 && groups != kTypes) || (groups == 1 && types) || (groups > 1 && rows > 0 && !types))
+    return REC_ATTN_ERR_INVALID_ARG;
+  if (width > kMaxNormWidth || rows >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
+  return REC_ATTN_OK;
+}
+
+cudaError_t device_and_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  return e;
+}
+
+}  // namespace
+
+REC_ATTN_API rec_attn_status rec_attn_layernorm_fwd(int32_t dtype, int64_t rows, int64_t width, int32_t num_groups,
+                                                    const void* x, const int8_t* types, const float* weight,
+                                                    const float* bias, float eps, void* y, void* stream) {
+  const rec_attn_status s = check_norm(dtype, rows, width, num_groups, types, eps);
+  if (s != REC_ATTN_OK) return s;
+  if (rows == 0) return REC_ATTN_OK;
+  if (!x || !weight || !y || misaligned16(x) || misaligned16(weight) || misaligned16(bias) || misaligned16(y))
+    return REC_ATTN_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)rows * width * (dtype == REC_ATTN_BF16 ? 2 : 4);
+  const size_t gain = (size_t)num_groups * width * sizeof(float);
+  if ((y != x && overlaps(y, bytes, x, bytes)) || overlaps(y, bytes, weight, gain) ||
+      (bias && overlaps(y, bytes, bias, gain)) || (types && overlaps(y, bytes, types, (size_t)rows)))
+    return REC_ATTN_ERR_INVALID_ARG;
+  int dev = -1, sms = 0;
+  const cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  NormArgs a{};
+  a.rows = rows; a.width = (int)width; a.eps = eps; a.ty = types; a.x = x; a.w = weight; a.b = bias; a.y = y;
+  return from_cuda(launch_layernorm_fwd(a, dtype, sms, static_cast<cudaStream_t>(stream)));
+}
+
+REC_ATTN_API rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows, int64_t width, int32_t num_groups,
+                                                    const void* x, const int8_t* types, const float* weight,
+                                                    float eps, const void* dy, void* dx, float* dweight,
+                                                    float* dbias, void* stream) {
+  const rec_attn_status s = check_norm(dtype, rows, width, num_groups, types, eps);
+  if (s != REC_ATTN_OK) return s;
+  if (misaligned16(dweight) || misaligned16(dbias)) return REC_ATTN_ERR_INVALID_ARG;
+  const size_t gain = (size_t)num_groups * width * sizeof(float);
+  if (dweight && dbias && overlaps(dweight, gain, dbias, gain)) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows > 0) {
+    if (!x || !weight || !dy || !dx || misaligned16(x) || misaligned16(weight) || misaligned16(dy) || misaligned16(dx))
+      return REC_ATTN_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)rows * width * (dtype == REC_ATTN_BF16 ? 2 : 4);
+    if ((dx != x && overlaps(dx, bytes, x, bytes)) || (dx != dy && overlaps(dx, bytes, dy, bytes)))
+      return REC_ATTN_ERR_INVALID_ARG;
+    const void* outs[3] = {dx, dweight, dbias};
+    const size_t out_bytes[3] = {bytes, gain, gain};
+    for (int o = 0; o < 3; ++o) {
+      if (!outs[o]) continue;
+      if (overlaps(outs[o], out_bytes[o], weight, gain) ||
+          (types && overlaps(outs[o], out_bytes[o], types, (size_t)rows)))
+        return REC_ATTN_ERR_INVALID_ARG;
+      if (o > 0 && (overlaps(outs[o], gain, x, bytes) || overlaps(outs[o], gain, dy, bytes) ||
+                    overlaps(outs[o], gain, dx, bytes)))
+        return REC_ATTN_ERR_INVALID_ARG;
+    }
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int dev = -1, sms = 0;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  if (rows == 0) {  // no row: the gains' gradients are zero
+    if (dweight) e = cudaMemsetAsync(dweight, 0, gain, st);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, gain, st);
+    return from_cuda(e);
+  }
+  NormArgs a{};
+  a.rows = rows; a.width = (int)width; a.eps = eps; a.ty = types; a.x = x; a.w = weight;
+  a.dy = dy; a.dx = dx; a.dw = dweight; a.db = dbias;
+  const NormBwdPlan p = layernorm_bwd_plan(rows, (int)width, types != nullptr, sms);
+  cudaMemPool_t pool;
+  void* ws = nullptr;
+  e = pool_for(dev, &pool);
+  if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&ws, p.bytes, pool, st);
+  if (e != cudaSuccess) return from_cuda(e);
+  e = launch_layernorm_bwd(a, p, ws, dtype, st);
+  const cudaError_t ef = cudaFreeAsync(ws, st);
+  return from_cuda(e != cudaSuccess ? e : ef);
+}
+
 REC_ATTN_API rec_attn_status rec_attn_fwd_compress(rec_attn_plan_t* plan, const void* q, const void* k,
                                                    const void* v, const int64_t* hist_begin_host,
                                                    const int64_t* hist_len_host, int32_t n_segments,
@@ -870,8 +985,9 @@ REC_ATTN_API rec_attn_status rec_attn_fwd_compress(rec_attn_plan_t* plan, const 
       (reinterpret_cast<uintptr_t>(timestamps_out) & 7u))
     return REC_ATTN_ERR_INVALID_ARG;
   const size_t row_bytes = (size_t)p.num_heads * p.head_dim * 2;
-  if (overlaps(x_out, rows_out * row_bytes, q, T * row_bytes) || overlaps(x_out, rows_out * row_bytes, k, T * row_bytes) ||
-      overlaps(x_out, rows_out * row_bytes, v, T * row_bytes))
+  if (overlaps(x_out, rows_out * row_bytes, q, T * row_bytes) ||
+      overlaps(x_out, rows_out * row_bytes, k, kv_bytes(plan)) ||
+      overlaps(x_out, rows_out * row_bytes, v, kv_bytes(plan)))
     return REC_ATTN_ERR_INVALID_ARG;
   // per request: where its rows go and its first 32-row block boundary in the fix-up buffer
   std::vector<CmpReq> creq((size_t)B);
@@ -1093,6 +1209,7 @@ REC_ATTN_API rec_attn_status rec_attn_device_status(rec_attn_plan_t* plan, int32
 struct rec_attn_kv_cache_s {
   rec_attn_params p{};   // the caller's parameters
   rec_attn_params pp{};  // those of the per-call plans: the rows are already rotated
+  int32_t kv_heads = 0;  // key/value heads; p.num_heads / kv_heads query heads share one
   int device = 0;
   int32_t batch = 0;
   int32_t max_cands = 0;
@@ -1149,15 +1266,17 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 }  // namespace
 
-REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params, int32_t batch,
-                                                   const int64_t* hist_offsets_host, const int64_t* hist_t_dev,
-                                                   const int8_t* hist_types_dev, const void* k_hist,
-                                                   const void* v_hist, int32_t max_cands, void* stream,
-                                                   rec_attn_kv_cache_t** cache_out) {
+namespace {
+
+rec_attn_status cache_create_impl(const rec_attn_params* params, int32_t kv_heads, int32_t batch,
+                                  const int64_t* hist_offsets_host, const int64_t* hist_t_dev,
+                                  const int8_t* hist_types_dev, const void* k_hist, const void* v_hist,
+                                  int32_t max_cands, void* stream, rec_attn_kv_cache_t** cache_out) {
   if (!cache_out) return REC_ATTN_ERR_INVALID_ARG;
   *cache_out = nullptr;
   rec_attn_status s = check_params(params);
   if (s != REC_ATTN_OK) return s;
+  if (kv_heads < 1 || params->num_heads % kv_heads != 0) return REC_ATTN_ERR_INVALID_ARG;
   if (batch < 1 || !hist_offsets_host || max_cands < 1) return REC_ATTN_ERR_INVALID_ARG;
   if (hist_offsets_host[0] != 0) return REC_ATTN_ERR_INVALID_ARG;
   long long Th = 0, Tc = 0;
@@ -1183,6 +1302,7 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params
   }
   c->p = *params;
   if (c->p.softmax_scale == 0.f) c->p.softmax_scale = 1.f / std::sqrt((float)params->head_dim);
+  c->kv_heads = kv_heads;
   c->pp = c->p;
   c->pp.use_rope = 0;
   c->batch = batch;
@@ -1199,6 +1319,8 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params
                             std::pow(params->rope_base, 2.0 * i / (double)params->head_dim));
   const size_t elem = params->dtype == REC_ATTN_BF16 ? 2 : 4;
   const size_t rows_bytes = ws_up((size_t)Tc * params->num_heads * params->head_dim * elem);
+  const size_t kvr_bytes = ws_up((size_t)Tc * kv_heads * params->head_dim * elem);
+  const size_t tens_bytes = 2 * rows_bytes + 2 * kvr_bytes;
   const size_t lse_bytes = ws_up((size_t)Tc * params->num_heads * 4);
   const size_t t_bytes = ws_up((size_t)Tc * 8), ty_bytes = ws_up((size_t)Tc), off_bytes = ws_up(8 * ((size_t)batch + 1));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1206,14 +1328,14 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params
   cudaMemPool_t pool;
   if (e == cudaSuccess) e = pool_for(c->device, &pool);
   if (e == cudaSuccess)
-    e = cudaMallocFromPoolAsync(&c->buf, 4 * rows_bytes + lse_bytes + t_bytes + ty_bytes + off_bytes, pool, st);
+    e = cudaMallocFromPoolAsync(&c->buf, tens_bytes + lse_bytes + t_bytes + ty_bytes + off_bytes, pool, st);
   if (e != cudaSuccess) { delete c; return from_cuda(e); }
   char* w = static_cast<char*>(c->buf);
-  c->q = w; c->k = w + rows_bytes; c->v = w + 2 * rows_bytes; c->o = w + 3 * rows_bytes;
-  c->lse = reinterpret_cast<float*>(w + 4 * rows_bytes);
-  c->t = reinterpret_cast<long long*>(w + 4 * rows_bytes + lse_bytes);
-  c->ty = reinterpret_cast<int8_t*>(w + 4 * rows_bytes + lse_bytes + t_bytes);
-  c->off_dev = reinterpret_cast<int64_t*>(w + 4 * rows_bytes + lse_bytes + t_bytes + ty_bytes);
+  c->q = w; c->o = w + rows_bytes; c->k = w + 2 * rows_bytes; c->v = w + 2 * rows_bytes + kvr_bytes;
+  c->lse = reinterpret_cast<float*>(w + tens_bytes);
+  c->t = reinterpret_cast<long long*>(w + tens_bytes + lse_bytes);
+  c->ty = reinterpret_cast<int8_t*>(w + tens_bytes + lse_bytes + t_bytes);
+  c->off_dev = reinterpret_cast<int64_t*>(w + tens_bytes + lse_bytes + t_bytes + ty_bytes);
   // history rows: rotated keys, values, times and types (queries stay zero: no user
   // token queries in a scoring call); the candidate slots are written by each call
   std::vector<SlotReq> reqs((size_t)batch);
@@ -1242,7 +1364,7 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params
       a.ty_src = hist_types_dev;
       a.q_src = nullptr; a.k_src = k_hist; a.v_src = v_hist;
       a.q_dst = nullptr; a.k_dst = c->k; a.v_dst = c->v; a.t_dst = c->t; a.ty_dst = c->ty;
-      a.heads = params->num_heads; a.head_dim = params->head_dim;
+      a.heads = params->num_heads; a.kv_heads = kv_heads; a.head_dim = params->head_dim;
       std::memcpy(a.omega, c->omega, sizeof a.omega);
       e = launch_rope_slots(a, params->dtype, tab.n_chunks, st);
     }
@@ -1258,6 +1380,27 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params
   }
   *cache_out = c;
   return REC_ATTN_OK;
+}
+
+}  // namespace
+
+REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params, int32_t batch,
+                                                   const int64_t* hist_offsets_host, const int64_t* hist_t_dev,
+                                                   const int8_t* hist_types_dev, const void* k_hist,
+                                                   const void* v_hist, int32_t max_cands, void* stream,
+                                                   rec_attn_kv_cache_t** cache_out) {
+  return cache_create_impl(params, params ? params->num_heads : 0, batch, hist_offsets_host, hist_t_dev,
+                           hist_types_dev, k_hist, v_hist, max_cands, stream, cache_out);
+}
+
+REC_ATTN_API rec_attn_status rec_attn_cache_create_grouped(const rec_attn_params* params, int32_t num_kv_heads,
+                                                           int32_t batch, const int64_t* hist_offsets_host,
+                                                           const int64_t* hist_t_dev, const int8_t* hist_types_dev,
+                                                           const void* k_hist, const void* v_hist,
+                                                           int32_t max_cands, void* stream,
+                                                           rec_attn_kv_cache_t** cache_out) {
+  return cache_create_impl(params, num_kv_heads, batch, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist,
+                           v_hist, max_cands, stream, cache_out);
 }
 
 REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const int64_t* cand_offsets_host,
@@ -1278,8 +1421,9 @@ REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const 
       if (!aligned16(x)) return REC_ATTN_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(lse) & 3u) return REC_ATTN_ERR_INVALID_ARG;
     const size_t bytes = (size_t)Nc * p.num_heads * p.head_dim * elem;
-    if (overlaps(out, bytes, q_cand, bytes) || overlaps(out, bytes, k_cand, bytes) ||
-        overlaps(out, bytes, v_cand, bytes) || (lse && overlaps(lse, (size_t)Nc * p.num_heads * 4, out, bytes)))
+    const size_t kvb = bytes / (p.num_heads / c->kv_heads);
+    if (overlaps(out, bytes, q_cand, bytes) || overlaps(out, bytes, k_cand, kvb) ||
+        overlaps(out, bytes, v_cand, kvb) || (lse && overlaps(lse, (size_t)Nc * p.num_heads * 4, out, bytes)))
       return REC_ATTN_ERR_INVALID_ARG;
   }
   int dev = -1;
@@ -1314,7 +1458,7 @@ REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const 
     a.q_src = q_cand; a.k_src = k_cand; a.v_src = v_cand;
     a.q_dst = c->q; a.k_dst = c->k; a.v_dst = c->v; a.t_dst = c->t; a.ty_dst = c->ty;
     a.o_comb = c->o; a.lse_comb = c->lse; a.o_out = out; a.lse_out = lse;
-    a.heads = p.num_heads; a.head_dim = p.head_dim;
+    a.heads = p.num_heads; a.kv_heads = c->kv_heads; a.head_dim = p.head_dim;
     std::memcpy(a.omega, c->omega, sizeof a.omega);
     e = launch_rope_slots(a, p.dtype, tab.n_chunks, st);
   }
@@ -1322,7 +1466,7 @@ REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const 
   rec_attn_plan_t* plan = nullptr;
   rec_attn_status s = REC_ATTN_OK;
   if (e == cudaSuccess) {
-    s = plan_impl(&c->pp, 0, c->batch, c->comb_off.data(), c->off_dev, reinterpret_cast<const int64_t*>(c->t), c->ty,
+    s = plan_impl(&c->pp, c->kv_heads, 0, c->batch, c->comb_off.data(), c->off_dev, reinterpret_cast<const int64_t*>(c->t), c->ty,
                   st, &plan);
     if (s == REC_ATTN_OK) s = fwd_impl(plan, c->q, c->k, c->v, nullptr, c->o, lse ? c->lse : nullptr, st);
     if (s == REC_ATTN_OK) e = launch_slots_gather(a, p.dtype, tab.n_chunks, st);

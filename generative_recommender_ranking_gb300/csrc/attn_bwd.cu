@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(Split<D>::kThreads) k_bwd_dq(BwdArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
   const long long g = blockIdx.x;
-  const int h = blockIdx.y, H = a.heads;
+  const int h = blockIdx.y, H = a.heads, Hk = H / a.group, hk = h / a.group;
   const int b = tile_request(a.meta, a.batch, g);
   const ReqMeta m = a.meta[b];
   const int qt = (int)(g - m.tile_start), r = threadIdx.x / S, part = threadIdx.x % S, pi = qt * kTile + r;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(Split<D>::kThreads) k_bwd_dq(BwdArgs a) {
       const int c = idx / D, e = idx - c * D;
       const int pj = kt * kTile + c;
       const bool ok = pj < m.len;
-      const long long src = ((m.tok_start + pj) * H + h) * D + e;
+      const long long src = ((m.tok_start + pj) * Hk + hk) * D + e;
       sm.a[c][e] = ok ? ld_elem<E>(a.k, src) : 0.f;
       sm.b[c][e] = ok ? ld_elem<E>(a.v, src) : 0.f;
     }
@@ -200,19 +200,20 @@ __global__ void __launch_bounds__(Split<D>::kThreads) k_bwd_dq(BwdArgs a) {
   for (int e = 0; e < 32; ++e) st_elem<E>(a.dq, row * D + 32 * part + e, acc[e]);
 }
 
-// dK, dV: block = (key tile g, head h); kSplit threads per key row.
+// dK, dV: block = (key tile g, key/value head); kSplit threads per key row, the group's
+// query heads one after the other.
 template <typename E, int D>
 __global__ void __launch_bounds__(Split<D>::kThreads) k_bwd_dkv(BwdArgs a) {
   constexpr int S = Split<D>::kSplit;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
   const long long g = blockIdx.x;
-  const int h = blockIdx.y, H = a.heads;
+  const int hk = blockIdx.y, H = a.heads, Hk = H / a.group;
   const int b = tile_request(a.meta, a.batch, g);
   const ReqMeta m = a.meta[b];
   const int kt = (int)(g - m.tile_start), r = threadIdx.x / S, part = threadIdx.x % S, pj = kt * kTile + r;
   const bool row_ok = pj < m.len;
-  const long long tok = m.tok_start + pj, row = tok * H + h;
+  const long long tok = m.tok_start + pj, row = tok * Hk + hk;
   float k[32], v[32], dk[32], dv[32];
   long long tj = 0;
   int tyj = -1;
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(Split<D>::kThreads) k_bwd_dkv(BwdArgs a) {
     tyj = a.ty[tok];
   }
   const uint8_t* col = a.cls + m.cls_start + kt;  // column kt of the request's class matrix
-  for (int qt = 0; qt < m.ntiles; ++qt) {
+  for (int it = 0; it < a.group * m.ntiles; ++it) {
+    const int h = hk * a.group + it / m.ntiles, qt = it % m.ntiles;
     const int cl = col[(long long)qt * m.ntiles];
     if (cl == REC_ATTN_TILE_SKIP) continue;
     __syncthreads();
@@ -306,7 +308,8 @@ cudaError_t launch_bwd_t(const BwdArgs& a, long long n_tiles, cudaStream_t st) {
   k_bwd_dq<E, D><<<grid, Split<D>::kThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_bwd_dkv<E, D><<<grid, Split<D>::kThreads, smem, st>>>(a);
+  const dim3 grid_kv((unsigned)n_tiles, (unsigned)(a.heads / a.group));
+  k_bwd_dkv<E, D><<<grid_kv, Split<D>::kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -190,20 +190,26 @@ __device__ __forceinline__ bool next_item(uint8_t* sm, uint64_t* bars, uint32_t&
 }
 
 // The streamed tiles of an item, in order: request-local tile index, class and
-// mask-table slot (-1: none).
+// mask-table slot (-1: none).  DKV visits each listed query tile once for every query
+// head of the group (`reps` times in a row), so dK and dV sum over the group in TMEM.
 struct Cursor {
   const uint32_t* list;
   const int* slots;
-  int r;
-  __device__ __forceinline__ void init(const uint32_t* base, const int* slot_base, const BwdItemDesc& d) {
+  int r, rep, reps;
+  __device__ __forceinline__ void init(const uint32_t* base, const int* slot_base, const BwdItemDesc& d, int n_rep) {
     list = base + d.list;
     slots = slot_base + d.list;
     r = 0;
+    rep = 0;
+    reps = n_rep;
   }
   __device__ __forceinline__ void next(int& tile, int& cls, int& slot) {
     const uint32_t e = list[r];
     slot = slots[r];
-    ++r;
+    if (++rep == reps) {
+      rep = 0;
+      ++r;
+    }
     tile = (int)(e & 0xffffffu);
     cls = (int)(e >> 24);
   }
@@ -228,12 +234,13 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
   constexpr int kTileBytes = L::kTileBytes;
   ItemSlot* slots = reinterpret_cast<ItemSlot*>(sm + L::kItems);
   int* counter = a.counters + (DKV ? 5 : 3);
+  const long long n_items = DKV ? a.n_kv_items : a.n_items;
   for (;;) {
     const long long w = atomicAdd(counter, 1);
     const int slot = (int)(it_cnt & 1);
     if (!bw_wait(bars + kItemEmpty + slot, ((it_cnt >> 1) & 1) ^ 1, abort_flag, a.status)) goto drain;
     ++it_cnt;
-    if (w >= a.n_items) {
+    if (w >= n_items) {
       slots[slot].end = 1;
       ptx::mbar_arrive(bars + kItemFull + slot);
       break;
@@ -252,7 +259,7 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
     {
       const int x = d.h * D;
       const long long g = (long long)d.tile_start + d.tile;
-      const float2* rows_h = a.rowc + (long long)d.h * a.n_tiles * kTile;  // head h's row constants
+      const float2* rows_h = a.rowc + (long long)d.h * a.n_tiles * kTile;  // DQ: head h's row constants
       ptx::mbar_arrive_expect_tx(bars + kResFull, 2 * kTileBytes + kRecB + (DKV ? 0 : kRowB));
       const int y = (int)(d.tok_start + (long long)d.tile * kTile);
 #pragma unroll
@@ -266,9 +273,13 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
       res_ph = it_n & 1;
       ++it_n;
       Cursor cur;
-      cur.init(lists, DKV ? a.qslot : a.kslot, d);
+      cur.init(lists, DKV ? a.qslot : a.kslot, d, DKV ? a.group : 1);
+      const int kvx = (d.h / a.group) * D;  // DQ: the columns of the head's key/value head
       for (int j = 0; j < d.n; ++j) {
         int tile, cls, tslot;
+        // DKV: the query head of this visit, its columns and its row constants
+        const int hq = d.h * a.group + cur.rep;
+        const int xs = DKV ? hq * D : kvx;
         cur.next(tile, cls, tslot);
         const int st = (int)(s_it % kNS);
         const uint32_t ph = (s_it / kNS) & 1;
@@ -283,9 +294,9 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
                                    2 * kTileBytes + (tab ? kMaskB : rec ? kRecB : 0) + (DKV ? kRowB : 0));
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          ptx::tma_load_2d(sm + L::kStr + (2 * st) * kTileBytes + c * kSlab, str[0], x + 64 * c, ys,
+          ptx::tma_load_2d(sm + L::kStr + (2 * st) * kTileBytes + c * kSlab, str[0], xs + 64 * c, ys,
                            bars + kStrFull + st);
-          ptx::tma_load_2d(sm + L::kStr + (2 * st + 1) * kTileBytes + c * kSlab, str[1], x + 64 * c, ys,
+          ptx::tma_load_2d(sm + L::kStr + (2 * st + 1) * kTileBytes + c * kSlab, str[1], xs + 64 * c, ys,
                            bars + kStrFull + st);
         }
         if (tab)
@@ -293,7 +304,9 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
                          kMaskB, bars + kStrFull + st);
         else if (rec)
           ptx::bulk_load(sm + L::kSRec + st * kStageRecB, a.krec + gs, kRecB, bars + kStrFull + st);
-        if (DKV) ptx::bulk_load(sm + L::kSRow + st * kRowB, rows_h + gs * kTile, kRowB, bars + kStrFull + st);
+        if (DKV)
+          ptx::bulk_load(sm + L::kSRow + st * kRowB, a.rowc + ((long long)hq * a.n_tiles + gs) * kTile, kRowB,
+                         bars + kStrFull + st);
         str_used[st] = true;
         str_ph[st] = ph;
         ++s_it;
@@ -567,7 +580,7 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
     RowMask rm;
     row_mask_setup(a.mask, live, pi, ti, tyi, rm);
     Cursor cur;
-    cur.init(a.klist, a.kslot, it);
+    cur.init(a.klist, a.kslot, it, 1);
     for (int j = 0; j < it.n; ++j) {
       int kt, cls, tslot;
       cur.next(kt, cls, tslot);
@@ -692,13 +705,13 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
   const unsigned long long sl2x2 = f2pack(sl2, sl2);
   const bool wide = ((reinterpret_cast<uintptr_t>(a.dk) | reinterpret_cast<uintptr_t>(a.dv)) & 31) == 0;
   uint32_t* colS = reinterpret_cast<uint32_t*>(sm + BL::kCol);
-  const int H = a.heads;
+  const int Hk = a.heads / a.group;
   uint32_t it_n = 0, s_it = 0, step = 0, grp = 0, cbuf = 0, it_cnt = 0;
   BwdItemDesc it;
   while (next_item<D>(sm, bars, it_cnt, true, it, abort_flag, a.status)) {
     const int pj = it.tile * kTile + row;
     const bool key_ok = pj < it.len;
-    const long long growk = (it.tok_start + pj) * H + it.h;
+    const long long growk = (it.tok_start + pj) * Hk + it.h;
     __nv_bfloat16* dkr = static_cast<__nv_bfloat16*>(a.dk) + growk * D;
     __nv_bfloat16* dvr = static_cast<__nv_bfloat16*>(a.dv) + growk * D;
     if (it.n <= 0) {  // no query sees this key tile
@@ -708,7 +721,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     if (!bw_wait_warp(bars + kResFull, it_n & 1, abort_flag, a.status)) return;  // the key tile's record
     const long long tj = rrec->t[row];
     Cursor cur;
-    cur.init(a.qlist, a.qslot, it);
+    cur.init(a.qlist, a.qslot, it, a.group);
     // Column bits of the item's j-th query tile (stage st) into buffer `buf`: the key's
     // words of the mask table's columns when the pair has a slot; otherwise, as query
     // row `row` of the tile, this thread builds the row's bits over the key tile and
@@ -897,10 +910,36 @@ __global__ void __launch_bounds__(256) k_bwd_rowc(BwdArgs a) {
 }
 
 // ------------------------------------------------------------------ schedule
+// group > 1: dK/dV items are (tile, key/value head) pairs, one block compacting the
+// planner's order of (tile, query head) items to each group's first head, in order.
+__global__ void __launch_bounds__(1024) k_bwd_kv_items(BwdSchedArgs s) {
+  __shared__ int s_warp[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hk = s.heads / s.group;
+  long long base = 0;
+  for (long long i0 = 0; i0 < s.n_items; i0 += 1024) {
+    const long long i = i0 + threadIdx.x;
+    const int e = i < s.n_items ? s.items[i] : 0;
+    const int h = e % s.heads;
+    const bool take = i < s.n_items && h % s.group == 0;
+    const unsigned bal = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) s_warp[warp] = __popc(bal);
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < 32; ++w) {
+      before += w < warp ? s_warp[w] : 0;
+      total += s_warp[w];
+    }
+    const long long at = base + before + __popc(bal & ((1u << lane) - 1u));
+    if (take && at < s.n_kv_items) s.kv_items[at] = (e / s.heads) * Hk + h / s.group;
+    base += total;
+    __syncthreads();
+  }
+}
+
 // Threads [0, n_tiles): the transposed tile lists -- for key tile g, the query tiles
 // of its request whose class against it is not SKIP, in order.  Threads
 // [n_tiles, n_tiles + n_items): the descriptors of item w for both modes (DKV: the
-// mirrored key tile of the item's query tile).
+// mirrored key tile of the item's query tile, for the first n_kv_items threads).
 __global__ void __launch_bounds__(128) k_bwd_schedule(BwdSchedArgs s) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i < s.n_tiles) {
@@ -924,8 +963,9 @@ __global__ void __launch_bounds__(128) k_bwd_schedule(BwdSchedArgs s) {
   if (w >= s.n_items) return;
   const long long e = s.items[w];
   const long long g = e / s.heads;
-  const ReqMeta m = s.meta[s.qreq[g]];
-  const int qt = (int)(g - m.tile_start), kt = m.ntiles - 1 - qt;
+  ReqMeta m = s.meta[s.qreq[g]];
+  const int qt = (int)(g - m.tile_start);
+  int kt = m.ntiles - 1 - qt;
   BwdItemDesc d;
   d.tok_start = m.tok_start;
   d.t_ref = s.t[m.tok_start];
@@ -937,12 +977,24 @@ __global__ void __launch_bounds__(128) k_bwd_schedule(BwdSchedArgs s) {
   d.tile = qt;
   d.n = max(s.kcount[g], 0);
   s.desc[w] = d;
+  if (w >= s.n_kv_items) return;
+  if (s.group > 1) {  // dK/dV item w has a tile and a head of its own
+    const int Hk = s.heads / s.group;
+    const long long ek = s.kv_items[w], gk = ek / Hk;
+    m = s.meta[s.qreq[gk]];
+    kt = m.ntiles - 1 - (int)(gk - m.tile_start);
+    d.tok_start = m.tok_start;
+    d.t_ref = s.t[m.tok_start];
+    d.len = m.len;
+    d.tile_start = (int)m.tile_start;
+    d.h = (int)(ek % Hk);
+  }
   const uint8_t* col = s.cls + m.cls_start + kt;
   int n = 0;
   for (int r = 0; r < m.ntiles; ++r) n += col[(long long)r * m.ntiles] != REC_ATTN_TILE_SKIP;
   d.list = m.cls_start + (long long)kt * m.ntiles;
   d.tile = kt;
-  d.n = n;
+  d.n = n * s.group;
   s.desc[s.n_items + w] = d;
 }
 
@@ -962,7 +1014,7 @@ __global__ void __launch_bounds__(kTile) k_bwd_colmask(BwdSchedArgs s) {
 }
 
 // ------------------------------------------------------------------ kernel
-// maps: Q', K', V, dO, each a [T][H*64] bf16 view with 64 x 128 boxes.
+// maps: Q', K', V, dO as bf16 views [T][heads * d] (K', V: key/value heads), 64 x 128 boxes.
 template <int D, bool DKV>
 __global__ void __launch_bounds__(kThreadsB, BCfg<D>::kBlocksPerSM)
     k_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -1050,10 +1102,9 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long cap = (long long)BCfg<D>::kBlocksPerSM * num_sms;
-  const int grid = (int)(a.n_items < cap ? a.n_items : cap);
-  e = launch_mode<D, false>(maps, a, grid, st);
+  e = launch_mode<D, false>(maps, a, (int)(a.n_items < cap ? a.n_items : cap), st);
   if (e != cudaSuccess) return e;
-  return launch_mode<D, true>(maps, a, grid, st);
+  return launch_mode<D, true>(maps, a, (int)(a.n_kv_items < cap ? a.n_kv_items : cap), st);
 }
 
 }  // namespace
@@ -1061,6 +1112,11 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
 cudaError_t launch_bwd_schedule(const BwdSchedArgs& s, int num_sms, cudaStream_t st) {
   const long long n = s.n_tiles + s.n_items;
   if (n <= 0) return cudaSuccess;
+  if (s.group > 1) {
+    k_bwd_kv_items<<<1, 1024, 0, st>>>(s);
+    const cudaError_t ek = cudaGetLastError();
+    if (ek != cudaSuccess) return ek;
+  }
   k_bwd_schedule<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || s.mcap <= 0) return e;

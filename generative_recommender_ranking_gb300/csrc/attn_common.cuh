@@ -79,6 +79,7 @@ struct AttnArgs {
   const uint32_t* mtab;   // mask table: [slot][128 rows][4 words]
   long long n_items; // query tiles x heads
   int heads;
+  int group;         // query heads that share a key/value head (k, v: [T][heads / group][d])
   float scale;       // softmax scale (natural-log domain)
   MaskP mask;
   CmpArgs cmp;       // compression epilogue (kernels instantiated with it only)
@@ -93,11 +94,11 @@ struct RopeArgs {
   const long long* t;
   const int8_t* ty;        // token types (read only when skip_user_q)
   int skip_user_q;         // 1: no Q' for GLOBAL / HIST tokens (a plan where no user token queries)
-  const void* q;
-  const void* k;
-  void* qr;                // rotated outputs, same layout [T][H][d]
+  const void* q;           // [T][heads][d]
+  const void* k;           // [T][kv_heads][d], kv_heads <= heads
+  void* qr;                // rotated outputs, same layouts
   void* kr;
-  int heads, head_dim;
+  int heads, kv_heads, head_dim;
   float omega[kMaxPairs];  // rad per second, pair i
 };
 
@@ -125,7 +126,7 @@ struct SlotArgs {
   const int8_t* ty_src;    // [source rows], or null: every written row takes ty_const
   int ty_const;
   const void* q_src;       // [source][H][d] or null (no queries)
-  const void* k_src;
+  const void* k_src;       // [source][kv_heads][d], v_src too; kv_heads <= heads
   const void* v_src;
   void* q_dst;             // [destination][H][d]
   void* k_dst;
@@ -137,7 +138,7 @@ struct SlotArgs {
   const float* lse_comb;   // [destination][H] or null
   void* o_out;             // [source][H][d]
   float* lse_out;          // [source][H] or null
-  int heads, head_dim;
+  int heads, kv_heads, head_dim;
   float omega[kMaxPairs];  // rad per second, pair i (all zero: no rotation)
 };
 
@@ -150,8 +151,8 @@ struct BwdItemDesc {
   int len;              // request length
   int tile;             // request-local tile whose rows the item owns
   int tile_start;       // global index of the request's first tile
-  int h;
-  int n;                // streamed tiles
+  int h;                // query head (dQ), key/value head (dK/dV)
+  int n;                // streamed tiles (dK/dV: each listed query tile once per head of the group)
   int pad;
 };
 static_assert(sizeof(BwdItemDesc) == 48, "three 16-byte loads");
@@ -163,12 +164,13 @@ struct BwdArgs {
   const int* items;        // work items (query tile * H + head), the planner's execution order
   const int* qreq;         // request of each tile
   const KeyTileRec* krec;  // per tile: type bitmaps and times (tensor-core kernels' masks)
-  long long n_items;       // tiles x heads
+  long long n_items;       // tiles x heads: dQ items
+  long long n_kv_items;    // tiles x key/value heads: dK/dV items
   int* status;             // device status word (first error wins)
   int* counters;           // [3], [4]: dQ item counter and exit ticket; [5], [6]: dK/dV (reset at kernel end)
   long long n_tiles;
   // tensor-core path (bf16): per-plan schedule and per-call row constants
-  const BwdItemDesc* desc;  // [2][n_items]: dQ items, then dK/dV items (mirrored key tiles)
+  const BwdItemDesc* desc;  // [n_items] dQ items, then [n_kv_items] dK/dV items (mirrored key tiles)
   const uint32_t* qlist;    // per key tile: query tiles with a non-SKIP class (qt | class << 24)
   float2* rowc;             // [H][n_tiles][128 rows]: -lse * log2(e) and -D, rows paired as
                             // {-lse2(2k), -lse2(2k+1), -D(2k), -D(2k+1)} (lse2 -inf: the row sees
@@ -191,11 +193,12 @@ struct BwdArgs {
   const void* dout_attn;   // the gradient that reaches the attention (dO, or dO * sigmoid(output gate))
   const float* lse;        // forward log-sum-exp [T][H]
   float* delta;            // workspace [T][H]: <dO, O> per row
-  void* dq;                // outputs [T][H][d] (w.r.t. the unrotated Q, K)
-  void* dk;
+  void* dq;                // output [T][H][d] (w.r.t. the unrotated Q)
+  void* dk;                // outputs [T][H / group][d] (w.r.t. the unrotated K), summed over the group's heads
   void* dv;
   long long rows;          // T * H
   int heads;
+  int group;               // query heads that share a key/value head
   float scale;
   int rotate;              // 1: undo the time-RoPE on dQ', dK'
   MaskP mask;
@@ -210,8 +213,9 @@ struct BwdSchedArgs {
   const int* kcount;
   const uint8_t* cls;
   const long long* t;
-  long long n_tiles, n_items;
-  int heads;
+  long long n_tiles, n_items, n_kv_items;
+  int heads, group;
+  int* kv_items;            // group > 1: written, (tile * kv heads + kv head) in the order of `items`
   BwdItemDesc* desc;
   uint32_t* qlist;
   const int* pslot;         // per (query tile, key tile): mask-table slot, -1 if none

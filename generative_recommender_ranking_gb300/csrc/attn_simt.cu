@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kTile) k_attn_simt(AttnArgs a) {
   const int r = threadIdx.x, pi = it.qt * kTile + r;
   const bool row_ok = pi < it.m.len;
   const long long tok = it.m.tok_start + pi;
-  const int H = a.heads;
+  const int H = a.heads, Hk = H / a.group, hk = it.h / a.group;
   const float* Q = static_cast<const float*>(a.q);
   const float* K = static_cast<const float*>(a.k);
   const float* Vv = static_cast<const float*>(a.v);
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kTile) k_attn_simt(AttnArgs a) {
       const int c = idx / D, e = idx - c * D;
       const int pj = kt * kTile + c;
       const bool ok = pj < it.m.len;
-      const long long src = ((it.m.tok_start + pj) * H + it.h) * D + e;
+      const long long src = ((it.m.tok_start + pj) * Hk + hk) * D + e;
       s_k[c][e] = ok ? K[src] : 0.f;
       s_v[c][e] = ok ? Vv[src] : 0.f;
     }

@@ -242,6 +242,7 @@ __device__ void run_producer(const AttnArgs& a, const void* tq, const void* tk, 
     ptx::bulk_load(qrbuf + qb * kRecBytes, a.krec + it.m.tile_start + it.qt, kRecBytes, B.q_full + qb);
     q_used[qb] = true; q_ph[qb] = (q_it / QB) & 1;
     ++q_it;
+    const int kvx = (it.h / a.group) * D;  // the key/value head the item's query head shares
     for (int j = 0; j < it.n; ++j) {
       const uint32_t e = it.list[j];
       const int slot = it.slots[j];
@@ -258,7 +259,7 @@ __device__ void run_producer(const AttnArgs& a, const void* tq, const void* tk, 
       ptx::mbar_arrive_expect_tx(B.k_full + st, L::kKVBytes + (partial ? (tab ? kMaskBytes : kRecBytes) : 0));
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
-        ptx::tma_load_2d(kbuf + st * L::kKVBytes + c * kSlab, tk, it.h * D + c * 64, y, B.k_full + st);
+        ptx::tma_load_2d(kbuf + st * L::kKVBytes + c * kSlab, tk, kvx + c * 64, y, B.k_full + st);
       if (tab) ptx::bulk_load(rbuf + st * kStageRec, a.mtab + (long long)slot * (kMaskBytes / 4), kMaskBytes, B.k_full + st);
       else if (partial) ptx::bulk_load(rbuf + st * kStageRec, a.krec + it.m.tile_start + kt, kRecBytes, B.k_full + st);
       k_used[st] = true; k_ph[st] = ph;
@@ -266,7 +267,7 @@ __device__ void run_producer(const AttnArgs& a, const void* tq, const void* tk, 
       ptx::mbar_arrive_expect_tx(B.v_full + st, L::kKVBytes);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
-        ptx::tma_load_2d(vbuf + st * L::kKVBytes + c * kSlab, tv, it.h * D + c * 64, y, B.v_full + st);
+        ptx::tma_load_2d(vbuf + st * L::kKVBytes + c * kSlab, tv, kvx + c * 64, y, B.v_full + st);
       v_used[st] = true; v_ph[st] = ph;
       ++kv_it;
     }

@@ -43,6 +43,36 @@ cudaError_t launch_bwd_norm_gate(const NormGateArgs& a, int dtype, cudaStream_t 
 // req_len: device int [B] request lengths.
 cudaError_t launch_cmp_fixup(const CmpArgs& c, int batch, const int* req_len, long long n_fix, int heads,
                              int head_dim, cudaStream_t st);
+// Layer norm (layernorm.cu).
+struct NormArgs {
+  long long rows;
+  int width;            // values per row; width * element size a multiple of 16
+  float eps;
+  const int8_t* ty;     // [rows] token types (the row's gain and bias), or null: one for all
+  const void* x;        // [rows][width]
+  const float* w;       // [4 or 1][width]
+  const float* b;       // [4 or 1][width] or null
+  void* y;              // forward output
+  const void* dy;       // backward: upstream gradient
+  void* dx;
+  float* dw;            // [4 or 1][width] or null
+  float* db;
+  // set by the launchers
+  int tpr;              // threads per row
+  long long rows_per_block;
+  unsigned* seen;       // [blocks]: types whose sums the block wrote
+  float* part;          // [blocks][types][2][width]
+  float* flush;         // [blocks][row groups][4][2][width] (by type only)
+};
+// The backward's grid and workspace for a shape.
+struct NormBwdPlan {
+  int blocks;
+  long long rows_per_block;
+  size_t off_part, off_flush, bytes;
+};
+cudaError_t launch_layernorm_fwd(NormArgs a, int dtype, int num_sms, cudaStream_t st);
+NormBwdPlan layernorm_bwd_plan(long long rows, int width, bool by_type, int num_sms);
+cudaError_t launch_layernorm_bwd(NormArgs a, const NormBwdPlan& p, void* ws, int dtype, cudaStream_t st);
 cudaError_t launch_wait_timeout(int* status, unsigned long long limit_ns, cudaStream_t st);
 cudaError_t launch_attn_tc(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                            const CUtensorMap& v, int head_dim, int grid, cudaStream_t st);

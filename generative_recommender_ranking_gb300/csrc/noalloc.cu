@@ -90,7 +90,8 @@ REC_ATTN_API rec_attn_status rec_attn_fwd_noalloc(const rec_attn_params* params,
   const size_t tensor_bytes = (size_t)T * params->num_heads * params->head_dim * elem;
   // workspace layout inside the static array
   // no mask table here: the kernels build every PARTIAL tile's bits themselves
-  const WsLayout lay = ws_layout(batch, NT, NC, params->num_heads, params->use_rope ? tensor_bytes : 0, 0);
+  const WsLayout lay = ws_layout(batch, NT, NC, params->num_heads, params->use_rope ? tensor_bytes : 0,
+                                 params->use_rope ? tensor_bytes : 0, 0);
   if (lay.total > kScratchBytes) return REC_ATTN_ERR_UNSUPPORTED;  // batch too large for the static workspace
   if (T > 0) {
     if (!offsets_dev || !timestamps_dev || !types_dev || !q || !k || !v || !out) return REC_ATTN_ERR_INVALID_ARG;
@@ -176,7 +177,7 @@ REC_ATTN_API rec_attn_status rec_attn_fwd_noalloc(const rec_attn_params* params,
     ra.meta = pd.meta; ra.tile_req = pd.treq; ra.batch = batch; ra.t = t;
     ra.ty = types_dev; ra.skip_user_q = 0;
     ra.q = q; ra.k = k; ra.qr = w + lay.rq; ra.kr = w + lay.rk;
-    ra.heads = params->num_heads; ra.head_dim = params->head_dim;
+    ra.heads = ra.kv_heads = params->num_heads; ra.head_dim = params->head_dim;
     for (int i = 0; i < kMaxPairs; ++i)
       ra.omega[i] = i < params->head_dim / 2
                         ? (float)(params->phi_min / params->dt_max_s *
@@ -193,7 +194,7 @@ REC_ATTN_API rec_attn_status rec_attn_fwd_noalloc(const rec_attn_params* params,
   a.kslot = pd.kslot; a.mtab = pd.mtab;
   a.t = t; a.ty = types_dev; a.q = qs; a.k = ks; a.v = v; a.out = out; a.lse = lse; a.status = pd.status;
   a.out_gate = nullptr;
-  a.n_items = NT * params->num_heads; a.heads = params->num_heads;
+  a.n_items = NT * params->num_heads; a.heads = params->num_heads; a.group = 1;
   a.scale = params->softmax_scale > 0.f ? params->softmax_scale : 1.f / std::sqrt((float)params->head_dim);
   a.mask = mask;
   a.long_items = long_items(*params, batch, NT);

@@ -63,16 +63,19 @@ struct Chunk<float> {
 template <typename E, bool WQ>
 __device__ __forceinline__ void rope_rows(const RopeArgs& a, const char* __restrict__ q, const char* __restrict__ k,
                                           char* __restrict__ qr, char* __restrict__ kr, long long head_bytes,
-                                          long long tok, long long row0, int c, long long t_ref) {
+                                          long long tok, int c, long long t_ref) {
   using C = Chunk<E>;
   constexpr int kPairs = C::kPairs;
+  const long long row0 = tok * a.heads * head_bytes + (long long)c * 16;
+  const long long krow0 = tok * a.kv_heads * head_bytes + (long long)c * 16;
+  const int nh = WQ ? a.heads : a.kv_heads;
   uint4 rq[4], rk[4];  // raw 16-byte chunks of four heads
   auto load4 = [&](int h0) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (h0 + u < a.heads) {
+      if (h0 + u < nh) {
         if constexpr (WQ) rq[u] = *reinterpret_cast<const uint4*>(q + row0 + (h0 + u) * head_bytes);
-        rk[u] = *reinterpret_cast<const uint4*>(k + row0 + (h0 + u) * head_bytes);
+        if (h0 + u < a.kv_heads) rk[u] = *reinterpret_cast<const uint4*>(k + krow0 + (h0 + u) * head_bytes);
       }
   };
   load4(0);
@@ -80,13 +83,11 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, const char* __restr
   float sn[kPairs], cs[kPairs];
 #pragma unroll
   for (int p = 0; p < kPairs; ++p) sincosf(dt * a.omega[c * kPairs + p], &sn[p], &cs[p]);
-  for (int h0 = 0; h0 < a.heads; h0 += 4) {
+  for (int h0 = 0; h0 < nh; h0 += 4) {
     if (h0 > 0) load4(h0);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (h0 + u >= a.heads) break;
-      float y[8];
-      C::unpack(rk[u], y);
+      if (h0 + u >= nh) break;
       if constexpr (WQ) {
         float x[8];
         C::unpack(rq[u], x);
@@ -98,13 +99,16 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, const char* __restr
         }
         C::store(qr + row0 + (h0 + u) * head_bytes, x);
       }
+      if (h0 + u >= a.kv_heads) continue;  // the key heads come first, query heads may be more
+      float y[8];
+      C::unpack(rk[u], y);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         const float y0 = y[2 * p], y1 = y[2 * p + 1];
         y[2 * p] = y0 * cs[p] - y1 * sn[p];
         y[2 * p + 1] = y0 * sn[p] + y1 * cs[p];
       }
-      C::store(kr + row0 + (h0 + u) * head_bytes, y);
+      C::store(kr + krow0 + (h0 + u) * head_bytes, y);
     }
   }
 }
@@ -133,12 +137,11 @@ __global__ void __launch_bounds__(256, 4) k_rope(RopeArgs a) {
   char* __restrict__ kr = static_cast<char*>(a.kr);
   const long long head_bytes = (long long)a.head_dim * (long long)sizeof(E);
   const long long tok = m.tok_start + tl * kTile + r;
-  const long long row0 = tok * a.heads * head_bytes + (long long)c * 16;
   const long long t_ref = a.t[m.tok_start];
   // a plan in which no user token queries never reads their Q' rows (their query tiles
   // are skipped or their rows are computed and not written), so they are not rotated
-  if (a.skip_user_q && is_user(a.ty[tok])) rope_rows<E, false>(a, q, k, qr, kr, head_bytes, tok, row0, c, t_ref);
-  else rope_rows<E, true>(a, q, k, qr, kr, head_bytes, tok, row0, c, t_ref);
+  if (a.skip_user_q && is_user(a.ty[tok])) rope_rows<E, false>(a, q, k, qr, kr, head_bytes, tok, c, t_ref);
+  else rope_rows<E, true>(a, q, k, qr, kr, head_bytes, tok, c, t_ref);
 }
 
 // Sum of v over the `group` consecutive lanes that hold one head row (group is a
@@ -196,6 +199,7 @@ __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) 
     const int r = act ? rr : 0, c = (int)threadIdx.x % chunks;
     const long long tok = m.tok_start + tl * kTile + r;
     const long long row0 = tok * a.heads * head_bytes + (long long)c * 16;
+    const long long krow0 = tok * a.kv_heads * head_bytes + (long long)c * 16;
     const bool qg = f.q_gate != nullptr, kg = f.k_gate != nullptr;
     // two heads at a time: their q, k and gate chunks (up to eight 16-byte loads) in flight
     // together, kept raw until used; the first two heads' loads go out before the angles
@@ -205,11 +209,13 @@ __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) 
       for (int u = 0; u < 2; ++u) {
         rq[u] = rk[u] = rgq[u] = rgk[u] = make_uint4(0u, 0u, 0u, 0u);
         if (act && h0 + u < a.heads) {
-          const long long off = row0 + (h0 + u) * head_bytes;
+          const long long off = row0 + (h0 + u) * head_bytes, koff = krow0 + (h0 + u) * head_bytes;
           rq[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + off);
-          rk[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + off);
           if (qg) rgq[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(f.q_gate) + off);
-          if (kg) rgk[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(f.k_gate) + off);
+          if (h0 + u < a.kv_heads) {
+            rk[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + koff);
+            if (kg) rgk[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(f.k_gate) + koff);
+          }
         }
       }
     };
@@ -232,7 +238,8 @@ __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) 
         C::unpack(rgk[u], gy);
         const int e0 = h * a.head_dim + c * 2 * kPairs;
         norm_gate<E>(x, act, f.q_norm_w, f.eps, qg, gx, e0, chunks, a.head_dim);
-        norm_gate<E>(y, act, f.k_norm_w, f.eps, kg, gy, e0, chunks, a.head_dim);
+        const bool has_k = h < a.kv_heads;  // uniform across the block
+        if (has_k) norm_gate<E>(y, act, f.k_norm_w, f.eps, kg, gy, e0, chunks, a.head_dim);
 #pragma unroll
         for (int p = 0; p < kPairs; ++p) {
           const float x0 = x[2 * p], x1 = x[2 * p + 1], y0 = y[2 * p], y1 = y[2 * p + 1];
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) 
         }
         if (act) {
           C::store(static_cast<char*>(a.qr) + off, x);
-          C::store(static_cast<char*>(a.kr) + off, y);
+          if (has_k) C::store(static_cast<char*>(a.kr) + krow0 + h * head_bytes, y);
         }
       }
     }
@@ -269,11 +276,14 @@ __global__ void __launch_bounds__(256, 4) k_rope_slots(SlotArgs a) {
   const long long head_bytes = (long long)a.head_dim * (long long)sizeof(E);
   const long long dst = rq.dst_start + row;
   const long long d0 = dst * a.heads * head_bytes + (long long)c * 16;
+  const long long dk0 = dst * a.kv_heads * head_bytes + (long long)c * 16;
   if (row >= rq.len) {  // padding
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     for (int h = 0; h < a.heads; ++h) {
-      *reinterpret_cast<uint4*>(static_cast<char*>(a.k_dst) + d0 + h * head_bytes) = z;
-      *reinterpret_cast<uint4*>(static_cast<char*>(a.v_dst) + d0 + h * head_bytes) = z;
+      if (h < a.kv_heads) {
+        *reinterpret_cast<uint4*>(static_cast<char*>(a.k_dst) + dk0 + h * head_bytes) = z;
+        *reinterpret_cast<uint4*>(static_cast<char*>(a.v_dst) + dk0 + h * head_bytes) = z;
+      }
       if (a.q_dst) *reinterpret_cast<uint4*>(static_cast<char*>(a.q_dst) + d0 + h * head_bytes) = z;
     }
     if (c == 0) {
@@ -285,6 +295,7 @@ __global__ void __launch_bounds__(256, 4) k_rope_slots(SlotArgs a) {
   }
   const long long src = rq.src_start + row;
   const long long s0 = src * a.heads * head_bytes + (long long)c * 16;
+  const long long sk0 = src * a.kv_heads * head_bytes + (long long)c * 16;
   const long long t_ref = rq.ref_dst ? a.t_dst[rq.ref_row] : a.t_src[rq.ref_row];
   const long long ts = a.t_src[src];
   const float dt = (float)(ts - t_ref);  // exact int64 difference, then fp32
@@ -293,18 +304,21 @@ __global__ void __launch_bounds__(256, 4) k_rope_slots(SlotArgs a) {
   for (int p = 0; p < kPairs; ++p) sincosf(dt * a.omega[c * kPairs + p], &sn[p], &cs[p]);
   for (int h = 0; h < a.heads; ++h) {
     const long long so = s0 + h * head_bytes, dof = d0 + h * head_bytes;
-    const uint4 rk = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k_src) + so);
-    const uint4 rv = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v_src) + so);
-    float y[8];
-    C::unpack(rk, y);
+    if (h < a.kv_heads) {
+      const long long sk = sk0 + h * head_bytes, dk = dk0 + h * head_bytes;
+      const uint4 rk = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k_src) + sk);
+      const uint4 rv = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v_src) + sk);
+      float y[8];
+      C::unpack(rk, y);
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      const float y0 = y[2 * p], y1 = y[2 * p + 1];
-      y[2 * p] = y0 * cs[p] - y1 * sn[p];
-      y[2 * p + 1] = y0 * sn[p] + y1 * cs[p];
+      for (int p = 0; p < kPairs; ++p) {
+        const float y0 = y[2 * p], y1 = y[2 * p + 1];
+        y[2 * p] = y0 * cs[p] - y1 * sn[p];
+        y[2 * p + 1] = y0 * sn[p] + y1 * cs[p];
+      }
+      C::store(static_cast<char*>(a.k_dst) + dk, y);
+      *reinterpret_cast<uint4*>(static_cast<char*>(a.v_dst) + dk) = rv;
     }
-    C::store(static_cast<char*>(a.k_dst) + dof, y);
-    *reinterpret_cast<uint4*>(static_cast<char*>(a.v_dst) + dof) = rv;
     if (a.q_src) {
       float x[8];
       C::load(static_cast<const char*>(a.q_src) + so, x);

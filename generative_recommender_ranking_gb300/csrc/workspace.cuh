@@ -22,9 +22,9 @@ inline int mask_capacity(long long NT, long long NC) {
 
 inline size_t ws_up(size_t x) { return (x + 255) & ~size_t(255); }
 
-// rot_bytes: bytes of one rotated [T][H][d] copy (0 when the RoPE is off); mcap: slots
+// rot_q, rot_k: bytes of the rotated Q and K copies (0 when the RoPE is off); mcap: slots
 // of the mask table (0: none).
-inline WsLayout ws_layout(long long batch, long long NT, long long NC, long long heads, size_t rot_bytes,
+inline WsLayout ws_layout(long long batch, long long NT, long long NC, long long heads, size_t rot_q, size_t rot_k,
                           int mcap) {
   WsLayout L;
   L.mcap = mcap;
@@ -48,8 +48,8 @@ inline WsLayout ws_layout(long long batch, long long NT, long long NC, long long
   L.ps = off; off = ws_up(off + 4 * (size_t)NC);
   L.mi = off; off = ws_up(off + 8 * (size_t)mcap);
   L.mt = off; off = ws_up(off + 16 * (size_t)kTile * (size_t)mcap);
-  L.rq = off; off = ws_up(off + rot_bytes);
-  L.rk = off; off = ws_up(off + rot_bytes);
+  L.rq = off; off = ws_up(off + rot_q);
+  L.rk = off; off = ws_up(off + rot_k);
   L.total = off;
   return L;
 }

@@ -154,6 +154,30 @@ rec_attn_status rec_attn_plan_query_pruned(const rec_attn_params* params, int32_
                                            rec_attn_plan_t** plan_out);
 
 /*
+ * rec_attn_plan_grouped -- rec_attn_plan_query_pruned for attention whose query heads
+ * share key/value heads in groups: params->num_heads = H query heads, num_kv_heads = Hk
+ * key/value heads, and query head h reads key/value head h / (H / Hk).  (The pages give
+ * every query head its own keys and values; Hk = H is that case and gives the same
+ * results as the plans above.)
+ *
+ *   num_kv_heads       1 <= Hk <= H, H a multiple of Hk.
+ *   keep_user_queries  as for rec_attn_plan_query_pruned (-1: every query).
+ *
+ * Every call that takes a plan takes this one.  On it the key-side tensors of those
+ * calls have Hk heads: k, v, dk and dv (and the history's and candidates' keys and
+ * values of a grouped cache) are [T][Hk][d], k_gate and dk_gate [T][Hk][d], k_norm_weight
+ * and dk_norm_weight [Hk][d]; the query-side tensors and lse keep H heads.  dk and dv are
+ * the sums over the query heads of the group, accumulated in fp32 and rounded once.
+ * Masks, time-RoPE, types, errors and ownership as for rec_attn_plan; INVALID_ARG also
+ * for num_kv_heads that does not divide num_heads.
+ */
+rec_attn_status rec_attn_plan_grouped(const rec_attn_params* params, int32_t num_kv_heads,
+                                      int32_t keep_user_queries, int32_t batch,
+                                      const int64_t* offsets_host, const int64_t* offsets_dev,
+                                      const int64_t* timestamps_dev, const int8_t* types_dev,
+                                      void* stream, rec_attn_plan_t** plan_out);
+
+/*
  * rec_attn_query_keep -- LazFormer Eq. 22: user queries kept at layer `layer`
  * (1-based) of an `n_layers`-layer stack, N_l = min(hist_len, max(n_min,
  * Round[hist_len - (layer - 1) / (n_layers - 1) * (hist_len - n_min)])), Round to the
@@ -324,6 +348,37 @@ rec_attn_status rec_attn_compress(int32_t batch, const int64_t* offsets_host,
                                   int8_t* types_out, void* stream);
 
 /*
+ * Layer norm of packed token rows, with a gain and a bias for each token type (MTGR
+ * notes on the blog index page: GroupLayerNorm, a layer norm per kind of token) or one of
+ * each for every row.  Row x of group g (its type, or 0 without types):
+ *   y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight[g] + bias[g].
+ * rec_attn_layernorm_bwd gives, for the upstream gradient dy, dx and the sums over each
+ * group's rows dweight[g] = sum dy (x - mean) / sqrt(var + eps), dbias[g] = sum dy.
+ *   dtype    rec_attn_dtype of x, y, dy and dx; the gains and their gradients are float.
+ *   x, y, dy, dx  device [rows][width], 16-byte aligned, width * element size a multiple
+ *            of 16 bytes, width <= 16384.  y may be x itself, dx may be x or dy itself; any
+ *            other overlap of an output with an input or output is refused.
+ *   num_groups  1: one gain and bias for every row, types NULL; 4: one for each token type.
+ *   types    device int8[rows] (0..3) when num_groups is 4.  A row whose type is outside
+ *            0..3 belongs to no group: its y or dx is zero and it adds nothing.
+ *   weight, bias, dweight, dbias  device float [num_groups][width], 16-byte aligned; bias may be NULL (zero), dweight and dbias may be NULL (not
+ *            wanted).  dweight and dbias are overwritten (zero for a group without rows).
+ *   eps      >= 0, finite.
+ * Statistics and sums are fp32 (the variance from the differences to the mean); outputs are
+ * rounded once.  The sums have a fixed order: equal calls give equal bits.  The backward
+ * recomputes the statistics and takes a workspace from the library pool on `stream`.
+ * Asynchronous; both calls may be captured into a CUDA graph.
+ * Errors: INVALID_ARG, UNSUPPORTED (width > 16384, rows >= 2^31), OOM, CUDA.
+ */
+rec_attn_status rec_attn_layernorm_fwd(int32_t dtype, int64_t rows, int64_t width, int32_t num_groups,
+                                       const void* x, const int8_t* types, const float* weight,
+                                       const float* bias, float eps, void* y, void* stream);
+rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows, int64_t width, int32_t num_groups,
+                                       const void* x, const int8_t* types, const float* weight,
+                                       float eps, const void* dy, void* dx, float* dweight,
+                                       float* dbias, void* stream);
+
+/*
  * rec_attn_fwd_compress -- rec_attn_fwd whose output is written already compressed:
  * the history compression above (same segments, hist_begin / hist_len per request, same
  * output layout, times and types) applied to the attention output O, fused into the
@@ -436,6 +491,11 @@ rec_attn_status rec_attn_visible_pairs(rec_attn_plan_t* plan, uint64_t* host_out
  * Errors: INVALID_ARG (NULL cache or pointers, misalignment, aliasing, more than
  * max_cands candidates, another current device), OOM, CUDA.  Asynchronous.
  *
+ * rec_attn_cache_create_grouped -- rec_attn_cache_create for query heads that share
+ * num_kv_heads key/value heads (as in rec_attn_plan_grouped): k_hist, v_hist, and the
+ * k_cand, v_cand of every rec_attn_cache_score on it, have num_kv_heads heads.
+ * INVALID_ARG also for num_kv_heads that does not divide params->num_heads.
+ *
  * rec_attn_cache_free -- release a cache (NULL-safe).  Synchronizes the device
  * (cudaFree), so work still reading the cache completes first.
  */
@@ -444,6 +504,12 @@ rec_attn_status rec_attn_cache_create(const rec_attn_params* params, int32_t bat
                                       const int64_t* hist_offsets_host, const int64_t* hist_t_dev,
                                       const int8_t* hist_types_dev, const void* k_hist, const void* v_hist,
                                       int32_t max_cands, void* stream, rec_attn_kv_cache_t** cache_out);
+rec_attn_status rec_attn_cache_create_grouped(const rec_attn_params* params, int32_t num_kv_heads,
+                                              int32_t batch, const int64_t* hist_offsets_host,
+                                              const int64_t* hist_t_dev, const int8_t* hist_types_dev,
+                                              const void* k_hist, const void* v_hist,
+                                              int32_t max_cands, void* stream,
+                                              rec_attn_kv_cache_t** cache_out);
 rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* cache, const int64_t* cand_offsets_host,
                                      const int64_t* cand_t_dev, const void* q_cand, const void* k_cand,
                                      const void* v_cand, void* out, float* lse, void* stream);
