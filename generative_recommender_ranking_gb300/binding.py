@@ -461,6 +461,17 @@ def rec_attn_cache_score(cache: KVCache, cand_offsets_host, cand_t, q, k, v, out
                                                           _ptr(v), _ptr(out), _ptr(lse), _stream(stream)))
 
 
+def rec_attn_cache_device_status(cache: KVCache, stream=None) -> int:
+    """Status word of a bf16 cache with shared heads (OK for other caches)."""
+    L = lib()
+    L.rec_attn_cache_device_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p]
+    L.rec_attn_cache_device_status.restype = ctypes.c_int
+    s = ctypes.c_int32()
+    _check("rec_attn_cache_device_status", L.rec_attn_cache_device_status(cache.handle, ctypes.byref(s),
+                                                                          _stream(stream)))
+    return int(s.value)
+
+
 def rec_attn_cache_free(cache: KVCache) -> None:
     if cache is not None and cache.handle:
         L = lib()

@@ -101,13 +101,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D map over a [T][H*d] bf16 tensor; box = 64 columns x 128 rows, 128-byte swizzle.
-bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols) {
+// 2-D map over a [T][H*d] bf16 tensor; box = 64 columns x `rows` rows, 128-byte swizzle.
+bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, int rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)T};
   cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)kTile};
+  cuuint32_t box[2] = {64, (cuuint32_t)rows};
   cuuint32_t es[2] = {1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1223,6 +1223,15 @@ struct rec_attn_kv_cache_s {
   int8_t* ty = nullptr;
   int64_t* off_dev = nullptr;
   float omega[kMaxPairs] = {};
+  // bf16 with shared heads: the history rows alone (K' and V packed as the caller's history),
+  // read in place by the kernels of score.cu; no slots
+  bool shared = false;
+  long long Th = 0;
+  int num_sms = 0;
+  long long *need = nullptr, *block_need = nullptr, *t_ref = nullptr;
+  int* block_off = nullptr;
+  int* status = nullptr;
+  CUtensorMap map_k, map_v;
 };
 
 namespace {
@@ -1268,7 +1277,162 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 namespace {
 
-rec_attn_status cache_create_impl(const rec_attn_params* params, int32_t kv_heads, int32_t batch,
+// The buffer of a bf16 cache with shared heads, and the kernels that fill it: K' rotated
+// against each request's first time, V copied, and the times from which each key is visible.
+rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offsets_host, const int64_t* hist_t_dev,
+                              const int8_t* hist_types_dev, const void* k_hist, const void* v_hist, void* stream,
+                              rec_attn_kv_cache_t** cache_out) {
+  const rec_attn_params& p = c->p;
+  const int32_t B = c->batch;
+  const long long Th = c->Th;
+  std::vector<int> block_off((size_t)B + 1, 0);
+  for (int32_t b = 0; b < B; ++b)
+    block_off[b + 1] = block_off[b] + (int)((c->hist_len[b] + kNeedBlock - 1) / kNeedBlock);
+  const int blocks = block_off[B];
+  const size_t kv = ws_up((size_t)Th * c->kv_heads * p.head_dim * 2), th8 = ws_up((size_t)Th * 8);
+  const size_t off_t = 2 * kv, off_ty = off_t + th8, off_need = off_ty + ws_up((size_t)Th);
+  const size_t off_bn = off_need + th8, off_ref = off_bn + ws_up((size_t)blocks * 8);
+  // the tables go up in one copy: hist_off, block_off, the status word
+  const size_t tab_bo = ws_up(8 * ((size_t)B + 1)), tab_st = tab_bo + ws_up(4 * ((size_t)B + 1));
+  const size_t off_tab = off_ref + ws_up(8 * (size_t)B), total = off_tab + tab_st + 256;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaMemPool_t pool;
+  cudaError_t e = device_and_sms(&c->device, &c->num_sms);
+  if (e == cudaSuccess) e = pool_for(c->device, &pool);
+  if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&c->buf, total, pool, st);
+  if (e != cudaSuccess) { delete c; return from_cuda(e); }
+  char* w = static_cast<char*>(c->buf);
+  c->k = w; c->v = w + kv;
+  c->t = reinterpret_cast<long long*>(w + off_t);
+  c->ty = reinterpret_cast<int8_t*>(w + off_ty);
+  c->need = reinterpret_cast<long long*>(w + off_need);
+  c->block_need = reinterpret_cast<long long*>(w + off_bn);
+  c->t_ref = reinterpret_cast<long long*>(w + off_ref);
+  c->off_dev = reinterpret_cast<int64_t*>(w + off_tab);
+  c->block_off = reinterpret_cast<int*>(w + off_tab + tab_bo);
+  c->status = reinterpret_cast<int*>(w + off_tab + tab_st);
+  std::vector<char> up(tab_st + 256, 0);
+  std::memcpy(up.data(), hist_offsets_host, 8 * ((size_t)B + 1));
+  std::memcpy(up.data() + tab_bo, block_off.data(), 4 * ((size_t)B + 1));
+  e = cudaMemcpyAsync(w + off_tab, up.data(), up.size(), cudaMemcpyHostToDevice, st);  // staged before the call returns
+  if (e == cudaSuccess) e = cudaMemsetAsync(c->t_ref, 0, 8 * (size_t)B, st);
+  if (e == cudaSuccess && Th > 0) {
+    const int tk = score_tile_keys(p.head_dim);
+    const long long cols = (long long)c->kv_heads * p.head_dim;
+    if (!encode_map(&c->map_k, c->k, Th, cols, tk) || !encode_map(&c->map_v, c->v, Th, cols, tk)) e = cudaErrorUnknown;
+    std::vector<SlotReq> reqs((size_t)B);
+    for (int32_t b = 0; b < B; ++b) {
+      SlotReq& r = reqs[b];
+      r.src_start = r.dst_start = r.ref_row = hist_offsets_host[b];
+      r.ref_dst = 0;
+      r.len = r.cap = (int)c->hist_len[b];
+      r.pad = 0;
+    }
+    const SlotTable tab = slot_table(reqs);
+    void* dtab = nullptr;
+    if (e == cudaSuccess) e = upload_table(tab, c->device, st, &dtab);
+    if (e == cudaSuccess) {
+      SlotArgs a{};
+      a.req = static_cast<const SlotReq*>(dtab);
+      a.chunk_req = reinterpret_cast<const int*>(static_cast<char*>(dtab) + tab.off_chunk_req);
+      a.chunk_row0 = reinterpret_cast<const int*>(static_cast<char*>(dtab) + tab.off_chunk_row0);
+      a.t_src = reinterpret_cast<const long long*>(hist_t_dev);
+      a.ty_src = hist_types_dev;
+      a.k_src = k_hist; a.v_src = v_hist;
+      a.k_dst = c->k; a.v_dst = c->v; a.t_dst = c->t; a.ty_dst = c->ty;
+      a.heads = a.kv_heads = c->kv_heads; a.head_dim = p.head_dim;
+      std::memcpy(a.omega, c->omega, sizeof a.omega);
+      e = launch_rope_slots(a, p.dtype, tab.n_chunks, st);
+    }
+    if (dtab) {
+      const cudaError_t ef = cudaFreeAsync(dtab, st);
+      if (e == cudaSuccess) e = ef;
+    }
+    if (e == cudaSuccess) {
+      NeedArgs n{};
+      n.hist_off = reinterpret_cast<const long long*>(c->off_dev);
+      n.block_off = c->block_off; n.t = c->t; n.ty = c->ty; n.batch = B;
+      n.use_delay = p.use_delay; n.delay = p.delay_s;
+      n.need = c->need; n.block_need = c->block_need; n.t_ref = c->t_ref; n.status = c->status;
+      e = launch_score_need(n, blocks, st);
+    }
+  }
+  if (e != cudaSuccess) {
+    cudaFreeAsync(c->buf, st);
+    delete c;
+    return from_cuda(e);
+  }
+  *cache_out = c;
+  return REC_ATTN_OK;
+}
+
+// One scoring call on such a cache (arguments checked): requests in launches of kScoreMaxReq.
+rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_offsets_host, const int64_t* cand_t_dev,
+                             const void* q, const void* k, const void* v, void* out, float* lse, cudaStream_t st) {
+  const rec_attn_params& p = c->p;
+  const int G = p.num_heads / c->kv_heads, D = p.head_dim, tk = score_tile_keys(D);
+  ScoreArgs a{};
+  a.hist_off = reinterpret_cast<const long long*>(c->off_dev);
+  a.need = c->need; a.block_need = c->block_need; a.block_off = c->block_off; a.t_ref = c->t_ref; a.status = c->status;
+  a.tc = reinterpret_cast<const long long*>(cand_t_dev);
+  a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse;
+  a.heads = p.num_heads; a.kv_heads = c->kv_heads; a.rotate = p.use_rope;
+  a.tile_keys = tk;
+  a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
+  std::memcpy(a.omega, c->omega, sizeof a.omega);
+  for (int32_t b0 = 0; b0 < c->batch; b0 += kScoreMaxReq) {
+    const int n = std::min<int32_t>(kScoreMaxReq, c->batch - b0);
+    long long max_rows = 0;
+    for (int i = 0; i < n; ++i)
+      max_rows = std::max<long long>(max_rows, (cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G);
+    if (max_rows == 0) continue;
+    const int rows = score_rows_per_item(D, (int)std::min<long long>(max_rows, 1024));
+    // key tiles per block: about four blocks for each of the two places on every SM, so that
+    // blocks of unequal histories even out
+    auto groups_of = [&](int i) {
+      return ((cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G + rows - 1) / rows * c->kv_heads;
+    };
+    auto tiles_of = [&](int i) { return (c->hist_len[b0 + i] + tk - 1) / tk; };
+    long long work = 0;
+    for (int i = 0; i < n; ++i) work += groups_of(i) * tiles_of(i);
+    a.chunk_tiles = (int)std::max<long long>(1, (work + 8LL * c->num_sms - 1) / (8LL * c->num_sms));
+    long long items = 0, most_splits = 1;
+    for (int i = 0; i < n; ++i) {
+      a.cand_start[i] = (int)cand_offsets_host[b0 + i];
+      a.item_start[i] = (int)items;
+      const long long splits = std::max<long long>(1, (tiles_of(i) + a.chunk_tiles - 1) / a.chunk_tiles);
+      items += groups_of(i) * splits;
+      if (groups_of(i) > 0) most_splits = std::max(most_splits, splits);
+      if (items >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
+    }
+    a.cand_start[n] = (int)cand_offsets_host[b0 + n];
+    a.item_start[n] = (int)items;
+    a.req0 = b0;
+    a.n_req = n;
+    void* ws = nullptr;
+    cudaError_t e = cudaSuccess;
+    a.part_ml = nullptr;
+    if (most_splits > 1) {
+      const size_t ml = ws_up((size_t)items * rows * sizeof(float2));
+      cudaMemPool_t pool;
+      e = pool_for(c->device, &pool);
+      if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&ws, ml + (size_t)items * rows * D * sizeof(float), pool, st);
+      if (e != cudaSuccess) return from_cuda(e);
+      a.part_ml = static_cast<float2*>(ws);
+      a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + ml);
+    }
+    e = launch_score_rows(c->map_k, c->map_v, a, D, rows, (int)items, st);
+    if (ws) {
+      const cudaError_t ef = cudaFreeAsync(ws, st);
+      if (e == cudaSuccess) e = ef;
+    }
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  return REC_ATTN_OK;
+}
+
+// shared: a cache of rec_attn_cache_create_grouped.
+rec_attn_status cache_create_impl(const rec_attn_params* params, int32_t kv_heads, bool shared, int32_t batch,
                                   const int64_t* hist_offsets_host, const int64_t* hist_t_dev,
                                   const int8_t* hist_types_dev, const void* k_hist, const void* v_hist,
                                   int32_t max_cands, void* stream, rec_attn_kv_cache_t** cache_out) {
@@ -1317,6 +1481,9 @@ rec_attn_status cache_create_impl(const rec_attn_params* params, int32_t kv_head
     for (int i = 0; i < params->head_dim / 2 && i < kMaxPairs; ++i)
       c->omega[i] = (float)(params->phi_min / params->dt_max_s *
                             std::pow(params->rope_base, 2.0 * i / (double)params->head_dim));
+  c->shared = shared && params->dtype == REC_ATTN_BF16;
+  c->Th = Th;
+  if (c->shared) return create_shared(c, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist, v_hist, stream, cache_out);
   const size_t elem = params->dtype == REC_ATTN_BF16 ? 2 : 4;
   const size_t rows_bytes = ws_up((size_t)Tc * params->num_heads * params->head_dim * elem);
   const size_t kvr_bytes = ws_up((size_t)Tc * kv_heads * params->head_dim * elem);
@@ -1389,7 +1556,7 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create(const rec_attn_params* params
                                                    const int8_t* hist_types_dev, const void* k_hist,
                                                    const void* v_hist, int32_t max_cands, void* stream,
                                                    rec_attn_kv_cache_t** cache_out) {
-  return cache_create_impl(params, params ? params->num_heads : 0, batch, hist_offsets_host, hist_t_dev,
+  return cache_create_impl(params, params ? params->num_heads : 0, false, batch, hist_offsets_host, hist_t_dev,
                            hist_types_dev, k_hist, v_hist, max_cands, stream, cache_out);
 }
 
@@ -1399,7 +1566,7 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create_grouped(const rec_attn_params
                                                            const void* k_hist, const void* v_hist,
                                                            int32_t max_cands, void* stream,
                                                            rec_attn_kv_cache_t** cache_out) {
-  return cache_create_impl(params, num_kv_heads, batch, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist,
+  return cache_create_impl(params, num_kv_heads, true, batch, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist,
                            v_hist, max_cands, stream, cache_out);
 }
 
@@ -1431,6 +1598,10 @@ REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const 
   if (e != cudaSuccess) return from_cuda(e);
   if (dev != c->device) return REC_ATTN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (c->shared) {
+    if (Nc >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
+    return score_shared(c, cand_offsets_host, cand_t_dev, q_cand, k_cand, v_cand, out, lse, st);
+  }
   // the candidate slots: rotated Q' and K' against the request's reference time (its
   // first history row, else its first candidate), V, time and type CAND; padding after
   std::vector<SlotReq> reqs((size_t)c->batch);
@@ -1478,6 +1649,19 @@ REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const 
   }
   if (s != REC_ATTN_OK) return s;
   return from_cuda(e);
+}
+
+REC_ATTN_API rec_attn_status rec_attn_cache_device_status(rec_attn_kv_cache_t* c, int32_t* status_out, void* stream) {
+  if (!c || !status_out) return REC_ATTN_ERR_INVALID_ARG;
+  int s = 0;
+  if (c->status) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(&s, c->status, sizeof s, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  *status_out = s;
+  return REC_ATTN_OK;
 }
 
 REC_ATTN_API void rec_attn_cache_free(rec_attn_kv_cache_t* c) {

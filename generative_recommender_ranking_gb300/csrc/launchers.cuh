@@ -43,6 +43,49 @@ cudaError_t launch_bwd_norm_gate(const NormGateArgs& a, int dtype, cudaStream_t 
 // req_len: device int [B] request lengths.
 cudaError_t launch_cmp_fixup(const CmpArgs& c, int batch, const int* req_len, long long n_fix, int heads,
                              int head_dim, cudaStream_t st);
+// Candidates against a cached history with shared heads (score.cu).
+constexpr int kNeedBlock = 64;     // keys per entry of block_need
+constexpr int kScoreMaxReq = 1000; // requests per launch (their tables are kernel parameters)
+struct ScoreArgs {
+  // the cache
+  const long long* hist_off;    // [B + 1] rows of each request in K', V
+  const long long* need;        // [Th]: least time of a candidate that sees the key
+  const long long* block_need;  // per 64-key block of a request: the largest of its keys' need
+  const int* block_off;         // [B + 1] first block of each request
+  const long long* t_ref;       // [B] the rotation's reference time
+  int* status;
+  // the call
+  const long long* tc;          // [Nc]
+  const void *q, *k, *v;        // [Nc][heads or kv_heads][d], not rotated
+  void* out;
+  float* lse;
+  float2* part_ml;              // [items][rows per item]: maximum and sum; null: one part per row
+  float* part_o;                // [items][rows per item][d]: unnormalised outputs
+  int heads, kv_heads;
+  int rotate;
+  int tile_keys, chunk_tiles;   // keys per tile, tiles per item
+  float scale_log2;             // softmax scale * log2(e)
+  float omega[kMaxPairs];
+  int req0, n_req;              // the launch's requests
+  int cand_start[kScoreMaxReq + 1];  // first candidate of each
+  int item_start[kScoreMaxReq + 1];  // first block of each: [row group][kv head][run of tiles]
+};
+struct NeedArgs {
+  const long long* hist_off;
+  const int* block_off;
+  const long long* t;
+  const int8_t* ty;
+  int batch, use_delay;
+  long long delay;
+  long long *need, *block_need, *t_ref;
+  int* status;
+};
+int score_tile_keys(int head_dim);
+int score_rows_per_item(int head_dim, int max_rows);
+cudaError_t launch_score_need(const NeedArgs& a, int blocks, cudaStream_t st);
+cudaError_t launch_score_rows(const CUtensorMap& k, const CUtensorMap& v, const ScoreArgs& a, int head_dim,
+                              int rows_per_item, int items, cudaStream_t st);
+
 // Layer norm (layernorm.cu).
 struct NormArgs {
   long long rows;
@@ -79,9 +122,9 @@ cudaError_t launch_attn_tc(const AttnArgs& a, const CUtensorMap& q, const CUtens
 
 // Host helpers shared by the entry points (api.cu): the parameter checks of
 // rec_attn_params, and a 2-D TMA map over a [T][cols] bf16 tensor (box 64 columns x
-// 128 rows, 128-byte swizzle).
+// `rows` rows, 128-byte swizzle).
 rec_attn_status check_params(const rec_attn_params* p);
-bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols);
+bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, int rows = kTile);
 // 1 when the plan's items run over many key tiles (AttnArgs::long_items).
 int long_items(const rec_attn_params& p, int batch, long long n_tiles);
 

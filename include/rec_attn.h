@@ -495,6 +495,18 @@ rec_attn_status rec_attn_visible_pairs(rec_attn_plan_t* plan, uint64_t* host_out
  * num_kv_heads key/value heads (as in rec_attn_plan_grouped): k_hist, v_hist, and the
  * k_cand, v_cand of every rec_attn_cache_score on it, have num_kv_heads heads.
  * INVALID_ARG also for num_kv_heads that does not divide params->num_heads.
+ * In bf16 such a cache keeps only the history's rotated keys, its values and the time
+ * from which each key is visible to a candidate; a scoring call reads them once for all
+ * candidates and all heads of a group, plans nothing and writes nothing into the cache, so
+ * calls on one cache may overlap on any streams and may be captured into a CUDA graph (the
+ * candidate counts are those of the capture).  Its workspace comes from the library pool on
+ * `stream`.  A history key whose type is not GLOBAL, HIST or RT, or whose time is not
+ * within +-2^62, is seen by no candidate.  (fp32: as rec_attn_cache_create, with slots.)
+ *
+ * rec_attn_cache_device_status -- the status word of a bf16 cache with shared heads
+ * (REC_ATTN_OK, REC_ATTN_ERR_DEVICE_INPUT for a history type outside 0..3 or a time out of
+ * range, REC_ATTN_ERR_TIMEOUT; the first error wins; other caches: REC_ATTN_OK).
+ * Synchronizes `stream`.  Errors: INVALID_ARG, CUDA.
  *
  * rec_attn_cache_free -- release a cache (NULL-safe).  Synchronizes the device
  * (cudaFree), so work still reading the cache completes first.
@@ -513,6 +525,7 @@ rec_attn_status rec_attn_cache_create_grouped(const rec_attn_params* params, int
 rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* cache, const int64_t* cand_offsets_host,
                                      const int64_t* cand_t_dev, const void* q_cand, const void* k_cand,
                                      const void* v_cand, void* out, float* lse, void* stream);
+rec_attn_status rec_attn_cache_device_status(rec_attn_kv_cache_t* cache, int32_t* status_out, void* stream);
 void rec_attn_cache_free(rec_attn_kv_cache_t* cache);
 
 /*

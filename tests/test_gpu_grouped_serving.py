@@ -136,6 +136,7 @@ def test_against_the_oracle(name):
     with b.cache() as cache:
         out, lse = b.score(cache)
         again, _ = b.score(cache, with_lse=False)
+        assert bd.rec_attn_cache_device_status(cache) == bd.OK
     if name == "large_scores":  # scores of rms 9 carry nine times the rounding of unit ones
         ref, _ = b.reference()
         assert np.linalg.norm(gu.to_f64(out) - ref) <= 9 * 6.6e-3 * np.linalg.norm(ref)
@@ -198,3 +199,77 @@ def test_refusals():
         assert code(q=q.data_ptr() + 8) == bd.ERR_INVALID_ARG
         assert code(off=(0, 0), tc=None, q=None, k=None, v=None, out=None) == bd.OK  # nothing to score
         torch.cuda.synchronize()
+
+
+def test_two_streams_and_a_graph_share_one_cache():
+    """Calls on one bf16 cache write nothing into it: two at once, and a replayed capture whose
+    inputs change between replays."""
+    b = Batch(hist=[3000, 1200, 64], cands=[3, 1, 2], heads=8, kv=2, d=64, rt=40)
+    with b.cache() as cache:
+        ref, _ = b.score(cache)
+        tc, q, k, v = b.device()
+        streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.empty_like(q) for _ in range(8)]
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            with torch.cuda.stream(streams[i % 2]):
+                bd.rec_attn_cache_score(cache, b.coff, tc, q, k, v, o)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, ref) for o in outs)
+        graphs = []
+        for _ in range(2):
+            out = torch.empty_like(q)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                bd.rec_attn_cache_score(cache, b.coff, tc, q, k, v, out)
+            graphs.append((graph, out))
+        for _ in range(3):
+            for graph, out in graphs:
+                out.fill_(float("nan"))
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, ref) for _, out in graphs)
+        q.copy_(q.flip(0))
+        want = torch.empty_like(q)
+        bd.rec_attn_cache_score(cache, b.coff, tc, q, k, v, want)
+        graphs[0][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[0][1], want) and not torch.equal(want, ref)
+        del graphs
+
+
+def test_rows_behind_the_last_candidate_stay_as_they_were():
+    b = Batch(hist=[300, 50], cands=[2, 1], heads=8, kv=2, d=64)
+    tc, q, k, v = b.device()
+    out = torch.full((8,) + q.shape[1:], 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((8, b.H), 7.0, device="cuda")
+    with b.cache() as cache:
+        bd.rec_attn_cache_score(cache, b.coff, tc, q, k, v, out, lse)
+        torch.cuda.synchronize()
+    assert (out[3:] == 7).all() and (lse[3:] == 7).all() and torch.isfinite(lse[:3]).all()
+
+
+def test_bad_history_keys_are_seen_by_nobody():
+    """Types outside the user side and times out of range: reported where they are device
+    errors, and without weight."""
+    b = Batch(hist=[200], cands=[3], heads=8, kv=2, d=64)
+    with b.cache() as cache:
+        out, _ = b.score(cache)
+    keep = np.ones(200, dtype=bool)
+    keep[[5, 77, 130]] = False
+    b.ty[5], b.ty[77] = 9, W.CAND
+    b.t[130] = 1 << 62
+    with b.cache() as cache:
+        got, lse = b.score(cache)
+        assert bd.rec_attn_cache_device_status(cache) == bd.ERR_DEVICE_INPUT
+    small = Batch(hist=[197], cands=[3], heads=8, kv=2, d=64)
+    small.k, small.v, small.t, small.ty = b.k[keep], b.v[keep], b.t[keep], b.ty[keep]
+    small.qc, small.kc, small.vc, small.tc = b.qc, b.kc, b.vc, b.tc
+    small.check(got, lse)
+
+
+def test_more_requests_than_one_launch_takes():
+    n = 1100
+    b = Batch(hist=[i % 7 for i in range(n)], cands=[i % 3 for i in range(n)], heads=4, kv=2, d=64)
+    with b.cache() as cache:
+        out, lse = b.score(cache)
+    b.check(out, lse)
