@@ -107,6 +107,38 @@ def lib() -> ctypes.CDLL:
         L.rec_attn_device_status.restype = ctypes.c_int
         L.rec_attn_status_string.argtypes = [ctypes.c_int]
         L.rec_attn_status_string.restype = ctypes.c_char_p
+        L.rec_attn_plan_grouped.argtypes = [ctypes.POINTER(RecAttnParams), i32, i32, i32,
+                                            vp, vp, vp, vp, vp, ctypes.POINTER(vp)]
+        L.rec_attn_plan_grouped.restype = ctypes.c_int
+        L.rec_attn_bwd_fused.argtypes = [vp, vp, vp, vp, ctypes.POINTER(RecAttnFused), vp, vp, vp, vp, vp, vp,
+                                         ctypes.POINTER(RecAttnFusedGrads), vp]
+        L.rec_attn_bwd_fused.restype = ctypes.c_int
+        L.rec_attn_layernorm_fwd.argtypes = [i32, i64, i64, i32, vp, vp, vp, vp, ctypes.c_float, vp, vp]
+        L.rec_attn_layernorm_fwd.restype = ctypes.c_int
+        L.rec_attn_layernorm_bwd.argtypes = [i32, i64, i64, i32, vp, vp, vp, ctypes.c_float, vp, vp,
+                                             vp, vp, vp]
+        L.rec_attn_layernorm_bwd.restype = ctypes.c_int
+        L.rec_attn_fwd_compress.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+        L.rec_attn_fwd_compress.restype = ctypes.c_int
+        L.rec_attn_cache_create.argtypes = [ctypes.POINTER(RecAttnParams), i32, vp, vp, vp, vp, vp,
+                                            i32, vp, ctypes.POINTER(vp)]
+        L.rec_attn_cache_create.restype = ctypes.c_int
+        L.rec_attn_cache_create_grouped.argtypes = [ctypes.POINTER(RecAttnParams), i32, i32, vp, vp,
+                                                    vp, vp, vp, i32, vp, ctypes.POINTER(vp)]
+        L.rec_attn_cache_create_grouped.restype = ctypes.c_int
+        L.rec_attn_cache_score.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.rec_attn_cache_score.restype = ctypes.c_int
+        L.rec_attn_cache_device_status.argtypes = [vp, ctypes.POINTER(i32), vp]
+        L.rec_attn_cache_device_status.restype = ctypes.c_int
+        L.rec_attn_applied_masks.argtypes = [vp, i32, vp, i32, vp, vp, vp]
+        L.rec_attn_applied_masks.restype = ctypes.c_int
+        L.rec_attn_enable_timing.argtypes = [vp]
+        L.rec_attn_enable_timing.restype = ctypes.c_int
+        L.rec_attn_read_timings.argtypes = [vp, ctypes.POINTER(RecAttnTimings)]
+        L.rec_attn_read_timings.restype = ctypes.c_int
+        L.rec_attn_fwd_noalloc.argtypes = [ctypes.POINTER(RecAttnParams), i32, vp, vp, vp, vp,
+                                           vp, vp, vp, vp, vp, vp]
+        L.rec_attn_fwd_noalloc.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -122,22 +154,29 @@ def make_params(num_heads: int, head_dim: int, dtype: str = "bf16", use_delay: b
 
 
 def _ptr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     if isinstance(x, np.ndarray):
-        return x.ctypes.data
+        return x.__array_interface__["data"][0]
     return x.data_ptr()  # torch.Tensor
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of torch.cuda.current_stream(), without building the stream object
+        # (a few microseconds, which a small call would notice)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _host_int64(a) -> np.ndarray:
+    if isinstance(a, np.ndarray) and a.dtype == np.int64 and a.flags.c_contiguous:
+        return a
+    return np.ascontiguousarray(np.asarray(a, dtype=np.int64))
 
 
 def _check(fn: str, code: int):
@@ -168,7 +207,7 @@ def rec_attn_plan(params: RecAttnParams, offsets_host, offsets_dev, timestamps_d
                   stream=None) -> Plan:
     """Plan a packed batch.  offsets_host: host int64 [B+1] (numpy or CPU tensor);
     offsets_dev / timestamps_dev: device int64; types_dev: device int8."""
-    off_h = np.ascontiguousarray(np.asarray(offsets_host, dtype=np.int64))
+    off_h = _host_int64(offsets_host)
     B = len(off_h) - 1
     h = ctypes.c_void_p()
     code = lib().rec_attn_plan(ctypes.byref(params), B, _ptr(off_h), _ptr(offsets_dev),
@@ -181,7 +220,7 @@ def rec_attn_plan_query_pruned(params: RecAttnParams, keep_user_queries: int, of
                                timestamps_dev, types_dev, stream=None) -> Plan:
     """rec_attn_plan for a layer that computes every non-user query and the last
     `keep_user_queries` user queries of each request (-1: all)."""
-    off_h = np.ascontiguousarray(np.asarray(offsets_host, dtype=np.int64))
+    off_h = _host_int64(offsets_host)
     B = len(off_h) - 1
     h = ctypes.c_void_p()
     code = lib().rec_attn_plan_query_pruned(ctypes.byref(params), int(keep_user_queries), B, _ptr(off_h),
@@ -197,13 +236,9 @@ def rec_attn_plan_grouped(params: RecAttnParams, num_kv_heads: int, offsets_host
     that share num_kv_heads key/value heads: k, v, dk, dv of every call on the plan are
     [T, num_kv_heads, d]."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_plan_grouped.argtypes = [ctypes.POINTER(RecAttnParams), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
-                                        vp, vp, vp, vp, vp, ctypes.POINTER(vp)]
-    L.rec_attn_plan_grouped.restype = ctypes.c_int
-    off_h = np.ascontiguousarray(np.asarray(offsets_host, dtype=np.int64))
+    off_h = _host_int64(offsets_host)
     B = len(off_h) - 1
-    h = vp()
+    h = ctypes.c_void_p()
     _check("rec_attn_plan_grouped", L.rec_attn_plan_grouped(
         ctypes.byref(params), int(num_kv_heads), int(keep_user_queries), B, _ptr(off_h), _ptr(offsets_dev),
         _ptr(timestamps_dev), _ptr(types_dev), _stream(stream), ctypes.byref(h)))
@@ -251,10 +286,6 @@ def rec_attn_bwd_fused(plan: Plan, q, k, v, out, lse, dout, dq, dk, dv, stream=N
     """Gradients of rec_attn_fwd_fused (the fused steps' arguments as there) into dq, dk,
     dv and the gate / gain gradients of the steps that are on."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_bwd_fused.argtypes = [vp, vp, vp, vp, ctypes.POINTER(RecAttnFused), vp, vp, vp, vp, vp, vp,
-                                     ctypes.POINTER(RecAttnFusedGrads), vp]
-    L.rec_attn_bwd_fused.restype = ctypes.c_int
     f = RecAttnFused(_ptr(q_norm_weight), _ptr(k_norm_weight), float(norm_eps), _ptr(q_gate), _ptr(k_gate),
                      _ptr(out_gate))
     g = RecAttnFusedGrads(_ptr(dq_gate), _ptr(dk_gate), _ptr(dout_gate), _ptr(dq_norm_weight), _ptr(dk_norm_weight))
@@ -272,9 +303,9 @@ def _segments(segments):
 def rec_attn_compress_lengths(offsets_host, hist_begin, hist_len, segments) -> np.ndarray:
     """Output offsets of history compression; segments = [(length or -1, group), ...]
     from the most recent."""
-    off = np.ascontiguousarray(np.asarray(offsets_host, dtype=np.int64))
-    hb = np.ascontiguousarray(np.asarray(hist_begin, dtype=np.int64))
-    hl = np.ascontiguousarray(np.asarray(hist_len, dtype=np.int64))
+    off = _host_int64(offsets_host)
+    hb = _host_int64(hist_begin)
+    hl = _host_int64(hist_len)
     sl, sg = _segments(segments)
     out = np.zeros(len(off), dtype=np.int64)
     _check("rec_attn_compress_lengths",
@@ -286,9 +317,9 @@ def rec_attn_compress_lengths(offsets_host, hist_begin, hist_len, segments) -> n
 def rec_attn_compress(offsets_host, hist_begin, hist_len, segments, x, timestamps, types, x_out, t_out, ty_out,
                       stream=None) -> None:
     """History compression of device rows x [T, width] (bf16 or float32) into x_out."""
-    off = np.ascontiguousarray(np.asarray(offsets_host, dtype=np.int64))
-    hb = np.ascontiguousarray(np.asarray(hist_begin, dtype=np.int64))
-    hl = np.ascontiguousarray(np.asarray(hist_len, dtype=np.int64))
+    off = _host_int64(offsets_host)
+    hb = _host_int64(hist_begin)
+    hl = _host_int64(hist_len)
     sl, sg = _segments(segments)
     import torch
     dtype = BF16 if x.dtype == torch.bfloat16 else FP32
@@ -330,9 +361,6 @@ def rec_attn_layernorm_fwd(x, weight, bias, y, types=None, eps: float = 1e-5, st
     """Layer norm of rows x [rows, width] (bf16 or float32) into y; weight and bias float32
     [1, width], or [4, width] with types int8 [rows]: a gain and bias per token type."""
     L = lib()
-    vp, i64 = ctypes.c_void_p, ctypes.c_int64
-    L.rec_attn_layernorm_fwd.argtypes = [ctypes.c_int32, i64, i64, ctypes.c_int32, vp, vp, vp, vp, ctypes.c_float, vp, vp]
-    L.rec_attn_layernorm_fwd.restype = ctypes.c_int
     dtype, rows, width = _rows("rec_attn_layernorm_fwd", x, y=y)
     groups = _gains("rec_attn_layernorm_fwd", x, types, weight=weight, bias=bias)
     _check("rec_attn_layernorm_fwd", L.rec_attn_layernorm_fwd(dtype, rows, width, groups, _ptr(x), _ptr(types),
@@ -345,10 +373,6 @@ def rec_attn_layernorm_bwd(x, weight, dy, dx, dweight=None, dbias=None, types=No
     """Gradients of rec_attn_layernorm_fwd for the upstream gradient dy: dx, and dweight and
     dbias (float32, shaped as weight; None: not wanted), overwritten."""
     L = lib()
-    vp, i64 = ctypes.c_void_p, ctypes.c_int64
-    L.rec_attn_layernorm_bwd.argtypes = [ctypes.c_int32, i64, i64, ctypes.c_int32, vp, vp, vp, ctypes.c_float, vp, vp,
-                                         vp, vp, vp]
-    L.rec_attn_layernorm_bwd.restype = ctypes.c_int
     dtype, rows, width = _rows("rec_attn_layernorm_bwd", x, dy=dy, dx=dx)
     groups = _gains("rec_attn_layernorm_bwd", x, types, weight=weight, dweight=dweight, dbias=dbias)
     _check("rec_attn_layernorm_bwd", L.rec_attn_layernorm_bwd(dtype, rows, width, groups, _ptr(x), _ptr(types),
@@ -361,11 +385,8 @@ def rec_attn_fwd_compress(plan: Plan, q, k, v, hist_begin, hist_len, segments, x
     """Attention forward whose output is written already history-compressed
     (segments = [(length or -1, group), ...] from the most recent; groups <= 32)."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_fwd_compress.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, vp]
-    L.rec_attn_fwd_compress.restype = ctypes.c_int
-    hb = np.ascontiguousarray(np.asarray(hist_begin, dtype=np.int64))
-    hl = np.ascontiguousarray(np.asarray(hist_len, dtype=np.int64))
+    hb = _host_int64(hist_begin)
+    hl = _host_int64(hist_len)
     sl, sg = _segments(segments)
     _check("rec_attn_fwd_compress", L.rec_attn_fwd_compress(
         plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(hb), _ptr(hl), len(sl), _ptr(sl), _ptr(sg), _ptr(x_out),
@@ -421,11 +442,7 @@ def rec_attn_cache_create(params: RecAttnParams, hist_offsets_host, hist_t, hist
     """Cache the rotated history keys, values, times and types of a batch of requests
     (serving: candidate micro-batches are then scored against them)."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_cache_create.argtypes = [ctypes.POINTER(RecAttnParams), ctypes.c_int32, vp, vp, vp, vp, vp,
-                                        ctypes.c_int32, vp, ctypes.POINTER(vp)]
-    L.rec_attn_cache_create.restype = ctypes.c_int
-    off = np.ascontiguousarray(np.asarray(hist_offsets_host, dtype=np.int64))
+    off = _host_int64(hist_offsets_host)
     h = ctypes.c_void_p()
     _check("rec_attn_cache_create", L.rec_attn_cache_create(
         ctypes.byref(params), len(off) - 1, _ptr(off), _ptr(hist_t), _ptr(hist_types), _ptr(k_hist), _ptr(v_hist),
@@ -438,12 +455,8 @@ def rec_attn_cache_create_grouped(params: RecAttnParams, num_kv_heads: int, hist
     """rec_attn_cache_create for query heads that share num_kv_heads key/value heads:
     k_hist, v_hist [Th, num_kv_heads, d], and the candidates' keys and values alike."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_cache_create_grouped.argtypes = [ctypes.POINTER(RecAttnParams), ctypes.c_int32, ctypes.c_int32, vp, vp,
-                                                vp, vp, vp, ctypes.c_int32, vp, ctypes.POINTER(vp)]
-    L.rec_attn_cache_create_grouped.restype = ctypes.c_int
-    off = np.ascontiguousarray(np.asarray(hist_offsets_host, dtype=np.int64))
-    h = vp()
+    off = _host_int64(hist_offsets_host)
+    h = ctypes.c_void_p()
     _check("rec_attn_cache_create_grouped", L.rec_attn_cache_create_grouped(
         ctypes.byref(params), int(num_kv_heads), len(off) - 1, _ptr(off), _ptr(hist_t), _ptr(hist_types),
         _ptr(k_hist), _ptr(v_hist), int(max_cands), _stream(stream), ctypes.byref(h)))
@@ -453,10 +466,7 @@ def rec_attn_cache_create_grouped(params: RecAttnParams, num_kv_heads: int, hist
 def rec_attn_cache_score(cache: KVCache, cand_offsets_host, cand_t, q, k, v, out, lse=None, stream=None) -> None:
     """Outputs of one micro-batch of candidates per request against the cached history."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_cache_score.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp]
-    L.rec_attn_cache_score.restype = ctypes.c_int
-    off = np.ascontiguousarray(np.asarray(cand_offsets_host, dtype=np.int64))
+    off = _host_int64(cand_offsets_host)
     _check("rec_attn_cache_score", L.rec_attn_cache_score(cache.handle, _ptr(off), _ptr(cand_t), _ptr(q), _ptr(k),
                                                           _ptr(v), _ptr(out), _ptr(lse), _stream(stream)))
 
@@ -464,8 +474,6 @@ def rec_attn_cache_score(cache: KVCache, cand_offsets_host, cand_t, q, k, v, out
 def rec_attn_cache_device_status(cache: KVCache, stream=None) -> int:
     """Status word of a bf16 cache with shared heads (OK for other caches)."""
     L = lib()
-    L.rec_attn_cache_device_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p]
-    L.rec_attn_cache_device_status.restype = ctypes.c_int
     s = ctypes.c_int32()
     _check("rec_attn_cache_device_status", L.rec_attn_cache_device_status(cache.handle, ctypes.byref(s),
                                                                           _stream(stream)))
@@ -489,9 +497,6 @@ def rec_attn_applied_masks(plan: Plan, pairs, mode: int = MASK_APPLIED):
     pairs: returns (bits uint32 [n, 128, 4], list class uint8 [n] (0xff: not listed),
     mask-table slot int32 [n])."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_applied_masks.argtypes = [vp, ctypes.c_int32, vp, ctypes.c_int32, vp, vp, vp]
-    L.rec_attn_applied_masks.restype = ctypes.c_int
     pr = np.ascontiguousarray(np.asarray(pairs, dtype=np.int32).reshape(-1, 3))
     n = pr.shape[0]
     bits = np.zeros((n, TILE, 4), dtype=np.uint32)
@@ -514,16 +519,12 @@ class RecAttnTimings(ctypes.Structure):
 
 def rec_attn_enable_timing(plan: Plan) -> None:
     L = lib()
-    L.rec_attn_enable_timing.argtypes = [ctypes.c_void_p]
-    L.rec_attn_enable_timing.restype = ctypes.c_int
     _check("rec_attn_enable_timing", L.rec_attn_enable_timing(plan.handle))
 
 
 def rec_attn_read_timings(plan: Plan) -> tuple[float, float]:
     """(rope_ms, attn_ms) of the last timed rec_attn_fwd."""
     L = lib()
-    L.rec_attn_read_timings.argtypes = [ctypes.c_void_p, ctypes.POINTER(RecAttnTimings)]
-    L.rec_attn_read_timings.restype = ctypes.c_int
     t = RecAttnTimings()
     _check("rec_attn_read_timings", L.rec_attn_read_timings(plan.handle, ctypes.byref(t)))
     return float(t.rope_ms), float(t.attn_ms)
@@ -537,11 +538,7 @@ def rec_attn_fwd_noalloc(params: RecAttnParams, offsets_host, offsets_dev, times
     """Plan + RoPE + attention without any device allocation (static workspace of
     NOALLOC_SCRATCH_BYTES shared by all calls; calls must not overlap on the GPU)."""
     L = lib()
-    vp = ctypes.c_void_p
-    L.rec_attn_fwd_noalloc.argtypes = [ctypes.POINTER(RecAttnParams), ctypes.c_int32, vp, vp, vp, vp,
-                                       vp, vp, vp, vp, vp, vp]
-    L.rec_attn_fwd_noalloc.restype = ctypes.c_int
-    off_h = np.ascontiguousarray(np.asarray(offsets_host, dtype=np.int64))
+    off_h = _host_int64(offsets_host)
     code = L.rec_attn_fwd_noalloc(ctypes.byref(params), len(off_h) - 1, _ptr(off_h), _ptr(offsets_dev),
                                   _ptr(timestamps_dev), _ptr(types_dev), _ptr(q), _ptr(k), _ptr(v),
                                   _ptr(out), _ptr(lse), _stream(stream))
