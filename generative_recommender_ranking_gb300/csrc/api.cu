@@ -1231,7 +1231,8 @@ struct rec_attn_kv_cache_s {
   long long *need = nullptr, *block_need = nullptr, *t_ref = nullptr;
   int* block_off = nullptr;
   int* status = nullptr;
-  CUtensorMap map_k, map_v;
+  CUtensorMap map_k, map_v;      // boxes of score_tile_keys rows
+  CUtensorMap map_k128, map_v128;  // boxes of 128 rows
 };
 
 namespace {
@@ -1319,7 +1320,9 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
   if (e == cudaSuccess && Th > 0) {
     const int tk = score_tile_keys(p.head_dim);
     const long long cols = (long long)c->kv_heads * p.head_dim;
-    if (!encode_map(&c->map_k, c->k, Th, cols, tk) || !encode_map(&c->map_v, c->v, Th, cols, tk)) e = cudaErrorUnknown;
+    if (!encode_map(&c->map_k, c->k, Th, cols, tk) || !encode_map(&c->map_v, c->v, Th, cols, tk) ||
+        !encode_map(&c->map_k128, c->k, Th, cols) || !encode_map(&c->map_v128, c->v, Th, cols))
+      e = cudaErrorUnknown;
     std::vector<SlotReq> reqs((size_t)B);
     for (int32_t b = 0; b < B; ++b) {
       SlotReq& r = reqs[b];
@@ -1366,18 +1369,21 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
   return REC_ATTN_OK;
 }
 
+// Rows of a key/value head (candidates x heads of the group) above which a call takes the
+// many-row path.
+constexpr int kScoreManyRows = 32;
+
 // One scoring call on such a cache (arguments checked): requests in launches of kScoreMaxReq.
 rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_offsets_host, const int64_t* cand_t_dev,
                              const void* q, const void* k, const void* v, void* out, float* lse, cudaStream_t st) {
   const rec_attn_params& p = c->p;
-  const int G = p.num_heads / c->kv_heads, D = p.head_dim, tk = score_tile_keys(D);
+  const int G = p.num_heads / c->kv_heads, D = p.head_dim;
   ScoreArgs a{};
   a.hist_off = reinterpret_cast<const long long*>(c->off_dev);
   a.need = c->need; a.block_need = c->block_need; a.block_off = c->block_off; a.t_ref = c->t_ref; a.status = c->status;
   a.tc = reinterpret_cast<const long long*>(cand_t_dev);
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse;
   a.heads = p.num_heads; a.kv_heads = c->kv_heads; a.rotate = p.use_rope;
-  a.tile_keys = tk;
   a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
   std::memcpy(a.omega, c->omega, sizeof a.omega);
   for (int32_t b0 = 0; b0 < c->batch; b0 += kScoreMaxReq) {
@@ -1386,9 +1392,13 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
     for (int i = 0; i < n; ++i)
       max_rows = std::max<long long>(max_rows, (cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G);
     if (max_rows == 0) continue;
-    const int rows = score_rows_per_item(D, (int)std::min<long long>(max_rows, 1024));
+    // many rows per key/value head: 128 of them at a time on the tensor cores' large tiles
+    const bool many = max_rows > kScoreManyRows && c->Th > 0;
+    const int tk = many ? kTile : score_tile_keys(D);
+    const int rows = many ? kTile : score_rows_per_item(D, (int)max_rows);
+    a.tile_keys = tk;
     // key tiles per block: about four blocks for each of the two places on every SM, so that
-    // blocks of unequal histories even out
+    // blocks of unequal histories even out (many rows: four items for each stream)
     auto groups_of = [&](int i) {
       return ((cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G + rows - 1) / rows * c->kv_heads;
     };
@@ -1409,19 +1419,41 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
     a.item_start[n] = (int)items;
     a.req0 = b0;
     a.n_req = n;
-    void* ws = nullptr;
+    // workspace: the runs' parts | many rows: Q' in row order, the items and their counters
+    const bool parts = most_splits > 1;
+    const size_t off_o = parts ? ws_up((size_t)items * rows * sizeof(float2)) : 0;
+    const size_t off_q = off_o + (parts ? ws_up((size_t)items * rows * D * sizeof(float)) : 0);
+    const size_t off_it = off_q + (many ? ws_up((size_t)items * kTile * D * 2) : 0);
+    const size_t off_cnt = off_it + (many ? ws_up((size_t)items * sizeof(CandItem)) : 0);
+    const size_t bytes = off_cnt + (many ? 256 : 0);
+    char* ws = nullptr;
     cudaError_t e = cudaSuccess;
-    a.part_ml = nullptr;
-    if (most_splits > 1) {
-      const size_t ml = ws_up((size_t)items * rows * sizeof(float2));
+    if (bytes > 0) {
       cudaMemPool_t pool;
       e = pool_for(c->device, &pool);
-      if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&ws, ml + (size_t)items * rows * D * sizeof(float), pool, st);
+      if (e == cudaSuccess) e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), bytes, pool, st);
       if (e != cudaSuccess) return from_cuda(e);
-      a.part_ml = static_cast<float2*>(ws);
-      a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + ml);
     }
-    e = launch_score_rows(c->map_k, c->map_v, a, D, rows, (int)items, st);
+    a.part_ml = parts ? reinterpret_cast<float2*>(ws) : nullptr;
+    a.part_o = parts ? reinterpret_cast<float*>(ws + off_o) : nullptr;
+    if (!many) {
+      e = launch_score_rows(c->map_k, c->map_v, a, D, rows, (int)items, st);
+    } else {
+      CandItem* desc = reinterpret_cast<CandItem*>(ws + off_it);
+      int* counters = reinterpret_cast<int*>(ws + off_cnt);
+      e = launch_score_pack(a, D, (int)items, desc, ws + off_q, counters, st);
+      CUtensorMap map_q;
+      if (e == cudaSuccess && !encode_map(&map_q, ws + off_q, items * kTile, D)) e = cudaErrorUnknown;
+      AttnArgs t{};
+      t.out = out; t.lse = lse; t.status = c->status; t.counters = counters;
+      t.n_items = items; t.heads = p.num_heads; t.group = G; t.scale = p.softmax_scale;
+      t.cand.items = desc; t.cand.need = c->need; t.cand.block_need = c->block_need; t.cand.tc = a.tc;
+      t.cand.q = q; t.cand.k = k; t.cand.v = v;
+      t.cand.part_ml = a.part_ml; t.cand.part_o = a.part_o; t.cand.kv_heads = c->kv_heads;
+      const int grid = (int)std::min<long long>((items + 1) / 2, c->num_sms);
+      if (e == cudaSuccess) e = launch_attn_tc(t, map_q, c->map_k128, c->map_v128, D, grid, st);
+    }
+    if (e == cudaSuccess && parts) e = launch_score_combine(a, D, rows, st);
     if (ws) {
       const cudaError_t ef = cudaFreeAsync(ws, st);
       if (e == cudaSuccess) e = ef;

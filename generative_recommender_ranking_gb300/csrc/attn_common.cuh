@@ -57,6 +57,32 @@ __host__ __device__ __forceinline__ long long cmp_group_of(const CmpArgs& c, con
   return r.out_start + pi;
 }
 
+// Candidates against a cached history with shared heads (score.cu): one work item of the
+// tensor-core kernel, 128 rows r = candidate * G + head of the group against a run of the
+// request's key tiles, and what the kernel needs besides.
+struct CandItem {
+  long long hist0;   // first history row of the request
+  long long cand0;   // first candidate of the request
+  long long t_lo;    // least time of the item's candidates
+  int len;           // history rows
+  int row0, rows;    // first row, rows
+  int hk;            // key/value head
+  int tile0, n;      // first key tile, key tiles
+  int block0;        // the request's first entry of block_need
+  int pad;
+};
+static_assert(sizeof(CandItem) == 56, "");
+struct CandArgs {
+  const CandItem* items;
+  const long long* need;        // [Th]: least time of a candidate that sees the key
+  const long long* block_need;  // per 64 keys of a request: the largest of them
+  const long long* tc;          // [Nc] candidate times
+  const void *q, *k, *v;        // [Nc][heads or kv_heads][d], not rotated (the candidate's own pair)
+  float2* part_ml;              // [items][128]: maximum and sum of a run (null: the row's only run)
+  float* part_o;                // [items][128][d]: unnormalised outputs
+  int kv_heads;
+};
+
 struct AttnArgs {
   const ReqMeta* meta;
   const int* qreq;
@@ -83,6 +109,7 @@ struct AttnArgs {
   float scale;       // softmax scale (natural-log domain)
   MaskP mask;
   CmpArgs cmp;       // compression epilogue (kernels instantiated with it only)
+  CandArgs cand;     // candidates against a cached history (the CAND instantiations only)
   int long_items;    // 1: the items run over many key tiles (the softmax's lazy maximum pays)
 };
 

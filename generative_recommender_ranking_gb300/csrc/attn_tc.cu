@@ -28,6 +28,13 @@
 //                 is the fp32 sum of the unrounded exponentials.  Row times and types
 //                 come from the query tile's planner record, bulk-copied next to Q.
 // Every wait on an mbarrier is bounded (REC_ATTN_ERR_TIMEOUT in the status word).
+//
+// The CAND instantiations score candidates against a cached history whose key/value heads
+// are shared by groups of G query heads (score.cu): an item is 128 rows (candidate, head of
+// the group) of one request and one key/value head, so all of them read the same keys, and
+// its key tiles are a run of the history's.  Q' comes packed in row order; PARTIAL tiles take
+// each key's time of visibility; the epilogue joins the candidate's own key and value, or
+// leaves the run's maximum, sum and unnormalised output for k_score_combine.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -194,7 +201,7 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 }
 
 // ------------------------------------------------------------------ producer
-template <int D>
+template <int D, bool CAND>
 __device__ void run_producer(const AttnArgs& a, const void* tq, const void* tk, const void* tv, uint8_t* sm,
                              int s, const SBars& B, volatile int* abort_flag) {
   using L = Layout<D>;
@@ -222,45 +229,70 @@ __device__ void run_producer(const AttnArgs& a, const void* tq, const void* tk, 
       ptx::mbar_arrive(B.item_full + slot);
       break;
     }
-    const WorkItem it = decode_item(a, w, true);
-    d->tok0 = it.m.tok_start + (long long)it.qt * kTile;
-    d->pos0 = it.qt * kTile;
-    d->rows = min(kTile, it.m.len - it.qt * kTile);
-    d->h = it.h;
-    d->n = it.n;
-    d->keep = it.keep;
-    d->req = it.b;
+    WorkItem it;
+    CandItem ci;
+    if constexpr (CAND) {
+      ci = a.cand.items[w];
+      d->tok0 = w * kTile;
+      d->pos0 = ci.row0;
+      d->rows = ci.rows;
+      d->h = ci.hk;
+      d->n = it.n = ci.n;
+      d->keep = (int)w;
+      d->req = 0;
+    } else {
+      it = decode_item(a, w, true);
+      d->tok0 = it.m.tok_start + (long long)it.qt * kTile;
+      d->pos0 = it.qt * kTile;
+      d->rows = min(kTile, it.m.len - it.qt * kTile);
+      d->h = it.h;
+      d->n = it.n;
+      d->keep = it.keep;
+      d->req = it.b;
+    }
     ptx::mbar_arrive(B.item_full + slot);
     if (it.n <= 0) continue;
     const int qb = (int)(q_it % QB);
     if (!wait_bar(B.q_empty + qb, ((q_it / QB) & 1) ^ 1, abort_flag, a.status)) break;
-    ptx::mbar_arrive_expect_tx(B.q_full + qb, L::kQBytes + kRecBytes);
+    ptx::mbar_arrive_expect_tx(B.q_full + qb, L::kQBytes + (CAND ? 0 : kRecBytes));
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      ptx::tma_load_2d(qbuf + qb * L::kQBytes + c * kSlab, tq, it.h * D + c * 64, (int)d->tok0, B.q_full + qb);
+      ptx::tma_load_2d(qbuf + qb * L::kQBytes + c * kSlab, tq, (CAND ? 0 : it.h * D) + c * 64, (int)(CAND ? w * kTile : d->tok0),
+                       B.q_full + qb);
     // the query tile's times and type bitmaps (its rows' metadata for the softmax)
-    ptx::bulk_load(qrbuf + qb * kRecBytes, a.krec + it.m.tile_start + it.qt, kRecBytes, B.q_full + qb);
+    if constexpr (!CAND)
+      ptx::bulk_load(qrbuf + qb * kRecBytes, a.krec + it.m.tile_start + it.qt, kRecBytes, B.q_full + qb);
     q_used[qb] = true; q_ph[qb] = (q_it / QB) & 1;
     ++q_it;
-    const int kvx = (it.h / a.group) * D;  // the key/value head the item's query head shares
+    const int kvx = (CAND ? ci.hk : it.h / a.group) * D;  // the key/value head the item's query head shares
     for (int j = 0; j < it.n; ++j) {
-      const uint32_t e = it.list[j];
-      const int slot = it.slots[j];
-      const int kt = (int)(e & 0xffffffu), cl = (int)(e >> 24);
+      int kt, cl, slot;
+      if constexpr (CAND) {
+        kt = ci.tile0 + j;
+        slot = -1;
+        const long long* bn = a.cand.block_need + ci.block0 + 2 * kt;
+        cl = (kt + 1) * kTile <= ci.len && max(bn[0], bn[1]) <= ci.t_lo ? REC_ATTN_TILE_FULL : REC_ATTN_TILE_PARTIAL;
+      } else {
+        const uint32_t e = it.list[j];
+        slot = it.slots[j];
+        kt = (int)(e & 0xffffffu);
+        cl = (int)(e >> 24);
+      }
       const int st = (int)(kv_it % NS);
       const uint32_t ph = (kv_it / NS) & 1;
       if (!wait_bar(B.k_free + st, ph ^ 1, abort_flag, a.status)) goto drain;
       info[st].kt = kt;
       info[st].cls = cl;
       const bool partial = cl != REC_ATTN_TILE_FULL;
-      const int y = (int)(it.m.tok_start + (long long)kt * kTile);
+      const int y = (int)((CAND ? ci.hist0 : it.m.tok_start) + (long long)kt * kTile);
       const bool tab = partial && slot >= 0;
       info[st].tab = tab ? 1 : 0;
-      ptx::mbar_arrive_expect_tx(B.k_full + st, L::kKVBytes + (partial ? (tab ? kMaskBytes : kRecBytes) : 0));
+      ptx::mbar_arrive_expect_tx(B.k_full + st, L::kKVBytes + (partial && !CAND ? (tab ? kMaskBytes : kRecBytes) : 0));
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
         ptx::tma_load_2d(kbuf + st * L::kKVBytes + c * kSlab, tk, kvx + c * 64, y, B.k_full + st);
-      if (tab) ptx::bulk_load(rbuf + st * kStageRec, a.mtab + (long long)slot * (kMaskBytes / 4), kMaskBytes, B.k_full + st);
+      if constexpr (CAND) {}
+      else if (tab) ptx::bulk_load(rbuf + st * kStageRec, a.mtab + (long long)slot * (kMaskBytes / 4), kMaskBytes, B.k_full + st);
       else if (partial) ptx::bulk_load(rbuf + st * kStageRec, a.krec + it.m.tile_start + kt, kRecBytes, B.k_full + st);
       k_used[st] = true; k_ph[st] = ph;
       if (!wait_bar(B.v_empty + st, ph ^ 1, abort_flag, a.status)) goto drain;
@@ -565,11 +597,85 @@ __device__ __forceinline__ void cmp_store(const AttnArgs& a, const CmpReq& cr, i
   }
 }
 
+// CAND: the 128 visibility bits of a row whose candidate stands at time t, over key tile kt
+// of its request (all lanes read the same keys' times).
+__device__ __forceinline__ void cand_mask(const CandArgs& c, const CandItem& ci, int kt, long long t, uint32_t (&vm)[4]) {
+  const long long* need = c.need + ci.hist0 + (long long)kt * kTile;
+  const int n = min(kTile, ci.len - kt * kTile);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t bits = 0;
+#pragma unroll 8
+    for (int e = 0; e < 32; ++e)
+      if (32 * w + e < n && __ldg(need + 32 * w + e) <= t) bits |= 1u << e;
+    vm[w] = bits;
+  }
+}
+
+// CAND: scale log2(e) <q, k> of the row's own pair (one thread: 16 bytes at a time).
+template <int D>
+__device__ __forceinline__ float own_score(const __nv_bfloat16* q, const __nv_bfloat16* k, float sl2) {
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = reinterpret_cast<const uint4*>(q)[c], y = reinterpret_cast<const uint4*>(k)[c];
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 fx = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xs[i]));
+      const float2 fy = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ys[i]));
+      s = fmaf(fx.x, fy.x, fmaf(fx.y, fy.y, s));
+    }
+  }
+  return s * sl2;
+}
+
+// CAND: the row's output.  m, l: maximum (log2 domain) and sum of the run; o: its 64 columns
+// at `half` (zeros when the run is empty).
+template <int D>
+__device__ __forceinline__ void cand_store(const AttnArgs& a, const CandItem& ci, long long item, int row, int half,
+                                           float m, float l, float own, const uint32_t (&o)[64]) {
+  const CandArgs& c = a.cand;
+  if (c.part_ml) {
+    const long long at = item * kTile + row;
+    if (half == 0) c.part_ml[at] = make_float2(l > 0.f ? m : -INFINITY, l);
+    float4* dst = reinterpret_cast<float4*>(c.part_o + at * D + half * 64);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                           __uint_as_float(o[4 * e + 3]));
+    return;
+  }
+  const int r = ci.row0 + row;
+  const long long cand = ci.cand0 + r / a.group;
+  const int h = ci.hk * a.group + r % a.group;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(c.v) + (cand * c.kv_heads + ci.hk) * D + half * 64;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (cand * a.heads + h) * D + half * 64;
+  const float top = l > 0.f ? fmaxf(m, own) : own;
+  const float wp = l > 0.f ? ex2(m - top) : 0.f, ws = ex2(own - top);
+  const float sum = l * wp + ws, inv = 1.f / sum, fp = wp * inv, fs = ws * inv;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint4 vv = reinterpret_cast<const uint4*>(v)[q];
+    const uint32_t vs[4] = {vv.x, vv.y, vv.z, vv.w};
+    uint32_t wv[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&vs[e]));
+      const __nv_bfloat162 pb = __floats2bfloat162_rn(__uint_as_float(o[8 * q + 2 * e]) * fp + f.x * fs,
+                                                      __uint_as_float(o[8 * q + 2 * e + 1]) * fp + f.y * fs);
+      wv[e] = *reinterpret_cast<const uint32_t*>(&pb);
+    }
+    reinterpret_cast<uint4*>(out)[q] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+  }
+  if (half == 0 && a.lse) a.lse[cand * a.heads + h] = (top + __log2f(sum)) * 0.6931471805599453f;
+}
+
 // GATE: the attention output gate is applied in the epilogue (a separate
 // instantiation, so the plain epilogue carries none of its code).  CMP: the output is
 // the history compression of O (cmp_store) instead of O.  LAZY: softmax_chunk's lazy
 // maximum, for plans whose items run over many key tiles.
-template <int D, bool GATE, bool CMP, bool LAZY>
+template <int D, bool GATE, bool CMP, bool LAZY, bool CAND>
 __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, uint32_t tmem,
                             volatile int* abort_flag) {
   using L = Layout<D>;
@@ -599,6 +705,25 @@ __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& 
     const int pi = d.pos0 + row;
     const long long tok = d.tok0 + row;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + (tok * H + d.h) * D;
+    CandItem ci;
+    long long ti = 0;
+    float own = 0.f;
+    if constexpr (CAND) {
+      ci = a.cand.items[d.keep];
+      const long long cand = ci.cand0 + (ci.row0 + (row_ok ? row : 0)) / a.group;
+      ti = a.cand.tc[cand];
+      if (!a.cand.part_ml && row_ok)
+        own = own_score<D>(static_cast<const __nv_bfloat16*>(a.cand.q) +
+                               (cand * H + ci.hk * a.group + (ci.row0 + row) % a.group) * D,
+                           static_cast<const __nv_bfloat16*>(a.cand.k) + (cand * a.cand.kv_heads + ci.hk) * D, sl2);
+      if (d.n <= 0) {  // no history: the candidate sees itself alone
+        const uint32_t z[64] = {};
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half)
+          if (row_ok) cand_store<D>(a, ci, d.keep, row, half, -INFINITY, 0.f, own, z);
+        continue;
+      }
+    }
     if (d.n <= 0) {  // no visible key tile: zero rows; -1: a tile of pruned queries
       if constexpr (CMP) {  // every row is computed (no pruning): zeros into the groups
         const CmpReq cr = a.cmp.req[d.req];
@@ -621,14 +746,17 @@ __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& 
     const int qb = (int)(q_it % L::QB);
     if (!wait_bar_warp(B.q_full + qb, (q_it / L::QB) & 1, abort_flag, a.status)) return;
     ++q_it;
-    const KeyTileRec* qr = qrecs + qb;
-    const long long ti = qr->t[row];
     int tyi = -1;
+    if constexpr (!CAND) {
+      const KeyTileRec* qr = qrecs + qb;
+      ti = qr->t[row];
 #pragma unroll
-    for (int c = 0; c < kTypes; ++c)
-      if ((qr->typebits[c][row >> 5] >> (row & 31)) & 1u) tyi = c;
+      for (int c = 0; c < kTypes; ++c)
+        if ((qr->typebits[c][row >> 5] >> (row & 31)) & 1u) tyi = c;
+    }
     ptx::mbar_arrive(B.q_empty + qb);  // the Q buffer and its record may be refilled
-    const bool out_ok = row_ok && query_kept(tyi, pi, d.keep);  // pruned rows are computed, not written
+    // pruned rows are computed, not written
+    const bool out_ok = row_ok && (CAND || query_kept(tyi, pi, d.keep));
     // GATE: the row's gate (D bf16, whole 128-byte lines) is prefetched into L2 while the
     // item runs and read in the epilogue, so no registers hold it through the tiles
     if constexpr (GATE) {
@@ -640,7 +768,7 @@ __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& 
       }
     }
     RowMask rm;
-    row_mask_setup(a.mask, row_ok, pi, ti, tyi, rm);
+    if constexpr (!CAND) row_mask_setup(a.mask, row_ok, pi, ti, tyi, rm);
     float m_ref = -INFINITY, l = 0.f;
     bool p1_pending = false;
     for (int j = 0; j < d.n; ++j) {
@@ -652,7 +780,9 @@ __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& 
       const StageInfo inf = info[st];
       const bool partial = inf.cls != REC_ATTN_TILE_FULL;
       uint32_t vm[4] = {~0u, ~0u, ~0u, ~0u};
-      if (partial) {
+      if (CAND && partial) {
+        cand_mask(a.cand, ci, inf.kt, ti, vm);
+      } else if (partial) {
         if (inf.tab) {
           const uint4 w = reinterpret_cast<const uint4*>(recs + st * kStageRec)[row];
           vm[0] = w.x; vm[1] = w.y; vm[2] = w.z; vm[3] = w.w;
@@ -754,6 +884,8 @@ __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& 
 #pragma unroll
         for (int e = 0; e < 64; ++e) v[e] = __uint_as_float(o[e]) * inv;
         cmp_store<D>(a, a.cmp.req[d.req], d.h, pi, row_ok, lane, v, half);
+      } else if (CAND) {
+        if (out_ok) cand_store<D>(a, ci, d.keep, row, half, m_ref, l, own, o);
       } else if (out_ok) {
         // two 16-byte chunks (16 columns) at a time: one 32-byte store when O is 32-byte
         // aligned (whole sectors; a warp's rows lie H * d * 2 bytes apart), else two
@@ -794,7 +926,7 @@ __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& 
         }
       }
     }
-    if (!CMP && out_ok && a.lse) {
+    if (!CMP && !CAND && out_ok && a.lse) {
       const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
       a.lse[tok * H + d.h] = l > 0.f ? (m_use + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
@@ -802,7 +934,7 @@ __device__ void run_softmax(const AttnArgs& a, uint8_t* sm, int s, const SBars& 
   }
 }
 
-template <int D, bool GATE, bool CMP, bool LAZY>
+template <int D, bool GATE, bool CMP, bool LAZY, bool CAND>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
@@ -859,14 +991,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     SBars B;
     B.bind<D>(bars + s * L::kBarsPerStream);
     if ((threadIdx.x & 31) == 0) {
-      if (warp < 2) run_producer<D>(a, &tm_q, &tm_k, &tm_v, sm, s, B, abort_flag);
+      if (warp < 2) run_producer<D, CAND>(a, &tm_q, &tm_k, &tm_v, sm, s, B, abort_flag);
       else run_mma<D>(a, sm, s, B, tmem, abort_flag);
     }
   } else {
     const int s = (warp - kRoleWarps) >> 2;
     SBars B;
     B.bind<D>(bars + s * L::kBarsPerStream);
-    run_softmax<D, GATE, CMP, LAZY>(a, sm, s, B, tmem, abort_flag);
+    run_softmax<D, GATE, CMP, LAZY, CAND>(a, sm, s, B, tmem, abort_flag);
   }
 
   ptx::tc_fence_before();
@@ -885,21 +1017,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool GATE, bool CMP, bool LAZY>
+template <int D, bool GATE, bool CMP, bool LAZY, bool CAND = false>
 cudaError_t launch_t(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                      int grid, cudaStream_t st) {
   using L = Layout<D>;
   static_assert(L::kDynamic <= 227 * 1024, "shared memory budget");
   cudaError_t e =
-      cudaFuncSetAttribute(k_attn_tc<D, GATE, CMP, LAZY>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynamic);
+      cudaFuncSetAttribute(k_attn_tc<D, GATE, CMP, LAZY, CAND>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynamic);
   if (e != cudaSuccess) return e;
-  k_attn_tc<D, GATE, CMP, LAZY><<<grid, kThreads, L::kDynamic, st>>>(q, k, v, a);
+  k_attn_tc<D, GATE, CMP, LAZY, CAND><<<grid, kThreads, L::kDynamic, st>>>(q, k, v, a);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, int grid,
                    cudaStream_t st) {
+  if (a.cand.items) return launch_t<D, false, false, Cfg<D>::WIDE, true>(a, q, k, v, grid, st);
   if (a.cmp.req) return launch_t<D, false, true, false>(a, q, k, v, grid, st);
   if (a.out_gate) return launch_t<D, true, false, false>(a, q, k, v, grid, st);
   if constexpr (Cfg<D>::WIDE) {

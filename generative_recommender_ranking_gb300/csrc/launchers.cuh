@@ -83,6 +83,11 @@ struct NeedArgs {
 int score_tile_keys(int head_dim);
 int score_rows_per_item(int head_dim, int max_rows);
 cudaError_t launch_score_need(const NeedArgs& a, int blocks, cudaStream_t st);
+// The many-row path: k_score_pack, k_attn_tc's CAND instantiation (launch_attn_tc with
+// a.cand), and with more than one run per row k_score_combine.
+cudaError_t launch_score_pack(const ScoreArgs& a, int head_dim, int items, CandItem* desc, void* qp, int* counters,
+                              cudaStream_t st);
+cudaError_t launch_score_combine(const ScoreArgs& a, int head_dim, int rows_per_item, cudaStream_t st);
 cudaError_t launch_score_rows(const CUtensorMap& k, const CUtensorMap& v, const ScoreArgs& a, int head_dim,
                               int rows_per_item, int items, cudaStream_t st);
 

@@ -382,6 +382,70 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   }
 }
 
+// The many-row path's prologue.  Block = one work item of k_attn_tc's CAND instantiation: its
+// 128 rows of Q' (rotated against the request's reference time, rounded to bf16; rows past
+// the request's last are zero) packed in row order, its descriptor, and (block 0) the item
+// counters.
+template <int D>
+__global__ void __launch_bounds__(128) k_score_pack(const __grid_constant__ ScoreArgs a, CandItem* items,
+                                                    __nv_bfloat16* qp, int* counters) {
+  const int x = blockIdx.x, i = upper_index(a.item_start, a.n_req, x), b = a.req0 + i;
+  const int G = a.heads / a.kv_heads, tiles = request_tiles(a, b), nsplit = n_splits(a, tiles);
+  const int local = x - a.item_start[i], split = local % nsplit, hk = local / nsplit % a.kv_heads;
+  const int row0 = local / nsplit / a.kv_heads * kTile;
+  const int rows = min(kTile, (a.cand_start[i + 1] - a.cand_start[i]) * G - row0);
+  const long long cand0 = a.cand_start[i], t_ref = a.t_ref[b];
+  constexpr int kChunks = D / 8;
+  const int c = threadIdx.x % kChunks;
+  long long t_lo = LLONG_MAX;
+  for (int r = threadIdx.x / kChunks; r < kTile; r += 128 / kChunks) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const long long cand = cand0 + (row0 + r) / G, t = a.tc[cand];
+      t_lo = min(t_lo, t);
+      w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                          (cand * a.heads + hk * G + (row0 + r) % G) * D + c * 8);
+      if (a.rotate) {
+        const float dt = (float)(t - t_ref);
+        uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const float2 f = bf16x2_float(ws[p]);
+          float sn, cs;
+          sincosf(dt * a.omega[c * 4 + p], &sn, &cs);
+          ws[p] = bf16_pair(f.x * cs - f.y * sn, f.x * sn + f.y * cs);
+        }
+        w = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+      }
+    }
+    *reinterpret_cast<uint4*>(qp + ((long long)x * kTile + r) * D + c * 8) = w;
+  }
+  __shared__ long long s_lo[4];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const long long u = __shfl_xor_sync(0xffffffffu, t_lo, o);
+    t_lo = min(t_lo, u);
+  }
+  if ((threadIdx.x & 31) == 0) s_lo[threadIdx.x >> 5] = t_lo;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    CandItem it;
+    it.hist0 = a.hist_off[b];
+    it.cand0 = cand0;
+    it.t_lo = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
+    it.len = (int)(a.hist_off[b + 1] - it.hist0);
+    it.row0 = row0;
+    it.rows = rows;
+    it.hk = hk;
+    it.tile0 = split * a.chunk_tiles;
+    it.n = min(tiles - it.tile0, a.chunk_tiles);
+    it.block0 = a.block_off[b];
+    it.pad = 0;
+    items[x] = it;
+  }
+  if (x == 0 && threadIdx.x < 8) counters[threadIdx.x] = 0;
+}
+
 // One warp per output row (candidate, head): its parts, in the order of the key tiles.
 template <int D>
 __global__ void __launch_bounds__(128) k_score_combine(const __grid_constant__ ScoreArgs a, int rows_per_item) {
@@ -441,14 +505,29 @@ cudaError_t launch_rows_t(const CUtensorMap& k, const CUtensorMap& v, const Scor
   cudaError_t e = cudaFuncSetAttribute(k_score_rows<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   k_score_rows<D, M><<<items, kScoreThreads, smem, st>>>(k, v, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !a.part_ml) return e;
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_combine(const ScoreArgs& a, int rows_per_item, cudaStream_t st) {
   const long long rows = (long long)(a.cand_start[a.n_req] - a.cand_start[0]) * a.heads;
-  k_score_combine<D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, 8 * M);
+  k_score_combine<D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, rows_per_item);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t launch_score_pack(const ScoreArgs& a, int head_dim, int items, CandItem* desc, void* qp, int* counters,
+                              cudaStream_t st) {
+  __nv_bfloat16* q = static_cast<__nv_bfloat16*>(qp);
+  if (head_dim == 64) k_score_pack<64><<<items, 128, 0, st>>>(a, desc, q, counters);
+  else k_score_pack<128><<<items, 128, 0, st>>>(a, desc, q, counters);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_combine(const ScoreArgs& a, int head_dim, int rows_per_item, cudaStream_t st) {
+  return head_dim == 64 ? launch_combine<64>(a, rows_per_item, st) : launch_combine<128>(a, rows_per_item, st);
+}
 
 int score_tile_keys(int head_dim) { return head_dim == 64 ? SCfg<64>::kKeys : SCfg<128>::kKeys; }
 
