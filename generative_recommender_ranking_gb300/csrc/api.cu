@@ -581,17 +581,19 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   plan->stream = st;
   if (T == 0) return REC_ATTN_OK;
   const bool tc = p.dtype == REC_ATTN_BF16;
-  const long long n_items = plan->NT * p.num_heads, n_kv_items = plan->NT * plan->kv_heads;
   const int group = p.num_heads / plan->kv_heads;
+  const int parts = tc ? bwd_kv_parts(plan->NT, plan->kv_heads, group, p.head_dim, plan->num_sms) : 1;
+  const int reps = group / parts;  // query heads of a dK/dV item
+  const long long n_items = plan->NT * p.num_heads, n_kv_items = plan->NT * plan->kv_heads * parts;
   // bf16 workspace: descriptors [n_items], [n_kv_items] | row constants [H][NT][128] | lists [NC] |
-  // their mask-table slots [NC] | the mask table's columns [mcap][128][4] | with shared heads
-  // the dK/dV items' order [n_kv_items]
+  // their mask-table slots [NC] | the mask table's columns [mcap][128][4] | with items of
+  // several heads the dK/dV items' order [n_kv_items]
   const size_t off_rowc = (size_t)(n_items + n_kv_items) * sizeof(BwdItemDesc);
   const size_t off_ql = off_rowc + (size_t)plan->NT * p.num_heads * kTile * sizeof(float2);
   const size_t off_qs = off_ql + (((size_t)plan->NC * sizeof(uint32_t) + 15) & ~(size_t)15);
   const size_t off_ct = off_qs + (((size_t)plan->NC * sizeof(int) + 15) & ~(size_t)15);
   const size_t off_ki = off_ct + (size_t)plan->pd.mcap * kTile * 16;
-  const size_t ws_bytes = tc ? off_ki + (group > 1 ? (size_t)n_kv_items * sizeof(int) : 0)
+  const size_t ws_bytes = tc ? off_ki + (reps > 1 ? (size_t)n_kv_items * sizeof(int) : 0)
                              : (size_t)T * p.num_heads * sizeof(float);
   if (!plan->bwd_ws) {
     cudaMemPool_t pool;
@@ -641,7 +643,8 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   a.qslot = tc ? reinterpret_cast<const int*>(bws + off_qs) : nullptr;
   a.ctab = tc ? reinterpret_cast<const uint32_t*>(bws + off_ct) : nullptr;
   a.dq = dq; a.dk = dk; a.dv = dv;
-  a.rows = T * p.num_heads; a.heads = p.num_heads; a.group = group; a.scale = p.softmax_scale;
+  a.rows = T * p.num_heads; a.heads = p.num_heads; a.group = group; a.parts = parts;
+  a.kv_part = nullptr; a.scale = p.softmax_scale;
   a.rotate = p.use_rope; a.mask = plan->mask;
   std::memcpy(a.omega, plan->omega, sizeof a.omega);
   if (!tc) {
@@ -653,7 +656,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
     BwdSchedArgs sa;
     sa.meta = plan->pd.meta; sa.qreq = plan->pd.qreq; sa.items = plan->pd.items; sa.kcount = plan->pd.kcount;
     sa.cls = plan->pd.cls; sa.t = plan->t; sa.n_tiles = plan->NT; sa.n_items = n_items; sa.n_kv_items = n_kv_items;
-    sa.heads = p.num_heads; sa.group = group; sa.kv_items = reinterpret_cast<int*>(bws + off_ki);
+    sa.heads = p.num_heads; sa.reps = reps; sa.kv_items = reinterpret_cast<int*>(bws + off_ki);
     sa.desc = reinterpret_cast<BwdItemDesc*>(bws);
     sa.qlist = reinterpret_cast<uint32_t*>(bws + off_ql);
     sa.pslot = plan->pd.pslot; sa.qslot = reinterpret_cast<int*>(bws + off_qs);
@@ -668,7 +671,20 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   const int map_heads[4] = {p.num_heads, plan->kv_heads, plan->kv_heads, p.num_heads};
   for (int i = 0; i < 4; ++i)
     if (!encode_map(&maps[i], srcs[i], T, (long long)map_heads[i] * p.head_dim)) return REC_ATTN_ERR_CUDA;
-  return from_cuda(launch_attn_bwd_tc(a, maps, p.head_dim, plan->num_sms, st));
+  if (parts > 1) {  // fp32 parts of dK and dV, for this call
+    cudaMemPool_t pool;
+    e = pool_for(plan->device, &pool);
+    if (e == cudaSuccess)
+      e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&a.kv_part),
+                                  (size_t)2 * plan->kv_heads * parts * T * p.head_dim * sizeof(float), pool, st);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  e = launch_attn_bwd_tc(a, maps, p.head_dim, plan->num_sms, st);
+  if (a.kv_part) {
+    const cudaError_t ef = cudaFreeAsync(a.kv_part, st);
+    if (e == cudaSuccess) e = ef;
+  }
+  return from_cuda(e);
 }
 
 }  // namespace
@@ -951,7 +967,7 @@ REC_ATTN_API rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows,
   NormArgs a{};
   a.rows = rows; a.width = (int)width; a.eps = eps; a.ty = types; a.x = x; a.w = weight;
   a.dy = dy; a.dx = dx; a.dw = dweight; a.db = dbias;
-  const NormBwdPlan p = layernorm_bwd_plan(rows, (int)width, types != nullptr, sms);
+  const NormBwdPlan p = layernorm_bwd_plan(rows, (int)width, dtype, types != nullptr, sms);
   cudaMemPool_t pool;
   void* ws = nullptr;
   e = pool_for(dev, &pool);

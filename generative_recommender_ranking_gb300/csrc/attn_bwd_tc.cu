@@ -191,7 +191,8 @@ __device__ __forceinline__ bool next_item(uint8_t* sm, uint64_t* bars, uint32_t&
 
 // The streamed tiles of an item, in order: request-local tile index, class and
 // mask-table slot (-1: none).  DKV visits each listed query tile once for every query
-// head of the group (`reps` times in a row), so dK and dV sum over the group in TMEM.
+// head of the item's part of the group (`reps` times in a row), so dK and dV sum over those
+// heads in TMEM.
 struct Cursor {
   const uint32_t* list;
   const int* slots;
@@ -257,7 +258,7 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
 
     if (!bw_wait(bars + kResEmpty, (it_n & 1) ^ 1, abort_flag, a.status)) goto drain;
     {
-      const int x = d.h * D;
+      const int x = (DKV ? d.h / a.parts : d.h) * D;
       const long long g = (long long)d.tile_start + d.tile;
       const float2* rows_h = a.rowc + (long long)d.h * a.n_tiles * kTile;  // DQ: head h's row constants
       ptx::mbar_arrive_expect_tx(bars + kResFull, 2 * kTileBytes + kRecB + (DKV ? 0 : kRowB));
@@ -273,12 +274,13 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
       res_ph = it_n & 1;
       ++it_n;
       Cursor cur;
-      cur.init(lists, DKV ? a.qslot : a.kslot, d, DKV ? a.group : 1);
+      const int reps = DKV ? a.group / a.parts : 1;
+      cur.init(lists, DKV ? a.qslot : a.kslot, d, reps);
       const int kvx = (d.h / a.group) * D;  // DQ: the columns of the head's key/value head
       for (int j = 0; j < d.n; ++j) {
         int tile, cls, tslot;
         // DKV: the query head of this visit, its columns and its row constants
-        const int hq = d.h * a.group + cur.rep;
+        const int hq = d.h * reps + cur.rep;
         const int xs = DKV ? hq * D : kvx;
         cur.next(tile, cls, tslot);
         const int st = (int)(s_it % kNS);
@@ -711,17 +713,25 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
   while (next_item<D>(sm, bars, it_cnt, true, it, abort_flag, a.status)) {
     const int pj = it.tile * kTile + row;
     const bool key_ok = pj < it.len;
-    const long long growk = (it.tok_start + pj) * Hk + it.h;
+    const long long growk = (it.tok_start + pj) * Hk + it.h / a.parts;
+    const long long n_part = (long long)Hk * a.parts * (a.rows / a.heads) * D;  // one gradient's parts
+    float* part = a.kv_part ? a.kv_part + ((long long)it.h * (a.rows / a.heads) + it.tok_start + pj) * D : nullptr;
     __nv_bfloat16* dkr = static_cast<__nv_bfloat16*>(a.dk) + growk * D;
     __nv_bfloat16* dvr = static_cast<__nv_bfloat16*>(a.dv) + growk * D;
     if (it.n <= 0) {  // no query sees this key tile
-      if (key_ok) { zero_row<D>(dkr); zero_row<D>(dvr); }
+      if (key_ok && part) {
+        for (int e = 0; e < D; e += 4)
+          *reinterpret_cast<float4*>(part + e) = *reinterpret_cast<float4*>(part + n_part + e) = make_float4(0, 0, 0, 0);
+      } else if (key_ok) {
+        zero_row<D>(dkr);
+        zero_row<D>(dvr);
+      }
       continue;
     }
     if (!bw_wait_warp(bars + kResFull, it_n & 1, abort_flag, a.status)) return;  // the key tile's record
     const long long tj = rrec->t[row];
     Cursor cur;
-    cur.init(a.qlist, a.qslot, it, a.group);
+    cur.init(a.qlist, a.qslot, it, a.group / a.parts);
     // Column bits of the item's j-th query tile (stage st) into buffer `buf`: the key's
     // words of the mask table's columns when the pair has a slot; otherwise, as query
     // row `row` of the tile, this thread builds the row's bits over the key tile and
@@ -841,6 +851,26 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     if (!bw_wait_warp(bars + kAccFull, it_n & 1, abort_flag, a.status)) return;
     ++it_n;
     ptx::tc_fence_after();
+    if (part) {  // the part's sums as they are: k_bwd_kv_sum adds the parts of the group
+#pragma unroll 1
+      for (int hc = 0; hc < 2 * D / 64; ++hc) {
+        uint32_t acc[64];
+        ptx::tmem_ld64(tl + BCfg<D>::kDV + 64 * hc, acc);  // dV, then dK behind it
+        if (hc == 2 * D / 64 - 1) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
+        }
+        if (key_ok) {
+          float* dst = part + (hc < D / 64 ? n_part + 64 * hc : 64 * (hc - D / 64));
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            ptx::st_global_v8(dst + 8 * c, acc[8 * c], acc[8 * c + 1], acc[8 * c + 2], acc[8 * c + 3], acc[8 * c + 4],
+                              acc[8 * c + 5], acc[8 * c + 6], acc[8 * c + 7]);
+        }
+      }
+      continue;
+    }
     // 64 columns at a time: dV packed and stored, then dK scaled, rotated back and stored
 #pragma unroll 1
     for (int hc = 0; hc < D / 64; ++hc) {
@@ -910,17 +940,17 @@ __global__ void __launch_bounds__(256) k_bwd_rowc(BwdArgs a) {
 }
 
 // ------------------------------------------------------------------ schedule
-// group > 1: dK/dV items are (tile, key/value head) pairs, one block compacting the
-// planner's order of (tile, query head) items to each group's first head, in order.
+// reps > 1: dK/dV items are (tile, part of reps query heads) pairs, one block compacting the
+// planner's order of (tile, query head) items to each part's first head, in order.
 __global__ void __launch_bounds__(1024) k_bwd_kv_items(BwdSchedArgs s) {
   __shared__ int s_warp[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hk = s.heads / s.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hp = s.heads / s.reps;
   long long base = 0;
   for (long long i0 = 0; i0 < s.n_items; i0 += 1024) {
     const long long i = i0 + threadIdx.x;
     const int e = i < s.n_items ? s.items[i] : 0;
     const int h = e % s.heads;
-    const bool take = i < s.n_items && h % s.group == 0;
+    const bool take = i < s.n_items && h % s.reps == 0;
     const unsigned bal = __ballot_sync(0xffffffffu, take);
     if (lane == 0) s_warp[warp] = __popc(bal);
     __syncthreads();
@@ -930,7 +960,7 @@ __global__ void __launch_bounds__(1024) k_bwd_kv_items(BwdSchedArgs s) {
       total += s_warp[w];
     }
     const long long at = base + before + __popc(bal & ((1u << lane) - 1u));
-    if (take && at < s.n_kv_items) s.kv_items[at] = (e / s.heads) * Hk + h / s.group;
+    if (take && at < s.n_kv_items) s.kv_items[at] = (e / s.heads) * Hp + h / s.reps;
     base += total;
     __syncthreads();
   }
@@ -978,23 +1008,23 @@ __global__ void __launch_bounds__(128) k_bwd_schedule(BwdSchedArgs s) {
   d.n = max(s.kcount[g], 0);
   s.desc[w] = d;
   if (w >= s.n_kv_items) return;
-  if (s.group > 1) {  // dK/dV item w has a tile and a head of its own
-    const int Hk = s.heads / s.group;
-    const long long ek = s.kv_items[w], gk = ek / Hk;
+  if (s.reps > 1) {  // dK/dV item w has a tile and heads of its own
+    const int Hp = s.heads / s.reps;
+    const long long ek = s.kv_items[w], gk = ek / Hp;
     m = s.meta[s.qreq[gk]];
     kt = m.ntiles - 1 - (int)(gk - m.tile_start);
     d.tok_start = m.tok_start;
     d.t_ref = s.t[m.tok_start];
     d.len = m.len;
     d.tile_start = (int)m.tile_start;
-    d.h = (int)(ek % Hk);
+    d.h = (int)(ek % Hp);
   }
   const uint8_t* col = s.cls + m.cls_start + kt;
   int n = 0;
   for (int r = 0; r < m.ntiles; ++r) n += col[(long long)r * m.ntiles] != REC_ATTN_TILE_SKIP;
   d.list = m.cls_start + (long long)kt * m.ntiles;
   d.tile = kt;
-  d.n = n * s.group;
+  d.n = n * s.reps;
   s.desc[s.n_items + w] = d;
 }
 
@@ -1010,6 +1040,57 @@ __global__ void __launch_bounds__(kTile) k_bwd_colmask(BwdSchedArgs s) {
     uint32_t* out = s.ctab + (long long)slot * kTile * 4;
 #pragma unroll
     for (int wd = 0; wd < 4; ++wd) out[(32 * wd + lane) * 4 + quad] = transpose32(vm[wd], lane);
+  }
+}
+
+// ------------------------------------------------------------------ sum of the parts
+// Block = (tile g, key/value head): dK and dV of the tile's rows as the sums of the group's
+// parts, in order; dK is scaled and rotated back; both rounded once.  Eight columns a thread.
+template <int D>
+__global__ void __launch_bounds__(256) k_bwd_kv_sum(BwdArgs a) {
+  constexpr int kLanes = D / 8;
+  const long long g = blockIdx.x;
+  const int hk = blockIdx.y, Hk = a.heads / a.group;
+  const ReqMeta m = a.meta[a.qreq[g]];
+  const int tile = (int)(g - m.tile_start), c = threadIdx.x & (kLanes - 1);
+  const long long T = a.rows / a.heads, n_part = (long long)Hk * a.parts * T * D;
+  const long long t_ref = a.t[m.tok_start];
+  for (int r = threadIdx.x / kLanes; r < kTile; r += 256 / kLanes) {
+    const int p = tile * kTile + r;
+    if (p >= m.len) return;
+    const long long tok = m.tok_start + p;
+    const float* src = a.kv_part + ((long long)hk * a.parts * T + tok) * D + 8 * c;
+    float k[8], v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < a.parts; ++i) {
+      const float4* pk = reinterpret_cast<const float4*>(src + (long long)i * T * D);
+      const float4* pv = reinterpret_cast<const float4*>(src + (long long)i * T * D + n_part);
+      const float4 k0 = __ldcs(pk), k1 = __ldcs(pk + 1), v0 = __ldcs(pv), v1 = __ldcs(pv + 1);
+      k[0] += k0.x; k[1] += k0.y; k[2] += k0.z; k[3] += k0.w;
+      k[4] += k1.x; k[5] += k1.y; k[6] += k1.z; k[7] += k1.w;
+      v[0] += v0.x; v[1] += v0.y; v[2] += v0.z; v[3] += v0.w;
+      v[4] += v1.x; v[5] += v1.y; v[6] += v1.z; v[7] += v1.w;
+    }
+    uint32_t wk[4], wv[4];
+    const float dt = (float)(a.t[tok] - t_ref);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x = k[2 * e] * a.scale, y = k[2 * e + 1] * a.scale;
+      if (a.rotate) {
+        float sn, cs;
+        __sincosf(dt * a.omega[4 * c + e], &sn, &cs);
+        const float x2 = x * cs + y * sn;
+        y = -x * sn + y * cs;
+        x = x2;
+      }
+      wk[e] = bf16x2(x, y);
+      wv[e] = bf16x2(v[2 * e], v[2 * e + 1]);
+    }
+    const long long at = (tok * Hk + hk) * D + 8 * c;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dk) + at) = make_uint4(wk[0], wk[1], wk[2], wk[3]);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dv) + at) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
   }
 }
 
@@ -1104,15 +1185,28 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
   const long long cap = (long long)BCfg<D>::kBlocksPerSM * num_sms;
   e = launch_mode<D, false>(maps, a, (int)(a.n_items < cap ? a.n_items : cap), st);
   if (e != cudaSuccess) return e;
-  return launch_mode<D, true>(maps, a, (int)(a.n_kv_items < cap ? a.n_kv_items : cap), st);
+  e = launch_mode<D, true>(maps, a, (int)(a.n_kv_items < cap ? a.n_kv_items : cap), st);
+  if (e != cudaSuccess || a.parts == 1) return e;
+  k_bwd_kv_sum<D><<<dim3((unsigned)a.n_tiles, (unsigned)(a.heads / a.group)), 256, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
+int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int head_dim, int num_sms) {
+  const long long slots = (long long)(head_dim == 64 ? BCfg<64>::kBlocksPerSM : BCfg<128>::kBlocksPerSM) * num_sms;
+  int parts = 1;
+  while (parts < group && n_tiles * kv_heads * parts < 3 * slots) {
+    ++parts;
+    while (group % parts) ++parts;
+  }
+  return parts;
+}
+
 cudaError_t launch_bwd_schedule(const BwdSchedArgs& s, int num_sms, cudaStream_t st) {
   const long long n = s.n_tiles + s.n_items;
   if (n <= 0) return cudaSuccess;
-  if (s.group > 1) {
+  if (s.reps > 1) {
     k_bwd_kv_items<<<1, 1024, 0, st>>>(s);
     const cudaError_t ek = cudaGetLastError();
     if (ek != cudaSuccess) return ek;

@@ -178,8 +178,8 @@ struct BwdItemDesc {
   int len;              // request length
   int tile;             // request-local tile whose rows the item owns
   int tile_start;       // global index of the request's first tile
-  int h;                // query head (dQ), key/value head (dK/dV)
-  int n;                // streamed tiles (dK/dV: each listed query tile once per head of the group)
+  int h;                // query head (dQ), part of a group (dK/dV)
+  int n;                // streamed tiles (dK/dV: each listed query tile once per head of the part)
   int pad;
 };
 static_assert(sizeof(BwdItemDesc) == 48, "three 16-byte loads");
@@ -192,7 +192,7 @@ struct BwdArgs {
   const int* qreq;         // request of each tile
   const KeyTileRec* krec;  // per tile: type bitmaps and times (tensor-core kernels' masks)
   long long n_items;       // tiles x heads: dQ items
-  long long n_kv_items;    // tiles x key/value heads: dK/dV items
+  long long n_kv_items;    // tiles x key/value heads x parts: dK/dV items
   int* status;             // device status word (first error wins)
   int* counters;           // [3], [4]: dQ item counter and exit ticket; [5], [6]: dK/dV (reset at kernel end)
   long long n_tiles;
@@ -226,6 +226,8 @@ struct BwdArgs {
   long long rows;          // T * H
   int heads;
   int group;               // query heads that share a key/value head
+  int parts;               // dK/dV items per key/value head and tile: group / parts query heads each
+  float* kv_part;          // parts > 1: [2 (dK, dV)][kv heads * parts][T][d], unscaled, not rotated back
   float scale;
   int rotate;              // 1: undo the time-RoPE on dQ', dK'
   MaskP mask;
@@ -241,8 +243,9 @@ struct BwdSchedArgs {
   const uint8_t* cls;
   const long long* t;
   long long n_tiles, n_items, n_kv_items;
-  int heads, group;
-  int* kv_items;            // group > 1: written, (tile * kv heads + kv head) in the order of `items`
+  int heads;
+  int reps;                 // query heads of a dK/dV item
+  int* kv_items;            // reps > 1: written, (tile * heads / reps + part) in the order of `items`
   BwdItemDesc* desc;
   uint32_t* qlist;
   const int* pslot;         // per (query tile, key tile): mask-table slot, -1 if none

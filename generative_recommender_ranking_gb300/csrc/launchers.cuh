@@ -33,6 +33,9 @@ cudaError_t launch_slots_gather(const SlotArgs& a, int dtype, long long n_chunks
 cudaError_t launch_attn_simt(const AttnArgs& a, int head_dim, cudaStream_t st);
 cudaError_t launch_bwd_delta(const BwdArgs& a, int dtype, int head_dim, cudaStream_t st);
 cudaError_t launch_attn_bwd_simt(const BwdArgs& a, int head_dim, long long n_tiles, cudaStream_t st);
+// Parts of a group's query heads that dK/dV items take apart (a divisor of the group): the
+// fewest that give every place of the persistent grid three items.
+int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int head_dim, int num_sms);
 cudaError_t launch_bwd_schedule(const BwdSchedArgs& s, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_bwd_tc(const BwdArgs& a, const CUtensorMap (&maps)[4], int head_dim, int num_sms,
                                cudaStream_t st);
@@ -119,7 +122,7 @@ struct NormBwdPlan {
   size_t off_part, off_flush, bytes;
 };
 cudaError_t launch_layernorm_fwd(NormArgs a, int dtype, int num_sms, cudaStream_t st);
-NormBwdPlan layernorm_bwd_plan(long long rows, int width, bool by_type, int num_sms);
+NormBwdPlan layernorm_bwd_plan(long long rows, int width, int dtype, bool by_type, int num_sms);
 cudaError_t launch_layernorm_bwd(NormArgs a, const NormBwdPlan& p, void* ws, int dtype, cudaStream_t st);
 cudaError_t launch_wait_timeout(int* status, unsigned long long limit_ns, cudaStream_t st);
 cudaError_t launch_attn_tc(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,

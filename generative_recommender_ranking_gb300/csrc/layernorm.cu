@@ -8,8 +8,7 @@
 //   dx = r (u - mean(u) - n mean(u n)),  dw[g] = sum dy n,  db[g] = sum dy  (rows of g).
 //
 // Both directions are bound by HBM: every row is read once and written once.  A row is
-// held in the registers of `tpr` threads, 16 values each (two 16-byte chunks of bf16, four
-// of fp32), so the variance is the mean of squared differences from the mean itself and
+// held in the registers of `tpr` threads, two 16-byte chunks each, so the variance is the mean of squared differences from the mean itself and
 // the backward recomputes both statistics from the row it reads anyway.  The backward takes
 // two reductions a row: {sum x, sum u}, then {sum (x - m)^2, sum u (x - m)}.
 // Statistics, sums and gradients of the gains are fp32; outputs are rounded once.
@@ -21,7 +20,6 @@ namespace recattn {
 
 namespace {
 
-constexpr int kEpt = 16;       // values of a row per thread
 constexpr int kNormThreads = 256;
 
 template <typename E>
@@ -72,16 +70,22 @@ struct RowGroup {
     red = s_red + id * 2 * warps;
     buf = 0;
   }
-  // Sums of a and b over the row's threads, to every thread.
+  // Sums over the row's threads, to every thread: of a and b, or of a alone.
   __device__ __forceinline__ float2 sum2(float a, float b) {
     for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
       b += __shfl_xor_sync(0xffffffffu, b, o);
     }
-    if (warps == 1) return make_float2(a, b);
+    return warps == 1 ? make_float2(a, b) : across(make_float2(a, b));
+  }
+  __device__ __forceinline__ float sum1(float a) {
+    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return warps == 1 ? a : across(make_float2(a, 0.f)).x;
+  }
+  __device__ __forceinline__ float2 across(float2 v) {
     float2* r = red + buf * warps;
     buf ^= 1;  // the next reduction writes the other half: one barrier each suffices
-    if ((lane & 31) == 0) r[lane >> 5] = make_float2(a, b);
+    if ((lane & 31) == 0) r[lane >> 5] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(tpr) : "memory");
     float2 t = r[0];
     for (int w = 1; w < warps; ++w) {
@@ -92,41 +96,54 @@ struct RowGroup {
   }
 };
 
-__device__ __forceinline__ void load_gain(const float* p, float* x, int n) {
-  for (int i = 0; i < n; i += 4) {
+template <int N>
+__device__ __forceinline__ void load_gain(const float* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
     const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
     x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
   }
 }
 
-// Rows of a block: groups of tpr threads take consecutive rows in turn, so at any time a
-// block reads neighbouring rows.  A row whose type is outside 0..3 belongs to no group:
-// its output (or gradient) is zero.
-template <typename E>
-__global__ void __launch_bounds__(1024) k_layernorm_fwd(NormArgs a) {
-  constexpr int N = Vec<E>::kN, NV = kEpt / N;
+// A row's 16-byte chunks lane, lane + tpr, ... (zeros past the row or for no row).
+template <typename E, int NV>
+__device__ __forceinline__ void load_row(const void* base, long long row, bool in, int width, int chunks,
+                                         const RowGroup& g, uint4 (&raw)[NV]) {
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const E*>(base) + (in ? row : 0) * width);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * g.tpr + g.lane;
+    raw[i] = in && c < chunks ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// A block's groups take consecutive rows in turn; the next row's chunks are loaded before
+// this row's reductions.  A row whose type is outside 0..3 belongs to no group: its output (or
+// gradient) is zero.
+template <typename E, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_layernorm_fwd(NormArgs a) {
+  constexpr int N = Vec<E>::kN, EPT = NV * N;
   __shared__ float2 s_red[64];
   RowGroup g;
   g.init(a.tpr, s_red);
   const int groups = blockDim.x / a.tpr, chunks = a.width / N;
   const float inv_w = 1.f / (float)a.width;
-  // whole warps run every iteration (rows past the end are loaded as zeros and not stored)
   const long long stride = (long long)gridDim.x * groups;
-  for (long long r0 = (long long)blockIdx.x * groups; r0 < a.rows; r0 += stride) {
-    const long long row = r0 + g.id;
+  long long row = (long long)blockIdx.x * groups + g.id;
+  uint4 next[NV];
+  load_row<E, NV>(a.x, row, row < a.rows, a.width, chunks, g, next);
+  // whole warps run every iteration (rows past the end are loaded as zeros and not stored)
+  for (long long r0 = (long long)blockIdx.x * groups; r0 < a.rows; r0 += stride, row += stride) {
     const bool in = row < a.rows;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const E*>(a.x) + (in ? row : 0) * a.width);
-    float x[kEpt];
+    float x[EPT];
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = i * a.tpr + g.lane;
-      Vec<E>::unpack(in && c < chunks ? src[c] : make_uint4(0, 0, 0, 0), x + i * N);
-    }
+    for (int i = 0; i < NV; ++i) Vec<E>::unpack(next[i], x + i * N);
+    load_row<E, NV>(a.x, row + stride, row + stride < a.rows, a.width, chunks, g, next);
     const int ty = in && a.ty ? a.ty[row] : 0;
 #pragma unroll
-    for (int e = 0; e < kEpt; ++e) s += x[e];
-    const float mean = g.sum2(s, 0.f).x * inv_w;
+    for (int e = 0; e < EPT; ++e) s += x[e];
+    const float mean = g.sum1(s) * inv_w;
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -137,7 +154,7 @@ __global__ void __launch_bounds__(1024) k_layernorm_fwd(NormArgs a) {
         q = fmaf(x[i * N + e], x[i * N + e], q);
       }
     }
-    const float rstd = rsqrtf(g.sum2(q, 0.f).x * inv_w + a.eps);
+    const float rstd = rsqrtf(g.sum1(q) * inv_w + a.eps);
     if (!in) continue;
     const bool ok = (unsigned)ty <= 3u;
     const float* w = a.w + (long long)(ok ? ty : 0) * a.width;
@@ -148,85 +165,88 @@ __global__ void __launch_bounds__(1024) k_layernorm_fwd(NormArgs a) {
       const int c = i * a.tpr + g.lane;
       if (c >= chunks) continue;
       float wv[N], bv[N], y[N];
-      load_gain(w + c * N, wv, N);
-      if (b) load_gain(b + c * N, bv, N);
+      load_gain<N>(w + c * N, wv);
+      if (b) load_gain<N>(b + c * N, bv);
 #pragma unroll
       for (int e = 0; e < N; ++e) y[e] = ok ? fmaf(x[i * N + e] * rstd, wv[e], b ? bv[e] : 0.f) : 0.f;
-      dst[c] = Vec<E>::pack(y);
+      __stcs(dst + c, Vec<E>::pack(y));
     }
   }
 }
 
 // Backward.  Block k takes the contiguous rows [k R, (k + 1) R), its groups in turn, and
-// keeps the gains' gradients of its columns in registers while the type stays the same (a
-// request's types come in a few runs).  When the type changes, a group adds what it holds
-// to a slot of its own in a.flush; at the end the block sums its groups, type by type, into
-// its row of a.part.  k_layernorm_dw then sums the blocks.  Every sum has a fixed order, so
+// keeps the gains and the gains' gradients of its columns in registers while the type stays the
+// same (a request's types come in a few runs).  When the type changes, a group adds what it
+// holds to a slot of its own in a.flush; at the end the block sums its groups, type by type,
+// into its row of a.part.  k_layernorm_dw then sums the blocks.  Every sum has a fixed order, so
 // the gradients do not change from call to call.
-template <typename E>
-__global__ void __launch_bounds__(1024) k_layernorm_bwd(NormArgs a) {
-  constexpr int N = Vec<E>::kN, NV = kEpt / N;
+template <typename E, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
+  constexpr int N = Vec<E>::kN, EPT = NV * N;
   __shared__ float2 s_red[64];
   __shared__ int s_open[32];                  // per group: the type it still holds (-1: none)
   __shared__ unsigned s_flushed[32];          // per group: types with sums in its slot
-  extern __shared__ float s_sum[];            // [groups][2][width padded to 4]: open sums
+  extern __shared__ float s_sum[];            // [groups][2][width]: open sums
   RowGroup g;
   g.init(a.tpr, s_red);
   const int groups = blockDim.x / a.tpr, chunks = a.width / N;
   const float inv_w = 1.f / (float)a.width;
-  float dw[kEpt], db[kEpt];
+  float w[EPT], dw[EPT], db[EPT];
 #pragma unroll
-  for (int e = 0; e < kEpt; ++e) dw[e] = db[e] = 0.f;
+  for (int e = 0; e < EPT; ++e) w[e] = dw[e] = db[e] = 0.f;
   int cur = -1;
   unsigned flushed = 0;
   float* slots = a.flush ? a.flush + ((long long)blockIdx.x * groups + g.id) * 4 * 2 * a.width : nullptr;
-  auto flush = [&]() {
-    float* p = slots + (long long)cur * 2 * a.width;
-    const bool add = (flushed >> cur) & 1u;
+  // the type changes: what is held goes to the group's slot, the new type's gains come in
+  auto change = [&](int ty) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * a.tpr + g.lane;
       if (c >= chunks) continue;
+      if (cur >= 0) {
+        float* p = slots + (long long)cur * 2 * a.width + c * N;
+        const bool add = (flushed >> cur) & 1u;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        float* pw = p + c * N + e;
-        float* pb = pw + a.width;
-        *pw = add ? *pw + dw[i * N + e] : dw[i * N + e];
-        *pb = add ? *pb + db[i * N + e] : db[i * N + e];
+        for (int e = 0; e < N; ++e) {
+          p[e] = add ? p[e] + dw[i * N + e] : dw[i * N + e];
+          p[a.width + e] = add ? p[a.width + e] + db[i * N + e] : db[i * N + e];
+          dw[i * N + e] = db[i * N + e] = 0.f;
+        }
       }
+      load_gain<N>(a.w + (long long)ty * a.width + c * N, w + i * N);
     }
-    flushed |= 1u << cur;
-#pragma unroll
-    for (int e = 0; e < kEpt; ++e) dw[e] = db[e] = 0.f;
+    if (cur >= 0) flushed |= 1u << cur;
+    cur = ty;
   };
   const long long first = (long long)blockIdx.x * a.rows_per_block;
   const long long last = min(first + a.rows_per_block, a.rows);
-  for (long long r0 = first; r0 < last; r0 += groups) {
-    const long long row = r0 + g.id;
+  long long row = first + g.id;
+  uint4 nx[NV], ny[NV];
+  load_row<E, NV>(a.x, row, row < last, a.width, chunks, g, nx);
+  load_row<E, NV>(a.dy, row, row < last, a.width, chunks, g, ny);
+  int nty = row < last ? (a.ty ? a.ty[row] : 0) : -1;
+  for (long long r0 = first; r0 < last; r0 += groups, row += groups) {
     const bool in = row < last;
-    const uint4* sx = reinterpret_cast<const uint4*>(static_cast<const E*>(a.x) + (in ? row : 0) * a.width);
-    const uint4* sy = reinterpret_cast<const uint4*>(static_cast<const E*>(a.dy) + (in ? row : 0) * a.width);
-    float x[kEpt], u[kEpt], dy[kEpt];
-    const int ty = in ? (a.ty ? a.ty[row] : 0) : -1;
+    float x[EPT], dy[EPT];
+    const int ty = nty;
     const bool ok = (unsigned)ty <= 3u;
-    const float* w = a.w + (long long)(ok ? ty : 0) * a.width;
-    float s = 0.f, su = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * a.tpr + g.lane;
-      const bool act = in && c < chunks;
-      Vec<E>::unpack(act ? sx[c] : make_uint4(0, 0, 0, 0), x + i * N);
-      Vec<E>::unpack(act ? sy[c] : make_uint4(0, 0, 0, 0), dy + i * N);
-      float wv[N];
+      Vec<E>::unpack(nx[i], x + i * N);
+      Vec<E>::unpack(ny[i], dy + i * N);
+    }
+    {
+      const long long nr = row + groups;
+      load_row<E, NV>(a.x, nr, nr < last, a.width, chunks, g, nx);
+      load_row<E, NV>(a.dy, nr, nr < last, a.width, chunks, g, ny);
+      nty = nr < last ? (a.ty ? a.ty[nr] : 0) : -1;
+    }
+    if (ok && ty != cur) change(ty);
+    float s = 0.f, su = 0.f;
 #pragma unroll
-      for (int e = 0; e < N; ++e) wv[e] = 0.f;
-      if (act) load_gain(w + c * N, wv, N);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        u[i * N + e] = dy[i * N + e] * wv[e];
-        s += x[i * N + e];
-        su += u[i * N + e];
-      }
+    for (int e = 0; e < EPT; ++e) {
+      s += x[e];
+      su = fmaf(dy[e], w[e], su);
     }
     const float2 t1 = g.sum2(s, su);
     const float mean = t1.x * inv_w, mu = t1.y * inv_w;
@@ -236,19 +256,16 @@ __global__ void __launch_bounds__(1024) k_layernorm_bwd(NormArgs a) {
       if (i * a.tpr + g.lane >= chunks) continue;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        x[i * N + e] -= mean;
-        q = fmaf(x[i * N + e], x[i * N + e], q);
-        ux = fmaf(u[i * N + e], x[i * N + e], ux);
+        const int k = i * N + e;
+        x[k] -= mean;
+        q = fmaf(x[k], x[k], q);
+        ux = fmaf(dy[k] * w[k], x[k], ux);
       }
     }
     const float2 t2 = g.sum2(q, ux);
     const float rstd = rsqrtf(t2.x * inv_w + a.eps);
     const float mun = t2.y * inv_w * rstd;  // mean of u n
     if (!in) continue;
-    if (ok && ty != cur) {
-      if (cur >= 0) flush();
-      cur = ty;
-    }
     uint4* dst = reinterpret_cast<uint4*>(static_cast<E*>(a.dx) + row * a.width);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -259,13 +276,13 @@ __global__ void __launch_bounds__(1024) k_layernorm_bwd(NormArgs a) {
       for (int e = 0; e < N; ++e) {
         const int k = i * N + e;
         const float n = x[k] * rstd;
-        d[e] = ok ? rstd * (u[k] - mu - n * mun) : 0.f;
+        d[e] = ok ? rstd * (fmaf(dy[k], w[k], -mu) - n * mun) : 0.f;
         if (ok) {
           dw[k] = fmaf(dy[k], n, dw[k]);
           db[k] += dy[k];
         }
       }
-      dst[c] = Vec<E>::pack(d);
+      __stcs(dst + c, Vec<E>::pack(d));
     }
   }
   // the block's sums, type by type: each group's slot, then what it still holds
@@ -326,60 +343,79 @@ __global__ void __launch_bounds__(256) k_layernorm_dw(NormArgs a, int blocks) {
   }
 }
 
-// Threads per row: 16 values each, rounded up to a power of two of at least 8 (within a
-// warp; so a block has at most 32 rows at a time) or to whole warps.
-int threads_per_row(int width) {
-  const int n = (width + kEpt - 1) / kEpt;
-  if (n > 32) return (n + 31) / 32 * 32;
-  int t = 8;
-  while (t < n) t *= 2;
-  return t;
+// Two 16-byte chunks of a row per thread (four for rows of more than 32 KB), the threads
+// rounded up to a power of two of at least 8 (within a warp; so a block has at most 32 rows at
+// a time) or to whole warps.
+struct NormShape {
+  int nv, tpr, threads, groups;
+};
+NormShape norm_shape(int width, int dtype) {
+  const int chunks = width * (dtype == REC_ATTN_BF16 ? 2 : 4) / 16;
+  NormShape s;
+  s.nv = chunks > 2048 ? 4 : 2;
+  const int n = (chunks + s.nv - 1) / s.nv;
+  if (n > 32) {
+    s.tpr = (n + 31) / 32 * 32;
+  } else {
+    s.tpr = 8;
+    while (s.tpr < n) s.tpr *= 2;
+  }
+  s.threads = s.tpr <= kNormThreads ? kNormThreads / s.tpr * s.tpr : s.tpr;
+  s.groups = s.threads / s.tpr;
+  return s;
 }
 
-int block_threads(int tpr) { return tpr <= kNormThreads ? kNormThreads / tpr * tpr : tpr; }
+using NormKernel = void (*)(NormArgs);
+template <typename E>
+NormKernel norm_kernel(const NormShape& s, bool bwd) {
+  if (s.nv > 2) return bwd ? k_layernorm_bwd<E, 4, 1024> : k_layernorm_fwd<E, 4, 1024>;
+  if (s.threads > 512) return bwd ? k_layernorm_bwd<E, 2, 1024> : k_layernorm_fwd<E, 2, 1024>;
+  if (s.threads > kNormThreads && s.threads <= 512) return bwd ? k_layernorm_bwd<E, 2, 512> : k_layernorm_fwd<E, 2, 512>;
+  return bwd ? k_layernorm_bwd<E, 2, kNormThreads> : k_layernorm_fwd<E, 2, kNormThreads>;
+}
+NormKernel norm_kernel(const NormShape& s, int dtype, bool bwd) {
+  return dtype == REC_ATTN_BF16 ? norm_kernel<__nv_bfloat16>(s, bwd) : norm_kernel<float>(s, bwd);
+}
 
 }  // namespace
 
 cudaError_t launch_layernorm_fwd(NormArgs a, int dtype, int num_sms, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
-  a.tpr = threads_per_row(a.width);
-  const int threads = block_threads(a.tpr), groups = threads / a.tpr;
-  const long long need = (a.rows + groups - 1) / groups, cap = (long long)num_sms * (2048 / threads);
-  const unsigned grid = (unsigned)(need < cap ? need : cap);
-  if (dtype == REC_ATTN_BF16) k_layernorm_fwd<__nv_bfloat16><<<grid, threads, 0, st>>>(a);
-  else k_layernorm_fwd<float><<<grid, threads, 0, st>>>(a);
+  const NormShape s = norm_shape(a.width, dtype);
+  a.tpr = s.tpr;
+  const long long need = (a.rows + s.groups - 1) / s.groups, cap = (long long)num_sms * (2048 / s.threads);
+  norm_kernel(s, dtype, false)<<<(unsigned)(need < cap ? need : cap), s.threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-NormBwdPlan layernorm_bwd_plan(long long rows, int width, bool by_type, int num_sms) {
+NormBwdPlan layernorm_bwd_plan(long long rows, int width, int dtype, bool by_type, int num_sms) {
   NormBwdPlan p;
-  const int tpr = threads_per_row(width), threads = block_threads(tpr), groups = threads / tpr;
-  const long long need = (rows + groups - 1) / groups, cap = 2LL * num_sms;
+  const NormShape s = norm_shape(width, dtype);
+  const long long need = (rows + s.groups - 1) / s.groups, cap = (long long)num_sms * (s.threads > kNormThreads ? 1 : 2);
   p.blocks = (int)(need < cap ? need : cap);
   p.rows_per_block = (rows + p.blocks - 1) / p.blocks;
-  p.rows_per_block = (p.rows_per_block + groups - 1) / groups * groups;
+  p.rows_per_block = (p.rows_per_block + s.groups - 1) / s.groups * s.groups;
   p.blocks = (int)((rows + p.rows_per_block - 1) / p.rows_per_block);
   const int types = by_type ? 4 : 1;
   p.off_part = ((size_t)p.blocks * sizeof(unsigned) + 255) & ~(size_t)255;
   p.off_flush = p.off_part + (size_t)p.blocks * types * 2 * width * sizeof(float);
-  p.bytes = p.off_flush + (by_type ? (size_t)p.blocks * groups * 4 * 2 * width * sizeof(float) : 0);
+  p.bytes = p.off_flush + (by_type ? (size_t)p.blocks * s.groups * 4 * 2 * width * sizeof(float) : 0);
   return p;
 }
 
 cudaError_t launch_layernorm_bwd(NormArgs a, const NormBwdPlan& p, void* ws, int dtype, cudaStream_t st) {
-  a.tpr = threads_per_row(a.width);
-  const int threads = block_threads(a.tpr), groups = threads / a.tpr;
+  const NormShape s = norm_shape(a.width, dtype);
+  a.tpr = s.tpr;
   a.rows_per_block = p.rows_per_block;
   char* w = static_cast<char*>(ws);
   a.seen = reinterpret_cast<unsigned*>(w);
   a.part = reinterpret_cast<float*>(w + p.off_part);
   a.flush = a.ty ? reinterpret_cast<float*>(w + p.off_flush) : nullptr;
-  const int smem = groups * 2 * a.width * (int)sizeof(float);
-  const void* fn = dtype == REC_ATTN_BF16 ? (const void*)k_layernorm_bwd<__nv_bfloat16> : (const void*)k_layernorm_bwd<float>;
+  const int smem = s.groups * 2 * a.width * (int)sizeof(float);
+  const NormKernel fn = norm_kernel(s, dtype, true);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  if (dtype == REC_ATTN_BF16) k_layernorm_bwd<__nv_bfloat16><<<p.blocks, threads, smem, st>>>(a);
-  else k_layernorm_bwd<float><<<p.blocks, threads, smem, st>>>(a);
+  fn<<<p.blocks, s.threads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((2 * a.width + 31) / 32), a.ty ? 4u : 1u);
