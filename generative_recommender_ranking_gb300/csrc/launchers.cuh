@@ -117,7 +117,7 @@ struct NormArgs {
 };
 // The backward's grid and workspace for a shape.
 struct NormBwdPlan {
-  int blocks;
+  int blocks, smem;
   long long rows_per_block;
   size_t off_part, off_flush, bytes;
 };

@@ -14,6 +14,10 @@
 // Statistics, sums and gradients of the gains are fp32; outputs are rounded once.
 #include <cuda_bf16.h>
 
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "launchers.cuh"
 
 namespace recattn {
@@ -22,24 +26,54 @@ namespace {
 
 constexpr int kNormThreads = 256;
 
+// Pairs of fp32 for the packed instructions (fma.rn.f32x2 and its kin: two values an issue).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float total(f2 v) {
+  const float2 r = both(v);
+  return r.x + r.y;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <typename E>
-struct Vec;  // a 16-byte chunk
+struct Vec;  // a 16-byte chunk: kN values, as pairs
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void unpack(const uint4 v, float* x) {
+  static __device__ __forceinline__ void unpack(const uint4 v, f2* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
+  static __device__ __forceinline__ uint4 pack(const f2* x) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const float2 v = both(x[i]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -48,12 +82,13 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void unpack(const uint4 v, float* x) {
-    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+  static __device__ __forceinline__ void unpack(const uint4 v, f2* x) {
+    x[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  static __device__ __forceinline__ uint4 pack(const f2* x) {
+    const float2 a = both(x[0]), b = both(x[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
 };
 
@@ -97,11 +132,12 @@ struct RowGroup {
 };
 
 template <int N>
-__device__ __forceinline__ void load_gain(const float* p, float* x) {
+__device__ __forceinline__ void load_gain(const float* p, f2* x) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
-    x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    x[i / 2] = pair(v.x, v.y);
+    x[i / 2 + 1] = pair(v.z, v.w);
   }
 }
 
@@ -135,41 +171,43 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_fwd(NormArgs a) {
   // whole warps run every iteration (rows past the end are loaded as zeros and not stored)
   for (long long r0 = (long long)blockIdx.x * groups; r0 < a.rows; r0 += stride, row += stride) {
     const bool in = row < a.rows;
-    float x[EPT];
-    float s = 0.f;
+    f2 x[EPT / 2];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) Vec<E>::unpack(next[i], x + i * N);
+    for (int i = 0; i < NV; ++i) Vec<E>::unpack(next[i], x + i * (N / 2));
     load_row<E, NV>(a.x, row + stride, row + stride < a.rows, a.width, chunks, g, next);
     const int ty = in && a.ty ? a.ty[row] : 0;
+    f2 s = x[0];
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) s += x[e];
-    const float mean = g.sum1(s) * inv_w;
-    float q = 0.f;
+    for (int e = 1; e < EPT / 2; ++e) s = add2(s, x[e]);
+    const float mean = g.sum1(total(s)) * inv_w;
+    f2 q = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (i * a.tpr + g.lane >= chunks) continue;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        x[i * N + e] -= mean;
-        q = fmaf(x[i * N + e], x[i * N + e], q);
+      for (int e = i * (N / 2); e < (i + 1) * (N / 2); ++e) {
+        x[e] = add2(x[e], pair(-mean, -mean));
+        q = fma2(x[e], x[e], q);
       }
     }
-    const float rstd = rsqrtf(g.sum1(q) * inv_w + a.eps);
+    const float rstd = rsqrtf(g.sum1(total(q)) * inv_w + a.eps);
     if (!in) continue;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<E*>(a.y) + row * a.width);
     const bool ok = (unsigned)ty <= 3u;
     const float* w = a.w + (long long)(ok ? ty : 0) * a.width;
     const float* b = a.b ? a.b + (long long)(ok ? ty : 0) * a.width : nullptr;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<E*>(a.y) + row * a.width);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * a.tpr + g.lane;
       if (c >= chunks) continue;
-      float wv[N], bv[N], y[N];
+      f2 wv[N / 2], y[N / 2];
       load_gain<N>(w + c * N, wv);
-      if (b) load_gain<N>(b + c * N, bv);
 #pragma unroll
-      for (int e = 0; e < N; ++e) y[e] = ok ? fmaf(x[i * N + e] * rstd, wv[e], b ? bv[e] : 0.f) : 0.f;
-      __stcs(dst + c, Vec<E>::pack(y));
+      for (int e = 0; e < N / 2; ++e) y[e] = 0ull;
+      if (b) load_gain<N>(b + c * N, y);
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) y[e] = fma2(mul2(x[i * (N / 2) + e], pair(rstd, rstd)), wv[e], y[e]);
+      __stcs(dst + c, ok ? Vec<E>::pack(y) : make_uint4(0, 0, 0, 0));
     }
   }
 }
@@ -180,8 +218,9 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_fwd(NormArgs a) {
 // holds to a slot of its own in a.flush; at the end the block sums its groups, type by type,
 // into its row of a.part.  k_layernorm_dw then sums the blocks.  Every sum has a fixed order, so
 // the gradients do not change from call to call.
+// Registers: two blocks of 256 threads per SM in bf16 (16 columns a thread), three in fp32 (8).
 template <typename E, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 2 : 3) k_layernorm_bwd(NormArgs a) {
   constexpr int N = Vec<E>::kN, EPT = NV * N;
   __shared__ float2 s_red[64];
   __shared__ int s_open[32];                  // per group: the type it still holds (-1: none)
@@ -191,9 +230,9 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
   g.init(a.tpr, s_red);
   const int groups = blockDim.x / a.tpr, chunks = a.width / N;
   const float inv_w = 1.f / (float)a.width;
-  float w[EPT], dw[EPT], db[EPT];
+  f2 w[EPT / 2], dw[EPT / 2], db[EPT / 2];
 #pragma unroll
-  for (int e = 0; e < EPT; ++e) w[e] = dw[e] = db[e] = 0.f;
+  for (int e = 0; e < EPT / 2; ++e) w[e] = dw[e] = db[e] = 0ull;
   int cur = -1;
   unsigned flushed = 0;
   float* slots = a.flush ? a.flush + ((long long)blockIdx.x * groups + g.id) * 4 * 2 * a.width : nullptr;
@@ -207,13 +246,16 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
         float* p = slots + (long long)cur * 2 * a.width + c * N;
         const bool add = (flushed >> cur) & 1u;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          p[e] = add ? p[e] + dw[i * N + e] : dw[i * N + e];
-          p[a.width + e] = add ? p[a.width + e] + db[i * N + e] : db[i * N + e];
-          dw[i * N + e] = db[i * N + e] = 0.f;
+        for (int e = 0; e < N / 2; ++e) {
+          float2* pw = reinterpret_cast<float2*>(p + 2 * e);
+          float2* pb = reinterpret_cast<float2*>(p + a.width + 2 * e);
+          const float2 ow = add ? *pw : make_float2(0.f, 0.f), ob = add ? *pb : make_float2(0.f, 0.f);
+          *pw = both(add2(dw[i * (N / 2) + e], pair(ow.x, ow.y)));
+          *pb = both(add2(db[i * (N / 2) + e], pair(ob.x, ob.y)));
+          dw[i * (N / 2) + e] = db[i * (N / 2) + e] = 0ull;
         }
       }
-      load_gain<N>(a.w + (long long)ty * a.width + c * N, w + i * N);
+      load_gain<N>(a.w + (long long)ty * a.width + c * N, w + i * (N / 2));
     }
     if (cur >= 0) flushed |= 1u << cur;
     cur = ty;
@@ -227,13 +269,13 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
   int nty = row < last ? (a.ty ? a.ty[row] : 0) : -1;
   for (long long r0 = first; r0 < last; r0 += groups, row += groups) {
     const bool in = row < last;
-    float x[EPT], dy[EPT];
+    f2 x[EPT / 2], dy[EPT / 2];
     const int ty = nty;
     const bool ok = (unsigned)ty <= 3u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      Vec<E>::unpack(nx[i], x + i * N);
-      Vec<E>::unpack(ny[i], dy + i * N);
+      Vec<E>::unpack(nx[i], x + i * (N / 2));
+      Vec<E>::unpack(ny[i], dy + i * (N / 2));
     }
     {
       const long long nr = row + groups;
@@ -242,27 +284,26 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
       nty = nr < last ? (a.ty ? a.ty[nr] : 0) : -1;
     }
     if (ok && ty != cur) change(ty);
-    float s = 0.f, su = 0.f;
+    f2 s = 0ull, su = 0ull;
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      s += x[e];
-      su = fmaf(dy[e], w[e], su);
+    for (int e = 0; e < EPT / 2; ++e) {
+      s = add2(s, x[e]);
+      su = fma2(dy[e], w[e], su);
     }
-    const float2 t1 = g.sum2(s, su);
+    const float2 t1 = g.sum2(total(s), total(su));
     const float mean = t1.x * inv_w, mu = t1.y * inv_w;
-    float q = 0.f, ux = 0.f;
+    f2 q = 0ull, ux = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (i * a.tpr + g.lane >= chunks) continue;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int k = i * N + e;
-        x[k] -= mean;
-        q = fmaf(x[k], x[k], q);
-        ux = fmaf(dy[k] * w[k], x[k], ux);
+      for (int e = i * (N / 2); e < (i + 1) * (N / 2); ++e) {
+        x[e] = add2(x[e], pair(-mean, -mean));
+        q = fma2(x[e], x[e], q);
+        ux = fma2(mul2(dy[e], w[e]), x[e], ux);
       }
     }
-    const float2 t2 = g.sum2(q, ux);
+    const float2 t2 = g.sum2(total(q), total(ux));
     const float rstd = rsqrtf(t2.x * inv_w + a.eps);
     const float mun = t2.y * inv_w * rstd;  // mean of u n
     if (!in) continue;
@@ -271,16 +312,18 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
     for (int i = 0; i < NV; ++i) {
       const int c = i * a.tpr + g.lane;
       if (c >= chunks) continue;
-      float d[N];
+      if (!ok) {
+        __stcs(dst + c, make_uint4(0, 0, 0, 0));
+        continue;
+      }
+      f2 d[N / 2];
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int k = i * N + e;
-        const float n = x[k] * rstd;
-        d[e] = ok ? rstd * (fmaf(dy[k], w[k], -mu) - n * mun) : 0.f;
-        if (ok) {
-          dw[k] = fmaf(dy[k], n, dw[k]);
-          db[k] += dy[k];
-        }
+      for (int e = 0; e < N / 2; ++e) {
+        const int k = i * (N / 2) + e;
+        const f2 n = mul2(x[k], pair(rstd, rstd));
+        d[e] = mul2(fma2(n, pair(-mun, -mun), fma2(dy[k], w[k], pair(-mu, -mu))), pair(rstd, rstd));
+        dw[k] = fma2(dy[k], n, dw[k]);
+        db[k] = add2(db[k], dy[k]);
       }
       __stcs(dst + c, Vec<E>::pack(d));
     }
@@ -296,9 +339,10 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
       const int c = i * a.tpr + g.lane;
       if (c >= chunks) continue;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        s_sum[(g.id * 2 + 0) * a.width + c * N + e] = dw[i * N + e];
-        s_sum[(g.id * 2 + 1) * a.width + c * N + e] = db[i * N + e];
+      for (int e = 0; e < N / 2; ++e) {
+        float* p = s_sum + g.id * 2 * a.width + c * N + 2 * e;
+        *reinterpret_cast<float2*>(p) = both(dw[i * (N / 2) + e]);
+        *reinterpret_cast<float2*>(p + a.width) = both(db[i * (N / 2) + e]);
       }
     }
   }
@@ -310,8 +354,10 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_bwd(NormArgs a) {
   for (int t = 0; t < types; ++t) {
     if (!((seen >> t) & 1u)) continue;
     float* out = a.part + ((long long)blockIdx.x * types + t) * 2 * a.width;
+#pragma unroll 1
     for (int c = threadIdx.x; c < 2 * a.width; c += blockDim.x) {
       float v = 0.f;
+#pragma unroll 2
       for (int k = 0; k < groups; ++k) {
         if ((s_flushed[k] >> t) & 1u)
           v += a.flush[(((long long)blockIdx.x * groups + k) * 4 + t) * 2 * a.width + c];
@@ -377,21 +423,39 @@ NormKernel norm_kernel(const NormShape& s, int dtype, bool bwd) {
   return dtype == REC_ATTN_BF16 ? norm_kernel<__nv_bfloat16>(s, bwd) : norm_kernel<float>(s, bwd);
 }
 
+// Blocks of a kernel that an SM holds (asked once per kernel and shape).
+int blocks_per_sm(NormKernel fn, int threads, int smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<NormKernel, int, int>, int> known;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(fn, threads, smem);
+  const auto at = known.find(key);
+  if (at != known.end()) return at->second;
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess || n < 1) return 1;
+  known[key] = n;
+  return n;
+}
+
 }  // namespace
 
 cudaError_t launch_layernorm_fwd(NormArgs a, int dtype, int num_sms, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   const NormShape s = norm_shape(a.width, dtype);
   a.tpr = s.tpr;
-  const long long need = (a.rows + s.groups - 1) / s.groups, cap = (long long)num_sms * (2048 / s.threads);
-  norm_kernel(s, dtype, false)<<<(unsigned)(need < cap ? need : cap), s.threads, 0, st>>>(a);
+  const NormKernel fn = norm_kernel(s, dtype, false);
+  const long long need = (a.rows + s.groups - 1) / s.groups, cap = (long long)num_sms * blocks_per_sm(fn, s.threads, 0);
+  fn<<<(unsigned)(need < cap ? need : cap), s.threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 NormBwdPlan layernorm_bwd_plan(long long rows, int width, int dtype, bool by_type, int num_sms) {
   NormBwdPlan p;
   const NormShape s = norm_shape(width, dtype);
-  const long long need = (rows + s.groups - 1) / s.groups, cap = (long long)num_sms * (s.threads > kNormThreads ? 1 : 2);
+  const NormKernel fn = norm_kernel(s, dtype, true);
+  p.smem = s.groups * 2 * width * (int)sizeof(float);
+  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);  // a failure shows at the launch
+  const long long need = (rows + s.groups - 1) / s.groups, cap = (long long)num_sms * blocks_per_sm(fn, s.threads, p.smem);
   p.blocks = (int)(need < cap ? need : cap);
   p.rows_per_block = (rows + p.blocks - 1) / p.blocks;
   p.rows_per_block = (p.rows_per_block + s.groups - 1) / s.groups * s.groups;
@@ -411,12 +475,8 @@ cudaError_t launch_layernorm_bwd(NormArgs a, const NormBwdPlan& p, void* ws, int
   a.seen = reinterpret_cast<unsigned*>(w);
   a.part = reinterpret_cast<float*>(w + p.off_part);
   a.flush = a.ty ? reinterpret_cast<float*>(w + p.off_flush) : nullptr;
-  const int smem = s.groups * 2 * a.width * (int)sizeof(float);
-  const NormKernel fn = norm_kernel(s, dtype, true);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  fn<<<p.blocks, s.threads, smem, st>>>(a);
-  e = cudaGetLastError();
+  norm_kernel(s, dtype, true)<<<p.blocks, s.threads, p.smem, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((2 * a.width + 31) / 32), a.ty ? 4u : 1u);
   k_layernorm_dw<<<grid, 256, 0, st>>>(a, p.blocks);
