@@ -14,6 +14,7 @@
 // Statistics, sums and gradients of the gains are fp32; outputs are rounded once.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -25,6 +26,7 @@ namespace recattn {
 namespace {
 
 constexpr int kNormThreads = 256;
+constexpr int kNormMaxSmem = 160 * 1024;  // 128 KB of rows or sums at the widest
 
 // Pairs of fp32 for the packed instructions (fma.rn.f32x2 and its kin: two values an issue).
 using f2 = unsigned long long;
@@ -92,29 +94,32 @@ struct Vec<float> {
   }
 };
 
-// The threads of one row: a power of two from 8 to 32, or a multiple of 32.
+// The threads of one row: LANES (8 or 16) neighbouring lanes, or with LANES = 32 whole warps.
+template <int LANES>
 struct RowGroup {
   int tpr, lane, id, warps;  // tpr: threads per row; lane: thread within the row; id: row group within the block
   float2* red;               // [2][warps] of this group (rows of more than one warp)
   int buf;
   __device__ __forceinline__ void init(int threads_per_row, float2* s_red) {
-    tpr = threads_per_row;
+    tpr = LANES < 32 ? LANES : threads_per_row;
     lane = threadIdx.x % tpr;
     id = threadIdx.x / tpr;
-    warps = tpr > 32 ? tpr / 32 : 1;
+    warps = LANES < 32 ? 1 : tpr / 32;
     red = s_red + id * 2 * warps;
     buf = 0;
   }
   // Sums over the row's threads, to every thread: of a and b, or of a alone.
   __device__ __forceinline__ float2 sum2(float a, float b) {
-    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
       b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     return warps == 1 ? make_float2(a, b) : across(make_float2(a, b));
   }
   __device__ __forceinline__ float sum1(float a) {
-    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     return warps == 1 ? a : across(make_float2(a, 0.f)).x;
   }
   __device__ __forceinline__ float2 across(float2 v) {
@@ -141,49 +146,133 @@ __device__ __forceinline__ void load_gain(const float* p, f2* x) {
   }
 }
 
-// A row's 16-byte chunks lane, lane + tpr, ... (zeros past the row or for no row).
-template <typename E, int NV>
-__device__ __forceinline__ void load_row(const void* base, long long row, bool in, int width, int chunks,
-                                         const RowGroup& g, uint4 (&raw)[NV]) {
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const E*>(base) + (in ? row : 0) * width);
+// Where a thread stands in a row: its chunks are lane, lane + tpr, ... and `act` those that the
+// row has (FULL: all of them, so no test remains).
+template <int NV, bool FULL>
+struct Chunks {
+  bool act[NV];
+  __device__ __forceinline__ void init(int lane, int tpr, int chunks) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = i * g.tpr + g.lane;
-    raw[i] = in && c < chunks ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < NV; ++i) act[i] = FULL || i * tpr + lane < chunks;
   }
+  __device__ __forceinline__ bool has(int i) const { return FULL || act[i]; }
+};
+
+// Rows on their way: each thread copies its own chunks into its own slots of shared memory,
+// NS - 1 rows ahead (cp.async), and reads them back itself, so no barrier is needed and no
+// register holds them meanwhile.
+__device__ __forceinline__ void copy16(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-// A block's groups take consecutive rows in turn; the next row's chunks are loaded before
-// this row's reductions.  A row whose type is outside 0..3 belongs to no group: its output (or
-// gradient) is zero.
-template <typename E, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_layernorm_fwd(NormArgs a) {
+// The types of a group's rows r0, r0 + stride, ...: the group's lanes (of each warp) hold the next
+// LANES of them, loaded together, so a row's type costs a shuffle and no wait on memory.
+template <int LANES>
+struct RowTypes {
+  const int8_t* ty;
+  int held, k;
+  __device__ __forceinline__ void init(const int8_t* types) {
+    ty = types;
+    held = 0;
+    k = LANES;
+  }
+  // The type of row r (0 without types, -1 past `last`); r goes up by stride from call to call.
+  __device__ __forceinline__ int next(int r, int stride, int last) {
+    if (!ty) return 0;
+    if (k == LANES) {
+      const int mine = r + (int)(threadIdx.x & (LANES - 1)) * stride;
+      held = mine < last ? ty[mine] : -1;
+      k = 0;
+    }
+    return __shfl_sync(0xffffffffu, held, k++, LANES);
+  }
+};
+
+// Forward.  Block k takes the contiguous rows [k R, (k + 1) R), its groups in turn, and keeps
+// the gain and bias of its columns in registers while the type stays the same (a request's
+// types come in a few runs; read for every row they would fill the L1 pipe).  With whole warps
+// per row each group walks its own rows; groups within a warp walk together, `in` false past the
+// end (their lanes take part in shuffles).  A row whose type is outside 0..3 belongs to no group:
+// its output (or gradient) is zero.
+template <typename E, int NV, int LANES, bool FULL, int THREADS, int NS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2) k_layernorm_fwd(NormArgs a) {
   constexpr int N = Vec<E>::kN, EPT = NV * N;
   __shared__ float2 s_red[64];
-  RowGroup g;
+  extern __shared__ uint4 s_rows[];  // [NS][NV][threads]
+  RowGroup<LANES> g;
   g.init(a.tpr, s_red);
-  const int groups = blockDim.x / a.tpr, chunks = a.width / N;
+  const int groups = blockDim.x / g.tpr, chunks = a.width / N;
+  Chunks<NV, FULL> ch;
+  ch.init(g.lane, g.tpr, chunks);
   const float inv_w = 1.f / (float)a.width;
-  const long long stride = (long long)gridDim.x * groups;
-  long long row = (long long)blockIdx.x * groups + g.id;
-  uint4 next[NV];
-  load_row<E, NV>(a.x, row, row < a.rows, a.width, chunks, g, next);
-  // whole warps run every iteration (rows past the end are loaded as zeros and not stored)
-  for (long long r0 = (long long)blockIdx.x * groups; r0 < a.rows; r0 += stride, row += stride) {
-    const bool in = row < a.rows;
+  const long long first = (long long)blockIdx.x * a.rows_per_block;
+  const int last = (int)min(first + a.rows_per_block, a.rows);
+  int left = last - (int)first;  // rows from the block's (whole warps: the group's) next on
+  if (LANES == 32) left -= g.id;
+  const int lead = LANES == 32 ? 0 : g.id;  // the row is in while left > lead
+  const int step = groups * chunks;
+  const uint4* const px = static_cast<const uint4*>(a.x);
+  uint4* const py = static_cast<uint4*>(a.y);
+  long long at = (first + g.id) * chunks + g.lane;
+  int r = (int)first + g.id;
+  int slot = 0, ahead_left = left;
+  long long ahead = at;  // the next row to copy
+  auto copy = [&]() {
+    if (ahead_left > lead) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (ch.has(i)) copy16(s_rows + (slot * NV + i) * blockDim.x + threadIdx.x, px + ahead + i * g.tpr);
+    }
+    copies_end();
+    slot = slot + 1 == NS ? 0 : slot + 1;
+    ahead += step;
+    ahead_left -= groups;
+  };
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy();
+  RowTypes<LANES> types;
+  types.init(a.ty);
+  f2 w[EPT / 2], b[EPT / 2];
+#pragma unroll
+  for (int e = 0; e < EPT / 2; ++e) w[e] = b[e] = 0ull;
+  int cur = -1, here = 0;
+  for (; left > 0; left -= groups, at += step, r += groups) {
+    copy();
+    const int ty = types.next(r, groups, last);
+    const bool in = left > lead, ok = (unsigned)ty <= 3u;
+    if (ok && ty != cur) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!ch.has(i)) continue;
+        const long long col = (long long)ty * a.width + (i * g.tpr + g.lane) * N;
+        load_gain<N>(a.w + col, w + i * (N / 2));
+        if (a.b) load_gain<N>(a.b + col, b + i * (N / 2));
+      }
+      cur = ty;
+    }
+    copies_wait<NS - 1>();
     f2 x[EPT / 2];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) Vec<E>::unpack(next[i], x + i * (N / 2));
-    load_row<E, NV>(a.x, row + stride, row + stride < a.rows, a.width, chunks, g, next);
-    const int ty = in && a.ty ? a.ty[row] : 0;
-    f2 s = x[0];
+    for (int i = 0; i < NV; ++i) Vec<E>::unpack(s_rows[(here * NV + i) * blockDim.x + threadIdx.x], x + i * (N / 2));
+    here = here + 1 == NS ? 0 : here + 1;
+    f2 s = 0ull;
 #pragma unroll
-    for (int e = 1; e < EPT / 2; ++e) s = add2(s, x[e]);
+    for (int i = 0; i < NV; ++i) {
+      if (!ch.has(i)) continue;
+#pragma unroll
+      for (int e = i * (N / 2); e < (i + 1) * (N / 2); ++e) s = add2(s, x[e]);
+    }
     const float mean = g.sum1(total(s)) * inv_w;
     f2 q = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i * a.tpr + g.lane >= chunks) continue;
+      if (!ch.has(i)) continue;
 #pragma unroll
       for (int e = i * (N / 2); e < (i + 1) * (N / 2); ++e) {
         x[e] = add2(x[e], pair(-mean, -mean));
@@ -191,23 +280,17 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_fwd(NormArgs a) {
       }
     }
     const float rstd = rsqrtf(g.sum1(total(q)) * inv_w + a.eps);
-    if (!in) continue;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<E*>(a.y) + row * a.width);
-    const bool ok = (unsigned)ty <= 3u;
-    const float* w = a.w + (long long)(ok ? ty : 0) * a.width;
-    const float* b = a.b ? a.b + (long long)(ok ? ty : 0) * a.width : nullptr;
+    if (LANES < 32 && !in) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * a.tpr + g.lane;
-      if (c >= chunks) continue;
-      f2 wv[N / 2], y[N / 2];
-      load_gain<N>(w + c * N, wv);
+      if (!ch.has(i)) continue;
+      f2 y[N / 2];
 #pragma unroll
-      for (int e = 0; e < N / 2; ++e) y[e] = 0ull;
-      if (b) load_gain<N>(b + c * N, y);
-#pragma unroll
-      for (int e = 0; e < N / 2; ++e) y[e] = fma2(mul2(x[i * (N / 2) + e], pair(rstd, rstd)), wv[e], y[e]);
-      __stcs(dst + c, ok ? Vec<E>::pack(y) : make_uint4(0, 0, 0, 0));
+      for (int e = 0; e < N / 2; ++e) {
+        const int k = i * (N / 2) + e;
+        y[e] = fma2(mul2(x[k], pair(rstd, rstd)), w[k], b[k]);
+      }
+      __stcs(py + at + i * g.tpr, ok ? Vec<E>::pack(y) : make_uint4(0, 0, 0, 0));
     }
   }
 }
@@ -218,32 +301,32 @@ __global__ void __launch_bounds__(THREADS) k_layernorm_fwd(NormArgs a) {
 // holds to a slot of its own in a.flush; at the end the block sums its groups, type by type,
 // into its row of a.part.  k_layernorm_dw then sums the blocks.  Every sum has a fixed order, so
 // the gradients do not change from call to call.
-// Registers: two blocks of 256 threads per SM in bf16 (16 columns a thread), three in fp32 (8).
-template <typename E, int NV, int THREADS>
+template <typename E, int NV, int LANES, bool FULL, int THREADS, int NS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 2 : 3) k_layernorm_bwd(NormArgs a) {
   constexpr int N = Vec<E>::kN, EPT = NV * N;
   __shared__ float2 s_red[64];
   __shared__ int s_open[32];                  // per group: the type it still holds (-1: none)
   __shared__ unsigned s_flushed[32];          // per group: types with sums in its slot
   extern __shared__ float s_sum[];            // [groups][2][width]: open sums
-  RowGroup g;
+  RowGroup<LANES> g;
   g.init(a.tpr, s_red);
-  const int groups = blockDim.x / a.tpr, chunks = a.width / N;
+  const int groups = blockDim.x / g.tpr, chunks = a.width / N;
+  Chunks<NV, FULL> ch;
+  ch.init(g.lane, g.tpr, chunks);
   const float inv_w = 1.f / (float)a.width;
   f2 w[EPT / 2], dw[EPT / 2], db[EPT / 2];
 #pragma unroll
   for (int e = 0; e < EPT / 2; ++e) w[e] = dw[e] = db[e] = 0ull;
   int cur = -1;
   unsigned flushed = 0;
-  float* slots = a.flush ? a.flush + ((long long)blockIdx.x * groups + g.id) * 4 * 2 * a.width : nullptr;
   // the type changes: what is held goes to the group's slot, the new type's gains come in
   auto change = [&](int ty) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * a.tpr + g.lane;
-      if (c >= chunks) continue;
+      if (!ch.has(i)) continue;
+      const int col = (i * g.tpr + g.lane) * N;
       if (cur >= 0) {
-        float* p = slots + (long long)cur * 2 * a.width + c * N;
+        float* p = a.flush + (((long long)blockIdx.x * groups + g.id) * 4 + cur) * 2 * a.width + col;
         const bool add = (flushed >> cur) & 1u;
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
@@ -255,47 +338,77 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 
           dw[i * (N / 2) + e] = db[i * (N / 2) + e] = 0ull;
         }
       }
-      load_gain<N>(a.w + (long long)ty * a.width + c * N, w + i * (N / 2));
+      load_gain<N>(a.w + (long long)ty * a.width + col, w + i * (N / 2));
     }
     if (cur >= 0) flushed |= 1u << cur;
     cur = ty;
   };
   const long long first = (long long)blockIdx.x * a.rows_per_block;
-  const long long last = min(first + a.rows_per_block, a.rows);
-  long long row = first + g.id;
-  uint4 nx[NV], ny[NV];
-  load_row<E, NV>(a.x, row, row < last, a.width, chunks, g, nx);
-  load_row<E, NV>(a.dy, row, row < last, a.width, chunks, g, ny);
-  int nty = row < last ? (a.ty ? a.ty[row] : 0) : -1;
-  for (long long r0 = first; r0 < last; r0 += groups, row += groups) {
-    const bool in = row < last;
-    f2 x[EPT / 2], dy[EPT / 2];
-    const int ty = nty;
+  const int last = (int)min(first + a.rows_per_block, a.rows);
+  int left = last - (int)first;
+  if (LANES == 32) left -= g.id;
+  const int lead = LANES == 32 ? 0 : g.id;
+  const int step = groups * chunks;
+  // one running offset for x, dy and dx (their bases stay in constant memory)
+  const uint4* const px = static_cast<const uint4*>(a.x);
+  const uint4* const py = static_cast<const uint4*>(a.dy);
+  uint4* const pd = static_cast<uint4*>(a.dx);
+  long long at = (first + g.id) * chunks + g.lane;
+  int r = (int)first + g.id;
+  uint4* const s_rows = reinterpret_cast<uint4*>(s_sum);  // [NS][x, dy][NV][threads], before the sums
+  int slot = 0, ahead_left = left;
+  long long ahead = at;  // the next row to copy
+  auto copy = [&]() {
+    if (ahead_left > lead) {
+      uint4* const s = s_rows + slot * 2 * NV * blockDim.x + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (ch.has(i)) {
+          copy16(s + i * blockDim.x, px + ahead + i * g.tpr);
+          copy16(s + (NV + i) * blockDim.x, py + ahead + i * g.tpr);
+        }
+    }
+    copies_end();
+    slot = slot + 1 == NS ? 0 : slot + 1;
+    ahead += step;
+    ahead_left -= groups;
+  };
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy();
+  int here = 0;  // the slot of this row
+  RowTypes<LANES> types;
+  types.init(a.ty);
+  for (; left > 0; left -= groups, at += step, r += groups) {
+    copy();
+    const bool in = left > lead;
+    const int ty = in || a.ty ? types.next(r, groups, last) : -1;
     const bool ok = (unsigned)ty <= 3u;
+    copies_wait<NS - 1>();
+    f2 x[EPT / 2], dy[EPT / 2];
+    const uint4* const s_row = s_rows + here * 2 * NV * blockDim.x + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      Vec<E>::unpack(nx[i], x + i * (N / 2));
-      Vec<E>::unpack(ny[i], dy + i * (N / 2));
+      Vec<E>::unpack(s_row[i * blockDim.x], x + i * (N / 2));
+      Vec<E>::unpack(s_row[(NV + i) * blockDim.x], dy + i * (N / 2));
     }
-    {
-      const long long nr = row + groups;
-      load_row<E, NV>(a.x, nr, nr < last, a.width, chunks, g, nx);
-      load_row<E, NV>(a.dy, nr, nr < last, a.width, chunks, g, ny);
-      nty = nr < last ? (a.ty ? a.ty[nr] : 0) : -1;
-    }
+    here = here + 1 == NS ? 0 : here + 1;
     if (ok && ty != cur) change(ty);
     f2 s = 0ull, su = 0ull;
 #pragma unroll
-    for (int e = 0; e < EPT / 2; ++e) {
-      s = add2(s, x[e]);
-      su = fma2(dy[e], w[e], su);
+    for (int i = 0; i < NV; ++i) {
+      if (!ch.has(i)) continue;
+#pragma unroll
+      for (int e = i * (N / 2); e < (i + 1) * (N / 2); ++e) {
+        s = add2(s, x[e]);
+        su = fma2(dy[e], w[e], su);
+      }
     }
     const float2 t1 = g.sum2(total(s), total(su));
     const float mean = t1.x * inv_w, mu = t1.y * inv_w;
     f2 q = 0ull, ux = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i * a.tpr + g.lane >= chunks) continue;
+      if (!ch.has(i)) continue;
 #pragma unroll
       for (int e = i * (N / 2); e < (i + 1) * (N / 2); ++e) {
         x[e] = add2(x[e], pair(-mean, -mean));
@@ -306,16 +419,16 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 
     const float2 t2 = g.sum2(total(q), total(ux));
     const float rstd = rsqrtf(t2.x * inv_w + a.eps);
     const float mun = t2.y * inv_w * rstd;  // mean of u n
-    if (!in) continue;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<E*>(a.dx) + row * a.width);
+    if (LANES < 32 && !in) continue;
+    if (!ok) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (ch.has(i)) __stcs(pd + at + i * g.tpr, make_uint4(0, 0, 0, 0));
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * a.tpr + g.lane;
-      if (c >= chunks) continue;
-      if (!ok) {
-        __stcs(dst + c, make_uint4(0, 0, 0, 0));
-        continue;
-      }
+      if (!ch.has(i)) continue;
       f2 d[N / 2];
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) {
@@ -325,9 +438,11 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 
         dw[k] = fma2(dy[k], n, dw[k]);
         db[k] = add2(db[k], dy[k]);
       }
-      __stcs(dst + c, Vec<E>::pack(d));
+      __stcs(pd + at + i * g.tpr, Vec<E>::pack(d));
     }
   }
+  copies_wait<0>();
+  __syncthreads();  // the rows' slots are read: the sums take their place
   // the block's sums, type by type: each group's slot, then what it still holds
   if (g.lane == 0) {
     s_open[g.id] = cur;
@@ -336,24 +451,23 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 
   if (cur >= 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * a.tpr + g.lane;
-      if (c >= chunks) continue;
+      if (!ch.has(i)) continue;
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) {
-        float* p = s_sum + g.id * 2 * a.width + c * N + 2 * e;
+        float* p = s_sum + g.id * 2 * a.width + (i * g.tpr + g.lane) * N + 2 * e;
         *reinterpret_cast<float2*>(p) = both(dw[i * (N / 2) + e]);
         *reinterpret_cast<float2*>(p + a.width) = both(db[i * (N / 2) + e]);
       }
     }
   }
   __syncthreads();  // slots (global) and open sums (shared) of every group are written
-  const int types = a.ty ? 4 : 1;
+  const int n_types = a.ty ? 4 : 1;
   unsigned seen = 0;
   for (int k = 0; k < groups; ++k) seen |= s_flushed[k] | (s_open[k] >= 0 ? 1u << s_open[k] : 0u);
   if (threadIdx.x == 0) a.seen[blockIdx.x] = seen;
-  for (int t = 0; t < types; ++t) {
+  for (int t = 0; t < n_types; ++t) {
     if (!((seen >> t) & 1u)) continue;
-    float* out = a.part + ((long long)blockIdx.x * types + t) * 2 * a.width;
+    float* out = a.part + ((long long)blockIdx.x * n_types + t) * 2 * a.width;
 #pragma unroll 1
     for (int c = threadIdx.x; c < 2 * a.width; c += blockDim.x) {
       float v = 0.f;
@@ -394,6 +508,9 @@ __global__ void __launch_bounds__(256) k_layernorm_dw(NormArgs a, int blocks) {
 // a time) or to whole warps.
 struct NormShape {
   int nv, tpr, threads, groups;
+  bool full;  // every thread has all its chunks
+  int ns;     // rows on their way per thread, this one included: 64 to 128 KB a block
+  int rows_smem(bool bwd) const { return ns * nv * threads * 16 * (bwd ? 2 : 1); }
 };
 NormShape norm_shape(int width, int dtype) {
   const int chunks = width * (dtype == REC_ATTN_BF16 ? 2 : 4) / 16;
@@ -408,16 +525,24 @@ NormShape norm_shape(int width, int dtype) {
   }
   s.threads = s.tpr <= kNormThreads ? kNormThreads / s.tpr * s.tpr : s.tpr;
   s.groups = s.threads / s.tpr;
+  s.full = chunks == s.nv * s.tpr;
+  s.ns = s.nv > 2 ? 1 : s.threads > 512 ? 2 : s.threads > kNormThreads ? 3 : 4;
   return s;
 }
 
 using NormKernel = void (*)(NormArgs);
+template <typename E, int NV, int LANES, bool FULL, int THREADS, int NS>
+NormKernel norm_dir(bool bwd) {
+  return bwd ? k_layernorm_bwd<E, NV, LANES, FULL, THREADS, NS> : k_layernorm_fwd<E, NV, LANES, FULL, THREADS, NS>;
+}
 template <typename E>
 NormKernel norm_kernel(const NormShape& s, bool bwd) {
-  if (s.nv > 2) return bwd ? k_layernorm_bwd<E, 4, 1024> : k_layernorm_fwd<E, 4, 1024>;
-  if (s.threads > 512) return bwd ? k_layernorm_bwd<E, 2, 1024> : k_layernorm_fwd<E, 2, 1024>;
-  if (s.threads > kNormThreads && s.threads <= 512) return bwd ? k_layernorm_bwd<E, 2, 512> : k_layernorm_fwd<E, 2, 512>;
-  return bwd ? k_layernorm_bwd<E, 2, kNormThreads> : k_layernorm_fwd<E, 2, kNormThreads>;
+  if (s.nv > 2) return norm_dir<E, 4, 32, false, 1024, 1>(bwd);
+  if (s.threads > 512) return norm_dir<E, 2, 32, false, 1024, 2>(bwd);
+  if (s.threads > kNormThreads) return norm_dir<E, 2, 32, false, 512, 3>(bwd);
+  if (s.tpr == 8) return norm_dir<E, 2, 8, false, kNormThreads, 4>(bwd);
+  if (s.tpr == 16) return norm_dir<E, 2, 16, false, kNormThreads, 4>(bwd);
+  return s.full ? norm_dir<E, 2, 32, true, kNormThreads, 4>(bwd) : norm_dir<E, 2, 32, false, kNormThreads, 4>(bwd);
 }
 NormKernel norm_kernel(const NormShape& s, int dtype, bool bwd) {
   return dtype == REC_ATTN_BF16 ? norm_kernel<__nv_bfloat16>(s, bwd) : norm_kernel<float>(s, bwd);
@@ -432,6 +557,8 @@ int blocks_per_sm(NormKernel fn, int threads, int smem) {
   const auto at = known.find(key);
   if (at != known.end()) return at->second;
   int n = 0;
+  // (one limit for every shape of a kernel; a failure shows at the launch)
+  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess || n < 1) return 1;
   known[key] = n;
   return n;
@@ -439,27 +566,31 @@ int blocks_per_sm(NormKernel fn, int threads, int smem) {
 
 }  // namespace
 
+// Contiguous runs of rows, one per resident block, in whole turns of the block's groups.
+static void split_rows(long long rows, int groups, long long places, int* blocks, long long* rows_per_block) {
+  const long long turns = (rows + groups - 1) / groups, n = turns < places ? turns : places;
+  *rows_per_block = (turns + n - 1) / n * groups;
+  *blocks = (int)((rows + *rows_per_block - 1) / *rows_per_block);
+}
+
 cudaError_t launch_layernorm_fwd(NormArgs a, int dtype, int num_sms, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   const NormShape s = norm_shape(a.width, dtype);
   a.tpr = s.tpr;
   const NormKernel fn = norm_kernel(s, dtype, false);
-  const long long need = (a.rows + s.groups - 1) / s.groups, cap = (long long)num_sms * blocks_per_sm(fn, s.threads, 0);
-  fn<<<(unsigned)(need < cap ? need : cap), s.threads, 0, st>>>(a);
+  int blocks = 0;
+  split_rows(a.rows, s.groups, (long long)num_sms * blocks_per_sm(fn, s.threads, s.rows_smem(false)), &blocks,
+             &a.rows_per_block);
+  fn<<<blocks, s.threads, s.rows_smem(false), st>>>(a);
   return cudaGetLastError();
 }
 
 NormBwdPlan layernorm_bwd_plan(long long rows, int width, int dtype, bool by_type, int num_sms) {
   NormBwdPlan p;
   const NormShape s = norm_shape(width, dtype);
-  const NormKernel fn = norm_kernel(s, dtype, true);
-  p.smem = s.groups * 2 * width * (int)sizeof(float);
-  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);  // a failure shows at the launch
-  const long long need = (rows + s.groups - 1) / s.groups, cap = (long long)num_sms * blocks_per_sm(fn, s.threads, p.smem);
-  p.blocks = (int)(need < cap ? need : cap);
-  p.rows_per_block = (rows + p.blocks - 1) / p.blocks;
-  p.rows_per_block = (p.rows_per_block + s.groups - 1) / s.groups * s.groups;
-  p.blocks = (int)((rows + p.rows_per_block - 1) / p.rows_per_block);
+  p.smem = std::max(s.groups * 2 * width * (int)sizeof(float), s.rows_smem(true));
+  split_rows(rows, s.groups, (long long)num_sms * blocks_per_sm(norm_kernel(s, dtype, true), s.threads, p.smem),
+             &p.blocks, &p.rows_per_block);
   const int types = by_type ? 4 : 1;
   p.off_part = ((size_t)p.blocks * sizeof(unsigned) + 255) & ~(size_t)255;
   p.off_flush = p.off_part + (size_t)p.blocks * types * 2 * width * sizeof(float);
