@@ -295,6 +295,17 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2) k_layernorm_fw
   }
 }
 
+// Four sums into a thread's own slot: stored the first time, added afterwards (without waiting
+// for the old value; one thread's operations on an address happen in its order).
+__device__ __forceinline__ void slot_put(float* p, f2 a, f2 b, bool add) {
+  const float2 x = both(a), y = both(b);
+  if (add)
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x.x), "f"(x.y), "f"(y.x),
+                 "f"(y.y) : "memory");
+  else
+    *reinterpret_cast<float4*>(p) = make_float4(x.x, x.y, y.x, y.y);
+}
+
 // Backward.  Block k takes the contiguous rows [k R, (k + 1) R), its groups in turn, and
 // keeps the gains and the gains' gradients of its columns in registers while the type stays the
 // same (a request's types come in a few runs).  When the type changes, a group adds what it
@@ -329,14 +340,12 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 
         float* p = a.flush + (((long long)blockIdx.x * groups + g.id) * 4 + cur) * 2 * a.width + col;
         const bool add = (flushed >> cur) & 1u;
 #pragma unroll
-        for (int e = 0; e < N / 2; ++e) {
-          float2* pw = reinterpret_cast<float2*>(p + 2 * e);
-          float2* pb = reinterpret_cast<float2*>(p + a.width + 2 * e);
-          const float2 ow = add ? *pw : make_float2(0.f, 0.f), ob = add ? *pb : make_float2(0.f, 0.f);
-          *pw = both(add2(dw[i * (N / 2) + e], pair(ow.x, ow.y)));
-          *pb = both(add2(db[i * (N / 2) + e], pair(ob.x, ob.y)));
-          dw[i * (N / 2) + e] = db[i * (N / 2) + e] = 0ull;
+        for (int e = 0; e < N / 2; e += 2) {
+          slot_put(p + 2 * e, dw[i * (N / 2) + e], dw[i * (N / 2) + e + 1], add);
+          slot_put(p + a.width + 2 * e, db[i * (N / 2) + e], db[i * (N / 2) + e + 1], add);
         }
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) dw[i * (N / 2) + e] = db[i * (N / 2) + e] = 0ull;
       }
       load_gain<N>(a.w + (long long)ty * a.width + col, w + i * (N / 2));
     }
@@ -465,37 +474,52 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : sizeof(E) == 2 ? 
   unsigned seen = 0;
   for (int k = 0; k < groups; ++k) seen |= s_flushed[k] | (s_open[k] >= 0 ? 1u << s_open[k] : 0u);
   if (threadIdx.x == 0) a.seen[blockIdx.x] = seen;
-  for (int t = 0; t < n_types; ++t) {
+  // four columns of one type at a time, the slots of eight groups read together
+  const int cols4 = 2 * a.width / 4;
+  for (int x = threadIdx.x; x < n_types * cols4; x += blockDim.x) {
+    const int t = x / cols4, c = x - t * cols4;
     if (!((seen >> t) & 1u)) continue;
-    float* out = a.part + ((long long)blockIdx.x * n_types + t) * 2 * a.width;
-#pragma unroll 1
-    for (int c = threadIdx.x; c < 2 * a.width; c += blockDim.x) {
-      float v = 0.f;
-#pragma unroll 2
-      for (int k = 0; k < groups; ++k) {
-        if ((s_flushed[k] >> t) & 1u)
-          v += a.flush[(((long long)blockIdx.x * groups + k) * 4 + t) * 2 * a.width + c];
-        if (s_open[k] == t) v += s_sum[k * 2 * a.width + c];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < groups; k0 += 8) {
+      float4 u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = k0 + i;
+        u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < groups && ((s_flushed[k] >> t) & 1u))
+          u[i] = __ldcg(reinterpret_cast<const float4*>(
+                            a.flush + (((long long)blockIdx.x * groups + k) * 4 + t) * 2 * a.width) + c);
       }
-      out[c] = v;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = k0 + i;
+        if (k < groups && s_open[k] == t) {
+          const float4 o = reinterpret_cast<const float4*>(s_sum + k * 2 * a.width)[c];
+          u[i].x += o.x; u[i].y += o.y; u[i].z += o.z; u[i].w += o.w;
+        }
+        v.x += u[i].x; v.y += u[i].y; v.z += u[i].z; v.w += u[i].w;
+      }
     }
+    reinterpret_cast<float4*>(a.part + ((long long)blockIdx.x * n_types + t) * 2 * a.width)[c] = v;
   }
 }
 
-// Sums of the blocks' rows: 32 columns of one type's {dw | db} per block, eight threads a
-// column over the blocks k, k + 8, ...
-__global__ void __launch_bounds__(256) k_layernorm_dw(NormArgs a, int blocks) {
-  __shared__ float s[8][33];
+// Sums of the blocks' rows: 32 columns of one type's {dw | db} per block, 32 threads a column
+// over the blocks k, k + 32, ...
+__global__ void __launch_bounds__(1024) k_layernorm_dw(NormArgs a, int blocks) {
+  __shared__ float s[32][33];
   const int types = a.ty ? 4 : 1, t = blockIdx.y;
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
   float v = 0.f;
   if (c < 2 * a.width)
-    for (int k = part; k < blocks; k += 8)
+#pragma unroll 4
+    for (int k = part; k < blocks; k += 32)
       if ((a.seen[k] >> t) & 1u) v += a.part[((long long)k * types + t) * 2 * a.width + c];
   s[part][threadIdx.x & 31] = v;
   __syncthreads();
   if (part != 0 || c >= 2 * a.width) return;
-  for (int p = 1; p < 8; ++p) v += s[p][threadIdx.x];
+#pragma unroll
+  for (int p = 1; p < 32; ++p) v += s[p][threadIdx.x];
   if (c < a.width) {
     if (a.dw) a.dw[(long long)t * a.width + c] = v;
   } else if (a.db) {
@@ -509,7 +533,9 @@ __global__ void __launch_bounds__(256) k_layernorm_dw(NormArgs a, int blocks) {
 struct NormShape {
   int nv, tpr, threads, groups;
   bool full;  // every thread has all its chunks
-  int ns;     // rows on their way per thread, this one included: 64 to 128 KB a block
+  // rows on their way per thread, this one included.  Two: with three or four the backward
+  // of 320016 x 512 bf16 took 183 and 187 us instead of 165, the forward 112 and 120 instead of 112
+  int ns;
   int rows_smem(bool bwd) const { return ns * nv * threads * 16 * (bwd ? 2 : 1); }
 };
 NormShape norm_shape(int width, int dtype) {
@@ -526,7 +552,7 @@ NormShape norm_shape(int width, int dtype) {
   s.threads = s.tpr <= kNormThreads ? kNormThreads / s.tpr * s.tpr : s.tpr;
   s.groups = s.threads / s.tpr;
   s.full = chunks == s.nv * s.tpr;
-  s.ns = s.nv > 2 ? 1 : s.threads > 512 ? 2 : s.threads > kNormThreads ? 3 : 4;
+  s.ns = s.nv > 2 ? 1 : 2;
   return s;
 }
 
@@ -539,10 +565,10 @@ template <typename E>
 NormKernel norm_kernel(const NormShape& s, bool bwd) {
   if (s.nv > 2) return norm_dir<E, 4, 32, false, 1024, 1>(bwd);
   if (s.threads > 512) return norm_dir<E, 2, 32, false, 1024, 2>(bwd);
-  if (s.threads > kNormThreads) return norm_dir<E, 2, 32, false, 512, 3>(bwd);
-  if (s.tpr == 8) return norm_dir<E, 2, 8, false, kNormThreads, 4>(bwd);
-  if (s.tpr == 16) return norm_dir<E, 2, 16, false, kNormThreads, 4>(bwd);
-  return s.full ? norm_dir<E, 2, 32, true, kNormThreads, 4>(bwd) : norm_dir<E, 2, 32, false, kNormThreads, 4>(bwd);
+  if (s.threads > kNormThreads) return norm_dir<E, 2, 32, false, 512, 2>(bwd);
+  if (s.tpr == 8) return norm_dir<E, 2, 8, false, kNormThreads, 2>(bwd);
+  if (s.tpr == 16) return norm_dir<E, 2, 16, false, kNormThreads, 2>(bwd);
+  return s.full ? norm_dir<E, 2, 32, true, kNormThreads, 2>(bwd) : norm_dir<E, 2, 32, false, kNormThreads, 2>(bwd);
 }
 NormKernel norm_kernel(const NormShape& s, int dtype, bool bwd) {
   return dtype == REC_ATTN_BF16 ? norm_kernel<__nv_bfloat16>(s, bwd) : norm_kernel<float>(s, bwd);
@@ -610,7 +636,7 @@ cudaError_t launch_layernorm_bwd(NormArgs a, const NormBwdPlan& p, void* ws, int
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((2 * a.width + 31) / 32), a.ty ? 4u : 1u);
-  k_layernorm_dw<<<grid, 256, 0, st>>>(a, p.blocks);
+  k_layernorm_dw<<<grid, 1024, 0, st>>>(a, p.blocks);
   return cudaGetLastError();
 }
 
