@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <map>
@@ -1245,6 +1246,7 @@ struct rec_attn_kv_cache_s {
   long long Th = 0;
   int num_sms = 0;
   long long *need = nullptr, *block_need = nullptr, *t_ref = nullptr;
+  uint8_t* block_ordered = nullptr;
   int* block_off = nullptr;
   int* status = nullptr;
   CUtensorMap map_k, map_v;      // boxes of score_tile_keys rows
@@ -1311,7 +1313,8 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
   const size_t off_bn = off_need + th8, off_ref = off_bn + ws_up((size_t)blocks * 8);
   // the tables go up in one copy: hist_off, block_off, the status word
   const size_t tab_bo = ws_up(8 * ((size_t)B + 1)), tab_st = tab_bo + ws_up(4 * ((size_t)B + 1));
-  const size_t off_tab = off_ref + ws_up(8 * (size_t)B), total = off_tab + tab_st + 256;
+  const size_t off_ord = off_ref + ws_up(8 * (size_t)B);
+  const size_t off_tab = off_ord + ws_up((size_t)blocks), total = off_tab + tab_st + 256;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaMemPool_t pool;
   cudaError_t e = device_and_sms(&c->device, &c->num_sms);
@@ -1325,6 +1328,7 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
   c->need = reinterpret_cast<long long*>(w + off_need);
   c->block_need = reinterpret_cast<long long*>(w + off_bn);
   c->t_ref = reinterpret_cast<long long*>(w + off_ref);
+  c->block_ordered = reinterpret_cast<uint8_t*>(w + off_ord);
   c->off_dev = reinterpret_cast<int64_t*>(w + off_tab);
   c->block_off = reinterpret_cast<int*>(w + off_tab + tab_bo);
   c->status = reinterpret_cast<int*>(w + off_tab + tab_st);
@@ -1372,7 +1376,7 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
       n.hist_off = reinterpret_cast<const long long*>(c->off_dev);
       n.block_off = c->block_off; n.t = c->t; n.ty = c->ty; n.batch = B;
       n.use_delay = p.use_delay; n.delay = p.delay_s;
-      n.need = c->need; n.block_need = c->block_need; n.t_ref = c->t_ref; n.status = c->status;
+      n.need = c->need; n.block_need = c->block_need; n.t_ref = c->t_ref; n.block_ordered = c->block_ordered; n.status = c->status;
       e = launch_score_need(n, blocks, st);
     }
   }
@@ -1388,6 +1392,7 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
 // Rows of a key/value head (candidates x heads of the group) above which a call takes the
 // many-row path.
 constexpr int kScoreManyRows = 32;
+constexpr int kScoreCluster = 8;  // the largest cluster that every device places
 
 // One scoring call on such a cache (arguments checked): requests in launches of kScoreMaxReq.
 rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_offsets_host, const int64_t* cand_t_dev,
@@ -1413,15 +1418,37 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
     const int tk = many ? kTile : score_tile_keys(D);
     const int rows = many ? kTile : score_rows_per_item(D, (int)max_rows);
     a.tile_keys = tk;
-    // key tiles per block: about four blocks for each of the two places on every SM, so that
-    // blocks of unequal histories even out (many rows: four items for each stream)
     auto groups_of = [&](int i) {
       return ((cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G + rows - 1) / rows * c->kv_heads;
     };
     auto tiles_of = [&](int i) { return (c->hist_len[b0 + i] + tk - 1) / tk; };
-    long long work = 0;
-    for (int i = 0; i < n; ++i) work += groups_of(i) * tiles_of(i);
-    a.chunk_tiles = (int)std::max<long long>(1, (work + 8LL * c->num_sms - 1) / (8LL * c->num_sms));
+    long long groups = 0, work = 0, most_tiles = 1;
+    for (int i = 0; i < n; ++i) {
+      const long long g = groups_of(i), t = tiles_of(i);
+      groups += g;
+      work += g * t;
+      if (g > 0) most_tiles = std::max<long long>(most_tiles, t);
+    }
+    a.cluster = 0;
+    if (many) {
+      // runs per row group: the fewest steps of the busiest of the two streams on every SM, an
+      // item costing two steps of its own and each extra run (written, read and joined) four
+      const long long streams = 2LL * c->num_sms;
+      long long best = 1, best_cost = LLONG_MAX;
+      for (long long s = 1; s <= std::min<long long>(most_tiles, 32); ++s) {
+        const long long cost = (groups * s + streams - 1) / streams * ((most_tiles + s - 1) / s + 2) + (s > 1 ? 4 * s : 0);
+        if (cost < best_cost) { best = s; best_cost = cost; }
+      }
+      a.chunk_tiles = (int)((most_tiles + best - 1) / best);
+    } else if (groups * kScoreCluster >= c->num_sms || most_tiles <= kScoreCluster) {
+      // a cluster per row group, of as many blocks as give each place (two per SM) four of them
+      a.cluster = 1;
+      while (a.cluster < kScoreCluster && a.cluster < most_tiles && groups * a.cluster < 8LL * c->num_sms) a.cluster *= 2;
+      a.chunk_tiles = (int)most_tiles;
+    } else {
+      // few rows, long histories: runs over the whole chip, four for each place
+      a.chunk_tiles = (int)std::max<long long>(1, (work + 8LL * c->num_sms - 1) / (8LL * c->num_sms));
+    }
     long long items = 0, most_splits = 1;
     for (int i = 0; i < n; ++i) {
       a.cand_start[i] = (int)cand_offsets_host[b0 + i];
@@ -1429,7 +1456,7 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
       const long long splits = std::max<long long>(1, (tiles_of(i) + a.chunk_tiles - 1) / a.chunk_tiles);
       items += groups_of(i) * splits;
       if (groups_of(i) > 0) most_splits = std::max(most_splits, splits);
-      if (items >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
+      if (items * kScoreCluster >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
     }
     a.cand_start[n] = (int)cand_offsets_host[b0 + n];
     a.item_start[n] = (int)items;
@@ -1463,7 +1490,8 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
       AttnArgs t{};
       t.out = out; t.lse = lse; t.status = c->status; t.counters = counters;
       t.n_items = items; t.heads = p.num_heads; t.group = G; t.scale = p.softmax_scale;
-      t.cand.items = desc; t.cand.need = c->need; t.cand.block_need = c->block_need; t.cand.tc = a.tc;
+      t.cand.items = desc; t.cand.need = c->need; t.cand.block_need = c->block_need;
+      t.cand.block_ordered = c->block_ordered; t.cand.tc = a.tc;
       t.cand.q = q; t.cand.k = k; t.cand.v = v;
       t.cand.part_ml = a.part_ml; t.cand.part_o = a.part_o; t.cand.kv_heads = c->kv_heads;
       const int grid = (int)std::min<long long>((items + 1) / 2, c->num_sms);

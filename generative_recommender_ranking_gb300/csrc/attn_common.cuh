@@ -76,6 +76,7 @@ struct CandArgs {
   const CandItem* items;
   const long long* need;        // [Th]: least time of a candidate that sees the key
   const long long* block_need;  // per 64 keys of a request: the largest of them
+  const uint8_t* block_ordered; // per 64 keys: their times of visibility do not go down
   const long long* tc;          // [Nc] candidate times
   const void *q, *k, *v;        // [Nc][heads or kv_heads][d], not rotated (the candidate's own pair)
   float2* part_ml;              // [items][128]: maximum and sum of a run (null: the row's only run)

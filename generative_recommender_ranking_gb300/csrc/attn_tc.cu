@@ -598,17 +598,30 @@ __device__ __forceinline__ void cmp_store(const AttnArgs& a, const CmpReq& cr, i
 }
 
 // CAND: the 128 visibility bits of a row whose candidate stands at time t, over key tile kt
-// of its request (all lanes read the same keys' times).
+// of its request.  Histories stand in time order, so in each 64-key block the visible keys are a
+// prefix (block_ordered), found by bisection; otherwise every key's time is compared.
 __device__ __forceinline__ void cand_mask(const CandArgs& c, const CandItem& ci, int kt, long long t, uint32_t (&vm)[4]) {
-  const long long* need = c.need + ci.hist0 + (long long)kt * kTile;
-  const int n = min(kTile, ci.len - kt * kTile);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    uint32_t bits = 0;
-#pragma unroll 8
-    for (int e = 0; e < 32; ++e)
-      if (32 * w + e < n && __ldg(need + 32 * w + e) <= t) bits |= 1u << e;
-    vm[w] = bits;
+  for (int b = 0; b < 2; ++b) {
+    const int n = min(64, ci.len - kt * kTile - 64 * b);
+    unsigned long long bits = 0ull;
+    if (n > 0) {
+      const long long* need = c.need + ci.hist0 + (long long)kt * kTile + 64 * b;
+      if (c.block_ordered[ci.block0 + 2 * kt + b]) {
+        int lo = 0, hi = n;  // the first key that is not visible
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(need + mid) <= t) lo = mid + 1;
+          else hi = mid;
+        }
+        bits = lo == 64 ? ~0ull : (1ull << lo) - 1ull;
+      } else {
+        for (int e = 0; e < n; ++e)
+          if (__ldg(need + e) <= t) bits |= 1ull << e;
+      }
+    }
+    vm[2 * b] = (uint32_t)bits;
+    vm[2 * b + 1] = (uint32_t)(bits >> 32);
   }
 }
 

@@ -67,6 +67,7 @@ struct ScoreArgs {
   int heads, kv_heads;
   int rotate;
   int tile_keys, chunk_tiles;   // keys per tile, tiles per item
+  int cluster;                  // > 0: an item's tiles are shared by a cluster of so many blocks
   float scale_log2;             // softmax scale * log2(e)
   float omega[kMaxPairs];
   int req0, n_req;              // the launch's requests
@@ -81,6 +82,7 @@ struct NeedArgs {
   int batch, use_delay;
   long long delay;
   long long *need, *block_need, *t_ref;
+  uint8_t* block_ordered;       // 1: the block's keys stand in order of visibility
   int* status;
 };
 int score_tile_keys(int head_dim);

@@ -18,8 +18,10 @@
 // the end.  The scores' and outputs' matrix products are m16n8k16 with 8 rows in the 16: the
 // upper 8 hold the operand rounded to bf16 and the lower 8 what the rounding left, so Q' and P
 // enter with 16 bits of mantissa at no cost (a thread holds row g and row g + 8 of every
-// product).  Blocks over the same rows leave their maximum, sum and unnormalised output in a
-// workspace, which k_score_combine joins in a fixed order.
+// product).  The blocks of a thread-block cluster share one item's key tiles and join their parts
+// through distributed shared memory; where clusters of eight would leave most SMs idle (few rows,
+// long histories) blocks leave their maximum, sum and unnormalised output in a workspace, which
+// k_score_combine joins.  Both orders are fixed.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -134,24 +136,57 @@ __device__ __forceinline__ void finish_row(const ScoreArgs& a, long long cand, i
   if (a.lse && lane == 0) a.lse[cand * a.heads + h] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Joins n parts of one row, part i at ml[i * ml_step], o[i * o_step] (this lane's columns).
-template <int D>
-__device__ __forceinline__ void join_parts(const float2* ml, long long ml_step, const float* o, long long o_step, int n,
-                                           int lane, float& m, float& l, float (&out)[D / 32]) {
+// Joins the parts of one row into (m, l, this lane's columns of the output): lane i brings part
+// i's maximum and sum (-inf and 0 past the last), cols(i, x) reads its columns.
+template <int D, typename Cols>
+__device__ __forceinline__ void join_parts(float2 part, int n, const Cols& cols, float& m, float& l,
+                                           float (&out)[D / 32]) {
   constexpr int DL = D / 32;
-  m = -INFINITY;
-  l = 0.f;
+  float top = part.x;
 #pragma unroll
-  for (int e = 0; e < DL; ++e) out[e] = 0.f;
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  const float m_new = fmaxf(m, top);
+  const float wo = m == -INFINITY ? 0.f : exp2_fast(m - m_new);
+  const float w = part.x == -INFINITY ? 0.f : exp2_fast(part.x - m_new);  // 0: nothing visible in the part
+  float sum = part.y * w;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  l = l * wo + sum;
+#pragma unroll
+  for (int e = 0; e < DL; ++e) out[e] *= wo;
+#pragma unroll 4
   for (int i = 0; i < n; ++i) {
-    const float2 p = ml[i * ml_step];
-    if (p.x == -INFINITY) continue;  // nothing visible in this part
-    const float top = fmaxf(m, p.x), wo = exp2_fast(m - top), wn = exp2_fast(p.x - top);
-    l = l * wo + p.y * wn;
+    const float wi = __shfl_sync(0xffffffffu, w, i);
+    float x[DL];
+    cols(i, x);
 #pragma unroll
-    for (int e = 0; e < DL; ++e) out[e] = out[e] * wo + o[i * o_step + lane * DL + e] * wn;
-    m = top;
+    for (int e = 0; e < DL; ++e) out[e] = fmaf(wi, x[e], out[e]);
   }
+  m = m_new;
+}
+template <int DL>
+__device__ __forceinline__ void read_cols(const float* p, float (&x)[DL]) {
+#pragma unroll
+  for (int e = 0; e < DL; e += 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p + e);
+    x[e] = v.x;
+    x[e + 1] = v.y;
+  }
+}
+
+// Shared memory of the cluster's block `rank`: the address of the same object there, and loads.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(ptx::smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 remote_float2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // M groups of 8 rows.
@@ -180,11 +215,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 
   ScoreItem it;
   {
-    const int x = blockIdx.x, i = upper_index(a.item_start, a.n_req, x);
+    const int x = a.cluster > 0 ? blockIdx.x / a.cluster : blockIdx.x, i = upper_index(a.item_start, a.n_req, x);
     it.b = a.req0 + i;
     it.cand0 = a.cand_start[i];
     const int G = a.heads / a.kv_heads;
-    it.nsplit = n_splits(a, request_tiles(a, it.b));
+    it.nsplit = a.cluster > 0 ? 1 : n_splits(a, request_tiles(a, it.b));
     const int local = x - a.item_start[i];
     it.split = local % it.nsplit;
     it.hk = local / it.nsplit % a.kv_heads;
@@ -194,7 +229,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   const long long hist0 = a.hist_off[it.b];
   const int hist_len = (int)(a.hist_off[it.b + 1] - hist0);
   const int tiles = request_tiles(a, it.b);
-  const int tile0 = it.split * a.chunk_tiles, tile1 = min(tiles, tile0 + a.chunk_tiles);
+  // the block's run of key tiles: an item of its own, or its share of the cluster's
+  const int rank = a.cluster > 0 ? blockIdx.x % a.cluster : 0;
+  const int tile0 = a.cluster > 0 ? tiles * rank / a.cluster : it.split * a.chunk_tiles;
+  const int tile1 = a.cluster > 0 ? tiles * (rank + 1) / a.cluster : min(tiles, tile0 + a.chunk_tiles);
   const int G = a.heads / a.kv_heads;
 
   if (warp == kScoreWarps) {
@@ -368,10 +406,17 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
   }
   __syncthreads();
   for (int r = warp; r < it.rows; r += kScoreWarps + 1) {
-    float m, l, out[D / 32];
-    join_parts<D>(&s_ml[0][r], kRows, s_o + r * D, (long long)kRows * D, kScoreWarps, lane, m, l, out);
+    float m = -INFINITY, l = 0.f, out[D / 32] = {};
+    join_parts<D>(lane < kScoreWarps ? s_ml[lane][r] : make_float2(-INFINITY, 0.f), kScoreWarps,
+                  [&](int i, float (&x)[D / 32]) { read_cols(s_o + (i * kRows + r) * D + lane * (D / 32), x); }, m, l, out);
     const int row = it.rb * kRows + r;
-    if (a.part_ml == nullptr) {
+    if (a.cluster > 1) {  // over the row's first part, which this warp alone has read
+      __syncwarp();
+      if (lane == 0) s_ml[0][r] = make_float2(m, l);
+#pragma unroll
+      for (int e = 0; e < D / 32; e += 2)
+        *reinterpret_cast<float2*>(s_o + r * D + lane * (D / 32) + e) = make_float2(out[e], out[e + 1]);
+    } else if (a.part_ml == nullptr) {
       finish_row<D>(a, it.cand0 + row / G, it.hk * G + row % G, lane, m, l, out);
     } else {
       const long long at = (long long)blockIdx.x * kRows + r;
@@ -379,6 +424,27 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) a.part_o[at * D + lane * (D / 32) + e] = out[e];
     }
+  }
+  if (a.cluster > 1) {  // the cluster's blocks share the rows out and read one another's parts
+    cluster_sync();
+    for (int r = rank + a.cluster * warp; r < it.rows; r += a.cluster * (kScoreWarps + 1)) {
+      float m = -INFINITY, l = 0.f, out[D / 32] = {};
+      const float2 part = lane < a.cluster ? remote_float2(at_rank(&s_ml[0][r], lane)) : make_float2(-INFINITY, 0.f);
+      join_parts<D>(part, a.cluster,
+                    [&](int i, float (&x)[D / 32]) {
+                      const uint32_t p = at_rank(s_o + r * D + lane * (D / 32), i);
+#pragma unroll
+                      for (int e = 0; e < D / 32; e += 2) {
+                        const float2 v = remote_float2(p + 4 * e);
+                        x[e] = v.x;
+                        x[e + 1] = v.y;
+                      }
+                    },
+                    m, l, out);
+      const int row = it.rb * kRows + r;
+      finish_row<D>(a, it.cand0 + row / G, it.hk * G + row % G, lane, m, l, out);
+    }
+    cluster_sync();  // no block leaves while another reads its shared memory
   }
 }
 
@@ -459,8 +525,16 @@ __global__ void __launch_bounds__(128) k_score_combine(const __grid_constant__ S
   const int r = (cand - a.cand_start[i]) * G + h % G, rb = r / rows_per_item;
   const long long at = ((long long)a.item_start[i] + (rb * a.kv_heads + h / G) * nsplit) * rows_per_item +
                        r % rows_per_item;
-  float m, l, o[D / 32];
-  join_parts<D>(a.part_ml + at, rows_per_item, a.part_o + at * D, (long long)rows_per_item * D, nsplit, lane, m, l, o);
+  float m = -INFINITY, l = 0.f, o[D / 32] = {};
+  for (int s0 = 0; s0 < nsplit; s0 += 32) {
+    const int n = min(32, nsplit - s0);
+    const long long p = at + (long long)s0 * rows_per_item;
+    join_parts<D>(lane < n ? a.part_ml[p + (long long)lane * rows_per_item] : make_float2(-INFINITY, 0.f), n,
+                  [&](int i, float (&x)[D / 32]) {
+                    read_cols(a.part_o + (p + (long long)i * rows_per_item) * D + lane * (D / 32), x);
+                  },
+                  m, l, o);
+  }
   finish_row<D>(a, cand, h, lane, m, l, o);
 }
 
@@ -495,7 +569,13 @@ __global__ void __launch_bounds__(kNeedBlock) k_score_need(NeedArgs a) {
     if (threadIdx.x < o) s_max[threadIdx.x] = max(s_max[threadIdx.x], s_max[threadIdx.x + o]);
     __syncthreads();
   }
+  __syncthreads();
   if (threadIdx.x == 0) a.block_need[blockIdx.x] = s_max[0];
+  // keys in order of visibility: a candidate then sees a prefix of the block
+  s_max[threadIdx.x] = p < len ? need : LLONG_MAX;
+  __syncthreads();
+  const int ordered = __syncthreads_and(threadIdx.x == 0 || s_max[threadIdx.x - 1] <= s_max[threadIdx.x]);
+  if (threadIdx.x == 0) a.block_ordered[blockIdx.x] = (uint8_t)(ordered != 0);
 }
 
 template <int D, int M>
@@ -504,8 +584,22 @@ cudaError_t launch_rows_t(const CUtensorMap& k, const CUtensorMap& v, const Scor
   static_assert(kScoreWarps * 8 * M * D * 4 <= kScoreStages * 2 * kOperand, "the warps' outputs fit the stages");
   cudaError_t e = cudaFuncSetAttribute(k_score_rows<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_score_rows<D, M><<<items, kScoreThreads, smem, st>>>(k, v, a);
-  return cudaGetLastError();
+  if (a.cluster <= 1) {
+    k_score_rows<D, M><<<items, kScoreThreads, smem, st>>>(k, v, a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)items * a.cluster);
+  cfg.blockDim = dim3(kScoreThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)a.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_score_rows<D, M>, k, v, a);
 }
 
 template <int D>
