@@ -12,7 +12,7 @@
 // Both modes share one persistent kernel shape: at head_dim 64 two CTAs per SM (256
 // TMEM columns each), at 128 one (512 columns: the accumulators are twice as wide), and
 // six warps -- warp 0 loads with TMA, one thread of warp 1 issues every MMA,
-// warps 2..5 are the compute warpgroup (one TMEM lane, i.e. one tile row, per
+// warps 2 on are the compute warps (one TMEM lane, i.e. one tile row, per
 // thread).  The producer claims the planner's (tile, head) items from a global counter
 // and publishes each item's descriptor in shared memory for the other roles; mode DKV
 // visits key tiles in the mirrored order of the query tiles, so under causal masks
@@ -28,6 +28,12 @@
 //        (bf16) over them; dV += P^T dO_h and dK += dS^T Q'_h.
 // TMEM columns:  DQ   S[0] 0..63 | S[1] 64..127 | dP 128..191 | dQ 192..192+d
 //                DKV  S^T 0..63 | dP^T 64..127 | dV 128..128+d | dK 128+d..128+2d
+// At head_dim 128, where one CTA has the SM and all 512 columns to itself, the other scores have
+// buffers too (DQ: dP[1] 320..383; DKV: S^T[1] 384..447 | dP^T[1] 448..511), so the next step's
+// scores always run under this step's compute, and there are two compute warpgroups: each
+// takes 32 of a step's 64 columns and half of the epilogue's (with one warpgroup and one buffer
+// the SM had four compute warps, all of them waiting for the step's MMAs in turn: 16 ragged
+// requests of 603 to 1850 tokens, 8 query and 2 key/value heads, dQ 228 and dK/dV 383 us).
 // The accumulators stay in TMEM across an item's tiles; the epilogue scales, undoes
 // the rotation and writes bf16 rows.  Everything a compute thread needs besides TMEM
 // comes through shared memory with the tiles: the planner's records of the item's tile
@@ -68,11 +74,21 @@ struct BCfg {
   static constexpr uint32_t kCols = D == 64 ? 256 : 512;
   static constexpr int kBlocksPerSM = D == 64 ? 2 : 1;
   static constexpr uint32_t kDQ = 192, kDV = 128, kDK = 128 + D;
+  static constexpr int kWG = D == 64 ? 1 : 2;     // compute warpgroups
+  static constexpr bool kDB = D == 128;           // every score buffer twice
+  static constexpr int kThreads = 64 + 128 * kWG;
+  // the bf16 operand of a step, 32 columns (two K steps) per chunk: with one warpgroup both chunks
+  // packed over the first 32 score columns (the first chunk's were read before), with two each
+  // over its own
+  static constexpr uint32_t kChunkCols = kWG == 1 ? 16 : 32;
+  // score buffers of step parity b
+  __host__ __device__ static constexpr uint32_t dq_s(uint32_t b) { return b * 64; }
+  __host__ __device__ static constexpr uint32_t dq_dp(uint32_t b) { return kDB && b ? 320u : 128u; }
+  __host__ __device__ static constexpr uint32_t dkv_s(uint32_t b) { return kDB && b ? 384u : 0u; }
 };
 constexpr int kRecB = (int)sizeof(KeyTileRec);
 constexpr int kMaskB = kTile * 16;  // a PARTIAL pair's 128 rows (or columns) of the mask table
 constexpr int kStageRecB = kMaskB > kRecB ? kMaskB : kRecB;  // per streamed stage: one or the other
-constexpr int kThreadsB = 192;
 constexpr uint64_t kWaitNsB = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -82,8 +98,9 @@ enum : int {
   kResEmpty,
   kStrFull,
   kStrEmpty = kStrFull + kNS,
-  kSyFull = kStrEmpty + kNS,  // the step's two score MMAs completed
-  kXReady,                    // [2, by step parity] the compute warps wrote the step's bf16 operands
+  kSyFull = kStrEmpty + kNS,  // [2] the step's two score MMAs completed (by step parity where the
+                              // scores have two buffers, else the first only)
+  kXReady = kSyFull + 2,      // [2, by step parity] the compute warps wrote the step's bf16 operands
                               // (in mode DQ the next step's scores go out before this step's
                               // operands are consumed, so the compute warps may finish a whole step
                               // ahead of the issuer's wait; with one barrier per parity a barrier
@@ -91,7 +108,7 @@ enum : int {
   kDpFree = kXReady + 2,      // DQ: the compute warps loaded the step's dP
   kAccFull,                   // the item's last accumulating MMA completed
   kAccEmpty,                  // the compute warps read the accumulators
-  kGroup,                     // DKV: barrier of the 128 compute threads
+  kGroup,                     // DKV: barrier of the compute threads
   kItemFull,                  // [2] the producer published an item descriptor
   kItemEmpty = kItemFull + 2, // [2] the MMA issuer and the compute warps copied it
   kMmaDone = kItemEmpty + 2,
@@ -101,6 +118,12 @@ enum : int {
 // The ready barrier of step `step` (a stream-wide step count) and its wait parity.
 __host__ __device__ constexpr int xready(uint32_t step) { return kXReady + (int)(step & 1u); }
 __host__ __device__ constexpr uint32_t xready_parity(uint32_t step) { return (step >> 1) & 1u; }
+
+// The scores' barrier of a step and its wait parity.
+template <int D>
+__host__ __device__ constexpr int syfull(uint32_t step) { return kSyFull + (BCfg<D>::kDB ? (int)(step & 1u) : 0); }
+template <int D>
+__host__ __device__ constexpr uint32_t syfull_parity(uint32_t step) { return BCfg<D>::kDB ? (step >> 1) & 1u : step & 1u; }
 
 // Byte offsets from the 1024-aligned base of dynamic shared memory.
 constexpr int kRowB = kTile * 8;  // {-lse2, -D} of a tile's rows, paired (row_neg_lse2 / row_neg_d)
@@ -345,7 +368,8 @@ __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a_tmem, uint32_t b_
   constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, D, false, true);
 #pragma unroll
   for (int kk = 0; kk < kStep / 16; ++kk)
-    ptx::umma_f16_ts(d, a_tmem + kk * 8, mndesc(b_rows + kk * 16 * 128), id, (accumulate || kk > 0) ? 1u : 0u);
+    ptx::umma_f16_ts(d, a_tmem + (kk >> 1) * BCfg<D>::kChunkCols + (kk & 1) * 8, mndesc(b_rows + kk * 16 * 128), id,
+                     (accumulate || kk > 0) ? 1u : 0u);
 }
 
 template <int D, bool DKV>
@@ -384,7 +408,40 @@ __device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
         ptx::tc_fence_after();
         return true;
       };
-      if constexpr (!DKV) {
+      if constexpr (C::kDB) {
+        // two buffers of every score: the scores of step ls + 1 go out before this step's operands are
+        // waited for.  Their buffer was last read by the accumulation of step ls - 1, issued before
+        // them, and by the compute warps, whose operands of that step were waited for.
+        auto issue_scores = [&](int ls) -> bool {
+          int st;
+          if (!stage_of(ls, true, st)) return false;
+          const uint32_t b = (step0 + ls) & 1, half = (uint32_t)(ls & 1) * kHalfBytes;
+          const uint32_t s0 = tmem + (DKV ? C::dkv_s(b) : C::dq_s(b)), s1 = DKV ? s0 + 64 : tmem + C::dq_dp(b);
+          mma_scores<D>(s0, res0, str + (2 * st) * kTileBytes + half);
+          mma_scores<D>(s1, res1, str + (2 * st + 1) * kTileBytes + half);
+          ptx::umma_commit(bars + syfull<D>(step0 + ls));
+          if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // the resident pair read for the last time
+          return true;
+        };
+        if (!issue_scores(0)) goto out;
+        for (int ls = 0; ls < nsteps; ++ls) {
+          int st;
+          stage_of(ls, false, st);
+          if (ls + 1 < nsteps && !issue_scores(ls + 1)) goto out;
+          if (!bw_wait(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
+          ptx::tc_fence_after();
+          if (ls == 0 && !acc_free()) goto out;
+          const uint32_t b = (step0 + ls) & 1, half = (uint32_t)(ls & 1) * kHalfBytes;
+          const uint32_t r0 = str + (2 * st) * kTileBytes + half, r1 = str + (2 * st + 1) * kTileBytes + half;
+          if constexpr (DKV) {
+            mma_acc<D>(tmem + C::kDV, tmem + C::dkv_s(b), r1, ls > 0);       // dV += P^T dO_h
+            mma_acc<D>(tmem + C::kDK, tmem + C::dkv_s(b) + 64, r0, ls > 0);  // dK += dS^T Q'_h
+          } else {
+            mma_acc<D>(tmem + C::kDQ, tmem + C::dq_s(b), r0, ls > 0);  // dQ += dS K'_h
+          }
+          if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
+        }
+      } else if constexpr (!DKV) {
         // S(ls) = Q' K'_h^T into S buffer (step0 + ls) % 2, dP(ls) = dO V_h^T.  dP(ls + 1)
         // goes out as soon as the compute warps have loaded dP(ls), so both scores of
         // the next step are ready when this step's compute ends.
@@ -547,7 +604,9 @@ template <int D>
 __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem,
                                volatile int* abort_flag) {
   using BL = recattn::BL<D>;
+  using C = BCfg<D>;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
+  const int wg = C::kWG == 1 ? 0 : (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
   const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
   const float sl2 = a.scale * kLog2e;
   const uint8_t* sstage = sm + BL::kSRec;  // per stage: key record or mask-table rows
@@ -564,7 +623,7 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
     const long long tok = it.tok_start + pi, grow = tok * H + it.h;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + grow * D;
     if (it.n <= 0) {  // no visible key tile
-      if (row_ok) zero_row<D>(dst);
+      if (row_ok && wg == 0) zero_row<D>(dst);
       continue;
     }
     // the row's time, type and constants, loaded with Q'
@@ -604,40 +663,49 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
       if (lane == 0) ptx::mbar_arrive(bars + kStrEmpty + st);  // the stage's record was read
 #pragma unroll 1
       for (int hh = 0; hh < 2; ++hh, ++step) {
-        if (!bw_wait_warp(bars + kSyFull, step & 1, abort_flag, a.status)) return;
+        if (!bw_wait_warp(bars + syfull<D>(step), syfull_parity<D>(step), abort_flag, a.status)) return;
         ptx::tc_fence_after();
-        const uint32_t sb = tl + (step & 1) * kStep;
+        const uint32_t sb = tl + C::dq_s(step & 1), db = tl + C::dq_dp(step & 1);
         const uint32_t wb[2] = {hh ? vm[2] : vm[0], hh ? vm[3] : vm[1]};  // this step's 64 keys
-        // dP of both chunks and S of the first, then dP's columns go back to the MMA issuer
-        uint32_t d[64], sr[32], pk[16];
-        ptx::tmem_ld32x2_async(tl + 128, tl + 160, d);
-        ptx::tmem_ld32_async(sb, sr);
-        ptx::tmem_wait_ld(d);
-        ptx::tmem_wait_ld32(sr);
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars + kDpFree);
+        uint32_t d[32 * (2 / C::kWG)], sr[32], pk[16];
+        if constexpr (C::kWG == 1) {
+          // dP of both chunks and S of the first, then dP's columns go back to the MMA issuer
+          ptx::tmem_ld32x2_async(db, db + 32, d);
+          ptx::tmem_ld32_async(sb, sr);
+          ptx::tmem_wait_ld(d);
+          ptx::tmem_wait_ld32(sr);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bars + kDpFree);
+        } else {  // this warpgroup's chunk of both
+          ptx::tmem_ld32_async(db + 32 * wg, d);
+          ptx::tmem_ld32_async(sb + 32 * wg, sr);
+          ptx::tmem_wait_ld32(d);
+          ptx::tmem_wait_ld32(sr);
+        }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c == 1) {
+        for (int ci = 0; ci < 2 / C::kWG; ++ci) {
+          const int c = C::kWG == 1 ? ci : wg;  // the step's chunk
+          if (ci == 1) {
             ptx::tmem_ld32_async(sb + 32, sr);
             ptx::tmem_wait_ld32(sr);
           }
+          const uint32_t bits = C::kWG == 1 ? wb[ci] : (wg ? wb[1] : wb[0]);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float y0, y1;
             f2unpack(f2fma(f2pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sl2x2, nl2), y0, y1);
             float p0 = ex2(y0), p1 = ex2(y1);
             if (cls != REC_ATTN_TILE_FULL) {
-              p0 = ((wb[c] >> (2 * e)) & 1u) ? p0 : 0.f;
-              p1 = ((wb[c] >> (2 * e + 1)) & 1u) ? p1 : 0.f;
+              p0 = ((bits >> (2 * e)) & 1u) ? p0 : 0.f;
+              p1 = ((bits >> (2 * e + 1)) & 1u) ? p1 : 0.f;
             }
             float g0, g1;
-            f2unpack(f2mul(f2pack(p0, p1), f2add(f2pack(__uint_as_float(d[32 * c + 2 * e]),
-                                                        __uint_as_float(d[32 * c + 2 * e + 1])), nd2)), g0, g1);
+            f2unpack(f2mul(f2pack(p0, p1), f2add(f2pack(__uint_as_float(d[32 * ci + 2 * e]),
+                                                        __uint_as_float(d[32 * ci + 2 * e + 1])), nd2)), g0, g1);
             pk[e] = bf16x2(g0, g1);
           }
-          ptx::tmem_st16_async(sb + 16 * c, pk);  // dS over S columns already read
+          ptx::tmem_st16_async(sb + C::kChunkCols * c, pk);  // dS over S columns already read
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
@@ -655,19 +723,14 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
       if (row_ok) store_row(dst, acc, a.scale, a.rotate != 0, (float)(ti - it.t_ref), a.omega, wide);
-    } else {
-#pragma unroll 1
-      for (int hc = 0; hc < D / 64; ++hc) {
-        uint32_t acc[64];
-        ptx::tmem_ld64(tl + BCfg<D>::kDQ + 64 * hc, acc);
-        if (hc == D / 64 - 1) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
-        }
-        if (row_ok)
-          store_row(dst + 64 * hc, acc, a.scale, a.rotate != 0, (float)(ti - it.t_ref), a.omega + 32 * hc, wide);
-      }
+    } else {  // each warpgroup 64 of the columns
+      uint32_t acc[64];
+      ptx::tmem_ld64(tl + C::kDQ + 64 * wg, acc);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
+      if (row_ok)
+        store_row(dst + 64 * wg, acc, a.scale, a.rotate != 0, (float)(ti - it.t_ref), a.omega + 32 * wg, wide);
     }
   }
 }
@@ -685,7 +748,7 @@ __device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
   return x;
 }
 
-// The 128 compute threads meet (bounded); `n` counts the uses of the barrier.
+// The compute threads meet (bounded); `n` counts the uses of the barrier.
 __device__ __forceinline__ bool group_sync(uint64_t* bar, uint32_t& n, volatile int* abort_flag, int* status) {
   ptx::mbar_arrive(bar);
   return bw_wait_warp(bar, (n++) & 1, abort_flag, status);
@@ -698,7 +761,9 @@ template <int D>
 __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem,
                                 volatile int* abort_flag) {
   using BL = recattn::BL<D>;
+  using C = BCfg<D>;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
+  const int wg = C::kWG == 1 ? 0 : (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
   const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
   const float sl2 = a.scale * kLog2e;
   const KeyTileRec* rrec = reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec);
@@ -719,6 +784,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     __nv_bfloat16* dkr = static_cast<__nv_bfloat16*>(a.dk) + growk * D;
     __nv_bfloat16* dvr = static_cast<__nv_bfloat16*>(a.dv) + growk * D;
     if (it.n <= 0) {  // no query sees this key tile
+      if (wg != 0) continue;
       if (key_ok && part) {
         for (int e = 0; e < D; e += 4)
           *reinterpret_cast<float4*>(part + e) = *reinterpret_cast<float4*>(part + n_part + e) = make_float4(0, 0, 0, 0);
@@ -745,8 +811,8 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
           if (lane == 0) ptx::mbar_arrive(bars + kResEmpty);
         }
       };
-      if (cls == REC_ATTN_TILE_FULL) {  // the steps of a FULL tile apply no mask
-        release_rec();
+      if (cls == REC_ATTN_TILE_FULL || wg != 0) {  // the steps of a FULL tile apply no mask
+        release_rec();                             // (and one warpgroup builds the others' bits)
         return true;
       }
       if (tslot >= 0) {
@@ -792,17 +858,19 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
       }
       // one 64-query step: P^T and dS^T over the scores' TMEM columns
       auto do_step = [&](int hh) -> bool {
-        if (!bw_wait_warp(bars + kSyFull, step & 1, abort_flag, a.status)) return false;
+        if (!bw_wait_warp(bars + syfull<D>(step), syfull_parity<D>(step), abort_flag, a.status)) return false;
+        const uint32_t sb = tl + C::dkv_s(step & 1);
         ++step;
         ptx::tc_fence_after();
         const uint32_t wb[2] = {hh ? cm.z : cm.x, hh ? cm.w : cm.y};  // this step's 64 queries
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
+        for (int ci = 0; ci < 2 / C::kWG; ++ci) {
+          const int c = C::kWG == 1 ? ci : wg;  // the step's chunk
           uint32_t r[64], pk[16];
-          ptx::tmem_ld32x2_async(tl + 32 * c, tl + 64 + 32 * c, r);
+          ptx::tmem_ld32x2_async(sb + 32 * c, sb + 64 + 32 * c, r);
           // {-lse2, -D} of the chunk's 32 queries, a pair per 16-byte load (broadcast)
           const float4* q4 = reinterpret_cast<const float4*>(rows + (hh * kStep + c * 32) * 2);
-          const uint32_t bits = wb[c];
+          const uint32_t bits = C::kWG == 1 ? wb[c] : (wg ? wb[1] : wb[0]);
           ptx::tmem_wait_ld(r);
           float p[32];
 #pragma unroll
@@ -821,7 +889,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
             p[2 * g + 1] = x1;
             pk[g] = bf16x2(x0, x1);
           }
-          ptx::tmem_st16_async(tl + 16 * c, pk);  // P^T over S^T columns already read
+          ptx::tmem_st16_async(sb + C::kChunkCols * c, pk);  // P^T over S^T columns already read
 #pragma unroll
           for (int g = 0; g < 16; ++g) {
             const float4 k2 = q4[g];
@@ -831,7 +899,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
                                  f2pack(k2.z, k2.w))), g0, g1);
             pk[g] = bf16x2(g0, g1);
           }
-          ptx::tmem_st16_async(tl + 64 + 16 * c, pk);  // dS^T over dP^T columns already read
+          ptx::tmem_st16_async(sb + 64 + C::kChunkCols * c, pk);  // dS^T over dP^T columns already read
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
@@ -853,10 +921,10 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     ptx::tc_fence_after();
     if (part) {  // the part's sums as they are: k_bwd_kv_sum adds the parts of the group
 #pragma unroll 1
-      for (int hc = 0; hc < 2 * D / 64; ++hc) {
+      for (int hc = wg; hc < 2 * D / 64; hc += C::kWG) {
         uint32_t acc[64];
         ptx::tmem_ld64(tl + BCfg<D>::kDV + 64 * hc, acc);  // dV, then dK behind it
-        if (hc == 2 * D / 64 - 1) {
+        if (hc + C::kWG >= 2 * D / 64) {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
@@ -873,13 +941,13 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     }
     // 64 columns at a time: dV packed and stored, then dK scaled, rotated back and stored
 #pragma unroll 1
-    for (int hc = 0; hc < D / 64; ++hc) {
+    for (int hc = wg; hc < D / 64; hc += C::kWG) {
       uint32_t acc[64], wv[32];
       ptx::tmem_ld64(tl + BCfg<D>::kDV + 64 * hc, acc);  // dV, packed before dK is read
 #pragma unroll
       for (int p = 0; p < 32; ++p) wv[p] = bf16x2(__uint_as_float(acc[2 * p]), __uint_as_float(acc[2 * p + 1]));
       ptx::tmem_ld64(tl + BCfg<D>::kDK + 64 * hc, acc);
-      if (hc == D / 64 - 1) {
+      if (hc + C::kWG >= D / 64) {
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
@@ -1097,33 +1165,36 @@ __global__ void __launch_bounds__(256) k_bwd_kv_sum(BwdArgs a) {
 // ------------------------------------------------------------------ kernel
 // maps: Q', K', V, dO as bf16 views [T][heads * d] (K', V: key/value heads), 64 x 128 boxes.
 template <int D, bool DKV>
-__global__ void __launch_bounds__(kThreadsB, BCfg<D>::kBlocksPerSM)
+__global__ void __launch_bounds__(BCfg<D>::kThreads, BCfg<D>::kBlocksPerSM)
     k_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const BwdArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using BL = recattn::BL<D>;
   constexpr uint32_t kCols = BCfg<D>::kCols;
+  constexpr uint32_t kCW = 4 * BCfg<D>::kWG;  // compute warps
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + BL::kBarsOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kNumBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars) + 1;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     ptx::mbar_init(bars + kResFull, 1);
-    ptx::mbar_init(bars + kResEmpty, 1 + 4);  // MMAs done + the compute warps read the record
+    ptx::mbar_init(bars + kResEmpty, 1 + kCW);  // MMAs done + the compute warps read the record
     for (int i = 0; i < kNS; ++i) {
       ptx::mbar_init(bars + kStrFull + i, 1);
-      ptx::mbar_init(bars + kStrEmpty + i, 1 + 4);  // MMAs done + the compute warps read the record
+      ptx::mbar_init(bars + kStrEmpty + i, 1 + kCW);  // MMAs done + the compute warps read the record
     }
-    ptx::mbar_init(bars + kSyFull, 1);
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(bars + kXReady + i, 4);
-    ptx::mbar_init(bars + kDpFree, 4);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars + kSyFull + i, 1);
+      ptx::mbar_init(bars + kXReady + i, kCW);
+    }
+    ptx::mbar_init(bars + kDpFree, kCW);
     ptx::mbar_init(bars + kAccFull, 1);
-    ptx::mbar_init(bars + kAccEmpty, 4);
-    ptx::mbar_init(bars + kGroup, 128);
+    ptx::mbar_init(bars + kAccEmpty, kCW);
+    ptx::mbar_init(bars + kGroup, 32 * kCW);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + kItemFull + i, 1);
-      ptx::mbar_init(bars + kItemEmpty + i, 1 + 4);  // the MMA issuer and the four compute warps
+      ptx::mbar_init(bars + kItemEmpty + i, 1 + kCW);  // the MMA issuer and the compute warps
     }
     ptx::mbar_init(bars + kMmaDone, 1);
     *abort_flag = 0;
@@ -1173,7 +1244,7 @@ cudaError_t launch_mode(const CUtensorMap (&maps)[4], const BwdArgs& a, int grid
   cudaError_t e =
       cudaFuncSetAttribute(k_bwd_tc<D, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize, BL<D>::kDynamic);
   if (e != cudaSuccess) return e;
-  k_bwd_tc<D, DKV><<<grid, kThreadsB, BL<D>::kDynamic, st>>>(maps[0], maps[1], maps[2], maps[3], a);
+  k_bwd_tc<D, DKV><<<grid, BCfg<D>::kThreads, BL<D>::kDynamic, st>>>(maps[0], maps[1], maps[2], maps[3], a);
   return cudaGetLastError();
 }
 
