@@ -1241,8 +1241,8 @@ __global__ void __launch_bounds__(BCfg<D>::kThreads, BCfg<D>::kBlocksPerSM)
 
 template <int D, bool DKV>
 cudaError_t launch_mode(const CUtensorMap (&maps)[4], const BwdArgs& a, int grid, cudaStream_t st) {
-  cudaError_t e =
-      cudaFuncSetAttribute(k_bwd_tc<D, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize, BL<D>::kDynamic);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(done, (const void*)k_bwd_tc<D, DKV>, BL<D>::kDynamic);
   if (e != cudaSuccess) return e;
   k_bwd_tc<D, DKV><<<grid, BCfg<D>::kThreads, BL<D>::kDynamic, st>>>(maps[0], maps[1], maps[2], maps[3], a);
   return cudaGetLastError();

@@ -40,6 +40,7 @@
 #include <cuda_bf16.h>
 
 #include "attn_common.cuh"
+#include "launchers.cuh"
 #include "ptx_sm103.cuh"
 #include "row_mask.cuh"
 #include "wait.cuh"
@@ -1035,8 +1036,8 @@ cudaError_t launch_t(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap&
                      int grid, cudaStream_t st) {
   using L = Layout<D>;
   static_assert(L::kDynamic <= 227 * 1024, "shared memory budget");
-  cudaError_t e =
-      cudaFuncSetAttribute(k_attn_tc<D, GATE, CMP, LAZY, CAND>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynamic);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(done, (const void*)k_attn_tc<D, GATE, CMP, LAZY, CAND>, L::kDynamic);
   if (e != cudaSuccess) return e;
   k_attn_tc<D, GATE, CMP, LAZY, CAND><<<grid, kThreads, L::kDynamic, st>>>(q, k, v, a);
   return cudaGetLastError();

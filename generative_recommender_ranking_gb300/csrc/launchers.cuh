@@ -1,11 +1,26 @@
 // launchers.cuh -- host entry points of the kernels (internal to the library).
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 
 #include "attn_common.cuh"
 
 namespace recattn {
+
+// Raises a kernel's limit of dynamic shared memory, once per kernel and device (`done`: a static
+// of the caller, one bit per device): the call costs a launch's worth of host time.
+inline cudaError_t allow_smem(std::atomic<unsigned long long>& done, const void* fn, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // prologue_ok (may be null) is recorded on st once the RoPE prologue, on another stream,
 // may start: before the planner when it is one kernel, after its first kernel when a
@@ -48,7 +63,7 @@ cudaError_t launch_cmp_fixup(const CmpArgs& c, int batch, const int* req_len, lo
                              int head_dim, cudaStream_t st);
 // Candidates against a cached history with shared heads (score.cu).
 constexpr int kNeedBlock = 64;     // keys per entry of block_need
-constexpr int kScoreMaxReq = 1000; // requests per launch (their tables are kernel parameters)
+constexpr int kScoreMaxReq = 250;  // requests per launch (their tables are kernel parameters: 2 KB)
 struct ScoreArgs {
   // the cache
   const long long* hist_off;    // [B + 1] rows of each request in K', V

@@ -582,7 +582,8 @@ template <int D, int M>
 cudaError_t launch_rows_t(const CUtensorMap& k, const CUtensorMap& v, const ScoreArgs& a, int items, cudaStream_t st) {
   const int smem = kScoreStages * 2 * kOperand + 1024;
   static_assert(kScoreWarps * 8 * M * D * 4 <= kScoreStages * 2 * kOperand, "the warps' outputs fit the stages");
-  cudaError_t e = cudaFuncSetAttribute(k_score_rows<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(done, (const void*)k_score_rows<D, M>, smem);
   if (e != cudaSuccess) return e;
   if (a.cluster <= 1) {
     k_score_rows<D, M><<<items, kScoreThreads, smem, st>>>(k, v, a);
