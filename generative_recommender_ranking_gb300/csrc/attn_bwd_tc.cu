@@ -355,10 +355,11 @@ __device__ __forceinline__ uint64_t mndesc(uint32_t addr) { return ptx::smem_des
 template <int D>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
   constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, kStep, false, false);
+  const uint64_t da = kdesc(a_addr), db = kdesc(b_addr);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
-    ptx::umma_f16(d, kdesc(a_addr + off), kdesc(b_addr + off), id, kk > 0);
+    ptx::umma_f16(d, ptx::smem_desc_at(da, off), ptx::smem_desc_at(db, off), id, kk > 0);
   }
 }
 // D (+)= A B with A (128 x 64, bf16) in TMEM and B = 64 rows of a tile as the K
@@ -366,9 +367,10 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a_addr, uint32_t
 template <int D>
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a_tmem, uint32_t b_rows, bool accumulate) {
   constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, D, false, true);
+  const uint64_t db = mndesc(b_rows);
 #pragma unroll
   for (int kk = 0; kk < kStep / 16; ++kk)
-    ptx::umma_f16_ts(d, a_tmem + (kk >> 1) * BCfg<D>::kChunkCols + (kk & 1) * 8, mndesc(b_rows + kk * 16 * 128), id,
+    ptx::umma_f16_ts(d, a_tmem + (kk >> 1) * BCfg<D>::kChunkCols + (kk & 1) * 8, ptx::smem_desc_at(db, kk * 16 * 128), id,
                      (accumulate || kk > 0) ? 1u : 0u);
 }
 
@@ -872,9 +874,11 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
           const float4* q4 = reinterpret_cast<const float4*>(rows + (hh * kStep + c * 32) * 2);
           const uint32_t bits = C::kWG == 1 ? wb[c] : (wg ? wb[1] : wb[0]);
           ptx::tmem_wait_ld(r);
-          float p[32];
+          uint32_t pd[16];
 #pragma unroll
           for (int g = 0; g < 16; ++g) {
+            // one load for P^T and dS^T: the scores' MMAs take most of the shared memory's
+            // bandwidth, and these loads wait behind them
             const float4 k2 = q4[g];
             float x0, x1;
             f2unpack(f2fma(f2pack(__uint_as_float(r[2 * g]), __uint_as_float(r[2 * g + 1])), sl2x2,
@@ -885,21 +889,15 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
               x0 = ((bits >> (2 * g)) & 1u) ? x0 : 0.f;
               x1 = ((bits >> (2 * g + 1)) & 1u) ? x1 : 0.f;
             }
-            p[2 * g] = x0;
-            p[2 * g + 1] = x1;
             pk[g] = bf16x2(x0, x1);
-          }
-          ptx::tmem_st16_async(sb + C::kChunkCols * c, pk);  // P^T over S^T columns already read
-#pragma unroll
-          for (int g = 0; g < 16; ++g) {
-            const float4 k2 = q4[g];
             float g0, g1;
-            f2unpack(f2mul(f2pack(p[2 * g], p[2 * g + 1]),
+            f2unpack(f2mul(f2pack(x0, x1),
                            f2add(f2pack(__uint_as_float(r[32 + 2 * g]), __uint_as_float(r[32 + 2 * g + 1])),
                                  f2pack(k2.z, k2.w))), g0, g1);
-            pk[g] = bf16x2(g0, g1);
+            pd[g] = bf16x2(g0, g1);
           }
-          ptx::tmem_st16_async(sb + 64 + C::kChunkCols * c, pk);  // dS^T over dP^T columns already read
+          ptx::tmem_st16_async(sb + C::kChunkCols * c, pk);       // P^T over S^T columns already read
+          ptx::tmem_st16_async(sb + 64 + C::kChunkCols * c, pd);  // dS^T over dP^T columns already read
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
@@ -1112,26 +1110,27 @@ __global__ void __launch_bounds__(kTile) k_bwd_colmask(BwdSchedArgs s) {
 }
 
 // ------------------------------------------------------------------ sum of the parts
-// Block = (tile g, key/value head): dK and dV of the tile's rows as the sums of the group's
-// parts, in order; dK is scaled and rotated back; both rounded once.  Eight columns a thread.
+// Block = (part of tile g, key/value head): dK and dV of its rows as the sums of the group's
+// parts, in order; dK is scaled and rotated back; both rounded once.  Eight columns of one row
+// a thread.
 template <int D>
 __global__ void __launch_bounds__(256) k_bwd_kv_sum(BwdArgs a) {
   constexpr int kLanes = D / 8;
-  const long long g = blockIdx.x;
+  constexpr int kBlocks = kTile * kLanes / 256;  // blocks per tile
+  const long long g = blockIdx.x / kBlocks;
   const int hk = blockIdx.y, Hk = a.heads / a.group;
   const ReqMeta m = a.meta[a.qreq[g]];
   const int tile = (int)(g - m.tile_start), c = threadIdx.x & (kLanes - 1);
   const long long T = a.rows / a.heads, n_part = (long long)Hk * a.parts * T * D;
   const long long t_ref = a.t[m.tok_start];
-  for (int r = threadIdx.x / kLanes; r < kTile; r += 256 / kLanes) {
-    const int p = tile * kTile + r;
-    if (p >= m.len) return;
+  const int p = tile * kTile + (int)(blockIdx.x % kBlocks) * (256 / kLanes) + threadIdx.x / kLanes;
+  if (p < m.len) {
     const long long tok = m.tok_start + p;
     const float* src = a.kv_part + ((long long)hk * a.parts * T + tok) * D + 8 * c;
     float k[8], v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = 0; i < a.parts; ++i) {
       const float4* pk = reinterpret_cast<const float4*>(src + (long long)i * T * D);
       const float4* pv = reinterpret_cast<const float4*>(src + (long long)i * T * D + n_part);
@@ -1258,7 +1257,8 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
   if (e != cudaSuccess) return e;
   e = launch_mode<D, true>(maps, a, (int)(a.n_kv_items < cap ? a.n_kv_items : cap), st);
   if (e != cudaSuccess || a.parts == 1) return e;
-  k_bwd_kv_sum<D><<<dim3((unsigned)a.n_tiles, (unsigned)(a.heads / a.group)), 256, 0, st>>>(a);
+  const dim3 grid((unsigned)(a.n_tiles * (kTile * D / 8 / 256)), (unsigned)(a.heads / a.group));
+  k_bwd_kv_sum<D><<<grid, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -356,7 +356,7 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
     if (!wait_bar(B.q_full + qb, (q_it / QB) & 1, abort_flag, a.status)) break;
     ++q_it;
     ptx::tc_fence_after();
-    const uint32_t qa = q_addr + qb * L::kQBytes;
+    const uint64_t dq = ptx::smem_desc_sw128(q_addr + qb * L::kQBytes, 16, 1024);
     if constexpr (WIDE) {
       // S(j) of this item; s_ch counts the stream's S tiles
       auto issue_s = [&](int j) -> bool {
@@ -364,12 +364,11 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
         if (s_ch > 0 && !wait_bar(B.s_free, (s_ch - 1) & 1, abort_flag, a.status)) return false;
         if (!wait_bar(B.k_full + st, ((kv_it + j) / NS) & 1, abort_flag, a.status)) return false;
         ptx::tc_fence_after();
-        const uint32_t kb = k_addr + st * L::kKVBytes;
+        const uint64_t dk = ptx::smem_desc_sw128(k_addr + st * L::kKVBytes, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
-          ptx::umma_f16(tm.s, ptx::smem_desc_sw128(qa + off, 16, 1024), ptx::smem_desc_sw128(kb + off, 16, 1024),
-                        idesc_s, kk > 0 ? 1u : 0u);
+          ptx::umma_f16(tm.s, ptx::smem_desc_at(dq, off), ptx::smem_desc_at(dk, off), idesc_s, kk > 0 ? 1u : 0u);
         }
         ptx::umma_commit(B.s_full);
         ++s_ch;
@@ -380,7 +379,7 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
       for (int j = 0; j < n; ++j) {
         if (j + 1 < n && !issue_s(j + 1)) goto out;
         const int st = (int)((kv_it + j) % NS);
-        const uint32_t vb = v_addr + st * L::kKVBytes;
+        const uint64_t dv = ptx::smem_desc_sw128(v_addr + st * L::kKVBytes, kSlab, 1024);
         const uint32_t pc = p_it++;  // the stream's PV tile count
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
@@ -393,7 +392,7 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
 #pragma unroll
           for (int kk = 0; kk < kChunk / 16; ++kk)
             ptx::umma_f16_ts(tm.o, tm.p + c * (kChunk / 2) + kk * 8,
-                             ptx::smem_desc_sw128(vb + (c * kChunk + kk * 16) * 128, kSlab, 1024), idesc_o,
+                             ptx::smem_desc_at(dv, (c * kChunk + kk * 16) * 128), idesc_o,
                              (j > 0 || c > 0 || kk > 0) ? 1u : 0u);
           ptx::umma_commit(B.pv_done + c);
         }
@@ -409,13 +408,12 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
           if (!wait_bar(B.k_full + st, ((kv_it + j) / NS) & 1, abort_flag, a.status)) return false;
           ptx::tc_fence_after();
         }
-        const uint32_t kb = k_addr + st * L::kKVBytes + c * (kChunk * 128);
+        const uint64_t dk = ptx::smem_desc_sw128(k_addr + st * L::kKVBytes + c * (kChunk * 128), 16, 1024);
         const uint32_t d_tmem = tm.s + (s_ch & 1) * kChunk;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
-          ptx::umma_f16(d_tmem, ptx::smem_desc_sw128(qa + off, 16, 1024), ptx::smem_desc_sw128(kb + off, 16, 1024),
-                        idesc_s, kk > 0 ? 1u : 0u);
+          ptx::umma_f16(d_tmem, ptx::smem_desc_at(dq, off), ptx::smem_desc_at(dk, off), idesc_s, kk > 0 ? 1u : 0u);
         }
         ptx::umma_commit(B.s_full + (s_ch & 1));
         ++s_ch;
@@ -435,12 +433,12 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
           ptx::tc_fence_after();
         }
         // O += P(g) V(g): P from TMEM, V rows of this chunk (both 64-column slabs)
-        const uint32_t vb = v_addr + st * L::kKVBytes;
+        const uint64_t dv = ptx::smem_desc_sw128(v_addr + st * L::kKVBytes + c * (kChunk * 128), kSlab, 1024);
         const uint32_t pa = tm.s + ((ch0 + g) & 1) * kChunk;
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
           ptx::umma_f16_ts(tm.o, pa + kk * 8,
-                           ptx::smem_desc_sw128(vb + c * (kChunk * 128) + kk * 16 * 128, kSlab, 1024), idesc_o,
+                           ptx::smem_desc_at(dv, kk * 16 * 128), idesc_o,
                            (g > 0 || kk > 0) ? 1u : 0u);
         ptx::umma_commit(B.pv_done + (pc & 1));
         if (c == 1) ptx::umma_commit(B.v_empty + st);

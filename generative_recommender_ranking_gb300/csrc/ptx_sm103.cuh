@@ -141,6 +141,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo,
   d |= (uint64_t)2 << 61;
   return d;
 }
+// The descriptor of the same operand `bytes` further on (a multiple of 16, inside the block's
+// shared memory, so the address field does not carry).  One add: a descriptor rebuilt from its
+// address for every MMA made the issuing thread slower than the tensor core (60 cycles an MMA of
+// N = 64 instead of 49).
+__device__ __forceinline__ uint64_t smem_desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 // Instruction descriptor for kind::f16 with bf16 A/B and fp32 D.
 //   bits 4-5 D format (1 = f32), 7-9 A format (1 = bf16), 10-12 B format (1 = bf16),
 //   bit 15 A MN-major, bit 16 B MN-major, bits 17-22 N >> 3, bits 24-28 M >> 4.
