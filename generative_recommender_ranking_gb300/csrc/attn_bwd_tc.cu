@@ -187,26 +187,20 @@ __device__ __forceinline__ BwdItemDesc unpack_desc(const uint4 (&nx)[3]) {
   return d;
 }
 
-// Consumer side of the item slots: the next item's descriptor, or false at the end
-// (or after an abort).  warp_arrive: the compute warps arrive once per warp.
+// Consumer side of the item slots (whole warps): the next item's descriptor, or false at the end
+// (or after an abort).
 template <int D>
-__device__ __forceinline__ bool next_item(uint8_t* sm, uint64_t* bars, uint32_t& it_cnt, bool warp_arrive,
-                                          BwdItemDesc& d, volatile int* abort_flag, int* status) {
+__device__ __forceinline__ bool next_item(uint8_t* sm, uint64_t* bars, uint32_t& it_cnt, BwdItemDesc& d,
+                                          volatile int* abort_flag, int* status) {
   const int slot = (int)(it_cnt & 1);
   const uint32_t ph = (it_cnt >> 1) & 1;
   ++it_cnt;
-  const bool ok = warp_arrive ? bw_wait_warp(bars + kItemFull + slot, ph, abort_flag, status)
-                              : bw_wait(bars + kItemFull + slot, ph, abort_flag, status);
-  if (!ok) return false;
+  if (!bw_wait_warp(bars + kItemFull + slot, ph, abort_flag, status)) return false;
   const ItemSlot* is = reinterpret_cast<const ItemSlot*>(sm + BL<D>::kItems) + slot;
   const uint4 nx[3] = {is->d[0], is->d[1], is->d[2]};
   const int end = is->end;
-  if (warp_arrive) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bars + kItemEmpty + slot);
-  } else {
-    ptx::mbar_arrive(bars + kItemEmpty + slot);
-  }
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bars + kItemEmpty + slot);
   if (end) return false;
   d = unpack_desc(nx);
   return true;
@@ -375,7 +369,7 @@ __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a_tmem, uint32_t b_
 }
 
 template <int D, bool DKV>
-__device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
+__device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem_base, volatile int* abort_flag) {
   using L = BL<D>;
   using C = BCfg<D>;
   constexpr int kTileBytes = L::kTileBytes;
@@ -383,21 +377,24 @@ __device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
   const uint32_t str = ptx::smem_u32(sm + L::kStr);
   constexpr uint32_t kHalfBytes = kStep * 128;  // 64 rows of a tile
   uint32_t it_n = 0, s_it = 0, step = 0, it_cnt = 0;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+  const bool el = ptx::elect_one();  // issues for the warp
   BwdItemDesc it;
-  while (next_item<D>(sm, bars, it_cnt, false, it, abort_flag, a.status)) {
-    if (it.n <= 0) continue;
-    if (!bw_wait(bars + kResFull, it_n & 1, abort_flag, a.status)) goto out;
+  while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
+    const int n = __shfl_sync(0xffffffffu, it.n, 0);
+    if (n <= 0) continue;
+    if (!bw_wait_warp(bars + kResFull, it_n & 1, abort_flag, a.status)) goto out;
     ptx::tc_fence_after();
     {
       const uint32_t ii = it_n++;
-      const int nsteps = 2 * it.n;
+      const int nsteps = 2 * n;
       const uint32_t step0 = step;
       // the streamed stage of local step ls; waits for it on the tile's first step
       auto stage_of = [&](int ls, bool wait_full, int& st) -> bool {
         const uint32_t sj = s_it + (uint32_t)(ls >> 1);
         st = (int)(sj % kNS);
         if (wait_full && (ls & 1) == 0) {
-          if (!bw_wait(bars + kStrFull + st, (sj / kNS) & 1, abort_flag, a.status)) return false;
+          if (!bw_wait_warp(bars + kStrFull + st, (sj / kNS) & 1, abort_flag, a.status)) return false;
           ptx::tc_fence_after();
         }
         return true;
@@ -406,7 +403,7 @@ __device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
       // warps must have read the previous item's
       auto acc_free = [&]() -> bool {
         if (ii == 0) return true;
-        if (!bw_wait(bars + kAccEmpty, (ii - 1) & 1, abort_flag, a.status)) return false;
+        if (!bw_wait_warp(bars + kAccEmpty, (ii - 1) & 1, abort_flag, a.status)) return false;
         ptx::tc_fence_after();
         return true;
       };
@@ -419,10 +416,13 @@ __device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
           if (!stage_of(ls, true, st)) return false;
           const uint32_t b = (step0 + ls) & 1, half = (uint32_t)(ls & 1) * kHalfBytes;
           const uint32_t s0 = tmem + (DKV ? C::dkv_s(b) : C::dq_s(b)), s1 = DKV ? s0 + 64 : tmem + C::dq_dp(b);
-          mma_scores<D>(s0, res0, str + (2 * st) * kTileBytes + half);
-          mma_scores<D>(s1, res1, str + (2 * st + 1) * kTileBytes + half);
-          ptx::umma_commit(bars + syfull<D>(step0 + ls));
-          if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // the resident pair read for the last time
+          if (el) {
+            mma_scores<D>(s0, res0, str + (2 * st) * kTileBytes + half);
+            mma_scores<D>(s1, res1, str + (2 * st + 1) * kTileBytes + half);
+            ptx::umma_commit(bars + syfull<D>(step0 + ls));
+            if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // the resident pair read for the last time
+          }
+          __syncwarp();
           return true;
         };
         if (!issue_scores(0)) goto out;
@@ -430,18 +430,21 @@ __device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
           int st;
           stage_of(ls, false, st);
           if (ls + 1 < nsteps && !issue_scores(ls + 1)) goto out;
-          if (!bw_wait(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
+          if (!bw_wait_warp(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
           ptx::tc_fence_after();
           if (ls == 0 && !acc_free()) goto out;
           const uint32_t b = (step0 + ls) & 1, half = (uint32_t)(ls & 1) * kHalfBytes;
           const uint32_t r0 = str + (2 * st) * kTileBytes + half, r1 = str + (2 * st + 1) * kTileBytes + half;
-          if constexpr (DKV) {
-            mma_acc<D>(tmem + C::kDV, tmem + C::dkv_s(b), r1, ls > 0);       // dV += P^T dO_h
-            mma_acc<D>(tmem + C::kDK, tmem + C::dkv_s(b) + 64, r0, ls > 0);  // dK += dS^T Q'_h
-          } else {
-            mma_acc<D>(tmem + C::kDQ, tmem + C::dq_s(b), r0, ls > 0);  // dQ += dS K'_h
+          if (el) {
+            if constexpr (DKV) {
+              mma_acc<D>(tmem + C::kDV, tmem + C::dkv_s(b), r1, ls > 0);       // dV += P^T dO_h
+              mma_acc<D>(tmem + C::kDK, tmem + C::dkv_s(b) + 64, r0, ls > 0);  // dK += dS^T Q'_h
+            } else {
+              mma_acc<D>(tmem + C::kDQ, tmem + C::dq_s(b), r0, ls > 0);  // dQ += dS K'_h
           }
           if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
+          }
+          __syncwarp();
         }
       } else if constexpr (!DKV) {
         // S(ls) = Q' K'_h^T into S buffer (step0 + ls) % 2, dP(ls) = dO V_h^T.  dP(ls + 1)
@@ -451,10 +454,13 @@ __device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
           int st;
           if (!stage_of(ls, true, st)) return false;
           const uint32_t half = (uint32_t)(ls & 1) * kHalfBytes;
-          mma_scores<D>(tmem + ((step0 + ls) & 1) * kStep, res0, str + (2 * st) * kTileBytes + half);
-          mma_scores<D>(tmem + 128, res1, str + (2 * st + 1) * kTileBytes + half);
-          ptx::umma_commit(bars + kSyFull);
-          if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // Q' and dO read for the last time
+          if (el) {
+            mma_scores<D>(tmem + ((step0 + ls) & 1) * kStep, res0, str + (2 * st) * kTileBytes + half);
+            mma_scores<D>(tmem + 128, res1, str + (2 * st + 1) * kTileBytes + half);
+            ptx::umma_commit(bars + kSyFull);
+            if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // Q' and dO read for the last time
+          }
+          __syncwarp();
           return true;
         };
         if (!issue_scores(0)) goto out;
@@ -462,51 +468,62 @@ __device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
           int st;
           stage_of(ls, false, st);
           if (ls + 1 < nsteps) {
-            if (!bw_wait(bars + kDpFree, (step0 + ls) & 1, abort_flag, a.status)) goto out;
+            if (!bw_wait_warp(bars + kDpFree, (step0 + ls) & 1, abort_flag, a.status)) goto out;
             ptx::tc_fence_after();
             if (!issue_scores(ls + 1)) goto out;
           }
-          if (!bw_wait(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
+          if (!bw_wait_warp(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
           ptx::tc_fence_after();
           if (ls == 0 && !acc_free()) goto out;
           const uint32_t kb = str + (2 * st) * kTileBytes + (ls & 1) * kHalfBytes;
-          mma_acc<D>(tmem + C::kDQ, tmem + ((step0 + ls) & 1) * kStep, kb, ls > 0);  // dQ += dS K'_h
-          if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
+          if (el) {
+            mma_acc<D>(tmem + C::kDQ, tmem + ((step0 + ls) & 1) * kStep, kb, ls > 0);  // dQ += dS K'_h
+            if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
+          }
+          __syncwarp();
         }
       } else {
         // S^T = K' Q'_h^T and dP^T = V dO_h^T
         auto issue_scores = [&](int ls) -> bool {
           int st;
           if (!stage_of(ls, true, st)) return false;
-          mma_scores<D>(tmem + 0, res0, str + (2 * st) * kTileBytes + (ls & 1) * kHalfBytes);
-          mma_scores<D>(tmem + 64, res1, str + (2 * st + 1) * kTileBytes + (ls & 1) * kHalfBytes);
-          ptx::umma_commit(bars + kSyFull);
-          if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // K' and V read for the last time
+          if (el) {
+            mma_scores<D>(tmem + 0, res0, str + (2 * st) * kTileBytes + (ls & 1) * kHalfBytes);
+            mma_scores<D>(tmem + 64, res1, str + (2 * st + 1) * kTileBytes + (ls & 1) * kHalfBytes);
+            ptx::umma_commit(bars + kSyFull);
+            if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // K' and V read for the last time
+          }
+          __syncwarp();
           return true;
         };
         if (!issue_scores(0)) goto out;
         for (int ls = 0; ls < nsteps; ++ls) {
           int st;
           stage_of(ls, false, st);
-          if (!bw_wait(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
+          if (!bw_wait_warp(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
           ptx::tc_fence_after();
           if (ls == 0 && !acc_free()) goto out;
           const uint32_t qb = str + (2 * st) * kTileBytes + (ls & 1) * kHalfBytes;
           const uint32_t ob = str + (2 * st + 1) * kTileBytes + (ls & 1) * kHalfBytes;
-          mma_acc<D>(tmem + C::kDV, tmem + 0, ob, ls > 0);   // dV += P^T dO_h
-          mma_acc<D>(tmem + C::kDK, tmem + 64, qb, ls > 0);  // dK += dS^T Q'_h
-          if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
+          if (el) {
+            mma_acc<D>(tmem + C::kDV, tmem + 0, ob, ls > 0);   // dV += P^T dO_h
+            mma_acc<D>(tmem + C::kDK, tmem + 64, qb, ls > 0);  // dK += dS^T Q'_h
+            if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
+          }
+          __syncwarp();
           if (ls + 1 < nsteps && !issue_scores(ls + 1)) goto out;
         }
       }
       step += (uint32_t)nsteps;
-      s_it += (uint32_t)it.n;
-      ptx::umma_commit(bars + kAccFull);
+      s_it += (uint32_t)n;
+      if (el) ptx::umma_commit(bars + kAccFull);
+      __syncwarp();
     }
   }
 out:
   // all issued MMAs must complete before TMEM is released
-  ptx::umma_commit(bars + kMmaDone);
+  if (el) ptx::umma_commit(bars + kMmaDone);
+  __syncwarp();
   bw_drain(bars + kMmaDone, 0);
 }
 
@@ -619,7 +636,7 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
   const bool wide = (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;  // row pieces 32-byte aligned
   uint32_t it_n = 0, s_it = 0, step = 0, it_cnt = 0;
   BwdItemDesc it;
-  while (next_item<D>(sm, bars, it_cnt, true, it, abort_flag, a.status)) {
+  while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
     const int pi = it.tile * kTile + row;
     const bool row_ok = pi < it.len;
     const long long tok = it.tok_start + pi, grow = tok * H + it.h;
@@ -777,7 +794,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
   const int Hk = a.heads / a.group;
   uint32_t it_n = 0, s_it = 0, step = 0, grp = 0, cbuf = 0, it_cnt = 0;
   BwdItemDesc it;
-  while (next_item<D>(sm, bars, it_cnt, true, it, abort_flag, a.status)) {
+  while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
     const int pj = it.tile * kTile + row;
     const bool key_ok = pj < it.len;
     const long long growk = (it.tok_start + pj) * Hk + it.h / a.parts;
@@ -1216,7 +1233,7 @@ __global__ void __launch_bounds__(BCfg<D>::kThreads, BCfg<D>::kBlocksPerSM)
       bwd_producer<D, DKV>(a, res, str, sm, bars, abort_flag);
     }
   } else if (warp == 1) {
-    if ((threadIdx.x & 31) == 0) bwd_mma<D, DKV>(a, sm, bars, tmem, abort_flag);
+    bwd_mma<D, DKV>(a, sm, bars, tmem, abort_flag);
   } else {
     if constexpr (DKV) bwd_compute_dkv<D>(a, sm, bars, tmem, abort_flag);
     else bwd_compute_dq<D>(a, sm, bars, tmem, abort_flag);

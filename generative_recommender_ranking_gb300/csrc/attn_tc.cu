@@ -316,7 +316,11 @@ drain:
 }
 
 // ------------------------------------------------------------------ MMA issuer
-// Per stream, one thread issues every MMA; tiles are counted across the stream's items.
+// Per stream, one thread issues every MMA; tiles are counted across the stream's items.  At
+// head_dim 128 the whole warp runs this and an elected lane issues (ptx::elect_one: faster
+// issue; 16 requests of 603 to 1850 tokens 114 -> 106 us); at 64, where the softmax is what bounds
+// the kernel and a tile has half as many MMAs, one lane alone is faster (20001 tokens causal:
+// 519 us against 544).
 //
 // WIDE (d = 64): S(t) = Q' K'(t)^T over the whole 128-key tile (N = 128) into the
 // stream's single S buffer.  S(t+1) is issued as soon as the softmax has read S(t)
@@ -330,6 +334,8 @@ drain:
 // g: PV(g) once P(g) is ready, then S(g+2) into the buffer PV(g) has just read (the
 // tensor core runs one thread's MMAs in order).
 template <int D>
+constexpr bool kWarpMma = D == 128;
+template <int D>
 __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, uint32_t tmem,
                         volatile int* abort_flag) {
   using L = Layout<D>;
@@ -341,19 +347,26 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
   const uint32_t q_addr = ptx::smem_u32(sm + L::kQ + s * QB * L::kQBytes);
   const uint32_t k_addr = ptx::smem_u32(sm + L::kK + s * NS * L::kKVBytes);
   const uint32_t v_addr = ptx::smem_u32(sm + L::kV + s * NS * L::kKVBytes);
-  const TmemMap tm = tmem_map<D>(tmem, s);
+  const TmemMap tm = tmem_map<D>(kWarpMma<D> ? __shfl_sync(0xffffffffu, tmem, 0) : tmem, s);
+  const bool el = kWarpMma<D> ? ptx::elect_one() : true;  // issues for the warp
+  auto sync_warp = [] { if constexpr (kWarpMma<D>) __syncwarp(); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return kWarpMma<D> ? wait_bar_warp(bar, parity, abort_flag, a.status) : wait_bar(bar, parity, abort_flag, a.status);
+  };
+  auto uniform = [](int x) { return kWarpMma<D> ? __shfl_sync(0xffffffffu, x, 0) : x; };
   uint32_t it_cnt = 0, q_it = 0, kv_it = 0, p_it = 0, s_ch = 0;
   for (;;) {
     const int slot = (int)(it_cnt & 1);
-    if (!wait_bar(B.item_full + slot, (it_cnt >> 1) & 1, abort_flag, a.status)) break;
+    if (!wait(B.item_full + slot, (it_cnt >> 1) & 1)) break;
     ++it_cnt;
-    const bool end = items[slot].req < 0;
-    const int n = items[slot].n;
-    ptx::mbar_arrive(B.item_empty + slot);
+    const bool end = uniform(items[slot].req) < 0;
+    const int n = uniform(items[slot].n);
+    if (el) ptx::mbar_arrive(B.item_empty + slot);
+    sync_warp();
     if (end) break;
     if (n <= 0) continue;
     const int qb = (int)(q_it % QB);
-    if (!wait_bar(B.q_full + qb, (q_it / QB) & 1, abort_flag, a.status)) break;
+    if (!wait(B.q_full + qb, (q_it / QB) & 1)) break;
     ++q_it;
     ptx::tc_fence_after();
     const uint64_t dq = ptx::smem_desc_sw128(q_addr + qb * L::kQBytes, 16, 1024);
@@ -361,18 +374,21 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
       // S(j) of this item; s_ch counts the stream's S tiles
       auto issue_s = [&](int j) -> bool {
         const int st = (int)((kv_it + j) % NS);
-        if (s_ch > 0 && !wait_bar(B.s_free, (s_ch - 1) & 1, abort_flag, a.status)) return false;
-        if (!wait_bar(B.k_full + st, ((kv_it + j) / NS) & 1, abort_flag, a.status)) return false;
+        if (s_ch > 0 && !wait(B.s_free, (s_ch - 1) & 1)) return false;
+        if (!wait(B.k_full + st, ((kv_it + j) / NS) & 1)) return false;
         ptx::tc_fence_after();
         const uint64_t dk = ptx::smem_desc_sw128(k_addr + st * L::kKVBytes, 16, 1024);
+        if (el) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
-          ptx::umma_f16(tm.s, ptx::smem_desc_at(dq, off), ptx::smem_desc_at(dk, off), idesc_s, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
+            ptx::umma_f16(tm.s, ptx::smem_desc_at(dq, off), ptx::smem_desc_at(dk, off), idesc_s, kk > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit(B.s_full);
+          if (j == n - 1) ptx::umma_commit(B.q_empty + qb);  // last S of the item issued
         }
-        ptx::umma_commit(B.s_full);
+        sync_warp();
         ++s_ch;
-        if (j == n - 1) ptx::umma_commit(B.q_empty + qb);  // last S of the item issued
         return true;
       };
       if (!issue_s(0)) goto out;
@@ -383,20 +399,24 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
         const uint32_t pc = p_it++;  // the stream's PV tile count
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          if (!wait_bar(B.p_full + c, pc & 1, abort_flag, a.status)) goto out;
+          if (!wait(B.p_full + c, pc & 1)) goto out;
           ptx::tc_fence_after();
           if (c == 0) {
-            if (!wait_bar(B.v_full + st, ((kv_it + j) / NS) & 1, abort_flag, a.status)) goto out;
+            if (!wait(B.v_full + st, ((kv_it + j) / NS) & 1)) goto out;
             ptx::tc_fence_after();
           }
+          if (el) {
 #pragma unroll
-          for (int kk = 0; kk < kChunk / 16; ++kk)
-            ptx::umma_f16_ts(tm.o, tm.p + c * (kChunk / 2) + kk * 8,
-                             ptx::smem_desc_at(dv, (c * kChunk + kk * 16) * 128), idesc_o,
-                             (j > 0 || c > 0 || kk > 0) ? 1u : 0u);
-          ptx::umma_commit(B.pv_done + c);
+            for (int kk = 0; kk < kChunk / 16; ++kk)
+              ptx::umma_f16_ts(tm.o, tm.p + c * (kChunk / 2) + kk * 8,
+                               ptx::smem_desc_at(dv, (c * kChunk + kk * 16) * 128), idesc_o,
+                               (j > 0 || c > 0 || kk > 0) ? 1u : 0u);
+            ptx::umma_commit(B.pv_done + c);
+          }
+          sync_warp();
         }
-        ptx::umma_commit(B.v_empty + st);
+        if (el) ptx::umma_commit(B.v_empty + st);
+        sync_warp();
       }
     } else {
       const int nch = 2 * n;
@@ -405,19 +425,22 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
         const int j = g >> 1, c = g & 1;
         const int st = (int)((kv_it + j) % NS);
         if (c == 0) {
-          if (!wait_bar(B.k_full + st, ((kv_it + j) / NS) & 1, abort_flag, a.status)) return false;
+          if (!wait(B.k_full + st, ((kv_it + j) / NS) & 1)) return false;
           ptx::tc_fence_after();
         }
         const uint64_t dk = ptx::smem_desc_sw128(k_addr + st * L::kKVBytes + c * (kChunk * 128), 16, 1024);
         const uint32_t d_tmem = tm.s + (s_ch & 1) * kChunk;
+        if (el) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
-          ptx::umma_f16(d_tmem, ptx::smem_desc_at(dq, off), ptx::smem_desc_at(dk, off), idesc_s, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
+            ptx::umma_f16(d_tmem, ptx::smem_desc_at(dq, off), ptx::smem_desc_at(dk, off), idesc_s, kk > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit(B.s_full + (s_ch & 1));
+          if (g == nch - 1) ptx::umma_commit(B.q_empty + qb);  // last S of the item issued
         }
-        ptx::umma_commit(B.s_full + (s_ch & 1));
+        sync_warp();
         ++s_ch;
-        if (g == nch - 1) ptx::umma_commit(B.q_empty + qb);  // last S of the item issued
         return true;
       };
       const uint32_t ch0 = s_ch;  // global chunk index of this item's chunk 0
@@ -426,22 +449,24 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
         const int j = g >> 1, c = g & 1;
         const int st = (int)((kv_it + j) % NS);
         const uint32_t pc = p_it++;  // the stream's chunk count
-        if (!wait_bar(B.p_full + (pc & 1), (pc >> 1) & 1, abort_flag, a.status)) goto out;
+        if (!wait(B.p_full + (pc & 1), (pc >> 1) & 1)) goto out;
         ptx::tc_fence_after();
         if (c == 0) {
-          if (!wait_bar(B.v_full + st, ((kv_it + j) / NS) & 1, abort_flag, a.status)) goto out;
+          if (!wait(B.v_full + st, ((kv_it + j) / NS) & 1)) goto out;
           ptx::tc_fence_after();
         }
         // O += P(g) V(g): P from TMEM, V rows of this chunk (both 64-column slabs)
         const uint64_t dv = ptx::smem_desc_sw128(v_addr + st * L::kKVBytes + c * (kChunk * 128), kSlab, 1024);
         const uint32_t pa = tm.s + ((ch0 + g) & 1) * kChunk;
+        if (el) {
 #pragma unroll
-        for (int kk = 0; kk < kChunk / 16; ++kk)
-          ptx::umma_f16_ts(tm.o, pa + kk * 8,
-                           ptx::smem_desc_at(dv, kk * 16 * 128), idesc_o,
-                           (g > 0 || kk > 0) ? 1u : 0u);
-        ptx::umma_commit(B.pv_done + (pc & 1));
-        if (c == 1) ptx::umma_commit(B.v_empty + st);
+          for (int kk = 0; kk < kChunk / 16; ++kk)
+            ptx::umma_f16_ts(tm.o, pa + kk * 8, ptx::smem_desc_at(dv, kk * 16 * 128), idesc_o,
+                             (g > 0 || kk > 0) ? 1u : 0u);
+          ptx::umma_commit(B.pv_done + (pc & 1));
+          if (c == 1) ptx::umma_commit(B.v_empty + st);
+        }
+        sync_warp();
         if (NS >= 2) {
           if (g + 2 < nch && !issue_s(g + 2)) goto out;
         } else if (c == 1) {
@@ -452,12 +477,14 @@ __device__ void run_mma(const AttnArgs& a, uint8_t* sm, int s, const SBars& B, u
         }
       }
     }
-    ptx::umma_commit(B.o_ready);
+    if (el) ptx::umma_commit(B.o_ready);
+    sync_warp();
     kv_it += n;
   }
 out:
   // all issued MMAs must complete before TMEM is released
-  ptx::umma_commit(B.mma_done);
+  if (el) ptx::umma_commit(B.mma_done);
+  sync_warp();
   drain_bar(B.mma_done, 0);
 }
 
@@ -1002,7 +1029,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp & 1;
     SBars B;
     B.bind<D>(bars + s * L::kBarsPerStream);
-    if ((threadIdx.x & 31) == 0) {
+    if (kWarpMma<D> && warp >= 2) {
+      run_mma<D>(a, sm, s, B, tmem, abort_flag);
+    } else if ((threadIdx.x & 31) == 0) {
       if (warp < 2) run_producer<D, CAND>(a, &tm_q, &tm_k, &tm_v, sm, s, B, abort_flag);
       else run_mma<D>(a, sm, s, B, tmem, abort_flag);
     }
