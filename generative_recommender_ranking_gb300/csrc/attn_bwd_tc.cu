@@ -74,13 +74,13 @@ struct BCfg {
   static constexpr uint32_t kCols = D == 64 ? 256 : 512;
   static constexpr int kBlocksPerSM = D == 64 ? 2 : 1;
   static constexpr uint32_t kDQ = 192, kDV = 128, kDK = 128 + D;
-  static constexpr int kWG = D == 64 ? 1 : 2;     // compute warpgroups
+  static constexpr int kWG = 2;                   // compute warpgroups, 32 of a step's 64 columns each
+  static constexpr int kSub = D == 64 ? 16 : 32;  // columns a thread holds at a time
   static constexpr bool kDB = D == 128;           // every score buffer twice
   static constexpr int kThreads = 64 + 128 * kWG;
-  // the bf16 operand of a step, 32 columns (two K steps) per chunk: with one warpgroup both chunks
-  // packed over the first 32 score columns (the first chunk's were read before), with two each
-  // over its own
-  static constexpr uint32_t kChunkCols = kWG == 1 ? 16 : 32;
+  // the bf16 operand of a step: each warpgroup's 16 columns of packed pairs (two K steps) over the
+  // first half of the 32 score columns that it has read
+  static constexpr uint32_t kChunkCols = 32;
   // score buffers of step parity b
   __host__ __device__ static constexpr uint32_t dq_s(uint32_t b) { return b * 64; }
   __host__ __device__ static constexpr uint32_t dq_dp(uint32_t b) { return kDB && b ? 320u : 128u; }
@@ -564,31 +564,14 @@ __device__ __forceinline__ unsigned long long f2mul(unsigned long long a, unsign
 __device__ __forceinline__ float row_neg_lse2(const float* tab, int r) { return tab[(r >> 1) * 4 + (r & 1)]; }
 __device__ __forceinline__ float row_neg_d(const float* tab, int r) { return tab[(r >> 1) * 4 + 2 + (r & 1)]; }
 
-// 32 words (64 bf16, one 128-byte row piece) to global memory: 32-byte stores when the
-// gradient buffers are 32-byte aligned (each store then fills whole sectors; the rows of
-// a warp lie H * d * 2 bytes apart), else 16-byte stores.
-__device__ __forceinline__ void st_words(void* dst, const uint32_t (&w)[32], bool wide) {
-  if (wide) {
+// 32 columns of a gradient row, scaled and (rotate) turned back by dt, to global memory in bf16:
+// 32-byte stores when the gradient buffers are 32-byte aligned (each store then fills whole
+// sectors; the rows of a warp lie H * d * 2 bytes apart), else 16-byte stores.
+__device__ __forceinline__ void store_cols(__nv_bfloat16* dst, const uint32_t (&acc)[32], float scale, bool rotate,
+                                          float dt, const float* omega, bool wide) {
+  uint32_t w[16];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      ptx::st_global_v8(static_cast<char*>(dst) + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3],
-                        w[8 * c + 4], w[8 * c + 5], w[8 * c + 6], w[8 * c + 7]);
-  } else {
-    uint4* d4 = static_cast<uint4*>(dst);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) d4[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-  }
-}
-
-// One output row: x * scale, then (rotate) R(dt)^T over adjacent pairs, as bf16.  The
-// angles (at most a few tens of radians) take the hardware sine and cosine: their
-// error, about 1e-5 rad here, is far below the bf16 rounding of the result.
-// (64 columns of a row at dst; omega: their 32 rotation pairs)
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t (&acc)[64], float scale, bool rotate,
-                                         float dt, const float* omega, bool wide) {
-  uint32_t w[32];
-#pragma unroll
-  for (int p = 0; p < 32; ++p) {
+  for (int p = 0; p < 16; ++p) {
     float u = __uint_as_float(acc[2 * p]) * scale, v = __uint_as_float(acc[2 * p + 1]) * scale;
     if (rotate) {
       float sn, cs;
@@ -599,7 +582,16 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t (&a
     }
     w[p] = bf16x2(u, v);
   }
-  st_words(dst, w, wide);
+  if (wide) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      ptx::st_global_v8(reinterpret_cast<char*>(dst) + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3],
+                        w[8 * c + 4], w[8 * c + 5], w[8 * c + 6], w[8 * c + 7]);
+  } else {
+    uint4* d4 = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) d4[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
 }
 
 template <int D>
@@ -625,7 +617,7 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
   using BL = recattn::BL<D>;
   using C = BCfg<D>;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
-  const int wg = C::kWG == 1 ? 0 : (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
+  const int wg = (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
   const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
   const float sl2 = a.scale * kLog2e;
   const uint8_t* sstage = sm + BL::kSRec;  // per stage: key record or mask-table rows
@@ -686,45 +678,38 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
         ptx::tc_fence_after();
         const uint32_t sb = tl + C::dq_s(step & 1), db = tl + C::dq_dp(step & 1);
         const uint32_t wb[2] = {hh ? vm[2] : vm[0], hh ? vm[3] : vm[1]};  // this step's 64 keys
-        uint32_t d[32 * (2 / C::kWG)], sr[32], pk[16];
-        if constexpr (C::kWG == 1) {
-          // dP of both chunks and S of the first, then dP's columns go back to the MMA issuer
-          ptx::tmem_ld32x2_async(db, db + 32, d);
-          ptx::tmem_ld32_async(sb, sr);
-          ptx::tmem_wait_ld(d);
-          ptx::tmem_wait_ld32(sr);
+        constexpr int SUB = C::kSub;
+        const uint32_t bits = wg ? wb[1] : wb[0];  // this warpgroup's 32 keys
+        uint32_t d[32], sr[SUB], pk[SUB / 2];
+        ptx::tmem_ld32_async(db + 32 * wg, d);
+        if constexpr (SUB == 32) ptx::tmem_ld32_async(sb + 32 * wg, sr);
+        ptx::tmem_wait_ld32(d);
+        if constexpr (SUB == 32) ptx::tmem_wait_ld32(sr);
+        if constexpr (!C::kDB) {  // dP's columns go back to the MMA issuer
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bars + kDpFree);
-        } else {  // this warpgroup's chunk of both
-          ptx::tmem_ld32_async(db + 32 * wg, d);
-          ptx::tmem_ld32_async(sb + 32 * wg, sr);
-          ptx::tmem_wait_ld32(d);
-          ptx::tmem_wait_ld32(sr);
         }
 #pragma unroll
-        for (int ci = 0; ci < 2 / C::kWG; ++ci) {
-          const int c = C::kWG == 1 ? ci : wg;  // the step's chunk
-          if (ci == 1) {
-            ptx::tmem_ld32_async(sb + 32, sr);
-            ptx::tmem_wait_ld32(sr);
-          }
-          const uint32_t bits = C::kWG == 1 ? wb[ci] : (wg ? wb[1] : wb[0]);
+        for (int u = 0; u < 32 / SUB; ++u) {
+          if constexpr (SUB == 16) ptx::tmem_ld16(sb + 32 * wg + 16 * u, sr);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < SUB / 2; ++e) {
             float y0, y1;
             f2unpack(f2fma(f2pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sl2x2, nl2), y0, y1);
             float p0 = ex2(y0), p1 = ex2(y1);
             if (cls != REC_ATTN_TILE_FULL) {
-              p0 = ((bits >> (2 * e)) & 1u) ? p0 : 0.f;
-              p1 = ((bits >> (2 * e + 1)) & 1u) ? p1 : 0.f;
+              p0 = ((bits >> (SUB * u + 2 * e)) & 1u) ? p0 : 0.f;
+              p1 = ((bits >> (SUB * u + 2 * e + 1)) & 1u) ? p1 : 0.f;
             }
             float g0, g1;
-            f2unpack(f2mul(f2pack(p0, p1), f2add(f2pack(__uint_as_float(d[32 * ci + 2 * e]),
-                                                        __uint_as_float(d[32 * ci + 2 * e + 1])), nd2)), g0, g1);
+            f2unpack(f2mul(f2pack(p0, p1), f2add(f2pack(__uint_as_float(d[SUB * u + 2 * e]),
+                                                        __uint_as_float(d[SUB * u + 2 * e + 1])), nd2)), g0, g1);
             pk[e] = bf16x2(g0, g1);
           }
-          ptx::tmem_st16_async(sb + C::kChunkCols * c, pk);  // dS over S columns already read
+          // dS over S columns already read
+          if constexpr (SUB == 16) ptx::tmem_st8_async(sb + 32 * wg + 8 * u, pk);
+          else ptx::tmem_st16_async(sb + 32 * wg, pk);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
@@ -735,21 +720,19 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
     if (!bw_wait_warp(bars + kAccFull, it_n & 1, abort_flag, a.status)) return;
     ++it_n;
     ptx::tc_fence_after();
-    if constexpr (D == 64) {
-      uint32_t acc[64];
-      ptx::tmem_ld64(tl + BCfg<D>::kDQ, acc);
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
-      if (row_ok) store_row(dst, acc, a.scale, a.rotate != 0, (float)(ti - it.t_ref), a.omega, wide);
-    } else {  // each warpgroup 64 of the columns
-      uint32_t acc[64];
-      ptx::tmem_ld64(tl + C::kDQ + 64 * wg, acc);
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
+    // each warpgroup half of the columns, 32 at a time
+#pragma unroll 1
+    for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
+      uint32_t acc[32];
+      ptx::tmem_ld32(tl + C::kDQ + c0, acc);
+      if (c0 + 32 >= (wg + 1) * (D / 2)) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
+      }
       if (row_ok)
-        store_row(dst + 64 * wg, acc, a.scale, a.rotate != 0, (float)(ti - it.t_ref), a.omega + 32 * wg, wide);
+        store_cols(dst + c0, acc, a.scale, a.rotate != 0, (float)(ti - it.t_ref), a.omega + c0 / 2, wide);
+      __syncwarp();
     }
   }
 }
@@ -782,7 +765,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
   using BL = recattn::BL<D>;
   using C = BCfg<D>;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
-  const int wg = C::kWG == 1 ? 0 : (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
+  const int wg = (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
   const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
   const float sl2 = a.scale * kLog2e;
   const KeyTileRec* rrec = reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec);
@@ -862,10 +845,15 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     if (!prepare(0, qt, cls, tslot, st, (s_it / kNS) & 1, cbuf)) return;
     ++s_it;
     for (int j = 0; j < it.n; ++j) {
-      // every thread's words of this tile are written, and every thread has read the
-      // other buffer's (a tile ago), which prepare() overwrites next
-      if (!group_sync(bars + kGroup, grp, abort_flag, a.status)) return;
-      const uint4 cm = reinterpret_cast<const uint4*>(colS)[cbuf * kTile + row];
+      // a masked tile's words, written by the first warpgroup, are read by both.  The other buffer,
+      // which prepare() overwrites next, was read at the start of the last tile by every thread:
+      // prepare() comes after this tile's first scores, and those went out after the last tile's
+      // first operands were ready.
+      uint4 cm = make_uint4(0, 0, 0, 0);
+      if (scls != REC_ATTN_TILE_FULL) {
+        if (!group_sync(bars + kGroup, grp, abort_flag, a.status)) return;
+        cm = reinterpret_cast<const uint4*>(colS)[cbuf * kTile + row];
+      }
       const float* rows = srow + st * 2 * kTile;
       int nqt = 0, ncls = 0, nslot = -1, nst = 0;
       uint32_t nph = 0;
@@ -882,39 +870,47 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
         ++step;
         ptx::tc_fence_after();
         const uint32_t wb[2] = {hh ? cm.z : cm.x, hh ? cm.w : cm.y};  // this step's 64 queries
-#pragma unroll 1
-        for (int ci = 0; ci < 2 / C::kWG; ++ci) {
-          const int c = C::kWG == 1 ? ci : wg;  // the step's chunk
-          uint32_t r[64], pk[16];
-          ptx::tmem_ld32x2_async(sb + 32 * c, sb + 64 + 32 * c, r);
-          // {-lse2, -D} of the chunk's 32 queries, a pair per 16-byte load (broadcast)
-          const float4* q4 = reinterpret_cast<const float4*>(rows + (hh * kStep + c * 32) * 2);
-          const uint32_t bits = C::kWG == 1 ? wb[c] : (wg ? wb[1] : wb[0]);
-          ptx::tmem_wait_ld(r);
-          uint32_t pd[16];
+        constexpr int SUB = C::kSub;
+        const uint32_t bits = wg ? wb[1] : wb[0];  // this warpgroup's 32 queries
+        // {-lse2, -D} of the 32 queries, a pair per 16-byte load (broadcast; one load for P^T and
+        // dS^T: the scores' MMAs take most of the shared memory's bandwidth, loads wait behind them)
+        const float4* q4 = reinterpret_cast<const float4*>(rows + (hh * kStep + 32 * wg) * 2);
 #pragma unroll
-          for (int g = 0; g < 16; ++g) {
-            // one load for P^T and dS^T: the scores' MMAs take most of the shared memory's
-            // bandwidth, and these loads wait behind them
-            const float4 k2 = q4[g];
+        for (int u = 0; u < 32 / SUB; ++u) {
+          uint32_t r[2 * SUB], pk[SUB / 2], pd[SUB / 2];  // S^T, then dP^T
+          if constexpr (SUB == 16) {
+            ptx::tmem_ld16x2(sb + 32 * wg + 16 * u, sb + 64 + 32 * wg + 16 * u, r);
+          } else {
+            ptx::tmem_ld32x2_async(sb + 32 * wg, sb + 64 + 32 * wg, r);
+            ptx::tmem_wait_ld(r);
+          }
+#pragma unroll
+          for (int g = 0; g < SUB / 2; ++g) {
+            const float4 k2 = q4[SUB / 2 * u + g];
             float x0, x1;
             f2unpack(f2fma(f2pack(__uint_as_float(r[2 * g]), __uint_as_float(r[2 * g + 1])), sl2x2,
                            f2pack(k2.x, k2.y)), x0, x1);
             x0 = ex2(x0);
             x1 = ex2(x1);
             if (scls != REC_ATTN_TILE_FULL) {  // FULL: queries past the request end have -lse2 = -inf
-              x0 = ((bits >> (2 * g)) & 1u) ? x0 : 0.f;
-              x1 = ((bits >> (2 * g + 1)) & 1u) ? x1 : 0.f;
+              x0 = ((bits >> (SUB * u + 2 * g)) & 1u) ? x0 : 0.f;
+              x1 = ((bits >> (SUB * u + 2 * g + 1)) & 1u) ? x1 : 0.f;
             }
             pk[g] = bf16x2(x0, x1);
             float g0, g1;
             f2unpack(f2mul(f2pack(x0, x1),
-                           f2add(f2pack(__uint_as_float(r[32 + 2 * g]), __uint_as_float(r[32 + 2 * g + 1])),
+                           f2add(f2pack(__uint_as_float(r[SUB + 2 * g]), __uint_as_float(r[SUB + 2 * g + 1])),
                                  f2pack(k2.z, k2.w))), g0, g1);
             pd[g] = bf16x2(g0, g1);
           }
-          ptx::tmem_st16_async(sb + C::kChunkCols * c, pk);       // P^T over S^T columns already read
-          ptx::tmem_st16_async(sb + 64 + C::kChunkCols * c, pd);  // dS^T over dP^T columns already read
+          // P^T and dS^T over the columns already read
+          if constexpr (SUB == 16) {
+            ptx::tmem_st8_async(sb + 32 * wg + 8 * u, pk);
+            ptx::tmem_st8_async(sb + 64 + 32 * wg + 8 * u, pd);
+          } else {
+            ptx::tmem_st16_async(sb + 32 * wg, pk);
+            ptx::tmem_st16_async(sb + 64 + 32 * wg, pd);
+          }
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
@@ -934,43 +930,32 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     if (!bw_wait_warp(bars + kAccFull, it_n & 1, abort_flag, a.status)) return;
     ++it_n;
     ptx::tc_fence_after();
-    if (part) {  // the part's sums as they are: k_bwd_kv_sum adds the parts of the group
+    // dV and dK behind it, 32 columns at a time, the warpgroups in turn
 #pragma unroll 1
-      for (int hc = wg; hc < 2 * D / 64; hc += C::kWG) {
-        uint32_t acc[64];
-        ptx::tmem_ld64(tl + BCfg<D>::kDV + 64 * hc, acc);  // dV, then dK behind it
-        if (hc + C::kWG >= 2 * D / 64) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
-        }
-        if (key_ok) {
-          float* dst = part + (hc < D / 64 ? n_part + 64 * hc : 64 * (hc - D / 64));
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            ptx::st_global_v8(dst + 8 * c, acc[8 * c], acc[8 * c + 1], acc[8 * c + 2], acc[8 * c + 3], acc[8 * c + 4],
-                              acc[8 * c + 5], acc[8 * c + 6], acc[8 * c + 7]);
-        }
-      }
-      continue;
-    }
-    // 64 columns at a time: dV packed and stored, then dK scaled, rotated back and stored
-#pragma unroll 1
-    for (int hc = wg; hc < D / 64; hc += C::kWG) {
-      uint32_t acc[64], wv[32];
-      ptx::tmem_ld64(tl + BCfg<D>::kDV + 64 * hc, acc);  // dV, packed before dK is read
-#pragma unroll
-      for (int p = 0; p < 32; ++p) wv[p] = bf16x2(__uint_as_float(acc[2 * p]), __uint_as_float(acc[2 * p + 1]));
-      ptx::tmem_ld64(tl + BCfg<D>::kDK + 64 * hc, acc);
-      if (hc + C::kWG >= D / 64) {
+    for (int c0 = 32 * wg; c0 < 2 * D; c0 += 64) {
+      uint32_t acc[32];
+      ptx::tmem_ld32(tl + C::kDV + c0, acc);
+      if (c0 + 64 >= 2 * D) {
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
       }
-      if (key_ok) {
-        st_words(dvr + 64 * hc, wv, wide);
-        store_row(dkr + 64 * hc, acc, a.scale, a.rotate != 0, (float)(tj - it.t_ref), a.omega + 32 * hc, wide);
+      const bool is_v = c0 < D;
+      const int col = is_v ? c0 : c0 - D;
+      if (!key_ok) {
+        // nothing to store
+      } else if (part) {  // the part's sums as they are: k_bwd_kv_sum adds the parts of the group
+        float* dst = part + (is_v ? n_part : 0) + col;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          ptx::st_global_v8(dst + 8 * c, acc[8 * c], acc[8 * c + 1], acc[8 * c + 2], acc[8 * c + 3], acc[8 * c + 4],
+                            acc[8 * c + 5], acc[8 * c + 6], acc[8 * c + 7]);
+      } else if (is_v) {
+        store_cols(dvr + col, acc, 1.f, false, 0.f, a.omega, wide);
+      } else {  // scaled and rotated back
+        store_cols(dkr + col, acc, a.scale, a.rotate != 0, (float)(tj - it.t_ref), a.omega + col / 2, wide);
       }
+      __syncwarp();
     }
   }
 }
