@@ -1389,9 +1389,14 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
   return REC_ATTN_OK;
 }
 
-// Rows of a key/value head (candidates x heads of the group) above which a call takes the
-// many-row path.
-constexpr int kScoreManyRows = 32;
+// Which kernel a scoring call takes, by their measured times in microseconds (64 to 8192 keys,
+// 1 to 64 requests, 4 to 128 rows a key/value head): k_score_rows 10 plus 5.8e-3 (head_dim 64; 128:
+// 2.9e-3) for each 32 KB of keys and values that a group of its rows passes over, the many-row
+// kernel 28 plus 4.7e-3 (9e-3) for each 128 keys that 128 of its rows pass over.
+bool score_many(int head_dim, long long small_passes, long long large_passes) {
+  const bool d64 = head_dim == 64;
+  return 10.0 + small_passes * (d64 ? 5.8e-3 : 2.9e-3) > 28.0 + large_passes * (d64 ? 4.7e-3 : 9e-3);
+}
 constexpr int kScoreCluster = 8;  // the largest cluster that every device places
 
 // One scoring call on such a cache (arguments checked): requests in launches of kScoreMaxReq.
@@ -1413,10 +1418,16 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
     for (int i = 0; i < n; ++i)
       max_rows = std::max<long long>(max_rows, (cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G);
     if (max_rows == 0) continue;
-    // many rows per key/value head: 128 of them at a time on the tensor cores' large tiles
-    const bool many = max_rows > kScoreManyRows && c->Th > 0;
-    const int tk = many ? kTile : score_tile_keys(D);
-    const int rows = many ? kTile : score_rows_per_item(D, (int)max_rows);
+    const int small_rows = score_rows_per_item(D, (int)std::min<long long>(max_rows, kTile));
+    const int small_keys = score_tile_keys(D);
+    long long small_passes = 0, large_passes = 0;
+    for (int i = 0; i < n; ++i) {
+      const long long r = (cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G, len = c->hist_len[b0 + i];
+      small_passes += (r + small_rows - 1) / small_rows * c->kv_heads * ((len + small_keys - 1) / small_keys);
+      large_passes += (r + kTile - 1) / kTile * c->kv_heads * ((len + kTile - 1) / kTile);
+    }
+    const bool many = c->Th > 0 && score_many(D, small_passes, large_passes);
+    const int tk = many ? kTile : small_keys, rows = many ? kTile : small_rows;
     a.tile_keys = tk;
     auto groups_of = [&](int i) {
       return ((cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G + rows - 1) / rows * c->kv_heads;
@@ -1441,13 +1452,17 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
       }
       a.chunk_tiles = (int)((most_tiles + best - 1) / best);
     } else if (groups * kScoreCluster >= c->num_sms || most_tiles <= kScoreCluster) {
-      // a cluster per row group, of as many blocks as give each place (two per SM) four of them
+      // a cluster per row group, of as many blocks as still run all at once, two per SM (each block
+      // pays about as much to start as four tiles cost: 64 requests of 8192 keys, 4 rows, head_dim 128:
+      // clusters of 1, 2, 4, 8 took 93, 87, 94, 110 us; of 1000 keys, 15, 14, 20, 31 us)
       a.cluster = 1;
-      while (a.cluster < kScoreCluster && a.cluster < most_tiles && groups * a.cluster < 8LL * c->num_sms) a.cluster *= 2;
+      while (a.cluster < kScoreCluster && a.cluster < most_tiles && 2 * groups * a.cluster <= 2LL * c->num_sms)
+        a.cluster *= 2;
       a.chunk_tiles = (int)most_tiles;
     } else {
-      // few rows, long histories: runs over the whole chip, four for each place
-      a.chunk_tiles = (int)std::max<long long>(1, (work + 8LL * c->num_sms - 1) / (8LL * c->num_sms));
+      // few rows, long histories: runs that fill the chip once (two blocks per SM), and at most about
+      // 64 of them for a row (each costs its join)
+      a.chunk_tiles = (int)std::max<long long>((work + 2LL * c->num_sms - 1) / (2LL * c->num_sms), (most_tiles + 63) / 64);
     }
     long long items = 0, most_splits = 1;
     for (int i = 0; i < n; ++i) {

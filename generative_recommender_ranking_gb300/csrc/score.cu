@@ -512,30 +512,50 @@ __global__ void __launch_bounds__(128) k_score_pack(const __grid_constant__ Scor
   if (x == 0 && threadIdx.x < 8) counters[threadIdx.x] = 0;
 }
 
-// One warp per output row (candidate, head): its parts, in the order of the key tiles.
-template <int D>
+// WPR warps per output row (candidate, head), four rows' worth of warps a block: each joins a
+// run of the row's parts, in the order of the key tiles, the first then joins the warps' in order.
+template <int D, int WPR>
 __global__ void __launch_bounds__(128) k_score_combine(const __grid_constant__ ScoreArgs a, int rows_per_item) {
-  const int lane = threadIdx.x & 31;
+  constexpr int DL = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
   const int first = a.cand_start[0];
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= (long long)(a.cand_start[a.n_req] - first) * a.heads) return;
-  const int cand = first + (int)(w / a.heads), h = (int)(w % a.heads);
-  const int i = upper_index(a.cand_start, a.n_req, cand);
-  const int G = a.heads / a.kv_heads, nsplit = n_splits(a, request_tiles(a, a.req0 + i));
-  const int r = (cand - a.cand_start[i]) * G + h % G, rb = r / rows_per_item;
-  const long long at = ((long long)a.item_start[i] + (rb * a.kv_heads + h / G) * nsplit) * rows_per_item +
-                       r % rows_per_item;
-  float m = -INFINITY, l = 0.f, o[D / 32] = {};
-  for (int s0 = 0; s0 < nsplit; s0 += 32) {
-    const int n = min(32, nsplit - s0);
-    const long long p = at + (long long)s0 * rows_per_item;
-    join_parts<D>(lane < n ? a.part_ml[p + (long long)lane * rows_per_item] : make_float2(-INFINITY, 0.f), n,
-                  [&](int i, float (&x)[D / 32]) {
-                    read_cols(a.part_o + (p + (long long)i * rows_per_item) * D + lane * (D / 32), x);
-                  },
-                  m, l, o);
+  const long long w = (long long)blockIdx.x * (4 / WPR) + warp / WPR;
+  const bool in = w < (long long)(a.cand_start[a.n_req] - first) * a.heads;
+  const int cand = first + (int)(in ? w / a.heads : 0), h = (int)(in ? w % a.heads : 0);
+  float m = -INFINITY, l = 0.f, o[DL] = {};
+  if (in) {
+    const int i = upper_index(a.cand_start, a.n_req, cand);
+    const int G = a.heads / a.kv_heads, nsplit = n_splits(a, request_tiles(a, a.req0 + i));
+    const int r = (cand - a.cand_start[i]) * G + h % G, rb = r / rows_per_item;
+    const long long at = ((long long)a.item_start[i] + (rb * a.kv_heads + h / G) * nsplit) * rows_per_item +
+                         r % rows_per_item;
+    const int s1 = nsplit * (sub + 1) / WPR;
+    for (int s0 = nsplit * sub / WPR; s0 < s1; s0 += 32) {
+      const int n = min(32, s1 - s0);
+      const long long p = at + (long long)s0 * rows_per_item;
+      join_parts<D>(lane < n ? a.part_ml[p + (long long)lane * rows_per_item] : make_float2(-INFINITY, 0.f), n,
+                    [&](int k, float (&x)[DL]) {
+                      read_cols(a.part_o + (p + (long long)k * rows_per_item) * D + lane * DL, x);
+                    },
+                    m, l, o);
+    }
   }
-  finish_row<D>(a, cand, h, lane, m, l, o);
+  if constexpr (WPR > 1) {
+    __shared__ float2 s_ml[4];
+    __shared__ float s_o[4][D];
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+    for (int e = 0; e < DL; ++e) s_o[warp][lane * DL + e] = o[e];
+    __syncthreads();
+    if (sub != 0) return;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < DL; ++e) o[e] = 0.f;
+    join_parts<D>(lane < WPR ? s_ml[warp + lane] : make_float2(-INFINITY, 0.f), WPR,
+                  [&](int k, float (&x)[DL]) { read_cols(&s_o[warp + k][lane * DL], x); }, m, l, o);
+  }
+  if (in) finish_row<D>(a, cand, h, lane, m, l, o);
 }
 
 // When key j becomes visible to a candidate, as the least candidate time; per 64-key block of
@@ -606,7 +626,9 @@ cudaError_t launch_rows_t(const CUtensorMap& k, const CUtensorMap& v, const Scor
 template <int D>
 cudaError_t launch_combine(const ScoreArgs& a, int rows_per_item, cudaStream_t st) {
   const long long rows = (long long)(a.cand_start[a.n_req] - a.cand_start[0]) * a.heads;
-  k_score_combine<D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, rows_per_item);
+  // a warp per row where the rows alone fill the chip, else four (long histories, few rows)
+  if (rows >= 4096) k_score_combine<D, 1><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, rows_per_item);
+  else k_score_combine<D, 4><<<(unsigned)rows, 128, 0, st>>>(a, rows_per_item);
   return cudaGetLastError();
 }
 
