@@ -331,10 +331,12 @@ def rec_attn_compress(offsets_host, hist_begin, hist_len, segments, x, timestamp
 
 
 def _rows(fn: str, x, **others):
-    """(dtype, rows, width) of a contiguous [rows, width] tensor; the others must match it."""
+    """(dtype, rows, width) of a contiguous [rows, width] tensor of the current device; the
+    others must match it."""
     import torch
     dtypes = {torch.bfloat16: BF16, torch.float32: FP32}
     ok = x.dim() == 2 and x.dtype in dtypes and x.is_contiguous()
+    ok = ok and x.is_cuda and x.device.index == torch.cuda.current_device()
     for o in others.values():
         ok = ok and o.dtype == x.dtype and o.shape == x.shape and o.device == x.device and o.is_contiguous()
     if not ok:

@@ -26,6 +26,7 @@ using namespace recattn;
 struct rec_attn_plan_s {
   rec_attn_params p;
   int32_t kv_heads = 0;  // key/value heads; p.num_heads / kv_heads query heads share one
+  bool grouped = false;  // made by rec_attn_plan_grouped
   int device = 0;
   int num_sms = 0;
   int32_t batch = 0;
@@ -164,6 +165,7 @@ cudaError_t pool_for(int device, cudaMemPool_t* out) {
   props.location.type = cudaMemLocationTypeDevice;
   props.location.id = device;
   cudaMemPool_t pool;
+  const OutsideCapture now;
   cudaError_t e = cudaMemPoolCreate(&pool, &props);
   if (e != cudaSuccess) return e;
   uint64_t keep = ~0ull;
@@ -207,6 +209,16 @@ REC_ATTN_API const char* rec_attn_status_string(rec_attn_status s) {
 }
 
 namespace {
+
+// Whether work on the stream would enter a graph (or could, for the legacy stream, while another
+// stream of the device is being captured).
+bool capturing(void* stream) {
+  cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &s);
+  if (e == cudaSuccess) return s != cudaStreamCaptureStatusNone;
+  cudaGetLastError();
+  return e == cudaErrorStreamCaptureImplicit;
+}
 
 // kv_heads: key/value heads (params->num_heads: one per query head).
 rec_attn_status plan_impl(const rec_attn_params* params, int32_t kv_heads, int32_t keep_user_queries, int32_t batch,
@@ -359,8 +371,16 @@ REC_ATTN_API rec_attn_status rec_attn_plan_grouped(const rec_attn_params* params
                                                    void* stream, rec_attn_plan_t** plan_out) {
   if (plan_out) *plan_out = nullptr;
   if (keep_user_queries < -1) return REC_ATTN_ERR_INVALID_ARG;
-  return plan_impl(params, num_kv_heads, keep_user_queries, batch, offsets_host, offsets_dev, timestamps_dev,
-                   types_dev, stream, plan_out);
+  if (plan_out) *plan_out = nullptr;
+  if (capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;  // its tables are staged from the call's own memory
+  try {
+    const rec_attn_status s = plan_impl(params, num_kv_heads, keep_user_queries, batch, offsets_host, offsets_dev,
+                                        timestamps_dev, types_dev, stream, plan_out);
+    if (s == REC_ATTN_OK) (*plan_out)->grouped = true;
+    return s;
+  } catch (...) {
+    return REC_ATTN_ERR_OOM;
+  }
 }
 
 REC_ATTN_API int64_t rec_attn_query_keep(int64_t hist_len, int64_t n_min, int32_t layer, int32_t n_layers) {
@@ -447,6 +467,7 @@ rec_attn_status fwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return from_cuda(e);
   if (dev != plan->device) return REC_ATTN_ERR_INVALID_ARG;
+  if (plan->grouped && capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   plan->stream = st;
   if (T == 0) return REC_ATTN_OK;
@@ -578,6 +599,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return from_cuda(e);
   if (dev != plan->device) return REC_ATTN_ERR_INVALID_ARG;
+  if (plan->grouped && capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   plan->stream = st;
   if (T == 0) return REC_ATTN_OK;
@@ -886,6 +908,7 @@ REC_ATTN_API rec_attn_status rec_attn_compress(int32_t batch, const int64_t* off
 namespace {
 
 constexpr int kMaxNormWidth = 16384;
+constexpr long long kMaxNormRows = (1LL << 31) - 65536;  // a block's reads ahead count rows past its last in 32 bits
 
 bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
@@ -896,7 +919,7 @@ rec_attn_status check_norm(int32_t dtype, int64_t rows, int64_t width, int32_t g
   if (!(std::isfinite(eps) && eps >= 0.f)) return REC_ATTN_ERR_INVALID_ARG;
   if ((groups != 1 && groups != kTypes) || (groups == 1 && types) || (groups > 1 && rows > 0 && !types))
     return REC_ATTN_ERR_INVALID_ARG;
-  if (width > kMaxNormWidth || rows >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
+  if (width > kMaxNormWidth || rows > kMaxNormRows) return REC_ATTN_ERR_UNSUPPORTED;
   return REC_ATTN_OK;
 }
 
@@ -1240,10 +1263,13 @@ struct rec_attn_kv_cache_s {
   int8_t* ty = nullptr;
   int64_t* off_dev = nullptr;
   float omega[kMaxPairs] = {};
-  // bf16 with shared heads: the history rows alone (K' and V packed as the caller's history),
-  // read in place by the kernels of score.cu; no slots
+  // bf16 with shared heads: the history rows alone, read in place by the kernels of score.cu; no
+  // slots.  Each request's rows of K' and V end in zero rows up to a whole tile, so that no tile
+  // holds another request's values (a masked key enters with weight 0, and 0 times NaN is NaN)
   bool shared = false;
-  long long Th = 0;
+  bool grouped = false;  // made by rec_attn_cache_create_grouped
+  long long Th = 0;      // history rows, the zero rows included
+  int32_t* len_dev = nullptr;  // [B] keys of each request
   int num_sms = 0;
   long long *need = nullptr, *block_need = nullptr, *t_ref = nullptr;
   uint8_t* block_ordered = nullptr;
@@ -1303,18 +1329,38 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
                               rec_attn_kv_cache_t** cache_out) {
   const rec_attn_params& p = c->p;
   const int32_t B = c->batch;
-  const long long Th = c->Th;
+  std::vector<int64_t> rows_off((size_t)B + 1, 0);
   std::vector<int> block_off((size_t)B + 1, 0);
-  for (int32_t b = 0; b < B; ++b)
+  for (int32_t b = 0; b < B; ++b) {
+    rows_off[b + 1] = rows_off[b] + (c->hist_len[b] + kTile - 1) / kTile * kTile;
     block_off[b + 1] = block_off[b] + (int)((c->hist_len[b] + kNeedBlock - 1) / kNeedBlock);
+  }
+  const long long Th = c->Th = rows_off[B];
+  if (Th >= (1LL << 31)) { delete c; return REC_ATTN_ERR_UNSUPPORTED; }
   const int blocks = block_off[B];
   const size_t kv = ws_up((size_t)Th * c->kv_heads * p.head_dim * 2), th8 = ws_up((size_t)Th * 8);
   const size_t off_t = 2 * kv, off_ty = off_t + th8, off_need = off_ty + ws_up((size_t)Th);
   const size_t off_bn = off_need + th8, off_ref = off_bn + ws_up((size_t)blocks * 8);
-  // the tables go up in one copy: hist_off, block_off, the status word
-  const size_t tab_bo = ws_up(8 * ((size_t)B + 1)), tab_st = tab_bo + ws_up(4 * ((size_t)B + 1));
+  // the tables go up in one copy: rows_off, block_off, hist_len, the status word
+  const size_t tab_bo = ws_up(8 * ((size_t)B + 1)), tab_len = tab_bo + ws_up(4 * ((size_t)B + 1));
+  const size_t tab_st = tab_len + ws_up(4 * (size_t)B);
   const size_t off_ord = off_ref + ws_up(8 * (size_t)B);
   const size_t off_tab = off_ord + ws_up((size_t)blocks), total = off_tab + tab_st + 256;
+  std::vector<char> up(tab_st + 256, 0);
+  std::memcpy(up.data(), rows_off.data(), 8 * ((size_t)B + 1));
+  std::memcpy(up.data() + tab_bo, block_off.data(), 4 * ((size_t)B + 1));
+  for (int32_t b = 0; b < B; ++b) reinterpret_cast<int32_t*>(up.data() + tab_len)[b] = (int32_t)c->hist_len[b];
+  std::vector<SlotReq> reqs((size_t)B);
+  for (int32_t b = 0; b < B; ++b) {
+    SlotReq& r = reqs[b];
+    r.src_start = r.ref_row = hist_offsets_host[b];
+    r.dst_start = rows_off[b];
+    r.ref_dst = 0;
+    r.len = (int)c->hist_len[b];
+    r.cap = (int)(rows_off[b + 1] - rows_off[b]);
+    r.pad = 0;
+  }
+  const SlotTable tab = slot_table(reqs);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaMemPool_t pool;
   cudaError_t e = device_and_sms(&c->device, &c->num_sms);
@@ -1331,10 +1377,8 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
   c->block_ordered = reinterpret_cast<uint8_t*>(w + off_ord);
   c->off_dev = reinterpret_cast<int64_t*>(w + off_tab);
   c->block_off = reinterpret_cast<int*>(w + off_tab + tab_bo);
+  c->len_dev = reinterpret_cast<int32_t*>(w + off_tab + tab_len);
   c->status = reinterpret_cast<int*>(w + off_tab + tab_st);
-  std::vector<char> up(tab_st + 256, 0);
-  std::memcpy(up.data(), hist_offsets_host, 8 * ((size_t)B + 1));
-  std::memcpy(up.data() + tab_bo, block_off.data(), 4 * ((size_t)B + 1));
   e = cudaMemcpyAsync(w + off_tab, up.data(), up.size(), cudaMemcpyHostToDevice, st);  // staged before the call returns
   if (e == cudaSuccess) e = cudaMemsetAsync(c->t_ref, 0, 8 * (size_t)B, st);
   if (e == cudaSuccess && Th > 0) {
@@ -1343,15 +1387,6 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
     if (!encode_map(&c->map_k, c->k, Th, cols, tk) || !encode_map(&c->map_v, c->v, Th, cols, tk) ||
         !encode_map(&c->map_k128, c->k, Th, cols) || !encode_map(&c->map_v128, c->v, Th, cols))
       e = cudaErrorUnknown;
-    std::vector<SlotReq> reqs((size_t)B);
-    for (int32_t b = 0; b < B; ++b) {
-      SlotReq& r = reqs[b];
-      r.src_start = r.dst_start = r.ref_row = hist_offsets_host[b];
-      r.ref_dst = 0;
-      r.len = r.cap = (int)c->hist_len[b];
-      r.pad = 0;
-    }
-    const SlotTable tab = slot_table(reqs);
     void* dtab = nullptr;
     if (e == cudaSuccess) e = upload_table(tab, c->device, st, &dtab);
     if (e == cudaSuccess) {
@@ -1374,7 +1409,7 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
     if (e == cudaSuccess) {
       NeedArgs n{};
       n.hist_off = reinterpret_cast<const long long*>(c->off_dev);
-      n.block_off = c->block_off; n.t = c->t; n.ty = c->ty; n.batch = B;
+      n.hist_len = c->len_dev; n.block_off = c->block_off; n.t = c->t; n.ty = c->ty; n.batch = B;
       n.use_delay = p.use_delay; n.delay = p.delay_s;
       n.need = c->need; n.block_need = c->block_need; n.t_ref = c->t_ref; n.block_ordered = c->block_ordered; n.status = c->status;
       e = launch_score_need(n, blocks, st);
@@ -1406,6 +1441,7 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
   const int G = p.num_heads / c->kv_heads, D = p.head_dim;
   ScoreArgs a{};
   a.hist_off = reinterpret_cast<const long long*>(c->off_dev);
+  a.hist_len = c->len_dev;
   a.need = c->need; a.block_need = c->block_need; a.block_off = c->block_off; a.t_ref = c->t_ref; a.status = c->status;
   a.tc = reinterpret_cast<const long long*>(cand_t_dev);
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse;
@@ -1418,6 +1454,8 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
     for (int i = 0; i < n; ++i)
       max_rows = std::max<long long>(max_rows, (cand_offsets_host[b0 + i + 1] - cand_offsets_host[b0 + i]) * G);
     if (max_rows == 0) continue;
+    if ((cand_offsets_host[b0 + n] - cand_offsets_host[b0]) * p.num_heads >= (1LL << 31))
+      return REC_ATTN_ERR_UNSUPPORTED;
     const int small_rows = score_rows_per_item(D, (int)std::min<long long>(max_rows, kTile));
     const int small_keys = score_tile_keys(D);
     long long small_passes = 0, large_passes = 0;
@@ -1471,7 +1509,7 @@ rec_attn_status score_shared(const rec_attn_kv_cache_s* c, const int64_t* cand_o
       const long long splits = std::max<long long>(1, (tiles_of(i) + a.chunk_tiles - 1) / a.chunk_tiles);
       items += groups_of(i) * splits;
       if (groups_of(i) > 0) most_splits = std::max(most_splits, splits);
-      if (items * kScoreCluster >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
+      if (items * (many ? kTile : kScoreCluster) >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
     }
     a.cand_start[n] = (int)cand_offsets_host[b0 + n];
     a.item_start[n] = (int)items;
@@ -1572,9 +1610,17 @@ rec_attn_status cache_create_impl(const rec_attn_params* params, int32_t kv_head
     for (int i = 0; i < params->head_dim / 2 && i < kMaxPairs; ++i)
       c->omega[i] = (float)(params->phi_min / params->dt_max_s *
                             std::pow(params->rope_base, 2.0 * i / (double)params->head_dim));
+  c->grouped = shared;
   c->shared = shared && params->dtype == REC_ATTN_BF16;
   c->Th = Th;
-  if (c->shared) return create_shared(c, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist, v_hist, stream, cache_out);
+  if (c->shared) {
+    try {
+      return create_shared(c, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist, v_hist, stream, cache_out);
+    } catch (...) {  // (its tables are made before anything is allocated on the device)
+      delete c;
+      return REC_ATTN_ERR_OOM;
+    }
+  }
   const size_t elem = params->dtype == REC_ATTN_BF16 ? 2 : 4;
   const size_t rows_bytes = ws_up((size_t)Tc * params->num_heads * params->head_dim * elem);
   const size_t kvr_bytes = ws_up((size_t)Tc * kv_heads * params->head_dim * elem);
@@ -1657,8 +1703,14 @@ REC_ATTN_API rec_attn_status rec_attn_cache_create_grouped(const rec_attn_params
                                                            const void* k_hist, const void* v_hist,
                                                            int32_t max_cands, void* stream,
                                                            rec_attn_kv_cache_t** cache_out) {
-  return cache_create_impl(params, num_kv_heads, true, batch, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist,
-                           v_hist, max_cands, stream, cache_out);
+  if (cache_out) *cache_out = nullptr;
+  if (capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;  // its tables are staged from the call's own memory
+  try {
+    return cache_create_impl(params, num_kv_heads, true, batch, hist_offsets_host, hist_t_dev, hist_types_dev, k_hist,
+                             v_hist, max_cands, stream, cache_out);
+  } catch (...) {
+    return REC_ATTN_ERR_OOM;
+  }
 }
 
 REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const int64_t* cand_offsets_host,
@@ -1693,6 +1745,7 @@ REC_ATTN_API rec_attn_status rec_attn_cache_score(rec_attn_kv_cache_t* c, const 
     if (Nc >= (1LL << 31)) return REC_ATTN_ERR_UNSUPPORTED;
     return score_shared(c, cand_offsets_host, cand_t_dev, q_cand, k_cand, v_cand, out, lse, st);
   }
+  if (c->grouped && capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;
   // the candidate slots: rotated Q' and K' against the request's reference time (its
   // first history row, else its first candidate), V, time and type CAND; padding after
   std::vector<SlotReq> reqs((size_t)c->batch);

@@ -9,6 +9,17 @@
 
 namespace recattn {
 
+// While it lives, the thread may make calls that a stream capture forbids it otherwise: for what is
+// set up once and belongs to no stream (a memory pool, a kernel's attributes), should the first
+// call that needs it be captured.
+struct OutsideCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  OutsideCapture(const OutsideCapture&) = delete;
+  OutsideCapture& operator=(const OutsideCapture&) = delete;
+};
+
 // Raises a kernel's limit of dynamic shared memory, once per kernel and device (`done`: a static
 // of the caller, one bit per device): the call costs a launch's worth of host time.
 inline cudaError_t allow_smem(std::atomic<unsigned long long>& done, const void* fn, int bytes) {
@@ -17,6 +28,7 @@ inline cudaError_t allow_smem(std::atomic<unsigned long long>& done, const void*
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  const OutsideCapture now;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
@@ -66,7 +78,8 @@ constexpr int kNeedBlock = 64;     // keys per entry of block_need
 constexpr int kScoreMaxReq = 250;  // requests per launch (their tables are kernel parameters: 2 KB)
 struct ScoreArgs {
   // the cache
-  const long long* hist_off;    // [B + 1] rows of each request in K', V
+  const long long* hist_off;    // [B + 1] rows of each request in K', V (whole 128-row tiles)
+  const int* hist_len;          // [B] its keys; the rows behind them are zero
   const long long* need;        // [Th]: least time of a candidate that sees the key
   const long long* block_need;  // per 64-key block of a request: the largest of its keys' need
   const int* block_off;         // [B + 1] first block of each request
@@ -91,7 +104,7 @@ struct ScoreArgs {
 };
 struct NeedArgs {
   const long long* hist_off;
-  const int* block_off;
+  const int *hist_len, *block_off;
   const long long* t;
   const int8_t* ty;
   int batch, use_delay;

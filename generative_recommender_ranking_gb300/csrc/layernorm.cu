@@ -574,19 +574,25 @@ NormKernel norm_kernel(const NormShape& s, int dtype, bool bwd) {
   return dtype == REC_ATTN_BF16 ? norm_kernel<__nv_bfloat16>(s, bwd) : norm_kernel<float>(s, bwd);
 }
 
-// Blocks of a kernel that an SM holds (asked once per kernel and shape).
+// Blocks of a kernel that an SM of the current device holds (asked once per device, kernel and
+// shape; one that cannot be asked counts as 1, and its failure shows at the launch).
 int blocks_per_sm(NormKernel fn, int threads, int smem) {
   static std::mutex mu;
-  static std::map<std::tuple<NormKernel, int, int>, int> known;
+  static std::map<std::tuple<int, NormKernel, int, int>, int> known;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_tuple(fn, threads, smem);
+  const auto key = std::make_tuple(dev, fn, threads, smem);
   const auto at = known.find(key);
   if (at != known.end()) return at->second;
-  int n = 0;
-  // (one limit for every shape of a kernel; a failure shows at the launch)
-  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
+  const OutsideCapture now;
+  // one limit for every shape of a kernel
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem) != cudaSuccess) return 1;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess || n < 1) return 1;
-  known[key] = n;
+  try {
+    known[key] = n;
+  } catch (...) {  // asked again by the next call
+  }
   return n;
 }
 

@@ -101,7 +101,7 @@ __device__ __forceinline__ int n_splits(const ScoreArgs& a, int tiles) {
   return n > 0 ? n : 1;
 }
 __device__ __forceinline__ int request_tiles(const ScoreArgs& a, int b) {
-  return (int)((a.hist_off[b + 1] - a.hist_off[b] + a.tile_keys - 1) / a.tile_keys);
+  return (a.hist_len[b] + a.tile_keys - 1) / a.tile_keys;
 }
 
 // A row's parts (maximum, sum, this lane's DL output columns) joined with the candidate's own
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     it.rows = min(kRows, (a.cand_start[i + 1] - a.cand_start[i]) * G - it.rb * kRows);
   }
   const long long hist0 = a.hist_off[it.b];
-  const int hist_len = (int)(a.hist_off[it.b + 1] - hist0);
+  const int hist_len = a.hist_len[it.b];
   const int tiles = request_tiles(a, it.b);
   // the block's run of key tiles: an item of its own, or its share of the cluster's
   const int rank = a.cluster > 0 ? blockIdx.x % a.cluster : 0;
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(128) k_score_pack(const __grid_constant__ Scor
     it.hist0 = a.hist_off[b];
     it.cand0 = cand0;
     it.t_lo = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
-    it.len = (int)(a.hist_off[b + 1] - it.hist0);
+    it.len = a.hist_len[b];
     it.row0 = row0;
     it.rows = rows;
     it.hk = hk;
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(128) k_score_combine(const __grid_constant__ S
 __global__ void __launch_bounds__(kNeedBlock) k_score_need(NeedArgs a) {
   const int b = upper_index(a.block_off, a.batch, blockIdx.x);
   const long long h0 = a.hist_off[b];
-  const int len = (int)(a.hist_off[b + 1] - h0);
+  const int len = a.hist_len[b];
   const int p = ((int)blockIdx.x - a.block_off[b]) * kNeedBlock + threadIdx.x;
   long long need = LLONG_MIN;
   if (p < len) {

@@ -169,7 +169,10 @@ rec_attn_status rec_attn_plan_query_pruned(const rec_attn_params* params, int32_
  * and dk_norm_weight [Hk][d]; the query-side tensors and lse keep H heads.  dk and dv are
  * the sums over the query heads of the group, accumulated in fp32 and rounded once.
  * Masks, time-RoPE, types, errors and ownership as for rec_attn_plan; INVALID_ARG also
- * for num_kv_heads that does not divide num_heads.
+ * for num_kv_heads that does not divide num_heads.  The planning reads host memory of this
+ * call and the plan's calls wait for it, so neither may be captured into a CUDA graph:
+ * rec_attn_plan_grouped on a capturing stream, and the forward and backward calls on its
+ * plan there, return UNSUPPORTED and leave the capture valid.
  */
 rec_attn_status rec_attn_plan_grouped(const rec_attn_params* params, int32_t num_kv_heads,
                                       int32_t keep_user_queries, int32_t batch,
@@ -368,7 +371,7 @@ rec_attn_status rec_attn_compress(int32_t batch, const int64_t* offsets_host,
  * rounded once.  The sums have a fixed order: equal calls give equal bits.  The backward
  * recomputes the statistics and takes a workspace from the library pool on `stream`.
  * Asynchronous; both calls may be captured into a CUDA graph.
- * Errors: INVALID_ARG, UNSUPPORTED (width > 16384, rows >= 2^31), OOM, CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (width > 16384, rows > 2^31 - 65536), OOM, CUDA.
  */
 rec_attn_status rec_attn_layernorm_fwd(int32_t dtype, int64_t rows, int64_t width, int32_t num_groups,
                                        const void* x, const int8_t* types, const float* weight,
@@ -501,7 +504,13 @@ rec_attn_status rec_attn_visible_pairs(rec_attn_plan_t* plan, uint64_t* host_out
  * calls on one cache may overlap on any streams and may be captured into a CUDA graph (the
  * candidate counts are those of the capture).  Its workspace comes from the library pool on
  * `stream`.  A history key whose type is not GLOBAL, HIST or RT, or whose time is not
- * within +-2^62, is seen by no candidate.  (fp32: as rec_attn_cache_create, with slots.)
+ * within +-2^62, is seen by no candidate.  The cache rounds each request's rows up to a
+ * multiple of 128, with zeros: a value that is not finite reaches candidates of its own request
+ * alone (those that see its key and, since a masked key's weight 0 times NaN is NaN, others).
+ * UNSUPPORTED also for a scoring call of 2^31 or more rows (candidates times query heads) in
+ * 250 requests.  (fp32: as rec_attn_cache_create, with slots.)  The creation stages tables
+ * from host memory of the call: on a capturing stream it returns UNSUPPORTED, as scoring
+ * against such a cache in fp32 does, and leaves the capture valid.
  *
  * rec_attn_cache_device_status -- the status word of a bf16 cache with shared heads
  * (REC_ATTN_OK, REC_ATTN_ERR_DEVICE_INPUT for a history type outside 0..3 or a time out of

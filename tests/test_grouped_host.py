@@ -121,3 +121,8 @@ def test_layernorm_binding_checks_the_tensors():
         with pytest.raises(bd.RecAttnError) as e:
             call()
         assert e.value.code == INVALID
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_layernorm_rows_are_counted_in_32_bits(L, call):
+    assert call(L, rows=(1 << 31) - 65535) == UNSUPPORTED
