@@ -329,7 +329,7 @@ rec_attn_status plan_impl(const rec_attn_params* params, int32_t kv_heads, int32
   }
   if (e == cudaSuccess)
     e = launch_plan(plan->mask, params->num_heads, pd, reinterpret_cast<const long long*>(offsets_dev), plan->t,
-                    plan->ty, batch, NT, plan->ev_meta, plan->side);
+                    plan->ty, batch, NT, 2 * row_bytes * kv_heads, plan->ev_meta, plan->side);
   if (e == cudaSuccess) e = launch_build_masks(plan->mask, pd, plan->num_sms, plan->side);
   if (e == cudaSuccess) e = cudaEventRecord(plan->ev_plan, plan->side);
   if (e != cudaSuccess) {

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) k_plan_tiles(PlanDev pd, cons
 __global__ void __launch_bounds__(kPlanThreads) k_plan(MaskP mp, int heads, PlanDev pd,
                                                        const long long* offsets, const long long* t,
                                                        const int8_t* ty, int batch, int slices,
-                                                       long long n_tiles) {
+                                                       long long n_tiles, long long heavy_den) {
   __shared__ __align__(16) unsigned char s_scratch[kScratchBytes];
   const int b = (int)(blockIdx.x / slices), sl = (int)(blockIdx.x % slices);
   const ReqMeta m = pd.meta[b];
@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(MaskP mp, int heads, Plan
   // Phase 4: the last block to finish writes the work-item order.  The order only
   // affects load balance and cache reuse, never results.
   //  - heavy query tiles (cost above 16x the mean, e.g. a candidate tile that reads a
-  //    whole 20K history next to window-only tiles) go first, most expensive first;
+  //    whole 20K history next to window-only tiles, or above 1 / heavy_den of all items'
+  //    cost: started last, such an item would run on alone) go first, most expensive first;
   //  - then the rest, request by request (most expensive first), inside a request
   //    head by head, inside a head from the last query tile to the first, so the
   //    items running at the same time share K'/V tiles in L2.
@@ -425,23 +426,28 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(MaskP mp, int heads, Plan
   __syncthreads();
   const long long total = (long long)s_sum;
   auto qc = [&](long long q) { return staged ? s_qc[q] : __ldcg(pd.qcost + q); };
-  // heavy: qcost * n_tiles > 16 * total
-  auto heavy = [&](long long q) { return (long long)qc(q) * n_tiles > 16 * total; };
+  const long long heavy_above = min(16 * total / max(n_tiles, 1LL), total * heads / heavy_den);
+  auto heavy = [&](long long q) { return qc(q) > heavy_above; };
   // heavy query tiles, counting-sorted by cost (descending) into the front of `items`
-  for (long long q = threadIdx.x; q < n_tiles; q += blockDim.x)
-    if (heavy(q)) {
-      atomicAdd(&s_hist[kCostBins - 1 - min(qc(q), kCostBins - 1)], 1);
-      atomicAdd(&s_nheavy, 1);
-    }
+  // (whole warps in both loops: tiles of equal cost share a bin)
+  for (long long q0 = threadIdx.x & ~31; q0 < n_tiles; q0 += blockDim.x) {
+    const long long q = q0 + (threadIdx.x & 31);
+    const bool in = q < n_tiles && heavy(q);
+    agg_inc(s_hist, kCostBins - 1 - (in ? min(qc(q), kCostBins - 1) : 0), in);
+    const unsigned n = __ballot_sync(0xffffffffu, in);
+    if ((threadIdx.x & 31) == 0 && n) atomicAdd(&s_nheavy, __popc(n));
+  }
   __syncthreads();
   const long long heavy_items = (long long)s_nheavy * heads;
   if (heavy_items > 0) {
     block_exclusive_scan_bins(s_hist, s_part);
-    for (long long q = threadIdx.x; q < n_tiles; q += blockDim.x)
-      if (heavy(q)) {
-        const int pos = atomicAdd(&s_hist[kCostBins - 1 - min(qc(q), kCostBins - 1)], 1);
+    for (long long q0 = threadIdx.x & ~31; q0 < n_tiles; q0 += blockDim.x) {
+      const long long q = q0 + (threadIdx.x & 31);
+      const bool in = q < n_tiles && heavy(q);
+      const int pos = agg_inc(s_hist, kCostBins - 1 - (in ? min(qc(q), kCostBins - 1) : 0), in);
+      if (in)
         for (int h = 0; h < heads; ++h) pd.items[(long long)pos * heads + h] = (int)(q * heads + h);
-      }
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < kCostBins; i += blockDim.x) s_hist[i] = 0;
     __syncthreads();
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kTile) k_count_pairs(MaskP mp, PlanDev pd, con
 }  // namespace
 
 cudaError_t launch_plan(const MaskP& mp, int heads, const PlanDev& pd, const long long* offsets_dev,
-                        const long long* t, const int8_t* ty, int batch, long long n_tiles,
+                        const long long* t, const int8_t* ty, int batch, long long n_tiles, size_t kv_bytes,
                         cudaEvent_t prologue_ok, cudaStream_t st) {
   if (batch <= 0) return prologue_ok ? cudaEventRecord(prologue_ok, st) : cudaSuccess;
   // One block per request while requests are short: the planner then runs beside the
@@ -619,11 +625,18 @@ cudaError_t launch_plan(const MaskP& mp, int heads, const PlanDev& pd, const lon
   // phase 1 in a kernel of its own before them.
   long long slices = 1;
   const long long mean_tiles = (n_tiles + batch - 1) / batch;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // Items run in two streams (or blocks) per SM.  An item of 1/32 of a stream's share of the work
+  // counts as heavy while K' and V stay in half of the L2, whatever order reads them; else one of
+  // 1/8: request by request, each request's keys are read from memory about once, which sorting all
+  // tiles by cost would give up.  (One causal request of 20001 tokens, 8 heads, forward:
+  // 529 us in the requests' order, 459 sorted; two of 8192 and 7000 tokens, forward and backward 763
+  // and 643; sixteen of 20001: no item is that large, the order stays.)
+  const long long heavy_den = 2LL * sms * (kv_bytes <= (64ull << 20) ? 32 : 8);
   if (mean_tiles >= kSplitTiles) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
     slices = (2LL * sms + batch - 1) / batch;
     if (slices > mean_tiles) slices = mean_tiles;
   }
@@ -633,11 +646,11 @@ cudaError_t launch_plan(const MaskP& mp, int heads, const PlanDev& pd, const lon
   } else {
     slices = 1;
   }
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e == cudaSuccess && prologue_ok) e = cudaEventRecord(prologue_ok, st);
   if (e != cudaSuccess) return e;
   k_plan<<<(unsigned)(batch * slices), kPlanThreads, 0, st>>>(mp, heads, pd, offsets_dev, t, ty, batch,
-                                                              (int)slices, n_tiles);
+                                                              (int)slices, n_tiles, heavy_den);
   return cudaGetLastError();
 }
 
