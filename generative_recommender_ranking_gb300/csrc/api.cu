@@ -611,8 +611,8 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   // bf16 workspace: descriptors [n_items], [n_kv_items] | row constants [H][NT][128] | lists [NC] |
   // their mask-table slots [NC] | the mask table's columns [mcap][128][4] | with items of
   // several heads the dK/dV items' order [n_kv_items]
-  const size_t off_rowc = (size_t)(n_items + n_kv_items) * sizeof(BwdItemDesc);
-  const size_t off_ql = off_rowc + (size_t)plan->NT * p.num_heads * kTile * sizeof(float2);
+  const size_t off_rowx = (size_t)(n_items + n_kv_items) * sizeof(BwdItemDesc);
+  const size_t off_ql = off_rowx + (size_t)plan->NT * p.num_heads * kTile * sizeof(uint4);
   const size_t off_qs = off_ql + (((size_t)plan->NC * sizeof(uint32_t) + 15) & ~(size_t)15);
   const size_t off_ct = off_qs + (((size_t)plan->NC * sizeof(int) + 15) & ~(size_t)15);
   const size_t off_ki = off_ct + (size_t)plan->pd.mcap * kTile * 16;
@@ -660,7 +660,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   a.delta = tc ? nullptr : reinterpret_cast<float*>(bws);
   a.n_tiles = plan->NT;
   a.desc = tc ? reinterpret_cast<const BwdItemDesc*>(bws) : nullptr;
-  a.rowc = tc ? reinterpret_cast<float2*>(bws + off_rowc) : nullptr;
+  a.rowx = tc ? reinterpret_cast<uint4*>(bws + off_rowx) : nullptr;
   a.qlist = tc ? reinterpret_cast<const uint32_t*>(bws + off_ql) : nullptr;
   a.kslot = plan->pd.kslot; a.mtab = plan->pd.mtab;
   a.qslot = tc ? reinterpret_cast<const int*>(bws + off_qs) : nullptr;

@@ -62,94 +62,97 @@ namespace recattn {
 
 namespace {
 
-constexpr int kStep = 64;                   // keys (DQ) or queries (DKV) per MMA step
 constexpr int kSlab = kTile * 128;          // 128 rows x 64 bf16 columns, 128-byte swizzled
-constexpr int kNS = 2;                      // stages of the streamed ring
-// Per head dimension: a [128][D] bf16 tile is D / 64 slabs; TMEM columns of the
-// accumulators (DQ: S[0] 0..63 | S[1] 64..127 | dP 128..191 | dQ 192..; DKV: S^T 0..63 |
-// dP^T 64..127 | dV 128.. | dK 128 + D..); d = 64 runs two CTAs per SM, d = 128 one.
+// Per head dimension: a [128][D] bf16 tile is D / 64 slabs.
 template <int D>
 struct BCfg {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr uint32_t kCols = D == 64 ? 256 : 512;
-  static constexpr int kBlocksPerSM = D == 64 ? 2 : 1;
-  static constexpr uint32_t kDQ = 192, kDV = 128, kDK = 128 + D;
-  static constexpr int kWG = 2;                   // compute warpgroups, 32 of a step's 64 columns each
-  static constexpr int kSub = D == 64 ? 16 : 32;  // columns a thread holds at a time
-  static constexpr bool kDB = D == 128;           // every score buffer twice
-  static constexpr int kThreads = 64 + 128 * kWG;
-  // the bf16 operand of a step: each warpgroup's 16 columns of packed pairs (two K steps) over the
-  // first half of the 32 score columns that it has read
-  static constexpr uint32_t kChunkCols = 32;
-  // score buffers of step parity b
-  __host__ __device__ static constexpr uint32_t dq_s(uint32_t b) { return b * 64; }
-  __host__ __device__ static constexpr uint32_t dq_dp(uint32_t b) { return kDB && b ? 320u : 128u; }
-  __host__ __device__ static constexpr uint32_t dkv_s(uint32_t b) { return kDB && b ? 384u : 0u; }
+  // stages of the streamed rings (first and second operand)
+  template <bool DKV>
+  static constexpr int kNS0 = D == 64 ? 4 : DKV ? 2 : 3;
+  template <bool DKV>
+  static constexpr int kNS1 = D == 64 ? 4 : DKV ? 2 : 1;
+  static constexpr int kWG = 4;                   // compute warpgroups, 32 of a step's 128 columns each
+  static constexpr int kRoles = 3;                // producer, one or two issuers
+  static constexpr int kThreads = 32 * kRoles + 128 * kWG;
+  // TMEM columns of S (step parity b), dP and the accumulators
+  template <bool DKV>
+  __host__ __device__ static constexpr uint32_t s_col(uint32_t b) {
+    return D == 64 ? b * 128 : (DKV ? 0u : b * 384);
+  }
+  static constexpr uint32_t kDP = D == 64 ? 256 : 128;
+  static constexpr uint32_t kDQ = D == 64 ? 384 : 256, kDV = kDQ, kDK = kDV + D;
+  // whether S has two buffers (head_dim 128 leaves DKV none)
+  template <bool DKV>
+  static constexpr bool kTwoS = D == 64 || !DKV;
 };
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kChunkCols = 32;         // a step's bf16 operand: each warpgroup's 16 columns of packed pairs
+                                            // (two K steps) over the first half of the 32 columns it has read
+constexpr uint32_t kDsCols = 16;            // DKV with two S: dS^T stands over the second half, beside P^T
 constexpr int kRecB = (int)sizeof(KeyTileRec);
 constexpr int kMaskB = kTile * 16;  // a PARTIAL pair's 128 rows (or columns) of the mask table
 constexpr int kStageRecB = kMaskB > kRecB ? kMaskB : kRecB;  // per streamed stage: one or the other
 constexpr uint64_t kWaitNsB = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 
-// mbarriers
+// mbarriers (steps are counted over the CTA's life; [2]: by step parity)
 enum : int {
   kResFull = 0,
   kResEmpty,
-  kStrFull,
-  kStrEmpty = kStrFull + kNS,
-  kSyFull = kStrEmpty + kNS,  // [2] the step's two score MMAs completed (by step parity where the
-                              // scores have two buffers, else the first only)
-  kXReady = kSyFull + 2,      // [2, by step parity] the compute warps wrote the step's bf16 operands
-                              // (in mode DQ the next step's scores go out before this step's
-                              // operands are consumed, so the compute warps may finish a whole step
-                              // ahead of the issuer's wait; with one barrier per parity a barrier
-                              // cannot complete twice before its wait)
-  kDpFree = kXReady + 2,      // DQ: the compute warps loaded the step's dP
-  kAccFull,                   // the item's last accumulating MMA completed
-  kAccEmpty,                  // the compute warps read the accumulators
-  kGroup,                     // DKV: barrier of the compute threads
-  kItemFull,                  // [2] the producer published an item descriptor
-  kItemEmpty = kItemFull + 2, // [2] the MMA issuer and the compute warps copied it
-  kMmaDone = kItemEmpty + 2,
-  kNumBars
+  kStr0Full,                    // [4] the streamed tile of the scores S (DQ: K', DKV: Q'), with the record
+  kStr0Empty = kStr0Full + 4,   // [4] and the row constants
+  kStr1Full = kStr0Empty + 4,   // [4] the streamed tile of dP (DQ: V, DKV: dO)
+  kStr1Empty = kStr1Full + 4,   // [4]
+  kSFull = kStr1Empty + 4,      // [2] S completed
+  kDpFull = kSFull + 2,         // dP completed
+  kDpFree,                      // DQ: the compute warps loaded dP
+  kPReady,                      // [2] DQ: the compute warps wrote dS; DKV: P^T (the next step's may be
+                                // written before the issuer looks for this one's)
+  kDsReady = kPReady + 2,       // DKV, one S: the compute warps wrote dS^T
+  kSFree,                       // [2] two S: the accumulation read the step's operand in S's columns
+  kAccFull = kSFree + 2,        // the item's last accumulating MMA completed
+  kAccEmpty,                    // the compute warps read the accumulators
+  kGroup,                       // DKV: barrier of the compute threads
+  kItemFull,                    // [2] the producer published an item descriptor
+  kItemEmpty = kItemFull + 2,   // [2] the MMA issuer and the compute warps copied it
+  kMmaDone = kItemEmpty + 2,    // [2] an issuing warp's MMAs are done, at the end
+  kNumBars = kMmaDone + 2
 };
-
-// The ready barrier of step `step` (a stream-wide step count) and its wait parity.
-__host__ __device__ constexpr int xready(uint32_t step) { return kXReady + (int)(step & 1u); }
-__host__ __device__ constexpr uint32_t xready_parity(uint32_t step) { return (step >> 1) & 1u; }
-
-// The scores' barrier of a step and its wait parity.
-template <int D>
-__host__ __device__ constexpr int syfull(uint32_t step) { return kSyFull + (BCfg<D>::kDB ? (int)(step & 1u) : 0); }
-template <int D>
-__host__ __device__ constexpr uint32_t syfull_parity(uint32_t step) { return BCfg<D>::kDB ? (step >> 1) & 1u : step & 1u; }
+// wait parity of step `step` on a barrier of its own and on one of two
+__host__ __device__ constexpr uint32_t par1(uint32_t step) { return step & 1u; }
+__host__ __device__ constexpr uint32_t par2(uint32_t step) { return (step >> 1) & 1u; }
 
 // Byte offsets from the 1024-aligned base of dynamic shared memory.
-constexpr int kRowB = kTile * 8;  // {-lse2, -D} of a tile's rows, paired (row_neg_lse2 / row_neg_d)
+constexpr int kRowX = kTile * 16;    // a tile's rows of the constants' operand, 8 bf16 each
+constexpr int kAugB = 2 * kRowX;     // an operand of 16 columns: two 8-column halves, the second zero
 template <int D>
 struct BL {
+  static constexpr int kTiles = D == 64 ? 8 : 4;             // streamed tiles: kNS0 + kNS1 of both modes
+  static constexpr int kRecs = D == 64 ? 4 : 3;              // at least kNS0 of both modes,
+  static constexpr int kAugs = BCfg<D>::template kNS0<true>; // of DKV
   static constexpr int kTileBytes = BCfg<D>::kTileBytes;
-  static constexpr int kRes = 0;                             // [2] resident tiles
-  static constexpr int kStr = kRes + 2 * kTileBytes;         // [kNS][2] streamed tiles
-  static constexpr int kSRec = kStr + 2 * kNS * kTileBytes;  // [kNS] records of the streamed tiles
-  static constexpr int kSRow = kSRec + kNS * kStageRecB;     // DKV: [kNS] row constants of the query tiles
-  static constexpr int kRRec = kSRow + kNS * kRowB;          // record of the item's tile
-  static constexpr int kRRow = kRRec + kRecB;                // DQ: row constants of the query tile
-  static constexpr int kCol = kRRow + kRowB;                 // DKV: [2][128 keys] 128 query bits
+  static constexpr int kOnes = 0;                            // [2 (S, dP)] ones that pick the constants
+  static constexpr int kAug = kOnes + 2 * kAugB;              // constants of the query tiles (DKV: [kNS0]; DQ: one)
+  static constexpr int kRes = kAug + kAugs * kAugB;           // [2] resident tiles
+  static constexpr int kStr = kRes + 2 * kTileBytes;         // the streamed tiles, [kNS0] first operands, then [kNS1]
+  static constexpr int kSRec = kStr + kTiles * kTileBytes;  // [kNS0] records of the streamed tiles
+  static constexpr int kRRec = kSRec + kRecs * kStageRecB;   // record of the item's tile
+  static constexpr int kCol = kRRec + kRecB;                 // DKV: [2][128 keys] 128 query bits
   static constexpr int kItems = kCol + 2 * kTile * 16;       // [2] published item descriptors
   static constexpr int kBarsOff = kItems + 2 * 64;
   static constexpr int kTotal = kBarsOff + kNumBars * 8 + 16;  // + abort flag and TMEM slot
   static constexpr int kDynamic = kTotal + 1024;               // slack to align the base
 };
-static_assert(BL<64>::kSRec % 16 == 0 && BL<64>::kSRow % 16 == 0 && BL<64>::kRRec % 16 == 0 &&
-                  BL<64>::kRRow % 16 == 0 && BL<64>::kCol % 16 == 0 && BL<128>::kSRec % 16 == 0 &&
-                  BL<128>::kSRow % 16 == 0 && BL<128>::kRRec % 16 == 0 && BL<128>::kRRow % 16 == 0 &&
-                  BL<128>::kCol % 16 == 0,
-              "bulk-copy alignment");
-static_assert(BL<64>::kBarsOff % 8 == 0 && BL<128>::kBarsOff % 8 == 0, "mbarrier alignment");
-static_assert(2 * (BL<64>::kDynamic + 1024) <= 228 * 1024, "two CTAs per SM at d = 64");
-static_assert(BL<128>::kDynamic <= 227 * 1024, "one CTA per SM at d = 128");
+template <int D>
+constexpr bool layout_ok() {
+  using L = BL<D>;
+  return L::kRes % 1024 == 0 && L::kStr % 1024 == 0 && L::kSRec % 16 == 0 && L::kRRec % 16 == 0 &&
+         L::kCol % 16 == 0 && L::kBarsOff % 8 == 0 && L::kDynamic <= 227 * 1024 &&
+         BCfg<D>::template kNS0<true> + BCfg<D>::template kNS1<true> <= L::kTiles && BCfg<D>::template kNS0<true> <= L::kRecs &&
+         BCfg<D>::template kNS0<false> + BCfg<D>::template kNS1<false> <= L::kTiles && BCfg<D>::template kNS0<false> <= L::kRecs;
+}
+static_assert(layout_ok<64>() && layout_ok<128>(), "shared memory layout");
 
 __device__ __forceinline__ bool bw_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   return bounded_wait(bar, parity, abort_flag, status, kWaitNsB);
@@ -159,6 +162,22 @@ __device__ __forceinline__ bool bw_wait_warp(uint64_t* bar, uint32_t parity, vol
   const bool ok = bw_wait(bar, parity, abort_flag, status);
   return __all_sync(0xffffffffu, ok);
 }
+// The compute warps' barriers by their shared-memory address (32 bits: a step has few instructions).
+struct WarpBars {
+  uint32_t base;
+  uint64_t* bars;
+  volatile int* abort_flag;
+  int* status;
+  __device__ __forceinline__ bool wait(int bar, uint32_t parity) const {
+    const bool ok = ptx::mbar_try_wait_at(base + 8 * bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return bw_wait_warp(bars + bar, parity, abort_flag, status);
+  }
+  __device__ __forceinline__ void arrive(int bar) const {  // one arrival for the warp
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive_at(base + 8 * bar);
+  }
+};
 __device__ __forceinline__ void bw_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer();
   while (!ptx::mbar_try_wait(bar, parity))
@@ -210,46 +229,85 @@ __device__ __forceinline__ bool next_item(uint8_t* sm, uint64_t* bars, uint32_t&
 // mask-table slot (-1: none).  DKV visits each listed query tile once for every query
 // head of the item's part of the group (`reps` times in a row), so dK and dV sum over those
 // heads in TMEM.
+template <bool DKV>
 struct Cursor {
-  const uint32_t* list;
-  const int* slots;
-  int r, rep, reps;
-  __device__ __forceinline__ void init(const uint32_t* base, const int* slot_base, const BwdItemDesc& d, int n_rep) {
-    list = base + d.list;
-    slots = slot_base + d.list;
-    r = 0;
+  long long at;
+  int rep, reps;
+  __device__ __forceinline__ void init(const BwdItemDesc& d, int n_rep) {
+    at = d.list;
     rep = 0;
     reps = n_rep;
   }
-  __device__ __forceinline__ void next(int& tile, int& cls, int& slot) {
-    const uint32_t e = list[r];
-    slot = slots[r];
-    if (++rep == reps) {
+  // The entry as loaded, so that a caller may fetch it ahead without waiting for it.
+  struct Entry {
+    uint32_t e;
+    int slot;
+    __device__ __forceinline__ int tile() const { return (int)(e & 0xffffffu); }
+    __device__ __forceinline__ int cls() const { return (int)(e >> 24); }
+  };
+  __device__ __forceinline__ Entry next(const BwdArgs& a) {
+    Entry x;
+    x.e = (DKV ? a.qlist : a.klist)[at];
+    x.slot = (DKV ? a.qslot : a.kslot)[at];
+    if (!DKV || ++rep == reps) {
       rep = 0;
-      ++r;
+      ++at;
     }
-    tile = (int)(e & 0xffffffu);
-    cls = (int)(e >> 24);
+    return x;
+  }
+};
+
+// The same for the compute warps, which need to know little of most tiles: lane i holds the i-th of 32
+// entries, and one bit of each says whether the tile is FULL.  (One entry loaded ahead for every
+// step cost 185 cycles of a step of 2100: address arithmetic and a queue for the load.)
+template <bool DKV>
+struct WarpCursor {
+  long long at;
+  uint32_t e, full;
+  int slot, r, rep, left;
+  __device__ __forceinline__ void window(const BwdArgs& a) {
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < left;
+    e = in ? (DKV ? a.qlist : a.klist)[at + lane] : 0u;
+    slot = in ? (DKV ? a.qslot : a.kslot)[at + lane] : -1;
+    full = __ballot_sync(0xffffffffu, in && (e >> 24) == (uint32_t)REC_ATTN_TILE_FULL);
+    at += 32;
+    left -= 32;
+    r = 0;
+  }
+  __device__ __forceinline__ void init(const BwdArgs& a, const BwdItemDesc& d, int entries) {
+    at = d.list;
+    left = entries;
+    rep = 0;
+    window(a);
+  }
+  __device__ __forceinline__ bool is_full() const { return (full >> r) & 1u; }
+  __device__ __forceinline__ int tile() const { return (int)(__shfl_sync(0xffffffffu, e, r) & 0xffffffu); }
+  __device__ __forceinline__ int table_slot() const { return __shfl_sync(0xffffffffu, slot, r); }
+  __device__ __forceinline__ void next(const BwdArgs& a, int reps) {
+    if (DKV && ++rep < reps) return;
+    rep = 0;
+    if (++r == 32 && left > 0) window(a);
   }
 };
 
 // ------------------------------------------------------------------ producer
 // maps: resident pair res[0], res[1]; streamed pair str[0], str[1].
-//   DQ:  resident Q', dO + the query tile's record and row constants; streamed K', V
-//        (+ the key tile's record when the tile is PARTIAL).
-//   DKV: resident K', V + the key tile's record; streamed Q', dO + the query tile's
-//        record and row constants.
+//   DQ:  resident Q', dO + the query tile's record and row constants; streamed K' (+ the key
+//        tile's record or mask rows when the tile is PARTIAL) and V.
+//   DKV: resident K', V + the key tile's record; streamed Q' + the query tile's record and its
+//        constants' operand, and dO.
+// The two streamed tiles have rings of their own: the second is free again as soon as dP (DQ) or
+// dV (DKV) has read it, the first after dQ or dK, the step's last MMA.
 template <int D, bool DKV>
 __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], const void* const (&str)[2],
                              uint8_t* sm, uint64_t* bars, volatile int* abort_flag) {
-  const uint32_t* lists = DKV ? a.qlist : a.klist;
-  uint32_t it_n = 0, s_it = 0, it_cnt = 0;
-  bool res_used = false, str_used[kNS];
-  uint32_t res_ph = 0, str_ph[kNS];
-  for (int i = 0; i < kNS; ++i) { str_used[i] = false; str_ph[i] = 0; }
-  const uint4* descs = reinterpret_cast<const uint4*>(a.desc + (DKV ? a.n_items : 0));
   using L = BL<D>;
-  constexpr int kTileBytes = L::kTileBytes;
+  constexpr int kTileBytes = L::kTileBytes, kNS0 = BCfg<D>::template kNS0<DKV>, kNS1 = BCfg<D>::template kNS1<DKV>;
+  uint32_t it_n = 0, s_it = 0, it_cnt = 0;
+  bool res_used = false;
+  uint32_t res_ph = 0, n0 = 0, n1 = 0;  // steps whose first, second operand was loaded
+  const uint4* descs = reinterpret_cast<const uint4*>(a.desc + (DKV ? a.n_items : 0));
   ItemSlot* slots = reinterpret_cast<ItemSlot*>(sm + L::kItems);
   int* counter = a.counters + (DKV ? 5 : 3);
   const long long n_items = DKV ? a.n_kv_items : a.n_items;
@@ -277,8 +335,7 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
     {
       const int x = (DKV ? d.h / a.parts : d.h) * D;
       const long long g = (long long)d.tile_start + d.tile;
-      const float2* rows_h = a.rowc + (long long)d.h * a.n_tiles * kTile;  // DQ: head h's row constants
-      ptx::mbar_arrive_expect_tx(bars + kResFull, 2 * kTileBytes + kRecB + (DKV ? 0 : kRowB));
+      ptx::mbar_arrive_expect_tx(bars + kResFull, 2 * kTileBytes + kRecB + (DKV ? 0 : kRowX));
       const int y = (int)(d.tok_start + (long long)d.tile * kTile);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -286,57 +343,65 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
         ptx::tma_load_2d(sm + L::kRes + kTileBytes + c * kSlab, res[1], x + 64 * c, y, bars + kResFull);
       }
       ptx::bulk_load(sm + L::kRRec, a.krec + g, kRecB, bars + kResFull);
-      if (!DKV) ptx::bulk_load(sm + L::kRRow, rows_h + g * kTile, kRowB, bars + kResFull);
+      if (!DKV)
+        ptx::bulk_load(sm + L::kAug, a.rowx + ((long long)d.h * a.n_tiles + g) * kTile, kRowX, bars + kResFull);
       res_used = true;
       res_ph = it_n & 1;
       ++it_n;
-      Cursor cur;
+      Cursor<DKV> cur;
       const int reps = DKV ? a.group / a.parts : 1;
-      cur.init(lists, DKV ? a.qslot : a.kslot, d, reps);
+      cur.init(d, reps);
       const int kvx = (d.h / a.group) * D;  // DQ: the columns of the head's key/value head
-      for (int j = 0; j < d.n; ++j) {
-        int tile, cls, tslot;
+      for (int j = 0; j < d.n; ++j, ++s_it) {
         // DKV: the query head of this visit, its columns and its row constants
         const int hq = d.h * reps + cur.rep;
         const int xs = DKV ? hq * D : kvx;
-        cur.next(tile, cls, tslot);
-        const int st = (int)(s_it % kNS);
-        const uint32_t ph = (s_it / kNS) & 1;
-        if (!bw_wait(bars + kStrEmpty + st, ph ^ 1, abort_flag, a.status)) goto drain;
+        const auto x_at = cur.next(a);
+        const int tile = x_at.tile(), cls = x_at.cls(), tslot = x_at.slot;
+        const int st = (int)(s_it % kNS0), st1 = (int)(s_it % kNS1);
         const long long gs = (long long)d.tile_start + tile;
-        // PARTIAL tiles with a mask-table slot: the tile's rows (DQ) or columns (DKV) of the
-        // table; otherwise DQ reads the key record on PARTIAL tiles, DKV the query record
-        const bool tab = cls != REC_ATTN_TILE_FULL && tslot >= 0;
-        const bool rec = !tab && (DKV || cls != REC_ATTN_TILE_FULL);
         const int ys = (int)(d.tok_start + (long long)tile * kTile);
-        ptx::mbar_arrive_expect_tx(bars + kStrFull + st,
-                                   2 * kTileBytes + (tab ? kMaskB : rec ? kRecB : 0) + (DKV ? kRowB : 0));
+        auto load1 = [&]() -> bool {
+          if (!bw_wait(bars + kStr1Empty + st1, ((s_it / kNS1) & 1) ^ 1, abort_flag, a.status)) return false;
+          ptx::mbar_arrive_expect_tx(bars + kStr1Full + st1, kTileBytes);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          ptx::tma_load_2d(sm + L::kStr + (2 * st) * kTileBytes + c * kSlab, str[0], xs + 64 * c, ys,
-                           bars + kStrFull + st);
-          ptx::tma_load_2d(sm + L::kStr + (2 * st + 1) * kTileBytes + c * kSlab, str[1], xs + 64 * c, ys,
-                           bars + kStrFull + st);
-        }
+          for (int c = 0; c < D / 64; ++c)
+            ptx::tma_load_2d(sm + L::kStr + (kNS0 + st1) * kTileBytes + c * kSlab, str[1], xs + 64 * c, ys,
+                             bars + kStr1Full + st1);
+          ++n1;
+          return true;
+        };
+        // the operand whose place is free earlier goes first
+        constexpr bool kSecondFirst = kNS1 >= kNS0;
+        if (kSecondFirst && !load1()) goto drain;
+        if (!bw_wait(bars + kStr0Empty + st, ((s_it / kNS0) & 1) ^ 1, abort_flag, a.status)) goto drain;
+        // PARTIAL tiles with a mask-table slot: the tile's rows (DQ) or columns (DKV) of the
+        // table; otherwise the key (DQ) or query (DKV) tile's record
+        const bool part = cls != REC_ATTN_TILE_FULL, tab = part && tslot >= 0, rec = part && !tab;
+        ptx::mbar_arrive_expect_tx(bars + kStr0Full + st,
+                                   kTileBytes + (tab ? kMaskB : rec ? kRecB : 0) + (DKV ? kRowX : 0));
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          ptx::tma_load_2d(sm + L::kStr + st * kTileBytes + c * kSlab, str[0], xs + 64 * c, ys,
+                           bars + kStr0Full + st);
         if (tab)
           ptx::bulk_load(sm + L::kSRec + st * kStageRecB, (DKV ? a.ctab : a.mtab) + (long long)tslot * (kMaskB / 4),
-                         kMaskB, bars + kStrFull + st);
+                         kMaskB, bars + kStr0Full + st);
         else if (rec)
-          ptx::bulk_load(sm + L::kSRec + st * kStageRecB, a.krec + gs, kRecB, bars + kStrFull + st);
+          ptx::bulk_load(sm + L::kSRec + st * kStageRecB, a.krec + gs, kRecB, bars + kStr0Full + st);
         if (DKV)
-          ptx::bulk_load(sm + L::kSRow + st * kRowB, a.rowc + ((long long)hq * a.n_tiles + gs) * kTile, kRowB,
-                         bars + kStrFull + st);
-        str_used[st] = true;
-        str_ph[st] = ph;
-        ++s_it;
+          ptx::bulk_load(sm + L::kAug + st * kAugB, a.rowx + ((long long)hq * a.n_tiles + gs) * kTile, kRowX,
+                         bars + kStr0Full + st);
+        ++n0;
+        if (!kSecondFirst && !load1()) goto drain;
       }
     }
   }
 drain:
-  // every copy issued must land before the CTA exits (only waits after an abort)
+  // every copy issued must land before the CTA exits (only waits after an abort): the rings' last ones
   if (res_used) bw_drain(bars + kResFull, res_ph);
-  for (int i = 0; i < kNS; ++i)
-    if (str_used[i]) bw_drain(bars + kStrFull + i, str_ph[i]);
+  for (uint32_t u = n0 > kNS0 ? n0 - kNS0 : 0; u < n0; ++u) bw_drain(bars + kStr0Full + u % kNS0, (u / kNS0) & 1);
+  for (uint32_t u = n1 > kNS1 ? n1 - kNS1 : 0; u < n1; ++u) bw_drain(bars + kStr1Full + u % kNS1, (u / kNS1) & 1);
 }
 
 // ------------------------------------------------------------------ MMA issuer
@@ -344,11 +409,10 @@ __device__ __forceinline__ uint64_t kdesc(uint32_t addr) { return ptx::smem_desc
 // MN-major operand: 64-column blocks of N one slab apart
 __device__ __forceinline__ uint64_t mndesc(uint32_t addr) { return ptx::smem_desc_sw128(addr, kSlab, 1024); }
 
-// Scores over K = D (both operands K-major, the K steps of 16 columns four per slab;
-// B = 64 rows of a tile): N = 64.
+// Scores of a whole tile over K = D (both operands K-major, the K steps of 16 columns four per slab).
 template <int D>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
-  constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, kStep, false, false);
+  constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, kTile, false, false);
   const uint64_t da = kdesc(a_addr), db = kdesc(b_addr);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
@@ -356,175 +420,192 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a_addr, uint32_t
     ptx::umma_f16(d, ptx::smem_desc_at(da, off), ptx::smem_desc_at(db, off), id, kk > 0);
   }
 }
-// D (+)= A B with A (128 x 64, bf16) in TMEM and B = 64 rows of a tile as the K
-// dimension (MN-major: the tile's D columns are N).
+// The constants of the queries added to scores, one more K step: ones x constants (DKV: the queries are
+// the columns) or constants x ones (DQ: the rows).
+__device__ __forceinline__ void mma_consts(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
+  constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, kTile, false, false);
+  ptx::umma_f16(d, ptx::smem_desc_plain(a_addr, kRowX, 128), ptx::smem_desc_plain(b_addr, kRowX, 128), id, 1u);
+}
+// D (+)= A B with A (128 x 128, bf16) in TMEM and the tile's 128 rows as the K dimension
+// (MN-major: the tile's D columns are N).
 template <int D>
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a_tmem, uint32_t b_rows, bool accumulate) {
   constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, D, false, true);
   const uint64_t db = mndesc(b_rows);
 #pragma unroll
-  for (int kk = 0; kk < kStep / 16; ++kk)
-    ptx::umma_f16_ts(d, a_tmem + (kk >> 1) * BCfg<D>::kChunkCols + (kk & 1) * 8, ptx::smem_desc_at(db, kk * 16 * 128), id,
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    ptx::umma_f16_ts(d, a_tmem + (kk >> 1) * kChunkCols + (kk & 1) * 8, ptx::smem_desc_at(db, kk * 16 * 128), id,
                      (accumulate || kk > 0) ? 1u : 0u);
 }
 
+// What the issuing warps share: addresses, the barriers they wait for, and the MMAs of a step.
 template <int D, bool DKV>
-__device__ void bwd_mma(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem_base, volatile int* abort_flag) {
+struct Issuer {
   using L = BL<D>;
   using C = BCfg<D>;
-  constexpr int kTileBytes = L::kTileBytes;
-  const uint32_t res0 = ptx::smem_u32(sm + L::kRes), res1 = res0 + kTileBytes;
-  const uint32_t str = ptx::smem_u32(sm + L::kStr);
-  constexpr uint32_t kHalfBytes = kStep * 128;  // 64 rows of a tile
-  uint32_t it_n = 0, s_it = 0, step = 0, it_cnt = 0;
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
-  const bool el = ptx::elect_one();  // issues for the warp
+  static constexpr int kNS0 = C::template kNS0<DKV>, kNS1 = C::template kNS1<DKV>;
+  uint8_t* sm;
+  uint64_t* bars;
+  volatile int* abort_flag;
+  int* status;
+  uint32_t res0, str0, str1, aug, ones, tmem;
+  bool el;  // this lane issues for the warp
+  __device__ __forceinline__ Issuer(const BwdArgs& a, uint8_t* smem, uint64_t* b, uint32_t tmem_base, volatile int* ab)
+      : sm(smem), bars(b), abort_flag(ab), status(a.status), res0(ptx::smem_u32(smem + L::kRes)),
+        str0(ptx::smem_u32(smem + L::kStr)), str1(str0 + kNS0 * L::kTileBytes), aug(ptx::smem_u32(smem + L::kAug)),
+        ones(ptx::smem_u32(smem + L::kOnes)), tmem(__shfl_sync(0xffffffffu, tmem_base, 0)), el(ptx::elect_one()) {}
+  __device__ __forceinline__ bool ready(int bar, uint32_t parity) const {
+    if (!bw_wait_warp(bars + bar, parity, abort_flag, status)) return false;
+    ptx::tc_fence_after();
+    return true;
+  }
+  // step s's operands are there, and its S and dP
+  __device__ __forceinline__ bool full0(uint32_t s) const { return ready(kStr0Full + (int)(s % kNS0), (s / kNS0) & 1); }
+  __device__ __forceinline__ bool full1(uint32_t s) const { return ready(kStr1Full + (int)(s % kNS1), (s / kNS1) & 1); }
+  __device__ __forceinline__ uint32_t op0(uint32_t s) const { return str0 + (s % kNS0) * L::kTileBytes; }
+  __device__ __forceinline__ uint32_t op1(uint32_t s) const { return str1 + (s % kNS1) * L::kTileBytes; }
+  __device__ __forceinline__ uint32_t s_at(uint32_t s) const { return tmem + C::template s_col<DKV>(s & 1); }
+  __device__ __forceinline__ void scores_s(uint32_t s) const {
+    if (el) {
+      mma_scores<D>(s_at(s), res0, op0(s));
+      if constexpr (DKV) mma_consts(s_at(s), ones, aug + (s % kNS0) * kAugB);
+      else mma_consts(s_at(s), aug, ones);
+      ptx::umma_commit(bars + kSFull + (s & 1));
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void scores_dp(uint32_t s, bool last) const {
+    if (el) {
+      mma_scores<D>(tmem + C::kDP, res0 + L::kTileBytes, op1(s));
+      if constexpr (DKV) mma_consts(tmem + C::kDP, ones + kAugB, aug + (s % kNS0) * kAugB);
+      else mma_consts(tmem + C::kDP, aug, ones + kAugB);
+      ptx::umma_commit(bars + kDpFull);
+      if constexpr (!DKV) ptx::umma_commit(bars + kStr1Empty + s % kNS1);
+      if (last) ptx::umma_commit(bars + kResEmpty);  // the resident pair read for the last time
+    }
+    __syncwarp();
+  }
+  // all MMAs this warp issued must complete before TMEM is released
+  __device__ __forceinline__ void finish(int bar) const {
+    if (el) ptx::umma_commit(bars + bar);
+    __syncwarp();
+    bw_drain(bars + bar, 0);
+  }
+};
+
+// Two S buffers: one warp issues the scores and another the accumulation, so that neither's waits
+// (over 100 cycles each, even for what is there: the MMAs' operands take the shared memory) leave the
+// tensor core idle.
+template <int D, bool DKV>
+__device__ void bwd_issue_scores(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem_base,
+                                 volatile int* abort_flag) {
+  const Issuer<D, DKV> q(a, sm, bars, tmem_base, abort_flag);
+  uint32_t it_n = 0, step = 0, it_cnt = 0;
   BwdItemDesc it;
   while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
     const int n = __shfl_sync(0xffffffffu, it.n, 0);
     if (n <= 0) continue;
-    if (!bw_wait_warp(bars + kResFull, it_n & 1, abort_flag, a.status)) goto out;
-    ptx::tc_fence_after();
-    {
-      const uint32_t ii = it_n++;
-      const int nsteps = 2 * n;
-      const uint32_t step0 = step;
-      // the streamed stage of local step ls; waits for it on the tile's first step
-      auto stage_of = [&](int ls, bool wait_full, int& st) -> bool {
-        const uint32_t sj = s_it + (uint32_t)(ls >> 1);
-        st = (int)(sj % kNS);
-        if (wait_full && (ls & 1) == 0) {
-          if (!bw_wait_warp(bars + kStrFull + st, (sj / kNS) & 1, abort_flag, a.status)) return false;
-          ptx::tc_fence_after();
-        }
-        return true;
-      };
-      // the first accumulating MMA of an item overwrites the accumulators: the compute
-      // warps must have read the previous item's
-      auto acc_free = [&]() -> bool {
-        if (ii == 0) return true;
-        if (!bw_wait_warp(bars + kAccEmpty, (ii - 1) & 1, abort_flag, a.status)) return false;
-        ptx::tc_fence_after();
-        return true;
-      };
-      if constexpr (C::kDB) {
-        // two buffers of every score: the scores of step ls + 1 go out before this step's operands are
-        // waited for.  Their buffer was last read by the accumulation of step ls - 1, issued before
-        // them, and by the compute warps, whose operands of that step were waited for.
-        auto issue_scores = [&](int ls) -> bool {
-          int st;
-          if (!stage_of(ls, true, st)) return false;
-          const uint32_t b = (step0 + ls) & 1, half = (uint32_t)(ls & 1) * kHalfBytes;
-          const uint32_t s0 = tmem + (DKV ? C::dkv_s(b) : C::dq_s(b)), s1 = DKV ? s0 + 64 : tmem + C::dq_dp(b);
-          if (el) {
-            mma_scores<D>(s0, res0, str + (2 * st) * kTileBytes + half);
-            mma_scores<D>(s1, res1, str + (2 * st + 1) * kTileBytes + half);
-            ptx::umma_commit(bars + syfull<D>(step0 + ls));
-            if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // the resident pair read for the last time
-          }
-          __syncwarp();
-          return true;
-        };
-        if (!issue_scores(0)) goto out;
-        for (int ls = 0; ls < nsteps; ++ls) {
-          int st;
-          stage_of(ls, false, st);
-          if (ls + 1 < nsteps && !issue_scores(ls + 1)) goto out;
-          if (!bw_wait_warp(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
-          ptx::tc_fence_after();
-          if (ls == 0 && !acc_free()) goto out;
-          const uint32_t b = (step0 + ls) & 1, half = (uint32_t)(ls & 1) * kHalfBytes;
-          const uint32_t r0 = str + (2 * st) * kTileBytes + half, r1 = str + (2 * st + 1) * kTileBytes + half;
-          if (el) {
-            if constexpr (DKV) {
-              mma_acc<D>(tmem + C::kDV, tmem + C::dkv_s(b), r1, ls > 0);       // dV += P^T dO_h
-              mma_acc<D>(tmem + C::kDK, tmem + C::dkv_s(b) + 64, r0, ls > 0);  // dK += dS^T Q'_h
-            } else {
-              mma_acc<D>(tmem + C::kDQ, tmem + C::dq_s(b), r0, ls > 0);  // dQ += dS K'_h
-          }
-          if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
-          }
-          __syncwarp();
-        }
-      } else if constexpr (!DKV) {
-        // S(ls) = Q' K'_h^T into S buffer (step0 + ls) % 2, dP(ls) = dO V_h^T.  dP(ls + 1)
-        // goes out as soon as the compute warps have loaded dP(ls), so both scores of
-        // the next step are ready when this step's compute ends.
-        auto issue_scores = [&](int ls) -> bool {
-          int st;
-          if (!stage_of(ls, true, st)) return false;
-          const uint32_t half = (uint32_t)(ls & 1) * kHalfBytes;
-          if (el) {
-            mma_scores<D>(tmem + ((step0 + ls) & 1) * kStep, res0, str + (2 * st) * kTileBytes + half);
-            mma_scores<D>(tmem + 128, res1, str + (2 * st + 1) * kTileBytes + half);
-            ptx::umma_commit(bars + kSyFull);
-            if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // Q' and dO read for the last time
-          }
-          __syncwarp();
-          return true;
-        };
-        if (!issue_scores(0)) goto out;
-        for (int ls = 0; ls < nsteps; ++ls) {
-          int st;
-          stage_of(ls, false, st);
-          if (ls + 1 < nsteps) {
-            if (!bw_wait_warp(bars + kDpFree, (step0 + ls) & 1, abort_flag, a.status)) goto out;
-            ptx::tc_fence_after();
-            if (!issue_scores(ls + 1)) goto out;
-          }
-          if (!bw_wait_warp(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
-          ptx::tc_fence_after();
-          if (ls == 0 && !acc_free()) goto out;
-          const uint32_t kb = str + (2 * st) * kTileBytes + (ls & 1) * kHalfBytes;
-          if (el) {
-            mma_acc<D>(tmem + C::kDQ, tmem + ((step0 + ls) & 1) * kStep, kb, ls > 0);  // dQ += dS K'_h
-            if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
-          }
-          __syncwarp();
-        }
-      } else {
-        // S^T = K' Q'_h^T and dP^T = V dO_h^T
-        auto issue_scores = [&](int ls) -> bool {
-          int st;
-          if (!stage_of(ls, true, st)) return false;
-          if (el) {
-            mma_scores<D>(tmem + 0, res0, str + (2 * st) * kTileBytes + (ls & 1) * kHalfBytes);
-            mma_scores<D>(tmem + 64, res1, str + (2 * st + 1) * kTileBytes + (ls & 1) * kHalfBytes);
-            ptx::umma_commit(bars + kSyFull);
-            if (ls == nsteps - 1) ptx::umma_commit(bars + kResEmpty);  // K' and V read for the last time
-          }
-          __syncwarp();
-          return true;
-        };
-        if (!issue_scores(0)) goto out;
-        for (int ls = 0; ls < nsteps; ++ls) {
-          int st;
-          stage_of(ls, false, st);
-          if (!bw_wait_warp(bars + xready(step0 + ls), xready_parity(step0 + ls), abort_flag, a.status)) goto out;
-          ptx::tc_fence_after();
-          if (ls == 0 && !acc_free()) goto out;
-          const uint32_t qb = str + (2 * st) * kTileBytes + (ls & 1) * kHalfBytes;
-          const uint32_t ob = str + (2 * st + 1) * kTileBytes + (ls & 1) * kHalfBytes;
-          if (el) {
-            mma_acc<D>(tmem + C::kDV, tmem + 0, ob, ls > 0);   // dV += P^T dO_h
-            mma_acc<D>(tmem + C::kDK, tmem + 64, qb, ls > 0);  // dK += dS^T Q'_h
-            if (ls & 1) ptx::umma_commit(bars + kStrEmpty + st);
-          }
-          __syncwarp();
-          if (ls + 1 < nsteps && !issue_scores(ls + 1)) goto out;
-        }
-      }
-      step += (uint32_t)nsteps;
-      s_it += (uint32_t)n;
-      if (el) ptx::umma_commit(bars + kAccFull);
-      __syncwarp();
+    if (!q.ready(kResFull, (it_n++) & 1)) goto out;
+    for (int j = 0; j < n; ++j, ++step) {
+      const uint32_t s = __shfl_sync(0xffffffffu, step, 0);
+      // S's buffer: free when the accumulation of the step before last has read it
+      if (s >= 2 && !q.ready(kSFree + (int)(s & 1), par2(s - 2))) goto out;
+      if (!q.full0(s)) goto out;
+      q.scores_s(s);
+      if (s >= 1 && !q.ready(kDpFree, par1(s - 1))) goto out;
+      if (!q.full1(s)) goto out;
+      q.scores_dp(s, j == n - 1);
     }
   }
 out:
-  // all issued MMAs must complete before TMEM is released
-  if (el) ptx::umma_commit(bars + kMmaDone);
-  __syncwarp();
-  bw_drain(bars + kMmaDone, 0);
+  q.finish(kMmaDone);
+}
+template <int D, bool DKV>
+__device__ void bwd_issue_acc(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem_base, volatile int* abort_flag) {
+  using C = BCfg<D>;
+  const Issuer<D, DKV> q(a, sm, bars, tmem_base, abort_flag);
+  uint32_t it_n = 0, step = 0, it_cnt = 0;
+  BwdItemDesc it;
+  while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
+    const int n = __shfl_sync(0xffffffffu, it.n, 0);
+    if (n <= 0) continue;
+    for (int j = 0; j < n; ++j, ++step) {
+      const uint32_t s = __shfl_sync(0xffffffffu, step, 0);
+      if (!q.ready(kPReady + (int)(s & 1), par2(s))) goto out;
+      // the item's first MMA overwrites the accumulators: the compute warps must have read the last item's
+      if (j == 0 && it_n > 0 && !q.ready(kAccEmpty, (it_n - 1) & 1)) goto out;
+      if (q.el) {
+        // (the step's scores are complete too: the compute warps have read them)
+        if constexpr (DKV) {
+          mma_acc<D>(q.tmem + C::kDV, q.s_at(s), q.op1(s), j > 0);  // dV += P^T dO
+          ptx::umma_commit(bars + kStr1Empty + s % q.kNS1);
+          mma_acc<D>(q.tmem + C::kDK, q.s_at(s) + kDsCols, q.op0(s), j > 0);  // dK += dS^T Q'
+        } else {
+          mma_acc<D>(q.tmem + C::kDQ, q.s_at(s), q.op0(s), j > 0);  // dQ += dS K'
+        }
+        ptx::umma_commit(bars + kSFree + (s & 1));
+        ptx::umma_commit(bars + kStr0Empty + s % q.kNS0);
+        if (j == n - 1) ptx::umma_commit(bars + kAccFull);
+      }
+      __syncwarp();
+    }
+    ++it_n;
+  }
+out:
+  q.finish(kMmaDone + 1);
+}
+
+// One buffer of S and dP each (DKV at head_dim 128): one warp issues everything in order.  S goes out
+// behind dV, which reads P^T in its columns, and dP behind dK, which reads dS^T; each pair runs under
+// the compute of the other.
+template <int D>
+__device__ void bwd_issue_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem_base, volatile int* abort_flag) {
+  using C = BCfg<D>;
+  const Issuer<D, true> q(a, sm, bars, tmem_base, abort_flag);
+  uint32_t it_n = 0, step = 0, it_cnt = 0;
+  BwdItemDesc it;
+  while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
+    const int n = __shfl_sync(0xffffffffu, it.n, 0);
+    if (n <= 0) continue;
+    if (!q.ready(kResFull, it_n & 1)) goto out;
+    {
+      const uint32_t s0 = __shfl_sync(0xffffffffu, step, 0);
+      if (!q.full0(s0)) goto out;
+      q.scores_s(s0);
+      if (!q.full1(s0)) goto out;
+      q.scores_dp(s0, n == 1);
+      for (int j = 0; j < n; ++j) {
+        const uint32_t s = s0 + (uint32_t)j;
+        const bool more = j + 1 < n;
+        if (!q.ready(kPReady + (int)(s & 1), par2(s))) goto out;
+        if (j == 0 && it_n > 0 && !q.ready(kAccEmpty, (it_n - 1) & 1)) goto out;
+        if (q.el) {
+          mma_acc<D>(q.tmem + C::kDV, q.s_at(s), q.op1(s), j > 0);
+          ptx::umma_commit(bars + kStr1Empty + s % q.kNS1);
+        }
+        __syncwarp();
+        if (more) {
+          if (!q.full0(s + 1)) goto out;
+          q.scores_s(s + 1);
+        }
+        if (!q.ready(kDsReady, par1(s))) goto out;
+        if (q.el) {
+          mma_acc<D>(q.tmem + C::kDK, q.tmem + C::kDP, q.op0(s), j > 0);
+          ptx::umma_commit(bars + kStr0Empty + s % q.kNS0);
+          if (!more) ptx::umma_commit(bars + kAccFull);
+        }
+        __syncwarp();
+        if (more) {
+          if (!q.full1(s + 1)) goto out;
+          q.scores_dp(s + 1, j + 2 == n);
+        }
+      }
+      step += (uint32_t)n;
+      ++it_n;
+    }
+  }
+out:
+  q.finish(kMmaDone);
 }
 
 // ------------------------------------------------------------------ compute warps
@@ -558,11 +639,6 @@ __device__ __forceinline__ unsigned long long f2mul(unsigned long long a, unsign
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-
-// The row-constant table of one tile (128 rows): rows 2k and 2k+1 share 16 bytes,
-// {-lse2(2k), -lse2(2k+1), -D(2k), -D(2k+1)}, with lse2 = lse * log2(e).
-__device__ __forceinline__ float row_neg_lse2(const float* tab, int r) { return tab[(r >> 1) * 4 + (r & 1)]; }
-__device__ __forceinline__ float row_neg_d(const float* tab, int r) { return tab[(r >> 1) * 4 + 2 + (r & 1)]; }
 
 // 32 columns of a gradient row, scaled and (rotate) turned back by dt, to global memory in bf16:
 // 32-byte stores when the gradient buffers are 32-byte aligned (each store then fills whole
@@ -610,130 +686,121 @@ __device__ __forceinline__ void rec_row(const KeyTileRec* rec, int row, long lon
     if ((rec->typebits[c][row >> 5] >> (row & 31)) & 1u) ty = c;
 }
 
-// DQ: thread = query row of the item's tile.
+// A query row's visibility bits over a key tile without a slot in the mask table.  Not inlined: rare,
+// and its registers would be taken from the scores.
+__device__ __noinline__ uint4 built_mask(const MaskP& mask, bool live, int pi, long long ti, int tyi,
+                                         const KeyTileRec* rec, int key0) {
+  const uint32_t f = live ? ~0u : 0u;
+  uint32_t vm[4] = {f, f, f, f};
+  RowMask rm;
+  row_mask_setup(mask, live, pi, ti, tyi, rm);
+  build_mask(rm, rec, key0, vm);
+  return make_uint4(vm[0], vm[1], vm[2], vm[3]);
+}
+
+// DQ: thread = query row of the item's tile and 32 of its keys.
 template <int D>
 __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem,
                                volatile int* abort_flag) {
   using BL = recattn::BL<D>;
   using C = BCfg<D>;
+  constexpr int kNS0 = C::template kNS0<false>;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
-  const int wg = (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
+  const int wg = (int)((threadIdx.x - 32 * C::kRoles) >> 7);  // this thread's warpgroup
   const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
   const float sl2 = a.scale * kLog2e;
-  const uint8_t* sstage = sm + BL::kSRec;  // per stage: key record or mask-table rows
-  const KeyTileRec* rrec = reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec);
-  const float* rrow = reinterpret_cast<const float*>(sm + BL::kRRow);
-  const int H = a.heads;
   const unsigned long long sl2x2 = f2pack(sl2, sl2);
-  const bool wide = (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;  // row pieces 32-byte aligned
-  uint32_t it_n = 0, s_it = 0, step = 0, it_cnt = 0;
+  const WarpBars wb{ptx::smem_u32(bars), bars, abort_flag, a.status};
+  uint32_t it_n = 0, step = 0, it_cnt = 0;
   BwdItemDesc it;
   while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
     const int pi = it.tile * kTile + row;
     const bool row_ok = pi < it.len;
-    const long long tok = it.tok_start + pi, grow = tok * H + it.h;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + grow * D;
+    auto dst = [&]() {
+      return static_cast<__nv_bfloat16*>(a.dq) + ((it.tok_start + pi) * a.heads + it.h) * D;
+    };
     if (it.n <= 0) {  // no visible key tile
-      if (row_ok && wg == 0) zero_row<D>(dst);
+      if (row_ok && wg == 0) zero_row<D>(dst());
       continue;
     }
-    // the row's time, type and constants, loaded with Q'
-    if (!bw_wait_warp(bars + kResFull, it_n & 1, abort_flag, a.status)) return;
-    long long ti;
-    int tyi;
-    rec_row(rrec, row, ti, tyi);
-    const float nl = row_neg_lse2(rrow, row), nd = row_neg_d(rrow, row);
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bars + kResEmpty);
-    // a row that sees no key contributes nothing: its P is exp2(s - inf) = 0, so FULL
-    // tiles need no mask for it
-    const bool live = row_ok && nl != INFINITY;
-    const unsigned long long nl2 = f2pack(live ? nl : -INFINITY, live ? nl : -INFINITY), nd2 = f2pack(nd, nd);
-    RowMask rm;
-    row_mask_setup(a.mask, live, pi, ti, tyi, rm);
-    Cursor cur;
-    cur.init(a.klist, a.kslot, it, 1);
-    for (int j = 0; j < it.n; ++j) {
-      int kt, cls, tslot;
-      cur.next(kt, cls, tslot);
-      const int st = (int)(s_it % kNS);
-      const uint32_t ph = (s_it / kNS) & 1;
-      ++s_it;
-      const uint32_t f = live ? ~0u : 0u;
-      uint32_t vm[4] = {f, f, f, f};
-      if (cls != REC_ATTN_TILE_FULL) {
-        if (!bw_wait_warp(bars + kStrFull + st, ph, abort_flag, a.status)) return;
-        if (tslot >= 0) {  // the row's words of the mask table (zero for rows that see no key)
-          const uint4 w = reinterpret_cast<const uint4*>(sstage + st * kStageRecB)[row];
-          vm[0] = w.x; vm[1] = w.y; vm[2] = w.z; vm[3] = w.w;
+    // the row's time, loaded with Q'
+    if (!wb.wait(kResFull, it_n & 1)) return;
+    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec)->t[row] - it.t_ref);
+    wb.arrive(kResEmpty);
+    WarpCursor<false> cur;
+    cur.init(a, it, it.n);
+    for (int j = 0; j < it.n; ++j, ++step) {
+      // this thread's 32 keys (FULL: the constants of rows past the request's end and of rows that see
+      // no key make P zero)
+      uint32_t bits = ~0u;
+      const bool full = cur.is_full();
+      if (!full) {
+        const int st = (int)(step % kNS0);
+        if (!wb.wait(kStr0Full + st, (step / kNS0) & 1)) return;
+        const int tslot = cur.table_slot(), tile = cur.tile();
+        const uint8_t* rec = sm + BL::kSRec + st * kStageRecB;  // (read before the step's operand is ready)
+        if (tslot >= 0) {  // the row's words of the mask table
+          bits = reinterpret_cast<const uint32_t*>(rec)[4 * row + wg];
         } else {
-          build_mask(rm, reinterpret_cast<const KeyTileRec*>(sstage + st * kStageRecB), kt * kTile, vm);
+          const long long tok = it.tok_start + (row_ok ? pi : 0);
+          const uint4 vm = built_mask(a.mask, row_ok, pi, a.t[tok], a.ty[tok], reinterpret_cast<const KeyTileRec*>(rec),
+                                      tile * kTile);
+          bits = wg == 0 ? vm.x : wg == 1 ? vm.y : wg == 2 ? vm.z : vm.w;
         }
-      }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + kStrEmpty + st);  // the stage's record was read
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh, ++step) {
-        if (!bw_wait_warp(bars + syfull<D>(step), syfull_parity<D>(step), abort_flag, a.status)) return;
-        ptx::tc_fence_after();
-        const uint32_t sb = tl + C::dq_s(step & 1), db = tl + C::dq_dp(step & 1);
-        const uint32_t wb[2] = {hh ? vm[2] : vm[0], hh ? vm[3] : vm[1]};  // this step's 64 keys
-        constexpr int SUB = C::kSub;
-        const uint32_t bits = wg ? wb[1] : wb[0];  // this warpgroup's 32 keys
-        uint32_t d[32], sr[SUB], pk[SUB / 2];
-        ptx::tmem_ld32_async(db + 32 * wg, d);
-        if constexpr (SUB == 32) ptx::tmem_ld32_async(sb + 32 * wg, sr);
-        ptx::tmem_wait_ld32(d);
-        if constexpr (SUB == 32) ptx::tmem_wait_ld32(sr);
-        if constexpr (!C::kDB) {  // dP's columns go back to the MMA issuer
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bars + kDpFree);
-        }
-#pragma unroll
-        for (int u = 0; u < 32 / SUB; ++u) {
-          if constexpr (SUB == 16) ptx::tmem_ld16(sb + 32 * wg + 16 * u, sr);
-#pragma unroll
-          for (int e = 0; e < SUB / 2; ++e) {
-            float y0, y1;
-            f2unpack(f2fma(f2pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sl2x2, nl2), y0, y1);
-            float p0 = ex2(y0), p1 = ex2(y1);
-            if (cls != REC_ATTN_TILE_FULL) {
-              p0 = ((bits >> (SUB * u + 2 * e)) & 1u) ? p0 : 0.f;
-              p1 = ((bits >> (SUB * u + 2 * e + 1)) & 1u) ? p1 : 0.f;
-            }
-            float g0, g1;
-            f2unpack(f2mul(f2pack(p0, p1), f2add(f2pack(__uint_as_float(d[SUB * u + 2 * e]),
-                                                        __uint_as_float(d[SUB * u + 2 * e + 1])), nd2)), g0, g1);
-            pk[e] = bf16x2(g0, g1);
-          }
-          // dS over S columns already read
-          if constexpr (SUB == 16) ptx::tmem_st8_async(sb + 32 * wg + 8 * u, pk);
-          else ptx::tmem_st16_async(sb + 32 * wg, pk);
-        }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars + xready(step));
       }
+      cur.next(a, 1);
+      if (!wb.wait(kSFull + (step & 1), par2(step))) return;
+      ptx::tc_fence_after();
+      const uint32_t sb = tl + C::template s_col<false>(step & 1) + 32 * wg, db = tl + C::kDP + 32 * wg;
+      uint32_t p[32];
+      ptx::tmem_ld32(sb, p);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float y0, y1;
+        f2unpack(f2mul(f2pack(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1])), sl2x2), y0, y1);
+        p[2 * e] = __float_as_uint(ex2(y0));
+        p[2 * e + 1] = __float_as_uint(ex2(y1));
+      }
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) p[e] = ((bits >> e) & 1u) ? p[e] : 0u;
+      }
+      if (!wb.wait(kDpFull, par1(step))) return;
+      ptx::tc_fence_after();
+      uint32_t d[32], pk[16];
+      ptx::tmem_ld32(db, d);
+      ptx::tc_fence_before();  // dP's columns go back to the MMA issuer
+      wb.arrive(kDpFree);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float g0, g1;
+        f2unpack(f2mul(f2pack(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1])),
+                       f2pack(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]))), g0, g1);
+        pk[e] = bf16x2(g0, g1);
+      }
+      ptx::tmem_st16_async(sb, pk);  // dS over S columns already read
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      wb.arrive(kPReady + (step & 1));
     }
-    if (!bw_wait_warp(bars + kAccFull, it_n & 1, abort_flag, a.status)) return;
+    if (!wb.wait(kAccFull, it_n & 1)) return;
     ++it_n;
     ptx::tc_fence_after();
-    // each warpgroup half of the columns, 32 at a time
-#pragma unroll 1
-    for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
+    // 32 columns a warpgroup (at head_dim 64 the first two)
+    const int c0 = 32 * wg;
+    if (c0 < D) {
       uint32_t acc[32];
       ptx::tmem_ld32(tl + C::kDQ + c0, acc);
-      if (c0 + 32 >= (wg + 1) * (D / 2)) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
-      }
+      ptx::tc_fence_before();
+      wb.arrive(kAccEmpty);
       if (row_ok)
-        store_cols(dst + c0, acc, a.scale, a.rotate != 0, (float)(ti - it.t_ref), a.omega + c0 / 2, wide);
-      __syncwarp();
+        store_cols(dst() + c0, acc, a.scale, a.rotate != 0, dt, a.omega + c0 / 2,
+                   (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0);
+    } else if (lane == 0) {
+      ptx::mbar_arrive(bars + kAccEmpty);
     }
+    __syncwarp();
   }
 }
 
@@ -756,204 +823,160 @@ __device__ __forceinline__ bool group_sync(uint64_t* bar, uint32_t& n, volatile 
   return bw_wait_warp(bar, (n++) & 1, abort_flag, status);
 }
 
-// DKV: thread = key row of the item's tile (and, while the masks are built, a row of
-// the query tile).  The column bits of the next query tile are built while the tensor
-// core runs the second half of the current one (two buffers of column bits).
+// DKV: thread = key row of the item's tile and 32 queries of the step (and, while the first
+// warpgroup builds a mask, a row of the query tile).
 template <int D>
 __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem,
                                 volatile int* abort_flag) {
   using BL = recattn::BL<D>;
   using C = BCfg<D>;
+  constexpr int kNS0 = C::template kNS0<true>;
+  constexpr bool kTwoS = C::template kTwoS<true>;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
-  const int wg = (int)((threadIdx.x - 64) >> 7);  // this thread's warpgroup
+  const int wg = (int)((threadIdx.x - 32 * C::kRoles) >> 7);  // this thread's warpgroup
   const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
   const float sl2 = a.scale * kLog2e;
-  const KeyTileRec* rrec = reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec);
-  const uint8_t* sstage = sm + BL::kSRec;  // per stage: query record or mask-table columns
-  const float* srow = reinterpret_cast<const float*>(sm + BL::kSRow);
   const unsigned long long sl2x2 = f2pack(sl2, sl2);
-  const bool wide = ((reinterpret_cast<uintptr_t>(a.dk) | reinterpret_cast<uintptr_t>(a.dv)) & 31) == 0;
-  uint32_t* colS = reinterpret_cast<uint32_t*>(sm + BL::kCol);
-  const int Hk = a.heads / a.group;
-  uint32_t it_n = 0, s_it = 0, step = 0, grp = 0, cbuf = 0, it_cnt = 0;
+  const long long T = a.rows / a.heads;
+  const int reps = a.group / a.parts;
+  const WarpBars wb{ptx::smem_u32(bars), bars, abort_flag, a.status};
+  uint32_t it_n = 0, step = 0, grp = 0, it_cnt = 0;
   BwdItemDesc it;
   while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
     const int pj = it.tile * kTile + row;
     const bool key_ok = pj < it.len;
-    const long long growk = (it.tok_start + pj) * Hk + it.h / a.parts;
-    const long long n_part = (long long)Hk * a.parts * (a.rows / a.heads) * D;  // one gradient's parts
-    float* part = a.kv_part ? a.kv_part + ((long long)it.h * (a.rows / a.heads) + it.tok_start + pj) * D : nullptr;
-    __nv_bfloat16* dkr = static_cast<__nv_bfloat16*>(a.dk) + growk * D;
-    __nv_bfloat16* dvr = static_cast<__nv_bfloat16*>(a.dv) + growk * D;
+    // where the key's row of dK (at column 0) stands in the gradients, or in the parts
+    auto at = [&]() {
+      return a.kv_part ? ((long long)it.h * T + it.tok_start + pj) * D
+                       : ((it.tok_start + pj) * (a.heads / a.group) + it.h / a.parts) * D;
+    };
+    auto part_dv = [&]() { return (long long)(a.heads / a.group) * a.parts * T * D; };
     if (it.n <= 0) {  // no query sees this key tile
       if (wg != 0) continue;
-      if (key_ok && part) {
+      if (key_ok && a.kv_part) {
+        float* part = a.kv_part + at();
+        const long long n_part = part_dv();
         for (int e = 0; e < D; e += 4)
           *reinterpret_cast<float4*>(part + e) = *reinterpret_cast<float4*>(part + n_part + e) = make_float4(0, 0, 0, 0);
       } else if (key_ok) {
-        zero_row<D>(dkr);
-        zero_row<D>(dvr);
+        zero_row<D>(static_cast<__nv_bfloat16*>(a.dk) + at());
+        zero_row<D>(static_cast<__nv_bfloat16*>(a.dv) + at());
       }
       continue;
     }
-    if (!bw_wait_warp(bars + kResFull, it_n & 1, abort_flag, a.status)) return;  // the key tile's record
-    const long long tj = rrec->t[row];
-    Cursor cur;
-    cur.init(a.qlist, a.qslot, it, a.group / a.parts);
-    // Column bits of the item's j-th query tile (stage st) into buffer `buf`: the key's
-    // words of the mask table's columns when the pair has a slot; otherwise, as query
-    // row `row` of the tile, this thread builds the row's bits over the key tile and
-    // each warp transposes its 32 rows into per-key words.
-    auto prepare = [&](int j, int qt, int cls, int tslot, int st, uint32_t ph, uint32_t buf) -> bool {
-      if (!bw_wait_warp(bars + kStrFull + st, ph, abort_flag, a.status)) return false;
-      // after the item's last read of the key tile's record, its buffer may be refilled
-      auto release_rec = [&]() {
-        if (j == it.n - 1) {
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bars + kResEmpty);
+    if (!wb.wait(kResFull, it_n & 1)) return;  // the key tile's record
+    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec)->t[row] - it.t_ref);
+    WarpCursor<true> cur;
+    cur.init(a, it, it.n / reps);
+    for (int j = 0; j < it.n; ++j, ++step) {
+      // The key's bits for this thread's 32 queries: its word of the mask table's columns when the
+      // pair has a slot; otherwise the first warpgroup's threads, as rows of the query tile, build
+      // their rows' bits over the key tile and its warps transpose them into per-key words.  Two
+      // buffers in turn: a thread reads one before it meets the others for the next.
+      uint32_t bits = ~0u;  // (FULL: the constants of queries past the request's end make P zero)
+      const bool full = cur.is_full();
+      if (!full) {
+        const int st = (int)(step % kNS0);
+        if (!wb.wait(kStr0Full + st, (step / kNS0) & 1)) return;
+        const int tslot = cur.table_slot(), tile = cur.tile();
+        const uint8_t* rec = sm + BL::kSRec + st * kStageRecB;  // (read before the step's operands are ready)
+        if (tslot >= 0) {
+          bits = reinterpret_cast<const uint32_t*>(rec)[4 * row + wg];
+        } else {
+          uint32_t* col = reinterpret_cast<uint32_t*>(sm + BL::kCol) + (grp & 1) * (kTile * 4);
+          if (wg == 0) {
+            const int qi = tile * kTile + row;
+            long long tq;
+            int tyq;
+            rec_row(reinterpret_cast<const KeyTileRec*>(rec), row, tq, tyq);
+            const uint4 vm = built_mask(a.mask, qi < it.len, qi, tq, tyq,
+                                        reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec), it.tile * kTile);
+            const uint32_t w[4] = {vm.x, vm.y, vm.z, vm.w};
+#pragma unroll
+            for (int wd = 0; wd < 4; ++wd) col[(32 * wd + lane) * 4 + quad] = transpose32(w[wd], lane);
+          }
+          if (!group_sync(bars + kGroup, grp, abort_flag, a.status)) return;
+          bits = col[4 * row + wg];
         }
-      };
-      if (cls == REC_ATTN_TILE_FULL || wg != 0) {  // the steps of a FULL tile apply no mask
-        release_rec();                             // (and one warpgroup builds the others' bits)
-        return true;
+        __syncwarp();
       }
-      if (tslot >= 0) {
-        reinterpret_cast<uint4*>(colS + buf * (kTile * 4))[row] =
-            reinterpret_cast<const uint4*>(sstage + st * kStageRecB)[row];
-        release_rec();
-        return true;
+      if (j == it.n - 1) {  // the key tile's record was read for the last time
+        wb.arrive(kResEmpty);
       }
-      const int qi = qt * kTile + row;
-      long long tq;
-      int tyq;
-      rec_row(reinterpret_cast<const KeyTileRec*>(sstage + st * kStageRecB), row, tq, tyq);
-      const bool live = qi < it.len && row_neg_lse2(srow + st * 2 * kTile, row) != INFINITY;
-      const uint32_t f = live ? ~0u : 0u;
-      uint32_t vm[4] = {f, f, f, f};
-      RowMask rm;
-      row_mask_setup(a.mask, live, qi, tq, tyq, rm);
-      build_mask(rm, rrec, it.tile * kTile, vm);
-      release_rec();
+      cur.next(a, reps);
+      // P^T over the columns of S^T already read
+      if (!wb.wait(kSFull + (step & 1), par2(step))) return;
+      ptx::tc_fence_after();
+      const uint32_t sb = tl + C::template s_col<true>(step & 1) + 32 * wg, db = tl + C::kDP + 32 * wg;
+      uint32_t p[32], pk[16];
+      ptx::tmem_ld32(sb, p);
 #pragma unroll
-      for (int wd = 0; wd < 4; ++wd) colS[buf * (kTile * 4) + (32 * wd + lane) * 4 + quad] = transpose32(vm[wd], lane);
-      return true;
-    };
-    int qt, cls, tslot;
-    cur.next(qt, cls, tslot);
-    int scls = cls;  // the class of the query tile the steps run on
-    int st = (int)(s_it % kNS);
-    if (!prepare(0, qt, cls, tslot, st, (s_it / kNS) & 1, cbuf)) return;
-    ++s_it;
-    for (int j = 0; j < it.n; ++j) {
-      // a masked tile's words, written by the first warpgroup, are read by both.  The other buffer,
-      // which prepare() overwrites next, was read at the start of the last tile by every thread:
-      // prepare() comes after this tile's first scores, and those went out after the last tile's
-      // first operands were ready.
-      uint4 cm = make_uint4(0, 0, 0, 0);
-      if (scls != REC_ATTN_TILE_FULL) {
-        if (!group_sync(bars + kGroup, grp, abort_flag, a.status)) return;
-        cm = reinterpret_cast<const uint4*>(colS)[cbuf * kTile + row];
+      for (int e = 0; e < 16; ++e) {
+        float y0, y1;
+        f2unpack(f2mul(f2pack(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1])), sl2x2), y0, y1);
+        p[2 * e] = __float_as_uint(ex2(y0));
+        p[2 * e + 1] = __float_as_uint(ex2(y1));
       }
-      const float* rows = srow + st * 2 * kTile;
-      int nqt = 0, ncls = 0, nslot = -1, nst = 0;
-      uint32_t nph = 0;
-      if (j + 1 < it.n) {
-        cur.next(nqt, ncls, nslot);
-        nst = (int)(s_it % kNS);
-        nph = (s_it / kNS) & 1;
-        ++s_it;
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) p[e] = ((bits >> e) & 1u) ? p[e] : 0u;
       }
-      // one 64-query step: P^T and dS^T over the scores' TMEM columns
-      auto do_step = [&](int hh) -> bool {
-        if (!bw_wait_warp(bars + syfull<D>(step), syfull_parity<D>(step), abort_flag, a.status)) return false;
-        const uint32_t sb = tl + C::dkv_s(step & 1);
-        ++step;
-        ptx::tc_fence_after();
-        const uint32_t wb[2] = {hh ? cm.z : cm.x, hh ? cm.w : cm.y};  // this step's 64 queries
-        constexpr int SUB = C::kSub;
-        const uint32_t bits = wg ? wb[1] : wb[0];  // this warpgroup's 32 queries
-        // {-lse2, -D} of the 32 queries, a pair per 16-byte load (broadcast; one load for P^T and
-        // dS^T: the scores' MMAs take most of the shared memory's bandwidth, loads wait behind them)
-        const float4* q4 = reinterpret_cast<const float4*>(rows + (hh * kStep + 32 * wg) * 2);
 #pragma unroll
-        for (int u = 0; u < 32 / SUB; ++u) {
-          uint32_t r[2 * SUB], pk[SUB / 2], pd[SUB / 2];  // S^T, then dP^T
-          if constexpr (SUB == 16) {
-            ptx::tmem_ld16x2(sb + 32 * wg + 16 * u, sb + 64 + 32 * wg + 16 * u, r);
-          } else {
-            ptx::tmem_ld32x2_async(sb + 32 * wg, sb + 64 + 32 * wg, r);
-            ptx::tmem_wait_ld(r);
-          }
-#pragma unroll
-          for (int g = 0; g < SUB / 2; ++g) {
-            const float4 k2 = q4[SUB / 2 * u + g];
-            float x0, x1;
-            f2unpack(f2fma(f2pack(__uint_as_float(r[2 * g]), __uint_as_float(r[2 * g + 1])), sl2x2,
-                           f2pack(k2.x, k2.y)), x0, x1);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-            if (scls != REC_ATTN_TILE_FULL) {  // FULL: queries past the request end have -lse2 = -inf
-              x0 = ((bits >> (SUB * u + 2 * g)) & 1u) ? x0 : 0.f;
-              x1 = ((bits >> (SUB * u + 2 * g + 1)) & 1u) ? x1 : 0.f;
-            }
-            pk[g] = bf16x2(x0, x1);
-            float g0, g1;
-            f2unpack(f2mul(f2pack(x0, x1),
-                           f2add(f2pack(__uint_as_float(r[SUB + 2 * g]), __uint_as_float(r[SUB + 2 * g + 1])),
-                                 f2pack(k2.z, k2.w))), g0, g1);
-            pd[g] = bf16x2(g0, g1);
-          }
-          // P^T and dS^T over the columns already read
-          if constexpr (SUB == 16) {
-            ptx::tmem_st8_async(sb + 32 * wg + 8 * u, pk);
-            ptx::tmem_st8_async(sb + 64 + 32 * wg + 8 * u, pd);
-          } else {
-            ptx::tmem_st16_async(sb + 32 * wg, pk);
-            ptx::tmem_st16_async(sb + 64 + 32 * wg, pd);
-          }
-        }
+      for (int e = 0; e < 16; ++e) pk[e] = bf16x2(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]));
+      ptx::tmem_st16_async(sb, pk);
+      if constexpr (!kTwoS) {
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars + xready(step - 1));  // step was counted on at the wait
-        return true;
-      };
-      if (!do_step(0)) return;
-      if (j + 1 < it.n && !prepare(j + 1, nqt, ncls, nslot, nst, nph, cbuf ^ 1u)) return;
-      if (!do_step(1)) return;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + kStrEmpty + st);  // the stage's record and constants were read
-      st = nst;
-      scls = ncls;
-      cbuf ^= 1u;
+        wb.arrive(kPReady + (step & 1));
+      }
+      // dS^T beside P^T, or over the columns of dP^T
+      if (!wb.wait(kDpFull, par1(step))) return;
+      ptx::tc_fence_after();
+      uint32_t d[32];
+      ptx::tmem_ld32(db, d);
+      if constexpr (kTwoS) {
+        ptx::tc_fence_before();  // dP's columns go back to the MMA issuer
+        wb.arrive(kDpFree);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float g0, g1;
+        f2unpack(f2mul(f2pack(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1])),
+                       f2pack(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]))), g0, g1);
+        pk[e] = bf16x2(g0, g1);
+      }
+      ptx::tmem_st16_async(kTwoS ? sb + kDsCols : db, pk);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      wb.arrive(kTwoS ? kPReady + (int)(step & 1) : (int)kDsReady);
     }
-    if (!bw_wait_warp(bars + kAccFull, it_n & 1, abort_flag, a.status)) return;
+    if (!wb.wait(kAccFull, it_n & 1)) return;
     ++it_n;
     ptx::tc_fence_after();
     // dV and dK behind it, 32 columns at a time, the warpgroups in turn
 #pragma unroll 1
-    for (int c0 = 32 * wg; c0 < 2 * D; c0 += 64) {
+    for (int c0 = 32 * wg; c0 < 2 * D; c0 += 32 * C::kWG) {
       uint32_t acc[32];
       ptx::tmem_ld32(tl + C::kDV + c0, acc);
-      if (c0 + 64 >= 2 * D) {
+      if (c0 + 32 * C::kWG >= 2 * D) {
         ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty);
+        wb.arrive(kAccEmpty);
       }
       const bool is_v = c0 < D;
       const int col = is_v ? c0 : c0 - D;
+      const bool wide = ((reinterpret_cast<uintptr_t>(a.dk) | reinterpret_cast<uintptr_t>(a.dv)) & 31) == 0;
       if (!key_ok) {
         // nothing to store
-      } else if (part) {  // the part's sums as they are: k_bwd_kv_sum adds the parts of the group
-        float* dst = part + (is_v ? n_part : 0) + col;
+      } else if (a.kv_part) {  // the part's sums as they are: k_bwd_kv_sum adds the parts of the group
+        float* dst = a.kv_part + at() + (is_v ? part_dv() : 0) + col;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           ptx::st_global_v8(dst + 8 * c, acc[8 * c], acc[8 * c + 1], acc[8 * c + 2], acc[8 * c + 3], acc[8 * c + 4],
                             acc[8 * c + 5], acc[8 * c + 6], acc[8 * c + 7]);
       } else if (is_v) {
-        store_cols(dvr + col, acc, 1.f, false, 0.f, a.omega, wide);
+        store_cols(static_cast<__nv_bfloat16*>(a.dv) + at() + col, acc, 1.f, false, 0.f, a.omega, wide);
       } else {  // scaled and rotated back
-        store_cols(dkr + col, acc, a.scale, a.rotate != 0, (float)(tj - it.t_ref), a.omega + col / 2, wide);
+        store_cols(static_cast<__nv_bfloat16*>(a.dk) + at() + col, acc, a.scale, a.rotate != 0, dt, a.omega + col / 2, wide);
       }
       __syncwarp();
     }
@@ -962,10 +985,10 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
 
 // ------------------------------------------------------------------ row constants
 // Block = (tile g, head h): D_i = <dO_i, O_i> for the tile's 128 rows, eight threads per
-// row (16 bytes of dO and O each, coalesced), written negated with -lse * log2(e) into
-// the tile-padded table, rows paired (row_neg_lse2 / row_neg_d).  lse2 is -inf for rows
-// that see no key and +inf for rows past the request end and pruned rows, so that
-// every P of the latter is exp2(s - inf) = 0 whatever mask bits they have.
+// row (16 bytes of dO and O each, coalesced).  The row's constants as an operand row of the scores'
+// extra K step: -lse / scale (in the scores' unit) and -D, each as three bf16 that add up to it, and
+// -1e38 in place of the first for rows that see no key, rows past the request's end and pruned
+// rows, so that their every P is exp2(-1e38) = 0 whatever mask bits they have.
 template <int D>
 __global__ void __launch_bounds__(256) k_bwd_rowc(BwdArgs a) {
   constexpr int kLanes = D / 8;  // 16-byte chunks of a row, one per thread
@@ -975,7 +998,6 @@ __global__ void __launch_bounds__(256) k_bwd_rowc(BwdArgs a) {
   const ReqMeta m = a.meta[b];
   const int tile = (int)(g - m.tile_start);
   const int sub = threadIdx.x & (kLanes - 1);
-  float* out = reinterpret_cast<float*>(a.rowc + ((long long)h * a.n_tiles + g) * kTile);
   const int keep = a.qkeep[b];
 #pragma unroll 1
   for (int r = threadIdx.x / kLanes; r < kTile; r += 256 / kLanes) {
@@ -1001,8 +1023,15 @@ __global__ void __launch_bounds__(256) k_bwd_rowc(BwdArgs a) {
     for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     if (sub == 0) {
       const float l = ok ? a.lse[row] : INFINITY;
-      out[(r >> 1) * 4 + (r & 1)] = -(l == -INFINITY ? -INFINITY : l * kLog2e);
-      out[(r >> 1) * 4 + 2 + (r & 1)] = -acc;
+      const float c[2] = {isinf(l) ? -1e38f : -l / a.scale, -acc};
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // three bf16 that add up to it: 24 bits
+        const float hi = __bfloat162float(__float2bfloat16(c[i])), mid = __bfloat162float(__float2bfloat16(c[i] - hi));
+        w[2 * i] = bf16x2(hi, mid);
+        w[2 * i + 1] = bf16x2(c[i] - hi - mid, 0.f);
+      }
+      a.rowx[((long long)h * a.n_tiles + g) * kTile + r] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -1166,14 +1195,14 @@ __global__ void __launch_bounds__(256) k_bwd_kv_sum(BwdArgs a) {
 // ------------------------------------------------------------------ kernel
 // maps: Q', K', V, dO as bf16 views [T][heads * d] (K', V: key/value heads), 64 x 128 boxes.
 template <int D, bool DKV>
-__global__ void __launch_bounds__(BCfg<D>::kThreads, BCfg<D>::kBlocksPerSM)
+__global__ void __launch_bounds__(BCfg<D>::kThreads, 1)
     k_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const BwdArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using BL = recattn::BL<D>;
-  constexpr uint32_t kCols = BCfg<D>::kCols;
   constexpr uint32_t kCW = 4 * BCfg<D>::kWG;  // compute warps
+  constexpr bool kTwoS = BCfg<D>::template kTwoS<DKV>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + BL::kBarsOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kNumBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars) + 1;
@@ -1181,28 +1210,45 @@ __global__ void __launch_bounds__(BCfg<D>::kThreads, BCfg<D>::kBlocksPerSM)
   if (threadIdx.x == 0) {
     ptx::mbar_init(bars + kResFull, 1);
     ptx::mbar_init(bars + kResEmpty, 1 + kCW);  // MMAs done + the compute warps read the record
-    for (int i = 0; i < kNS; ++i) {
-      ptx::mbar_init(bars + kStrFull + i, 1);
-      ptx::mbar_init(bars + kStrEmpty + i, 1 + kCW);  // MMAs done + the compute warps read the record
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(bars + kStr0Full + i, 1);
+      ptx::mbar_init(bars + kStr0Empty + i, 1);  // the step's last MMA done (the record was read before it)
+      ptx::mbar_init(bars + kStr1Full + i, 1);
+      ptx::mbar_init(bars + kStr1Empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bars + kSyFull + i, 1);
-      ptx::mbar_init(bars + kXReady + i, kCW);
+      ptx::mbar_init(bars + kSFull + i, 1);
+      ptx::mbar_init(bars + kPReady + i, kCW);
     }
+    ptx::mbar_init(bars + kDpFull, 1);
     ptx::mbar_init(bars + kDpFree, kCW);
+    ptx::mbar_init(bars + kDsReady, kCW);
     ptx::mbar_init(bars + kAccFull, 1);
     ptx::mbar_init(bars + kAccEmpty, kCW);
     ptx::mbar_init(bars + kGroup, 32 * kCW);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + kItemFull + i, 1);
-      ptx::mbar_init(bars + kItemEmpty + i, 1 + kCW);  // the MMA issuer and the compute warps
+      ptx::mbar_init(bars + kItemEmpty + i, (kTwoS ? 2 : 1) + kCW);  // the issuers and the compute warps
+      ptx::mbar_init(bars + kSFree + i, 1);
+      ptx::mbar_init(bars + kMmaDone + i, 1);
     }
-    ptx::mbar_init(bars + kMmaDone, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
+  {
+    // ones over the first three values of a row's constants (S) or the next three (dP); the second
+    // halves of the operands are zero
+    for (int i = threadIdx.x; i < 2 * kAugB / 16; i += BCfg<D>::kThreads) {
+      const int half = i / kTile;  // S ones, zero, dP ones, zero
+      reinterpret_cast<uint4*>(sm + BL::kOnes)[i] = make_uint4(half == 0 ? 0x3f803f80u : 0u, half == 0 ? 0x3f80u : 0u,
+                                                               half == 2 ? 0x3f803f80u : 0u, half == 2 ? 0x3f80u : 0u);
+    }
+    for (int i = threadIdx.x; i < BL::kAugs * kAugB / 16; i += BCfg<D>::kThreads)
+      reinterpret_cast<uint4*>(sm + BL::kAug)[i] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+  }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, kCols);
+    ptx::tmem_alloc(tmem_slot, kTmemCols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -1218,7 +1264,10 @@ __global__ void __launch_bounds__(BCfg<D>::kThreads, BCfg<D>::kBlocksPerSM)
       bwd_producer<D, DKV>(a, res, str, sm, bars, abort_flag);
     }
   } else if (warp == 1) {
-    bwd_mma<D, DKV>(a, sm, bars, tmem, abort_flag);
+    if constexpr (kTwoS) bwd_issue_scores<D, DKV>(a, sm, bars, tmem, abort_flag);
+    else bwd_issue_dkv<D>(a, sm, bars, tmem, abort_flag);
+  } else if (warp == 2) {
+    if constexpr (kTwoS) bwd_issue_acc<D, DKV>(a, sm, bars, tmem, abort_flag);
   } else {
     if constexpr (DKV) bwd_compute_dkv<D>(a, sm, bars, tmem, abort_flag);
     else bwd_compute_dq<D>(a, sm, bars, tmem, abort_flag);
@@ -1227,7 +1276,7 @@ __global__ void __launch_bounds__(BCfg<D>::kThreads, BCfg<D>::kBlocksPerSM)
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, kCols);
+    ptx::tmem_dealloc(tmem, kTmemCols);
   }
   // the last CTA to leave resets the item counter for the next launch
   if (threadIdx.x == 0) {
@@ -1254,7 +1303,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
   k_bwd_rowc<D><<<dim3((unsigned)a.n_tiles, (unsigned)a.heads), 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long cap = (long long)BCfg<D>::kBlocksPerSM * num_sms;
+  const long long cap = num_sms;
   e = launch_mode<D, false>(maps, a, (int)(a.n_items < cap ? a.n_items : cap), st);
   if (e != cudaSuccess) return e;
   e = launch_mode<D, true>(maps, a, (int)(a.n_kv_items < cap ? a.n_kv_items : cap), st);
@@ -1267,7 +1316,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
 }  // namespace
 
 int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int head_dim, int num_sms) {
-  const long long slots = (long long)(head_dim == 64 ? BCfg<64>::kBlocksPerSM : BCfg<128>::kBlocksPerSM) * num_sms;
+  const long long slots = num_sms;
   int parts = 1;
   while (parts < group && n_tiles * kv_heads * parts < 3 * slots) {
     ++parts;

@@ -200,9 +200,9 @@ struct BwdArgs {
   // tensor-core path (bf16): per-plan schedule and per-call row constants
   const BwdItemDesc* desc;  // [n_items] dQ items, then [n_kv_items] dK/dV items (mirrored key tiles)
   const uint32_t* qlist;    // per key tile: query tiles with a non-SKIP class (qt | class << 24)
-  float2* rowc;             // [H][n_tiles][128 rows]: -lse * log2(e) and -D, rows paired as
-                            // {-lse2(2k), -lse2(2k+1), -D(2k), -D(2k+1)} (lse2 -inf: the row sees
-                            // no key; +inf: past the request end or pruned)
+  uint4* rowx;              // [H][n_tiles][128 rows]: -lse / scale and -D as 8 bf16, an operand's row:
+                            // each as three values that add up to it and a zero (-1e38: no key,
+                            // past the request's end or pruned)
   const int* kslot;         // per key-tile list entry: mask-table slot (-1: build the bits)
   const uint32_t* mtab;     // mask table, rows: [slot][128 query rows][4 words over the keys]
   const int* qslot;         // per query-tile list entry (qlist): mask-table slot, -1 if none
