@@ -265,21 +265,24 @@ struct WarpCursor {
   long long at;
   uint32_t e, full;
   int slot, r, rep, left;
-  __device__ __forceinline__ void window(const BwdArgs& a) {
+  __device__ __forceinline__ void load(const BwdArgs& a) {
     const int lane = threadIdx.x & 31;
     const bool in = lane < left;
-    e = in ? (DKV ? a.qlist : a.klist)[at + lane] : 0u;
+    e = in ? (DKV ? a.qlist : a.klist)[at + lane] : 0u;  // (class 0 is not FULL)
     slot = in ? (DKV ? a.qslot : a.kslot)[at + lane] : -1;
-    full = __ballot_sync(0xffffffffu, in && (e >> 24) == (uint32_t)REC_ATTN_TILE_FULL);
     at += 32;
     left -= 32;
     r = 0;
   }
+  __device__ __forceinline__ void vote() {
+    full = __ballot_sync(0xffffffffu, (e >> 24) == (uint32_t)REC_ATTN_TILE_FULL);
+  }
+  // init starts the first loads; vote() once, before the first step
   __device__ __forceinline__ void init(const BwdArgs& a, const BwdItemDesc& d, int entries) {
     at = d.list;
     left = entries;
     rep = 0;
-    window(a);
+    load(a);
   }
   __device__ __forceinline__ bool is_full() const { return (full >> r) & 1u; }
   __device__ __forceinline__ int tile() const { return (int)(__shfl_sync(0xffffffffu, e, r) & 0xffffffu); }
@@ -287,7 +290,10 @@ struct WarpCursor {
   __device__ __forceinline__ void next(const BwdArgs& a, int reps) {
     if (DKV && ++rep < reps) return;
     rep = 0;
-    if (++r == 32 && left > 0) window(a);
+    if (++r == 32 && left > 0) {
+      load(a);
+      vote();
+    }
   }
 };
 
@@ -723,12 +729,13 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
       if (row_ok && wg == 0) zero_row<D>(dst());
       continue;
     }
+    WarpCursor<false> cur;
+    cur.init(a, it, it.n);
     // the row's time, loaded with Q'
     if (!wb.wait(kResFull, it_n & 1)) return;
     const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec)->t[row] - it.t_ref);
     wb.arrive(kResEmpty);
-    WarpCursor<false> cur;
-    cur.init(a, it, it.n);
+    cur.vote();
     for (int j = 0; j < it.n; ++j, ++step) {
       // this thread's 32 keys (FULL: the constants of rows past the request's end and of rows that see
       // no key make P zero)
@@ -864,10 +871,11 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
       }
       continue;
     }
-    if (!wb.wait(kResFull, it_n & 1)) return;  // the key tile's record
-    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec)->t[row] - it.t_ref);
     WarpCursor<true> cur;
     cur.init(a, it, it.n / reps);
+    if (!wb.wait(kResFull, it_n & 1)) return;  // the key tile's record
+    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec)->t[row] - it.t_ref);
+    cur.vote();
     for (int j = 0; j < it.n; ++j, ++step) {
       // The key's bits for this thread's 32 queries: its word of the mask table's columns when the
       // pair has a slot; otherwise the first warpgroup's threads, as rows of the query tile, build
