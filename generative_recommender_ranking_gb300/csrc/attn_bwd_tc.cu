@@ -9,47 +9,49 @@
 //   mode DKV:  dV_j = sum_i P_ij dO_i,  dK'_j = scale sum_i dS_ij Q'_i
 // and dQ = R(t_i)^T dQ', dK = R(t_j)^T dK' (the rotation is orthogonal).
 //
-// Both modes share one persistent kernel shape: at head_dim 64 two CTAs per SM (256
-// TMEM columns each), at 128 one (512 columns: the accumulators are twice as wide), and
-// six warps -- warp 0 loads with TMA, one thread of warp 1 issues every MMA,
-// warps 2 on are the compute warps (one TMEM lane, i.e. one tile row, per
-// thread).  The producer claims the planner's (tile, head) items from a global counter
-// and publishes each item's descriptor in shared memory for the other roles; mode DKV
-// visits key tiles in the mirrored order of the query tiles, so under causal masks
-// both modes start with their heaviest items.  Per item the resident operand pair
-// stays in shared memory (DQ: Q', dO; DKV: K', V) and the streamed pair (DQ: K', V of
-// the query tile's non-SKIP key tiles; DKV: Q', dO of the query tiles whose class
-// against the key tile is not SKIP) runs through a two-stage ring.  A streamed tile
-// is two 64-wide steps:
-//   DQ   S = Q' K'_h^T and dP = dO V_h^T (N = 64); the compute warps write dS (bf16)
-//        over the first columns of S; dQ += dS K'_h with dS read from TMEM.  S is
-//        double-buffered, so the next step's S runs during this step's compute.
-//   DKV  S^T = K' Q'_h^T and dP^T = V dO_h^T; the compute warps write P^T and dS^T
-//        (bf16) over them; dV += P^T dO_h and dK += dS^T Q'_h.
-// TMEM columns:  DQ   S[0] 0..63 | S[1] 64..127 | dP 128..191 | dQ 192..192+d
-//                DKV  S^T 0..63 | dP^T 64..127 | dV 128..128+d | dK 128+d..128+2d
-// At head_dim 128, where one CTA has the SM and all 512 columns to itself, the other scores have
-// buffers too (DQ: dP[1] 320..383; DKV: S^T[1] 384..447 | dP^T[1] 448..511), so the next step's
-// scores always run under this step's compute, and there are two compute warpgroups: each
-// takes 32 of a step's 64 columns and half of the epilogue's (with one warpgroup and one buffer
-// the SM had four compute warps, all of them waiting for the step's MMAs in turn: 16 ragged
-// requests of 603 to 1850 tokens, 8 query and 2 key/value heads, dQ 228 and dK/dV 383 us).
-// The accumulators stay in TMEM across an item's tiles; the epilogue scales, undoes
-// the rotation and writes bf16 rows.  Everything a compute thread needs besides TMEM
-// comes through shared memory with the tiles: the planner's records of the item's tile
-// and the streamed tiles (times, type bitmaps) and the rows' constants -lse * log2(e)
-// and -D, stored for row pairs as {-lse2(2k), -lse2(2k+1), -D(2k), -D(2k+1)} so that a
-// pair of query columns takes one f32x2 operation (k_bwd_rowc, tile-padded so that a
-// bulk copy moves a tile's 128 rows), and the item descriptors (k_bwd_schedule, once
-// per plan) come from the producer.  PARTIAL tiles take the forward's per-row
-// visibility bits (row_mask.cuh), built from the key tile's planner record; in DKV
-// each thread first acts as a row of the query tile, builds that row's bits against
-// the item's key tile, and the warps transpose the bits into per-key columns with
-// shuffles.  PARTIAL pairs with a slot in the plan's mask table skip both: DQ reads the
-// table's rows, DKV its columns (transposed once per plan by k_bwd_colmask), bulk-copied
-// with the streamed tile.  FULL tiles skip the mask.  The MMAs of one thread run in issue order, so
-// an MMA that overwrites TMEM columns an earlier MMA reads needs no wait.  Every
-// mbarrier wait is bounded (REC_ATTN_ERR_TIMEOUT in the status word).
+// Both modes share one persistent kernel shape: one CTA per SM with all 512 TMEM columns and 19
+// warps.  Warp 0 loads with TMA; warps 1 and 2 issue the MMAs; sixteen compute warps (four
+// warpgroups) hold one tile row per thread (its TMEM lane) and 32 of a step's 128 columns each.
+// The producer claims the planner's (tile, head) items from a global counter and publishes each
+// item's descriptor in shared memory for the other roles; mode DKV visits key tiles in the mirrored
+// order of the query tiles, so under causal masks both modes start with their heaviest items.  Per
+// item the resident operand pair stays in shared memory (DQ: Q', dO; DKV: K', V) and the streamed
+// pair (DQ: K', V of the query tile's non-SKIP key tiles; DKV: Q', dO of the query tiles whose class
+// against the key tile is not SKIP) runs through two rings.  A step is a whole streamed tile:
+//   DQ   S = Q' K'^T - lse / scale, dP = dO V^T - D; the compute warps write dS (bf16) over the
+//        first half of the 32 columns of S that each has read; dQ += dS K' with dS read from TMEM.
+//   DKV  S^T = K' Q'^T - lse / scale, dP^T = V dO^T - D; P^T over the first half of S's columns,
+//        dS^T over the second; dV += P^T dO, dK += dS^T Q'.  (head_dim 128: dS^T over dP^T.)
+// The queries' constants enter as one more K step of 16 (constants x ones in DQ, ones x constants in
+// DKV), each split into three bf16 that add up to its 24 bits: the compute warps then take P =
+// exp2(scale log2(e) S) and dS = P dP from the products as they are.  In DKV, where the queries are
+// the columns, reading the constants from shared memory instead cost more of its bandwidth than the
+// scores' operands.
+// TMEM columns:  head_dim 64   S[0] 0..127 | S[1] 128..255 | dP 256..383 | dQ or dV 384.. | dK 448..
+//                head_dim 128  S[0] 0..127 | dP 128..255 | dQ or dV 256.. | DQ: S[1], DKV: dK 384..
+// With two buffers of S the next step's scores are issued during this step's compute: S when the
+// accumulation of the step before last has read its operands, dP when the compute warps have loaded
+// this step's; and warp 1 issues the scores while warp 2 issues the accumulation (one warp for both
+// spent 700 of a step's 2400 cycles in waits for what was already there).  With one buffer (DKV at
+// head_dim 128) warp 1 issues everything in turns: S behind dV, dP behind dK, each pair running under
+// the compute of the other.
+// What bounds it: a step's products take 1370 (DKV) and 1010 (DQ) tensor cycles at head_dim 64, 2200
+// and 1680 at 128, its exponentials 512 of the special-function unit; a step takes 1980, 1610, 3500
+// and 2750, the difference being the chain score - exponential - operand - sum between barriers, of
+// which one step (two with two S) is under way.  Sixteen ragged requests of 603 to 1850 tokens,
+// head_dim 128, 8 query and 2 key/value heads: dQ 133 us, dK/dV 174 us (two 64-column steps at a time
+// with two compute warpgroups: 170 and 231); two causal ones of 8192 and 7000 tokens, head_dim 64, 8
+// and 1 heads: 164 and 213 us (two such CTAs per SM: 470 in all).  Also slower there: 64-column steps
+// of two groups of eight warps in turn (307 and 385).
+// The accumulators stay in TMEM across an item's tiles; the epilogue scales, undoes the rotation and
+// writes bf16 rows.  The rest a compute thread needs comes through shared memory with the tiles: the
+// planner's record of the item's tile and the masks.  FULL tiles take no mask.  PARTIAL pairs
+// with a slot in the plan's mask table read its rows (DQ) or columns (DKV; transposed once per plan by
+// k_bwd_colmask), bulk-copied with the streamed tile; others the forward's per-row visibility bits
+// (row_mask.cuh), built from the key tile's record, in DKV by threads that act as rows of the
+// query tile, whose warps transpose the bits into per-key columns with shuffles.  The MMAs of one
+// thread run in issue order, so an MMA that overwrites TMEM columns an earlier MMA of it reads needs
+// no wait.  Every mbarrier wait is bounded (REC_ATTN_ERR_TIMEOUT in the status word).
 #include <cuda_bf16.h>
 
 #include "attn_common.cuh"
@@ -992,33 +994,37 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
 }
 
 // ------------------------------------------------------------------ row constants
-// Block = (tile g, head h): D_i = <dO_i, O_i> for the tile's 128 rows, eight threads per
-// row (16 bytes of dO and O each, coalesced).  The row's constants as an operand row of the scores'
+// Block = (tile g, head h, half): D_i = <dO_i, O_i> for 64 rows of the tile, 16 bytes of dO and O a
+// thread, every row's loads in flight at once (row by row the kernel took 23 us where it takes 18: 16 ragged requests,
+// head_dim 128).  The row's constants as an operand row of the scores'
 // extra K step: -lse / scale (in the scores' unit) and -D, each as three bf16 that add up to it, and
 // -1e38 in place of the first for rows that see no key, rows past the request's end and pruned
 // rows, so that their every P is exp2(-1e38) = 0 whatever mask bits they have.
 template <int D>
 __global__ void __launch_bounds__(256) k_bwd_rowc(BwdArgs a) {
   constexpr int kLanes = D / 8;  // 16-byte chunks of a row, one per thread
-  const long long g = blockIdx.x;
-  const int h = blockIdx.y, H = a.heads;
+  constexpr int kRows = kTile / 2;  // per block
+  const int H = a.heads, h = (int)((blockIdx.x >> 1) % H);
+  const long long g = (blockIdx.x >> 1) / H;
   const int b = a.qreq[g];
   const ReqMeta m = a.meta[b];
   const int tile = (int)(g - m.tile_start);
   const int sub = threadIdx.x & (kLanes - 1);
   const int keep = a.qkeep[b];
-#pragma unroll 1
-  for (int r = threadIdx.x / kLanes; r < kTile; r += 256 / kLanes) {
+#pragma unroll
+  for (int r0 = 0; r0 < kRows; r0 += 256 / kLanes) {
+    const int r = (int)(blockIdx.x & 1) * kRows + r0 + (int)threadIdx.x / kLanes;
     const int p = tile * kTile + r;
     const bool in = p < m.len;
+    const long long tok = m.tok_start + (in ? p : 0), row = tok * H + h;
+    const uint4 x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + row * D)[sub];
+    const uint4 y = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + row * D)[sub];
+    const float lse = a.lse[row];
     // a pruned query (a query-pruned plan) has no output, so no gradient flows from it;
     // its forward lse and O were never written
-    const bool ok = in && query_kept(a.ty[m.tok_start + p], p, keep);
-    const long long row = (m.tok_start + p) * H + h;
+    const bool ok = in && query_kept(a.ty[tok], p, keep);
     float acc = 0.f;
     if (ok) {
-      const uint4 x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + row * D)[sub];
-      const uint4 y = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + row * D)[sub];
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -1030,7 +1036,7 @@ __global__ void __launch_bounds__(256) k_bwd_rowc(BwdArgs a) {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     if (sub == 0) {
-      const float l = ok ? a.lse[row] : INFINITY;
+      const float l = ok ? lse : INFINITY;
       const float c[2] = {isinf(l) ? -1e38f : -l / a.scale, -acc};
       uint32_t w[4];
 #pragma unroll
@@ -1308,7 +1314,7 @@ cudaError_t launch_mode(const CUtensorMap (&maps)[4], const BwdArgs& a, int grid
 
 template <int D>
 cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num_sms, cudaStream_t st) {
-  k_bwd_rowc<D><<<dim3((unsigned)a.n_tiles, (unsigned)a.heads), 256, 0, st>>>(a);
+  k_bwd_rowc<D><<<(unsigned)(2 * a.n_tiles * a.heads), 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long cap = num_sms;
