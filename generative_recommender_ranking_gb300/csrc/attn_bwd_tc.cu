@@ -1332,7 +1332,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
 int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int head_dim, int num_sms) {
   const long long slots = num_sms;
   int parts = 1;
-  while (parts < group && n_tiles * kv_heads * parts < 3 * slots) {
+  while (parts < group && n_tiles * kv_heads * parts < 2 * slots) {
     ++parts;
     while (group % parts) ++parts;
   }
