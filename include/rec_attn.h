@@ -172,7 +172,8 @@ rec_attn_status rec_attn_plan_query_pruned(const rec_attn_params* params, int32_
  * for num_kv_heads that does not divide num_heads.  The planning reads host memory of this
  * call and the plan's calls wait for it, so neither may be captured into a CUDA graph:
  * rec_attn_plan_grouped on a capturing stream, and the forward and backward calls on its
- * plan there, return UNSUPPORTED and leave the capture valid.
+ * plan there, return UNSUPPORTED and leave the capture valid.  The calls of one plan share
+ * its workspace (as for rec_attn_plan): order them on one stream, or with events.
  */
 rec_attn_status rec_attn_plan_grouped(const rec_attn_params* params, int32_t num_kv_heads,
                                       int32_t keep_user_queries, int32_t batch,

@@ -266,3 +266,48 @@ def test_layernorm_takes_tensors_of_the_current_device_only():
         with pytest.raises(bd.RecAttnError) as e:
             bd.rec_attn_layernorm_fwd(*bad)
         assert e.value.code == bd.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name,lens,H,Hk,d", [
+    ("parts", [5000], 4, 1, 64), ("whole_groups", list(range(4200, 4700, 50)), 4, 1, 64), ("d128", [4500, 4224], 4, 2, 128),
+    ("edges", [4096, 4097, 4223], 2, 1, 64)])
+def test_items_of_many_tiles(name, lens, H, Hk, d):
+    """Causal rows of more than 32 tiles, alone and with the heads of a group in one item, against
+    64 bits: gradients to 1e-2 relative Frobenius and 2e-2 of the largest value (the bounds of the
+    ungrouped gradients), the output to 2e-2 and 2e-3 on average."""
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    T, G = int(off[-1]), H // Hk
+    g = torch.Generator(device="cuda").manual_seed(7)
+    new = lambda h: torch.randn(T, h, d, generator=g, device="cuda").bfloat16()
+    q, k, v, do = new(H), new(Hk), new(Hk), new(H)
+    t = torch.arange(T, device="cuda") * 60
+    ty = torch.full((T,), W.HIST, dtype=torch.int8, device="cuda")
+    o, dq, dk, dv = (torch.full_like(x, float("nan")) for x in (q, q, k, v))
+    lse = torch.empty(T, H, device="cuda")
+    with bd.rec_attn_plan_grouped(bd.make_params(H, d, use_rope=False), Hk, off, torch.from_numpy(off).cuda(), t, ty) as plan:
+        bd.rec_attn_fwd(plan, q, k, v, o, lse)
+        bd.rec_attn_bwd(plan, q, k, v, o, lse, do, dq, dk, dv)
+        torch.cuda.synchronize()
+        assert bd.rec_attn_device_status(plan) == bd.OK
+    ref = [torch.empty(x.shape, dtype=torch.float64, device="cuda") for x in (o, dq, dk, dv)]
+    for b in range(len(lens)):
+        r = slice(int(off[b]), int(off[b + 1]))
+        blind = torch.ones(lens[b], lens[b], dtype=torch.bool, device="cuda").triu(1)
+        for hk in range(Hk):
+            K, V = k[r, hk].double(), v[r, hk].double()
+            sums = [torch.zeros_like(K), torch.zeros_like(V)]
+            for h in range(hk * G, (hk + 1) * G):
+                Q, dO = q[r, h].double(), do[r, h].double()
+                P = torch.softmax((Q @ K.t() * d ** -0.5).masked_fill(blind, -float("inf")), 1)
+                O = P @ V
+                dS = P * (dO @ V.t() - (dO * O).sum(1, keepdim=True)) * d ** -0.5
+                ref[0][r, h], ref[1][r, h] = O, dS @ K
+                sums[0] += dS.t() @ Q
+                sums[1] += P.t() @ dO
+            ref[2][r, hk], ref[3][r, hk] = sums
+    err = (o.double() - ref[0]).abs()
+    assert err.max() <= gu.BF16_MAX_ABS and err.mean() <= gu.BF16_MEAN_ABS
+    for what, got, want in zip(("dq", "dk", "dv"), (dq, dk, dv), ref[1:]):
+        diff = got.double() - want
+        rel, top = float(diff.norm() / want.norm()), float(diff.abs().max() / want.abs().max())
+        assert rel <= 1e-2 and top <= 2e-2, (what, rel, top)
