@@ -27,7 +27,7 @@
 //
 // Many rows (score_many in api.cu has both kernels' measured cost): k_score_pack lays Q' out in row
 // order and k_attn_tc's CAND instantiation takes items of 128 rows.  16 requests of 3500 to 4096
-// keys, 420 to 500 candidates, head_dim 64: 12 + 107 us (540 TFLOP/s); bound by the softmax of its 1.6
+// keys, 420 to 500 candidates, head_dim 64: 8 + 107 us (540 TFLOP/s); bound by the softmax of its 1.6
 // items a stream.
 #include <climits>
 
@@ -459,8 +459,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 // 128 rows of Q' (rotated against the request's reference time, rounded to bf16; rows past
 // the request's last are zero) packed in row order, its descriptor, and (block 0) the item
 // counters.
+// A candidate's angles serve all heads of the group (computed for every row the kernel took 12 us on 476
+// items of head_dim 64, 8 now).
+constexpr int kPackThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(128) k_score_pack(const __grid_constant__ ScoreArgs a, CandItem* items,
+__global__ void __launch_bounds__(kPackThreads) k_score_pack(const __grid_constant__ ScoreArgs a, CandItem* items,
                                                     __nv_bfloat16* qp, int* counters) {
   const int x = blockIdx.x, i = upper_index(a.item_start, a.n_req, x), b = a.req0 + i;
   const int G = a.heads / a.kv_heads, tiles = request_tiles(a, b), nsplit = n_splits(a, tiles);
@@ -468,32 +471,37 @@ __global__ void __launch_bounds__(128) k_score_pack(const __grid_constant__ Scor
   const int row0 = local / nsplit / a.kv_heads * kTile;
   const int rows = min(kTile, (a.cand_start[i + 1] - a.cand_start[i]) * G - row0);
   const long long cand0 = a.cand_start[i], t_ref = a.t_ref[b];
-  constexpr int kChunks = D / 8;
+  constexpr int kChunks = D / 8;  // 16-byte pieces of a row, one per thread
   const int c = threadIdx.x % kChunks;
   long long t_lo = LLONG_MAX;
-  for (int r = threadIdx.x / kChunks; r < kTile; r += 128 / kChunks) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const long long cand = cand0 + (row0 + r) / G, t = a.tc[cand];
-      t_lo = min(t_lo, t);
-      w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                          (cand * a.heads + hk * G + (row0 + r) % G) * D + c * 8);
+  const int c0 = row0 / G, c1 = rows > 0 ? (row0 + rows - 1) / G + 1 : c0;  // candidates with rows here
+  for (int k = c0 + (int)threadIdx.x / kChunks; k < c1; k += kPackThreads / kChunks) {
+    const long long cand = cand0 + k, t = a.tc[cand];
+    t_lo = min(t_lo, t);
+    float sn[4], cs[4];
+    if (a.rotate) {
+      const float dt = (float)(t - t_ref);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) sincosf(dt * a.omega[c * 4 + p], &sn[p], &cs[p]);
+    }
+    for (int g = max(0, row0 - k * G); g < min(G, row0 + rows - k * G); ++g) {
+      uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                (cand * a.heads + hk * G + g) * D + c * 8);
       if (a.rotate) {
-        const float dt = (float)(t - t_ref);
         uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float2 f = bf16x2_float(ws[p]);
-          float sn, cs;
-          sincosf(dt * a.omega[c * 4 + p], &sn, &cs);
-          ws[p] = bf16_pair(f.x * cs - f.y * sn, f.x * sn + f.y * cs);
+          ws[p] = bf16_pair(f.x * cs[p] - f.y * sn[p], f.x * sn[p] + f.y * cs[p]);
         }
         w = make_uint4(ws[0], ws[1], ws[2], ws[3]);
       }
+      *reinterpret_cast<uint4*>(qp + ((long long)x * kTile + k * G + g - row0) * D + c * 8) = w;
     }
-    *reinterpret_cast<uint4*>(qp + ((long long)x * kTile + r) * D + c * 8) = w;
   }
-  __shared__ long long s_lo[4];
+  for (int r = rows + (int)threadIdx.x / kChunks; r < kTile; r += kPackThreads / kChunks)
+    *reinterpret_cast<uint4*>(qp + ((long long)x * kTile + r) * D + c * 8) = make_uint4(0, 0, 0, 0);
+  __shared__ long long s_lo[kPackThreads / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const long long u = __shfl_xor_sync(0xffffffffu, t_lo, o);
@@ -505,7 +513,8 @@ __global__ void __launch_bounds__(128) k_score_pack(const __grid_constant__ Scor
     CandItem it;
     it.hist0 = a.hist_off[b];
     it.cand0 = cand0;
-    it.t_lo = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
+    it.t_lo = s_lo[0];
+    for (int i = 1; i < kPackThreads / 32; ++i) it.t_lo = min(it.t_lo, s_lo[i]);
     it.len = a.hist_len[b];
     it.row0 = row0;
     it.rows = rows;
@@ -644,8 +653,8 @@ cudaError_t launch_combine(const ScoreArgs& a, int rows_per_item, cudaStream_t s
 cudaError_t launch_score_pack(const ScoreArgs& a, int head_dim, int items, CandItem* desc, void* qp, int* counters,
                               cudaStream_t st) {
   __nv_bfloat16* q = static_cast<__nv_bfloat16*>(qp);
-  if (head_dim == 64) k_score_pack<64><<<items, 128, 0, st>>>(a, desc, q, counters);
-  else k_score_pack<128><<<items, 128, 0, st>>>(a, desc, q, counters);
+  if (head_dim == 64) k_score_pack<64><<<items, kPackThreads, 0, st>>>(a, desc, q, counters);
+  else k_score_pack<128><<<items, kPackThreads, 0, st>>>(a, desc, q, counters);
   return cudaGetLastError();
 }
 
