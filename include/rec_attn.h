@@ -269,14 +269,16 @@ rec_attn_status rec_attn_fwd_fused(rec_attn_plan_t* plan, const void* q, const v
  * The plan must be the forward's (same offsets, times, types, params).  On a
  * query-pruned plan (rec_attn_plan_query_pruned) the gradients are those of the
  * computed rows' outputs: pruned queries have no output, so their out and lse rows
- * are never read, their dout rows are ignored (they must still be finite: they pass
+ * have no effect, their dout rows are ignored (they must still be finite: they pass
  * through the tensor cores with zero weights), their dq rows are zero and they add
  * nothing to dk and dv.
  * Supported: bf16 with head_dim 64 or 128, fp32 with
  * head_dim 32 or 64 (else UNSUPPORTED).  The first call takes workspace from the
  * library pool on `stream` (released with the plan): for bf16 the per-plan item
  * schedule (96 B per tile and head, 4 B per tile pair) and the rows' constants
- * (8 B per tile row and head); for fp32 T * H floats.  bf16: tensor cores (bf16
+ * (16 B per tile row and head); for fp32 T * H floats.  On a plan of shared heads with few
+ * tiles (bf16) each call also takes fp32 parts of dK and dV, 8 * d bytes per token, key/value
+ * head and part (up to H / Hk of them), from the pool.  bf16: tensor cores (bf16
  * operands, fp32 accumulation; P and dS rounded to bf16 for their MMAs, as in the
  * forward's P); fp32: CUDA cores in fp32.  Gradients are rounded once to
  * params->dtype.
