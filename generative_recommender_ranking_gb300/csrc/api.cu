@@ -605,7 +605,8 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   if (T == 0) return REC_ATTN_OK;
   const bool tc = p.dtype == REC_ATTN_BF16;
   const int group = p.num_heads / plan->kv_heads;
-  const int parts = tc ? bwd_kv_parts(plan->NT, plan->kv_heads, group, p.head_dim, plan->num_sms) : 1;
+  // (fp32 items are half tiles)
+  const int parts = bwd_kv_parts(tc ? plan->NT : 2 * plan->NT, plan->kv_heads, group, plan->num_sms);
   const int reps = group / parts;  // query heads of a dK/dV item
   const long long n_items = plan->NT * p.num_heads, n_kv_items = plan->NT * plan->kv_heads * parts;
   // bf16 workspace: descriptors [n_items], [n_kv_items] | row constants [H][NT][128] | lists [NC] |
@@ -662,7 +663,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   a.desc = tc ? reinterpret_cast<const BwdItemDesc*>(bws) : nullptr;
   a.rowx = tc ? reinterpret_cast<uint4*>(bws + off_rowx) : nullptr;
   a.qlist = tc ? reinterpret_cast<const uint32_t*>(bws + off_ql) : nullptr;
-  a.kslot = plan->pd.kslot; a.mtab = plan->pd.mtab;
+  a.kslot = plan->pd.kslot; a.mtab = plan->pd.mtab; a.pslot = plan->pd.pslot; a.mcap = plan->pd.mcap;
   a.qslot = tc ? reinterpret_cast<const int*>(bws + off_qs) : nullptr;
   a.ctab = tc ? reinterpret_cast<const uint32_t*>(bws + off_ct) : nullptr;
   a.dq = dq; a.dk = dk; a.dv = dv;
@@ -670,10 +671,25 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   a.kv_part = nullptr; a.scale = p.softmax_scale;
   a.rotate = p.use_rope; a.mask = plan->mask;
   std::memcpy(a.omega, plan->omega, sizeof a.omega);
+  // fp32 parts of dK and dV, for this call
+  auto take_parts = [&]() -> cudaError_t {
+    if (parts == 1) return cudaSuccess;
+    cudaMemPool_t pool;
+    const cudaError_t ep = pool_for(plan->device, &pool);
+    if (ep != cudaSuccess) return ep;
+    return cudaMallocFromPoolAsync(reinterpret_cast<void**>(&a.kv_part),
+                                   (size_t)2 * plan->kv_heads * parts * T * p.head_dim * sizeof(float), pool, st);
+  };
+  auto return_parts = [&](cudaError_t el) -> cudaError_t {
+    if (!a.kv_part) return el;
+    const cudaError_t ef = cudaFreeAsync(a.kv_part, st);
+    return el != cudaSuccess ? el : ef;
+  };
   if (!tc) {
     e = launch_bwd_delta(a, p.dtype, p.head_dim, st);
+    if (e == cudaSuccess) e = take_parts();
     if (e != cudaSuccess) return from_cuda(e);
-    return from_cuda(launch_attn_bwd_simt(a, p.head_dim, plan->NT, st));
+    return from_cuda(return_parts(launch_attn_bwd_simt(a, p.head_dim, plan->NT, st)));
   }
   if (!plan->bwd_sched) {  // the plan's masks never change: its backward schedule is built once
     BwdSchedArgs sa;
@@ -694,20 +710,9 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   const int map_heads[4] = {p.num_heads, plan->kv_heads, plan->kv_heads, p.num_heads};
   for (int i = 0; i < 4; ++i)
     if (!encode_map(&maps[i], srcs[i], T, (long long)map_heads[i] * p.head_dim)) return REC_ATTN_ERR_CUDA;
-  if (parts > 1) {  // fp32 parts of dK and dV, for this call
-    cudaMemPool_t pool;
-    e = pool_for(plan->device, &pool);
-    if (e == cudaSuccess)
-      e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&a.kv_part),
-                                  (size_t)2 * plan->kv_heads * parts * T * p.head_dim * sizeof(float), pool, st);
-    if (e != cudaSuccess) return from_cuda(e);
-  }
-  e = launch_attn_bwd_tc(a, maps, p.head_dim, plan->num_sms, st);
-  if (a.kv_part) {
-    const cudaError_t ef = cudaFreeAsync(a.kv_part, st);
-    if (e == cudaSuccess) e = ef;
-  }
-  return from_cuda(e);
+  e = take_parts();
+  if (e != cudaSuccess) return from_cuda(e);
+  return from_cuda(return_parts(launch_attn_bwd_tc(a, maps, p.head_dim, plan->num_sms, st)));
 }
 
 }  // namespace

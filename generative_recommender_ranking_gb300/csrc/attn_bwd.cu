@@ -10,20 +10,23 @@
 //   dS_ij = P_ij (dP_ij - D_i),  dQ'_i = scale sum_j dS_ij K'_j,  dK'_j = scale sum_i dS_ij Q'_i,
 // and dQ = R(t_i)^T dQ', dK = R(t_j)^T dK' (the rotation is orthogonal).
 //
-// Three kernels walk the planner's tile lists, so SKIP tiles cost nothing here either:
-//   k_bwd_delta  D_i per (token, head), fp32 or bf16 rows;
-//   k_bwd_dq     one block per (query tile, head), d/32 threads per query row, over the
-//                query tile's non-SKIP key tiles (K', V and key metadata staged in
-//                shared memory);
-//   k_bwd_dkv    one block per (key tile, head), d/32 threads per key row, over the
-//                query tiles whose class against this key tile is not SKIP (Q', dO,
-//                lse, D and query metadata staged in shared memory).
-// FULL tiles skip the per-pair mask predicate.  Rows with no visible key (lse = -inf)
-// contribute nothing.
+// Kernels over the planner's tile lists, so SKIP tiles cost nothing here either; the products are of
+// 64 x 64 tiles in registers (simt_tile.cuh):
+//   k_bwd_delta   D_i per (token, head), fp32 or bf16 rows;
+//   k_bwd_dq      a block per (half query tile, head), over the query tile's non-SKIP key tiles;
+//   k_bwd_dkv     a block per (half key tile, key/value head or part of its query heads), over the
+//                 query tiles whose class against this key tile is not SKIP;
+//   k_bwd_kv_add  with parts: their sums, in order.
+// FULL tiles skip the mask; PARTIAL tiles take the plan's mask table, or without a slot evaluate it.  Rows with no visible key (lse = -inf)
+// contribute nothing.  Bound by the fp32 units and the shared memory that feeds them (k_bwd_dkv at
+// head_dim 64: one block per SM).  Forward and backward of 16 causal requests of 400 to 700 tokens,
+// 8 query and 2 key/value heads, head_dim 64: 1325 us (a thread per row: 2306); of one request of 700
+// tokens, 8 and 1 heads: 336 us (2742, whose dK/dV had six blocks).
 #include <cuda_bf16.h>
 
 #include "attn_common.cuh"
 #include "launchers.cuh"
+#include "simt_tile.cuh"
 
 namespace recattn {
 
@@ -39,53 +42,6 @@ template <>
 __device__ __forceinline__ float ld_elem<__nv_bfloat16>(const void* base, long long i) {
   return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
 }
-template <typename E>
-__device__ __forceinline__ void st_elem(void* base, long long i, float x);
-template <>
-__device__ __forceinline__ void st_elem<float>(void* base, long long i, float x) {
-  static_cast<float*>(base)[i] = x;
-}
-
-// Each row (query or key) is handled by kSplit = D / 32 neighbouring threads; part p
-// of a row holds its 32 contiguous dims [32 p, 32 p + 32), so a thread reads its share
-// of a staged row with 16-byte shared-memory loads (all threads of a part read the same
-// address: a broadcast), a rotation pair never straddles two threads, and dot products
-// need log2(kSplit) shuffles.
-template <int D>
-struct Split {
-  static constexpr int kSplit = D / 32;
-  static constexpr int kThreads = kTile * kSplit;
-};
-
-template <int S>
-__device__ __forceinline__ float part_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < S; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// y <- R(t)^T y over adjacent pairs (the inverse of the prologue's rotation), on the
-// 32 dims [32 part, 32 part + 32) this thread holds: pairs 16 part .. 16 part + 15.
-__device__ __forceinline__ void rotate_back(float (&y)[32], int part, float dt, const float* omega) {
-#pragma unroll
-  for (int p = 0; p < 16; ++p) {
-    float sn, cs;
-    sincosf(dt * omega[16 * part + p], &sn, &cs);
-    const float u = y[2 * p], w = y[2 * p + 1];
-    y[2 * p] = u * cs + w * sn;
-    y[2 * p + 1] = -u * sn + w * cs;
-  }
-}
-
-// 32 contiguous floats of a staged shared-memory row, as eight 16-byte loads.
-__device__ __forceinline__ void lds32(const float* p, float (&x)[32]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float4 v = reinterpret_cast<const float4*>(p)[i];
-    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-  }
-}
-
 // The request of global tile g (binary search over the request table).
 __device__ __forceinline__ int tile_request(const ReqMeta* meta, int batch, long long g) {
   int lo = 0, hi = batch;
@@ -95,6 +51,31 @@ __device__ __forceinline__ int tile_request(const ReqMeta* meta, int batch, long
     else hi = mid;
   }
   return lo;
+}
+
+// A thread's N = D / 16 gradient columns of one row, turned back by dt (R(t)^T y over adjacent
+// pairs, the inverse of the prologue's rotation), to global memory.
+template <int D>
+__device__ __forceinline__ void store_grad(float* dst, float (&y)[D / 16], bool rotate, float dt, const float* omega) {
+#pragma unroll
+  for (int p = 0; p < D / 32; ++p) {
+    if (rotate) {
+      float sn, cs;
+      sincosf(dt * omega[p], &sn, &cs);
+      const float u = y[2 * p], w = y[2 * p + 1];
+      y[2 * p] = u * cs + w * sn;
+      y[2 * p + 1] = -u * sn + w * cs;
+    }
+    *reinterpret_cast<float2*>(dst + 2 * p) = make_float2(y[2 * p], y[2 * p + 1]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void row_of(const simt::f2 (&o)[2][N], int i, float (&y)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float2 v = simt::both(o[i >> 1][c]);
+    y[c] = (i & 1) ? v.y : v.x;
+  }
 }
 
 template <typename E, int D>
@@ -108,186 +89,234 @@ __global__ void __launch_bounds__(128) k_bwd_delta(BwdArgs a) {
 }
 
 template <int D>
-struct BwdSmem {
-  // K', V (dQ kernel) or Q' * scale, dO (dK/dV kernel); rows padded to keep 16-byte alignment
-  __align__(16) float a[kTile][D + 4];
-  __align__(16) float b[kTile][D + 4];
-  long long t[kTile];
-  int ty[kTile];
-  float lse[kTile], dlt[kTile];
+struct DqSmem {
+  __align__(16) float q[D * simt::kB], go[D * simt::kB];   // transposed; q times the scale
+  __align__(16) float k[D * simt::kB], v[D * simt::kB];    // transposed
+  __align__(16) float kr[simt::kB * D];
+  __align__(16) float ds[simt::kB * simt::kB];
+  simt::Tokens tq, tk;
+};
+template <int D>
+struct DkvSmem {
+  __align__(16) float k[D * simt::kB], v[D * simt::kB];    // transposed
+  __align__(16) float q[D * simt::kB], go[D * simt::kB];   // transposed; q times the scale
+  __align__(16) float qr[simt::kB * D], gor[simt::kB * D];
+  __align__(16) float p[simt::kB * simt::kB], ds[simt::kB * simt::kB];
+  simt::Tokens tq, tk;
+  float lse[simt::kB], dlt[simt::kB];
 };
 
-// dQ: block = (query tile g, head h); kSplit threads per query row.
-template <typename E, int D>
-__global__ void __launch_bounds__(Split<D>::kThreads) k_bwd_dq(BwdArgs a) {
-  constexpr int S = Split<D>::kSplit;
+// dQ: block = (half of query tile g, head h); thread (ty, tx) has query rows 4 ty ...
+template <int D>
+__global__ void __launch_bounds__(simt::kThreads) k_bwd_dq(BwdArgs a) {
+  using namespace simt;
+  constexpr int N = D / 16;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
-  const long long g = blockIdx.x;
+  DqSmem<D>& sm = *reinterpret_cast<DqSmem<D>*>(smem_raw);
+  const long long x = gridDim.x - 1 - blockIdx.x;  // (under causal masks the heaviest first)
+  const long long g = x / kPerTile;
   const int h = blockIdx.y, H = a.heads, Hk = H / a.group, hk = h / a.group;
   const int b = tile_request(a.meta, a.batch, g);
   const ReqMeta m = a.meta[b];
-  const int qt = (int)(g - m.tile_start), r = threadIdx.x / S, part = threadIdx.x % S, pi = qt * kTile + r;
-  const bool row_ok = pi < m.len;
-  const long long tok = m.tok_start + pi, row = tok * H + h;
-  float q[32], go[32], acc[32];
-  long long ti = 0;
-  int tyi = -1;
-  float lse = -INFINITY, dlt = 0.f;
+  const int qt = (int)(g - m.tile_start), pos0 = qt * kTile + (int)(x % kPerTile) * kB;
+  if (pos0 >= m.len) return;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const long long tok0 = m.tok_start + pos0, q0 = (tok0 * H + h) * D;
+  load_tile<D>(static_cast<const float*>(a.q) + q0, (long long)H * D, m.len - pos0, a.scale, sm.q, nullptr);
+  load_tile<D>(static_cast<const float*>(a.dout_attn) + q0, (long long)H * D, m.len - pos0, 1.f, sm.go, nullptr);
+  sm.tq.load(a.t, a.ty, tok0, pos0, m.len, a.mask.delay);
+  float lse[4], dlt[4];
+  bool live[4];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) { q[e] = 0.f; go[e] = 0.f; acc[e] = 0.f; }
-  if (row_ok) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      q[e] = ld_elem<E>(a.q, row * D + 32 * part + e) * a.scale;
-      go[e] = ld_elem<E>(a.dout_attn, row * D + 32 * part + e);
-    }
-    ti = a.t[tok];
-    tyi = a.ty[tok];
-    if (query_kept(tyi, pi, a.qkeep[b])) {  // a pruned query has no output: no gradient
-      lse = a.lse[row];
-      dlt = a.delta[row];
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int pi = pos0 + 4 * ty + i;
+    const long long row = (tok0 + 4 * ty + i) * H + h;
+    // a pruned query has no output: no gradient
+    const bool kept = pi < m.len && query_kept(a.ty[tok0 + 4 * ty + i], pi, a.qkeep[b]);
+    lse[i] = kept ? a.lse[row] : -INFINITY;
+    dlt[i] = kept ? a.delta[row] : 0.f;
+    live[i] = lse[i] != -INFINITY;
   }
-  const bool live = row_ok && lse != -INFINITY;
-  bool thr_ok; long long thr;
-  delay_bound(ti, a.mask.delay, thr_ok, thr);
+  f2 acc[2][N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) acc[0][c] = acc[1][c] = pair(0.f, 0.f);
   const int n = a.kcount[g];
   const uint32_t* list = a.klist + m.cls_start + (long long)qt * m.ntiles;
-  for (int j = 0; j < n; ++j) {
-    const uint32_t ent = list[j];
-    const int kt = (int)(ent & 0xffffffu), cl = (int)(ent >> 24);
+  const int* slots = a.kslot + m.cls_start + (long long)qt * m.ntiles;
+  for (int j = 0; j < n * kPerTile; ++j) {
+    const uint32_t ent = list[j / kPerTile];
+    const int key0 = (int)(ent & 0xffffffu) * kTile + j % kPerTile * kB;
+    const bool full = (int)(ent >> 24) == REC_ATTN_TILE_FULL;
+    const int slot = full ? -1 : slots[j / kPerTile];  // of the mask table
+    if (key0 >= m.len) continue;
+    const long long src = ((m.tok_start + key0) * Hk + hk) * D;
+    __syncthreads();  // the last step's operands were read
+    load_tile<D>(static_cast<const float*>(a.k) + src, (long long)Hk * D, m.len - key0, 1.f, sm.k, sm.kr);
+    load_tile<D>(static_cast<const float*>(a.v) + src, (long long)Hk * D, m.len - key0, 1.f, sm.v, nullptr);
+    if (!full && slot < 0) sm.tk.load(a.t, a.ty, m.tok_start + key0, key0, m.len, 0);
     __syncthreads();
-    for (int idx = threadIdx.x; idx < kTile * D; idx += blockDim.x) {
-      const int c = idx / D, e = idx - c * D;
-      const int pj = kt * kTile + c;
-      const bool ok = pj < m.len;
-      const long long src = ((m.tok_start + pj) * Hk + hk) * D + e;
-      sm.a[c][e] = ok ? ld_elem<E>(a.k, src) : 0.f;
-      sm.b[c][e] = ok ? ld_elem<E>(a.v, src) : 0.f;
-    }
-    for (int c = threadIdx.x; c < kTile; c += blockDim.x) {
-      const int pj = kt * kTile + c;
-      const bool ok = pj < m.len;
-      sm.t[c] = ok ? a.t[m.tok_start + pj] : 0;
-      sm.ty[c] = ok ? (int)a.ty[m.tok_start + pj] : -1;
-    }
-    __syncthreads();
-    // every part of a row takes the same branches, so the shuffles below see whole pairs
-    for (int c = 0; c < kTile; ++c) {
-      bool vis = live;
-      if (vis && cl != REC_ATTN_TILE_FULL)
-        vis = vis_pred(a.mask, pi, ti, tyi, thr_ok, thr, kt * kTile + c, sm.t[c], sm.ty[c]);
-      float kc[32], vc[32];
-      lds32(&sm.a[c][32 * part], kc);
-      lds32(&sm.b[c][32 * part], vc);
-      float s = 0.f, dp = 0.f;
+    f2 s[2][4], dp[2][4];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        s = fmaf(q[e], kc[e], s);
-        dp = fmaf(go[e], vc[e], dp);
+    for (int c = 0; c < 4; ++c) s[0][c] = s[1][c] = dp[0][c] = dp[1][c] = pair(0.f, 0.f);
+    scores<D>(sm.q, sm.k, ty, tx, s);
+    scores<D>(sm.go, sm.v, ty, tx, dp);
+    float x4[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float si[4], di[4];
+      row_of<4>(s, i, si);
+      row_of<4>(dp, i, di);
+      const uint32_t bits = slot >= 0 ? table_bits(a.mtab, slot, pos0 % kTile + 4 * ty + i, (key0 % kTile >> 2) + tx) : 15u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool vis = live[i] && (bits >> c & 1u) &&
+                         (full || slot >= 0 || visible(a.mask, sm.tq, 4 * ty + i, sm.tk, 4 * tx + c));
+        x4[i][c] = vis ? __expf(si[c] - lse[i]) * (di[c] - dlt[i]) * a.scale : 0.f;
       }
-      s = part_sum<S>(s);
-      dp = part_sum<S>(dp);
-      const float ds = vis ? __expf(s - lse) * (dp - dlt) * a.scale : 0.f;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) acc[e] = fmaf(ds, kc[e], acc[e]);
     }
+    store_scores(sm.ds, ty, tx, x4);
+    __syncthreads();
+    accumulate<D>(sm.ds, sm.kr, ty, tx, acc);
   }
-  if (!row_ok) return;
-  if (a.rotate) rotate_back(acc, part, (float)(ti - a.t[m.tok_start]), a.omega);
 #pragma unroll
-  for (int e = 0; e < 32; ++e) st_elem<E>(a.dq, row * D + 32 * part + e, acc[e]);
+  for (int i = 0; i < 4; ++i) {
+    const int pi = pos0 + 4 * ty + i;
+    if (pi >= m.len) break;
+    float y[N];
+    row_of<N>(acc, i, y);
+    store_grad<D>(static_cast<float*>(a.dq) + q0 + (long long)(4 * ty + i) * H * D + N * tx, y, a.rotate != 0,
+                  (float)(a.t[m.tok_start + pi] - a.t[m.tok_start]), a.omega + N / 2 * tx);
+  }
 }
 
-// dK, dV: block = (key tile g, key/value head); kSplit threads per key row, the group's
-// query heads one after the other.
-template <typename E, int D>
-__global__ void __launch_bounds__(Split<D>::kThreads) k_bwd_dkv(BwdArgs a) {
-  constexpr int S = Split<D>::kSplit;
+// dK, dV: block = (half of key tile g, key/value head and part of its query heads); thread (ty, tx)
+// has key rows 4 ty ...  The part's query heads one after the other.
+template <int D>
+__global__ void __launch_bounds__(simt::kThreads) k_bwd_dkv(BwdArgs a) {
+  using namespace simt;
+  constexpr int N = D / 16;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(smem_raw);
-  const long long g = blockIdx.x;
-  const int hk = blockIdx.y, H = a.heads, Hk = H / a.group;
+  DkvSmem<D>& sm = *reinterpret_cast<DkvSmem<D>*>(smem_raw);
+  const long long g = blockIdx.x / kPerTile;
+  const int H = a.heads, Hk = H / a.group, reps = a.group / a.parts, hk = (int)blockIdx.y / a.parts;
   const int b = tile_request(a.meta, a.batch, g);
   const ReqMeta m = a.meta[b];
-  const int kt = (int)(g - m.tile_start), r = threadIdx.x / S, part = threadIdx.x % S, pj = kt * kTile + r;
-  const bool row_ok = pj < m.len;
-  const long long tok = m.tok_start + pj, row = tok * Hk + hk;
-  float k[32], v[32], dk[32], dv[32];
-  long long tj = 0;
-  int tyj = -1;
+  const int kt = (int)(g - m.tile_start), pos0 = kt * kTile + (int)(blockIdx.x % kPerTile) * kB;
+  if (pos0 >= m.len) return;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const long long tok0 = m.tok_start + pos0, k0 = (tok0 * Hk + hk) * D;
+  load_tile<D>(static_cast<const float*>(a.k) + k0, (long long)Hk * D, m.len - pos0, 1.f, sm.k, nullptr);
+  load_tile<D>(static_cast<const float*>(a.v) + k0, (long long)Hk * D, m.len - pos0, 1.f, sm.v, nullptr);
+  sm.tk.load(a.t, a.ty, tok0, pos0, m.len, 0);
+  f2 dk[2][N], dv[2][N];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) { k[e] = 0.f; v[e] = 0.f; dk[e] = 0.f; dv[e] = 0.f; }
-  if (row_ok) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      k[e] = ld_elem<E>(a.k, row * D + 32 * part + e);
-      v[e] = ld_elem<E>(a.v, row * D + 32 * part + e);
-    }
-    tj = a.t[tok];
-    tyj = a.ty[tok];
-  }
+  for (int c = 0; c < N; ++c) dk[0][c] = dk[1][c] = dv[0][c] = dv[1][c] = pair(0.f, 0.f);
   const uint8_t* col = a.cls + m.cls_start + kt;  // column kt of the request's class matrix
-  for (int it = 0; it < a.group * m.ntiles; ++it) {
-    const int h = hk * a.group + it / m.ntiles, qt = it % m.ntiles;
+  for (int it = 0; it < reps * m.ntiles * kPerTile; ++it) {
+    const int h = (int)blockIdx.y * reps + it / (m.ntiles * kPerTile), half = it % (m.ntiles * kPerTile);
+    const int qt = half / kPerTile, query0 = half * kB;
     const int cl = col[(long long)qt * m.ntiles];
-    if (cl == REC_ATTN_TILE_SKIP) continue;
-    __syncthreads();
-    for (int idx = threadIdx.x; idx < kTile * D; idx += blockDim.x) {
-      const int c = idx / D, e = idx - c * D;
-      const int pi = qt * kTile + c;
-      const bool ok = pi < m.len;
-      const long long src = ((m.tok_start + pi) * H + h) * D + e;
-      sm.a[c][e] = ok ? ld_elem<E>(a.q, src) * a.scale : 0.f;
-      sm.b[c][e] = ok ? ld_elem<E>(a.dout_attn, src) : 0.f;
-    }
-    for (int c = threadIdx.x; c < kTile; c += blockDim.x) {
-      const int pi = qt * kTile + c;
-      const bool ok = pi < m.len;
-      const long long qrow = (m.tok_start + pi) * H + h;
-      sm.t[c] = ok ? a.t[m.tok_start + pi] : 0;
-      sm.ty[c] = ok ? (int)a.ty[m.tok_start + pi] : -1;
-      const bool kept = ok && query_kept(sm.ty[c], pi, a.qkeep[b]);  // pruned queries give no gradient
-      sm.lse[c] = kept ? a.lse[qrow] : -INFINITY;
-      sm.dlt[c] = kept ? a.delta[qrow] : 0.f;
+    if (cl == REC_ATTN_TILE_SKIP || query0 >= m.len) continue;
+    const bool full = cl == REC_ATTN_TILE_FULL;
+    const int in_table = full ? -1 : a.pslot[m.cls_start + (long long)qt * m.ntiles + kt];
+    const int slot = in_table < a.mcap ? in_table : -1;  // of the mask table
+    const long long qtok = m.tok_start + query0, src = (qtok * H + h) * D;
+    __syncthreads();  // the last step's operands were read
+    load_tile<D>(static_cast<const float*>(a.q) + src, (long long)H * D, m.len - query0, a.scale, sm.q, sm.qr);
+    load_tile<D>(static_cast<const float*>(a.dout_attn) + src, (long long)H * D, m.len - query0, 1.f, sm.go, sm.gor);
+    if (!full && slot < 0) sm.tq.load(a.t, a.ty, qtok, query0, m.len, a.mask.delay);
+    for (int c = threadIdx.x; c < kB; c += kThreads) {
+      const int pi = query0 + c;
+      // pruned queries give no gradient, nor do queries that see no key
+      const bool kept = pi < m.len && query_kept(a.ty[qtok + c], pi, a.qkeep[b]);
+      sm.lse[c] = kept ? a.lse[(qtok + c) * H + h] : -INFINITY;
+      sm.dlt[c] = kept ? a.delta[(qtok + c) * H + h] : 0.f;
     }
     __syncthreads();
-    for (int c = 0; c < kTile; ++c) {
-      const float lse = sm.lse[c];
-      bool vis = row_ok && lse != -INFINITY;  // a query that sees no key contributes nothing
-      if (vis && cl != REC_ATTN_TILE_FULL) {
-        bool thr_ok; long long thr;
-        delay_bound(sm.t[c], a.mask.delay, thr_ok, thr);
-        vis = vis_pred(a.mask, qt * kTile + c, sm.t[c], sm.ty[c], thr_ok, thr, pj, tj, tyj);
-      }
-      float qc[32], gc[32];
-      lds32(&sm.a[c][32 * part], qc);
-      lds32(&sm.b[c][32 * part], gc);
-      float s = 0.f, dp = 0.f;
+    f2 s[2][4], dp[2][4];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        s = fmaf(qc[e], k[e], s);
-        dp = fmaf(gc[e], v[e], dp);
-      }
-      s = part_sum<S>(s);
-      dp = part_sum<S>(dp);
-      const float p = vis ? __expf(s - lse) : 0.f;
-      const float ds = p * (dp - sm.dlt[c]);  // sm.a already carries the scale
+    for (int c = 0; c < 4; ++c) s[0][c] = s[1][c] = dp[0][c] = dp[1][c] = pair(0.f, 0.f);
+    scores<D>(sm.k, sm.q, ty, tx, s);
+    scores<D>(sm.v, sm.go, ty, tx, dp);
+    float p[4][4], x[4][4];
+    uint32_t bits[4];  // of each query's keys
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        dv[e] = fmaf(p, gc[e], dv[e]);
-        dk[e] = fmaf(ds, qc[e], dk[e]);
+    for (int c = 0; c < 4; ++c)
+      bits[c] = slot >= 0 ? table_bits(a.mtab, slot, query0 % kTile + 4 * tx + c, (pos0 % kTile >> 2) + ty) : 15u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float si[4], di[4];
+      row_of<4>(s, i, si);
+      row_of<4>(dp, i, di);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float lse = sm.lse[4 * tx + c];
+        const bool vis = lse != -INFINITY && (bits[c] >> i & 1u) &&
+                         (full || slot >= 0 || visible(a.mask, sm.tq, 4 * tx + c, sm.tk, 4 * ty + i));
+        p[i][c] = vis ? __expf(si[c] - lse) : 0.f;
+        x[i][c] = p[i][c] * (di[c] - sm.dlt[4 * tx + c]);  // (sm.q carries the scale)
       }
     }
+    store_scores(sm.p, ty, tx, p);
+    store_scores(sm.ds, ty, tx, x);
+    __syncthreads();
+    accumulate<D>(sm.p, sm.gor, ty, tx, dv);
+    accumulate<D>(sm.ds, sm.qr, ty, tx, dk);
   }
-  if (!row_ok) return;
-  if (a.rotate) rotate_back(dk, part, (float)(tj - a.t[m.tok_start]), a.omega);
+  const long long T = a.rows / H, n_part = (long long)Hk * a.parts * T * D;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    st_elem<E>(a.dk, row * D + 32 * part + e, dk[e]);
-    st_elem<E>(a.dv, row * D + 32 * part + e, dv[e]);
+  for (int i = 0; i < 4; ++i) {
+    const int pj = pos0 + 4 * ty + i;
+    if (pj >= m.len) break;
+    float yk[N], yv[N];
+    row_of<N>(dk, i, yk);
+    row_of<N>(dv, i, yv);
+    if (a.kv_part) {  // the part's sums as they are
+      float* dst = a.kv_part + ((long long)blockIdx.y * T + m.tok_start + pj) * D + N * tx;
+      store_grad<D>(dst, yk, false, 0.f, a.omega);
+      store_grad<D>(dst + n_part, yv, false, 0.f, a.omega);
+    } else {
+      const long long at = k0 + (long long)(4 * ty + i) * Hk * D + N * tx;
+      store_grad<D>(static_cast<float*>(a.dk) + at, yk, a.rotate != 0,
+                    (float)(a.t[m.tok_start + pj] - a.t[m.tok_start]), a.omega + N / 2 * tx);
+      store_grad<D>(static_cast<float*>(a.dv) + at, yv, false, 0.f, a.omega);
+    }
   }
+}
+
+// The parts' sums in order; dK is turned back.  A thread has two columns of a token and key/value head.
+template <int D>
+__global__ void __launch_bounds__(256) k_bwd_kv_add(BwdArgs a) {
+  const int Hk = a.heads / a.group;
+  const long long T = a.rows / a.heads, n_part = (long long)Hk * a.parts * T * D;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= T * Hk * (D / 2)) return;
+  const int c = (int)(i % (D / 2)), hk = (int)(i / (D / 2) % Hk);
+  const long long tok = i / (D / 2) / Hk;
+  const float* src = a.kv_part + ((long long)hk * a.parts * T + tok) * D + 2 * c;
+  float k0 = 0.f, k1 = 0.f, v0 = 0.f, v1 = 0.f;
+  for (int p = 0; p < a.parts; ++p) {
+    const float2 k = *reinterpret_cast<const float2*>(src + (long long)p * T * D);
+    const float2 v = *reinterpret_cast<const float2*>(src + (long long)p * T * D + n_part);
+    k0 += k.x; k1 += k.y;
+    v0 += v.x; v1 += v.y;
+  }
+  if (a.rotate) {
+    int lo = 0, hi = a.batch;  // the token's request
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.meta[mid].tok_start <= tok) lo = mid;
+      else hi = mid;
+    }
+    float sn, cs;
+    sincosf((float)(a.t[tok] - a.t[a.meta[lo].tok_start]) * a.omega[c], &sn, &cs);
+    const float u = k0;
+    k0 = u * cs + k1 * sn;
+    k1 = -u * sn + k1 * cs;
+  }
+  const long long at = (tok * Hk + hk) * D + 2 * c;
+  *reinterpret_cast<float2*>(static_cast<float*>(a.dk) + at) = make_float2(k0, k1);
+  *reinterpret_cast<float2*>(static_cast<float*>(a.dv) + at) = make_float2(v0, v1);
 }
 
 template <typename E, int D>
@@ -297,19 +326,23 @@ cudaError_t launch_delta_t(const BwdArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename E, int D>
+template <int D>
 cudaError_t launch_bwd_t(const BwdArgs& a, long long n_tiles, cudaStream_t st) {
   if (n_tiles <= 0) return cudaSuccess;
-  const dim3 grid((unsigned)n_tiles, (unsigned)a.heads);
-  const int smem = (int)sizeof(BwdSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(k_bwd_dq<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_bwd_dkv<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done_q{0}, done_kv{0};
+  cudaError_t e = allow_smem(done_q, (const void*)k_bwd_dq<D>, (int)sizeof(DqSmem<D>));
+  if (e == cudaSuccess) e = allow_smem(done_kv, (const void*)k_bwd_dkv<D>, (int)sizeof(DkvSmem<D>));
   if (e != cudaSuccess) return e;
-  k_bwd_dq<E, D><<<grid, Split<D>::kThreads, smem, st>>>(a);
+  const unsigned halves = (unsigned)(n_tiles * simt::kPerTile);
+  k_bwd_dq<D><<<dim3(halves, (unsigned)a.heads), simt::kThreads, sizeof(DqSmem<D>), st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 grid_kv((unsigned)n_tiles, (unsigned)(a.heads / a.group));
-  k_bwd_dkv<E, D><<<grid_kv, Split<D>::kThreads, smem, st>>>(a);
+  const int Hk = a.heads / a.group;
+  k_bwd_dkv<D><<<dim3(halves, (unsigned)(Hk * a.parts)), simt::kThreads, sizeof(DkvSmem<D>), st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.kv_part) return e;
+  const long long threads = a.rows / a.heads * Hk * (D / 2);
+  k_bwd_kv_add<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -326,8 +359,8 @@ cudaError_t launch_bwd_delta(const BwdArgs& a, int dtype, int head_dim, cudaStre
 }
 
 cudaError_t launch_attn_bwd_simt(const BwdArgs& a, int head_dim, long long n_tiles, cudaStream_t st) {
-  if (head_dim == 32) return launch_bwd_t<float, 32>(a, n_tiles, st);
-  if (head_dim == 64) return launch_bwd_t<float, 64>(a, n_tiles, st);
+  if (head_dim == 32) return launch_bwd_t<32>(a, n_tiles, st);
+  if (head_dim == 64) return launch_bwd_t<64>(a, n_tiles, st);
   return cudaErrorInvalidValue;
 }
 

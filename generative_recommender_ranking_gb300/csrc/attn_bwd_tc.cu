@@ -1329,10 +1329,9 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
 
 }  // namespace
 
-int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int head_dim, int num_sms) {
-  const long long slots = num_sms;
+int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int num_sms) {
   int parts = 1;
-  while (parts < group && n_tiles * kv_heads * parts < 2 * slots) {
+  while (parts < group && n_tiles * kv_heads * parts < 2LL * num_sms) {
     ++parts;
     while (group % parts) ++parts;
   }

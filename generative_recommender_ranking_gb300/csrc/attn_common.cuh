@@ -205,6 +205,8 @@ struct BwdArgs {
                             // past the request's end or pruned)
   const int* kslot;         // per key-tile list entry: mask-table slot (-1: build the bits)
   const uint32_t* mtab;     // mask table, rows: [slot][128 query rows][4 words over the keys]
+  const int* pslot;         // per pair, class-matrix order: mask-table slot, -1 if none (fp32 path)
+  int mcap;                 // slots of the table
   const int* qslot;         // per query-tile list entry (qlist): mask-table slot, -1 if none
   const uint32_t* ctab;     // mask table, columns: [slot][128 keys][4 words over the queries]
   const int* kcount;       // per query tile: entries in its key-tile list

@@ -2,107 +2,143 @@
 // outputs; tensor-core TF32 would not hold 1e-4 against the fp64 reference).
 //
 // Softmax(QK^T/sqrt(d) + M) V (TM20K review page, section 2.1; LazFormer review
-// page, Eq. 19-21) over the plan's non-SKIP key tiles: one block per (query tile,
-// head), one thread per query row, an exact online softmax in fp32 with expf.
-// PARTIAL tiles evaluate the mask per element; FULL tiles skip it.
+// page, Eq. 19-21) over the plan's non-SKIP key tiles, an online softmax in fp32 with expf.
+// A block takes half a query tile (64 rows) of one head and the keys 64 at a time: S as a
+// product of 64 x 64 tiles in registers, P through shared memory to the product with V
+// (simt_tile.cuh).  Bound by the fp32 units and the shared memory that feeds them: 16 causal
+// requests of 400 to 700 tokens, 8 query and 2 key/value heads, head_dim 64, 232 us against 63 of the
+// units alone (a thread per query row, reading every key element for one multiplication: 451).
+// PARTIAL tiles take the plan's mask table, or without a slot evaluate the mask per element; FULL
+// tiles skip it.
 #include "attn_common.cuh"
+#include "launchers.cuh"
+#include "simt_tile.cuh"
 
 namespace recattn {
 
 namespace {
 
 template <int D>
-__global__ void __launch_bounds__(kTile) k_attn_simt(AttnArgs a) {
+struct FwdSmem {
+  __align__(16) float q[D * simt::kB];  // transposed, times the scale
+  __align__(16) float k[D * simt::kB];  // transposed
+  __align__(16) float v[simt::kB * D];
+  __align__(16) float p[simt::kB * simt::kB];
+  simt::Tokens tq, tk;
+};
+
+template <int D>
+__global__ void __launch_bounds__(simt::kThreads) k_attn_simt(AttnArgs a) {
+  using namespace simt;
+  constexpr int N = D / 16;
   extern __shared__ __align__(16) unsigned char smem[];
-  long long* s_t = reinterpret_cast<long long*>(smem);
-  int* s_ty = reinterpret_cast<int*>(s_t + kTile);
-  float (*s_k)[D + 1] = reinterpret_cast<float (*)[D + 1]>(s_ty + kTile);
-  float (*s_v)[D] = reinterpret_cast<float (*)[D]>(&s_k[kTile][0]);
-  const WorkItem it = decode_item(a, blockIdx.x, false);
+  FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem);
+  const WorkItem it = decode_item(a, blockIdx.x / kPerTile, true);  // (the heaviest first)
   if (it.n < 0) return;  // every query of the tile is pruned
-  const int r = threadIdx.x, pi = it.qt * kTile + r;
-  const bool row_ok = pi < it.m.len;
-  const long long tok = it.m.tok_start + pi;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int pos0 = it.qt * kTile + (int)(blockIdx.x % kPerTile) * kB;
+  if (pos0 >= it.m.len) return;
   const int H = a.heads, Hk = H / a.group, hk = it.h / a.group;
-  const float* Q = static_cast<const float*>(a.q);
-  const float* K = static_cast<const float*>(a.k);
-  const float* Vv = static_cast<const float*>(a.v);
-  float q[D], o[D];
-  long long ti = 0;
-  int tyi = -1;
+  const long long tok0 = it.m.tok_start + pos0;
+  load_tile<D>(static_cast<const float*>(a.q) + (tok0 * H + it.h) * D, (long long)H * D, it.m.len - pos0, a.scale, sm.q, nullptr);
+  sm.tq.load(a.t, a.ty, tok0, pos0, it.m.len, a.mask.delay);
+  f2 o[2][N];
+  float m[4], l[4];
 #pragma unroll
-  for (int e = 0; e < D; ++e) { q[e] = 0.f; o[e] = 0.f; }
-  if (row_ok) {
-    const float* src = Q + (tok * H + it.h) * D;
-#pragma unroll
-    for (int e = 0; e < D; ++e) q[e] = src[e] * a.scale;
-    ti = a.t[tok];
-    tyi = a.ty[tok];
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
   }
-  bool thr_ok; long long thr;
-  delay_bound(ti, a.mask.delay, thr_ok, thr);
-  float mrun = -INFINITY, l = 0.f;
-  for (int j = 0; j < it.n; ++j) {
-    const uint32_t ent = it.list[j];
-    const int kt = (int)(ent & 0xffffffu), cl = (int)(ent >> 24);
-    __syncthreads();
-    // stage the key tile: K', V rows and key metadata
-    for (int idx = r; idx < kTile * D; idx += kTile) {
-      const int c = idx / D, e = idx - c * D;
-      const int pj = kt * kTile + c;
-      const bool ok = pj < it.m.len;
-      const long long src = ((it.m.tok_start + pj) * Hk + hk) * D + e;
-      s_k[c][e] = ok ? K[src] : 0.f;
-      s_v[c][e] = ok ? Vv[src] : 0.f;
-    }
-    {
-      const int pj = kt * kTile + r;
-      const bool ok = pj < it.m.len;
-      s_t[r] = ok ? a.t[it.m.tok_start + pj] : 0;
-      s_ty[r] = ok ? (int)a.ty[it.m.tok_start + pj] : -1;
-    }
-    __syncthreads();
-    if (!row_ok) continue;
-    for (int c = 0; c < kTile; ++c) {
-      if (cl != REC_ATTN_TILE_FULL &&
-          !vis_pred(a.mask, pi, ti, tyi, thr_ok, thr, kt * kTile + c, s_t[c], s_ty[c]))
-        continue;
-      float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < D; ++e) s = fmaf(q[e], s_k[c][e], s);
-      if (s > mrun) {
-        const float corr = expf(mrun - s);
-        l *= corr;
+  for (int j = 0; j < N; ++j) o[0][j] = o[1][j] = pair(0.f, 0.f);
+  for (int j = 0; j < it.n * kPerTile; ++j) {
+    const uint32_t ent = it.list[j / kPerTile];
+    const int key0 = (int)(ent & 0xffffffu) * kTile + j % kPerTile * kB;
+    const bool full = (int)(ent >> 24) == REC_ATTN_TILE_FULL;
+    const int slot = full ? -1 : it.slots[j / kPerTile];  // of the mask table
+    if (key0 >= it.m.len) continue;
+    const long long src = ((it.m.tok_start + key0) * Hk + hk) * D;
+    __syncthreads();  // the last step's operands were read
+    load_tile<D>(static_cast<const float*>(a.k) + src, (long long)Hk * D, it.m.len - key0, 1.f, sm.k, nullptr);
+    load_tile<D>(static_cast<const float*>(a.v) + src, (long long)Hk * D, it.m.len - key0, 1.f, nullptr, sm.v);
+    if (!full && slot < 0) sm.tk.load(a.t, a.ty, it.m.tok_start + key0, key0, it.m.len, 0);
+    __syncthreads();
+    f2 s[2][4];
 #pragma unroll
-        for (int e = 0; e < D; ++e) o[e] *= corr;
-        mrun = s;
+    for (int c = 0; c < 4; ++c) s[0][c] = s[1][c] = pair(0.f, 0.f);
+    scores<D>(sm.q, sm.k, ty, tx, s);
+    float x[4][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float2 v = both(s[p][c]);
+        x[2 * p][c] = v.x;
+        x[2 * p + 1][c] = v.y;
       }
-      const float p = expf(s - mrun);
-      l += p;
+    float corr[4];
 #pragma unroll
-      for (int e = 0; e < D; ++e) o[e] = fmaf(p, s_v[c][e], o[e]);
+    for (int i = 0; i < 4; ++i) {
+      if (slot >= 0) {
+        const uint32_t bits = table_bits(a.mtab, slot, pos0 % kTile + 4 * ty + i, (key0 % kTile >> 2) + tx);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (!(bits >> c & 1u)) x[i][c] = -INFINITY;
+      } else if (!full) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (!visible(a.mask, sm.tq, 4 * ty + i, sm.tk, 4 * tx + c)) x[i][c] = -INFINITY;
+      }
+      const float mx = row_max(fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
+      const float m_new = fmaxf(m[i], mx), m_use = m_new == -INFINITY ? 0.f : m_new;
+      corr[i] = expf(m[i] - m_use);  // 0 while nothing was visible
+      m[i] = m_new;
+      l[i] *= corr[i];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        x[i][c] = expf(x[i][c] - m_use);
+        l[i] += x[i][c];  // this thread's columns; summed over the row at the end
+      }
     }
-  }
-  if (!row_ok || !query_kept(tyi, pi, it.keep)) return;
-  float* dst = static_cast<float*>(a.out) + (tok * H + it.h) * D;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (a.out_gate) {  // the attention output gate, O * sigmoid(g)
-    const float* g = static_cast<const float*>(a.out_gate) + (tok * H + it.h) * D;
+    store_scores(sm.p, ty, tx, x);
 #pragma unroll
-    for (int e = 0; e < D; ++e) dst[e] = o[e] * inv * sigmoid_io<float>(g[e]);
-  } else {
+    for (int c = 0; c < N; ++c)
 #pragma unroll
-    for (int e = 0; e < D; ++e) dst[e] = o[e] * inv;
+      for (int p = 0; p < 2; ++p) {
+        const float2 v = both(o[p][c]);
+        o[p][c] = pair(v.x * corr[2 * p], v.y * corr[2 * p + 1]);
+      }
+    __syncthreads();
+    accumulate<D>(sm.p, sm.v, ty, tx, o);
   }
-  if (a.lse) a.lse[tok * H + it.h] = l > 0.f ? mrun + logf(l) : -INFINITY;
+  __syncthreads();  // (an item without a key: the query rows' types are there)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i, pi = pos0 + r;
+    const float sum = row_sum(l[i]);
+    if (pi >= it.m.len || !query_kept(sm.tq.ty[r], pi, it.keep)) continue;
+    const long long row = (tok0 + r) * H + it.h;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    float* dst = static_cast<float*>(a.out) + row * D + N * tx;
+    // the attention output gate, O * sigmoid(g)
+    const float* g = a.out_gate ? static_cast<const float*>(a.out_gate) + row * D + N * tx : nullptr;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      const float2 v = both(o[i >> 1][c]);
+      const float y = ((i & 1) ? v.y : v.x) * inv;
+      dst[c] = g ? y * sigmoid_io<float>(g[c]) : y;
+    }
+    if (a.lse && tx == 0) a.lse[row] = sum > 0.f ? m[i] + logf(sum) : -INFINITY;
+  }
 }
 
 template <int D>
-cudaError_t launch(const AttnArgs& a, unsigned grid, cudaStream_t st) {
-  const size_t smem = kTile * (sizeof(long long) + sizeof(int)) + kTile * (2 * D + 1) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(k_attn_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const int smem = (int)sizeof(FwdSmem<D>);
+  const cudaError_t e = allow_smem(done, (const void*)k_attn_simt<D>, smem);
   if (e != cudaSuccess) return e;
-  k_attn_simt<D><<<grid, kTile, smem, st>>>(a);
+  k_attn_simt<D><<<(unsigned)(a.n_items * simt::kPerTile), simt::kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -110,10 +146,9 @@ cudaError_t launch(const AttnArgs& a, unsigned grid, cudaStream_t st) {
 
 cudaError_t launch_attn_simt(const AttnArgs& a, int head_dim, cudaStream_t st) {
   if (a.n_items <= 0) return cudaSuccess;
-  const unsigned grid = (unsigned)a.n_items;
   switch (head_dim) {
-    case 32: return launch<32>(a, grid, st);
-    case 64: return launch<64>(a, grid, st);
+    case 32: return launch<32>(a, st);
+    case 64: return launch<64>(a, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -63,7 +63,7 @@ cudaError_t launch_attn_bwd_simt(const BwdArgs& a, int head_dim, long long n_til
 // Parts of a group's query heads that dK/dV items take apart (a divisor of the group): the
 // fewest that give every SM two items (161 tiles of 2 key/value heads, 152 SMs: parts of their own for
 // a better balance cost more in their sums, 516 against 494 us a training step).
-int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int head_dim, int num_sms);
+int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int num_sms);
 cudaError_t launch_bwd_schedule(const BwdSchedArgs& s, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_bwd_tc(const BwdArgs& a, const CUtensorMap (&maps)[4], int head_dim, int num_sms,
                                cudaStream_t st);

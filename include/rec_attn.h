@@ -555,7 +555,8 @@ void rec_attn_cache_free(rec_attn_kv_cache_t* cache);
  *                 construction otherwise;
  *                 1: the kernel's row construction for every PARTIAL pair (what a pair
  *                 beyond the table's capacity, and rec_attn_fwd_noalloc, apply);
- *                 2: the per-pair predicate of the CUDA-core kernels (fp32 path).
+ *                 2: the per-pair predicate of the CUDA-core kernels (fp32 path; what they
+ *                 evaluate for a pair without a slot).
  *   bits_host     host uint32[n_pairs][128][4]: for query row r of the tile (request-
  *                 local position 128 qt + r), bit (c % 32) of word c / 32 is 1 when key
  *                 c of the key tile (position 128 kt + c) enters the row's softmax.  A
