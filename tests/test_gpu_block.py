@@ -311,3 +311,51 @@ def test_items_of_many_tiles(name, lens, H, Hk, d):
         diff = got.double() - want
         rel, top = float(diff.norm() / want.norm()), float(diff.abs().max() / want.abs().max())
         assert rel <= 1e-2 and top <= 2e-2, (what, rel, top)
+
+
+F32 = {
+    # lengths, heads, key/value heads, head_dim, mask
+    "groups_in_parts_d64": ([700, 0, 63, 64, 65, 129], 8, 1, 64, {}),
+    "groups_of_three_d32": ([190, 1, 257], 6, 2, 32, dict(use_delay=True, delay_s=1800)),
+    "window_d64": ([300, 500], 4, 2, 64, dict(window=70)),
+    "whole_groups_d32": ([40] * 200, 4, 2, 32, dict(hist_bidirectional=True)),
+    "no_rotation_d64": ([128, 192], 2, 1, 64, dict(use_rope=False)),
+}
+
+
+@pytest.mark.parametrize("name", list(F32))
+def test_fp32_shared_heads_at_tile_edges(name):
+    """fp32 forward and backward with shared heads, lengths around the kernels' 64 rows, special tokens,
+    events and candidates, an empty request, with and without parts of the groups: the fp32 bounds
+    (outputs 1e-4; gradients 1e-5 relative Frobenius and 1e-4 of the largest value)."""
+    lens, H, Hk, d, mask = F32[name]
+    rng = np.random.default_rng(9)
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    T, G = int(off[-1]), H // Hk
+    t = np.concatenate([1_700_000_000 + np.cumsum(rng.integers(1, 2000, size=n)) for n in lens]).astype(np.int64)
+    ty = np.concatenate([np.array(([W.GLOBAL] * 3 + [W.HIST] * n + [W.RT] * (n // 8) + [W.CAND] * (n // 9))[-n:] if n else [], dtype=np.int8)
+                         for n in lens])
+    new = lambda h: rng.standard_normal((T, h, d)).astype(np.float32)
+    q, k, v, do = new(H), new(Hk), new(Hk), new(H)
+    params = {"use_delay": False, **mask}
+    dev = lambda a: torch.from_numpy(a).cuda()
+    Q, K, V, DO = dev(q), dev(k), dev(v), dev(do)
+    o, dq, dk, dv = (torch.full_like(x, float("nan")) for x in (Q, Q, K, V))
+    lse = torch.full((T, H), float("nan"), device="cuda")
+    with bd.rec_attn_plan_grouped(bd.make_params(H, d, dtype="fp32", **params), Hk, off, dev(off), dev(t), dev(ty)) as plan:
+        bd.rec_attn_fwd(plan, Q, K, V, o, lse)
+        bd.rec_attn_bwd(plan, Q, K, V, o, lse, DO, dq, dk, dv)
+        torch.cuda.synchronize()
+        assert bd.rec_attn_device_status(plan) == bd.OK
+    op = oracle.Params(H, d, **params)
+    kr, vr = np.repeat(k, G, 1), np.repeat(v, G, 1)
+    ref, ref_lse = oracle.attention(op, off, t, ty, q, kr, vr, with_lse=True)
+    rq, rk, rv = oracle.attention_bwd(op, off, t, ty, q, kr, vr, do)
+    assert np.abs(o.double().cpu().numpy() - ref).max() <= gu.FP32_MAX_ABS
+    fin, got = np.isfinite(ref_lse), lse.cpu().numpy()
+    assert (np.isfinite(got) == fin).all() and np.abs(got[fin] - ref_lse[fin]).max() <= 1e-4
+    shared = lambda a: a.reshape(T, Hk, G, d).sum(2)
+    for what, x, want in (("dq", dq, rq), ("dk", dk, shared(rk)), ("dv", dv, shared(rv))):
+        diff = x.double().cpu().numpy() - want
+        assert np.linalg.norm(diff) <= 1e-5 * np.linalg.norm(want), what
+        assert np.abs(diff).max() <= 1e-4 * np.abs(want).max(), what
