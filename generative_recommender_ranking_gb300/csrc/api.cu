@@ -606,7 +606,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   const bool tc = p.dtype == REC_ATTN_BF16;
   const int group = p.num_heads / plan->kv_heads;
   // (fp32 items are half tiles)
-  const int parts = bwd_kv_parts(tc ? plan->NT : 2 * plan->NT, plan->kv_heads, group, plan->num_sms);
+  const int parts = bwd_kv_parts(tc ? plan->NT : 2 * plan->NT, plan->kv_heads, group, (tc ? 2LL : 6LL) * plan->num_sms);
   const int reps = group / parts;  // query heads of a dK/dV item
   const long long n_items = plan->NT * p.num_heads, n_kv_items = plan->NT * plan->kv_heads * parts;
   // bf16 workspace: descriptors [n_items], [n_kv_items] | row constants [H][NT][128] | lists [NC] |
@@ -686,7 +686,7 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
     return el != cudaSuccess ? el : ef;
   };
   if (!tc) {
-    e = launch_bwd_delta(a, p.dtype, p.head_dim, st);
+    e = launch_bwd_delta(a, p.head_dim, st);
     if (e == cudaSuccess) e = take_parts();
     if (e != cudaSuccess) return from_cuda(e);
     return from_cuda(return_parts(launch_attn_bwd_simt(a, p.head_dim, plan->NT, st)));

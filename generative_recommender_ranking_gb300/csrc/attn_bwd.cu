@@ -1,6 +1,6 @@
 // attn_bwd.cu -- backward pass of the masked time-RoPE softmax attention on the CUDA
-// cores (fp32 inputs, head_dim 32 or 64), and the row term D of both backward paths
-// (the bf16 path runs on the tensor cores: attn_bwd_tc.cu).
+// cores (fp32 inputs, head_dim 32 or 64; the bf16 path runs on the tensor cores:
+// attn_bwd_tc.cu).
 //
 // Gradients of O = Softmax(QK^T/sqrt(d) + M) V (TM20K review page, section 2.1;
 // LazFormer review page, Eq. 19-21) through the time-RoPE (CADET review page, time
@@ -12,7 +12,7 @@
 //
 // Kernels over the planner's tile lists, so SKIP tiles cost nothing here either; the products are of
 // 64 x 64 tiles in registers (simt_tile.cuh):
-//   k_bwd_delta   D_i per (token, head), fp32 or bf16 rows;
+//   k_bwd_delta   D_i per (token, head);
 //   k_bwd_dq      a block per (half query tile, head), over the query tile's non-SKIP key tiles;
 //   k_bwd_dkv     a block per (half key tile, key/value head or part of its query heads), over the
 //                 query tiles whose class against this key tile is not SKIP;
@@ -20,10 +20,8 @@
 // FULL tiles skip the mask; PARTIAL tiles take the plan's mask table, or without a slot evaluate it.  Rows with no visible key (lse = -inf)
 // contribute nothing.  Bound by the fp32 units and the shared memory that feeds them (k_bwd_dkv at
 // head_dim 64: one block per SM).  Forward and backward of 16 causal requests of 400 to 700 tokens,
-// 8 query and 2 key/value heads, head_dim 64: 1325 us (a thread per row: 2306); of one request of 700
-// tokens, 8 and 1 heads: 336 us (2742, whose dK/dV had six blocks).
-#include <cuda_bf16.h>
-
+// 8 query and 2 key/value heads, head_dim 64: 1070 us, dQ 352 and dK/dV 462 of it (a thread per row: 2306);
+// of one request of 700 tokens, 8 and 1 heads: 293 us (2742, whose dK/dV had six blocks).
 #include "attn_common.cuh"
 #include "launchers.cuh"
 #include "simt_tile.cuh"
@@ -32,16 +30,6 @@ namespace recattn {
 
 namespace {
 
-template <typename E>
-__device__ __forceinline__ float ld_elem(const void* base, long long i);
-template <>
-__device__ __forceinline__ float ld_elem<float>(const void* base, long long i) {
-  return static_cast<const float*>(base)[i];
-}
-template <>
-__device__ __forceinline__ float ld_elem<__nv_bfloat16>(const void* base, long long i) {
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-}
 // The request of global tile g (binary search over the request table).
 __device__ __forceinline__ int tile_request(const ReqMeta* meta, int batch, long long g) {
   int lo = 0, hi = batch;
@@ -78,14 +66,19 @@ __device__ __forceinline__ void row_of(const simt::f2 (&o)[2][N], int i, float (
   }
 }
 
-template <typename E, int D>
-__global__ void __launch_bounds__(128) k_bwd_delta(BwdArgs a) {
-  const long long r = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // (token, head) row
-  if (r >= a.rows) return;
+// 16 bytes of dO and O a thread.
+template <int D>
+__global__ void __launch_bounds__(256) k_bwd_delta(BwdArgs a) {
+  constexpr int kLanes = D / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, r = i / kLanes;  // (token, head) row
   float acc = 0.f;
-#pragma unroll 8
-  for (int e = 0; e < D; ++e) acc = fmaf(ld_elem<E>(a.dout, r * D + e), ld_elem<E>(a.out, r * D + e), acc);
-  a.delta[r] = acc;
+  if (r < a.rows) {
+    const float4 x = static_cast<const float4*>(a.dout)[i], y = static_cast<const float4*>(a.out)[i];
+    acc = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (r < a.rows && i % kLanes == 0) a.delta[r] = acc;
 }
 
 template <int D>
@@ -143,18 +136,33 @@ __global__ void __launch_bounds__(simt::kThreads) k_bwd_dq(BwdArgs a) {
   const int n = a.kcount[g];
   const uint32_t* list = a.klist + m.cls_start + (long long)qt * m.ntiles;
   const int* slots = a.kslot + m.cls_start + (long long)qt * m.ntiles;
-  for (int j = 0; j < n * kPerTile; ++j) {
-    const uint32_t ent = list[j / kPerTile];
-    const int key0 = (int)(ent & 0xffffffu) * kTile + j % kPerTile * kB;
-    const bool full = (int)(ent >> 24) == REC_ATTN_TILE_FULL;
-    const int slot = full ? -1 : slots[j / kPerTile];  // of the mask table
-    if (key0 >= m.len) continue;
+  // steps of 64 keys; those past the request's end are left out
+  const int steps = n * kPerTile;
+  auto key_of = [&](int j) { return (int)(list[j / kPerTile] & 0xffffffu) * kTile + j % kPerTile * kB; };
+  auto next = [&](int j) {
+    while (j < steps && key_of(j) >= m.len) ++j;
+    return j;
+  };
+  Rows<D> nk, nv;
+  auto fetch = [&](int j) {
+    const int key0 = key_of(j);
     const long long src = ((m.tok_start + key0) * Hk + hk) * D;
+    nk.fetch(static_cast<const float*>(a.k) + src, (long long)Hk * D, m.len - key0);
+    nv.fetch(static_cast<const float*>(a.v) + src, (long long)Hk * D, m.len - key0);
+  };
+  int j = next(0);
+  if (j < steps) fetch(j);
+  while (j < steps) {
+    const int key0 = key_of(j);
+    const bool full = (int)(list[j / kPerTile] >> 24) == REC_ATTN_TILE_FULL;
+    const int slot = full ? -1 : slots[j / kPerTile];  // of the mask table
     __syncthreads();  // the last step's operands were read
-    load_tile<D>(static_cast<const float*>(a.k) + src, (long long)Hk * D, m.len - key0, 1.f, sm.k, sm.kr);
-    load_tile<D>(static_cast<const float*>(a.v) + src, (long long)Hk * D, m.len - key0, 1.f, sm.v, nullptr);
+    nk.put(1.f, sm.k, sm.kr);
+    nv.put(1.f, sm.v, nullptr);
     if (!full && slot < 0) sm.tk.load(a.t, a.ty, m.tok_start + key0, key0, m.len, 0);
     __syncthreads();
+    j = next(j + 1);
+    if (j < steps) fetch(j);
     f2 s[2][4], dp[2][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[0][c] = s[1][c] = dp[0][c] = dp[1][c] = pair(0.f, 0.f);
@@ -212,27 +220,47 @@ __global__ void __launch_bounds__(simt::kThreads) k_bwd_dkv(BwdArgs a) {
 #pragma unroll
   for (int c = 0; c < N; ++c) dk[0][c] = dk[1][c] = dv[0][c] = dv[1][c] = pair(0.f, 0.f);
   const uint8_t* col = a.cls + m.cls_start + kt;  // column kt of the request's class matrix
-  for (int it = 0; it < reps * m.ntiles * kPerTile; ++it) {
-    const int h = (int)blockIdx.y * reps + it / (m.ntiles * kPerTile), half = it % (m.ntiles * kPerTile);
-    const int qt = half / kPerTile, query0 = half * kB;
-    const int cl = col[(long long)qt * m.ntiles];
-    if (cl == REC_ATTN_TILE_SKIP || query0 >= m.len) continue;
-    const bool full = cl == REC_ATTN_TILE_FULL;
+  // steps of 64 queries of one head; SKIP tiles and those past the request's end are left out
+  const int halves = m.ntiles * kPerTile, steps = reps * halves;
+  auto next = [&](int it) {
+    while (it < steps) {
+      const int half = it % halves;
+      if (half * kB < m.len && col[(long long)(half / kPerTile) * m.ntiles] != REC_ATTN_TILE_SKIP) break;
+      ++it;
+    }
+    return it;
+  };
+  Rows<D> nq, ngo;
+  float nl = 0.f, nd = 0.f;  // the step's row constants: the first kB threads'
+  auto fetch = [&](int it) {
+    const int h = (int)blockIdx.y * reps + it / halves, query0 = it % halves * kB;
+    const long long qtok = m.tok_start + query0, src = (qtok * H + h) * D;
+    nq.fetch(static_cast<const float*>(a.q) + src, (long long)H * D, m.len - query0);
+    ngo.fetch(static_cast<const float*>(a.dout_attn) + src, (long long)H * D, m.len - query0);
+    const int c = threadIdx.x, pi = query0 + c;
+    // pruned queries give no gradient, nor do queries that see no key
+    const bool kept = c < kB && pi < m.len && query_kept(a.ty[qtok + c], pi, a.qkeep[b]);
+    nl = kept ? a.lse[(qtok + c) * H + h] : -INFINITY;
+    nd = kept ? a.delta[(qtok + c) * H + h] : 0.f;
+  };
+  int it = next(0);
+  if (it < steps) fetch(it);
+  while (it < steps) {
+    const int query0 = it % halves * kB, qt = query0 / kTile;
+    const bool full = col[(long long)qt * m.ntiles] == REC_ATTN_TILE_FULL;
     const int in_table = full ? -1 : a.pslot[m.cls_start + (long long)qt * m.ntiles + kt];
     const int slot = in_table < a.mcap ? in_table : -1;  // of the mask table
-    const long long qtok = m.tok_start + query0, src = (qtok * H + h) * D;
     __syncthreads();  // the last step's operands were read
-    load_tile<D>(static_cast<const float*>(a.q) + src, (long long)H * D, m.len - query0, a.scale, sm.q, sm.qr);
-    load_tile<D>(static_cast<const float*>(a.dout_attn) + src, (long long)H * D, m.len - query0, 1.f, sm.go, sm.gor);
-    if (!full && slot < 0) sm.tq.load(a.t, a.ty, qtok, query0, m.len, a.mask.delay);
-    for (int c = threadIdx.x; c < kB; c += kThreads) {
-      const int pi = query0 + c;
-      // pruned queries give no gradient, nor do queries that see no key
-      const bool kept = pi < m.len && query_kept(a.ty[qtok + c], pi, a.qkeep[b]);
-      sm.lse[c] = kept ? a.lse[(qtok + c) * H + h] : -INFINITY;
-      sm.dlt[c] = kept ? a.delta[(qtok + c) * H + h] : 0.f;
+    nq.put(a.scale, sm.q, sm.qr);
+    ngo.put(1.f, sm.go, sm.gor);
+    if (!full && slot < 0) sm.tq.load(a.t, a.ty, m.tok_start + query0, query0, m.len, a.mask.delay);
+    if (threadIdx.x < kB) {
+      sm.lse[threadIdx.x] = nl;
+      sm.dlt[threadIdx.x] = nd;
     }
     __syncthreads();
+    it = next(it + 1);
+    if (it < steps) fetch(it);
     f2 s[2][4], dp[2][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[0][c] = s[1][c] = dp[0][c] = dp[1][c] = pair(0.f, 0.f);
@@ -319,10 +347,10 @@ __global__ void __launch_bounds__(256) k_bwd_kv_add(BwdArgs a) {
   *reinterpret_cast<float2*>(static_cast<float*>(a.dv) + at) = make_float2(v0, v1);
 }
 
-template <typename E, int D>
+template <int D>
 cudaError_t launch_delta_t(const BwdArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
-  k_bwd_delta<E, D><<<(unsigned)((a.rows + 127) / 128), 128, 0, st>>>(a);
+  k_bwd_delta<D><<<(unsigned)((a.rows * (D / 4) + 255) / 256), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -348,13 +376,9 @@ cudaError_t launch_bwd_t(const BwdArgs& a, long long n_tiles, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_bwd_delta(const BwdArgs& a, int dtype, int head_dim, cudaStream_t st) {
-  if (dtype == REC_ATTN_BF16) {
-    if (head_dim == 64) return launch_delta_t<__nv_bfloat16, 64>(a, st);
-  } else {
-    if (head_dim == 32) return launch_delta_t<float, 32>(a, st);
-    if (head_dim == 64) return launch_delta_t<float, 64>(a, st);
-  }
+cudaError_t launch_bwd_delta(const BwdArgs& a, int head_dim, cudaStream_t st) {
+  if (head_dim == 32) return launch_delta_t<32>(a, st);
+  if (head_dim == 64) return launch_delta_t<64>(a, st);
   return cudaErrorInvalidValue;
 }
 

@@ -1329,9 +1329,9 @@ cudaError_t launch_bwd_d(const BwdArgs& a, const CUtensorMap (&maps)[4], int num
 
 }  // namespace
 
-int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int num_sms) {
+int bwd_kv_parts(long long n_tiles, int kv_heads, int group, long long least) {
   int parts = 1;
-  while (parts < group && n_tiles * kv_heads * parts < 2LL * num_sms) {
+  while (parts < group && n_tiles * kv_heads * parts < least) {
     ++parts;
     while (group % parts) ++parts;
   }

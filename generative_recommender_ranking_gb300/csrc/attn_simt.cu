@@ -6,8 +6,9 @@
 // A block takes half a query tile (64 rows) of one head and the keys 64 at a time: S as a
 // product of 64 x 64 tiles in registers, P through shared memory to the product with V
 // (simt_tile.cuh).  Bound by the fp32 units and the shared memory that feeds them: 16 causal
-// requests of 400 to 700 tokens, 8 query and 2 key/value heads, head_dim 64, 232 us against 63 of the
-// units alone (a thread per query row, reading every key element for one multiplication: 451).
+// requests of 400 to 700 tokens, 8 query and 2 key/value heads, head_dim 64, 212 us against 63 of the
+// units alone (a thread per query row, reading every key element for one multiplication: 451; three
+// blocks an SM with fewer registers, which spill: 232).
 // PARTIAL tiles take the plan's mask table, or without a slot evaluate the mask per element; FULL
 // tiles skip it.
 #include "attn_common.cuh"
@@ -51,18 +52,33 @@ __global__ void __launch_bounds__(simt::kThreads) k_attn_simt(AttnArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) o[0][j] = o[1][j] = pair(0.f, 0.f);
-  for (int j = 0; j < it.n * kPerTile; ++j) {
-    const uint32_t ent = it.list[j / kPerTile];
-    const int key0 = (int)(ent & 0xffffffu) * kTile + j % kPerTile * kB;
-    const bool full = (int)(ent >> 24) == REC_ATTN_TILE_FULL;
-    const int slot = full ? -1 : it.slots[j / kPerTile];  // of the mask table
-    if (key0 >= it.m.len) continue;
+  // steps of 64 keys; those past the request's end are left out
+  const int steps = it.n * kPerTile;
+  auto key_of = [&](int j) { return (int)(it.list[j / kPerTile] & 0xffffffu) * kTile + j % kPerTile * kB; };
+  auto next = [&](int j) {
+    while (j < steps && key_of(j) >= it.m.len) ++j;
+    return j;
+  };
+  Rows<D> nk, nv;
+  auto fetch = [&](int j) {
+    const int key0 = key_of(j);
     const long long src = ((it.m.tok_start + key0) * Hk + hk) * D;
+    nk.fetch(static_cast<const float*>(a.k) + src, (long long)Hk * D, it.m.len - key0);
+    nv.fetch(static_cast<const float*>(a.v) + src, (long long)Hk * D, it.m.len - key0);
+  };
+  int j = next(0);
+  if (j < steps) fetch(j);
+  while (j < steps) {
+    const int key0 = key_of(j);
+    const bool full = (int)(it.list[j / kPerTile] >> 24) == REC_ATTN_TILE_FULL;
+    const int slot = full ? -1 : it.slots[j / kPerTile];  // of the mask table
     __syncthreads();  // the last step's operands were read
-    load_tile<D>(static_cast<const float*>(a.k) + src, (long long)Hk * D, it.m.len - key0, 1.f, sm.k, nullptr);
-    load_tile<D>(static_cast<const float*>(a.v) + src, (long long)Hk * D, it.m.len - key0, 1.f, nullptr, sm.v);
+    nk.put(1.f, sm.k, nullptr);
+    nv.put(1.f, nullptr, sm.v);
     if (!full && slot < 0) sm.tk.load(a.t, a.ty, it.m.tok_start + key0, key0, it.m.len, 0);
     __syncthreads();
+    j = next(j + 1);
+    if (j < steps) fetch(j);
     f2 s[2][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[0][c] = s[1][c] = pair(0.f, 0.f);

@@ -58,12 +58,13 @@ cudaError_t launch_rope_fused(const RopeArgs& a, const FusedArgs& f, int dtype, 
 cudaError_t launch_rope_slots(const SlotArgs& a, int dtype, long long n_chunks, cudaStream_t st);
 cudaError_t launch_slots_gather(const SlotArgs& a, int dtype, long long n_chunks, cudaStream_t st);
 cudaError_t launch_attn_simt(const AttnArgs& a, int head_dim, cudaStream_t st);
-cudaError_t launch_bwd_delta(const BwdArgs& a, int dtype, int head_dim, cudaStream_t st);
+cudaError_t launch_bwd_delta(const BwdArgs& a, int head_dim, cudaStream_t st);
 cudaError_t launch_attn_bwd_simt(const BwdArgs& a, int head_dim, long long n_tiles, cudaStream_t st);
 // Parts of a group's query heads that dK/dV items take apart (a divisor of the group): the
-// fewest that give every SM two items (161 tiles of 2 key/value heads, 152 SMs: parts of their own for
-// a better balance cost more in their sums, 516 against 494 us a training step).
-int bwd_kv_parts(long long n_tiles, int kv_heads, int group, int num_sms);
+// fewest that give `least` items.  Tensor cores: two an SM (161 tiles of 2 key/value heads, 152 SMs: parts of
+// their own for a better balance cost more in their sums, 516 against 494 us a training step);
+// fp32, whose items are slow and of unequal length: six.
+int bwd_kv_parts(long long n_tiles, int kv_heads, int group, long long least);
 cudaError_t launch_bwd_schedule(const BwdSchedArgs& s, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_bwd_tc(const BwdArgs& a, const CUtensorMap (&maps)[4], int head_dim, int num_sms,
                                cudaStream_t st);

@@ -36,21 +36,38 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 // Four consecutive rows (4 * block ..) of a transposed operand at d.
 __device__ __forceinline__ int at(int block, int d) { return d * kB + ((block ^ ((d >> 2) & 15)) << 2); }
 
-// The 64 rows at src (`stride` floats apart; zeros from row `valid` on), times scale: transposed
-// into T and / or as they are into R (either may be null).
+// The 64 rows at src (`stride` floats apart; zeros from row `valid` on): into registers, so that a
+// step's loads run under the last one's products, and from there, times scale, to shared memory:
+// transposed into T and / or as they are into R (either may be null).
+template <int D>
+struct Rows {
+  static constexpr int kChunks = kB * (D / 4) / kThreads;
+  float4 x[kChunks];
+  __device__ __forceinline__ void fetch(const float* src, long long stride, int valid) {
+#pragma unroll
+    for (int n = 0; n < kChunks; ++n) {
+      const int i = (int)threadIdx.x + n * kThreads, r = i / (D / 4), e = i % (D / 4) * 4;
+      x[n] = r < valid ? *reinterpret_cast<const float4*>(src + r * stride + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void put(float scale, float* T, float* R) const {
+#pragma unroll
+    for (int n = 0; n < kChunks; ++n) {
+      const int i = (int)threadIdx.x + n * kThreads, r = i / (D / 4), e = i % (D / 4) * 4;
+      const float4 y = make_float4(x[n].x * scale, x[n].y * scale, x[n].z * scale, x[n].w * scale);
+      if (T) {
+        float* t = T + at(r >> 2, e) + (r & 3);
+        t[0] = y.x; t[kB] = y.y; t[2 * kB] = y.z; t[3 * kB] = y.w;
+      }
+      if (R) *reinterpret_cast<float4*>(R + r * D + e) = y;
+    }
+  }
+};
 template <int D>
 __device__ __forceinline__ void load_tile(const float* src, long long stride, int valid, float scale, float* T, float* R) {
-  for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
-    const int r = i / (D / 4), e = i % (D / 4) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < valid) x = *reinterpret_cast<const float4*>(src + r * stride + e);
-    x.x *= scale; x.y *= scale; x.z *= scale; x.w *= scale;
-    if (T) {
-      float* t = T + at(r >> 2, e) + (r & 3);
-      t[0] = x.x; t[kB] = x.y; t[2 * kB] = x.z; t[3 * kB] = x.w;
-    }
-    if (R) *reinterpret_cast<float4*>(R + r * D + e) = x;
-  }
+  Rows<D> x;
+  x.fetch(src, stride, valid);
+  x.put(scale, T, R);
 }
 
 // s[p][j] += sum_d A(rows 4 ty + 2 p, + 1; d) B(row 4 tx + j; d), both transposed.
