@@ -277,7 +277,7 @@ rec_attn_status rec_attn_fwd_fused(rec_attn_plan_t* plan, const void* q, const v
  * library pool on `stream` (released with the plan): for bf16 the per-plan item
  * schedule (96 B per tile and head, 4 B per tile pair) and the rows' constants
  * (16 B per tile row and head); for fp32 T * H floats.  On a plan of shared heads with few
- * tiles (bf16) each call also takes fp32 parts of dK and dV, 8 * d bytes per token, key/value
+ * tiles each call also takes fp32 parts of dK and dV, 8 * d bytes per token, key/value
  * head and part (up to H / Hk of them), from the pool.  bf16: tensor cores (bf16
  * operands, fp32 accumulation; P and dS rounded to bf16 for their MMAs, as in the
  * forward's P); fp32: CUDA cores in fp32.  Gradients are rounded once to
