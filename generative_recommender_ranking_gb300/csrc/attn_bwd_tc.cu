@@ -17,7 +17,9 @@
 // order of the query tiles, so under causal masks both modes start with their heaviest items.  Per
 // item the resident operand pair stays in shared memory (DQ: Q', dO; DKV: K', V) and the streamed
 // pair (DQ: K', V of the query tile's non-SKIP key tiles; DKV: Q', dO of the query tiles whose class
-// against the key tile is not SKIP) runs through two rings.  A step is a whole streamed tile:
+// against the key tile is not SKIP) runs through two rings; at head_dim 64 there is room for two
+// resident pairs, and the next item's loads while this one runs (1% on items of a few tiles).  A step
+// is a whole streamed tile:
 //   DQ   S = Q' K'^T - lse / scale, dP = dO V^T - D; the compute warps write dS (bf16) over the
 //        first half of the 32 columns of S that each has read; dQ += dS K' with dS read from TMEM.
 //   DKV  S^T = K' Q'^T - lse / scale, dP^T = V dO^T - D; P^T over the first half of S's columns,
@@ -71,9 +73,11 @@ struct BCfg {
   static constexpr int kTileBytes = kTile * D * 2;
   // stages of the streamed rings (first and second operand)
   template <bool DKV>
-  static constexpr int kNS0 = D == 64 ? 4 : DKV ? 2 : 3;
+  static constexpr int kNS0 = D == 64 ? 3 : DKV ? 2 : 3;
   template <bool DKV>
-  static constexpr int kNS1 = D == 64 ? 4 : DKV ? 2 : 1;
+  static constexpr int kNS1 = D == 64 ? 3 : DKV ? 2 : 1;
+  // resident pairs in shared memory: at head_dim 64 the next item's loads while this one runs
+  static constexpr int kRB = D == 64 ? 2 : 1;
   static constexpr int kWG = 4;                   // compute warpgroups, 32 of a step's 128 columns each
   static constexpr int kRoles = 3;                // producer, one or two issuers
   static constexpr int kThreads = 32 * kRoles + 128 * kWG;
@@ -100,9 +104,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // mbarriers (steps are counted over the CTA's life; [2]: by step parity)
 enum : int {
-  kResFull = 0,
-  kResEmpty,
-  kStr0Full,                    // [4] the streamed tile of the scores S (DQ: K', DKV: Q'), with the record
+  kResFull = 0,                 // [kRB]
+  kResEmpty = kResFull + 2,     // [kRB]
+  kStr0Full = kResEmpty + 2,    // [4] the streamed tile of the scores S (DQ: K', DKV: Q'), with the record
   kStr0Empty = kStr0Full + 4,   // [4] and the row constants
   kStr1Full = kStr0Empty + 4,   // [4] the streamed tile of dP (DQ: V, DKV: dO)
   kStr1Empty = kStr1Full + 4,   // [4]
@@ -130,17 +134,18 @@ constexpr int kRowX = kTile * 16;    // a tile's rows of the constants' operand,
 constexpr int kAugB = 2 * kRowX;     // an operand of 16 columns: two 8-column halves, the second zero
 template <int D>
 struct BL {
-  static constexpr int kTiles = D == 64 ? 8 : 4;             // streamed tiles: kNS0 + kNS1 of both modes
-  static constexpr int kRecs = D == 64 ? 4 : 3;              // at least kNS0 of both modes,
-  static constexpr int kAugs = BCfg<D>::template kNS0<true>; // of DKV
+  static constexpr int kRB = BCfg<D>::kRB;
+  static constexpr int kTiles = D == 64 ? 6 : 4;             // streamed tiles: kNS0 + kNS1 of both modes
+  static constexpr int kRecs = 3;                            // at least kNS0 of both modes,
+  static constexpr int kAugs = BCfg<D>::template kNS0<true>; // of DKV (and at least kRB)
   static constexpr int kTileBytes = BCfg<D>::kTileBytes;
   static constexpr int kOnes = 0;                            // [2 (S, dP)] ones that pick the constants
-  static constexpr int kAug = kOnes + 2 * kAugB;              // constants of the query tiles (DKV: [kNS0]; DQ: one)
-  static constexpr int kRes = kAug + kAugs * kAugB;           // [2] resident tiles
-  static constexpr int kStr = kRes + 2 * kTileBytes;         // the streamed tiles, [kNS0] first operands, then [kNS1]
+  static constexpr int kAug = kOnes + 2 * kAugB;              // constants of the query tiles (DKV: [kNS0]; DQ: [kRB])
+  static constexpr int kRes = kAug + kAugs * kAugB;           // [kRB][2] resident tiles
+  static constexpr int kStr = kRes + kRB * 2 * kTileBytes;         // the streamed tiles, [kNS0] first operands, then [kNS1]
   static constexpr int kSRec = kStr + kTiles * kTileBytes;  // [kNS0] records of the streamed tiles
-  static constexpr int kRRec = kSRec + kRecs * kStageRecB;   // record of the item's tile
-  static constexpr int kCol = kRRec + kRecB;                 // DKV: [2][128 keys] 128 query bits
+  static constexpr int kRRec = kSRec + kRecs * kStageRecB;   // [kRB] record of the item's tile
+  static constexpr int kCol = kRRec + kRB * kRecB;                 // DKV: [2][128 keys] 128 query bits
   static constexpr int kItems = kCol + 2 * kTile * 16;       // [2] published item descriptors
   static constexpr int kBarsOff = kItems + 2 * 64;
   static constexpr int kTotal = kBarsOff + kNumBars * 8 + 16;  // + abort flag and TMEM slot
@@ -149,7 +154,7 @@ struct BL {
 template <int D>
 constexpr bool layout_ok() {
   using L = BL<D>;
-  return L::kRes % 1024 == 0 && L::kStr % 1024 == 0 && L::kSRec % 16 == 0 && L::kRRec % 16 == 0 &&
+  return L::kAugs >= L::kRB && L::kRes % 1024 == 0 && L::kStr % 1024 == 0 && L::kSRec % 16 == 0 && L::kRRec % 16 == 0 &&
          L::kCol % 16 == 0 && L::kBarsOff % 8 == 0 && L::kDynamic <= 227 * 1024 &&
          BCfg<D>::template kNS0<true> + BCfg<D>::template kNS1<true> <= L::kTiles && BCfg<D>::template kNS0<true> <= L::kRecs &&
          BCfg<D>::template kNS0<false> + BCfg<D>::template kNS1<false> <= L::kTiles && BCfg<D>::template kNS0<false> <= L::kRecs;
@@ -313,8 +318,7 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
   using L = BL<D>;
   constexpr int kTileBytes = L::kTileBytes, kNS0 = BCfg<D>::template kNS0<DKV>, kNS1 = BCfg<D>::template kNS1<DKV>;
   uint32_t it_n = 0, s_it = 0, it_cnt = 0;
-  bool res_used = false;
-  uint32_t res_ph = 0, n0 = 0, n1 = 0;  // steps whose first, second operand was loaded
+  uint32_t n0 = 0, n1 = 0;  // steps whose first, second operand was loaded
   const uint4* descs = reinterpret_cast<const uint4*>(a.desc + (DKV ? a.n_items : 0));
   ItemSlot* slots = reinterpret_cast<ItemSlot*>(sm + L::kItems);
   int* counter = a.counters + (DKV ? 5 : 3);
@@ -339,22 +343,23 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
     const BwdItemDesc d = unpack_desc(nx);
     if (d.n <= 0) continue;
 
-    if (!bw_wait(bars + kResEmpty, (it_n & 1) ^ 1, abort_flag, a.status)) goto drain;
+    const int rb = (int)(it_n % L::kRB);
+    if (!bw_wait(bars + kResEmpty + rb, ((it_n / L::kRB) & 1) ^ 1, abort_flag, a.status)) goto drain;
     {
+      uint64_t* const res_full = bars + kResFull + rb;
+      uint8_t* const res_at = sm + L::kRes + rb * 2 * kTileBytes;
       const int x = (DKV ? d.h / a.parts : d.h) * D;
       const long long g = (long long)d.tile_start + d.tile;
-      ptx::mbar_arrive_expect_tx(bars + kResFull, 2 * kTileBytes + kRecB + (DKV ? 0 : kRowX));
+      ptx::mbar_arrive_expect_tx(res_full, 2 * kTileBytes + kRecB + (DKV ? 0 : kRowX));
       const int y = (int)(d.tok_start + (long long)d.tile * kTile);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        ptx::tma_load_2d(sm + L::kRes + c * kSlab, res[0], x + 64 * c, y, bars + kResFull);
-        ptx::tma_load_2d(sm + L::kRes + kTileBytes + c * kSlab, res[1], x + 64 * c, y, bars + kResFull);
+        ptx::tma_load_2d(res_at + c * kSlab, res[0], x + 64 * c, y, res_full);
+        ptx::tma_load_2d(res_at + kTileBytes + c * kSlab, res[1], x + 64 * c, y, res_full);
       }
-      ptx::bulk_load(sm + L::kRRec, a.krec + g, kRecB, bars + kResFull);
+      ptx::bulk_load(sm + L::kRRec + rb * kRecB, a.krec + g, kRecB, res_full);
       if (!DKV)
-        ptx::bulk_load(sm + L::kAug, a.rowx + ((long long)d.h * a.n_tiles + g) * kTile, kRowX, bars + kResFull);
-      res_used = true;
-      res_ph = it_n & 1;
+        ptx::bulk_load(sm + L::kAug + rb * kAugB, a.rowx + ((long long)d.h * a.n_tiles + g) * kTile, kRowX, res_full);
       ++it_n;
       Cursor<DKV> cur;
       const int reps = DKV ? a.group / a.parts : 1;
@@ -407,7 +412,8 @@ __device__ void bwd_producer(const BwdArgs& a, const void* const (&res)[2], cons
   }
 drain:
   // every copy issued must land before the CTA exits (only waits after an abort): the rings' last ones
-  if (res_used) bw_drain(bars + kResFull, res_ph);
+  for (uint32_t u = it_n > L::kRB ? it_n - L::kRB : 0; u < it_n; ++u)
+    bw_drain(bars + kResFull + u % L::kRB, (u / L::kRB) & 1);
   for (uint32_t u = n0 > kNS0 ? n0 - kNS0 : 0; u < n0; ++u) bw_drain(bars + kStr0Full + u % kNS0, (u / kNS0) & 1);
   for (uint32_t u = n1 > kNS1 ? n1 - kNS1 : 0; u < n1; ++u) bw_drain(bars + kStr1Full + u % kNS1, (u / kNS1) & 1);
 }
@@ -457,6 +463,7 @@ struct Issuer {
   volatile int* abort_flag;
   int* status;
   uint32_t res0, str0, str1, aug, ones, tmem;
+  uint32_t rb = 0;  // the item's resident buffer
   bool el;  // this lane issues for the warp
   __device__ __forceinline__ Issuer(const BwdArgs& a, uint8_t* smem, uint64_t* b, uint32_t tmem_base, volatile int* ab)
       : sm(smem), bars(b), abort_flag(ab), status(a.status), res0(ptx::smem_u32(smem + L::kRes)),
@@ -467,6 +474,12 @@ struct Issuer {
     ptx::tc_fence_after();
     return true;
   }
+  // the it-th item's resident pair
+  __device__ __forceinline__ bool resident(uint32_t it) {
+    rb = __shfl_sync(0xffffffffu, it % L::kRB, 0);
+    return ready(kResFull + (int)rb, (it / L::kRB) & 1);
+  }
+  __device__ __forceinline__ uint32_t res_at() const { return res0 + rb * 2 * L::kTileBytes; }
   // step s's operands are there, and its S and dP
   __device__ __forceinline__ bool full0(uint32_t s) const { return ready(kStr0Full + (int)(s % kNS0), (s / kNS0) & 1); }
   __device__ __forceinline__ bool full1(uint32_t s) const { return ready(kStr1Full + (int)(s % kNS1), (s / kNS1) & 1); }
@@ -475,21 +488,21 @@ struct Issuer {
   __device__ __forceinline__ uint32_t s_at(uint32_t s) const { return tmem + C::template s_col<DKV>(s & 1); }
   __device__ __forceinline__ void scores_s(uint32_t s) const {
     if (el) {
-      mma_scores<D>(s_at(s), res0, op0(s));
+      mma_scores<D>(s_at(s), res_at(), op0(s));
       if constexpr (DKV) mma_consts(s_at(s), ones, aug + (s % kNS0) * kAugB);
-      else mma_consts(s_at(s), aug, ones);
+      else mma_consts(s_at(s), aug + rb * kAugB, ones);
       ptx::umma_commit(bars + kSFull + (s & 1));
     }
     __syncwarp();
   }
   __device__ __forceinline__ void scores_dp(uint32_t s, bool last) const {
     if (el) {
-      mma_scores<D>(tmem + C::kDP, res0 + L::kTileBytes, op1(s));
+      mma_scores<D>(tmem + C::kDP, res_at() + L::kTileBytes, op1(s));
       if constexpr (DKV) mma_consts(tmem + C::kDP, ones + kAugB, aug + (s % kNS0) * kAugB);
-      else mma_consts(tmem + C::kDP, aug, ones + kAugB);
+      else mma_consts(tmem + C::kDP, aug + rb * kAugB, ones + kAugB);
       ptx::umma_commit(bars + kDpFull);
       if constexpr (!DKV) ptx::umma_commit(bars + kStr1Empty + s % kNS1);
-      if (last) ptx::umma_commit(bars + kResEmpty);  // the resident pair read for the last time
+      if (last) ptx::umma_commit(bars + kResEmpty + rb);  // the resident pair read for the last time
     }
     __syncwarp();
   }
@@ -507,13 +520,13 @@ struct Issuer {
 template <int D, bool DKV>
 __device__ void bwd_issue_scores(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem_base,
                                  volatile int* abort_flag) {
-  const Issuer<D, DKV> q(a, sm, bars, tmem_base, abort_flag);
+  Issuer<D, DKV> q(a, sm, bars, tmem_base, abort_flag);
   uint32_t it_n = 0, step = 0, it_cnt = 0;
   BwdItemDesc it;
   while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
     const int n = __shfl_sync(0xffffffffu, it.n, 0);
     if (n <= 0) continue;
-    if (!q.ready(kResFull, (it_n++) & 1)) goto out;
+    if (!q.resident(it_n++)) goto out;
     for (int j = 0; j < n; ++j, ++step) {
       const uint32_t s = __shfl_sync(0xffffffffu, step, 0);
       // S's buffer: free when the accumulation of the step before last has read it
@@ -569,13 +582,13 @@ out:
 template <int D>
 __device__ void bwd_issue_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem_base, volatile int* abort_flag) {
   using C = BCfg<D>;
-  const Issuer<D, true> q(a, sm, bars, tmem_base, abort_flag);
+  Issuer<D, true> q(a, sm, bars, tmem_base, abort_flag);
   uint32_t it_n = 0, step = 0, it_cnt = 0;
   BwdItemDesc it;
   while (next_item<D>(sm, bars, it_cnt, it, abort_flag, a.status)) {
     const int n = __shfl_sync(0xffffffffu, it.n, 0);
     if (n <= 0) continue;
-    if (!q.ready(kResFull, it_n & 1)) goto out;
+    if (!q.resident(it_n)) goto out;
     {
       const uint32_t s0 = __shfl_sync(0xffffffffu, step, 0);
       if (!q.full0(s0)) goto out;
@@ -734,9 +747,10 @@ __device__ void bwd_compute_dq(const BwdArgs& a, uint8_t* sm, uint64_t* bars, ui
     WarpCursor<false> cur;
     cur.init(a, it, it.n);
     // the row's time, loaded with Q'
-    if (!wb.wait(kResFull, it_n & 1)) return;
-    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec)->t[row] - it.t_ref);
-    wb.arrive(kResEmpty);
+    const int rb = (int)(it_n % BL::kRB);
+    if (!wb.wait(kResFull + rb, (it_n / BL::kRB) & 1)) return;
+    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec + rb * kRecB)->t[row] - it.t_ref);
+    wb.arrive(kResEmpty + rb);
     cur.vote();
     for (int j = 0; j < it.n; ++j, ++step) {
       // this thread's 32 keys (FULL: the constants of rows past the request's end and of rows that see
@@ -875,8 +889,9 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
     }
     WarpCursor<true> cur;
     cur.init(a, it, it.n / reps);
-    if (!wb.wait(kResFull, it_n & 1)) return;  // the key tile's record
-    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec)->t[row] - it.t_ref);
+    const int rb = (int)(it_n % BL::kRB);
+    if (!wb.wait(kResFull + rb, (it_n / BL::kRB) & 1)) return;  // the key tile's record
+    const float dt = (float)(reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec + rb * kRecB)->t[row] - it.t_ref);
     cur.vote();
     for (int j = 0; j < it.n; ++j, ++step) {
       // The key's bits for this thread's 32 queries: its word of the mask table's columns when the
@@ -900,7 +915,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
             int tyq;
             rec_row(reinterpret_cast<const KeyTileRec*>(rec), row, tq, tyq);
             const uint4 vm = built_mask(a.mask, qi < it.len, qi, tq, tyq,
-                                        reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec), it.tile * kTile);
+                                        reinterpret_cast<const KeyTileRec*>(sm + BL::kRRec + rb * kRecB), it.tile * kTile);
             const uint32_t w[4] = {vm.x, vm.y, vm.z, vm.w};
 #pragma unroll
             for (int wd = 0; wd < 4; ++wd) col[(32 * wd + lane) * 4 + quad] = transpose32(w[wd], lane);
@@ -911,7 +926,7 @@ __device__ void bwd_compute_dkv(const BwdArgs& a, uint8_t* sm, uint64_t* bars, u
         __syncwarp();
       }
       if (j == it.n - 1) {  // the key tile's record was read for the last time
-        wb.arrive(kResEmpty);
+        wb.arrive(kResEmpty + rb);
       }
       cur.next(a, reps);
       // P^T over the columns of S^T already read
@@ -1222,8 +1237,10 @@ __global__ void __launch_bounds__(BCfg<D>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars) + 1;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bars + kResFull, 1);
-    ptx::mbar_init(bars + kResEmpty, 1 + kCW);  // MMAs done + the compute warps read the record
+    for (int i = 0; i < BL::kRB; ++i) {
+      ptx::mbar_init(bars + kResFull + i, 1);
+      ptx::mbar_init(bars + kResEmpty + i, 1 + kCW);  // MMAs done + the compute warps read the record
+    }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(bars + kStr0Full + i, 1);
       ptx::mbar_init(bars + kStr0Empty + i, 1);  // the step's last MMA done (the record was read before it)
