@@ -1092,26 +1092,32 @@ __global__ void __launch_bounds__(1024) k_bwd_kv_items(BwdSchedArgs s) {
   }
 }
 
-// Threads [0, n_tiles): the transposed tile lists -- for key tile g, the query tiles
-// of its request whose class against it is not SKIP, in order.  Threads
+// Warps [0, n_tiles): the transposed tile lists -- for key tile g, the query tiles
+// of its request whose class against it is not SKIP, in order.  Warps
 // [n_tiles, n_tiles + n_items): the descriptors of item w for both modes (DKV: the
-// mirrored key tile of the item's query tile, for the first n_kv_items threads).
+// mirrored key tile of the item's query tile, for the first n_kv_items warps).  Lanes take 32 tiles of
+// a column of the class matrix at a time (a thread each took 32 us at 64 tiles, 6 now).
 __global__ void __launch_bounds__(128) k_bwd_schedule(BwdSchedArgs s) {
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (i < s.n_tiles) {
     const ReqMeta m = s.meta[s.qreq[i]];
     const int kt = (int)(i - m.tile_start);
     uint32_t* out = s.qlist + m.cls_start + (long long)kt * m.ntiles;
     int* out_slot = s.qslot + m.cls_start + (long long)kt * m.ntiles;
     int n = 0;
-    for (int qt = 0; qt < m.ntiles; ++qt) {
+    for (int q0 = 0; q0 < m.ntiles; q0 += 32) {
+      const int qt = q0 + lane;
       const long long pair = m.cls_start + (long long)qt * m.ntiles + kt;
-      const int c = s.cls[pair];
-      if (c == REC_ATTN_TILE_SKIP) continue;
-      out[n] = (uint32_t)qt | ((uint32_t)c << 24);
-      const int p = c == REC_ATTN_TILE_PARTIAL ? s.pslot[pair] : -1;
-      out_slot[n] = (p >= 0 && p < s.mcap) ? p : -1;  // a slot always indexes the table
-      ++n;
+      const int c = qt < m.ntiles ? s.cls[pair] : REC_ATTN_TILE_SKIP;
+      const unsigned bal = __ballot_sync(0xffffffffu, c != REC_ATTN_TILE_SKIP);
+      if (c != REC_ATTN_TILE_SKIP) {
+        const int at = n + __popc(bal & ((1u << lane) - 1u));
+        out[at] = (uint32_t)qt | ((uint32_t)c << 24);
+        const int p = c == REC_ATTN_TILE_PARTIAL ? s.pslot[pair] : -1;
+        out_slot[at] = (p >= 0 && p < s.mcap) ? p : -1;  // a slot always indexes the table
+      }
+      n += __popc(bal);
     }
     return;
   }
@@ -1132,7 +1138,7 @@ __global__ void __launch_bounds__(128) k_bwd_schedule(BwdSchedArgs s) {
   d.list = m.cls_start + (long long)qt * m.ntiles;
   d.tile = qt;
   d.n = max(s.kcount[g], 0);
-  s.desc[w] = d;
+  if (lane == 0) s.desc[w] = d;
   if (w >= s.n_kv_items) return;
   if (s.reps > 1) {  // dK/dV item w has a tile and heads of its own
     const int Hp = s.heads / s.reps;
@@ -1147,11 +1153,14 @@ __global__ void __launch_bounds__(128) k_bwd_schedule(BwdSchedArgs s) {
   }
   const uint8_t* col = s.cls + m.cls_start + kt;
   int n = 0;
-  for (int r = 0; r < m.ntiles; ++r) n += col[(long long)r * m.ntiles] != REC_ATTN_TILE_SKIP;
+  for (int r0 = 0; r0 < m.ntiles; r0 += 32) {
+    const int r = r0 + lane;
+    n += __popc(__ballot_sync(0xffffffffu, r < m.ntiles && col[(long long)r * m.ntiles] != REC_ATTN_TILE_SKIP));
+  }
   d.list = m.cls_start + (long long)kt * m.ntiles;
   d.tile = kt;
   d.n = n * s.reps;
-  s.desc[s.n_items + w] = d;
+  if (lane == 0) s.desc[s.n_items + w] = d;
 }
 
 // The mask table's columns (once per plan): per slot, each warp transposes its 32 query
@@ -1363,7 +1372,7 @@ cudaError_t launch_bwd_schedule(const BwdSchedArgs& s, int num_sms, cudaStream_t
     const cudaError_t ek = cudaGetLastError();
     if (ek != cudaSuccess) return ek;
   }
-  k_bwd_schedule<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(s);
+  k_bwd_schedule<<<(unsigned)((n + 3) / 4), 128, 0, st>>>(s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || s.mcap <= 0) return e;
   k_bwd_colmask<<<s.mcap < 8 * num_sms ? s.mcap : 8 * num_sms, kTile, 0, st>>>(s);
