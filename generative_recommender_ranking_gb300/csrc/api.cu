@@ -1062,6 +1062,8 @@ REC_ATTN_API rec_attn_status rec_attn_fwd_compress(rec_attn_plan_t* plan, const 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return from_cuda(e);
   if (dev != plan->device) return REC_ATTN_ERR_INVALID_ARG;
+  // (before the tables below enter the capture: they are copied from this call's own memory)
+  if (plan->grouped && capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaMemPool_t pool;
   char* buf = nullptr;
