@@ -759,6 +759,8 @@ REC_ATTN_API rec_attn_status rec_attn_bwd_fused(rec_attn_plan_t* plan, const voi
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return from_cuda(e);
   if (dev != plan->device) return REC_ATTN_ERR_INVALID_ARG;
+  // (before the gate's kernel, which writes dout_gate, enters the capture)
+  if (plan->grouped && capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0) return bwd_impl(plan, q, k, v, out, lse, dout, dout, dq, dk, dv, stream, nullptr);
   // scratch: the attention's dO (with an output gate) and the gradients of the gated,

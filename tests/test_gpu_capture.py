@@ -77,3 +77,42 @@ def test_compressed_forward(case):
     call()  # the same call outside the capture is taken
     torch.cuda.synchronize()
     assert bd.rec_attn_device_status(c["plan"]) == bd.OK and torch.isfinite(x).all() and not (t == -7).any()
+
+
+def test_fused_backward(case):
+    c = case
+    f = dict(out_gate=torch.randn_like(c["q"]), k_norm_weight=torch.ones(HK, c["k"].shape[2], device="cuda"))
+    o, lse = torch.empty_like(c["o"]), torch.empty_like(c["lse"])
+    bd.rec_attn_fwd_fused(c["plan"], c["q"], c["k"], c["v"], o, lse, **f)
+    torch.cuda.synchronize()
+    outs = dict(dout_gate=torch.full_like(c["q"], 7.0), dk_norm_weight=torch.full_like(f["k_norm_weight"], 7.0))
+    dq, dk, dv = (torch.full_like(c[x], 7.0) for x in "qkv")
+    call = lambda s=None: bd.rec_attn_bwd_fused(c["plan"], c["q"], c["k"], c["v"], o, lse, c["do"], dq, dk, dv, stream=s, **f,
+                                                **outs)
+    assert captured(call) == (bd.ERR_UNSUPPORTED, 0)
+    torch.cuda.synchronize()
+    assert all((x == 7).all() for x in (dq, dk, dv, *outs.values()))
+    call()  # the same call outside the capture is taken
+    torch.cuda.synchronize()
+    assert bd.rec_attn_device_status(c["plan"]) == bd.OK
+    assert all(torch.isfinite(x).all() and not (x == 7).all() for x in (dq, dk, dv, *outs.values()))
+
+
+def test_the_other_calls(case):
+    c, w = case, case["w"]
+    dq, dk, dv = (torch.empty_like(c[x]) for x in "qkv")
+    gate = torch.ones_like(c["q"])
+    f32 = bd.make_params(8, 64, dtype="fp32")
+    q1, k1, o1 = c["q"][:2].float(), c["k"][:2].float(), torch.empty_like(c["q"][:2]).float()
+    hist = (w.offsets, c["t"], c["ty"], c["k"].float(), c["v"].float(), 1)
+    cands = np.arange(len(w.offsets), dtype=np.int64)
+    with bd.rec_attn_cache_create_grouped(f32, HK, *hist) as cache:
+        for call in (
+                lambda s: bd.rec_attn_plan_grouped(gu.params_for(w), HK, c["off_h"], c["off_d"], c["t"], c["ty"], stream=s),
+                lambda s: bd.rec_attn_cache_create_grouped(f32, HK, *hist, stream=s),
+                lambda s: bd.rec_attn_cache_score(cache, cands, c["t"], q1, k1, k1, o1, stream=s),
+                lambda s: bd.rec_attn_fwd(c["plan"], c["q"], c["k"], c["v"], c["o"], c["lse"], stream=s),
+                lambda s: bd.rec_attn_fwd_fused(c["plan"], c["q"], c["k"], c["v"], c["o"], c["lse"], stream=s,
+                                                out_gate=gate),
+                lambda s: bd.rec_attn_bwd(c["plan"], c["q"], c["k"], c["v"], c["o"], c["lse"], c["do"], dq, dk, dv, stream=s)):
+            assert captured(call) == (bd.ERR_UNSUPPORTED, 0)
