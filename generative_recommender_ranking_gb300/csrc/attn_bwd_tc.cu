@@ -166,8 +166,7 @@ __device__ __forceinline__ bool bw_wait(uint64_t* bar, uint32_t parity, volatile
 }
 __device__ __forceinline__ bool bw_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                              int* status) {
-  const bool ok = bw_wait(bar, parity, abort_flag, status);
-  return __all_sync(0xffffffffu, ok);
+  return bounded_wait_warp(bar, parity, abort_flag, status, kWaitNsB);
 }
 // The compute warps' barriers by their shared-memory address (32 bits: a step has few instructions).
 struct WarpBars {

@@ -168,8 +168,7 @@ __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                               int* status) {
-  const bool ok = wait_bar(bar, parity, abort_flag, status);
-  return __all_sync(0xffffffffu, ok);
+  return bounded_wait_warp(bar, parity, abort_flag, status, kWaitNs);
 }
 
 // Packed fp32 pairs for the fma.rn.f32x2 instruction.

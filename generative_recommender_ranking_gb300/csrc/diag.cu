@@ -1,4 +1,4 @@
-// diag.cu -- self-check of the bounded wait the attention kernels use: one CTA waits on
+// diag.cu -- self-check of the bounded waits the attention kernels use: one CTA waits on
 // an mbarrier that nothing ever arrives at, so the wait must give up after its limit,
 // record REC_ATTN_ERR_TIMEOUT in a status word and return, leaving the context usable.
 #include <cuda_runtime.h>
@@ -19,13 +19,15 @@ __global__ void k_wait_timeout(int* status, unsigned long long limit_ns) {
     ptx::fence_barrier_init();
   }
   __syncthreads();
-  if (threadIdx.x == 0) bounded_wait(&bar, 0, &abort_flag, status, limit_ns);  // no arrival ever comes
+  // no arrival ever comes: a whole warp waits, and one lane of another
+  if (threadIdx.x < 32) bounded_wait_warp(&bar, 0, &abort_flag, status, limit_ns);
+  else if (threadIdx.x == 32) bounded_wait(&bar, 0, &abort_flag, status, limit_ns);
 }
 
 }  // namespace
 
 cudaError_t launch_wait_timeout(int* status, unsigned long long limit_ns, cudaStream_t st) {
-  k_wait_timeout<<<1, 32, 0, st>>>(status, limit_ns);
+  k_wait_timeout<<<1, 64, 0, st>>>(status, limit_ns);
   return cudaGetLastError();
 }
 

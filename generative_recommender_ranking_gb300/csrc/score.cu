@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
       const bool any = pos0 < hist_len;
       const bool masked = any && (pos0 + C::kWarpKeys > hist_len ||
                                   a.block_need[a.block_off[it.b] + pos0 / kNeedBlock] > t_lo);
-      if (!bounded_wait(s_full + st, (kt / kScoreStages) & 1, abort_flag, a.status, kScoreWaitNs)) break;
+      if (!bounded_wait_warp(s_full + st, (kt / kScoreStages) & 1, abort_flag, a.status, kScoreWaitNs)) break;
       if (any) {
         const uint32_t kb = ptx::smem_u32(sm + st * 2 * kOperand), vb = kb + kOperand;
         float s[M][C::kNT][4];

@@ -29,4 +29,13 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, vol
   }
 }
 
+// The same for a whole warp, whose lanes leave together: at the limit, or when another warp raises the
+// abort flag, one lane may give up while the next sees the phase complete, and a warp that splits
+// there would meet in no later shuffle or matrix instruction again.
+__device__ __forceinline__ bool bounded_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                  uint64_t limit_ns) {
+  const bool ok = bounded_wait(bar, parity, abort_flag, status, limit_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+
 }  // namespace recattn
