@@ -185,9 +185,7 @@ struct WarpBars {
   }
 };
 __device__ __forceinline__ void bw_drain(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar, parity))
-    if (ptx::globaltimer() - t0 > kWaitNsB / 4) return;
+  bounded_drain(bar, parity, kWaitNsB / 4);
 }
 
 // A published item: its descriptor (as three 16-byte words) and the end flag.

@@ -162,9 +162,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   return bounded_wait(bar, parity, abort_flag, status, kWaitNs);
 }
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar, parity))
-    if (ptx::globaltimer() - t0 > kWaitNs / 4) return;
+  bounded_drain(bar, parity, kWaitNs / 4);
 }
 __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                               int* status) {

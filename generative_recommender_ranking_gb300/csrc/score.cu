@@ -244,15 +244,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
 
   if (warp == kScoreWarps) {
     if (lane == 0) {
-      for (int t = tile0; t < tile1; ++t) {
-        const int k = t - tile0, st = k % kScoreStages;
+      int k = 0;  // tiles loaded
+      for (; tile0 + k < tile1; ++k) {
+        const int t = tile0 + k, st = k % kScoreStages;
         const uint32_t ph = (k / kScoreStages) & 1;
-        if (!bounded_wait(s_empty + st, ph ^ 1, abort_flag, a.status, kScoreWaitNs)) {
-          // copies in flight land before the block leaves
-          for (int j = max(0, k - kScoreStages); j < k; ++j)
-            for (int w = 0; w < 1 << 20 && !ptx::mbar_try_wait(s_full + j % kScoreStages, (j / kScoreStages) & 1); ++w) {}
-          break;
-        }
+        if (!bounded_wait(s_empty + st, ph ^ 1, abort_flag, a.status, kScoreWaitNs)) break;
         ptx::mbar_arrive_expect_tx(s_full + st, 2 * kOperand);
         uint8_t* kb = sm + st * 2 * kOperand;
         const int y = (int)(hist0 + (long long)t * C::kKeys);
@@ -262,6 +258,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
           ptx::tma_load_2d(kb + kOperand + c * C::kSlab, &tm_v, it.hk * D + c * 64, y, s_full + st);
         }
       }
+      // the last copies land before the stages take the warps' outputs and the block leaves (the
+      // consumers may have given up on them)
+      for (int j = max(0, k - kScoreStages); j < k; ++j)
+        bounded_drain(s_full + j % kScoreStages, (j / kScoreStages) & 1, kScoreWaitNs / 4);
     }
   }
 

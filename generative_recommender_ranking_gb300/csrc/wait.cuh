@@ -38,4 +38,12 @@ __device__ __forceinline__ bool bounded_wait_warp(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, ok);
 }
 
+// Wait for a copy (or matrix instructions) of the thread's own to finish before the CTA reuses what they
+// write, or leaves.  Bounded too; it waits in earnest only after an abort.
+__device__ __forceinline__ void bounded_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (ptx::globaltimer() - t0 > limit_ns) return;
+}
+
 }  // namespace recattn

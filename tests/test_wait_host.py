@@ -42,3 +42,21 @@ def test_waits_of_whole_warps_are_voted_on(path):
     # the wrappers' own whole-warp forms vote
     for name, body in re.findall(r"bool (\w+_warp)\([^{}]*\)\s*(\{[^}]*\})", text):
         assert "bounded_wait_warp(" in body, name
+
+
+def test_scoring_waits_for_its_copies():
+    """The few-row scoring kernel's loading thread waits for its last copies after its loop, however that
+    ended: consumers that gave up on a tile write their outputs over the stages it lands in."""
+    text = code(os.path.join(bld.CSRC, "score.cu"))
+    loader = block(text, text.index("if (warp == kScoreWarps)"))
+    at = loader.index("for (")  # the tiles
+    loop = block(loader, at)
+    assert "tma_load_2d(" in loop and "tma_load_2d(" not in loader.replace(loop, "")
+    after = loader[loader.index(loop) + len(loop):]
+    drain = re.search(r"for \(int j = max\(0, k - (\w+)\); j < k; \+\+j\)\s*bounded_drain\(s_full \+ j % \1, \(j / \1\) & 1, ", after)
+    assert drain and drain.group(1) == "kScoreStages"
+    # those waits cover every copy that may still be in flight: all but the ones whose stage was refilled
+    for n in range(20):
+        for stages in (2, 3, 4):
+            last_use = {j % stages: (j // stages) & 1 for j in range(n)}
+            assert {j % stages: (j // stages) & 1 for j in range(max(0, n - stages), n)} == last_use
