@@ -28,17 +28,19 @@ struct FwdSmem {
   simt::Tokens tq, tk;
 };
 
-template <int D>
-__global__ void __launch_bounds__(simt::kThreads) k_attn_simt(AttnArgs a) {
+// One block's rows; false, with nothing written, when an output is not finite and HIDE is off.  HIDE: the
+// pairs that the mask hides are left out of the product with V instead of weighted with 0.
+template <int D, bool HIDE>
+__device__ __forceinline__ bool attend(const AttnArgs& a) {
   using namespace simt;
   constexpr int N = D / 16;
   extern __shared__ __align__(16) unsigned char smem[];
   FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem);
   const WorkItem it = decode_item(a, blockIdx.x / kPerTile, true);  // (the heaviest first)
-  if (it.n < 0) return;  // every query of the tile is pruned
+  if (it.n < 0) return true;  // every query of the tile is pruned
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int pos0 = it.qt * kTile + (int)(blockIdx.x % kPerTile) * kB;
-  if (pos0 >= it.m.len) return;
+  if (pos0 >= it.m.len) return true;
   const int H = a.heads, Hk = H / a.group, hk = it.h / a.group;
   const long long tok0 = it.m.tok_start + pos0;
   load_tile<D>(static_cast<const float*>(a.q) + (tok0 * H + it.h) * D, (long long)H * D, it.m.len - pos0, a.scale, sm.q, nullptr);
@@ -112,8 +114,9 @@ __global__ void __launch_bounds__(simt::kThreads) k_attn_simt(AttnArgs a) {
       l[i] *= corr[i];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        x[i][c] = expf(x[i][c] - m_use);
-        l[i] += x[i][c];  // this thread's columns; summed over the row at the end
+        const float p = expf(x[i][c] - m_use);
+        l[i] += p;  // this thread's columns; summed over the row at the end
+        x[i][c] = HIDE && x[i][c] == -INFINITY ? kHidden : p;
       }
     }
     store_scores(sm.p, ty, tx, x);
@@ -125,9 +128,19 @@ __global__ void __launch_bounds__(simt::kThreads) k_attn_simt(AttnArgs a) {
         o[p][c] = pair(v.x * corr[2 * p], v.y * corr[2 * p + 1]);
       }
     __syncthreads();
-    accumulate<D>(sm.p, sm.v, ty, tx, o);
+    if constexpr (HIDE) accumulate_seen<D>(sm.p, sm.v, ty, tx, o);
+    else accumulate<D>(sm.p, sm.v, ty, tx, o);
   }
-  __syncthreads();  // (an item without a key: the query rows' types are there)
+  bool finite = true;
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float2 v = both(o[p][c]);
+      finite = finite && fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY;
+    }
+  // (the barrier also serves an item without a key: the query rows' types are there)
+  if (__syncthreads_or(!finite) && !HIDE) return false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ty + i, pi = pos0 + r;
@@ -146,6 +159,20 @@ __global__ void __launch_bounds__(simt::kThreads) k_attn_simt(AttnArgs a) {
     }
     if (a.lse && tx == 0) a.lse[row] = sum > 0.f ? m[i] + logf(sum) : -INFINITY;
   }
+  return true;
+}
+
+// Not inlined: rare, and its registers would be taken from the usual pass.
+template <int D>
+__device__ __noinline__ void attend_hiding(const AttnArgs& a) {
+  attend<D, true>(a);
+}
+
+// A value that is not finite is to reach the rows that see its key alone, but 0 times it is NaN: a block
+// whose outputs are not all finite computes them once more, which costs the others nothing.
+template <int D>
+__global__ void __launch_bounds__(simt::kThreads, 2) k_attn_simt(const __grid_constant__ AttnArgs a) {
+  if (!attend<D, false>(a)) attend_hiding<D>(a);
 }
 
 template <int D>

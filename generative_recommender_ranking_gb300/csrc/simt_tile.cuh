@@ -118,6 +118,28 @@ __device__ __forceinline__ void accumulate(const float* P, const float* V, int t
   }
 }
 
+// The same without the pairs whose weight is -0, the mark of a pair that the mask hides: for rows of V
+// with values that are not finite.
+constexpr float kHidden = -0.f;
+template <int D>
+__device__ __forceinline__ void accumulate_seen(const float* P, const float* V, int ty, int tx, f2 (&o)[2][D / 16]) {
+  constexpr int N = D / 16;
+#pragma unroll 1
+  for (int c = 0; c < kB; ++c) {
+    const float4 p = *reinterpret_cast<const float4*>(P + at(ty, c));
+    auto add = [](float w, float v, float y) {
+      return __float_as_uint(w) == __float_as_uint(kHidden) ? y : fmaf(w, v, y);
+    };
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float v = V[c * D + N * tx + j];
+      const float2 a = both(o[0][j]), b = both(o[1][j]);
+      o[0][j] = pair(add(p.x, v, a.x), add(p.y, v, a.y));
+      o[1][j] = pair(add(p.z, v, b.x), add(p.w, v, b.y));
+    }
+  }
+}
+
 // A row over the 16 threads that share it.
 __device__ __forceinline__ float row_max(float x) {
 #pragma unroll
