@@ -59,23 +59,26 @@ struct Chunk<float> {
 
 // One (token, chunk) unit of the prologue: K' and, when WQ, Q' for every head.  The
 // first four heads' 16-byte loads go out before the angle math (they do not depend on
-// the time), later heads four at a time, all kept raw until used.
-template <typename E, bool WQ>
+// the time), later heads four at a time, all kept raw until used.  SHARED: the query heads
+// share key heads (as an instantiation of its own: tests of the key heads in every plan's
+// prologue took 10 to 13% of its time; mtgr 50 -> 56 us).
+template <typename E, bool WQ, bool SHARED>
 __device__ __forceinline__ void rope_rows(const RopeArgs& a, const char* __restrict__ q, const char* __restrict__ k,
                                           char* __restrict__ qr, char* __restrict__ kr, long long head_bytes,
                                           long long tok, int c, long long t_ref) {
   using C = Chunk<E>;
   constexpr int kPairs = C::kPairs;
   const long long row0 = tok * a.heads * head_bytes + (long long)c * 16;
-  const long long krow0 = tok * a.kv_heads * head_bytes + (long long)c * 16;
-  const int nh = WQ ? a.heads : a.kv_heads;
+  const int kv_heads = SHARED ? a.kv_heads : a.heads;
+  const long long krow0 = tok * kv_heads * head_bytes + (long long)c * 16;
+  const int nh = WQ ? a.heads : kv_heads;
   uint4 rq[4], rk[4];  // raw 16-byte chunks of four heads
   auto load4 = [&](int h0) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (h0 + u < nh) {
         if constexpr (WQ) rq[u] = *reinterpret_cast<const uint4*>(q + row0 + (h0 + u) * head_bytes);
-        if (h0 + u < a.kv_heads) rk[u] = *reinterpret_cast<const uint4*>(k + krow0 + (h0 + u) * head_bytes);
+        if (!SHARED || h0 + u < kv_heads) rk[u] = *reinterpret_cast<const uint4*>(k + krow0 + (h0 + u) * head_bytes);
       }
   };
   load4(0);
@@ -99,7 +102,7 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, const char* __restr
         }
         C::store(qr + row0 + (h0 + u) * head_bytes, x);
       }
-      if (h0 + u >= a.kv_heads) continue;  // the key heads come first, query heads may be more
+      if (SHARED && h0 + u >= kv_heads) continue;  // the key heads come first, query heads may be more
       float y[8];
       C::unpack(rk[u], y);
 #pragma unroll
@@ -117,7 +120,7 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, const char* __restr
 // so each angle's sin/cos is computed once per token.  A block covers 256 / chunks
 // tokens of one tile (chunks = 16-byte chunks per head row, 8 or 16), so a tile takes
 // chunks / 2 blocks and each thread one unit (`rope_rows`).
-template <typename E>
+template <typename E, bool SHARED>
 __global__ void __launch_bounds__(256, 4) k_rope(RopeArgs a) {
   using C = Chunk<E>;
   constexpr int kPairs = C::kPairs;
@@ -140,8 +143,8 @@ __global__ void __launch_bounds__(256, 4) k_rope(RopeArgs a) {
   const long long t_ref = a.t[m.tok_start];
   // a plan in which no user token queries never reads their Q' rows (their query tiles
   // are skipped or their rows are computed and not written), so they are not rotated
-  if (a.skip_user_q && is_user(a.ty[tok])) rope_rows<E, false>(a, q, k, qr, kr, head_bytes, tok, c, t_ref);
-  else rope_rows<E, true>(a, q, k, qr, kr, head_bytes, tok, c, t_ref);
+  if (a.skip_user_q && is_user(a.ty[tok])) rope_rows<E, false, SHARED>(a, q, k, qr, kr, head_bytes, tok, c, t_ref);
+  else rope_rows<E, true, SHARED>(a, q, k, qr, kr, head_bytes, tok, c, t_ref);
 }
 
 // Sum of v over the `group` consecutive lanes that hold one head row (group is a
@@ -179,7 +182,7 @@ __device__ __forceinline__ void norm_gate(float (&x)[8], bool act, const float* 
 // sigmoid gate on Q and K, then the rotation (omega all zero: none).  Every lane of
 // a warp runs every iteration (inactive lanes carry zeros), so the row sums can use
 // warp shuffles over the lanes of one row.
-template <typename E>
+template <typename E, bool SHARED>
 __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) {
   using C = Chunk<E>;
   constexpr int kPairs = C::kPairs;
@@ -199,7 +202,8 @@ __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) 
     const int r = act ? rr : 0, c = (int)threadIdx.x % chunks;
     const long long tok = m.tok_start + tl * kTile + r;
     const long long row0 = tok * a.heads * head_bytes + (long long)c * 16;
-    const long long krow0 = tok * a.kv_heads * head_bytes + (long long)c * 16;
+    const int kv_heads = SHARED ? a.kv_heads : a.heads;
+    const long long krow0 = tok * kv_heads * head_bytes + (long long)c * 16;
     const bool qg = f.q_gate != nullptr, kg = f.k_gate != nullptr;
     // two heads at a time: their q, k and gate chunks (up to eight 16-byte loads) in flight
     // together, kept raw until used; the first two heads' loads go out before the angles
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) 
           const long long off = row0 + (h0 + u) * head_bytes, koff = krow0 + (h0 + u) * head_bytes;
           rq[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + off);
           if (qg) rgq[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(f.q_gate) + off);
-          if (h0 + u < a.kv_heads) {
+          if (!SHARED || h0 + u < kv_heads) {
             rk[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + koff);
             if (kg) rgk[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(f.k_gate) + koff);
           }
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(256, 3) k_rope_fused(RopeArgs a, FusedArgs f) 
         C::unpack(rgk[u], gy);
         const int e0 = h * a.head_dim + c * 2 * kPairs;
         norm_gate<E>(x, act, f.q_norm_w, f.eps, qg, gx, e0, chunks, a.head_dim);
-        const bool has_k = h < a.kv_heads;  // uniform across the block
+        const bool has_k = !SHARED || h < kv_heads;  // uniform across the block
         if (has_k) norm_gate<E>(y, act, f.k_norm_w, f.eps, kg, gy, e0, chunks, a.head_dim);
 #pragma unroll
         for (int p = 0; p < kPairs; ++p) {
@@ -382,8 +386,10 @@ cudaError_t launch_rope_fused(const RopeArgs& a, const FusedArgs& f, int dtype, 
   if (n_tiles <= 0) return cudaSuccess;
   const int chunks = a.head_dim * (dtype == REC_ATTN_BF16 ? 2 : 4) / 16;
   const unsigned blocks = (unsigned)(n_tiles * (chunks / 2));  // 256 / chunks tokens per block
-  if (dtype == REC_ATTN_BF16) k_rope_fused<__nv_bfloat16><<<blocks, 256, 0, st>>>(a, f);
-  else k_rope_fused<float><<<blocks, 256, 0, st>>>(a, f);
+  const bool shared = a.kv_heads != a.heads;
+  auto fn = dtype == REC_ATTN_BF16 ? (shared ? k_rope_fused<__nv_bfloat16, true> : k_rope_fused<__nv_bfloat16, false>)
+                                   : (shared ? k_rope_fused<float, true> : k_rope_fused<float, false>);
+  fn<<<blocks, 256, 0, st>>>(a, f);
   return cudaGetLastError();
 }
 
@@ -392,8 +398,10 @@ cudaError_t launch_rope(const RopeArgs& a, int dtype, long long n_tiles, cudaStr
   // 256 threads = 256 / chunks tokens per block, chunks / 2 blocks per tile
   const int chunks = a.head_dim * (dtype == REC_ATTN_BF16 ? 2 : 4) / 16;
   const unsigned blocks = (unsigned)(n_tiles * (chunks / 2));
-  if (dtype == REC_ATTN_BF16) k_rope<__nv_bfloat16><<<blocks, 256, 0, st>>>(a);
-  else k_rope<float><<<blocks, 256, 0, st>>>(a);
+  const bool shared = a.kv_heads != a.heads;
+  auto fn = dtype == REC_ATTN_BF16 ? (shared ? k_rope<__nv_bfloat16, true> : k_rope<__nv_bfloat16, false>)
+                                   : (shared ? k_rope<float, true> : k_rope<float, false>);
+  fn<<<blocks, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
