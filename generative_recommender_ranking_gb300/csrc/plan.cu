@@ -634,8 +634,12 @@ cudaError_t launch_plan(const MaskP& mp, int heads, const PlanDev& pd, const lon
   // 1/8: request by request, each request's keys are read from memory about once, which sorting all
   // tiles by cost would give up.  (One causal request of 20001 tokens, 8 heads, forward:
   // 529 us in the requests' order, 459 sorted; two of 8192 and 7000 tokens, forward and backward 763
-  // and 643; sixteen of 20001: no item is that large, the order stays.)
-  const long long heavy_den = 2LL * sms * (kv_bytes <= (64ull << 20) ? 32 : 8);
+  // and 643; sixteen of 20001: no item is that large, the order stays.)  Two cases
+  // keep the requests' order.  Items that all run at once gain nothing from another (one request of sort:
+  // forward 49 us, sorted 53, and 3 us more to plan).  A query-pruned plan computes so few tiles that most
+  // of them would count as heavy (attention of mtgr with 64 user queries kept: 104 us, sorted 108).
+  const bool in_order = mp.keep_user >= 0 || n_tiles * heads <= 2LL * sms;
+  const long long heavy_den = in_order ? 1 : 2LL * sms * (kv_bytes <= (64ull << 20) ? 32 : 8);
   if (mean_tiles >= kSplitTiles) {
     slices = (2LL * sms + batch - 1) / batch;
     if (slices > mean_tiles) slices = mean_tiles;
