@@ -371,7 +371,6 @@ REC_ATTN_API rec_attn_status rec_attn_plan_grouped(const rec_attn_params* params
                                                    void* stream, rec_attn_plan_t** plan_out) {
   if (plan_out) *plan_out = nullptr;
   if (keep_user_queries < -1) return REC_ATTN_ERR_INVALID_ARG;
-  if (plan_out) *plan_out = nullptr;
   if (capturing(stream)) return REC_ATTN_ERR_UNSUPPORTED;  // its tables are staged from the call's own memory
   try {
     const rec_attn_status s = plan_impl(params, num_kv_heads, keep_user_queries, batch, offsets_host, offsets_dev,

@@ -565,7 +565,8 @@ NormKernel norm_dir(bool bwd) {
 }
 template <typename E>
 NormKernel norm_kernel(const NormShape& s, bool bwd) {
-  if (s.nv > 2) return norm_dir<E, 4, 32, false, 1024, 1>(bwd);
+  if constexpr (sizeof(E) == 4)  // (the widest bf16 rows are 32 KB)
+    if (s.nv > 2) return norm_dir<E, 4, 32, false, 1024, 1>(bwd);
   if (s.threads > 512) return norm_dir<E, 2, 32, false, 1024, 2>(bwd);
   if (s.threads > kNormThreads) return norm_dir<E, 2, 32, false, 512, 2>(bwd);
   if (s.tpr == 8) return norm_dir<E, 2, 8, false, kNormThreads, 2>(bwd);
