@@ -577,6 +577,9 @@ rec_attn_status bwd_impl(rec_attn_plan_t* plan, const void* q, const void* k, co
   const bool dim_ok = p.dtype == REC_ATTN_BF16 ? (p.head_dim == 64 || p.head_dim == 128)
                                                : (p.head_dim == 32 || p.head_dim == 64);
   if (!dim_ok) return REC_ATTN_ERR_UNSUPPORTED;
+  // bf16: the rows' constants stand in the scores' unit (-lse / scale, -1e38 for rows without a key, whose
+  // weights are exp2(scale log2(e) -1e38)): outside this range they overflow, or come out above zero
+  if (p.dtype == REC_ATTN_BF16 && !(p.softmax_scale >= 1e-30f && p.softmax_scale <= 1e30f)) return REC_ATTN_ERR_UNSUPPORTED;
   if (T > 0) {
     const void* ptrs[8] = {q, k, v, out, dout, dq, dk, dv};
     for (const void* x : ptrs)
