@@ -1435,8 +1435,8 @@ rec_attn_status create_shared(rec_attn_kv_cache_s* c, const int64_t* hist_offset
   return REC_ATTN_OK;
 }
 
-// Which kernel a scoring call takes, by their measured times in microseconds (64 to 8192 keys,
-// 1 to 64 requests, 4 to 128 rows a key/value head): k_score_rows 10 plus 5.8e-3 (head_dim 64; 128:
+// Which kernel a scoring call takes, by their measured times in microseconds on 152 SMs (64 to 8192
+// keys, 1 to 64 requests, 4 to 128 rows a key/value head; outside that by the same lines): k_score_rows 10 plus 5.8e-3 (head_dim 64; 128:
 // 2.9e-3) for each 32 KB of keys and values that a group of its rows passes over, the many-row
 // kernel 28 plus 4.7e-3 (9e-3) for each 128 keys that 128 of its rows pass over.
 bool score_many(int head_dim, long long small_passes, long long large_passes) {

@@ -6,6 +6,8 @@
 // dt = t - t_ref is formed exactly in int64 and only then converted to fp32, which
 // keeps Unix-scale timestamps (~1.7e9 s) from losing precision in the angle.  The
 // per-pair angular speed omega_i is computed on the host in fp64 and rounded once.
+// Q' and K' are rounded once to the input type: in bf16 they are the scores' operands, and
+// as wide as Q and K in memory.
 #include <cuda_bf16.h>
 
 #include "attn_common.cuh"

@@ -26,7 +26,8 @@
 // request of 1023 keys: 7 us.
 //
 // Many rows (score_many in api.cu has both kernels' measured cost): k_score_pack lays Q' out in row
-// order and k_attn_tc's CAND instantiation takes items of 128 rows.  16 requests of 3500 to 4096
+// order, rounded to bf16, and k_attn_tc's CAND instantiation takes items of 128 rows, P rounded too (the
+// output is off by 3.0e-3, relative, against 2.1e-3 to 2.3e-3 with few rows, 1.6e-3 being its own rounding).  16 requests of 3500 to 4096
 // keys, 420 to 500 candidates, head_dim 64: 8 + 107 us (540 TFLOP/s); bound by the softmax of its 1.6
 // items a stream.
 #include <climits>

@@ -172,7 +172,7 @@ rec_attn_status rec_attn_plan_query_pruned(const rec_attn_params* params, int32_
  * for num_kv_heads that does not divide num_heads.  The planning reads host memory of this
  * call and the plan's calls wait for it, so neither may be captured into a CUDA graph:
  * rec_attn_plan_grouped on a capturing stream, and the forward and backward calls on its
- * plan there, return UNSUPPORTED and leave the capture valid.  The calls of one plan share
+ * plan there, return UNSUPPORTED and leave the capture valid and without a node of theirs.  The calls of one plan share
  * its workspace (as for rec_attn_plan): order them on one stream, or with events.
  */
 rec_attn_status rec_attn_plan_grouped(const rec_attn_params* params, int32_t num_kv_heads,
@@ -207,6 +207,10 @@ int64_t rec_attn_query_keep(int64_t hist_len, int64_t n_min, int32_t layer, int3
  * Errors: INVALID_ARG (NULL plan or pointers, misalignment, aliasing), CUDA.
  * Asynchronous: returns after enqueueing.  Launch-time anomalies inside kernels
  * (a timed-out wait) are reported by rec_attn_device_status.
+ * bf16: Q' and K' after the rotation and the softmax's weights are rounded to bf16, the
+ * operands of the tensor cores' products; scores, maxima, sums and accumulators are fp32.
+ * The output is off by about 2.5e-3 (relative), its own rounding being 1.6e-3 of that.
+ * fp32: a key or value that is not finite reaches the rows that see it alone.
  */
 rec_attn_status rec_attn_fwd(rec_attn_plan_t* plan, const void* q, const void* k,
                              const void* v, void* out, float* lse, void* stream);
@@ -274,9 +278,12 @@ rec_attn_status rec_attn_fwd_fused(rec_attn_plan_t* plan, const void* q, const v
  * nothing to dk and dv.
  * Supported: bf16 with head_dim 64 or 128 and a softmax_scale in 1e-30..1e30, fp32 with
  * head_dim 32 or 64 (else UNSUPPORTED).  The first call takes workspace from the
- * library pool on `stream` (released with the plan): for bf16 the per-plan item
- * schedule (96 B per tile and head, 4 B per tile pair) and the rows' constants
- * (16 B per tile row and head); for fp32 T * H floats.  On a plan of shared heads with few
+ * library pool on `stream` (released with the plan).  For bf16, with N tiles of 128 rows
+ * and C pairs of tiles of the same request: the items' descriptors (48 B per tile and
+ * query head, and per tile and dK/dV item), the query tiles of each key tile (8 B per
+ * pair), the mask table's columns (2 KB for each of min(8 N + 1024, C) slots), the rows'
+ * constants (2 KB per tile and query head) and, on a plan whose dK/dV items hold several
+ * heads, their order (4 B each).  For fp32 T * H floats.  On a plan of shared heads with few
  * tiles each call also takes fp32 parts of dK and dV, 8 * d bytes per token, key/value
  * head and part (up to H / Hk of them), from the pool.  bf16: tensor cores (bf16
  * operands, fp32 accumulation; P and dS rounded to bf16 for their MMAs, as in the
@@ -505,7 +512,11 @@ rec_attn_status rec_attn_visible_pairs(rec_attn_plan_t* plan, uint64_t* host_out
  * from which each key is visible to a candidate; a scoring call reads them once for all
  * candidates and all heads of a group, plans nothing and writes nothing into the cache, so
  * calls on one cache may overlap on any streams and may be captured into a CUDA graph (the
- * candidate counts are those of the capture).  Its workspace comes from the library pool on
+ * candidate counts are those of the capture).  Equal calls give equal bits.  A candidate's last
+ * bits may change with the other candidates of the call: all of a call's rows (up to 250
+ * requests at a time) decide which of two kernels runs and how the history is split.  With few rows
+ * the rotated queries and the softmax's weights keep 16 bits, with many they are rounded to bf16,
+ * as in rec_attn_fwd.  Its workspace comes from the library pool on
  * `stream`.  A history key whose type is not GLOBAL, HIST or RT, or whose time is not
  * within +-2^62, is seen by no candidate.  The cache rounds each request's rows up to a
  * multiple of 128, with zeros: a value that is not finite reaches candidates of its own request
