@@ -8,7 +8,7 @@
 // (simt_tile.cuh).  Bound by the fp32 units and the shared memory that feeds them: 16 causal
 // requests of 400 to 700 tokens, 8 query and 2 key/value heads, head_dim 64, 212 us against 63 of the
 // units alone (a thread per query row, reading every key element for one multiplication: 451; three
-// blocks an SM with fewer registers, which spill: 232).
+// blocks an SM with fewer registers, which spill: 232); head_dim 32: 136 us.
 // PARTIAL tiles take the plan's mask table, or without a slot evaluate the mask per element; FULL
 // tiles skip it.
 #include "attn_common.cuh"

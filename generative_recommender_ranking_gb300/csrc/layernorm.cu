@@ -12,7 +12,11 @@
 // differences from the mean itself and the backward recomputes both statistics from the row it
 // reads anyway.  The backward takes two reductions a row: {sum x, sum u}, then {sum (x - m)^2,
 // sum u (x - m)}.  320016 rows of 512 bf16 by type: forward 111 us (5.9 TB/s, 88% of a copy's rate),
-// backward 175 us (5.6 TB/s); backward of 50001 rows of 1408 fp32: 147 us (5.7 TB/s).
+// backward 177 us (5.5 TB/s; without types 161); backward of 50001 rows of 1408 fp32: 149 us (5.7 TB/s).
+// Farther from HBM's rate are rows of more than 256 threads, of which a block holds one, its two
+// reductions' barriers exposed (20000 x 8192 bf16: 168 and 239 us; 10000 x 16384, whose backward spills
+// at the 64 registers of 1024 threads: 206 and 741 us; 98 and 147 at a copy's rate), and short rows, half
+// of whose chunks are empty at 64 values (1000000 x 64 by type: 68 and 103 us; 38 and 57).
 // Statistics, sums and gradients of the gains are fp32; outputs are rounded once.
 #include <cuda_bf16.h>
 
@@ -536,7 +540,7 @@ struct NormShape {
   int nv, tpr, threads, groups;
   bool full;  // every thread has all its chunks
   // rows on their way per thread, this one included.  Two: with three or four the backward
-  // of 320016 x 512 bf16 took 183 and 187 us instead of 165, the forward 112 and 120 instead of 112
+  // of 320016 x 512 bf16 without types took 183 and 187 us instead of 165, the forward 112 and 120 instead of 112
   int ns;
   int rows_smem(bool bwd) const { return ns * nv * threads * 16 * (bwd ? 2 : 1); }
 };
