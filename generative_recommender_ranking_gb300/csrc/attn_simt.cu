@@ -45,6 +45,12 @@ __device__ __forceinline__ bool attend(const AttnArgs& a) {
   const long long tok0 = it.m.tok_start + pos0;
   load_tile<D>(static_cast<const float*>(a.q) + (tok0 * H + it.h) * D, (long long)H * D, it.m.len - pos0, a.scale, sm.q, nullptr);
   sm.tq.load(a.t, a.ty, tok0, pos0, it.m.len, a.mask.delay);
+  if (a.mask.keep_user >= 0) {  // pruned queries may hold anything (some Q' is never written): zeros
+    __syncthreads();
+    const int r = threadIdx.x >> 2;
+    if (pos0 + r < it.m.len && !query_kept(sm.tq.ty[r], pos0 + r, it.keep))
+      for (int d = threadIdx.x & 3; d < D; d += 4) sm.q[at(r >> 2, d) + (r & 3)] = 0.f;
+  }
   f2 o[2][N];
   float m[4], l[4];
 #pragma unroll

@@ -114,3 +114,18 @@ def test_scoring(d, grouped):
     clean[3], clean[cands:2 * cands] = False, False
     assert torch.isfinite(outs[1][clean]).all() and torch.equal(outs[0][clean], outs[1][clean])
     assert not torch.isfinite(outs[1][~clean]).all(-1).any()
+
+
+def test_pruned_queries():
+    """Queries that a plan does not compute may hold anything."""
+    off, t, ty, q, k, v, hk, params, _ = batch("candidates_d64")
+    kept, outs = (ty == W.CAND).cpu(), []
+    for poison in (False, True):
+        if poison:
+            q[~kept.cuda()] = float("nan")
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+        with bd.rec_attn_plan_grouped(params, hk, off, torch.from_numpy(off).cuda(), t, ty, keep_user_queries=0) as plan:
+            bd.rec_attn_fwd(plan, q, k, v, out, lse)
+            torch.cuda.synchronize()
+        outs.append((out, lse))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and (outs[0][0][~kept.cuda()] == 0).all()
