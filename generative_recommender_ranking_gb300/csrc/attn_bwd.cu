@@ -20,8 +20,8 @@
 // FULL tiles skip the mask; PARTIAL tiles take the plan's mask table, or without a slot evaluate it.  Rows with no visible key (lse = -inf)
 // contribute nothing.  Bound by the fp32 units and the shared memory that feeds them (k_bwd_dkv at
 // head_dim 64: one block per SM).  Forward and backward of 16 causal requests of 400 to 700 tokens,
-// 8 query and 2 key/value heads, head_dim 64: 1070 us, dQ 352 and dK/dV 462 of it (a thread per row: 2306);
-// of one request of 700 tokens, 8 and 1 heads: 293 us (2742, whose dK/dV had six blocks).
+// 8 query and 2 key/value heads, head_dim 64: 1080 us, dQ 352 and dK/dV 462 of it (a thread per row: 2306);
+// of one request of 700 tokens, 8 and 1 heads: 283 us (2742, whose dK/dV had six blocks).
 #include "attn_common.cuh"
 #include "launchers.cuh"
 #include "simt_tile.cuh"
