@@ -21,6 +21,7 @@ MAX_REQUEST_LEN = 262144
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_OOM, ERR_TIMEOUT, ERR_DEVICE_INPUT = range(7)
 BF16, FP32 = 0, 1
+ACTIVATIONS = {"silu": 0, "gelu": 1}
 GLOBAL, HIST, RT, CAND = 0, 1, 2, 3
 TILE_SKIP, TILE_PARTIAL, TILE_FULL = 0, 1, 2
 
@@ -118,6 +119,12 @@ def lib() -> ctypes.CDLL:
         L.rec_attn_layernorm_bwd.argtypes = [i32, i64, i64, i32, vp, vp, vp, ctypes.c_float, vp, vp,
                                              vp, vp, vp]
         L.rec_attn_layernorm_bwd.restype = ctypes.c_int
+        L.rec_attn_ffn_fwd.argtypes = [i32, i32, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.rec_attn_ffn_fwd.restype = ctypes.c_int
+        L.rec_attn_ffn_bwd.argtypes = [i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.rec_attn_ffn_bwd.restype = ctypes.c_int
+        L.rec_attn_dense_device_status.argtypes = [ctypes.POINTER(i32), vp]
+        L.rec_attn_dense_device_status.restype = ctypes.c_int
         L.rec_attn_fwd_compress.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
         L.rec_attn_fwd_compress.restype = ctypes.c_int
         L.rec_attn_cache_create.argtypes = [ctypes.POINTER(RecAttnParams), i32, vp, vp, vp, vp, vp,
@@ -380,6 +387,59 @@ def rec_attn_layernorm_bwd(x, weight, dy, dx, dweight=None, dbias=None, types=No
     _check("rec_attn_layernorm_bwd", L.rec_attn_layernorm_bwd(dtype, rows, width, groups, _ptr(x), _ptr(types),
                                                               _ptr(weight), float(eps), _ptr(dy), _ptr(dx),
                                                               _ptr(dweight), _ptr(dbias), _stream(stream)))
+
+
+def _matrices(fn: str, x, *shaped):
+    """Contiguous matrices of x's device: (tensor or None, shape, dtype) each."""
+    for o, shape, dtype in shaped:
+        if o is not None and not (o.dtype == dtype and tuple(o.shape) == shape and o.is_contiguous()
+                                  and o.device == x.device):
+            raise RecAttnError(fn, ERR_INVALID_ARG)
+
+
+def _activation(fn: str, name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise RecAttnError(fn, ERR_INVALID_ARG)
+    return ACTIVATIONS[name]
+
+
+def _hidden(fn: str, w_out) -> int:
+    if w_out.dim() != 2:
+        raise RecAttnError(fn, ERR_INVALID_ARG)
+    return w_out.shape[1]
+
+
+def rec_attn_ffn_fwd(x, w_in, w_out, y, activation: str = "silu", stream=None) -> None:
+    """Gated feed-forward block y = (act(x Wg') * (x Wu')) w_out' of rows x [rows, width] (bf16 or
+    float32): w_in [2 hidden, width] holds Wg's rows, then Wu's; w_out [width, hidden];
+    activation "silu" or "gelu"."""
+    L, fn = lib(), "rec_attn_ffn_fwd"
+    dtype, rows, width = _rows(fn, x, y=y)
+    hidden = _hidden(fn, w_out)
+    _matrices(fn, x, (w_in, (2 * hidden, width), x.dtype), (w_out, (width, hidden), x.dtype))
+    _check(fn, L.rec_attn_ffn_fwd(dtype, _activation(fn, activation), rows, width, hidden, _ptr(x), _ptr(w_in),
+                                  _ptr(w_out), _ptr(y), _stream(stream)))
+
+
+def rec_attn_ffn_bwd(x, w_in, w_out, dy, dx=None, dw_in=None, dw_out=None, activation: str = "silu",
+                     stream=None) -> None:
+    """Gradients of rec_attn_ffn_fwd for the upstream gradient dy, in x's type, overwritten (None:
+    not wanted)."""
+    L, fn = lib(), "rec_attn_ffn_bwd"
+    dtype, rows, width = _rows(fn, x, dy=dy)
+    hidden = _hidden(fn, w_out)
+    w_in_s, w_out_s = ((2 * hidden, width), x.dtype), ((width, hidden), x.dtype)
+    _matrices(fn, x, (w_in, *w_in_s), (w_out, *w_out_s), (dx, (rows, width), x.dtype), (dw_in, *w_in_s),
+              (dw_out, *w_out_s))
+    _check(fn, L.rec_attn_ffn_bwd(dtype, _activation(fn, activation), rows, width, hidden, _ptr(x), _ptr(w_in),
+                                  _ptr(w_out), _ptr(dy), _ptr(dx), _ptr(dw_in), _ptr(dw_out), _stream(stream)))
+
+
+def rec_attn_dense_device_status(stream=None) -> int:
+    """Status word of the feed-forward and scaled calls on the current device."""
+    s = ctypes.c_int32()
+    _check("rec_attn_dense_device_status", lib().rec_attn_dense_device_status(ctypes.byref(s), _stream(stream)))
+    return int(s.value)
 
 
 def rec_attn_fwd_compress(plan: Plan, q, k, v, hist_begin, hist_len, segments, x_out, t_out, ty_out,

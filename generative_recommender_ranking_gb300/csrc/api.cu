@@ -147,6 +147,10 @@ cudaError_t side_stream_for(int device, cudaStream_t* out) {
   return cudaSuccess;
 }
 
+}  // namespace
+
+namespace recattn {
+
 rec_attn_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return REC_ATTN_OK;
   if (e == cudaErrorMemoryAllocation) return REC_ATTN_ERR_OOM;
@@ -176,6 +180,22 @@ cudaError_t pool_for(int device, cudaMemPool_t* out) {
   return cudaSuccess;
 }
 
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const char* x = static_cast<const char*>(a);
+  const char* y = static_cast<const char*>(b);
+  return x < y + nb && y < x + na;
+}
+
+cudaError_t device_and_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  return e;
+}
+
+}  // namespace recattn
+
+namespace {
+
 // Closes the attention kernel's timing window: events 0..1 bracket the RoPE
 // prologue, events 2..3 the attention kernel.
 rec_attn_status finish_timing(rec_attn_plan_s* plan, cudaStream_t st, cudaError_t launch_err) {
@@ -185,12 +205,6 @@ rec_attn_status finish_timing(rec_attn_plan_s* plan, cudaStream_t st, cudaError_
   if (e != cudaSuccess) return from_cuda(e);
   plan->timed = true;
   return REC_ATTN_OK;
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const char* x = static_cast<const char*>(a);
-  const char* y = static_cast<const char*>(b);
-  return x < y + nb && y < x + na;
 }
 
 }  // namespace
@@ -930,12 +944,6 @@ rec_attn_status check_norm(int32_t dtype, int64_t rows, int64_t width, int32_t g
     return REC_ATTN_ERR_INVALID_ARG;
   if (width > kMaxNormWidth || rows > kMaxNormRows) return REC_ATTN_ERR_UNSUPPORTED;
   return REC_ATTN_OK;
-}
-
-cudaError_t device_and_sms(int* dev, int* sms) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
-  return e;
 }
 
 }  // namespace

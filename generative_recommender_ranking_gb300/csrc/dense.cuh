@@ -1,0 +1,40 @@
+// dense.cuh -- the feed-forward block's matrix products: arguments and launchers (internal).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "rec_attn_internal.cuh"
+
+namespace recattn {
+
+// The products of the gated feed-forward block (dense_tc.cu); R rows, W width, H hidden.
+enum class DenseOp {
+  kGlu,   // h = act(x Wg') * (x Wu')                       [R][H]
+  kOut,   // y = h w_out'                                   [R][W]
+  kDglu,  // p = [dh u act'(g); dh act(g)], h, dh = dy w_out [R][2H], [R][H]
+  kDx,    // dx = p w_in                                    [R][W]
+  kDw,    // a' b summed over the rows: dw_in = p' x, dw_out = dy' h
+};
+
+struct DenseArgs {
+  int M, N;             // rows and columns of the result (kGlu, kDglu: N = H)
+  int kblocks;          // blocks of 64 along the summed axis
+  int tiles_m, tiles_n, splits;
+  int act;              // rec_attn_activation
+  int wide;             // the outputs' rows start on 32-byte boundaries
+  void* out;            // kGlu: h; kOut, kDx: the result; kDglu: p; kDw: the result (one split)
+  void* out2;           // kDglu: h
+  float* part;          // kDw: [splits][M][N] sums of parts (more than one split)
+  int* status;
+};
+
+// A row-major [rows][cols] bf16 operand as a TMA map; mn_major: the summed axis runs over its rows.
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major);
+int* dense_status();
+cudaError_t launch_dense(DenseOp op, const CUtensorMap (&maps)[4], DenseArgs a, int num_sms, cudaStream_t st);
+// kDw: parts of the summed axis.
+int dense_splits(int M, int N, int kblocks, int num_sms);
+cudaError_t launch_dense_sum(const float* part, void* out, long long n, int splits, int dtype, cudaStream_t st);
+
+}  // namespace recattn

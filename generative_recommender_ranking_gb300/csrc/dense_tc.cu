@@ -1,0 +1,427 @@
+// dense_tc.cu -- the matrix products of the gated feed-forward block on the sm_103a tensor cores.
+//
+// y = (act(x Wg') * (x Wu')) w_out' over packed token rows, and its gradients (dense.cuh lists the
+// five products).  One persistent CTA per SM takes tiles of 128 rows; a TMA warp keeps a ring of
+// 64-deep operand blocks full, one warp issues tcgen05 MMAs into TMEM, eight warps read a finished
+// tile out while the next one is summed.
+//  - kGlu: a tile's 256 columns are 128 gate and the 128 up columns that belong to them, so the
+//    activation and the product happen in the epilogue and neither projection reaches memory.
+//  - kDglu: nothing of the forward is kept; g and u are summed again (256 columns) beside
+//    dh = dy w_out (128 columns).  dh has two buffers and goes first: while it is summed for the
+//    next tile the epilogue reads this tile's g and u, which have one.
+//  - kDw sums over the rows; the rows are split into parts so that all SMs have work, the parts'
+//    sums are added in a fixed order (k_dense_sum).
+// Sums are fp32; h and p are rounded to bf16 once, as operands of the next product.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "dense.cuh"
+#include "launchers.cuh"
+#include "ptx_sm103.cuh"
+#include "wait.cuh"
+
+namespace recattn {
+
+namespace {
+
+__device__ int g_dense_status;
+
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
+constexpr int kBK = 64;                      // a block along the summed axis: 128 bytes
+constexpr int kSlab = 64 * 128;              // 64 rows of 128 bytes
+constexpr int kThreads = 384, kEpiWarps = 8;
+
+template <DenseOp OP, int BN>
+struct Cfg {
+  static constexpr bool kPair = OP == DenseOp::kGlu || OP == DenseOp::kDglu;  // gate and up columns
+  static constexpr bool kAMn = OP == DenseOp::kDw, kBMn = OP == DenseOp::kDx || OP == DenseOp::kDw;
+  static constexpr int kTileN = kPair ? BN / 2 : BN;  // columns of the result
+  static constexpr int kStage = 2 * kSlab + BN * 128;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kDynamic = kStages * kStage + 1024;
+  static constexpr uint32_t kTmem = 2 * BN;  // kDglu: g, u and two buffers of dh
+};
+
+// Barriers
+enum { kFull = 0, kEmpty = 8, kAccFull = 16, kAccEmpty = 18, kGuEmpty = 20, kDone = 21, kBars = 22 };
+
+struct Unit {
+  int m0, n0, kb0, kb1, split;
+};
+
+// Tiles in bands of 16 row tiles: the CTAs at work together share a band's rows and the columns'
+// weights in the L2.
+template <int TN>
+__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i) {
+  const int tiles = a.tiles_m * a.tiles_n;
+  Unit u;
+  u.split = i / tiles;
+  const int t = i - u.split * tiles;
+  const int band = t / (16 * a.tiles_n), in = t - band * 16 * a.tiles_n;
+  const int rows = min(16, a.tiles_m - band * 16);
+  u.m0 = (band * 16 + in % rows) * kTile;
+  u.n0 = in / rows * TN;
+  u.kb0 = (int)((long long)a.kblocks * u.split / a.splits);
+  u.kb1 = (int)((long long)a.kblocks * (u.split + 1) / a.splits);
+  return u;
+}
+
+// ------------------------------------------------------------------ loads
+// `rows` (a multiple of 128) rows of one operand at mn0, block kb of the summed axis.
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn0, int rows, int kb,
+                                             uint64_t* bar) {
+  if (MN) {
+    for (int i = 0; i < rows / 64; ++i) ptx::tma_load_2d(dst + i * kSlab, map, mn0 + 64 * i, kb * kBK, bar);
+  } else {
+    for (int i = 0; i < rows / kTile; ++i) ptx::tma_load_2d(dst + i * 2 * kSlab, map, kb * kBK, mn0 + kTile * i, bar);
+  }
+}
+
+template <DenseOp OP, int BN>
+__device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* ma2,
+                        const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, int lane) {
+  using C = Cfg<OP, BN>;
+  const int units = a.tiles_m * a.tiles_n * a.splits;
+  uint32_t n = 0;
+  for (int i = blockIdx.x; i < units; i += gridDim.x) {
+    const Unit u = unit_at<C::kTileN>(a, i);
+    const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
+    for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
+      const int st = n % C::kStages;
+      if (!bounded_wait_warp(bars + kEmpty + st, ((n / C::kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+      if (ptx::elect_one()) {
+        uint8_t* s = sm + st * C::kStage;
+        uint64_t* bar = bars + kFull + st;
+        if (OP == DenseOp::kDglu && kb < 0) {
+          ptx::mbar_arrive_expect_tx(bar, 4 * kSlab);
+          load_operand<false>(s, ma2, u.m0, kTile, kb + first, bar);
+          load_operand<true>(s + 2 * kSlab, mb2, u.n0, kTile, kb + first, bar);
+        } else {
+          ptx::mbar_arrive_expect_tx(bar, C::kStage);
+          load_operand<C::kAMn>(s, ma, u.m0, kTile, kb, bar);
+          if (C::kPair) {
+            load_operand<false>(s + 2 * kSlab, mb, u.n0, BN / 2, kb, bar);
+            load_operand<false>(s + 2 * kSlab + BN * 64, mb, a.N + u.n0, BN / 2, kb, bar);
+          } else {
+            load_operand<C::kBMn>(s + 2 * kSlab, mb, u.n0, BN, kb, bar);
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+out:
+  // after an abort, copies may still be in flight
+  if (lane == 0)
+    for (uint32_t j = n > C::kStages ? n - C::kStages : 0; j < n; ++j)
+      bounded_drain(bars + kFull + j % C::kStages, (j / C::kStages) & 1, kWaitNs / 4);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ MMAs
+template <bool MN>
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  return MN ? ptx::smem_desc_sw128(addr, kSlab, 1024) : ptx::smem_desc_sw128(addr, 16, 1024);
+}
+// the operand 16 values further along the summed axis
+template <bool MN>
+__device__ __forceinline__ uint64_t step(uint64_t desc, int k) {
+  return ptx::smem_desc_at(desc, k * (MN ? 16 * 128 : 32));
+}
+
+template <bool AMN, bool BMN, int N>
+__device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s, bool fresh) {
+  const uint32_t idesc = ptx::idesc_bf16_f32(kTile, N, AMN, BMN);
+  const uint64_t da = operand<AMN>(s), db = operand<BMN>(s + 2 * kSlab);
+#pragma unroll
+  for (int k = 0; k < kBK / 16; ++k) ptx::umma_f16(acc, step<AMN>(da, k), step<BMN>(db, k), idesc, !fresh || k > 0);
+}
+
+template <DenseOp OP, int BN>
+__device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
+  using C = Cfg<OP, BN>;
+  const int units = a.tiles_m * a.tiles_n * a.splits;
+  const uint32_t s0 = ptx::smem_u32(sm);
+  const bool el = ptx::elect_one();
+  uint32_t n = 0, it = 0;
+  for (int i = blockIdx.x; i < units; i += gridDim.x, ++it) {
+    const Unit u = unit_at<C::kTileN>(a, i);
+    const uint32_t buf = it & 1, round = (it >> 1) & 1;
+    if (!bounded_wait_warp(bars + kAccEmpty + buf, round ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+    ptx::tc_fence_after();
+    if (OP == DenseOp::kDglu) {
+      for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
+        const int st = n % C::kStages;
+        if (!bounded_wait_warp(bars + kFull + st, (n / C::kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
+        ptx::tc_fence_after();
+        if (el) {
+          block_mma<false, true, BN / 2>(tmem + BN + buf * (BN / 2), s0 + st * C::kStage, kb == 0);
+          ptx::umma_commit(bars + kEmpty + st);
+        }
+        __syncwarp();
+      }
+      if (!bounded_wait_warp(bars + kGuEmpty, (it & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+      ptx::tc_fence_after();
+    }
+    const uint32_t acc = OP == DenseOp::kDglu ? tmem : tmem + buf * BN;
+    for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
+      const int st = n % C::kStages;
+      if (!bounded_wait_warp(bars + kFull + st, (n / C::kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
+      ptx::tc_fence_after();
+      if (el) {
+        block_mma<C::kAMn, C::kBMn, BN>(acc, s0 + st * C::kStage, kb == u.kb0);
+        ptx::umma_commit(bars + kEmpty + st);
+      }
+      __syncwarp();
+    }
+    if (el) ptx::umma_commit(bars + kAccFull + buf);
+    __syncwarp();
+  }
+out:
+  if (el) {
+    ptx::umma_commit(bars + kDone);
+    bounded_drain(bars + kDone, 0, kWaitNs / 4);
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ epilogues
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// act(g), and its derivative.  silu: g / (1 + e^-g).  gelu: g Phi(g), Phi by the complementary error
+// function, which keeps its relative accuracy where Phi is small.
+__device__ __forceinline__ float act_value(float g, int act) {
+  if (act == REC_ATTN_SILU) return __fdividef(g, 1.f + __expf(-g));
+  return 0.5f * g * erfcf(-0.70710678f * g);
+}
+__device__ __forceinline__ float act_both(float g, int act, float& slope) {
+  if (act == REC_ATTN_SILU) {
+    const float p = __fdividef(1.f, 1.f + __expf(-g)), v = g * p;
+    slope = fmaf(v, 1.f - p, p);
+    return v;
+  }
+  const float p = 0.5f * erfcf(-0.70710678f * g);
+  slope = fmaf(g, 0.39894228f * __expf(-0.5f * g * g), p);
+  return g * p;
+}
+
+// 32 columns of a row in bf16; `left` columns of the result remain from the first on (a multiple of 8).
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&w)[16], int left, bool wide) {
+  if (wide && left >= 32) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      ptx::st_global_v8(reinterpret_cast<char*>(dst) + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3],
+                        w[8 * c + 4], w[8 * c + 5], w[8 * c + 6], w[8 * c + 7]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (8 * c < left) reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+}
+
+template <DenseOp OP, int BN>
+__device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
+  using C = Cfg<OP, BN>;
+  const int units = a.tiles_m * a.tiles_n * a.splits;
+  const int quad = warp & 3, half = (warp >> 2) & 1;
+  constexpr int kCols = C::kTileN / 2;  // of the result, a warp's share
+  uint32_t it = 0;
+  for (int i = blockIdx.x; i < units; i += gridDim.x, ++it) {
+    const Unit u = unit_at<C::kTileN>(a, i);
+    const uint32_t buf = it & 1, round = (it >> 1) & 1;
+    if (!bounded_wait_warp(bars + kAccFull + buf, round, abort_flag, a.status, kWaitNs)) return;
+    ptx::tc_fence_after();
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+    const long long row = u.m0 + quad * 32 + lane;
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+      const int col = u.n0 + half * kCols + c, left = a.N - col;
+      const bool in = row < a.M && left > 0;
+      if constexpr (OP == DenseOp::kGlu) {
+        uint32_t g[32], v[32], w[16];
+        ptx::tmem_ld32(lanes + buf * BN + c, g);
+        ptx::tmem_ld32(lanes + buf * BN + BN / 2 + c, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = bf16x2(act_value(__uint_as_float(g[2 * e]), a.act) * __uint_as_float(v[2 * e]),
+                        act_value(__uint_as_float(g[2 * e + 1]), a.act) * __uint_as_float(v[2 * e + 1]));
+        if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
+      } else if constexpr (OP == DenseOp::kDglu) {
+        uint32_t g[32], v[32], d[32], wg[16], wu[16], wh[16];
+        ptx::tmem_ld32(lanes + c, g);
+        ptx::tmem_ld32(lanes + BN / 2 + c, v);
+        ptx::tmem_ld32(lanes + BN + buf * (BN / 2) + c, d);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float dg[2], du[2], h[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float dh = __uint_as_float(d[2 * e + k]), up = __uint_as_float(v[2 * e + k]);
+            float slope;
+            const float act = act_both(__uint_as_float(g[2 * e + k]), a.act, slope);
+            dg[k] = dh * up * slope;
+            du[k] = dh * act;
+            h[k] = act * up;
+          }
+          wg[e] = bf16x2(dg[0], dg[1]);
+          wu[e] = bf16x2(du[0], du[1]);
+          wh[e] = bf16x2(h[0], h[1]);
+        }
+        if (in) {
+          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + row * 2 * a.N + col;
+          store_bf16(p, wg, left, a.wide);
+          store_bf16(p + a.N, wu, left, a.wide);
+          store_bf16(static_cast<__nv_bfloat16*>(a.out2) + row * a.N + col, wh, left, a.wide);
+        }
+      } else {
+        uint32_t r[32];
+        ptx::tmem_ld32(lanes + buf * BN + c, r);
+        if (OP == DenseOp::kDw && a.splits > 1) {
+          if (in) {
+            float4* dst = reinterpret_cast<float4*>(a.part + ((long long)u.split * a.M + row) * a.N + col);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (4 * e < left)
+                dst[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                     __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+          }
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
+        }
+      }
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      ptx::mbar_arrive(bars + kAccEmpty + buf);
+      if (OP == DenseOp::kDglu) ptx::mbar_arrive(bars + kGuEmpty);
+    }
+  }
+}
+
+template <DenseOp OP, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_dense(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+            const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2, const DenseArgs a) {
+  using C = Cfg<OP, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kBars];
+  __shared__ int s_abort;
+  __shared__ uint32_t tmem_slot;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      ptx::mbar_init(bars + kFull + i, 1);
+      ptx::mbar_init(bars + kEmpty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars + kAccFull + i, 1);
+      ptx::mbar_init(bars + kAccEmpty + i, kEpiWarps);
+    }
+    ptx::mbar_init(bars + kGuEmpty, kEpiWarps);
+    ptx::mbar_init(bars + kDone, 1);
+    s_abort = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&tmem_slot, C::kTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp == 0) produce<OP, BN>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, lane);
+  else if (warp == 1) issue<OP, BN>(a, sm, bars, tmem, abort_flag);
+  else if (warp >= 4) finish<OP, BN>(a, bars, tmem, abort_flag, warp, lane);
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+// The parts' sums, in their order.
+template <bool BF16>
+__global__ void k_dense_sum(const float* part, void* out, long long n, int splits) {
+  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 s = *reinterpret_cast<const float4*>(part + i);
+  for (int k = 1; k < splits; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(part + k * n + i);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  if (BF16) reinterpret_cast<uint2*>(out)[i / 4] = make_uint2(bf16x2(s.x, s.y), bf16x2(s.z, s.w));
+  else reinterpret_cast<float4*>(out)[i / 4] = s;
+}
+
+template <DenseOp OP, int BN>
+cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
+  using C = Cfg<OP, BN>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN>, C::kDynamic);
+  if (e != cudaSuccess) return e;
+  a.tiles_m = (a.M + kTile - 1) / kTile;
+  a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
+  const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;
+  k_dense<OP, BN><<<(int)(units < num_sms ? units : num_sms), kThreads, C::kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major) {
+  return encode_map(m, base, rows, cols, mn_major ? 64 : kTile);
+}
+
+// Asked once per device (the first call may be captured: the question belongs to no stream).
+int* dense_status() {
+  static std::atomic<int*> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  if (dev < 64)
+    if (int* w = known[dev].load(std::memory_order_relaxed)) return w;
+  const OutsideCapture now;
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_dense_status) != cudaSuccess) return nullptr;
+  if (dev < 64) known[dev].store(static_cast<int*>(p), std::memory_order_relaxed);
+  return static_cast<int*>(p);
+}
+
+int dense_splits(int M, int N, int kblocks, int num_sms) {
+  const long long tiles = (long long)((M + kTile - 1) / kTile) * ((N + 255) / 256);
+  long long s = (2 * num_sms + tiles - 1) / tiles;
+  if (s > kblocks) s = kblocks;
+  return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_dense_sum(const float* part, void* out, long long n, int splits, int dtype, cudaStream_t st) {
+  const unsigned blocks = (unsigned)((n / 4 + 255) / 256);
+  if (dtype == REC_ATTN_BF16) k_dense_sum<true><<<blocks, 256, 0, st>>>(part, out, n, splits);
+  else k_dense_sum<false><<<blocks, 256, 0, st>>>(part, out, n, splits);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dense(DenseOp op, const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
+  switch (op) {
+    case DenseOp::kGlu: return run<DenseOp::kGlu, 256>(m, a, num_sms, st);
+    case DenseOp::kOut: return run<DenseOp::kOut, 256>(m, a, num_sms, st);
+    case DenseOp::kDglu: return run<DenseOp::kDglu, 256>(m, a, num_sms, st);
+    case DenseOp::kDx: return run<DenseOp::kDx, 256>(m, a, num_sms, st);
+    case DenseOp::kDw: return run<DenseOp::kDw, 256>(m, a, num_sms, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace recattn

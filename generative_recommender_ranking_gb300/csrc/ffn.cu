@@ -1,0 +1,200 @@
+// ffn.cu -- host side of the feed-forward entry points: argument checks (before any CUDA call),
+// workspaces in stream order from the library's pool, tensor maps and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "dense.cuh"
+#include "launchers.cuh"
+#include "rec_attn.h"
+#include "workspace.cuh"
+
+#define REC_ATTN_API extern "C" __attribute__((visibility("default")))
+
+using namespace recattn;
+
+namespace {
+
+constexpr long long kMaxRows = (1LL << 31) - 65536;  // tiles past the last row are still 32-bit coordinates
+constexpr long long kMaxWidth = 65536;
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool wide_rows(const void* p, long long cols) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && cols % 16 == 0; }
+
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+// Whether one of the first `outs` ranges overlaps another range (NULL ranges apart).
+bool clash(const Range* r, int outs, int n) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (r[i].p && r[j].p && overlaps(r[i].p, r[i].bytes, r[j].p, r[j].bytes)) return true;
+  return false;
+}
+
+// The checks that both directions share.
+rec_attn_status check_ffn(int32_t dtype, int32_t act, int64_t rows, int64_t width, int64_t hidden) {
+  if (dtype != REC_ATTN_BF16 && dtype != REC_ATTN_FP32) return REC_ATTN_ERR_INVALID_ARG;
+  if (act != REC_ATTN_SILU && act != REC_ATTN_GELU) return REC_ATTN_ERR_INVALID_ARG;
+  const int unit = dtype == REC_ATTN_BF16 ? 8 : 4;  // 16 bytes
+  if (rows < 0 || width < 1 || hidden < 1 || width % unit || hidden % unit) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows > kMaxRows || width > kMaxWidth || hidden > kMaxWidth) return REC_ATTN_ERR_UNSUPPORTED;
+  // a launch's tiles are counted in 32 bits
+  if (((rows + kTile - 1) / kTile) * ((2 * hidden + kTile - 1) / kTile) > INT32_MAX / 2) return REC_ATTN_ERR_UNSUPPORTED;
+  return REC_ATTN_OK;
+}
+
+int blocks64(int64_t n) { return (int)((n + 63) / 64); }
+
+// A workspace of the library's pool, given back in stream order.
+struct Workspace {
+  void* p = nullptr;
+  cudaStream_t st;
+  explicit Workspace(cudaStream_t s) : st(s) {}
+  cudaError_t take(int dev, size_t bytes) {
+    cudaMemPool_t pool;
+    cudaError_t e = pool_for(dev, &pool);
+    if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&p, bytes, pool, st);
+    return e;
+  }
+  cudaError_t give_back() { return p ? cudaFreeAsync(p, st) : cudaSuccess; }
+};
+
+cudaError_t dense(DenseOp op, const DenseArgs& a, int sms, cudaStream_t st, bool encoded, const CUtensorMap (&m)[4]) {
+  return encoded ? launch_dense(op, m, a, sms, st) : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation, int64_t rows, int64_t width,
+                                              int64_t hidden, const void* x, const void* w_in, const void* w_out,
+                                              void* y, void* stream) {
+  const rec_attn_status s = check_ffn(dtype, activation, rows, width, hidden);
+  if (s != REC_ATTN_OK) return s;
+  if (rows == 0) return REC_ATTN_OK;
+  if (!x || !w_in || !w_out || !y || misaligned(x) || misaligned(w_in) || misaligned(w_out) || misaligned(y))
+    return REC_ATTN_ERR_INVALID_ARG;
+  const size_t es = dtype == REC_ATTN_BF16 ? 2 : 4;
+  const Range all[4] = {{y, rows * width * es}, {x, rows * width * es}, {w_in, 2 * hidden * width * es},
+                        {w_out, hidden * width * es}};
+  if (clash(all, 1, 4)) return REC_ATTN_ERR_INVALID_ARG;
+  if (dtype != REC_ATTN_BF16) return REC_ATTN_ERR_UNSUPPORTED;
+  int dev = -1, sms = 0;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Workspace ws(st);
+  e = ws.take(dev, rows * hidden * es);
+  if (e != cudaSuccess) return from_cuda(e);
+  CUtensorMap m[4];
+  DenseArgs a{};
+  a.act = activation;
+  a.splits = 1;
+  a.status = dense_status();
+  a.M = (int)rows;
+  a.N = (int)hidden;
+  a.kblocks = blocks64(width);
+  a.out = ws.p;
+  a.wide = wide_rows(ws.p, hidden);
+  e = dense(DenseOp::kGlu, a, sms, st,
+            encode_dense(&m[0], x, rows, width, false) && encode_dense(&m[1], w_in, 2 * hidden, width, false), m);
+  a.N = (int)width;
+  a.kblocks = blocks64(hidden);
+  a.out = y;
+  a.wide = wide_rows(y, width);
+  if (e == cudaSuccess)
+    e = dense(DenseOp::kOut, a, sms, st,
+              encode_dense(&m[0], ws.p, rows, hidden, false) && encode_dense(&m[1], w_out, width, hidden, false), m);
+  const cudaError_t ef = ws.give_back();
+  return from_cuda(e != cudaSuccess ? e : ef);
+}
+
+REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation, int64_t rows, int64_t width,
+                                              int64_t hidden, const void* x, const void* w_in, const void* w_out,
+                                              const void* dy, void* dx, void* dw_in, void* dw_out, void* stream) {
+  const rec_attn_status s = check_ffn(dtype, activation, rows, width, hidden);
+  if (s != REC_ATTN_OK) return s;
+  const size_t es = dtype == REC_ATTN_BF16 ? 2 : 4;
+  const size_t nx = rows * width * es, ni = 2 * hidden * width * es, no = hidden * width * es;
+  if (misaligned(dw_in) || misaligned(dw_out)) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !w_in || !w_out || !dy || misaligned(x) || misaligned(w_in) || misaligned(w_out) ||
+                   misaligned(dy) || misaligned(dx)))
+    return REC_ATTN_ERR_INVALID_ARG;
+  const Range all[7] = {{rows > 0 ? dx : nullptr, nx}, {dw_in, ni}, {dw_out, no}, {rows > 0 ? x : nullptr, nx},
+                        {w_in, ni}, {w_out, no}, {rows > 0 ? dy : nullptr, nx}};
+  if (clash(all, 3, 7)) return REC_ATTN_ERR_INVALID_ARG;
+  if (dtype != REC_ATTN_BF16) return REC_ATTN_ERR_UNSUPPORTED;
+  int dev = -1, sms = 0;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {  // no row: the weights' gradients are zero
+    if (dw_in) e = cudaMemsetAsync(dw_in, 0, ni, st);
+    if (e == cudaSuccess && dw_out) e = cudaMemsetAsync(dw_out, 0, no, st);
+    return from_cuda(e);
+  }
+  const int kr = blocks64(rows), W = (int)width, H = (int)hidden;
+  const int si = dw_in ? dense_splits(2 * H, W, kr, sms) : 1, so = dw_out ? dense_splits(W, H, kr, sms) : 1;
+  const size_t n_part = std::max(si > 1 ? (size_t)si * 2 * H * W : 0, so > 1 ? (size_t)so * H * W : 0);
+  const size_t off_h = ws_up(rows * 2 * hidden * es), off_part = off_h + ws_up(rows * hidden * es);
+  Workspace ws(st);
+  e = ws.take(dev, off_part + 4 * n_part);
+  if (e != cudaSuccess) return from_cuda(e);
+  char* const p = static_cast<char*>(ws.p);
+  char* const h = p + off_h;
+  CUtensorMap m[4];
+  DenseArgs a{};
+  a.act = activation;
+  a.splits = 1;
+  a.status = dense_status();
+  a.part = reinterpret_cast<float*>(p + off_part);
+  a.M = (int)rows;
+  a.N = H;
+  a.kblocks = blocks64(width);
+  a.out = p;
+  a.out2 = h;
+  a.wide = wide_rows(p, hidden);
+  e = dense(DenseOp::kDglu, a, sms, st,
+            encode_dense(&m[0], x, rows, width, false) && encode_dense(&m[1], w_in, 2 * hidden, width, false) &&
+                encode_dense(&m[2], dy, rows, width, false) && encode_dense(&m[3], w_out, width, hidden, true),
+            m);
+  if (e == cudaSuccess && dx) {
+    a.N = W;
+    a.kblocks = blocks64(2 * hidden);
+    a.out = dx;
+    a.wide = wide_rows(dx, width);
+    e = dense(DenseOp::kDx, a, sms, st,
+              encode_dense(&m[0], p, rows, 2 * hidden, false) && encode_dense(&m[1], w_in, 2 * hidden, width, true), m);
+  }
+  a.kblocks = kr;
+  for (int i = 0; i < 2; ++i) {
+    void* const dw = i ? dw_out : dw_in;
+    if (e != cudaSuccess || !dw) continue;
+    a.M = i ? W : 2 * H;
+    a.N = i ? H : W;
+    a.splits = i ? so : si;
+    a.out = dw;
+    a.wide = wide_rows(dw, a.N);
+    e = dense(DenseOp::kDw, a, sms, st,
+              (i ? encode_dense(&m[0], dy, rows, width, true) && encode_dense(&m[1], h, rows, hidden, true)
+                 : encode_dense(&m[0], p, rows, 2 * hidden, true) && encode_dense(&m[1], x, rows, width, true)),
+              m);
+    if (e == cudaSuccess && a.splits > 1) e = launch_dense_sum(a.part, dw, (long long)a.M * a.N, a.splits, dtype, st);
+  }
+  const cudaError_t ef = ws.give_back();
+  return from_cuda(e != cudaSuccess ? e : ef);
+}
+
+REC_ATTN_API rec_attn_status rec_attn_dense_device_status(int32_t* status_out, void* stream) {
+  if (!status_out) return REC_ATTN_ERR_INVALID_ARG;
+  int* const word = dense_status();
+  if (!word) return REC_ATTN_ERR_CUDA;
+  int s = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(&s, word, sizeof s, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess) *status_out = s;
+  return from_cuda(e);
+}

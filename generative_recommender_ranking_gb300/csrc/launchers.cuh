@@ -164,6 +164,10 @@ cudaError_t launch_attn_tc(const AttnArgs& a, const CUtensorMap& q, const CUtens
 // rec_attn_params, and a 2-D TMA map over a [T][cols] bf16 tensor (box 64 columns x
 // `rows` rows, 128-byte swizzle).
 rec_attn_status check_params(const rec_attn_params* p);
+rec_attn_status from_cuda(cudaError_t e);
+cudaError_t pool_for(int device, cudaMemPool_t* out);  // the library's memory pool of a device
+bool overlaps(const void* a, size_t na, const void* b, size_t nb);
+cudaError_t device_and_sms(int* dev, int* sms);  // the current device
 bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, int rows = kTile);
 // 1 when the plan's items run over many key tiles (AttnArgs::long_items).
 int long_items(const rec_attn_params& p, int batch, long long n_tiles);

@@ -392,6 +392,47 @@ rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows, int64_t widt
                                        float* dbias, void* stream);
 
 /*
+ * Gated feed-forward block of packed token rows (TM20K review page: the SwiGLU layer behind
+ * each attention block; LazFormer and SORT review pages: the same place in their blocks):
+ *   y = (act(x Wg') * (x Wu')) w_out',   w_in = [Wg; Wu].
+ * rec_attn_ffn_bwd gives, for the upstream gradient dy, with g = x Wg', u = x Wu',
+ * dh = dy w_out and p = [dh u act'(g), dh act(g)]:
+ *   dx = p w_in,  dw_in = p' x,  dw_out = dy' (act(g) u).
+ *   dtype       rec_attn_dtype of every tensor.
+ *   activation  rec_attn_activation: silu(g) = g / (1 + e^-g), or gelu(g) = g Phi(g) with the
+ *               normal distribution's Phi itself.
+ *   x, y, dy, dx     device [rows][width].
+ *   w_in, dw_in      device [2 * hidden][width]: the gate's rows, then the up projection's.
+ *   w_out, dw_out    device [width][hidden].
+ *   All contiguous and 16-byte aligned, width and hidden times the element size multiples of
+ *   16 bytes, both at most 65536.  Outputs overlap no input and no other output.  dx, dw_in and
+ *   dw_out may be NULL (not wanted); they are overwritten (rows = 0: dw_in and dw_out are zero).
+ * Sums are fp32.  The gated product h, and in the backward p, are rounded to dtype once as
+ * operands of the next product, and outputs are rounded once.  The backward computes g and u
+ * again from x: nothing of the forward is kept.  Equal calls give equal bits.
+ * Workspace from the library pool on `stream`: forward rows * hidden elements; backward
+ * 3 * rows * hidden elements, and fp32 sums of parts of the rows, at most twice the SMs times 128
+ * KB and a copy of the weights' gradients.
+ * Asynchronous; both calls may be captured into a CUDA graph.
+ * Errors: INVALID_ARG, UNSUPPORTED (too large), OOM, CUDA; a wait that ran out is reported by
+ * rec_attn_dense_device_status.
+ */
+typedef enum { REC_ATTN_SILU = 0, REC_ATTN_GELU = 1 } rec_attn_activation;
+rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation, int64_t rows, int64_t width, int64_t hidden,
+                                 const void* x, const void* w_in, const void* w_out, void* y, void* stream);
+rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation, int64_t rows, int64_t width, int64_t hidden,
+                                 const void* x, const void* w_in, const void* w_out, const void* dy, void* dx,
+                                 void* dw_in, void* dw_out, void* stream);
+
+/*
+ * rec_attn_dense_device_status -- the first error (rec_attn_status) that a kernel of the
+ * feed-forward and scaled calls recorded on the current device: OK, or TIMEOUT when a kernel's
+ * bounded wait ran out (its outputs are then not complete).  Synchronizes `stream`.
+ * Errors: INVALID_ARG, CUDA.
+ */
+rec_attn_status rec_attn_dense_device_status(int32_t* status_out, void* stream);
+
+/*
  * rec_attn_fwd_compress -- rec_attn_fwd whose output is written already compressed:
  * the history compression above (same segments, hist_begin / hist_len per request, same
  * output layout, times and types) applied to the attention output O, fused into the
