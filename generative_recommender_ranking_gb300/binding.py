@@ -123,6 +123,12 @@ def lib() -> ctypes.CDLL:
         L.rec_attn_ffn_fwd.restype = ctypes.c_int
         L.rec_attn_ffn_bwd.argtypes = [i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
         L.rec_attn_ffn_bwd.restype = ctypes.c_int
+        L.rec_attn_scaled_quantize.argtypes = [i32, i32, i64, i64, vp, vp, vp, vp]
+        L.rec_attn_scaled_quantize.restype = ctypes.c_int
+        L.rec_attn_scaled_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, vp]
+        L.rec_attn_scaled_matmul.restype = ctypes.c_int
+        L.rec_attn_ffn_scaled_fwd.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.rec_attn_ffn_scaled_fwd.restype = ctypes.c_int
         L.rec_attn_dense_device_status.argtypes = [ctypes.POINTER(i32), vp]
         L.rec_attn_dense_device_status.restype = ctypes.c_int
         L.rec_attn_fwd_compress.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
@@ -433,6 +439,61 @@ def rec_attn_ffn_bwd(x, w_in, w_out, dy, dx=None, dw_in=None, dw_out=None, activ
               (dw_out, *w_out_s))
     _check(fn, L.rec_attn_ffn_bwd(dtype, _activation(fn, activation), rows, width, hidden, _ptr(x), _ptr(w_in),
                                   _ptr(w_out), _ptr(dy), _ptr(dx), _ptr(dw_in), _ptr(dw_out), _stream(stream)))
+
+
+def _scale_shape(shape, block_rows):
+    return -(-shape[0] // block_rows), -(-shape[1] // 128)
+
+
+def _on_device(fn: str, x) -> None:
+    import torch
+    if not (x.dim() == 2 and x.is_contiguous() and x.is_cuda and x.device.index == torch.cuda.current_device()):
+        raise RecAttnError(fn, ERR_INVALID_ARG)
+
+
+def rec_attn_scaled_quantize(x, q, scale, block_rows: int = 1, stream=None) -> None:
+    """Rows x [rows, width] (bf16 or float32) to q (float8_e4m3fn) with a power-of-two scale
+    (float32) for each 128 values of a row (block_rows 1: [rows, ceil(width / 128)]) or each
+    128 x 128 values (block_rows 128: [ceil(rows / 128), ceil(width / 128)])."""
+    import torch
+    L, fn = lib(), "rec_attn_scaled_quantize"
+    dtype, rows, width = _rows(fn, x)
+    if block_rows not in (1, 128):
+        raise RecAttnError(fn, ERR_INVALID_ARG)
+    _matrices(fn, x, (q, (rows, width), torch.float8_e4m3fn), (scale, _scale_shape(x.shape, block_rows), torch.float32))
+    _check(fn, L.rec_attn_scaled_quantize(dtype, int(block_rows), rows, width, _ptr(x), _ptr(q), _ptr(scale),
+                                          _stream(stream)))
+
+
+def rec_attn_scaled_matmul(a, a_scale, b, b_scale, y, stream=None) -> None:
+    """y = a b' (bf16 [rows, cols]) of a [rows, depth] and b [cols, depth] in float8_e4m3fn: a_scale
+    float32 for each 128 values of a row, b_scale for each 128 x 128 values."""
+    import torch
+    L, fn = lib(), "rec_attn_scaled_matmul"
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _on_device(fn, a)
+    if b.dim() != 2:
+        raise RecAttnError(fn, ERR_INVALID_ARG)
+    (rows, depth), cols = a.shape, b.shape[0]
+    _matrices(fn, a, (a, (rows, depth), f8), (b, (cols, depth), f8), (a_scale, _scale_shape(a.shape, 1), f32),
+              (b_scale, _scale_shape(b.shape, 128), f32), (y, (rows, cols), torch.bfloat16))
+    _check(fn, L.rec_attn_scaled_matmul(rows, cols, depth, _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(y),
+                                        _stream(stream)))
+
+
+def rec_attn_ffn_scaled_fwd(x, w_in, w_in_scale, w_out, w_out_scale, y, activation: str = "silu", stream=None) -> None:
+    """rec_attn_ffn_fwd of bf16 rows with weights in float8_e4m3fn and a float32 scale for each of
+    their 128 x 128 blocks; x and the gated product are quantized on the way."""
+    import torch
+    L, fn = lib(), "rec_attn_ffn_scaled_fwd"
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _, rows, width = _rows(fn, x, y=y)
+    hidden = _hidden(fn, w_out)
+    _matrices(fn, x, (x, (rows, width), torch.bfloat16), (w_in, (2 * hidden, width), f8), (w_out, (width, hidden), f8),
+              (w_in_scale, _scale_shape((2 * hidden, width), 128), f32),
+              (w_out_scale, _scale_shape((width, hidden), 128), f32))
+    _check(fn, L.rec_attn_ffn_scaled_fwd(_activation(fn, activation), rows, width, hidden, _ptr(x), _ptr(w_in),
+                                         _ptr(w_in_scale), _ptr(w_out), _ptr(w_out_scale), _ptr(y), _stream(stream)))
 
 
 def rec_attn_dense_device_status(stream=None) -> int:

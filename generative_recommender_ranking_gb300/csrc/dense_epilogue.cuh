@@ -1,0 +1,57 @@
+// dense_epilogue.cuh -- what the epilogues of the matrix products share: the gate's activation and
+// the stores of result rows.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "ptx_sm103.cuh"
+#include "rec_attn_internal.cuh"
+
+namespace recattn {
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// act(g), and its derivative.  silu: g / (1 + e^-g).  gelu: g Phi(g), Phi by the complementary error
+// function, which keeps its relative accuracy where Phi is small.
+__device__ __forceinline__ float act_value(float g, int act) {
+  if (act == REC_ATTN_SILU) return __fdividef(g, 1.f + __expf(-g));
+  return 0.5f * g * erfcf(-0.70710678f * g);
+}
+__device__ __forceinline__ float act_both(float g, int act, float& slope) {
+  if (act == REC_ATTN_SILU) {
+    const float p = __fdividef(1.f, 1.f + __expf(-g)), v = g * p;
+    slope = fmaf(v, 1.f - p, p);
+    return v;
+  }
+  const float p = 0.5f * erfcf(-0.70710678f * g);
+  slope = fmaf(g, 0.39894228f * __expf(-0.5f * g * g), p);
+  return g * p;
+}
+
+// 32 columns of a row in bf16; `left` columns of the result remain from the first on (a multiple of
+// 8).  wide: the row starts on a 32-byte boundary, whole sectors are written.
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&w)[16], int left, bool wide) {
+  if (wide && left >= 32) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      ptx::st_global_v8(reinterpret_cast<char*>(dst) + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3],
+                        w[8 * c + 4], w[8 * c + 5], w[8 * c + 6], w[8 * c + 7]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (8 * c < left) reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+}
+
+// Tiles of tm x tn in bands of 16 row tiles: the CTAs at work together share a band's rows and the
+// columns' weights in the L2.  Row and column tile of tile t.
+__device__ __forceinline__ int2 band_tile(int t, int tiles_m, int tiles_n) {
+  const int band = t / (16 * tiles_n), in = t - band * 16 * tiles_n;
+  const int rows = min(16, tiles_m - band * 16);
+  return make_int2(band * 16 + in % rows, in / rows);
+}
+
+}  // namespace recattn

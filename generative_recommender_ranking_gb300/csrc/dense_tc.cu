@@ -12,11 +12,10 @@
 //  - kDw sums over the rows; the rows are split into parts so that all SMs have work, the parts'
 //    sums are added in a fixed order (k_dense_sum).
 // Sums are fp32; h and p are rounded to bf16 once, as operands of the next product.
-#include <cuda_bf16.h>
-
 #include <atomic>
 
 #include "dense.cuh"
+#include "dense_epilogue.cuh"
 #include "launchers.cuh"
 #include "ptx_sm103.cuh"
 #include "wait.cuh"
@@ -50,18 +49,15 @@ struct Unit {
   int m0, n0, kb0, kb1, split;
 };
 
-// Tiles in bands of 16 row tiles: the CTAs at work together share a band's rows and the columns'
-// weights in the L2.
 template <int TN>
 __device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i) {
   const int tiles = a.tiles_m * a.tiles_n;
   Unit u;
   u.split = i / tiles;
   const int t = i - u.split * tiles;
-  const int band = t / (16 * a.tiles_n), in = t - band * 16 * a.tiles_n;
-  const int rows = min(16, a.tiles_m - band * 16);
-  u.m0 = (band * 16 + in % rows) * kTile;
-  u.n0 = in / rows * TN;
+  const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
+  u.m0 = at.x * kTile;
+  u.n0 = at.y * TN;
   u.kb0 = (int)((long long)a.kblocks * u.split / a.splits);
   u.kb1 = (int)((long long)a.kblocks * (u.split + 1) / a.splits);
   return u;
@@ -188,42 +184,6 @@ out:
 }
 
 // ------------------------------------------------------------------ epilogues
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-// act(g), and its derivative.  silu: g / (1 + e^-g).  gelu: g Phi(g), Phi by the complementary error
-// function, which keeps its relative accuracy where Phi is small.
-__device__ __forceinline__ float act_value(float g, int act) {
-  if (act == REC_ATTN_SILU) return __fdividef(g, 1.f + __expf(-g));
-  return 0.5f * g * erfcf(-0.70710678f * g);
-}
-__device__ __forceinline__ float act_both(float g, int act, float& slope) {
-  if (act == REC_ATTN_SILU) {
-    const float p = __fdividef(1.f, 1.f + __expf(-g)), v = g * p;
-    slope = fmaf(v, 1.f - p, p);
-    return v;
-  }
-  const float p = 0.5f * erfcf(-0.70710678f * g);
-  slope = fmaf(g, 0.39894228f * __expf(-0.5f * g * g), p);
-  return g * p;
-}
-
-// 32 columns of a row in bf16; `left` columns of the result remain from the first on (a multiple of 8).
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&w)[16], int left, bool wide) {
-  if (wide && left >= 32) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      ptx::st_global_v8(reinterpret_cast<char*>(dst) + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3],
-                        w[8 * c + 4], w[8 * c + 5], w[8 * c + 6], w[8 * c + 7]);
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (8 * c < left) reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-  }
-}
-
 template <DenseOp OP, int BN>
 __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
   using C = Cfg<OP, BN>;
@@ -248,7 +208,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         ptx::tmem_ld32(lanes + buf * BN + BN / 2 + c, v);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          w[e] = bf16x2(act_value(__uint_as_float(g[2 * e]), a.act) * __uint_as_float(v[2 * e]),
+          w[e] = pack_bf16(act_value(__uint_as_float(g[2 * e]), a.act) * __uint_as_float(v[2 * e]),
                         act_value(__uint_as_float(g[2 * e + 1]), a.act) * __uint_as_float(v[2 * e + 1]));
         if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
       } else if constexpr (OP == DenseOp::kDglu) {
@@ -268,9 +228,9 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
             du[k] = dh * act;
             h[k] = act * up;
           }
-          wg[e] = bf16x2(dg[0], dg[1]);
-          wu[e] = bf16x2(du[0], du[1]);
-          wh[e] = bf16x2(h[0], h[1]);
+          wg[e] = pack_bf16(dg[0], dg[1]);
+          wu[e] = pack_bf16(du[0], du[1]);
+          wh[e] = pack_bf16(h[0], h[1]);
         }
         if (in) {
           __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + row * 2 * a.N + col;
@@ -293,7 +253,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         } else {
           uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
           if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
         }
       }
@@ -362,7 +322,7 @@ __global__ void k_dense_sum(const float* part, void* out, long long n, int split
     const float4 v = *reinterpret_cast<const float4*>(part + k * n + i);
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
-  if (BF16) reinterpret_cast<uint2*>(out)[i / 4] = make_uint2(bf16x2(s.x, s.y), bf16x2(s.z, s.w));
+  if (BF16) reinterpret_cast<uint2*>(out)[i / 4] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
   else reinterpret_cast<float4*>(out)[i / 4] = s;
 }
 

@@ -8,6 +8,7 @@
 #include "dense.cuh"
 #include "launchers.cuh"
 #include "rec_attn.h"
+#include "scaled.cuh"
 #include "workspace.cuh"
 
 #define REC_ATTN_API extern "C" __attribute__((visibility("default")))
@@ -183,6 +184,110 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
               m);
     if (e == cudaSuccess && a.splits > 1) e = launch_dense_sum(a.part, dw, (long long)a.M * a.N, a.splits, dtype, st);
   }
+  const cudaError_t ef = ws.give_back();
+  return from_cuda(e != cudaSuccess ? e : ef);
+}
+
+namespace {
+
+long long blocks128(long long n) { return (n + kScaleBlock - 1) / kScaleBlock; }
+
+bool scaled_tiles_ok(long long rows, long long cols) {  // a launch's tiles are counted in 32 bits
+  return blocks128(rows) * blocks128(cols) <= INT32_MAX / 2;
+}
+
+// The product of one scaled layer.
+cudaError_t scaled(bool gated, const void* a, const float* a_scale, long long rows, const void* b, const float* b_scale,
+                   long long cols, long long depth, int act, void* out, float* out_scale, int sms, cudaStream_t st) {
+  CUtensorMap ma, mb;
+  if (!encode_scaled(&ma, a, rows, depth) || !encode_scaled(&mb, b, gated ? 2 * cols : cols, depth))
+    return cudaErrorInvalidValue;
+  ScaledArgs s{};
+  s.M = (int)rows;
+  s.N = (int)cols;
+  s.kblocks = (int)blocks128(depth);
+  s.a_scale = a_scale;
+  s.b_scale = b_scale;
+  s.act = act;
+  s.wide = wide_rows(out, cols);
+  s.out = out;
+  s.out_scale = out_scale;
+  s.status = dense_status();
+  return launch_scaled(gated, ma, mb, s, sms, st);
+}
+
+}  // namespace
+
+REC_ATTN_API rec_attn_status rec_attn_scaled_quantize(int32_t dtype, int32_t block_rows, int64_t rows, int64_t width,
+                                                      const void* x, void* q, float* scale, void* stream) {
+  if (dtype != REC_ATTN_BF16 && dtype != REC_ATTN_FP32) return REC_ATTN_ERR_INVALID_ARG;
+  if ((block_rows != 1 && block_rows != kScaleBlock) || rows < 0 || width < 1 || width % 16) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows > kMaxRows || width > kMaxWidth || !scaled_tiles_ok(rows, width)) return REC_ATTN_ERR_UNSUPPORTED;
+  if (rows == 0) return REC_ATTN_OK;
+  if (!x || !q || !scale || misaligned(x) || misaligned(q) || misaligned(scale)) return REC_ATTN_ERR_INVALID_ARG;
+  const size_t n_scale = 4 * (size_t)((rows + block_rows - 1) / block_rows * blocks128(width));
+  const Range all[3] = {{q, (size_t)(rows * width)}, {scale, n_scale},
+                        {x, (size_t)(rows * width) * (dtype == REC_ATTN_BF16 ? 2 : 4)}};
+  if (clash(all, 2, 3)) return REC_ATTN_ERR_INVALID_ARG;
+  int dev = -1, sms = 0;
+  const cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  const QuantArgs a{x, static_cast<uint8_t*>(q), scale, rows, (int)width, (int)blocks128(width)};
+  return from_cuda(launch_quantize(a, dtype, block_rows, sms, static_cast<cudaStream_t>(stream)));
+}
+
+REC_ATTN_API rec_attn_status rec_attn_scaled_matmul(int64_t rows, int64_t cols, int64_t depth, const void* a,
+                                                    const float* a_scale, const void* b, const float* b_scale, void* y,
+                                                    void* stream) {
+  if (rows < 0 || cols < 1 || depth < 1 || cols % 8 || depth % 16) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows > kMaxRows || cols > 2 * kMaxWidth || depth > 2 * kMaxWidth || !scaled_tiles_ok(rows, cols))
+    return REC_ATTN_ERR_UNSUPPORTED;
+  if (rows == 0) return REC_ATTN_OK;
+  if (!a || !a_scale || !b || !b_scale || !y || misaligned(a) || misaligned(a_scale) || misaligned(b) ||
+      misaligned(b_scale) || misaligned(y))
+    return REC_ATTN_ERR_INVALID_ARG;
+  const size_t kb = blocks128(depth);
+  const Range all[5] = {{y, (size_t)(2 * rows * cols)}, {a, (size_t)(rows * depth)}, {a_scale, 4 * rows * kb},
+                        {b, (size_t)(cols * depth)}, {b_scale, 4 * blocks128(cols) * kb}};
+  if (clash(all, 1, 5)) return REC_ATTN_ERR_INVALID_ARG;
+  int dev = -1, sms = 0;
+  const cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  return from_cuda(scaled(false, a, a_scale, rows, b, b_scale, cols, depth, 0, y, nullptr, sms,
+                          static_cast<cudaStream_t>(stream)));
+}
+
+REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t rows, int64_t width, int64_t hidden,
+                                                     const void* x, const void* w_in, const float* w_in_scale,
+                                                     const void* w_out, const float* w_out_scale, void* y,
+                                                     void* stream) {
+  if (activation != REC_ATTN_SILU && activation != REC_ATTN_GELU) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows < 0 || width < 1 || hidden < 1 || width % 16 || hidden % kScaleBlock) return REC_ATTN_ERR_INVALID_ARG;
+  if (rows > kMaxRows || width > kMaxWidth || hidden > kMaxWidth || !scaled_tiles_ok(rows, std::max(2 * hidden, width)))
+    return REC_ATTN_ERR_UNSUPPORTED;
+  if (rows == 0) return REC_ATTN_OK;
+  if (!x || !w_in || !w_in_scale || !w_out || !w_out_scale || !y || misaligned(x) || misaligned(w_in) ||
+      misaligned(w_in_scale) || misaligned(w_out) || misaligned(w_out_scale) || misaligned(y))
+    return REC_ATTN_ERR_INVALID_ARG;
+  const size_t kw = blocks128(width), kh = blocks128(hidden), n = rows * width;
+  const Range all[6] = {{y, 2 * n}, {x, 2 * n}, {w_in, (size_t)(2 * hidden * width)}, {w_in_scale, 8 * kh * kw},
+                        {w_out, (size_t)(hidden * width)}, {w_out_scale, 4 * kh * kw}};
+  if (clash(all, 1, 6)) return REC_ATTN_ERR_INVALID_ARG;
+  int dev = -1, sms = 0;
+  cudaError_t e = device_and_sms(&dev, &sms);
+  if (e != cudaSuccess) return from_cuda(e);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t off_xs = ws_up(n), off_h = off_xs + ws_up(4 * rows * kw), off_hs = off_h + ws_up(rows * hidden);
+  Workspace ws(st);
+  e = ws.take(dev, off_hs + 4 * rows * kh);
+  if (e != cudaSuccess) return from_cuda(e);
+  uint8_t* const xq = static_cast<uint8_t*>(ws.p);
+  float* const xs = reinterpret_cast<float*>(xq + off_xs);
+  uint8_t* const hq = xq + off_h;
+  float* const hs = reinterpret_cast<float*>(xq + off_hs);
+  e = launch_quantize({x, xq, xs, rows, (int)width, (int)kw}, REC_ATTN_BF16, 1, sms, st);
+  if (e == cudaSuccess) e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, sms, st);
+  if (e == cudaSuccess) e = scaled(false, hq, hs, rows, w_out, w_out_scale, width, hidden, 0, y, nullptr, sms, st);
   const cudaError_t ef = ws.give_back();
   return from_cuda(e != cudaSuccess ? e : ef);
 }

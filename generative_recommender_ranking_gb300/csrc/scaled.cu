@@ -1,0 +1,391 @@
+// scaled.cu -- e4m3 matrices with a scale for each block of 128: the quantizer, and the product on
+// the sm_103a tensor cores.
+//
+// Quantizer: a block's scale is the least power of two that brings its largest value to at most 448,
+// so x / scale is exact and each value is rounded once, to the nearest e4m3 (ties to even).  A
+// floating-point format loses nothing by a power of two but the last step below 2^-6 of its range.
+//
+// Product: y[m][n] = sum over blocks b of sa[m][b] sb[n / 128][b] (sum over the block's k of a[m][k]
+// b[n][k]).  The tensor cores sum one block into one of two TMEM buffers; eight warps take it up,
+// times its scales, into fp32 sums in registers (128 a thread) while the next block is summed.  So the
+// scales may be any fp32, and no sum of more than 128 products is the tensor cores' own.  The gated form
+// takes 128 gate and 128 up columns as a tile and writes their product in e4m3 with its scales.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <atomic>
+
+#include "dense.cuh"
+#include "dense_epilogue.cuh"
+#include "launchers.cuh"
+#include "ptx_sm103.cuh"
+#include "scaled.cuh"
+#include "wait.cuh"
+
+namespace recattn {
+
+namespace {
+
+// ------------------------------------------------------------------ quantizer
+// The scale for a block whose largest finite value is `top`, and its reciprocal: 448 = 1.75 2^8.
+__device__ __forceinline__ float block_scale(float top, float& inverse) {
+  const uint32_t bits = __float_as_uint(top);
+  int e = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = e < 1 ? 1 : e;  // 2^-126: both the scale and its reciprocal are normal
+  if (top == 0.f) e = 127;
+  inverse = __uint_as_float((uint32_t)(254 - e) << 23);
+  return __uint_as_float((uint32_t)e << 23);
+}
+__device__ __forceinline__ float finite_size(float v) {
+  const float a = fabsf(v);
+  return a <= 3.402823466e38f ? a : 0.f;
+}
+// Four values in e4m3; one that is not finite becomes NaN.
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  const auto keep = [](float v) { return fabsf(v) <= 3.402823466e38f ? v : __uint_as_float(0x7fffffffu); };
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(keep(a), keep(b)), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(keep(c), keep(d)), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
+// Eight values of a row.
+template <typename E>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* x, long long i) { v = __ldcs(static_cast<const uint4*>(x) + i); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float at(int k) const {
+    const uint32_t w = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
+    return __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* x, long long i) {
+    a = __ldcs(static_cast<const float4*>(x) + 2 * i);
+    b = __ldcs(static_cast<const float4*>(x) + 2 * i + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float at(int k) const {
+    const float4 h = k < 4 ? a : b;
+    return (k & 3) == 0 ? h.x : (k & 3) == 1 ? h.y : (k & 3) == 2 ? h.z : h.w;
+  }
+};
+template <typename E>
+__device__ __forceinline__ float largest(const Eight<E>& x) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = fmaxf(m, finite_size(x.at(k)));
+  return m;
+}
+template <typename E>
+__device__ __forceinline__ uint2 quantized(const Eight<E>& x, float inv) {
+  return make_uint2(pack_e4m3(x.at(0) * inv, x.at(1) * inv, x.at(2) * inv, x.at(3) * inv),
+                    pack_e4m3(x.at(4) * inv, x.at(5) * inv, x.at(6) * inv, x.at(7) * inv));
+}
+
+constexpr int kQuantThreads = 256, kQuantRun = 4;
+
+// A scale per row and 128 columns: 16 lanes a block, four blocks of theirs in flight.
+template <typename E>
+__global__ void __launch_bounds__(kQuantThreads) k_quantize_rows(QuantArgs a) {
+  const int lane = threadIdx.x & 15, chunks = a.width / 8;
+  const long long units = a.rows * a.blocks, groups = (long long)gridDim.x * (kQuantThreads / 16);
+  const long long first = (long long)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
+  for (long long u0 = first; u0 - (threadIdx.x >> 4 & 1) < units; u0 += groups * kQuantRun) {  // (a warp's halves together)
+    Eight<E> x[kQuantRun];
+    long long at[kQuantRun];
+#pragma unroll
+    for (int j = 0; j < kQuantRun; ++j) {
+      const long long u = u0 + j * groups, row = u / a.blocks;
+      const int c = (int)(u - row * a.blocks) * 16 + lane;
+      const bool in = u < units && c < chunks;
+      at[j] = in ? row * chunks + c : -1;
+      if (in) x[j].load(a.x, at[j]);
+      else x[j].zero();
+    }
+#pragma unroll
+    for (int j = 0; j < kQuantRun; ++j) {
+      float top = largest(x[j]);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float inv;
+      const float scale = block_scale(top, inv);
+      if (at[j] >= 0) {
+        reinterpret_cast<uint2*>(a.q)[at[j]] = quantized(x[j], inv);
+        if (lane == 0) a.scale[u0 + j * groups] = scale;
+      }
+    }
+  }
+}
+
+// A scale per 128 x 128 block: one thread block each, its values in registers meanwhile.
+template <typename E>
+__global__ void __launch_bounds__(kQuantThreads) k_quantize_blocks(QuantArgs a) {
+  __shared__ float s_top[kQuantThreads / 32];
+  const int chunks = a.width / 8, c = (int)(blockIdx.x % a.blocks) * 16 + (threadIdx.x & 15);
+  const long long row0 = (long long)(blockIdx.x / a.blocks) * kScaleBlock + (threadIdx.x >> 4);
+  Eight<E> x[8];
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (row0 + 16 * j < a.rows && c < chunks) x[j].load(a.x, (row0 + 16 * j) * chunks + c);
+    else x[j].zero();
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, largest(x[j]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQuantThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+  float inv;
+  const float scale = block_scale(top, inv);
+  if (threadIdx.x == 0) a.scale[blockIdx.x] = scale;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (row0 + 16 * j < a.rows && c < chunks)
+      reinterpret_cast<uint2*>(a.q)[(row0 + 16 * j) * chunks + c] = quantized(x[j], inv);
+}
+
+// ------------------------------------------------------------------ product
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
+constexpr int kBN = 256;                     // columns of B a tile
+constexpr int kSlab = 128 * 128;             // 128 rows of a block: 128 bytes each
+constexpr int kStage = 3 * kSlab, kStages = 4;
+constexpr int kThreads = 320, kEpiWarps = 8;  // 320: up to 200 registers a thread
+constexpr int kDynamic = kStages * kStage + 1024;
+constexpr uint32_t kTmem = 512;               // two buffers of a block's sums
+
+enum { kFull = 0, kEmpty = 4, kAccFull = 8, kAccEmpty = 10, kPairs = 12, kDone = 13, kBars = 14 };
+
+template <bool GATED>
+__device__ void produce(const ScaledArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, uint8_t* sm, uint64_t* bars,
+                        volatile int* abort_flag, int lane) {
+  const int tiles = a.tiles_m * a.tiles_n;
+  uint32_t n = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
+    const int n0 = at.y * (GATED ? kBN / 2 : kBN), n1 = GATED ? a.N + n0 : n0 + 128;
+    for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
+      const int st = n % kStages;
+      if (!bounded_wait_warp(bars + kEmpty + st, ((n / kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+      if (ptx::elect_one()) {
+        uint8_t* s = sm + st * kStage;
+        ptx::mbar_arrive_expect_tx(bars + kFull + st, kStage);
+        ptx::tma_load_2d(s, ma, kb * 128, at.x * kTile, bars + kFull + st);
+        ptx::tma_load_2d(s + kSlab, mb, kb * 128, n0, bars + kFull + st);
+        ptx::tma_load_2d(s + 2 * kSlab, mb, kb * 128, n1, bars + kFull + st);
+      }
+      __syncwarp();
+    }
+  }
+out:
+  // after an abort, copies may still be in flight
+  if (lane == 0)
+    for (uint32_t j = n > kStages ? n - kStages : 0; j < n; ++j)
+      bounded_drain(bars + kFull + j % kStages, (j / kStages) & 1, kWaitNs / 4);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void issue(const ScaledArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem,
+                                      volatile int* abort_flag) {
+  const int tiles = a.tiles_m * a.tiles_n;
+  const uint32_t s0 = ptx::smem_u32(sm), idesc = ptx::idesc_e4m3_f32(kTile, kBN);
+  const bool el = ptx::elect_one();
+  uint32_t n = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
+      const int st = n % kStages;
+      const uint32_t buf = n & 1;
+      if (!bounded_wait_warp(bars + kAccEmpty + buf, ((n >> 1) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+      if (!bounded_wait_warp(bars + kFull + st, (n / kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
+      ptx::tc_fence_after();
+      if (el) {
+        const uint64_t da = ptx::smem_desc_sw128(s0 + st * kStage, 16, 1024);
+        const uint64_t db = ptx::smem_desc_sw128(s0 + st * kStage + kSlab, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ptx::umma_f8(tmem + buf * kBN, ptx::smem_desc_at(da, 32 * k), ptx::smem_desc_at(db, 32 * k), idesc, k > 0);
+        ptx::umma_commit(bars + kEmpty + st);
+        ptx::umma_commit(bars + kAccFull + buf);
+      }
+      __syncwarp();
+    }
+  }
+out:
+  if (el) {
+    ptx::umma_commit(bars + kDone);
+    bounded_drain(bars + kDone, 0, kWaitNs / 4);
+  }
+  __syncwarp();
+}
+
+// Eight warps: a thread has one row and half of the tile's columns (gated: 64 gate columns and the 64 up
+// columns that belong to them).
+template <bool GATED>
+__device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, float* s_top,
+                       int warp, int lane) {
+  const int tiles = a.tiles_m * a.tiles_n;
+  const int quad = warp & 3, half = (warp - 2) >> 2;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  uint32_t n = 0, it = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
+    const long long row = (long long)at.x * kTile + quad * 32 + lane;
+    const bool in = row < a.M;
+    const float* sa = a.a_scale + (in ? row : 0) * a.kblocks;
+    // the scales of this thread's first and second 64 columns' block
+    const int nb = GATED ? at.y : 2 * at.y + half;
+    const bool nb_in = GATED || (long long)nb * 128 < a.N;
+    const float* sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
+    const float* sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
+    float acc[128];
+#pragma unroll
+    for (int e = 0; e < 128; ++e) acc[e] = 0.f;
+    for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
+      const float sk = in ? __ldg(sa + kb) : 0.f;
+      const float f0 = sk * __ldg(sb0 + kb), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
+      const uint32_t buf = n & 1;
+      if (!bounded_wait_warp(bars + kAccFull + buf, (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        const int col = GATED ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
+        ptx::tmem_ld32(lanes + buf * kBN + col, r);
+        const float f = GATED && c >= 2 ? f1 : f0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[32 * c + e] = fmaf(__uint_as_float(r[e]), f, acc[32 * c + e]);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty + buf);
+    }
+    if constexpr (GATED) {
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < 64; ++e) {
+        acc[e] = act_value(acc[e], a.act) * acc[64 + e];
+        top = fmaxf(top, finite_size(acc[e]));
+      }
+      // the other half's largest value; the tiles take two places in turn
+      float* s = s_top + (it & 1) * 256;
+      s[half * 128 + quad * 32 + lane] = top;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars + kPairs);
+      if (!bounded_wait_warp(bars + kPairs, it & 1, abort_flag, a.status, kWaitNs)) return;
+      top = fmaxf(top, s[(half ^ 1) * 128 + quad * 32 + lane]);
+      float inv;
+      const float scale = block_scale(top, inv);
+      if (in) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack_e4m3(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
+        uint8_t* dst = static_cast<uint8_t*>(a.out) + row * a.N + at.y * 128 + half * 64;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          ptx::st_global_v8(dst + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3], w[8 * c + 4], w[8 * c + 5],
+                            w[8 * c + 6], w[8 * c + 7]);
+        if (half == 0) a.out_scale[row * (a.N / 128) + at.y] = scale;
+      }
+    } else {
+      const int col0 = at.y * kBN + half * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int col = col0 + 32 * c;
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = pack_bf16(acc[32 * c + 2 * e], acc[32 * c + 2 * e + 1]);
+        if (in && col < a.N) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, a.N - col, a.wide);
+      }
+    }
+  }
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_scaled(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const ScaledArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kBars];
+  __shared__ int s_abort;
+  __shared__ uint32_t tmem_slot;
+  __shared__ float s_top[GATED ? 512 : 1];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(bars + kFull + i, 1);
+      ptx::mbar_init(bars + kEmpty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars + kAccFull + i, 1);
+      ptx::mbar_init(bars + kAccEmpty + i, kEpiWarps);
+    }
+    ptx::mbar_init(bars + kPairs, kEpiWarps);
+    ptx::mbar_init(bars + kDone, 1);
+    s_abort = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&tmem_slot, kTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, lane);
+  else if (warp == 1) issue(a, sm, bars, tmem, abort_flag);
+  else finish<GATED>(a, bars, tmem, abort_flag, s_top, warp, lane);
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmem);
+  }
+}
+
+template <bool GATED>
+cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int num_sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED>, kDynamic);
+  if (e != cudaSuccess) return e;
+  const int tn = GATED ? kBN / 2 : kBN;
+  a.tiles_m = (a.M + kTile - 1) / kTile;
+  a.tiles_n = (a.N + tn - 1) / tn;
+  const int tiles = a.tiles_m * a.tiles_n;
+  k_scaled<GATED><<<tiles < num_sms ? tiles : num_sms, kThreads, kDynamic, st>>>(ma, mb, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const QuantArgs& a, int dtype, int block_rows, int num_sms, cudaStream_t st) {
+  const bool bf16 = dtype == REC_ATTN_BF16;
+  if (block_rows == 1) {
+    const long long units = a.rows * a.blocks, run = kQuantThreads / 16 * kQuantRun;
+    const long long blocks = (units + run - 1) / run;
+    const unsigned grid = (unsigned)(blocks < 32LL * num_sms ? blocks : 32LL * num_sms);
+    if (bf16) k_quantize_rows<__nv_bfloat16><<<grid, kQuantThreads, 0, st>>>(a);
+    else k_quantize_rows<float><<<grid, kQuantThreads, 0, st>>>(a);
+  } else {
+    const unsigned grid = (unsigned)((a.rows + kScaleBlock - 1) / kScaleBlock * a.blocks);
+    if (bf16) k_quantize_blocks<__nv_bfloat16><<<grid, kQuantThreads, 0, st>>>(a);
+    else k_quantize_blocks<float><<<grid, kQuantThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_scaled(bool gated, const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int num_sms,
+                          cudaStream_t st) {
+  return gated ? run<true>(ma, mb, a, num_sms, st) : run<false>(ma, mb, a, num_sms, st);
+}
+
+}  // namespace recattn

@@ -425,6 +425,44 @@ rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation, int64_t rows
                                  void* dw_in, void* dw_out, void* stream);
 
 /*
+ * Matrices in e4m3 (8-bit floating point, largest value 448) with a float scale for each block
+ * of 128: the value of an element is its e4m3 value times its block's scale (serving: weights of
+ * half the bytes, products at twice the rate).  Activations have a scale for 128 values of a
+ * row, [rows][ceil(width / 128)]; weights one for 128 x 128 values,
+ * [ceil(rows / 128)][ceil(width / 128)].  Blocks at an edge are smaller.
+ *
+ * rec_attn_scaled_quantize -- x [rows][width] (dtype) to q (e4m3) and scale.
+ *   block_rows  1 (activations) or 128 (weights).
+ *   A block's scale is the least power of two, from 2^-126 up, that brings its largest finite
+ *   value to at most 448 (1 for a block without any but zeros): x / scale is exact, and q is the
+ *   nearest e4m3 value, ties to even.  A value that is not finite becomes NaN.
+ *   width a multiple of 16, at most 65536.
+ *
+ * rec_attn_scaled_matmul -- y[m][n] = sum over blocks k of a_scale[m][k] b_scale[n / 128][k]
+ *   times the sum over the block of a[m][.] b[n][.]: a [rows][depth] with a scale for each row's
+ *   128 values, b [cols][depth] with one for each 128 x 128, any finite scales whose products are
+ *   finite; y bf16 [rows][cols].  cols a multiple of 8, depth of 16, both at most 131072.  A
+ *   block is summed by the tensor cores, the blocks in fp32; y is rounded once.
+ *
+ * rec_attn_ffn_scaled_fwd -- rec_attn_ffn_fwd for bf16 rows x and e4m3 weights
+ *   (w_in_scale [2 * hidden / 128][ceil(width / 128)], w_out_scale [ceil(width / 128)]
+ *   [hidden / 128]): x and the gated product h are quantized as above with a scale for 128 values
+ *   of a row.  width a multiple of 16, hidden of 128.  Workspace from the library pool on
+ *   `stream`: rows * (width + hidden) * (1 + 1 / 32) bytes.
+ *
+ * All device, contiguous, 16-byte aligned; outputs overlap nothing.  Asynchronous; the calls may
+ * be captured into a CUDA graph.  Equal calls give equal bits.
+ * Errors: INVALID_ARG, UNSUPPORTED (too large), OOM, CUDA; rec_attn_dense_device_status.
+ */
+rec_attn_status rec_attn_scaled_quantize(int32_t dtype, int32_t block_rows, int64_t rows, int64_t width, const void* x,
+                                         void* q, float* scale, void* stream);
+rec_attn_status rec_attn_scaled_matmul(int64_t rows, int64_t cols, int64_t depth, const void* a, const float* a_scale,
+                                       const void* b, const float* b_scale, void* y, void* stream);
+rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t rows, int64_t width, int64_t hidden, const void* x,
+                                        const void* w_in, const float* w_in_scale, const void* w_out,
+                                        const float* w_out_scale, void* y, void* stream);
+
+/*
  * rec_attn_dense_device_status -- the first error (rec_attn_status) that a kernel of the
  * feed-forward and scaled calls recorded on the current device: OK, or TIMEOUT when a kernel's
  * bounded wait ran out (its outputs are then not complete).  Synchronizes `stream`.
