@@ -32,6 +32,21 @@ struct DenseArgs {
 // A row-major [rows][cols] bf16 operand as a TMA map; mn_major: the summed axis runs over its rows.
 bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major);
 int* dense_status();
+
+// fp32 operands (dense_fp32.cu): a matrix as three bf16 planes whose sum it is, rows `ld` apart.
+struct Planes {
+  void* p;              // [3][rows][ld] bf16
+  long long rows, cols, ld;
+  __host__ __device__ size_t plane() const { return (size_t)rows * ld * 2; }
+};
+struct Dense32Args {
+  DenseArgs d;          // out: float rows (kOut, kDx, kDw); part as for kDw, of any of the three
+  Planes h, p;          // what kGlu and kDglu write
+};
+cudaError_t launch_split(const float* x, const Planes& to, cudaStream_t st);
+bool encode_planes(CUtensorMap* m, const Planes& a);
+cudaError_t launch_dense32(DenseOp op, const CUtensorMap (&maps)[4], Dense32Args a, int num_sms, cudaStream_t st);
+int dense32_splits(int M, int N, int kblocks, int num_sms);
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&maps)[4], DenseArgs a, int num_sms, cudaStream_t st);
 // kDw: parts of the summed axis.
 int dense_splits(int M, int N, int kblocks, int num_sms);

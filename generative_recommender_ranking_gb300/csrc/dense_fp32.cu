@@ -1,0 +1,361 @@
+// dense_fp32.cu -- the products of the gated feed-forward block in fp32, on the tensor cores.
+//
+// An fp32 value is the sum of three bf16 values (8 bits each: hi, mid, lo), and a product of two
+// such sums is, to 2^-24 of it, that of six pairs: hi lo, mid mid, lo hi, hi mid, mid hi, hi hi (in
+// this order, small ones first).  bf16 MMAs at a sixth of their rate are still five times CUDA cores.
+// The tensor cores cut each addition's result off (measured: 2^-24 of the sum for each 16 products,
+// always towards zero), so they sum no more than a block of 64; eight warps add the blocks up in
+// fp32 registers, rounded to nearest.
+// Tiles are 128 x 128 (gated: 64 gate and 64 up columns; the backward's dh 64), a ring of two
+// 64-deep stages holds all six planes, so each is loaded once.  h and p are written as planes.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "dense.cuh"
+#include "dense_epilogue.cuh"
+#include "launchers.cuh"
+#include "ptx_sm103.cuh"
+#include "wait.cuh"
+
+namespace recattn {
+
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
+constexpr int kBK = 64, kSlab = 64 * 128;    // 64 rows of 128 bytes
+constexpr int kPlane = 2 * kSlab;            // 128 rows of one plane
+constexpr int kStage = 6 * kPlane, kStages = 2;
+constexpr int kThreads = 320, kEpiWarps = 8;
+constexpr int kDynamic = kStages * kStage + 1024;
+constexpr uint32_t kTmem = 256;              // two buffers of a block's sums
+constexpr int kTileN = 128;
+
+enum { kFull = 0, kEmpty = 2, kAccFull = 4, kAccEmpty = 6, kDone = 8, kBars = 9 };
+
+template <DenseOp OP>
+struct Cfg {
+  static constexpr bool kPair = OP == DenseOp::kGlu || OP == DenseOp::kDglu;
+  static constexpr bool kAMn = OP == DenseOp::kDw, kBMn = OP == DenseOp::kDx || OP == DenseOp::kDw;
+  static constexpr int kCols = kPair ? 64 : 128;  // of the result
+};
+
+struct Unit {
+  int m0, n0, kb0, kb1, split;
+};
+template <int TN>
+__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i) {
+  const int tiles = a.tiles_m * a.tiles_n;
+  Unit u;
+  u.split = i / tiles;
+  const int2 at = band_tile(i - u.split * tiles, a.tiles_m, a.tiles_n);
+  u.m0 = at.x * kTile;
+  u.n0 = at.y * TN;
+  u.kb0 = (int)((long long)a.kblocks * u.split / a.splits);
+  u.kb1 = (int)((long long)a.kblocks * (u.split + 1) / a.splits);
+  return u;
+}
+
+// 64 rows (columns) of one plane at mn0, block kb of the summed axis.
+template <bool MN>
+__device__ __forceinline__ void load_slab(uint8_t* dst, const CUtensorMap* map, int mn0, int kb, int plane, uint64_t* bar) {
+  if (MN) ptx::tma_load_3d(dst, map, mn0, kb * kBK, plane, bar);
+  else ptx::tma_load_3d(dst, map, kb * kBK, mn0, plane, bar);
+}
+
+template <DenseOp OP>
+__device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* ma2,
+                        const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, int lane) {
+  using C = Cfg<OP>;
+  const int units = a.tiles_m * a.tiles_n * a.splits;
+  uint32_t n = 0;
+  for (int i = blockIdx.x; i < units; i += gridDim.x) {
+    const Unit u = unit_at<C::kCols>(a, i);
+    const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
+    for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
+      const int st = n % kStages;
+      if (!bounded_wait_warp(bars + kEmpty + st, ((n / kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+      if (ptx::elect_one()) {
+        uint8_t* s = sm + st * kStage;
+        uint64_t* bar = bars + kFull + st;
+        const bool grad = OP == DenseOp::kDglu && kb < 0;
+        ptx::mbar_arrive_expect_tx(bar, grad ? 9 * kSlab : kStage);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          uint8_t *sa = s + p * kPlane, *sb = s + (3 + p) * kPlane;
+          if (grad) {
+            load_slab<false>(sa, ma2, u.m0, kb + first, p, bar);
+            load_slab<false>(sa + kSlab, ma2, u.m0 + 64, kb + first, p, bar);
+            load_slab<true>(sb, mb2, u.n0, kb + first, p, bar);
+          } else {
+            load_slab<C::kAMn>(sa, ma, u.m0, kb, p, bar);
+            load_slab<C::kAMn>(sa + kSlab, ma, u.m0 + 64, kb, p, bar);
+            load_slab<C::kBMn>(sb, mb, u.n0, kb, p, bar);
+            load_slab<C::kBMn>(sb + kSlab, mb, C::kPair ? a.N + u.n0 : u.n0 + 64, kb, p, bar);
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+out:
+  // after an abort, copies may still be in flight
+  if (lane == 0)
+    for (uint32_t j = n > kStages ? n - kStages : 0; j < n; ++j)
+      bounded_drain(bars + kFull + j % kStages, (j / kStages) & 1, kWaitNs / 4);
+  __syncwarp();
+}
+
+// The six pairs of a stage's planes into one buffer.
+template <bool AMN, bool BMN, int N>
+__device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s) {
+  const uint32_t idesc = ptx::idesc_bf16_f32(kTile, N, AMN, BMN);
+  const uint64_t da = ptx::smem_desc_sw128(s, AMN ? kSlab : 16, 1024);
+  const uint64_t db = ptx::smem_desc_sw128(s + 3 * kPlane, BMN ? kSlab : 16, 1024);
+  constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+  for (int j = 0; j < 6; ++j)
+#pragma unroll
+    for (int k = 0; k < kBK / 16; ++k)
+      ptx::umma_f16(acc, ptx::smem_desc_at(da, kA[j] * kPlane + k * (AMN ? 2048 : 32)),
+                    ptx::smem_desc_at(db, kB[j] * kPlane + k * (BMN ? 2048 : 32)), idesc, j + k > 0);
+}
+
+template <DenseOp OP>
+__device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
+  using C = Cfg<OP>;
+  const int units = a.tiles_m * a.tiles_n * a.splits;
+  const uint32_t s0 = ptx::smem_u32(sm);
+  const bool el = ptx::elect_one();
+  uint32_t n = 0;
+  for (int i = blockIdx.x; i < units; i += gridDim.x) {
+    const Unit u = unit_at<C::kCols>(a, i);
+    for (int kb = OP == DenseOp::kDglu ? -a.kblocks : u.kb0; kb < u.kb1; ++kb, ++n) {
+      const int st = n % kStages;
+      const uint32_t buf = n & 1;
+      if (!bounded_wait_warp(bars + kAccEmpty + buf, ((n >> 1) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+      if (!bounded_wait_warp(bars + kFull + st, (n / kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
+      ptx::tc_fence_after();
+      if (el) {
+        if (OP == DenseOp::kDglu && kb < 0) block_mma<false, true, 64>(tmem + buf * kTileN, s0 + st * kStage);
+        else block_mma<C::kAMn, C::kBMn, kTileN>(tmem + buf * kTileN, s0 + st * kStage);
+        ptx::umma_commit(bars + kEmpty + st);
+        ptx::umma_commit(bars + kAccFull + buf);
+      }
+      __syncwarp();
+    }
+  }
+out:
+  if (el) {
+    ptx::umma_commit(bars + kDone);
+    bounded_drain(bars + kDone, 0, kWaitNs / 4);
+  }
+  __syncwarp();
+}
+
+// x as hi + mid + lo.  (A finite value past bf16's largest is cut instead of rounded to infinity;
+// one that is not finite is in hi alone.)
+__device__ __forceinline__ void split3(float x, float& hi, float& mid, float& lo) {
+  hi = __bfloat162float(__float2bfloat16_rn(x));
+  if (!(fabsf(hi) <= 3.402823466e38f)) hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  const float r = x - hi;
+  const bool fine = fabsf(r) <= 3.402823466e38f;
+  mid = fine ? __bfloat162float(__float2bfloat16_rn(r)) : 0.f;
+  lo = fine ? r - mid : 0.f;
+}
+// Four columns of a row into the planes.
+__device__ __forceinline__ void store_planes(const Planes& to, long long row, int col, float a, float b, float c, float d) {
+  const float x[4] = {a, b, c, d};
+  float v[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split3(x[i], v[0][i], v[1][i], v[2][i]);
+  char* at = static_cast<char*>(to.p) + (row * to.ld + col) * 2;
+#pragma unroll
+  for (int p = 0; p < 3; ++p, at += to.plane())
+    *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(v[p][0], v[p][1]), pack_bf16(v[p][2], v[p][3]));
+}
+
+__device__ __forceinline__ float silu_or_gelu(float g, int act, float& slope) {
+  if (act == REC_ATTN_SILU) {
+    const float p = 1.f / (1.f + expf(-g)), v = g * p;
+    slope = fmaf(v, 1.f - p, p);
+    return v;
+  }
+  const float p = 0.5f * erfcf(-0.70710678f * g);
+  slope = fmaf(g, 0.39894228f * expf(-0.5f * g * g), p);
+  return g * p;
+}
+
+template <DenseOp OP>
+__device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
+  using C = Cfg<OP>;
+  const DenseArgs& a = aa.d;
+  const int units = a.tiles_m * a.tiles_n * a.splits;
+  const int quad = warp & 3, half = (warp - 2) >> 2;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  const int c0 = C::kPair ? 32 * half : 64 * half, c1 = C::kPair ? 64 + 32 * half : 64 * half + 32;
+  uint32_t n = 0;
+  // a block's sums of 32 columns, added up
+  const auto take = [&](float (&to)[32], uint32_t buf, int col) {
+    uint32_t r[32];
+    ptx::tmem_ld32(lanes + buf * kTileN + col, r);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) to[e] += __uint_as_float(r[e]);
+  };
+  const auto taken = [&](uint32_t buf) {
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty + buf);
+  };
+  for (int i = blockIdx.x; i < units; i += gridDim.x) {
+    const Unit u = unit_at<C::kCols>(a, i);
+    float x0[32], x1[32], dh[OP == DenseOp::kDglu ? 32 : 1];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x0[e] = x1[e] = 0.f;
+    if constexpr (OP == DenseOp::kDglu) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) dh[e] = 0.f;
+      for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
+        if (!bounded_wait_warp(bars + kAccFull + (n & 1), (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
+        ptx::tc_fence_after();
+        take(dh, n & 1, 32 * half);
+        taken(n & 1);
+      }
+    }
+    for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
+      if (!bounded_wait_warp(bars + kAccFull + (n & 1), (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
+      ptx::tc_fence_after();
+      take(x0, n & 1, c0);
+      take(x1, n & 1, c1);
+      taken(n & 1);
+    }
+    const long long row = u.m0 + quad * 32 + lane;
+    if (row >= a.M) continue;
+    if constexpr (C::kPair) {
+      const int col = u.n0 + 32 * half;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        float h[4], dg[4], du[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float slope;
+          const float act = silu_or_gelu(x0[e + k], a.act, slope);
+          h[k] = act * x1[e + k];
+          if constexpr (OP == DenseOp::kDglu) {
+            dg[k] = dh[e + k] * x1[e + k] * slope;
+            du[k] = dh[e + k] * act;
+          }
+        }
+        if (col + e >= a.N) break;
+        store_planes(aa.h, row, col + e, h[0], h[1], h[2], h[3]);
+        if constexpr (OP == DenseOp::kDglu) {
+          store_planes(aa.p, row, col + e, dg[0], dg[1], dg[2], dg[3]);
+          store_planes(aa.p, row, a.N + col + e, du[0], du[1], du[2], du[3]);
+        }
+      }
+    } else {
+      float* const out = (a.splits > 1 ? a.part + (long long)u.split * a.M * a.N : static_cast<float*>(a.out)) + row * a.N;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        if (u.n0 + c0 + e < a.N)
+          *reinterpret_cast<float4*>(out + u.n0 + c0 + e) = make_float4(x0[e], x0[e + 1], x0[e + 2], x0[e + 3]);
+        if (u.n0 + c1 + e < a.N)
+          *reinterpret_cast<float4*>(out + u.n0 + c1 + e) = make_float4(x1[e], x1[e + 1], x1[e + 2], x1[e + 3]);
+      }
+    }
+  }
+}
+
+template <DenseOp OP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_dense32(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+              const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2, const Dense32Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kBars];
+  __shared__ int s_abort;
+  __shared__ uint32_t tmem_slot;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(bars + kFull + i, 1);
+      ptx::mbar_init(bars + kEmpty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars + kAccFull + i, 1);
+      ptx::mbar_init(bars + kAccEmpty + i, kEpiWarps);
+    }
+    ptx::mbar_init(bars + kDone, 1);
+    s_abort = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&tmem_slot, kTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp == 0) produce<OP>(a.d, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, lane);
+  else if (warp == 1) issue<OP>(a.d, sm, bars, tmem, abort_flag);
+  else finish<OP>(a, bars, tmem, abort_flag, warp, lane);
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmem);
+  }
+}
+
+__global__ void __launch_bounds__(256) k_split(const float* x, Planes to) {
+  const int per_row = (int)(to.cols / 4);
+  const long long n = to.rows * per_row;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(x) + i);
+    const long long row = i / per_row;
+    store_planes(to, row, 4 * (int)(i - row * per_row), v.x, v.y, v.z, v.w);
+  }
+}
+
+template <DenseOp OP>
+cudaError_t run(const CUtensorMap (&m)[4], Dense32Args a, int num_sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(done, (const void*)k_dense32<OP>, kDynamic);
+  if (e != cudaSuccess) return e;
+  a.d.tiles_m = (a.d.M + kTile - 1) / kTile;
+  a.d.tiles_n = (a.d.N + Cfg<OP>::kCols - 1) / Cfg<OP>::kCols;
+  const int units = a.d.tiles_m * a.d.tiles_n * a.d.splits;
+  k_dense32<OP><<<units < num_sms ? units : num_sms, kThreads, kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_split(const float* x, const Planes& to, cudaStream_t st) {
+  const long long blocks = (to.rows * (to.cols / 4) + 255) / 256;
+  k_split<<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, st>>>(x, to);
+  return cudaGetLastError();
+}
+
+// Parts of the summed axis that give every SM work: each at least four blocks deep.
+int dense32_splits(int M, int N, int kblocks, int num_sms) {
+  const long long tiles = (long long)((M + kTile - 1) / kTile) * ((N + kTileN - 1) / kTileN);
+  long long s = num_sms / tiles;
+  if (s > kblocks / 4) s = kblocks / 4;
+  return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_dense32(DenseOp op, const CUtensorMap (&m)[4], Dense32Args a, int num_sms, cudaStream_t st) {
+  switch (op) {
+    case DenseOp::kGlu: return run<DenseOp::kGlu>(m, a, num_sms, st);
+    case DenseOp::kOut: return run<DenseOp::kOut>(m, a, num_sms, st);
+    case DenseOp::kDglu: return run<DenseOp::kDglu>(m, a, num_sms, st);
+    case DenseOp::kDx: return run<DenseOp::kDx>(m, a, num_sms, st);
+    case DenseOp::kDw: return run<DenseOp::kDw>(m, a, num_sms, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace recattn

@@ -43,7 +43,7 @@ rec_attn_status check_ffn(int32_t dtype, int32_t act, int64_t rows, int64_t widt
   if (rows < 0 || width < 1 || hidden < 1 || width % unit || hidden % unit) return REC_ATTN_ERR_INVALID_ARG;
   if (rows > kMaxRows || width > kMaxWidth || hidden > kMaxWidth) return REC_ATTN_ERR_UNSUPPORTED;
   // a launch's tiles are counted in 32 bits
-  if (((rows + kTile - 1) / kTile) * ((2 * hidden + kTile - 1) / kTile) > INT32_MAX / 2) return REC_ATTN_ERR_UNSUPPORTED;
+  if (((rows + kTile - 1) / kTile) * ((2 * std::max(hidden, width) + kTile - 1) / kTile) > INT32_MAX / 2) return REC_ATTN_ERR_UNSUPPORTED;
   return REC_ATTN_OK;
 }
 
@@ -67,6 +67,109 @@ cudaError_t dense(DenseOp op, const DenseArgs& a, int sms, cudaStream_t st, bool
   return encoded ? launch_dense(op, m, a, sms, st) : cudaErrorInvalidValue;
 }
 
+// fp32 matrices as bf16 planes, laid out one after the other in a workspace.
+struct PlaneLayout {
+  size_t bytes = 0;
+  Planes add(long long rows, long long cols) {  // p: the offset, until the workspace is there
+    Planes a{reinterpret_cast<void*>(bytes), rows, cols, (cols + 7) / 8 * 8};
+    bytes += ws_up(3 * a.plane());
+    return a;
+  }
+};
+Planes placed(const Planes& a, const Workspace& ws) {
+  Planes b = a;
+  b.p = static_cast<char*>(ws.p) + reinterpret_cast<size_t>(a.p);
+  return b;
+}
+
+// out = a b' over `depth`, the sums of parts of it (s > 1) in part.
+cudaError_t plain32(DenseOp op, const Planes& a, const Planes& b, long long M, long long N, long long depth, int s,
+                    float* part, void* out, int sms, cudaStream_t st) {
+  CUtensorMap m[4];
+  if (!encode_planes(&m[0], a) || !encode_planes(&m[1], b)) return cudaErrorInvalidValue;
+  Dense32Args d{};
+  d.d.M = (int)M;
+  d.d.N = (int)N;
+  d.d.kblocks = blocks64(depth);
+  d.d.splits = s;
+  d.d.part = part;
+  d.d.out = out;
+  d.d.status = dense_status();
+  const cudaError_t e = launch_dense32(op, m, d, sms, st);
+  return e == cudaSuccess && s > 1 ? launch_dense_sum(part, out, M * N, s, REC_ATTN_FP32, st) : e;
+}
+
+cudaError_t ffn32_fwd(int act, long long R, long long W, long long H, const void* x, const void* w_in, const void* w_out,
+                      void* y, int dev, int sms, cudaStream_t st) {
+  PlaneLayout l;
+  Planes px = l.add(R, W), pi = l.add(2 * H, W), po = l.add(W, H), ph = l.add(R, H);
+  const int s = dense32_splits((int)R, (int)W, blocks64(H), sms);
+  const size_t off_part = l.bytes;
+  Workspace ws(st);
+  cudaError_t e = ws.take(dev, off_part + (s > 1 ? (size_t)s * R * W * 4 : 0));
+  if (e != cudaSuccess) return e;
+  px = placed(px, ws), pi = placed(pi, ws), po = placed(po, ws), ph = placed(ph, ws);
+  e = launch_split(static_cast<const float*>(x), px, st);
+  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_in), pi, st);
+  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_out), po, st);
+  CUtensorMap m[4];
+  if (e == cudaSuccess && !(encode_planes(&m[0], px) && encode_planes(&m[1], pi))) e = cudaErrorInvalidValue;
+  Dense32Args d{};
+  d.d.M = (int)R;
+  d.d.N = (int)H;
+  d.d.kblocks = blocks64(W);
+  d.d.splits = 1;
+  d.d.act = act;
+  d.d.status = dense_status();
+  d.h = ph;
+  if (e == cudaSuccess) e = launch_dense32(DenseOp::kGlu, m, d, sms, st);
+  if (e == cudaSuccess)
+    e = plain32(DenseOp::kOut, ph, po, R, W, H, s, reinterpret_cast<float*>(static_cast<char*>(ws.p) + off_part), y, sms, st);
+  const cudaError_t ef = ws.give_back();
+  return e != cudaSuccess ? e : ef;
+}
+
+cudaError_t ffn32_bwd(int act, long long R, long long W, long long H, const void* x, const void* w_in, const void* w_out,
+                      const void* dy, void* dx, void* dw_in, void* dw_out, int dev, int sms, cudaStream_t st) {
+  PlaneLayout l;
+  Planes px = l.add(R, W), pdy = l.add(R, W), pi = l.add(2 * H, W), po = l.add(W, H), ph = l.add(R, H), pp = l.add(R, 2 * H);
+  const int sx = dense32_splits((int)R, (int)W, blocks64(2 * H), sms);
+  const int si = dense32_splits((int)(2 * H), (int)W, blocks64(R), sms), so = dense32_splits((int)W, (int)H, blocks64(R), sms);
+  size_t n_part = 0;
+  if (dx && sx > 1) n_part = (size_t)sx * R * W;
+  if (dw_in && si > 1) n_part = std::max(n_part, (size_t)(si * 2 * H * W));
+  if (dw_out && so > 1) n_part = std::max(n_part, (size_t)(so * H * W));
+  const size_t off_part = l.bytes;
+  Workspace ws(st);
+  cudaError_t e = ws.take(dev, off_part + 4 * n_part);
+  if (e != cudaSuccess) return e;
+  px = placed(px, ws), pdy = placed(pdy, ws), pi = placed(pi, ws), po = placed(po, ws), ph = placed(ph, ws), pp = placed(pp, ws);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws.p) + off_part);
+  e = launch_split(static_cast<const float*>(x), px, st);
+  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(dy), pdy, st);
+  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_in), pi, st);
+  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_out), po, st);
+  CUtensorMap m[4];
+  if (e == cudaSuccess &&
+      !(encode_planes(&m[0], px) && encode_planes(&m[1], pi) && encode_planes(&m[2], pdy) && encode_planes(&m[3], po)))
+    e = cudaErrorInvalidValue;
+  Dense32Args d{};
+  d.d.M = (int)R;
+  d.d.N = (int)H;
+  d.d.kblocks = blocks64(W);
+  d.d.splits = 1;
+  d.d.act = act;
+  d.d.status = dense_status();
+  d.h = ph;
+  d.p = pp;
+  if (e == cudaSuccess) e = launch_dense32(DenseOp::kDglu, m, d, sms, st);
+  if (e == cudaSuccess && dx) e = plain32(DenseOp::kDx, pp, pi, R, W, 2 * H, sx, part, dx, sms, st);
+  if (e == cudaSuccess && dw_in) e = plain32(DenseOp::kDw, pp, px, 2 * H, W, R, si, part, dw_in, sms, st);
+  if (e == cudaSuccess && dw_out) e = plain32(DenseOp::kDw, pdy, ph, W, H, R, so, part, dw_out, sms, st);
+  const cudaError_t ef = ws.give_back();
+  return e != cudaSuccess ? e : ef;
+}
+
 }  // namespace
 
 REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation, int64_t rows, int64_t width,
@@ -81,11 +184,11 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
   const Range all[4] = {{y, rows * width * es}, {x, rows * width * es}, {w_in, 2 * hidden * width * es},
                         {w_out, hidden * width * es}};
   if (clash(all, 1, 4)) return REC_ATTN_ERR_INVALID_ARG;
-  if (dtype != REC_ATTN_BF16) return REC_ATTN_ERR_UNSUPPORTED;
   int dev = -1, sms = 0;
   cudaError_t e = device_and_sms(&dev, &sms);
   if (e != cudaSuccess) return from_cuda(e);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == REC_ATTN_FP32) return from_cuda(ffn32_fwd(activation, rows, width, hidden, x, w_in, w_out, y, dev, sms, st));
   Workspace ws(st);
   e = ws.take(dev, rows * hidden * es);
   if (e != cudaSuccess) return from_cuda(e);
@@ -126,7 +229,6 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
   const Range all[7] = {{rows > 0 ? dx : nullptr, nx}, {dw_in, ni}, {dw_out, no}, {rows > 0 ? x : nullptr, nx},
                         {w_in, ni}, {w_out, no}, {rows > 0 ? dy : nullptr, nx}};
   if (clash(all, 3, 7)) return REC_ATTN_ERR_INVALID_ARG;
-  if (dtype != REC_ATTN_BF16) return REC_ATTN_ERR_UNSUPPORTED;
   int dev = -1, sms = 0;
   cudaError_t e = device_and_sms(&dev, &sms);
   if (e != cudaSuccess) return from_cuda(e);
@@ -136,6 +238,8 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     if (e == cudaSuccess && dw_out) e = cudaMemsetAsync(dw_out, 0, no, st);
     return from_cuda(e);
   }
+  if (dtype == REC_ATTN_FP32)
+    return from_cuda(ffn32_bwd(activation, rows, width, hidden, x, w_in, w_out, dy, dx, dw_in, dw_out, dev, sms, st));
   const int kr = blocks64(rows), W = (int)width, H = (int)hidden;
   const int si = dw_in ? dense_splits(2 * H, W, kr, sms) : 1, so = dw_out ? dense_splits(W, H, kr, sms) : 1;
   const size_t n_part = std::max(si > 1 ? (size_t)si * 2 * H * W : 0, so > 1 ? (size_t)so * H * W : 0);
