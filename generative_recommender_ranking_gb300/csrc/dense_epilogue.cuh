@@ -16,12 +16,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // act(g), and its derivative.  silu: g / (1 + e^-g).  gelu: g Phi(g), Phi by the complementary error
 // function, which keeps its relative accuracy where Phi is small.
-__device__ __forceinline__ float act_value(float g, int act) {
-  if (act == REC_ATTN_SILU) return __fdividef(g, 1.f + __expf(-g));
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+  if (ACT == REC_ATTN_SILU) return __fdividef(g, 1.f + __expf(-g));
   return 0.5f * g * erfcf(-0.70710678f * g);
 }
-__device__ __forceinline__ float act_both(float g, int act, float& slope) {
-  if (act == REC_ATTN_SILU) {
+template <int ACT>
+__device__ __forceinline__ float act_both(float g, float& slope) {
+  if (ACT == REC_ATTN_SILU) {
     const float p = __fdividef(1.f, 1.f + __expf(-g)), v = g * p;
     slope = fmaf(v, 1.f - p, p);
     return v;
@@ -42,6 +44,17 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&
   } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
+      if (8 * c < left) reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+}
+
+// 16 columns.
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&w)[8], int left, bool wide) {
+  if (wide && left >= 16) {
+    ptx::st_global_v8(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
       if (8 * c < left) reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   }
 }

@@ -175,8 +175,10 @@ __device__ __forceinline__ void store_planes(const Planes& to, long long row, in
     *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(v[p][0], v[p][1]), pack_bf16(v[p][2], v[p][3]));
 }
 
-__device__ __forceinline__ float silu_or_gelu(float g, int act, float& slope) {
-  if (act == REC_ATTN_SILU) {
+// (the activation with the library's exponential: fp32 keeps its last bits)
+template <int ACT>
+__device__ __forceinline__ float act32(float g, float& slope) {
+  if (ACT == REC_ATTN_SILU) {
     const float p = 1.f / (1.f + expf(-g)), v = g * p;
     slope = fmaf(v, 1.f - p, p);
     return v;
@@ -186,7 +188,7 @@ __device__ __forceinline__ float silu_or_gelu(float g, int act, float& slope) {
   return g * p;
 }
 
-template <DenseOp OP>
+template <DenseOp OP, int ACT>
 __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
   using C = Cfg<OP>;
   const DenseArgs& a = aa.d;
@@ -239,7 +241,7 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float slope;
-          const float act = silu_or_gelu(x0[e + k], a.act, slope);
+          const float act = act32<ACT>(x0[e + k], slope);
           h[k] = act * x1[e + k];
           if constexpr (OP == DenseOp::kDglu) {
             dg[k] = dh[e + k] * x1[e + k] * slope;
@@ -266,7 +268,7 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
   }
 }
 
-template <DenseOp OP>
+template <DenseOp OP, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_dense32(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
               const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2, const Dense32Args a) {
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   if (warp == 0) produce<OP>(a.d, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, lane);
   else if (warp == 1) issue<OP>(a.d, sm, bars, tmem, abort_flag);
-  else finish<OP>(a, bars, tmem, abort_flag, warp, lane);
+  else finish<OP, ACT>(a, bars, tmem, abort_flag, warp, lane);
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -319,15 +321,15 @@ __global__ void __launch_bounds__(256) k_split(const float* x, Planes to) {
   }
 }
 
-template <DenseOp OP>
+template <DenseOp OP, int ACT>
 cudaError_t run(const CUtensorMap (&m)[4], Dense32Args a, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(done, (const void*)k_dense32<OP>, kDynamic);
+  const cudaError_t e = allow_smem(done, (const void*)k_dense32<OP, ACT>, kDynamic);
   if (e != cudaSuccess) return e;
   a.d.tiles_m = (a.d.M + kTile - 1) / kTile;
   a.d.tiles_n = (a.d.N + Cfg<OP>::kCols - 1) / Cfg<OP>::kCols;
   const int units = a.d.tiles_m * a.d.tiles_n * a.d.splits;
-  k_dense32<OP><<<units < num_sms ? units : num_sms, kThreads, kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
+  k_dense32<OP, ACT><<<units < num_sms ? units : num_sms, kThreads, kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
   return cudaGetLastError();
 }
 
@@ -349,11 +351,15 @@ int dense32_splits(int M, int N, int kblocks, int num_sms) {
 
 cudaError_t launch_dense32(DenseOp op, const CUtensorMap (&m)[4], Dense32Args a, int num_sms, cudaStream_t st) {
   switch (op) {
-    case DenseOp::kGlu: return run<DenseOp::kGlu>(m, a, num_sms, st);
-    case DenseOp::kOut: return run<DenseOp::kOut>(m, a, num_sms, st);
-    case DenseOp::kDglu: return run<DenseOp::kDglu>(m, a, num_sms, st);
-    case DenseOp::kDx: return run<DenseOp::kDx>(m, a, num_sms, st);
-    case DenseOp::kDw: return run<DenseOp::kDw>(m, a, num_sms, st);
+    case DenseOp::kGlu:
+      return a.d.act == REC_ATTN_SILU ? run<DenseOp::kGlu, REC_ATTN_SILU>(m, a, num_sms, st)
+                                      : run<DenseOp::kGlu, REC_ATTN_GELU>(m, a, num_sms, st);
+    case DenseOp::kDglu:
+      return a.d.act == REC_ATTN_SILU ? run<DenseOp::kDglu, REC_ATTN_SILU>(m, a, num_sms, st)
+                                      : run<DenseOp::kDglu, REC_ATTN_GELU>(m, a, num_sms, st);
+    case DenseOp::kOut: return run<DenseOp::kOut, 0>(m, a, num_sms, st);
+    case DenseOp::kDx: return run<DenseOp::kDx, 0>(m, a, num_sms, st);
+    case DenseOp::kDw: return run<DenseOp::kDw, 0>(m, a, num_sms, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -2,8 +2,8 @@
 //
 // y = (act(x Wg') * (x Wu')) w_out' over packed token rows, and its gradients (dense.cuh lists the
 // five products).  One persistent CTA per SM takes tiles of 128 rows; a TMA warp keeps a ring of
-// 64-deep operand blocks full, one warp issues tcgen05 MMAs into TMEM, eight warps read a finished
-// tile out while the next one is summed.
+// 64-deep operand blocks full, one warp issues tcgen05 MMAs into TMEM, eight or sixteen warps read a
+// finished tile out while the next one is summed.
 //  - kGlu: a tile's 256 columns are 128 gate and the 128 up columns that belong to them, so the
 //    activation and the product happen in the epilogue and neither projection reaches memory.
 //  - kDglu: nothing of the forward is kept; g and u are summed again (256 columns) beside
@@ -29,13 +29,14 @@ __device__ int g_dense_status;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBK = 64;                      // a block along the summed axis: 128 bytes
 constexpr int kSlab = 64 * 128;              // 64 rows of 128 bytes
-constexpr int kThreads = 384, kEpiWarps = 8;
 
 template <DenseOp OP, int BN>
 struct Cfg {
   static constexpr bool kPair = OP == DenseOp::kGlu || OP == DenseOp::kDglu;  // gate and up columns
   static constexpr bool kAMn = OP == DenseOp::kDw, kBMn = OP == DenseOp::kDx || OP == DenseOp::kDw;
   static constexpr int kTileN = kPair ? BN / 2 : BN;  // columns of the result
+  // Warps of the epilogue: 16 where it computes the activation (of kDglu 901 us with 8)
+  static constexpr int kEpiWarps = kPair ? 16 : 8, kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kStage = 2 * kSlab + BN * 128;
   static constexpr int kStages = BN == 256 ? 4 : 6;
   static constexpr int kDynamic = kStages * kStage + 1024;
@@ -184,46 +185,44 @@ out:
 }
 
 // ------------------------------------------------------------------ epilogues
-template <DenseOp OP, int BN>
+template <DenseOp OP, int BN, int ACT>
 __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
   using C = Cfg<OP, BN>;
   const int units = a.tiles_m * a.tiles_n * a.splits;
-  const int quad = warp & 3, half = (warp >> 2) & 1;
-  constexpr int kCols = C::kTileN / 2;  // of the result, a warp's share
+  const int quad = warp & 3, part = (warp - 4) >> 2;
+  constexpr int kCols = C::kTileN * 4 / C::kEpiWarps;  // of the result, a warp's share
+  constexpr int kStep = C::kPair ? 16 : 32;
   uint32_t it = 0;
   for (int i = blockIdx.x; i < units; i += gridDim.x, ++it) {
     const Unit u = unit_at<C::kTileN>(a, i);
     const uint32_t buf = it & 1, round = (it >> 1) & 1;
     if (!bounded_wait_warp(bars + kAccFull + buf, round, abort_flag, a.status, kWaitNs)) return;
     ptx::tc_fence_after();
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
     const long long row = u.m0 + quad * 32 + lane;
 #pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
-      const int col = u.n0 + half * kCols + c, left = a.N - col;
+    for (int c = 0; c < kCols; c += kStep) {
+      const int col = u.n0 + part * kCols + c, left = a.N - col;
       const bool in = row < a.M && left > 0;
       if constexpr (OP == DenseOp::kGlu) {
-        uint32_t g[32], v[32], w[16];
-        ptx::tmem_ld32(lanes + buf * BN + c, g);
-        ptx::tmem_ld32(lanes + buf * BN + BN / 2 + c, v);
+        uint32_t gu[32], w[8];
+        ptx::tmem_ld2x16(lanes + buf * BN + c, lanes + buf * BN + BN / 2 + c, gu);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = pack_bf16(act_value(__uint_as_float(g[2 * e]), a.act) * __uint_as_float(v[2 * e]),
-                        act_value(__uint_as_float(g[2 * e + 1]), a.act) * __uint_as_float(v[2 * e + 1]));
+        for (int e = 0; e < 8; ++e)
+          w[e] = pack_bf16(act_value<ACT>(__uint_as_float(gu[2 * e])) * __uint_as_float(gu[16 + 2 * e]),
+                           act_value<ACT>(__uint_as_float(gu[2 * e + 1])) * __uint_as_float(gu[16 + 2 * e + 1]));
         if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
       } else if constexpr (OP == DenseOp::kDglu) {
-        uint32_t g[32], v[32], d[32], wg[16], wu[16], wh[16];
-        ptx::tmem_ld32(lanes + c, g);
-        ptx::tmem_ld32(lanes + BN / 2 + c, v);
-        ptx::tmem_ld32(lanes + BN + buf * (BN / 2) + c, d);
+        uint32_t gud[48], wg[8], wu[8], wh[8];
+        ptx::tmem_ld3x16(lanes + c, lanes + BN / 2 + c, lanes + BN + buf * (BN / 2) + c, gud);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 8; ++e) {
           float dg[2], du[2], h[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float dh = __uint_as_float(d[2 * e + k]), up = __uint_as_float(v[2 * e + k]);
+            const float dh = __uint_as_float(gud[32 + 2 * e + k]), up = __uint_as_float(gud[16 + 2 * e + k]);
             float slope;
-            const float act = act_both(__uint_as_float(g[2 * e + k]), a.act, slope);
+            const float act = act_both<ACT>(__uint_as_float(gud[2 * e + k]), slope);
             dg[k] = dh * up * slope;
             du[k] = dh * act;
             h[k] = act * up;
@@ -267,8 +266,8 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
   }
 }
 
-template <DenseOp OP, int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+template <DenseOp OP, int BN, int ACT>
+__global__ void __launch_bounds__(Cfg<OP, BN>::kThreads, 1)
     k_dense(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
             const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2, const DenseArgs a) {
   using C = Cfg<OP, BN>;
@@ -286,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + kAccFull + i, 1);
-      ptx::mbar_init(bars + kAccEmpty + i, kEpiWarps);
+      ptx::mbar_init(bars + kAccEmpty + i, C::kEpiWarps);
     }
-    ptx::mbar_init(bars + kGuEmpty, kEpiWarps);
+    ptx::mbar_init(bars + kGuEmpty, C::kEpiWarps);
     ptx::mbar_init(bars + kDone, 1);
     s_abort = 0;
     ptx::fence_barrier_init();
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   if (warp == 0) produce<OP, BN>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, lane);
   else if (warp == 1) issue<OP, BN>(a, sm, bars, tmem, abort_flag);
-  else if (warp >= 4) finish<OP, BN>(a, bars, tmem, abort_flag, warp, lane);
+  else if (warp >= 4) finish<OP, BN, ACT>(a, bars, tmem, abort_flag, warp, lane);
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -326,16 +325,16 @@ __global__ void k_dense_sum(const float* part, void* out, long long n, int split
   else reinterpret_cast<float4*>(out)[i / 4] = s;
 }
 
-template <DenseOp OP, int BN>
+template <DenseOp OP, int BN, int ACT>
 cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
   using C = Cfg<OP, BN>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN>, C::kDynamic);
+  const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN, ACT>, C::kDynamic);
   if (e != cudaSuccess) return e;
   a.tiles_m = (a.M + kTile - 1) / kTile;
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;
-  k_dense<OP, BN><<<(int)(units < num_sms ? units : num_sms), kThreads, C::kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
+  k_dense<OP, BN, ACT><<<(int)(units < num_sms ? units : num_sms), C::kThreads, C::kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
   return cudaGetLastError();
 }
 
@@ -359,11 +358,21 @@ int* dense_status() {
   return static_cast<int*>(p);
 }
 
+// The parts that take the least time: rounds of the SMs times a part's blocks (0.4 us each), and the
+// parts' sums written and read.
 int dense_splits(int M, int N, int kblocks, int num_sms) {
   const long long tiles = (long long)((M + kTile - 1) / kTile) * ((N + 255) / 256);
-  long long s = (2 * num_sms + tiles - 1) / tiles;
-  if (s > kblocks) s = kblocks;
-  return s < 1 ? 1 : (int)s;
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= 64 && s <= kblocks; ++s) {
+    const long long rounds = (tiles * s + num_sms - 1) / num_sms;
+    const double us = rounds * (0.4 * ((kblocks + s - 1) / s) + 1) + (s > 1 ? s * 8e-6 / 5 * M * N + 3 : 0);
+    if (us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_dense_sum(const float* part, void* out, long long n, int splits, int dtype, cudaStream_t st) {
@@ -375,11 +384,15 @@ cudaError_t launch_dense_sum(const float* part, void* out, long long n, int spli
 
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
   switch (op) {
-    case DenseOp::kGlu: return run<DenseOp::kGlu, 256>(m, a, num_sms, st);
-    case DenseOp::kOut: return run<DenseOp::kOut, 256>(m, a, num_sms, st);
-    case DenseOp::kDglu: return run<DenseOp::kDglu, 256>(m, a, num_sms, st);
-    case DenseOp::kDx: return run<DenseOp::kDx, 256>(m, a, num_sms, st);
-    case DenseOp::kDw: return run<DenseOp::kDw, 256>(m, a, num_sms, st);
+    case DenseOp::kGlu:
+      return a.act == REC_ATTN_SILU ? run<DenseOp::kGlu, 256, REC_ATTN_SILU>(m, a, num_sms, st)
+                                    : run<DenseOp::kGlu, 256, REC_ATTN_GELU>(m, a, num_sms, st);
+    case DenseOp::kDglu:
+      return a.act == REC_ATTN_SILU ? run<DenseOp::kDglu, 256, REC_ATTN_SILU>(m, a, num_sms, st)
+                                    : run<DenseOp::kDglu, 256, REC_ATTN_GELU>(m, a, num_sms, st);
+    case DenseOp::kOut: return run<DenseOp::kOut, 256, 0>(m, a, num_sms, st);
+    case DenseOp::kDx: return run<DenseOp::kDx, 256, 0>(m, a, num_sms, st);
+    case DenseOp::kDw: return run<DenseOp::kDw, 256, 0>(m, a, num_sms, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -27,6 +27,8 @@ namespace recattn {
 namespace {
 
 // ------------------------------------------------------------------ quantizer
+constexpr float kFloatMax = 3.402823466e38f;
+
 // The scale for a block whose largest finite value is `top`, and its reciprocal: 448 = 1.75 2^8.
 __device__ __forceinline__ float block_scale(float top, float& inverse) {
   const uint32_t bits = __float_as_uint(top);
@@ -38,14 +40,24 @@ __device__ __forceinline__ float block_scale(float top, float& inverse) {
 }
 __device__ __forceinline__ float finite_size(float v) {
   const float a = fabsf(v);
-  return a <= 3.402823466e38f ? a : 0.f;
+  return a <= kFloatMax ? a : 0.f;
 }
-// Four values in e4m3; one that is not finite becomes NaN.
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  const auto keep = [](float v) { return fabsf(v) <= 3.402823466e38f ? v : __uint_as_float(0x7fffffffu); };
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(keep(a), keep(b)), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(keep(c), keep(d)), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
+// The larger of a size and a value's, NaN if the value is one.
+__device__ __forceinline__ float largest_or_nan(float top, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(v)));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2_e4m3(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// Four values in e4m3; one that is not finite (fine: there is none) becomes NaN.
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d, bool fine) {
+  if (!fine) {
+    const auto keep = [](float v) { return fabsf(v) <= kFloatMax ? v : __uint_as_float(0x7fffffffu); };
+    a = keep(a), b = keep(b), c = keep(c), d = keep(d);
+  }
+  return pack2_e4m3(a, b) | pack2_e4m3(c, d) << 16;
 }
 
 // Eight values of a row.
@@ -74,17 +86,24 @@ struct Eight<float> {
     return (k & 3) == 0 ? h.x : (k & 3) == 1 ? h.y : (k & 3) == 2 ? h.z : h.w;
   }
 };
+// The largest finite size; fine: there are no others.
 template <typename E>
-__device__ __forceinline__ float largest(const Eight<E>& x) {
+__device__ __forceinline__ float largest(const Eight<E>& x, bool& fine) {
   float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = fmaxf(m, finite_size(x.at(k)));
+  for (int k = 0; k < 8; ++k) m = largest_or_nan(m, x.at(k));
+  fine = m <= kFloatMax;
+  if (!fine) {
+    m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, finite_size(x.at(k)));
+  }
   return m;
 }
 template <typename E>
-__device__ __forceinline__ uint2 quantized(const Eight<E>& x, float inv) {
-  return make_uint2(pack_e4m3(x.at(0) * inv, x.at(1) * inv, x.at(2) * inv, x.at(3) * inv),
-                    pack_e4m3(x.at(4) * inv, x.at(5) * inv, x.at(6) * inv, x.at(7) * inv));
+__device__ __forceinline__ uint2 quantized(const Eight<E>& x, float inv, bool fine) {
+  return make_uint2(pack_e4m3(x.at(0) * inv, x.at(1) * inv, x.at(2) * inv, x.at(3) * inv, fine),
+                    pack_e4m3(x.at(4) * inv, x.at(5) * inv, x.at(6) * inv, x.at(7) * inv, fine));
 }
 
 constexpr int kQuantThreads = 256, kQuantRun = 4;
@@ -100,7 +119,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize_rows(QuantArgs a) {
     long long at[kQuantRun];
 #pragma unroll
     for (int j = 0; j < kQuantRun; ++j) {
-      const long long u = u0 + j * groups, row = u / a.blocks;
+      const long long u = u0 + j * groups;
+      const long long row = units >> 32 ? u / a.blocks : (long long)((uint32_t)u / (uint32_t)a.blocks);
       const int c = (int)(u - row * a.blocks) * 16 + lane;
       const bool in = u < units && c < chunks;
       at[j] = in ? row * chunks + c : -1;
@@ -109,13 +129,14 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize_rows(QuantArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < kQuantRun; ++j) {
-      float top = largest(x[j]);
+      bool fine;
+      float top = largest(x[j], fine);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       float inv;
       const float scale = block_scale(top, inv);
       if (at[j] >= 0) {
-        reinterpret_cast<uint2*>(a.q)[at[j]] = quantized(x[j], inv);
+        reinterpret_cast<uint2*>(a.q)[at[j]] = quantized(x[j], inv, fine);
         if (lane == 0) a.scale[u0 + j * groups] = scale;
       }
     }
@@ -130,13 +151,18 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize_blocks(QuantArgs a) 
   const long long row0 = (long long)(blockIdx.x / a.blocks) * kScaleBlock + (threadIdx.x >> 4);
   Eight<E> x[8];
   float top = 0.f;
+  bool all_fine = true;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (row0 + 16 * j < a.rows && c < chunks) x[j].load(a.x, (row0 + 16 * j) * chunks + c);
     else x[j].zero();
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, largest(x[j]));
+  for (int j = 0; j < 8; ++j) {
+    bool fine;
+    top = fmaxf(top, largest(x[j], fine));
+    all_fine = all_fine && fine;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
@@ -149,7 +175,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize_blocks(QuantArgs a) 
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (row0 + 16 * j < a.rows && c < chunks)
-      reinterpret_cast<uint2*>(a.q)[(row0 + 16 * j) * chunks + c] = quantized(x[j], inv);
+      reinterpret_cast<uint2*>(a.q)[(row0 + 16 * j) * chunks + c] = quantized(x[j], inv, all_fine);
 }
 
 // ------------------------------------------------------------------ product
@@ -157,7 +183,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBN = 256;                     // columns of B a tile
 constexpr int kSlab = 128 * 128;             // 128 rows of a block: 128 bytes each
 constexpr int kStage = 3 * kSlab, kStages = 4;
-constexpr int kThreads = 320, kEpiWarps = 8;  // 320: up to 200 registers a thread
+constexpr int kEpiWarps = 16, kThreads = 64 + 32 * kEpiWarps;
 constexpr int kDynamic = kStages * kStage + 1024;
 constexpr uint32_t kTmem = 512;               // two buffers of a block's sums
 
@@ -225,28 +251,28 @@ out:
   __syncwarp();
 }
 
-// Eight warps: a thread has one row and half of the tile's columns (gated: 64 gate columns and the 64 up
-// columns that belong to them).
-template <bool GATED>
+// Sixteen warps: a thread has one row and a quarter of the tile's columns (gated: 32 gate columns and
+// the 32 up columns that belong to them).
+template <bool GATED, int ACT>
 __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, float* s_top,
                        int warp, int lane) {
   const int tiles = a.tiles_m * a.tiles_n;
-  const int quad = warp & 3, half = (warp - 2) >> 2;
-  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  const int quad = warp & 3, part = (warp - 2) >> 2;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
   uint32_t n = 0, it = 0;
   for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
     const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
     const long long row = (long long)at.x * kTile + quad * 32 + lane;
     const bool in = row < a.M;
     const float* sa = a.a_scale + (in ? row : 0) * a.kblocks;
-    // the scales of this thread's first and second 64 columns' block
-    const int nb = GATED ? at.y : 2 * at.y + half;
+    // the scales of this thread's first and second 32 columns' block
+    const int nb = GATED ? at.y : 2 * at.y + (part >> 1);
     const bool nb_in = GATED || (long long)nb * 128 < a.N;
     const float* sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
     const float* sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
-    float acc[128];
+    float acc[64];
 #pragma unroll
-    for (int e = 0; e < 128; ++e) acc[e] = 0.f;
+    for (int e = 0; e < 64; ++e) acc[e] = 0.f;
     for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
       const float sk = in ? __ldg(sa + kb) : 0.f;
       const float f0 = sk * __ldg(sb0 + kb), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
@@ -255,12 +281,11 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       ptx::tc_fence_after();
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        const int col = GATED ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
-        ptx::tmem_ld32(lanes + buf * kBN + col, r);
+        uint32_t r[16];
+        ptx::tmem_ld16(lanes + buf * kBN + (GATED ? (c >> 1) * 128 + (c & 1) * 16 : c * 16), r);
         const float f = GATED && c >= 2 ? f1 : f0;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[32 * c + e] = fmaf(__uint_as_float(r[e]), f, acc[32 * c + e]);
+        for (int e = 0; e < 16; ++e) acc[16 * c + e] = fmaf(__uint_as_float(r[e]), f, acc[16 * c + e]);
       }
       ptx::tc_fence_before();
       __syncwarp();
@@ -269,53 +294,56 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
     if constexpr (GATED) {
       float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 64; ++e) {
-        acc[e] = act_value(acc[e], a.act) * acc[64 + e];
-        top = fmaxf(top, finite_size(acc[e]));
+      for (int e = 0; e < 32; ++e) {
+        acc[e] = act_value<ACT>(acc[e]) * acc[32 + e];
+        top = largest_or_nan(top, acc[e]);
       }
-      // the other half's largest value; the tiles take two places in turn
-      float* s = s_top + (it & 1) * 256;
-      s[half * 128 + quad * 32 + lane] = top;
+      const bool fine = top <= kFloatMax;
+      if (!fine) {
+        top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = fmaxf(top, finite_size(acc[e]));
+      }
+      // the other parts' largest values; the tiles take two places in turn
+      float* s = s_top + (it & 1) * 512 + quad * 32 + lane;
+      s[part * 128] = top;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bars + kPairs);
       if (!bounded_wait_warp(bars + kPairs, it & 1, abort_flag, a.status, kWaitNs)) return;
-      top = fmaxf(top, s[(half ^ 1) * 128 + quad * 32 + lane]);
+      top = fmaxf(fmaxf(s[0], s[128]), fmaxf(s[256], s[384]));
       float inv;
       const float scale = block_scale(top, inv);
       if (in) {
-        uint32_t w[16];
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = pack_e4m3(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
-        uint8_t* dst = static_cast<uint8_t*>(a.out) + row * a.N + at.y * 128 + half * 64;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          ptx::st_global_v8(dst + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3], w[8 * c + 4], w[8 * c + 5],
-                            w[8 * c + 6], w[8 * c + 7]);
-        if (half == 0) a.out_scale[row * (a.N / 128) + at.y] = scale;
+        for (int e = 0; e < 8; ++e)
+          w[e] = pack_e4m3(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv, fine);
+        ptx::st_global_v8(static_cast<uint8_t*>(a.out) + row * a.N + at.y * 128 + part * 32, w[0], w[1], w[2], w[3], w[4],
+                          w[5], w[6], w[7]);
+        if (part == 0) a.out_scale[row * (a.N / 128) + at.y] = scale;
       }
     } else {
-      const int col0 = at.y * kBN + half * 128;
+      const int col0 = at.y * kBN + part * 64;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int col = col0 + 32 * c;
-        uint32_t w[16];
+        const int col = col0 + 16 * c;
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack_bf16(acc[32 * c + 2 * e], acc[32 * c + 2 * e + 1]);
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(acc[16 * c + 2 * e], acc[16 * c + 2 * e + 1]);
         if (in && col < a.N) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, a.N - col, a.wide);
       }
     }
   }
 }
 
-template <bool GATED>
+template <bool GATED, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_scaled(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const ScaledArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ int s_abort;
   __shared__ uint32_t tmem_slot;
-  __shared__ float s_top[GATED ? 512 : 1];
+  __shared__ float s_top[GATED ? 1024 : 1];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -343,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, lane);
   else if (warp == 1) issue(a, sm, bars, tmem, abort_flag);
-  else finish<GATED>(a, bars, tmem, abort_flag, s_top, warp, lane);
+  else finish<GATED, ACT>(a, bars, tmem, abort_flag, s_top, warp, lane);
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -352,16 +380,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool GATED>
+template <bool GATED, int ACT>
 cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED>, kDynamic);
+  const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED, ACT>, kDynamic);
   if (e != cudaSuccess) return e;
   const int tn = GATED ? kBN / 2 : kBN;
   a.tiles_m = (a.M + kTile - 1) / kTile;
   a.tiles_n = (a.N + tn - 1) / tn;
   const int tiles = a.tiles_m * a.tiles_n;
-  k_scaled<GATED><<<tiles < num_sms ? tiles : num_sms, kThreads, kDynamic, st>>>(ma, mb, a);
+  k_scaled<GATED, ACT><<<tiles < num_sms ? tiles : num_sms, kThreads, kDynamic, st>>>(ma, mb, a);
   return cudaGetLastError();
 }
 
@@ -385,7 +413,9 @@ cudaError_t launch_quantize(const QuantArgs& a, int dtype, int block_rows, int n
 
 cudaError_t launch_scaled(bool gated, const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int num_sms,
                           cudaStream_t st) {
-  return gated ? run<true>(ma, mb, a, num_sms, st) : run<false>(ma, mb, a, num_sms, st);
+  if (!gated) return run<false, 0>(ma, mb, a, num_sms, st);
+  return a.act == REC_ATTN_SILU ? run<true, REC_ATTN_SILU>(ma, mb, a, num_sms, st)
+                                : run<true, REC_ATTN_GELU>(ma, mb, a, num_sms, st);
 }
 
 }  // namespace recattn
