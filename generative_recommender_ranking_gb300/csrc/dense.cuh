@@ -29,8 +29,8 @@ struct DenseArgs {
   int* status;
 };
 
-// A row-major [rows][cols] bf16 operand as a TMA map; mn_major: the summed axis runs over its rows.
-bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major);
+// A row-major [rows][cols] bf16 operand as a TMA map; box = 64 columns x 64 rows.
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols);
 int* dense_status();
 
 // fp32 operands (dense_fp32.cu): a matrix as three bf16 planes whose sum it is, rows `ld` apart.

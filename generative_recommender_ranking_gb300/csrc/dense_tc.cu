@@ -30,15 +30,17 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBK = 64;                      // a block along the summed axis: 128 bytes
 constexpr int kSlab = 64 * 128;              // 64 rows of 128 bytes
 
-template <DenseOp OP, int BN>
+template <DenseOp OP, int BN, int CG>
 struct Cfg {
   static constexpr bool kPair = OP == DenseOp::kGlu || OP == DenseOp::kDglu;  // gate and up columns
   static constexpr bool kAMn = OP == DenseOp::kDw, kBMn = OP == DenseOp::kDx || OP == DenseOp::kDw;
   static constexpr int kTileN = kPair ? BN / 2 : BN;  // columns of the result
   // Warps of the epilogue: 16 where it computes the activation (of kDglu 901 us with 8)
   static constexpr int kEpiWarps = kPair ? 16 : 8, kThreads = 128 + 32 * kEpiWarps;
-  static constexpr int kStage = 2 * kSlab + BN * 128;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kTileM = kTile * CG;
+  static constexpr int kBRows = BN / CG;               // of B in this CTA
+  static constexpr int kStage = 2 * kSlab + kBRows * 128;
+  static constexpr int kStages = 6 * 32 * 1024 / kStage;
   static constexpr int kDynamic = kStages * kStage + 1024;
   static constexpr uint32_t kTmem = 2 * BN;  // kDglu: g, u and two buffers of dh
 };
@@ -50,14 +52,15 @@ struct Unit {
   int m0, n0, kb0, kb1, split;
 };
 
-template <int TN>
-__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i) {
+// Work of pair (CTA) i; m0: this CTA's first row.
+template <int TN, int CG>
+__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i, uint32_t rank) {
   const int tiles = a.tiles_m * a.tiles_n;
   Unit u;
   u.split = i / tiles;
   const int t = i - u.split * tiles;
   const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
-  u.m0 = at.x * kTile;
+  u.m0 = (at.x * CG + (int)rank) * kTile;
   u.n0 = at.y * TN;
   u.kb0 = (int)((long long)a.kblocks * u.split / a.splits);
   u.kb1 = (int)((long long)a.kblocks * (u.split + 1) / a.splits);
@@ -65,44 +68,45 @@ __device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i) {
 }
 
 // ------------------------------------------------------------------ loads
-// `rows` (a multiple of 128) rows of one operand at mn0, block kb of the summed axis.
-template <bool MN>
-__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn0, int rows, int kb,
-                                             uint64_t* bar) {
-  if (MN) {
-    for (int i = 0; i < rows / 64; ++i) ptx::tma_load_2d(dst + i * kSlab, map, mn0 + 64 * i, kb * kBK, bar);
-  } else {
-    for (int i = 0; i < rows / kTile; ++i) ptx::tma_load_2d(dst + i * 2 * kSlab, map, kb * kBK, mn0 + kTile * i, bar);
+// `rows` (a multiple of 64) rows of one operand at mn0, block kb of the summed axis.
+template <bool MN, int CG>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn0, int rows, int kb, uint32_t bar) {
+  for (int i = 0; i < rows / 64; ++i) {
+    if (MN) ptx::tma_load_2d_pair<CG>(dst + i * kSlab, map, mn0 + 64 * i, kb * kBK, bar);
+    else ptx::tma_load_2d_pair<CG>(dst + i * kSlab, map, kb * kBK, mn0 + 64 * i, bar);
   }
 }
 
-template <DenseOp OP, int BN>
+template <DenseOp OP, int BN, int CG>
 __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* ma2,
-                        const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, int lane) {
-  using C = Cfg<OP, BN>;
+                        const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, uint32_t rank, int lane) {
+  using C = Cfg<OP, BN, CG>;
   const int units = a.tiles_m * a.tiles_n * a.splits;
   uint32_t n = 0;
-  for (int i = blockIdx.x; i < units; i += gridDim.x) {
-    const Unit u = unit_at<C::kTileN>(a, i);
+  for (int i = blockIdx.x / CG; i < units; i += gridDim.x / CG) {
+    const Unit u = unit_at<C::kTileN, CG>(a, i, rank);
     const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
     for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
       const int st = n % C::kStages;
       if (!bounded_wait_warp(bars + kEmpty + st, ((n / C::kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (ptx::elect_one()) {
         uint8_t* s = sm + st * C::kStage;
-        uint64_t* bar = bars + kFull + st;
-        if (OP == DenseOp::kDglu && kb < 0) {
-          ptx::mbar_arrive_expect_tx(bar, 4 * kSlab);
-          load_operand<false>(s, ma2, u.m0, kTile, kb + first, bar);
-          load_operand<true>(s + 2 * kSlab, mb2, u.n0, kTile, kb + first, bar);
+        const uint32_t bar = ptx::first_of_pair<CG>(bars + kFull + st);
+        const bool grad = OP == DenseOp::kDglu && kb < 0;
+        // (the first CTA's barrier counts the bytes of both)
+        if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, CG * (grad ? 2 * kSlab + C::kBRows * 64 : C::kStage));
+        if (grad) {
+          load_operand<false, CG>(s, ma2, u.m0, kTile, kb + first, bar);
+          load_operand<true, CG>(s + 2 * kSlab, mb2, u.n0 + (int)rank * (C::kBRows / 2), C::kBRows / 2, kb + first, bar);
         } else {
-          ptx::mbar_arrive_expect_tx(bar, C::kStage);
-          load_operand<C::kAMn>(s, ma, u.m0, kTile, kb, bar);
-          if (C::kPair) {
-            load_operand<false>(s + 2 * kSlab, mb, u.n0, BN / 2, kb, bar);
-            load_operand<false>(s + 2 * kSlab + BN * 64, mb, a.N + u.n0, BN / 2, kb, bar);
+          load_operand<C::kAMn, CG>(s, ma, u.m0, kTile, kb, bar);
+          if (C::kPair && CG == 2) {  // the gate's columns are the first CTA's rows of B, up's the second's
+            load_operand<false, CG>(s + 2 * kSlab, mb, (rank ? a.N : 0) + u.n0, C::kBRows, kb, bar);
+          } else if (C::kPair) {
+            load_operand<false, CG>(s + 2 * kSlab, mb, u.n0, BN / 2, kb, bar);
+            load_operand<false, CG>(s + 2 * kSlab + BN * 64, mb, a.N + u.n0, BN / 2, kb, bar);
           } else {
-            load_operand<C::kBMn>(s + 2 * kSlab, mb, u.n0, BN, kb, bar);
+            load_operand<C::kBMn, CG>(s + 2 * kSlab, mb, u.n0 + (int)rank * C::kBRows, C::kBRows, kb, bar);
           }
         }
       }
@@ -110,8 +114,8 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
     }
   }
 out:
-  // after an abort, copies may still be in flight
-  if (lane == 0)
+  // after an abort, copies may still be in flight (those of a pair count on the first CTA's barriers)
+  if (lane == 0 && rank == 0)
     for (uint32_t j = n > C::kStages ? n - C::kStages : 0; j < n; ++j)
       bounded_drain(bars + kFull + j % C::kStages, (j / C::kStages) & 1, kWaitNs / 4);
   __syncwarp();
@@ -128,23 +132,24 @@ __device__ __forceinline__ uint64_t step(uint64_t desc, int k) {
   return ptx::smem_desc_at(desc, k * (MN ? 16 * 128 : 32));
 }
 
-template <bool AMN, bool BMN, int N>
+template <bool AMN, bool BMN, int N, int CG>
 __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s, bool fresh) {
-  const uint32_t idesc = ptx::idesc_bf16_f32(kTile, N, AMN, BMN);
+  const uint32_t idesc = ptx::idesc_bf16_f32(kTile * CG, N, AMN, BMN);
   const uint64_t da = operand<AMN>(s), db = operand<BMN>(s + 2 * kSlab);
 #pragma unroll
-  for (int k = 0; k < kBK / 16; ++k) ptx::umma_f16(acc, step<AMN>(da, k), step<BMN>(db, k), idesc, !fresh || k > 0);
+  for (int k = 0; k < kBK / 16; ++k) ptx::umma_pair<CG, false>(acc, step<AMN>(da, k), step<BMN>(db, k), idesc, !fresh || k > 0);
 }
 
-template <DenseOp OP, int BN>
+template <DenseOp OP, int BN, int CG>
 __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
-  using C = Cfg<OP, BN>;
+  using C = Cfg<OP, BN, CG>;
   const int units = a.tiles_m * a.tiles_n * a.splits;
   const uint32_t s0 = ptx::smem_u32(sm);
   const bool el = ptx::elect_one();
+  constexpr uint32_t rank = 0;  // the first CTA issues for both
   uint32_t n = 0, it = 0;
-  for (int i = blockIdx.x; i < units; i += gridDim.x, ++it) {
-    const Unit u = unit_at<C::kTileN>(a, i);
+  for (int i = blockIdx.x / CG; i < units; i += gridDim.x / CG, ++it) {
+    const Unit u = unit_at<C::kTileN, CG>(a, i, rank);
     const uint32_t buf = it & 1, round = (it >> 1) & 1;
     if (!bounded_wait_warp(bars + kAccEmpty + buf, round ^ 1, abort_flag, a.status, kWaitNs)) goto out;
     ptx::tc_fence_after();
@@ -154,8 +159,8 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
         if (!bounded_wait_warp(bars + kFull + st, (n / C::kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
         ptx::tc_fence_after();
         if (el) {
-          block_mma<false, true, BN / 2>(tmem + BN + buf * (BN / 2), s0 + st * C::kStage, kb == 0);
-          ptx::umma_commit(bars + kEmpty + st);
+          block_mma<false, true, BN / 2, CG>(tmem + BN + buf * (BN / 2), s0 + st * C::kStage, kb == 0);
+          ptx::umma_commit_pair<CG>(bars + kEmpty + st);
         }
         __syncwarp();
       }
@@ -168,38 +173,49 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
       if (!bounded_wait_warp(bars + kFull + st, (n / C::kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
       ptx::tc_fence_after();
       if (el) {
-        block_mma<C::kAMn, C::kBMn, BN>(acc, s0 + st * C::kStage, kb == u.kb0);
-        ptx::umma_commit(bars + kEmpty + st);
+        block_mma<C::kAMn, C::kBMn, BN, CG>(acc, s0 + st * C::kStage, kb == u.kb0);
+        ptx::umma_commit_pair<CG>(bars + kEmpty + st);
       }
       __syncwarp();
     }
-    if (el) ptx::umma_commit(bars + kAccFull + buf);
+    if (el) ptx::umma_commit_pair<CG>(bars + kAccFull + buf);
     __syncwarp();
   }
 out:
   if (el) {
-    ptx::umma_commit(bars + kDone);
+    ptx::umma_commit_pair<CG>(bars + kDone);
     bounded_drain(bars + kDone, 0, kWaitNs / 4);
   }
   __syncwarp();
 }
 
 // ------------------------------------------------------------------ epilogues
-template <DenseOp OP, int BN, int ACT>
-__device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
-  using C = Cfg<OP, BN>;
+template <DenseOp OP, int BN, int CG, int ACT>
+__device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, uint32_t rank, int warp,
+                       int lane) {
+  using C = Cfg<OP, BN, CG>;
   const int units = a.tiles_m * a.tiles_n * a.splits;
   const int quad = warp & 3, part = (warp - 4) >> 2;
   constexpr int kCols = C::kTileN * 4 / C::kEpiWarps;  // of the result, a warp's share
   constexpr int kStep = C::kPair ? 16 : 32;
+  const uint32_t empty = ptx::first_of_pair<CG>(bars + kAccEmpty), gu_empty = ptx::first_of_pair<CG>(bars + kGuEmpty);
   uint32_t it = 0;
-  for (int i = blockIdx.x; i < units; i += gridDim.x, ++it) {
-    const Unit u = unit_at<C::kTileN>(a, i);
+  for (int i = blockIdx.x / CG; i < units; i += gridDim.x / CG, ++it) {
+    const Unit u = unit_at<C::kTileN, CG>(a, i, rank);
     const uint32_t buf = it & 1, round = (it >> 1) & 1;
     if (!bounded_wait_warp(bars + kAccFull + buf, round, abort_flag, a.status, kWaitNs)) return;
     ptx::tc_fence_after();
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
     const long long row = u.m0 + quad * 32 + lane;
+    const auto taken = [&](int c) {  // behind the loads of columns c: the last ones give the buffer back
+      if (c + kStep < kCols) return;
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive_pair<CG>(empty + 8 * buf);
+        if (OP == DenseOp::kDglu) ptx::mbar_arrive_pair<CG>(gu_empty);
+      }
+    };
 #pragma unroll 1
     for (int c = 0; c < kCols; c += kStep) {
       const int col = u.n0 + part * kCols + c, left = a.N - col;
@@ -207,6 +223,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
       if constexpr (OP == DenseOp::kGlu) {
         uint32_t gu[32], w[8];
         ptx::tmem_ld2x16(lanes + buf * BN + c, lanes + buf * BN + BN / 2 + c, gu);
+        taken(c);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           w[e] = pack_bf16(act_value<ACT>(__uint_as_float(gu[2 * e])) * __uint_as_float(gu[16 + 2 * e]),
@@ -215,6 +232,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
       } else if constexpr (OP == DenseOp::kDglu) {
         uint32_t gud[48], wg[8], wu[8], wh[8];
         ptx::tmem_ld3x16(lanes + c, lanes + BN / 2 + c, lanes + BN + buf * (BN / 2) + c, gud);
+        taken(c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float dg[2], du[2], h[2];
@@ -240,6 +258,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
       } else {
         uint32_t r[32];
         ptx::tmem_ld32(lanes + buf * BN + c, r);
+        taken(c);
         if (OP == DenseOp::kDw && a.splits > 1) {
           if (in) {
             float4* dst = reinterpret_cast<float4*>(a.part + ((long long)u.split * a.M + row) * a.N + col);
@@ -257,20 +276,14 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         }
       }
     }
-    ptx::tc_fence_before();
-    __syncwarp();
-    if (lane == 0) {
-      ptx::mbar_arrive(bars + kAccEmpty + buf);
-      if (OP == DenseOp::kDglu) ptx::mbar_arrive(bars + kGuEmpty);
-    }
   }
 }
 
-template <DenseOp OP, int BN, int ACT>
-__global__ void __launch_bounds__(Cfg<OP, BN>::kThreads, 1)
+template <DenseOp OP, int BN, int CG, int ACT>
+__global__ void __launch_bounds__(Cfg<OP, BN, CG>::kThreads, 1)
     k_dense(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
             const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2, const DenseArgs a) {
-  using C = Cfg<OP, BN>;
+  using C = Cfg<OP, BN, CG>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ int s_abort;
@@ -285,29 +298,33 @@ __global__ void __launch_bounds__(Cfg<OP, BN>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + kAccFull + i, 1);
-      ptx::mbar_init(bars + kAccEmpty + i, C::kEpiWarps);
+      ptx::mbar_init(bars + kAccEmpty + i, CG * C::kEpiWarps);
     }
-    ptx::mbar_init(bars + kGuEmpty, C::kEpiWarps);
+    ptx::mbar_init(bars + kGuEmpty, CG * C::kEpiWarps);
     ptx::mbar_init(bars + kDone, 1);
     s_abort = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 1) {
-    ptx::tmem_alloc(&tmem_slot, C::kTmem);
-    ptx::tmem_relinquish();
-  }
+  if (warp == 1) ptx::tmem_alloc_pair<CG>(&tmem_slot, C::kTmem);
   ptx::tc_fence_before();
   __syncthreads();
+  if (CG == 2) ptx::pair_sync<CG>();  // both CTAs' barriers are there
   ptx::tc_fence_after();
+  const uint32_t rank = ptx::pair_rank<CG>();
   const uint32_t tmem = tmem_slot;
-  if (warp == 0) produce<OP, BN>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, lane);
-  else if (warp == 1) issue<OP, BN>(a, sm, bars, tmem, abort_flag);
-  else if (warp >= 4) finish<OP, BN, ACT>(a, bars, tmem, abort_flag, warp, lane);
+  if (warp == 0) produce<OP, BN, CG>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
+  else if (warp == 1 && rank == 0) issue<OP, BN, CG>(a, sm, bars, tmem, abort_flag);
+  else if (warp >= 4) finish<OP, BN, CG, ACT>(a, bars, tmem, abort_flag, rank, warp, lane);
   ptx::tc_fence_before();
   __syncthreads();
+  if (CG == 2) {  // nothing of one CTA's reaches into the other any more, the last commit too
+    if (warp == 1 && rank == 1 && lane == 0) bounded_drain(bars + kDone, 0, kWaitNs / 4);
+    __syncwarp();
+    ptx::pair_sync<CG>();
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, C::kTmem);
+    ptx::tmem_dealloc_pair<CG>(tmem, C::kTmem);
   }
 }
 
@@ -325,23 +342,24 @@ __global__ void k_dense_sum(const float* part, void* out, long long n, int split
   else reinterpret_cast<float4*>(out)[i / 4] = s;
 }
 
-template <DenseOp OP, int BN, int ACT>
+template <DenseOp OP, int BN, int CG, int ACT>
 cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
-  using C = Cfg<OP, BN>;
+  using C = Cfg<OP, BN, CG>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN, ACT>, C::kDynamic);
+  const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN, CG, ACT>, C::kDynamic);
   if (e != cudaSuccess) return e;
-  a.tiles_m = (a.M + kTile - 1) / kTile;
+  a.tiles_m = (a.M + C::kTileM - 1) / C::kTileM;
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;
-  k_dense<OP, BN, ACT><<<(int)(units < num_sms ? units : num_sms), C::kThreads, C::kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
-  return cudaGetLastError();
+  const int places = num_sms / CG;
+  return launch_pairs(CG, k_dense<OP, BN, CG, ACT>, (int)(units < places ? units : places) * CG, C::kThreads, C::kDynamic,
+                      st, m[0], m[1], m[2], m[3], a);
 }
 
 }  // namespace
 
-bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major) {
-  return encode_map(m, base, rows, cols, mn_major ? 64 : kTile);
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols) {
+  return encode_map(m, base, rows, cols, 64);
 }
 
 // Asked once per device (the first call may be captured: the question belongs to no stream).
@@ -358,14 +376,14 @@ int* dense_status() {
   return static_cast<int*>(p);
 }
 
-// The parts that take the least time: rounds of the SMs times a part's blocks (0.4 us each), and the
+// The parts that take the least time: rounds of the pairs of SMs times a part's blocks (0.4 us each), and the
 // parts' sums written and read.
 int dense_splits(int M, int N, int kblocks, int num_sms) {
-  const long long tiles = (long long)((M + kTile - 1) / kTile) * ((N + 255) / 256);
+  const long long tiles = (long long)((M + 255) / 256) * ((N + 255) / 256), places = num_sms / 2;
   int best = 1;
   double least = 1e300;
   for (int s = 1; s <= 64 && s <= kblocks; ++s) {
-    const long long rounds = (tiles * s + num_sms - 1) / num_sms;
+    const long long rounds = (tiles * s + places - 1) / places;
     const double us = rounds * (0.4 * ((kblocks + s - 1) / s) + 1) + (s > 1 ? s * 8e-6 / 5 * M * N + 3 : 0);
     if (us < least) {
       least = us;
@@ -385,14 +403,14 @@ cudaError_t launch_dense_sum(const float* part, void* out, long long n, int spli
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
   switch (op) {
     case DenseOp::kGlu:
-      return a.act == REC_ATTN_SILU ? run<DenseOp::kGlu, 256, REC_ATTN_SILU>(m, a, num_sms, st)
-                                    : run<DenseOp::kGlu, 256, REC_ATTN_GELU>(m, a, num_sms, st);
+      return a.act == REC_ATTN_SILU ? run<DenseOp::kGlu, 256, 2, REC_ATTN_SILU>(m, a, num_sms, st)
+                                    : run<DenseOp::kGlu, 256, 2, REC_ATTN_GELU>(m, a, num_sms, st);
     case DenseOp::kDglu:
-      return a.act == REC_ATTN_SILU ? run<DenseOp::kDglu, 256, REC_ATTN_SILU>(m, a, num_sms, st)
-                                    : run<DenseOp::kDglu, 256, REC_ATTN_GELU>(m, a, num_sms, st);
-    case DenseOp::kOut: return run<DenseOp::kOut, 256, 0>(m, a, num_sms, st);
-    case DenseOp::kDx: return run<DenseOp::kDx, 256, 0>(m, a, num_sms, st);
-    case DenseOp::kDw: return run<DenseOp::kDw, 256, 0>(m, a, num_sms, st);
+      return a.act == REC_ATTN_SILU ? run<DenseOp::kDglu, 256, 2, REC_ATTN_SILU>(m, a, num_sms, st)
+                                    : run<DenseOp::kDglu, 256, 2, REC_ATTN_GELU>(m, a, num_sms, st);
+    case DenseOp::kOut: return run<DenseOp::kOut, 256, 2, 0>(m, a, num_sms, st);
+    case DenseOp::kDx: return run<DenseOp::kDx, 256, 2, 0>(m, a, num_sms, st);
+    case DenseOp::kDw: return run<DenseOp::kDw, 256, 2, 0>(m, a, num_sms, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -203,14 +203,14 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
   a.out = ws.p;
   a.wide = wide_rows(ws.p, hidden);
   e = dense(DenseOp::kGlu, a, sms, st,
-            encode_dense(&m[0], x, rows, width, false) && encode_dense(&m[1], w_in, 2 * hidden, width, false), m);
+            encode_dense(&m[0], x, rows, width) && encode_dense(&m[1], w_in, 2 * hidden, width), m);
   a.N = (int)width;
   a.kblocks = blocks64(hidden);
   a.out = y;
   a.wide = wide_rows(y, width);
   if (e == cudaSuccess)
     e = dense(DenseOp::kOut, a, sms, st,
-              encode_dense(&m[0], ws.p, rows, hidden, false) && encode_dense(&m[1], w_out, width, hidden, false), m);
+              encode_dense(&m[0], ws.p, rows, hidden) && encode_dense(&m[1], w_out, width, hidden), m);
   const cudaError_t ef = ws.give_back();
   return from_cuda(e != cudaSuccess ? e : ef);
 }
@@ -262,8 +262,8 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
   a.out2 = h;
   a.wide = wide_rows(p, hidden);
   e = dense(DenseOp::kDglu, a, sms, st,
-            encode_dense(&m[0], x, rows, width, false) && encode_dense(&m[1], w_in, 2 * hidden, width, false) &&
-                encode_dense(&m[2], dy, rows, width, false) && encode_dense(&m[3], w_out, width, hidden, true),
+            encode_dense(&m[0], x, rows, width) && encode_dense(&m[1], w_in, 2 * hidden, width) &&
+                encode_dense(&m[2], dy, rows, width) && encode_dense(&m[3], w_out, width, hidden),
             m);
   if (e == cudaSuccess && dx) {
     a.N = W;
@@ -271,7 +271,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     a.out = dx;
     a.wide = wide_rows(dx, width);
     e = dense(DenseOp::kDx, a, sms, st,
-              encode_dense(&m[0], p, rows, 2 * hidden, false) && encode_dense(&m[1], w_in, 2 * hidden, width, true), m);
+              encode_dense(&m[0], p, rows, 2 * hidden) && encode_dense(&m[1], w_in, 2 * hidden, width), m);
   }
   a.kblocks = kr;
   for (int i = 0; i < 2; ++i) {
@@ -283,8 +283,8 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     a.out = dw;
     a.wide = wide_rows(dw, a.N);
     e = dense(DenseOp::kDw, a, sms, st,
-              (i ? encode_dense(&m[0], dy, rows, width, true) && encode_dense(&m[1], h, rows, hidden, true)
-                 : encode_dense(&m[0], p, rows, 2 * hidden, true) && encode_dense(&m[1], x, rows, width, true)),
+              (i ? encode_dense(&m[0], dy, rows, width) && encode_dense(&m[1], h, rows, hidden)
+                 : encode_dense(&m[0], p, rows, 2 * hidden) && encode_dense(&m[1], x, rows, width)),
               m);
     if (e == cudaSuccess && a.splits > 1) e = launch_dense_sum(a.part, dw, (long long)a.M * a.N, a.splits, dtype, st);
   }

@@ -34,6 +34,23 @@ inline cudaError_t allow_smem(std::atomic<unsigned long long>& done, const void*
   return e;
 }
 
+// Launches blocks in clusters of `cluster` (1: none).
+template <typename... P, typename... A>
+cudaError_t launch_pairs(int cluster, void (*fn)(P...), int blocks, int threads, int smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
 // prologue_ok (may be null) is recorded on st once the RoPE prologue, on another stream,
 // may start: before the planner when it is one kernel, after its first kernel when a
 // long request's tiles are split over several blocks (so the second kernel's blocks,
