@@ -207,40 +207,30 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
     ptx::tc_fence_after();
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
     const long long row = u.m0 + quad * 32 + lane;
-    const auto taken = [&](int c) {  // behind the loads of columns c: the last ones give the buffer back
-      if (c + kStep < kCols) return;
+    const auto give_back = [&](uint32_t bar) {
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive_pair<CG>(empty + 8 * buf);
-        if (OP == DenseOp::kDglu) ptx::mbar_arrive_pair<CG>(gu_empty);
-      }
+      if (lane == 0) ptx::mbar_arrive_pair<CG>(bar);
     };
-#pragma unroll 1
-    for (int c = 0; c < kCols; c += kStep) {
-      const int col = u.n0 + part * kCols + c, left = a.N - col;
-      const bool in = row < a.M && left > 0;
-      if constexpr (OP == DenseOp::kGlu) {
-        uint32_t gu[32], w[8];
-        ptx::tmem_ld2x16(lanes + buf * BN + c, lanes + buf * BN + BN / 2 + c, gu);
-        taken(c);
+    if constexpr (OP == DenseOp::kDglu) {
+      // g and u of all of the warp's columns leave their only buffer at once, so that the next tile's can be
+      // summed into it; dh, which has two, is read 16 columns at a time.
+      uint32_t gu[64];
+      ptx::tmem_ld2x32(lanes, lanes + BN / 2, gu);
+      give_back(gu_empty);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e] = pack_bf16(act_value<ACT>(__uint_as_float(gu[2 * e])) * __uint_as_float(gu[16 + 2 * e]),
-                           act_value<ACT>(__uint_as_float(gu[2 * e + 1])) * __uint_as_float(gu[16 + 2 * e + 1]));
-        if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
-      } else if constexpr (OP == DenseOp::kDglu) {
-        uint32_t gud[48], wg[8], wu[8], wh[8];
-        ptx::tmem_ld3x16(lanes + c, lanes + BN / 2 + c, lanes + BN + buf * (BN / 2) + c, gud);
-        taken(c);
+      for (int c = 0; c < kCols; c += 16) {
+        uint32_t d[16], wg[8], wu[8], wh[8];
+        ptx::tmem_ld16(lanes + BN + buf * (BN / 2) + c, d);
+        if (c + 16 >= kCols) give_back(empty + 8 * buf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float dg[2], du[2], h[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float dh = __uint_as_float(gud[32 + 2 * e + k]), up = __uint_as_float(gud[16 + 2 * e + k]);
+            const float dh = __uint_as_float(d[2 * e + k]), up = __uint_as_float(gu[32 + c + 2 * e + k]);
             float slope;
-            const float act = act_both<ACT>(__uint_as_float(gud[2 * e + k]), slope);
+            const float act = act_both<ACT>(__uint_as_float(gu[c + 2 * e + k]), slope);
             dg[k] = dh * up * slope;
             du[k] = dh * act;
             h[k] = act * up;
@@ -249,16 +239,33 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
           wu[e] = pack_bf16(du[0], du[1]);
           wh[e] = pack_bf16(h[0], h[1]);
         }
-        if (in) {
+        const int col = u.n0 + part * kCols + c, left = a.N - col;
+        if (row < a.M && left > 0) {
           __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + row * 2 * a.N + col;
           store_bf16(p, wg, left, a.wide);
           store_bf16(p + a.N, wu, left, a.wide);
           store_bf16(static_cast<__nv_bfloat16*>(a.out2) + row * a.N + col, wh, left, a.wide);
         }
+      }
+      continue;
+    }
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += kStep) {
+      const int col = u.n0 + part * kCols + c, left = a.N - col;
+      const bool in = row < a.M && left > 0;
+      if constexpr (OP == DenseOp::kGlu) {
+        uint32_t gu[32], w[8];
+        ptx::tmem_ld2x16(lanes + buf * BN + c, lanes + buf * BN + BN / 2 + c, gu);
+        if (c + kStep >= kCols) give_back(empty + 8 * buf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[e] = pack_bf16(act_value<ACT>(__uint_as_float(gu[2 * e])) * __uint_as_float(gu[16 + 2 * e]),
+                           act_value<ACT>(__uint_as_float(gu[2 * e + 1])) * __uint_as_float(gu[16 + 2 * e + 1]));
+        if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
       } else {
         uint32_t r[32];
         ptx::tmem_ld32(lanes + buf * BN + c, r);
-        taken(c);
+        if (c + kStep >= kCols) give_back(empty + 8 * buf);
         if (OP == DenseOp::kDw && a.splits > 1) {
           if (in) {
             float4* dst = reinterpret_cast<float4*>(a.part + ((long long)u.split * a.M + row) * a.N + col);
