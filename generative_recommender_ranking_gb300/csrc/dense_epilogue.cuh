@@ -33,6 +33,19 @@ __device__ __forceinline__ float act_both(float g, float& slope) {
   return g * p;
 }
 
+// The same for fp32 results: the library's exponential and division keep its last bits.
+template <int ACT>
+__device__ __forceinline__ float act32(float g, float& slope) {
+  if (ACT == REC_ATTN_SILU) {
+    const float p = 1.f / (1.f + expf(-g)), v = g * p;
+    slope = fmaf(v, 1.f - p, p);
+    return v;
+  }
+  const float p = 0.5f * erfcf(-0.70710678f * g);
+  slope = fmaf(g, 0.39894228f * expf(-0.5f * g * g), p);
+  return g * p;
+}
+
 // 32 columns of a row in bf16; `left` columns of the result remain from the first on (a multiple of
 // 8).  wide: the row starts on a 32-byte boundary, whole sectors are written.
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&w)[16], int left, bool wide) {

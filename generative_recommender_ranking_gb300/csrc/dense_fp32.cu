@@ -175,19 +175,6 @@ __device__ __forceinline__ void store_planes(const Planes& to, long long row, in
     *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(v[p][0], v[p][1]), pack_bf16(v[p][2], v[p][3]));
 }
 
-// (the activation with the library's exponential: fp32 keeps its last bits)
-template <int ACT>
-__device__ __forceinline__ float act32(float g, float& slope) {
-  if (ACT == REC_ATTN_SILU) {
-    const float p = 1.f / (1.f + expf(-g)), v = g * p;
-    slope = fmaf(v, 1.f - p, p);
-    return v;
-  }
-  const float p = 0.5f * erfcf(-0.70710678f * g);
-  slope = fmaf(g, 0.39894228f * expf(-0.5f * g * g), p);
-  return g * p;
-}
-
 template <DenseOp OP, int ACT>
 __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
   using C = Cfg<OP>;

@@ -20,6 +20,12 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// A kernel launched with the programmatic attribute may start before its predecessor ends (once all of
+// that one's blocks have said successor_may_start); what it reads of the predecessor's stands behind
+// predecessor_done.
+__device__ __forceinline__ void predecessor_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void successor_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");

@@ -111,6 +111,7 @@ constexpr int kQuantThreads = 256, kQuantRun = 4;
 // A scale per row and 128 columns: 16 lanes a block, four blocks of theirs in flight.
 template <typename E>
 __global__ void __launch_bounds__(kQuantThreads) k_quantize_rows(QuantArgs a) {
+  ptx::successor_may_start();
   const int lane = threadIdx.x & 15, chunks = a.width / 8;
   const long long units = a.rows * a.blocks, groups = (long long)gridDim.x * (kQuantThreads / 16);
   const long long first = (long long)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);

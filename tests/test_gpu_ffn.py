@@ -109,3 +109,17 @@ def test_against_64_bits(rows, width, hidden, dtype, act):
     ref = reference(*t, act, torch.finfo(dtype).eps / 2)
     for n in ("y", "dx", "dw_in", "dw_out"):
         within(out[n], ref[n], n)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [2, 3, 7, 8, 9, 16, 17, 24, 25, 31, 32, 33, 64, 65, 127])
+def test_few_rows(rows, dtype, act):
+    """Row counts about the borders of the few-row kernels, columns and summed axes off their blocks."""
+    for width, hidden in ((72, 1096), (1160, 24), (200, 136)):
+        t = inputs(rows, width, hidden, dtype, seed=rows)
+        y = torch.full_like(t[0], float("nan"))
+        bd.rec_attn_ffn_fwd(t[0], t[2], t[3], y, activation=act)
+        torch.cuda.synchronize()
+        assert bd.rec_attn_dense_device_status() == bd.OK
+        within(y, reference(*t, act, torch.finfo(dtype).eps / 2)["y"], "y")
