@@ -132,13 +132,13 @@ bool encode_planes(CUtensorMap* m, const Planes& a) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D map over an e4m3 [rows][cols] matrix; box = 128 columns x 128 rows, 128-byte swizzle.
-bool encode_scaled(CUtensorMap* m, const void* base, long long rows, long long cols) {
+// 2-D map over an e4m3 [rows][cols] matrix; box = 128 columns x `box_rows` rows, 128-byte swizzle.
+bool encode_scaled(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)cols};
-  cuuint32_t box[2] = {128, 128};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -1,252 +1,305 @@
-// few.cu -- the feed-forward products for few rows (serving a handful of tokens).
+// few.cu -- the feed-forward products for few rows (serving a handful of tokens), bf16 and e4m3.
 //
-// Every weight is used once for each row, so the weights' bytes bound the time: they go from memory
-// straight into registers, 16 bytes a lane.  bf16 and e4m3 take mma.sync m16n8k16 with 16 rows of
-// weights as its first operand and 8 token rows as its second (a tile of the tensor cores' tcgen05
-// kind would hold 128 rows of which few are tokens, and needs the weights in shared memory first).
-// The order of the summed axis is free, so a lane's 16 bytes are the values it owns in both operands
-// and nothing is shuffled.  A block has 16 columns of the result (gated: the 16 gate rows and the 16 up
-// rows of w); its eight warps take blocks of 128 of the summed axis in turn and are added up in
-// shared memory, in their order.  e4m3 values are fp16 values: they are converted, summed block by
-// block and added in fp32 times the block's scales.  fp32 multiplies on the CUDA cores.
+// Every weight is used once for each row, so the weights' bytes bound the time.  The operands change
+// places: 128 rows of weights are the MMA's M side, the token rows (up to 64, padded to 16, 32 or 64) its
+// N side, and a CTA keeps all of its shared memory full of weights on their way (TMA, up to 180 KB).  A
+// tile is 128 columns of the result (gated: their gate rows and their up rows, two accumulators); where
+// tiles are fewer than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's summed axis, and each then adds
+// up its share of the token rows over the CTAs' sums through distributed shared memory, in their order.
+// e4m3: each block of 128 is summed by itself and taken into registers times its scales, as in scaled.cu.
+// The first weights of a product that follows another are fetched before that one has ended.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
+#include <atomic>
+
+#include "dense.cuh"
 #include "dense_epilogue.cuh"
 #include "few.cuh"
 #include "launchers.cuh"
+#include "ptx_sm103.cuh"
+#include "quantize.cuh"
+#include "scaled.cuh"
+#include "wait.cuh"
 
 namespace recattn {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kCols = 16;    // columns of the result a block
-constexpr int kChunk = 128;  // of the summed axis, a warp's turn
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
+constexpr int kThreads = 192, kSumWarps = 4;
+constexpr int kMat = 128 * 128;              // 128 rows of 128 bytes
+constexpr uint32_t kTmem = 256;
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+enum { kFull = 0, kEmpty = 12, kAccFull = 24, kAccEmpty = 26, kDone = 28, kBars = 29 };
+
+// TOKENS: rows of x that an MMA takes.
+template <bool GATED, int TOKENS>
+struct Cfg {
+  static constexpr int kMats = GATED ? 2 : 1;
+  static constexpr int kStage = kMats * kMat + TOKENS * 128;
+  static constexpr int kStages = 212 * 1024 / kStage < 12 ? 212 * 1024 / kStage : 12;
+  static constexpr int kDynamic = kStages * kStage + 1024;
+  static_assert(kStages * kStage >= kMats * TOKENS * 128 * 4, "the CTA's sums fit the ring");
+};
+
+// Four floats of another CTA's shared memory, at this one's place `p`.
+__device__ __forceinline__ float4 remote_float4(const void* p, int rank) {
+  uint32_t at;
+  float4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Four e4m3 values as two pairs of fp16.
-__device__ __forceinline__ uint2 halves(uint32_t w) {
-  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-  return make_uint2((uint32_t)lo.x | (uint32_t)lo.y << 16, (uint32_t)hi.x | (uint32_t)hi.y << 16);
+__device__ __forceinline__ float4 sum_of(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// 16 bytes each of rows g and g + 8 of w, and of a row of x, into d.
-template <bool E4M3>
-__device__ __forceinline__ void product(float (&d)[4], const uint4 a, const uint4 b, const uint4 x) {
-  if constexpr (E4M3) {
-    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w}, wx[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint2 ha = halves(wa[i]), hb = halves(wb[i]), hx = halves(wx[i]);
-      mma_f16(d, ha.x, hb.x, ha.y, hb.y, hx.x, hx.y);
+template <bool E4M3, bool GATED, int TOKENS>
+__device__ void load_all(const FewArgs& a, const CUtensorMap* mw, const CUtensorMap* mx, uint8_t* sm, uint64_t* bars,
+                         volatile int* abort_flag, int n0, int kb0, int kb1, int lane) {
+  using C = Cfg<GATED, TOKENS>;
+  constexpr int kX = E4M3 ? 128 : 64;  // values in 128 bytes
+  const auto weights = [&](int kb, int st) {
+    uint8_t* s = sm + st * C::kStage;
+    ptx::mbar_arrive_expect_tx(bars + kFull + st, C::kStage);
+    ptx::tma_load_2d(s, mw, kb * kX, n0, bars + kFull + st);
+    if (GATED) ptx::tma_load_2d(s + kMat, mw, kb * kX, a.N + n0, bars + kFull + st);
+  };
+  const int ahead = min(kb1 - kb0, C::kStages);
+  if (lane == 0)
+    for (int j = 0; j < ahead; ++j) weights(kb0 + j, j);
+  if (a.follows) ptx::predecessor_done();
+  if (lane == 0)
+    for (int j = 0; j < ahead; ++j)
+      ptx::tma_load_2d(sm + j * C::kStage + C::kMats * kMat, mx, (kb0 + j) * kX, 0, bars + kFull + j);
+  __syncwarp();
+  int n = ahead;
+  for (; n < kb1 - kb0; ++n) {
+    const int st = n % C::kStages;
+    if (!bounded_wait_warp(bars + kEmpty + st, (n / C::kStages + 1) & 1, abort_flag, a.status, kWaitNs)) break;
+    if (lane == 0) {
+      weights(kb0 + n, st);
+      ptx::tma_load_2d(sm + st * C::kStage + C::kMats * kMat, mx, (kb0 + n) * kX, 0, bars + kFull + st);
     }
-  } else {
-    mma_bf16(d, a.x, b.x, a.y, b.y, x.x, x.y);
-    mma_bf16(d, a.z, b.z, a.w, b.w, x.z, x.w);
+    __syncwarp();
   }
+  // after an abort, copies may still be in flight
+  if (lane == 0)
+    for (int j = max(0, n - C::kStages); j < n; ++j)
+      bounded_drain(bars + kFull + j % C::kStages, (j / C::kStages) & 1, kWaitNs / 4);
+  __syncwarp();
 }
 
-// TILES: groups of 8 token rows.
-template <bool E4M3, bool GATED, int ACT, int TILES>
-__global__ void __launch_bounds__(kThreads, 2) k_few(const FewArgs a) {
-  constexpr int kSize = E4M3 ? 1 : 2, kPer = 16 / kSize;        // values in 16 bytes
-  constexpr int kLoads = kChunk / (4 * kPer);                   // 16-byte loads of a row's chunk, a lane
-  constexpr int kMats = GATED ? 2 : 1;                          // gate and up
-  __shared__ float s_sum[kWarps][kMats * TILES * 4][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kCols;
-  const int chunks = (a.K + kChunk - 1) / kChunk;
-  ptx::successor_may_start();
-  const char* const w = static_cast<const char*>(a.w);
-  const char* const x = static_cast<const char*>(a.x);
-  float acc[kMats][TILES][4] = {};
-  uint4 wv[kMats][2][kLoads];
-  const auto load = [&](int c) {
+// bf16: one sum over all blocks; e4m3: a sum for each block, in two buffers.
+template <bool E4M3, bool GATED, int TOKENS>
+__device__ void issue(const FewArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int blocks) {
+  using C = Cfg<GATED, TOKENS>;
+  const uint32_t idesc = E4M3 ? ptx::idesc_e4m3_f32(128, TOKENS) : ptx::idesc_bf16_f32(128, TOKENS, false, false);
+  const uint32_t s0 = ptx::smem_u32(sm);
+  const bool el = ptx::elect_one();
+  for (int n = 0; n < blocks; ++n) {
+    const int st = n % C::kStages;
+    const uint32_t buf = E4M3 ? n & 1 : 0;
+    if (E4M3 && !bounded_wait_warp(bars + kAccEmpty + buf, ((n >> 1) & 1) ^ 1, abort_flag, a.status, kWaitNs)) break;
+    if (!bounded_wait_warp(bars + kFull + st, (n / C::kStages) & 1, abort_flag, a.status, kWaitNs)) break;
+    ptx::tc_fence_after();
+    if (el) {
+      const uint32_t s = s0 + st * C::kStage;
+      const uint64_t dx = ptx::smem_desc_sw128(s + C::kMats * kMat, 16, 1024);
 #pragma unroll
-    for (int m = 0; m < kMats; ++m)
+      for (int m = 0; m < C::kMats; ++m) {
+        const uint64_t dw = ptx::smem_desc_sw128(s + m * kMat, 16, 1024);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int n = n0 + g + 8 * r;
-        const char* row = w + ((long long)m * a.N + n) * a.K * kSize;
+        for (int k = 0; k < 4; ++k)
+          ptx::umma_pair<1, E4M3>(tmem + (buf * C::kMats + m) * TOKENS, ptx::smem_desc_at(dw, 32 * k),
+                                  ptx::smem_desc_at(dx, 32 * k), idesc, k > 0 || (!E4M3 && n > 0));
+      }
+      ptx::umma_commit(bars + kEmpty + st);
+      if (E4M3 || n == blocks - 1) ptx::umma_commit(bars + kAccFull + buf);
+    }
+    __syncwarp();
+  }
+  if (el) {
+    ptx::umma_commit(bars + kDone);
+    bounded_drain(bars + kDone, 0, kWaitNs / 4);
+  }
+  __syncwarp();
+}
+
+// Four warps: a thread has one weight row; its sums go to s_sum[matrix][token][row].
+template <bool E4M3, bool GATED, int TOKENS>
+__device__ void collect(const FewArgs& a, float* s_sum, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int n0,
+                        int kb0, int kb1, int warp, int lane) {
+  using C = Cfg<GATED, TOKENS>;
+  const int quad = warp & 3;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  float* const mine = s_sum + quad * 32 + lane;
+  if constexpr (E4M3) {
+    if (a.follows) ptx::predecessor_done();
+    float acc[C::kMats][TOKENS];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int k = c * kChunk + (4 * i + t) * kPer;
-          wv[m][r][i] = n < a.N && k < a.K ? __ldcs(reinterpret_cast<const uint4*>(row + (long long)k * kSize)) : make_uint4(0, 0, 0, 0);
+    for (int m = 0; m < C::kMats; ++m)
+#pragma unroll
+      for (int j = 0; j < TOKENS; ++j) acc[m][j] = 0.f;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int n = kb - kb0;
+      const uint32_t buf = n & 1;
+      // lane l: the scales of tokens l and 32 + l
+      float sx[(TOKENS + 31) / 32];
+#pragma unroll
+      for (int h = 0; h < (TOKENS + 31) / 32; ++h)
+        sx[h] = 32 * h + lane < a.rows ? a.x_scale[(long long)(32 * h + lane) * a.kblocks + kb] : 0.f;
+      float sw[C::kMats];
+#pragma unroll
+      for (int m = 0; m < C::kMats; ++m) sw[m] = __ldg(a.w_scale + (long long)((m * a.N + n0) / 128) * a.kblocks + kb);
+      if (!bounded_wait_warp(bars + kAccFull + buf, (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < TOKENS; c += 16) {
+#pragma unroll
+        for (int m = 0; m < C::kMats; ++m) {
+          uint32_t r[16];
+          ptx::tmem_ld16(lanes + (buf * C::kMats + m) * TOKENS + c, r);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            acc[m][c + e] = fmaf(__uint_as_float(r[e]), sw[m] * __shfl_sync(0xffffffffu, sx[(c + e) / 32], (c + e) & 31), acc[m][c + e]);
         }
       }
-  };
-  if (warp < chunks) load(warp);
-  if (a.follows) ptx::predecessor_done();
-  for (int c = warp; c < chunks; c += kWarps) {
-    float sum[kMats][TILES][4] = {};
-#pragma unroll
-    for (int j = 0; j < TILES; ++j) {
-      const int row = 8 * j + g;
-      uint4 xv[kLoads];
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int k = c * kChunk + (4 * i + t) * kPer;
-        xv[i] = row < a.rows && k < a.K ? *reinterpret_cast<const uint4*>(x + ((long long)row * a.K + k) * kSize) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int m = 0; m < kMats; ++m)
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) product<E4M3>(E4M3 ? sum[m][j] : acc[m][j], wv[m][0][i], wv[m][1][i], xv[i]);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty + buf);
     }
-    if (c + kWarps < chunks) load(c + kWarps);
-    if constexpr (E4M3) {
 #pragma unroll
-      for (int m = 0; m < kMats; ++m) {
-        const float sw = __ldg(a.w_scale + (long long)((m * a.N + n0) / kChunk) * chunks + c);
+    for (int m = 0; m < C::kMats; ++m)
 #pragma unroll
-        for (int j = 0; j < TILES; ++j)
+      for (int j = 0; j < TOKENS; ++j) mine[(m * TOKENS + j) * 128] = acc[m][j];
+  } else {
+    if (!bounded_wait_warp(bars + kAccFull, 0, abort_flag, a.status, kWaitNs)) return;
+    ptx::tc_fence_after();
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 8 * j + 2 * t + e;
-            const float f = row < a.rows ? sw * a.x_scale[(long long)row * chunks + c] : 0.f;
-            acc[m][j][e] = fmaf(sum[m][j][e], f, acc[m][j][e]);
-            acc[m][j][2 + e] = fmaf(sum[m][j][2 + e], f, acc[m][j][2 + e]);
-          }
-      }
+    for (int j = 0; j < C::kMats * TOKENS; j += 16) {
+      uint32_t r[16];
+      ptx::tmem_ld16(lanes + j, r);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mine[(j + e) * 128] = __uint_as_float(r[e]);
     }
-  }
-#pragma unroll
-  for (int m = 0; m < kMats; ++m)
-#pragma unroll
-    for (int j = 0; j < TILES; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s_sum[warp][(m * TILES + j) * 4 + e][lane] = acc[m][j][e];
-  __syncthreads();
-  // result (row, column) = (8 j + 2 t + (e & 1), g + 8 (e >> 1)); 16 neighbouring threads: a row's columns
-  for (int i = threadIdx.x; i < 8 * TILES * kCols; i += kThreads) {
-    const int col = i % kCols, row = i / kCols;
-    const int at = (row >> 3) * 4 + (col >> 3) * 2 + (row & 1), from = (col & 7) * 4 + ((row & 7) >> 1);
-    float v = 0.f, u = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      v += s_sum[k][at][from];
-      if (GATED) u += s_sum[k][TILES * 4 + at][from];
-    }
-    if (row >= a.rows || n0 + col >= a.N) continue;
-    const long long o = (long long)row * a.N + n0 + col;
-    if (GATED) v = act_value<ACT>(v) * u;
-    if (GATED && E4M3) static_cast<float*>(a.out)[o] = v;
-    else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+    ptx::tc_fence_before();
   }
 }
 
-// fp32: a warp has kCols32 columns of the result (gated: as many pairs) and 1 / kWarps of the summed axis;
-// a lane four neighbouring values of it.
-constexpr int kCols32 = 2;
-template <bool GATED, int ACT, int ROWS>
-__global__ void __launch_bounds__(kThreads, 2) k_few32(const FewArgs a) {
-  constexpr int kMats = GATED ? 2 : 1;
-  __shared__ float s_sum[kWarps][kMats * kCols32 * ROWS];
+template <bool E4M3, bool GATED, int ACT, int TOKENS>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_few(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, const FewArgs a) {
+  using C = Cfg<GATED, TOKENS>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kBars];
+  __shared__ int s_abort;
+  __shared__ uint32_t tmem_slot;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * kCols32;  // (N is a multiple of 4)
+  const int rank = a.cluster > 1 ? (int)ptx::pair_rank<2>() : 0, n0 = (int)(blockIdx.x / a.cluster) * 128;
+  const int kb0 = a.kblocks * rank / a.cluster, kb1 = a.kblocks * (rank + 1) / a.cluster;
   ptx::successor_may_start();
-  const float* const w = static_cast<const float*>(a.w);
-  const float* const x = static_cast<const float*>(a.x);
-  float acc[kMats][kCols32][ROWS] = {};
-  if (a.follows) ptx::predecessor_done();
-#pragma unroll 2
-  for (int k = (warp * 32 + lane) * 4; k < a.K; k += kThreads * 4) {
-    float4 wv[kMats][kCols32];
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      ptx::mbar_init(bars + kFull + i, 1);
+      ptx::mbar_init(bars + kEmpty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars + kAccFull + i, 1);
+      ptx::mbar_init(bars + kAccEmpty + i, kSumWarps);
+    }
+    ptx::mbar_init(bars + kDone, 1);
+    s_abort = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&tmem_slot, kTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  float* const s_sum = reinterpret_cast<float*>(sm);  // over the ring, once every block has been summed
+  if (warp == 0) load_all<E4M3, GATED, TOKENS>(a, &mw, &mx, sm, bars, abort_flag, n0, kb0, kb1, lane);
+  else if (warp == 1) issue<E4M3, GATED, TOKENS>(a, sm, bars, tmem, abort_flag, kb1 - kb0);
+  else collect<E4M3, GATED, TOKENS>(a, s_sum, bars, tmem, abort_flag, n0, kb0, kb1, warp, lane);
+  __syncthreads();
+  if (a.cluster > 1) ptx::pair_sync<2>();
+  // a warp per token row: 128 columns, four a lane
+  const int col = n0 + 4 * lane;
+  for (int t = rank + a.cluster * warp; t < a.rows; t += a.cluster * (kThreads / 32)) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v;
+    const float4* const at = reinterpret_cast<const float4*>(s_sum + t * 128) + lane;
+    for (int r = 0; r < a.cluster; ++r) {
+      v = sum_of(v, a.cluster > 1 ? remote_float4(at, r) : *at);
+      if (GATED) u = sum_of(u, a.cluster > 1 ? remote_float4(at + TOKENS * 32, r) : at[TOKENS * 32]);
+    }
+    if (GATED) {
+      v.x = act_value<ACT>(v.x) * u.x;
+      v.y = act_value<ACT>(v.y) * u.y;
+      v.z = act_value<ACT>(v.z) * u.z;
+      v.w = act_value<ACT>(v.w) * u.w;
+    }
+    const long long o = (long long)t * a.N + col;
+    if constexpr (E4M3 && GATED) {
+      float top = largest_or_nan(largest_or_nan(largest_or_nan(largest_or_nan(0.f, v.x), v.y), v.z), v.w);
+      const bool fine = top <= kFloatMax;
+      if (!fine) top = fmaxf(fmaxf(finite_size(v.x), finite_size(v.y)), fmaxf(finite_size(v.z), finite_size(v.w)));
 #pragma unroll
-    for (int m = 0; m < kMats; ++m)
-#pragma unroll
-      for (int c = 0; c < kCols32; ++c)
-        wv[m][c] = __ldcs(reinterpret_cast<const float4*>(w + ((long long)m * a.N + n0 + c) * a.K + k));
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      if (r >= a.rows) break;
-      const float4 xv = *reinterpret_cast<const float4*>(x + (long long)r * a.K + k);
-#pragma unroll
-      for (int m = 0; m < kMats; ++m)
-#pragma unroll
-        for (int c = 0; c < kCols32; ++c)
-          acc[m][c][r] = fmaf(xv.x, wv[m][c].x, fmaf(xv.y, wv[m][c].y, fmaf(xv.z, wv[m][c].z, fmaf(xv.w, wv[m][c].w, acc[m][c][r]))));
+      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      float inv;
+      const float scale = block_scale(top, inv);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + o) = pack_e4m3(v.x * inv, v.y * inv, v.z * inv, v.w * inv, fine);
+      if (lane == 0) a.out_scale[(long long)t * (a.N / 128) + n0 / 128] = scale;
+    } else if (col < a.N) {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
   }
-#pragma unroll
-  for (int m = 0; m < kMats; ++m)
-#pragma unroll
-    for (int c = 0; c < kCols32; ++c)
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        float v = acc[m][c][r];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) s_sum[warp][(m * kCols32 + c) * ROWS + r] = v;
-      }
+  ptx::tc_fence_before();
   __syncthreads();
-  if (threadIdx.x >= kCols32 * ROWS) return;
-  const int c = threadIdx.x % kCols32, r = threadIdx.x / kCols32;
-  if (r >= a.rows) return;
-  float v = 0.f, u = 0.f;
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    v += s_sum[k][c * ROWS + r];
-    if (GATED) u += s_sum[k][(kCols32 + c) * ROWS + r];
+  if (a.cluster > 1) ptx::pair_sync<2>();  // no CTA leaves while another reads its sums
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmem);
   }
-  if (GATED) {
-    float slope;
-    v = act32<ACT>(v, slope) * u;
-  }
-  static_cast<float*>(a.out)[(long long)r * a.N + n0 + c] = v;
 }
 
-cudaError_t go(void (*fn)(FewArgs), const FewArgs& a, int cols, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((a.N + cols - 1) / cols));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = a.follows ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fn, a);
+template <bool E4M3, bool GATED, int ACT, int TOKENS>
+cudaError_t run(const FewArgs& a, cudaStream_t st) {
+  using C = Cfg<GATED, TOKENS>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(done, (const void*)k_few<E4M3, GATED, ACT, TOKENS>, C::kDynamic);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mw, mx;
+  const long long wr = (long long)C::kMats * a.N;
+  const bool ok = E4M3 ? encode_scaled(&mw, a.w, wr, a.K) && encode_scaled(&mx, a.x, a.rows, a.K, TOKENS)
+                       : encode_map(&mw, a.w, wr, a.K, 128) && encode_map(&mx, a.x, a.rows, a.K, TOKENS);
+  if (!ok) return cudaErrorInvalidValue;
+  return launch_pairs(a.cluster, a.follows != 0, k_few<E4M3, GATED, ACT, TOKENS>, (a.N + 127) / 128 * a.cluster, kThreads,
+                      C::kDynamic, st, mw, mx, a);
 }
-
 template <bool E4M3, bool GATED, int ACT>
 cudaError_t by_rows(const FewArgs& a, cudaStream_t st) {
-  if (a.rows <= 8) return go(k_few<E4M3, GATED, ACT, 1>, a, kCols, st);
-  if (a.rows <= 16) return go(k_few<E4M3, GATED, ACT, 2>, a, kCols, st);
-  if (a.rows <= 24) return go(k_few<E4M3, GATED, ACT, 3>, a, kCols, st);
-  return go(k_few<E4M3, GATED, ACT, 4>, a, kCols, st);
+  if (a.rows <= 16) return run<E4M3, GATED, ACT, 16>(a, st);
+  if (a.rows <= 32) return run<E4M3, GATED, ACT, 32>(a, st);
+  return run<E4M3, GATED, ACT, 64>(a, st);
 }
 template <bool E4M3>
 cudaError_t by_kind(bool gated, const FewArgs& a, cudaStream_t st) {
   if (!gated) return by_rows<E4M3, false, 0>(a, st);
   return a.act == REC_ATTN_SILU ? by_rows<E4M3, true, REC_ATTN_SILU>(a, st) : by_rows<E4M3, true, REC_ATTN_GELU>(a, st);
 }
-template <bool GATED, int ACT>
-cudaError_t by_rows32(const FewArgs& a, cudaStream_t st) {
-  if (a.rows <= 2) return go(k_few32<GATED, ACT, 2>, a, kCols32, st);
-  return go(k_few32<GATED, ACT, kFewRows32>, a, kCols32, st);
-}
 
 }  // namespace
 
-cudaError_t launch_few(FewType type, bool gated, const FewArgs& a, cudaStream_t st) {
-  if (type == FewType::kBf16) return by_kind<false>(gated, a, st);
-  if (type == FewType::kE4m3) return by_kind<true>(gated, a, st);
-  if (!gated) return by_rows32<false, 0>(a, st);
-  return a.act == REC_ATTN_SILU ? by_rows32<true, REC_ATTN_SILU>(a, st) : by_rows32<true, REC_ATTN_GELU>(a, st);
+cudaError_t launch_few(bool e4m3, bool gated, FewArgs a, int num_sms, cudaStream_t st) {
+  a.kblocks = e4m3 ? (a.K + 127) / 128 : (a.K + 63) / 64;
+  a.cluster = 1;
+  while (a.cluster < 8 && 2 * a.cluster <= a.kblocks && 2LL * a.cluster * ((a.N + 127) / 128) <= num_sms) a.cluster *= 2;
+  return e4m3 ? by_kind<true>(gated, a, st) : by_kind<false>(gated, a, st);
 }
 
 }  // namespace recattn

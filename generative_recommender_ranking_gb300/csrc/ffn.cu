@@ -101,10 +101,10 @@ cudaError_t plain32(DenseOp op, const Planes& a, const Planes& b, long long M, l
 }
 
 // The forward for few rows: two kernels, h [rows][hidden] between them.
-cudaError_t ffn_few(FewType type, int act, long long R, long long W, long long H, const void* x, const void* w_in,
-                    const void* w_out, void* y, int dev, cudaStream_t st) {
+cudaError_t ffn_few(bool bf16, int act, long long R, long long W, long long H, const void* x, const void* w_in,
+                    const void* w_out, void* y, int dev, int sms, cudaStream_t st) {
   Workspace ws(st);
-  cudaError_t e = ws.take(dev, R * H * (type == FewType::kBf16 ? 2 : 4));
+  cudaError_t e = ws.take(dev, R * H * (bf16 ? 2 : 4));
   if (e != cudaSuccess) return e;
   FewArgs a{};
   a.rows = (int)R;
@@ -114,14 +114,15 @@ cudaError_t ffn_few(FewType type, int act, long long R, long long W, long long H
   a.w = w_in;
   a.act = act;
   a.out = ws.p;
-  e = launch_few(type, true, a, st);
+  a.status = dense_status();
+  e = bf16 ? launch_few(false, true, a, sms, st) : launch_few32(true, a, st);
   a.N = (int)W;
   a.K = (int)H;
   a.x = ws.p;
   a.w = w_out;
   a.out = y;
   a.follows = 1;
-  if (e == cudaSuccess) e = launch_few(type, false, a, st);
+  if (e == cudaSuccess) e = bf16 ? launch_few(false, false, a, sms, st) : launch_few32(false, a, st);
   const cudaError_t ef = ws.give_back();
   return e != cudaSuccess ? e : ef;
 }
@@ -217,8 +218,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == REC_ATTN_BF16;
   if (rows <= (bf16 ? kFewRows : kFewRows32))
-    return from_cuda(ffn_few(bf16 ? FewType::kBf16 : FewType::kFp32, activation, rows, width, hidden, x, w_in, w_out, y,
-                             dev, st));
+    return from_cuda(ffn_few(bf16, activation, rows, width, hidden, x, w_in, w_out, y, dev, sms, st));
   if (!bf16) return from_cuda(ffn32_fwd(activation, rows, width, hidden, x, w_in, w_out, y, dev, sms, st));
   Workspace ws(st);
   e = ws.take(dev, rows * hidden * es);
@@ -390,8 +390,8 @@ REC_ATTN_API rec_attn_status rec_attn_scaled_matmul(int64_t rows, int64_t cols, 
   if (e != cudaSuccess) return from_cuda(e);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (rows <= kFewRows)
-    return from_cuda(launch_few(FewType::kE4m3, false,
-                                {(int)rows, (int)cols, (int)depth, a, a_scale, b, b_scale, 0, y, 0}, st));
+    return from_cuda(launch_few(true, false, {(int)rows, (int)cols, (int)depth, a, a_scale, b, b_scale, 0, y, nullptr, 0,
+                                              dense_status()}, sms, st));
   return from_cuda(scaled(false, a, a_scale, rows, b, b_scale, cols, depth, 0, y, nullptr, sms, st));
 }
 
@@ -417,21 +417,19 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool few = rows <= kFewRows;
   const size_t off_xs = ws_up(n), off_h = off_xs + ws_up(4 * rows * kw), off_hs = off_h + ws_up(rows * hidden);
-  const size_t off_h32 = off_hs + ws_up(4 * rows * kh);
   Workspace ws(st);
-  e = ws.take(dev, off_h32 + (few ? 4 * rows * hidden : 0));
+  e = ws.take(dev, off_hs + 4 * rows * kh);
   if (e != cudaSuccess) return from_cuda(e);
   uint8_t* const xq = static_cast<uint8_t*>(ws.p);
   float* const xs = reinterpret_cast<float*>(xq + off_xs);
   uint8_t* const hq = xq + off_h;
   float* const hs = reinterpret_cast<float*>(xq + off_hs);
   e = launch_quantize({x, xq, xs, rows, (int)width, (int)kw}, REC_ATTN_BF16, 1, sms, st);
-  if (few) {  // a block of the few-row product has 16 of a scale's 128 columns: h in fp32 first
-    void* const h32 = xq + off_h32;
+  if (few) {
     const int R = (int)rows, W = (int)width, H = (int)hidden;
-    if (e == cudaSuccess) e = launch_few(FewType::kE4m3, true, {R, H, W, xq, xs, w_in, w_in_scale, activation, h32, 1}, st);
-    if (e == cudaSuccess) e = launch_quantize({h32, hq, hs, rows, H, (int)kh}, REC_ATTN_FP32, 1, sms, st);
-    if (e == cudaSuccess) e = launch_few(FewType::kE4m3, false, {R, W, H, hq, hs, w_out, w_out_scale, 0, y, 1}, st);
+    int* const word = dense_status();
+    if (e == cudaSuccess) e = launch_few(true, true, {R, H, W, xq, xs, w_in, w_in_scale, activation, hq, hs, 1, word}, sms, st);
+    if (e == cudaSuccess) e = launch_few(true, false, {R, W, H, hq, hs, w_out, w_out_scale, 0, y, nullptr, 1, word}, sms, st);
   } else {
     if (e == cudaSuccess) e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, sms, st);
     if (e == cudaSuccess) e = scaled(false, hq, hs, rows, w_out, w_out_scale, width, hidden, 0, y, nullptr, sms, st);

@@ -34,20 +34,29 @@ inline cudaError_t allow_smem(std::atomic<unsigned long long>& done, const void*
   return e;
 }
 
-// Launches blocks in clusters of `cluster` (1: none).
+// Launches blocks in clusters of `cluster` (1: none); early: before the stream's last kernel has ended
+// (the kernel itself waits for it, ptx::predecessor_done).
 template <typename... P, typename... A>
-cudaError_t launch_pairs(int cluster, void (*fn)(P...), int blocks, int threads, int smem, cudaStream_t st, A&&... args) {
+cudaError_t launch_pairs(int cluster, bool early, void (*fn)(P...), int blocks, int threads, int smem, cudaStream_t st,
+                         A&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (early) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
 

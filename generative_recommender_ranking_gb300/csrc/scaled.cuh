@@ -31,7 +31,7 @@ struct ScaledArgs {
   float* out_scale;        // gated: [M][N / 128]
   int* status;
 };
-bool encode_scaled(CUtensorMap* m, const void* base, long long rows, long long cols);
+bool encode_scaled(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows = 128);
 // y = a b' of e4m3 operands; gated: act(a g') * (a u') with b = [g; u], in e4m3 with its scales.
 cudaError_t launch_scaled(bool gated, const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int num_sms,
                           cudaStream_t st);
