@@ -343,18 +343,32 @@ def rec_attn_compress(offsets_host, hist_begin, hist_len, segments, x, timestamp
     _check("rec_attn_compress", code)
 
 
+_DTYPES: dict = {}  # torch dtype -> rec_attn_dtype, filled on first use
+
+
+def _dtypes() -> dict:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float32: FP32})
+    return _DTYPES
+
+
 def _rows(fn: str, x, **others):
     """(dtype, rows, width) of a contiguous [rows, width] tensor of the current device; the
     others must match it."""
-    import torch
-    dtypes = {torch.bfloat16: BF16, torch.float32: FP32}
-    ok = x.dim() == 2 and x.dtype in dtypes and x.is_contiguous()
-    ok = ok and x.is_cuda and x.device.index == torch.cuda.current_device()
+    dtype, shape = (_DTYPES or _dtypes()).get(x.dtype), x.shape
+    ok = len(shape) == 2 and dtype is not None and x.is_contiguous() and _here(x)
     for o in others.values():
-        ok = ok and o.dtype == x.dtype and o.shape == x.shape and o.device == x.device and o.is_contiguous()
+        ok = ok and o.dtype == x.dtype and o.shape == shape and o.get_device() == x.get_device() and o.is_contiguous()
     if not ok:
         raise RecAttnError(fn, ERR_INVALID_ARG)
-    return dtypes[x.dtype], x.shape[0], x.shape[1]
+    return dtype, shape[0], shape[1]
+
+
+def _here(x) -> bool:
+    """Whether a tensor is on the current device."""
+    import torch
+    return x.is_cuda and x.get_device() == torch.cuda.current_device()
 
 
 def _gains(fn: str, x, types, **gains):
@@ -397,22 +411,25 @@ def rec_attn_layernorm_bwd(x, weight, dy, dx, dweight=None, dbias=None, types=No
 
 def _matrices(fn: str, x, *shaped):
     """Contiguous matrices of x's device: (tensor or None, shape, dtype) each."""
+    device = x.get_device()
     for o, shape, dtype in shaped:
-        if o is not None and not (o.dtype == dtype and tuple(o.shape) == shape and o.is_contiguous()
-                                  and o.device == x.device):
+        if o is not None and not (o.dtype == dtype and o.shape == shape and o.get_device() == device
+                                  and o.is_contiguous()):
             raise RecAttnError(fn, ERR_INVALID_ARG)
 
 
 def _activation(fn: str, name: str) -> int:
-    if name not in ACTIVATIONS:
+    act = ACTIVATIONS.get(name)
+    if act is None:
         raise RecAttnError(fn, ERR_INVALID_ARG)
-    return ACTIVATIONS[name]
+    return act
 
 
 def _hidden(fn: str, w_out) -> int:
-    if w_out.dim() != 2:
+    shape = w_out.shape
+    if len(shape) != 2:
         raise RecAttnError(fn, ERR_INVALID_ARG)
-    return w_out.shape[1]
+    return shape[1]
 
 
 def rec_attn_ffn_fwd(x, w_in, w_out, y, activation: str = "silu", stream=None) -> None:
@@ -446,8 +463,7 @@ def _scale_shape(shape, block_rows):
 
 
 def _on_device(fn: str, x) -> None:
-    import torch
-    if not (x.dim() == 2 and x.is_contiguous() and x.is_cuda and x.device.index == torch.cuda.current_device()):
+    if not (len(x.shape) == 2 and x.is_contiguous() and _here(x)):
         raise RecAttnError(fn, ERR_INVALID_ARG)
 
 

@@ -54,32 +54,45 @@ __device__ __forceinline__ float4 sum_of(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
+// One thread: block n of this CTA's on its way into its stage.
 template <bool E4M3, bool GATED, int TOKENS>
-__device__ void load_all(const FewArgs& a, const CUtensorMap* mw, const CUtensorMap* mx, uint8_t* sm, uint64_t* bars,
-                         volatile int* abort_flag, int n0, int kb0, int kb1, int lane) {
+struct Loader {
   using C = Cfg<GATED, TOKENS>;
-  constexpr int kX = E4M3 ? 128 : 64;  // values in 128 bytes
-  const auto weights = [&](int kb, int st) {
+  static constexpr int kX = E4M3 ? 128 : 64;  // values in 128 bytes
+  const FewArgs& a;
+  const CUtensorMap *mw, *mx;
+  uint8_t* sm;
+  uint64_t* bars;
+  int n0, kb0;
+  __device__ __forceinline__ void weights(int n) const {
+    const int st = n % C::kStages;
     uint8_t* s = sm + st * C::kStage;
     ptx::mbar_arrive_expect_tx(bars + kFull + st, C::kStage);
-    ptx::tma_load_2d(s, mw, kb * kX, n0, bars + kFull + st);
-    if (GATED) ptx::tma_load_2d(s + kMat, mw, kb * kX, a.N + n0, bars + kFull + st);
-  };
-  const int ahead = min(kb1 - kb0, C::kStages);
-  if (lane == 0)
-    for (int j = 0; j < ahead; ++j) weights(kb0 + j, j);
+    ptx::tma_load_2d(s, mw, (kb0 + n) * kX, n0, bars + kFull + st);
+    if (GATED) ptx::tma_load_2d(s + kMat, mw, (kb0 + n) * kX, a.N + n0, bars + kFull + st);
+  }
+  __device__ __forceinline__ void tokens(int n) const {
+    const int st = n % C::kStages;
+    ptx::tma_load_2d(sm + st * C::kStage + C::kMats * kMat, mx, (kb0 + n) * kX, 0, bars + kFull + st);
+  }
+};
+
+// The loading warp; the first stages' weights are on their way already.
+template <bool E4M3, bool GATED, int TOKENS>
+__device__ void load_rest(const FewArgs& a, const Loader<E4M3, GATED, TOKENS>& in, uint64_t* bars,
+                          volatile int* abort_flag, int blocks, int lane) {
+  using C = Cfg<GATED, TOKENS>;
+  const int ahead = min(blocks, C::kStages);
   if (a.follows) ptx::predecessor_done();
   if (lane == 0)
-    for (int j = 0; j < ahead; ++j)
-      ptx::tma_load_2d(sm + j * C::kStage + C::kMats * kMat, mx, (kb0 + j) * kX, 0, bars + kFull + j);
+    for (int j = 0; j < ahead; ++j) in.tokens(j);
   __syncwarp();
   int n = ahead;
-  for (; n < kb1 - kb0; ++n) {
-    const int st = n % C::kStages;
-    if (!bounded_wait_warp(bars + kEmpty + st, (n / C::kStages + 1) & 1, abort_flag, a.status, kWaitNs)) break;
+  for (; n < blocks; ++n) {
+    if (!bounded_wait_warp(bars + kEmpty + n % C::kStages, (n / C::kStages + 1) & 1, abort_flag, a.status, kWaitNs)) break;
     if (lane == 0) {
-      weights(kb0 + n, st);
-      ptx::tma_load_2d(sm + st * C::kStage + C::kMats * kMat, mx, (kb0 + n) * kX, 0, bars + kFull + st);
+      in.weights(n);
+      in.tokens(n);
     }
     __syncwarp();
   }
@@ -200,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = a.cluster > 1 ? (int)ptx::pair_rank<2>() : 0, n0 = (int)(blockIdx.x / a.cluster) * 128;
   const int kb0 = a.kblocks * rank / a.cluster, kb1 = a.kblocks * (rank + 1) / a.cluster;
-  ptx::successor_may_start();
+  const Loader<E4M3, GATED, TOKENS> in{a, &mw, &mx, sm, bars, n0, kb0};
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       ptx::mbar_init(bars + kFull + i, 1);
@@ -213,7 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(bars + kDone, 1);
     s_abort = 0;
     ptx::fence_barrier_init();
+    for (int j = 0; j < min(kb1 - kb0, C::kStages); ++j) in.weights(j);
   }
+  ptx::successor_may_start();
   if (warp == 1) {
     ptx::tmem_alloc(&tmem_slot, kTmem);
     ptx::tmem_relinquish();
@@ -223,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   float* const s_sum = reinterpret_cast<float*>(sm);  // over the ring, once every block has been summed
-  if (warp == 0) load_all<E4M3, GATED, TOKENS>(a, &mw, &mx, sm, bars, abort_flag, n0, kb0, kb1, lane);
+  if (warp == 0) load_rest<E4M3, GATED, TOKENS>(a, in, bars, abort_flag, kb1 - kb0, lane);
   else if (warp == 1) issue<E4M3, GATED, TOKENS>(a, sm, bars, tmem, abort_flag, kb1 - kb0);
   else collect<E4M3, GATED, TOKENS>(a, s_sum, bars, tmem, abort_flag, n0, kb0, kb1, warp, lane);
   __syncthreads();
