@@ -311,6 +311,7 @@ cudaError_t by_kind(bool gated, const FewArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_few(bool e4m3, bool gated, FewArgs a, int num_sms, cudaStream_t st) {
+  if (few_is_thin(e4m3, gated, a)) return launch_thin(e4m3, gated, a, st);
   a.kblocks = e4m3 ? (a.K + 127) / 128 : (a.K + 63) / 64;
   a.cluster = 1;
   while (a.cluster < 8 && 2 * a.cluster <= a.kblocks && 2LL * a.cluster * ((a.N + 127) / 128) <= num_sms) a.cluster *= 2;

@@ -25,6 +25,8 @@ struct FewArgs {
 };
 constexpr int kFewRows = 64;   // most rows of a call, bf16 and e4m3 (few.cu)
 constexpr int kFewRows32 = 8;  // fp32 (few32.cu)
+bool few_is_thin(bool e4m3, bool gated, const FewArgs& a);
+cudaError_t launch_thin(bool e4m3, bool gated, const FewArgs& a, cudaStream_t st);
 cudaError_t launch_few(bool e4m3, bool gated, FewArgs a, int num_sms, cudaStream_t st);
 cudaError_t launch_few32(bool gated, const FewArgs& a, cudaStream_t st);
 
