@@ -124,11 +124,12 @@ __device__ __forceinline__ uint32_t first_of_pair(const void* p) {
   if (CG == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(a));
   return a;
 }
-// Arrive on a barrier by its address in the cluster's window.
+// Arrive on a barrier by its address in the cluster's window.  (It says that TMEM has been read, which the
+// tcgen05 fences order; a release over the cluster would first wait for the thread's global stores.)
 template <int CG>
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
   if (CG == 1) mbar_arrive_at(bar);
-  else asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A tiled load into this CTA's shared memory that completes on a barrier of the pair.
 template <int CG>

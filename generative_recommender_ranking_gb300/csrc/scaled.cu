@@ -6,8 +6,9 @@
 // floating-point format loses nothing by a power of two but the last step below 2^-6 of its range.
 //
 // Product: y[m][n] = sum over blocks b of sa[m][b] sb[n / 128][b] (sum over the block's k of a[m][k]
-// b[n][k]).  The tensor cores sum one block into one of two TMEM buffers; eight warps take it up,
-// times its scales, into fp32 sums in registers (128 a thread) while the next block is summed.  So the
+// b[n][k]).  A pair of CTAs has a tile of 256 x 256; the tensor cores sum one block into one of two TMEM
+// buffers; sixteen warps take it up, times its scales, into fp32 sums in registers (64 a thread, two to
+// an instruction) while the next block is summed.  So the
 // scales may be any fp32, and no sum of more than 128 products is the tensor cores' own.  The gated form
 // takes 128 gate and 128 up columns as a tile and writes their product in e4m3 with its scales.
 #include <cuda_bf16.h>
@@ -151,49 +152,61 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize_blocks(QuantArgs a) 
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBN = 256;                     // columns of B a tile
 constexpr int kSlab = 128 * 128;             // 128 rows of a block: 128 bytes each
-constexpr int kStage = 3 * kSlab, kStages = 4;
+constexpr int kStage = 2 * kSlab, kStages = 6;  // a CTA's 128 rows of A and its half of B's 256
 constexpr int kEpiWarps = 16, kThreads = 64 + 32 * kEpiWarps;
 constexpr int kDynamic = kStages * kStage + 1024;
 constexpr uint32_t kTmem = 512;               // two buffers of a block's sums
 
-enum { kFull = 0, kEmpty = 4, kAccFull = 8, kAccEmpty = 10, kPairs = 12, kDone = 13, kBars = 14 };
+enum { kFull = 0, kEmpty = 6, kAccFull = 12, kAccEmpty = 14, kParts = 16, kDone = 17, kBars = 18 };
+
+// Tile t's first row in this CTA and column of the result.
+struct Tile {
+  long long m0;
+  int n;  // column tile
+};
+__device__ __forceinline__ Tile tile_at(const ScaledArgs& a, int t, uint32_t rank) {
+  const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
+  return {((long long)at.x * 2 + rank) * kTile, at.y};
+}
 
 template <bool GATED>
 __device__ void produce(const ScaledArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, uint8_t* sm, uint64_t* bars,
-                        volatile int* abort_flag, int lane) {
+                        volatile int* abort_flag, uint32_t rank, int lane) {
   const int tiles = a.tiles_m * a.tiles_n;
   uint32_t n = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
-    const int n0 = at.y * (GATED ? kBN / 2 : kBN), n1 = GATED ? a.N + n0 : n0 + 128;
+  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
+    const Tile at = tile_at(a, t, rank);
+    // gated: the gate's columns are the first CTA's rows of B, up's the second's
+    const int nb = GATED ? at.n * (kBN / 2) + (rank ? a.N : 0) : at.n * kBN + (int)rank * (kBN / 2);
     for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
       const int st = n % kStages;
       if (!bounded_wait_warp(bars + kEmpty + st, ((n / kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (ptx::elect_one()) {
         uint8_t* s = sm + st * kStage;
-        ptx::mbar_arrive_expect_tx(bars + kFull + st, kStage);
-        ptx::tma_load_2d(s, ma, kb * 128, at.x * kTile, bars + kFull + st);
-        ptx::tma_load_2d(s + kSlab, mb, kb * 128, n0, bars + kFull + st);
-        ptx::tma_load_2d(s + 2 * kSlab, mb, kb * 128, n1, bars + kFull + st);
+        const uint32_t bar = ptx::first_of_pair<2>(bars + kFull + st);
+        if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * kStage);  // the bytes of both CTAs
+        ptx::tma_load_2d_pair<2>(s, ma, kb * 128, (int)at.m0, bar);
+        ptx::tma_load_2d_pair<2>(s + kSlab, mb, kb * 128, nb, bar);
       }
       __syncwarp();
     }
   }
 out:
-  // after an abort, copies may still be in flight
-  if (lane == 0)
+  // after an abort, copies may still be in flight (those of a pair count on the first CTA's barriers)
+  if (lane == 0 && rank == 0)
     for (uint32_t j = n > kStages ? n - kStages : 0; j < n; ++j)
       bounded_drain(bars + kFull + j % kStages, (j / kStages) & 1, kWaitNs / 4);
   __syncwarp();
 }
 
+// The first CTA issues for both.
 __device__ __forceinline__ void issue(const ScaledArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem,
                                       volatile int* abort_flag) {
   const int tiles = a.tiles_m * a.tiles_n;
-  const uint32_t s0 = ptx::smem_u32(sm), idesc = ptx::idesc_e4m3_f32(kTile, kBN);
+  const uint32_t s0 = ptx::smem_u32(sm), idesc = ptx::idesc_e4m3_f32(2 * kTile, kBN);
   const bool el = ptx::elect_one();
   uint32_t n = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
     for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
       const int st = n % kStages;
       const uint32_t buf = n & 1;
@@ -205,16 +218,16 @@ __device__ __forceinline__ void issue(const ScaledArgs& a, uint8_t* sm, uint64_t
         const uint64_t db = ptx::smem_desc_sw128(s0 + st * kStage + kSlab, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          ptx::umma_f8(tmem + buf * kBN, ptx::smem_desc_at(da, 32 * k), ptx::smem_desc_at(db, 32 * k), idesc, k > 0);
-        ptx::umma_commit(bars + kEmpty + st);
-        ptx::umma_commit(bars + kAccFull + buf);
+          ptx::umma_pair<2, true>(tmem + buf * kBN, ptx::smem_desc_at(da, 32 * k), ptx::smem_desc_at(db, 32 * k), idesc, k > 0);
+        ptx::umma_commit_pair<2>(bars + kEmpty + st);
+        ptx::umma_commit_pair<2>(bars + kAccFull + buf);
       }
       __syncwarp();
     }
   }
 out:
   if (el) {
-    ptx::umma_commit(bars + kDone);
+    ptx::umma_commit_pair<2>(bars + kDone);
     bounded_drain(bars + kDone, 0, kWaitNs / 4);
   }
   __syncwarp();
@@ -224,24 +237,25 @@ out:
 // the 32 up columns that belong to them).
 template <bool GATED, int ACT>
 __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, float* s_top,
-                       int warp, int lane) {
+                       uint32_t rank, int warp, int lane) {
   const int tiles = a.tiles_m * a.tiles_n;
   const int quad = warp & 3, part = (warp - 2) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
+  const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
   uint32_t n = 0, it = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
-    const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
-    const long long row = (long long)at.x * kTile + quad * 32 + lane;
+  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, ++it) {
+    const Tile at = tile_at(a, t, rank);
+    const long long row = at.m0 + quad * 32 + lane;
     const bool in = row < a.M;
     const float* sa = a.a_scale + (in ? row : 0) * a.kblocks;
     // the scales of this thread's first and second 32 columns' block
-    const int nb = GATED ? at.y : 2 * at.y + (part >> 1);
+    const int nb = GATED ? at.n : 2 * at.n + (part >> 1);
     const bool nb_in = GATED || (long long)nb * 128 < a.N;
     const float* sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
     const float* sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
-    float acc[64];
+    f32x2 sums[32];
 #pragma unroll
-    for (int e = 0; e < 64; ++e) acc[e] = 0.f;
+    for (int e = 0; e < 32; ++e) sums[e] = 0ull;
     for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
       const float sk = in ? __ldg(sa + kb) : 0.f;
       const float f0 = sk * __ldg(sb0 + kb), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
@@ -252,13 +266,21 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       for (int c = 0; c < 4; ++c) {
         uint32_t r[16];
         ptx::tmem_ld16(lanes + buf * kBN + (GATED ? (c >> 1) * 128 + (c & 1) * 16 : c * 16), r);
-        const float f = GATED && c >= 2 ? f1 : f0;
+        const f32x2 f = GATED && c >= 2 ? pair_of(f1, f1) : pair_of(f0, f0);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[16 * c + e] = fmaf(__uint_as_float(r[e]), f, acc[16 * c + e]);
+        for (int e = 0; e < 8; ++e)
+          sums[8 * c + e] = fma_pairs(pair_of(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f, sums[8 * c + e]);
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty + buf);
+      if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
+    }
+    float acc[64];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float2 v = values_of(sums[e]);
+      acc[2 * e] = v.x;
+      acc[2 * e + 1] = v.y;
     }
     if constexpr (GATED) {
       float top = 0.f;
@@ -277,8 +299,8 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       float* s = s_top + (it & 1) * 512 + quad * 32 + lane;
       s[part * 128] = top;
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + kPairs);
-      if (!bounded_wait_warp(bars + kPairs, it & 1, abort_flag, a.status, kWaitNs)) return;
+      if (lane == 0) ptx::mbar_arrive(bars + kParts);
+      if (!bounded_wait_warp(bars + kParts, it & 1, abort_flag, a.status, kWaitNs)) return;
       top = fmaxf(fmaxf(s[0], s[128]), fmaxf(s[256], s[384]));
       float inv;
       const float scale = block_scale(top, inv);
@@ -287,12 +309,12 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           w[e] = pack_e4m3(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv, fine);
-        ptx::st_global_v8(static_cast<uint8_t*>(a.out) + row * a.N + at.y * 128 + part * 32, w[0], w[1], w[2], w[3], w[4],
+        ptx::st_global_v8(static_cast<uint8_t*>(a.out) + row * a.N + at.n * 128 + part * 32, w[0], w[1], w[2], w[3], w[4],
                           w[5], w[6], w[7]);
-        if (part == 0) a.out_scale[row * (a.N / 128) + at.y] = scale;
+        if (part == 0) a.out_scale[row * (a.N / 128) + at.n] = scale;
       }
     } else {
-      const int col0 = at.y * kBN + part * 64;
+      const int col0 = at.n * kBN + part * 64;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int col = col0 + 16 * c;
@@ -323,29 +345,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + kAccFull + i, 1);
-      ptx::mbar_init(bars + kAccEmpty + i, kEpiWarps);
+      ptx::mbar_init(bars + kAccEmpty + i, 2 * kEpiWarps);
     }
-    ptx::mbar_init(bars + kPairs, kEpiWarps);
+    ptx::mbar_init(bars + kParts, kEpiWarps);
     ptx::mbar_init(bars + kDone, 1);
     s_abort = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 1) {
-    ptx::tmem_alloc(&tmem_slot, kTmem);
-    ptx::tmem_relinquish();
-  }
+  if (warp == 1) ptx::tmem_alloc_pair<2>(&tmem_slot, kTmem);
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::pair_sync<2>();  // both CTAs' barriers are there
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, lane);
-  else if (warp == 1) issue(a, sm, bars, tmem, abort_flag);
-  else finish<GATED, ACT>(a, bars, tmem, abort_flag, s_top, warp, lane);
+  const uint32_t tmem = tmem_slot, rank = ptx::pair_rank<2>();
+  if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, rank, lane);
+  else if (warp == 1 && rank == 0) issue(a, sm, bars, tmem, abort_flag);
+  else if (warp > 1) finish<GATED, ACT>(a, bars, tmem, abort_flag, s_top, rank, warp, lane);
   ptx::tc_fence_before();
   __syncthreads();
+  // nothing of one CTA's reaches into the other any more, the last commit too
+  if (warp == 1 && rank == 1 && lane == 0) bounded_drain(bars + kDone, 0, kWaitNs / 4);
+  __syncwarp();
+  ptx::pair_sync<2>();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, kTmem);
+    ptx::tmem_dealloc_pair<2>(tmem, kTmem);
   }
 }
 
@@ -355,11 +379,10 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int 
   const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED, ACT>, kDynamic);
   if (e != cudaSuccess) return e;
   const int tn = GATED ? kBN / 2 : kBN;
-  a.tiles_m = (a.M + kTile - 1) / kTile;
+  a.tiles_m = (a.M + 2 * kTile - 1) / (2 * kTile);
   a.tiles_n = (a.N + tn - 1) / tn;
-  const int tiles = a.tiles_m * a.tiles_n;
-  k_scaled<GATED, ACT><<<tiles < num_sms ? tiles : num_sms, kThreads, kDynamic, st>>>(ma, mb, a);
-  return cudaGetLastError();
+  const int tiles = a.tiles_m * a.tiles_n, places = num_sms / 2;
+  return launch_pairs(2, false, k_scaled<GATED, ACT>, (tiles < places ? tiles : places) * 2, kThreads, kDynamic, st, ma, mb, a);
 }
 
 }  // namespace
