@@ -20,6 +20,12 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// Registers a thread of this warpgroup gives up or takes on (the block keeps what it was launched with).
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // A kernel launched with the programmatic attribute may start before its predecessor ends (once all of
 // that one's blocks have said successor_may_start); what it reads of the predecessor's stands behind
 // predecessor_done.

@@ -153,7 +153,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBN = 256;                     // columns of B a tile
 constexpr int kSlab = 128 * 128;             // 128 rows of a block: 128 bytes each
 constexpr int kStage = 2 * kSlab, kStages = 6;  // a CTA's 128 rows of A and its half of B's 256
-constexpr int kEpiWarps = 16, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiWarps = 16, kThreads = 128 + 32 * kEpiWarps;
+// Registers a thread: what the block is launched with, and then of the loading and issuing warpgroup and
+// of the four that hold sums (64 of them, and the 32 that are being taken up).
+constexpr int kRegs = 96, kFewRegs = 32, kSumRegs = 112;
+static_assert(128 * kFewRegs + 32 * kEpiWarps * kSumRegs <= kThreads * kRegs, "the split is the block's own");
 constexpr int kDynamic = kStages * kStage + 1024;
 constexpr uint32_t kTmem = 512;               // two buffers of a block's sums
 
@@ -239,7 +243,7 @@ template <bool GATED, int ACT>
 __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, float* s_top,
                        uint32_t rank, int warp, int lane) {
   const int tiles = a.tiles_m * a.tiles_n;
-  const int quad = warp & 3, part = (warp - 2) >> 2;
+  const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
   const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
   uint32_t n = 0, it = 0;
@@ -263,13 +267,13 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       if (!bounded_wait_warp(bars + kAccFull + buf, (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
       ptx::tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[16];
-        ptx::tmem_ld16(lanes + buf * kBN + (GATED ? (c >> 1) * 128 + (c & 1) * 16 : c * 16), r);
-        const f32x2 f = GATED && c >= 2 ? pair_of(f1, f1) : pair_of(f0, f0);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32];
+        ptx::tmem_ld32(lanes + buf * kBN + c * (GATED ? 128 : 32), r);
+        const f32x2 f = GATED && c ? pair_of(f1, f1) : pair_of(f0, f0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          sums[8 * c + e] = fma_pairs(pair_of(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f, sums[8 * c + e]);
+        for (int e = 0; e < 16; ++e)
+          sums[16 * c + e] = fma_pairs(pair_of(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f, sums[16 * c + e]);
       }
       ptx::tc_fence_before();
       __syncwarp();
@@ -358,9 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::pair_sync<2>();  // both CTAs' barriers are there
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot, rank = ptx::pair_rank<2>();
-  if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, rank, lane);
-  else if (warp == 1 && rank == 0) issue(a, sm, bars, tmem, abort_flag);
-  else if (warp > 1) finish<GATED, ACT>(a, bars, tmem, abort_flag, s_top, rank, warp, lane);
+  if (warp < 4) {
+    ptx::fewer_registers<kFewRegs>();
+    if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, rank, lane);
+    else if (warp == 1 && rank == 0) issue(a, sm, bars, tmem, abort_flag);
+  } else {
+    ptx::more_registers<kSumRegs>();
+    finish<GATED, ACT>(a, bars, tmem, abort_flag, s_top, rank, warp, lane);
+  }
   ptx::tc_fence_before();
   __syncthreads();
   // nothing of one CTA's reaches into the other any more, the last commit too
@@ -379,6 +388,13 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int 
   const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED, ACT>, kDynamic);
   if (e != cudaSuccess) return e;
   const int tn = GATED ? kBN / 2 : kBN;
+  // (a block launched with fewer registers than the split counts on would wait for them forever)
+  static const int regs = [] {
+    cudaFuncAttributes at{};
+    const OutsideCapture now;
+    return cudaFuncGetAttributes(&at, k_scaled<GATED, ACT>) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs != kRegs) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + 2 * kTile - 1) / (2 * kTile);
   a.tiles_n = (a.N + tn - 1) / tn;
   const int tiles = a.tiles_m * a.tiles_n, places = num_sms / 2;
