@@ -237,6 +237,13 @@ out:
   __syncwarp();
 }
 
+// A row's scales of four blocks (n are left): every thread of a warp reads another row, 32 sectors, so they
+// are read together.
+__device__ __forceinline__ float4 next_scales(const float* s, int n, bool aligned) {
+  if (aligned) return __ldg(reinterpret_cast<const float4*>(s));
+  return make_float4(__ldg(s), n > 1 ? __ldg(s + 1) : 0.f, n > 2 ? __ldg(s + 2) : 0.f, n > 3 ? __ldg(s + 3) : 0.f);
+}
+
 // Sixteen warps: a thread has one row and a quarter of the tile's columns (gated: 32 gate columns and
 // the 32 up columns that belong to them).
 template <bool GATED, int ACT>
@@ -246,6 +253,7 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
   const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
+  const bool aligned = (a.kblocks & 3) == 0;  // (a.a_scale is on a 16-byte boundary)
   uint32_t n = 0, it = 0;
   for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, ++it) {
     const Tile at = tile_at(a, t, rank);
@@ -257,11 +265,13 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
     const bool nb_in = GATED || (long long)nb * 128 < a.N;
     const float* sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
     const float* sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
+    float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
     f32x2 sums[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) sums[e] = 0ull;
     for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
-      const float sk = in ? __ldg(sa + kb) : 0.f;
+      if ((kb & 3) == 0) s4 = next_scales(sa + kb, a.kblocks - kb, aligned);
+      const float sk = (kb & 2) ? (kb & 1 ? s4.w : s4.z) : (kb & 1 ? s4.y : s4.x);
       const float f0 = sk * __ldg(sb0 + kb), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
       const uint32_t buf = n & 1;
       if (!bounded_wait_warp(bars + kAccFull + buf, (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
@@ -270,14 +280,16 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       for (int c = 0; c < 2; ++c) {
         uint32_t r[32];
         ptx::tmem_ld32(lanes + buf * kBN + c * (GATED ? 128 : 32), r);
+        if (c == 1) {  // the buffer goes back before its last columns are added
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
+        }
         const f32x2 f = GATED && c ? pair_of(f1, f1) : pair_of(f0, f0);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           sums[16 * c + e] = fma_pairs(pair_of(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f, sums[16 * c + e]);
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
     }
     float acc[64];
 #pragma unroll
