@@ -43,7 +43,12 @@ struct Dense32Args {
   DenseArgs d;          // out: float rows (kOut, kDx, kDw); part as for kDw, of any of the three
   Planes h, p;          // what kGlu and kDglu write
 };
-cudaError_t launch_split(const float* x, const Planes& to, cudaStream_t st);
+struct SplitList {
+  int n;                // matrices, up to four
+  const void* x[4];     // fp32 rows
+  Planes to[4];
+};
+cudaError_t launch_split(const SplitList& l, cudaStream_t st);
 bool encode_planes(CUtensorMap* m, const Planes& a);
 cudaError_t launch_dense32(DenseOp op, const CUtensorMap (&maps)[4], Dense32Args a, int num_sms, cudaStream_t st);
 int dense32_splits(int M, int N, int kblocks, int num_sms);

@@ -6,8 +6,9 @@
 // The tensor cores cut each addition's result off (measured: 2^-24 of the sum for each 16 products,
 // always towards zero), so they sum no more than a block of 64; eight warps add the blocks up in
 // fp32 registers, rounded to nearest.
-// Tiles are 128 x 128 (gated: 64 gate and 64 up columns; the backward's dh 64), a ring of two
-// 64-deep stages holds all six planes, so each is loaded once.  h and p are written as planes.
+// A pair of CTAs has a tile of 256 x 128 (gated: 64 gate and 64 up columns; the backward's dh 64); a
+// ring of three 64-deep stages holds all six planes, so each is loaded once.  h and p are written as
+// planes.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -25,13 +26,13 @@ namespace {
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBK = 64, kSlab = 64 * 128;    // 64 rows of 128 bytes
 constexpr int kPlane = 2 * kSlab;            // 128 rows of one plane
-constexpr int kStage = 6 * kPlane, kStages = 2;
+constexpr int kStage = 3 * (kPlane + kSlab), kStages = 3;  // 128 rows of A and this CTA's 64 of B
 constexpr int kThreads = 320, kEpiWarps = 8;
 constexpr int kDynamic = kStages * kStage + 1024;
 constexpr uint32_t kTmem = 256;              // two buffers of a block's sums
 constexpr int kTileN = 128;
 
-enum { kFull = 0, kEmpty = 2, kAccFull = 4, kAccEmpty = 6, kDone = 8, kBars = 9 };
+enum { kFull = 0, kEmpty = 3, kAccFull = 6, kAccEmpty = 8, kDone = 10, kBars = 11 };
 
 template <DenseOp OP>
 struct Cfg {
@@ -43,13 +44,14 @@ struct Cfg {
 struct Unit {
   int m0, n0, kb0, kb1, split;
 };
+// Work of pair i; m0: this CTA's first row.
 template <int TN>
-__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i) {
+__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i, uint32_t rank) {
   const int tiles = a.tiles_m * a.tiles_n;
   Unit u;
   u.split = i / tiles;
   const int2 at = band_tile(i - u.split * tiles, a.tiles_m, a.tiles_n);
-  u.m0 = at.x * kTile;
+  u.m0 = (2 * at.x + (int)rank) * kTile;
   u.n0 = at.y * TN;
   u.kb0 = (int)((long long)a.kblocks * u.split / a.splits);
   u.kb1 = (int)((long long)a.kblocks * (u.split + 1) / a.splits);
@@ -58,40 +60,41 @@ __device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i) {
 
 // 64 rows (columns) of one plane at mn0, block kb of the summed axis.
 template <bool MN>
-__device__ __forceinline__ void load_slab(uint8_t* dst, const CUtensorMap* map, int mn0, int kb, int plane, uint64_t* bar) {
-  if (MN) ptx::tma_load_3d(dst, map, mn0, kb * kBK, plane, bar);
-  else ptx::tma_load_3d(dst, map, kb * kBK, mn0, plane, bar);
+__device__ __forceinline__ void load_slab(uint8_t* dst, const CUtensorMap* map, int mn0, int kb, int plane, uint32_t bar) {
+  if (MN) ptx::tma_load_3d_pair(dst, map, mn0, kb * kBK, plane, bar);
+  else ptx::tma_load_3d_pair(dst, map, kb * kBK, mn0, plane, bar);
 }
 
 template <DenseOp OP>
 __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* ma2,
-                        const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, int lane) {
+                        const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, uint32_t rank, int lane) {
   using C = Cfg<OP>;
   const int units = a.tiles_m * a.tiles_n * a.splits;
   uint32_t n = 0;
-  for (int i = blockIdx.x; i < units; i += gridDim.x) {
-    const Unit u = unit_at<C::kCols>(a, i);
+  for (int i = blockIdx.x / 2; i < units; i += gridDim.x / 2) {
+    const Unit u = unit_at<C::kCols>(a, i, rank);
     const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
     for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
       if (!bounded_wait_warp(bars + kEmpty + st, ((n / kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (ptx::elect_one()) {
         uint8_t* s = sm + st * kStage;
-        uint64_t* bar = bars + kFull + st;
+        const uint32_t bar = ptx::first_of_pair<2>(bars + kFull + st);
         const bool grad = OP == DenseOp::kDglu && kb < 0;
-        ptx::mbar_arrive_expect_tx(bar, grad ? 9 * kSlab : kStage);
+        // (the first CTA's barrier counts the bytes of both; dh has 64 columns, 32 rows of B from each)
+        if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * kStage);
+        const int nb = C::kPair ? (rank ? a.N : 0) + u.n0 : u.n0 + 64 * (int)rank;  // gated: the gate's rows, up's
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-          uint8_t *sa = s + p * kPlane, *sb = s + (3 + p) * kPlane;
+          uint8_t *sa = s + p * kPlane, *sb = s + 3 * kPlane + p * kSlab;
           if (grad) {
             load_slab<false>(sa, ma2, u.m0, kb + first, p, bar);
             load_slab<false>(sa + kSlab, ma2, u.m0 + 64, kb + first, p, bar);
-            load_slab<true>(sb, mb2, u.n0, kb + first, p, bar);
+            load_slab<true>(sb, mb2, u.n0 + 32 * (int)rank, kb + first, p, bar);
           } else {
             load_slab<C::kAMn>(sa, ma, u.m0, kb, p, bar);
             load_slab<C::kAMn>(sa + kSlab, ma, u.m0 + 64, kb, p, bar);
-            load_slab<C::kBMn>(sb, mb, u.n0, kb, p, bar);
-            load_slab<C::kBMn>(sb + kSlab, mb, C::kPair ? a.N + u.n0 : u.n0 + 64, kb, p, bar);
+            load_slab<C::kBMn>(sb, mb, nb, kb, p, bar);
           }
         }
       }
@@ -99,8 +102,8 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
     }
   }
 out:
-  // after an abort, copies may still be in flight
-  if (lane == 0)
+  // after an abort, copies may still be in flight (those of a pair count on the first CTA's barriers)
+  if (lane == 0 && rank == 0)
     for (uint32_t j = n > kStages ? n - kStages : 0; j < n; ++j)
       bounded_drain(bars + kFull + j % kStages, (j / kStages) & 1, kWaitNs / 4);
   __syncwarp();
@@ -109,7 +112,7 @@ out:
 // The six pairs of a stage's planes into one buffer.
 template <bool AMN, bool BMN, int N>
 __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s) {
-  const uint32_t idesc = ptx::idesc_bf16_f32(kTile, N, AMN, BMN);
+  const uint32_t idesc = ptx::idesc_bf16_f32(2 * kTile, N, AMN, BMN);
   const uint64_t da = ptx::smem_desc_sw128(s, AMN ? kSlab : 16, 1024);
   const uint64_t db = ptx::smem_desc_sw128(s + 3 * kPlane, BMN ? kSlab : 16, 1024);
   constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};
@@ -117,8 +120,8 @@ __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s) {
   for (int j = 0; j < 6; ++j)
 #pragma unroll
     for (int k = 0; k < kBK / 16; ++k)
-      ptx::umma_f16(acc, ptx::smem_desc_at(da, kA[j] * kPlane + k * (AMN ? 2048 : 32)),
-                    ptx::smem_desc_at(db, kB[j] * kPlane + k * (BMN ? 2048 : 32)), idesc, j + k > 0);
+      ptx::umma_pair<2, false>(acc, ptx::smem_desc_at(da, kA[j] * kPlane + k * (AMN ? 2048 : 32)),
+                               ptx::smem_desc_at(db, kB[j] * kSlab + k * (BMN ? 2048 : 32)), idesc, j + k > 0);
 }
 
 template <DenseOp OP>
@@ -127,9 +130,10 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
   const int units = a.tiles_m * a.tiles_n * a.splits;
   const uint32_t s0 = ptx::smem_u32(sm);
   const bool el = ptx::elect_one();
+  constexpr uint32_t rank = 0;  // the first CTA issues for both
   uint32_t n = 0;
-  for (int i = blockIdx.x; i < units; i += gridDim.x) {
-    const Unit u = unit_at<C::kCols>(a, i);
+  for (int i = blockIdx.x / 2; i < units; i += gridDim.x / 2) {
+    const Unit u = unit_at<C::kCols>(a, i, rank);
     for (int kb = OP == DenseOp::kDglu ? -a.kblocks : u.kb0; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
       const uint32_t buf = n & 1;
@@ -139,15 +143,15 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
       if (el) {
         if (OP == DenseOp::kDglu && kb < 0) block_mma<false, true, 64>(tmem + buf * kTileN, s0 + st * kStage);
         else block_mma<C::kAMn, C::kBMn, kTileN>(tmem + buf * kTileN, s0 + st * kStage);
-        ptx::umma_commit(bars + kEmpty + st);
-        ptx::umma_commit(bars + kAccFull + buf);
+        ptx::umma_commit_pair<2>(bars + kEmpty + st);
+        ptx::umma_commit_pair<2>(bars + kAccFull + buf);
       }
       __syncwarp();
     }
   }
 out:
   if (el) {
-    ptx::umma_commit(bars + kDone);
+    ptx::umma_commit_pair<2>(bars + kDone);
     bounded_drain(bars + kDone, 0, kWaitNs / 4);
   }
   __syncwarp();
@@ -176,13 +180,15 @@ __device__ __forceinline__ void store_planes(const Planes& to, long long row, in
 }
 
 template <DenseOp OP, int ACT>
-__device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, int warp, int lane) {
+__device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, uint32_t rank, int warp,
+                       int lane) {
   using C = Cfg<OP>;
   const DenseArgs& a = aa.d;
   const int units = a.tiles_m * a.tiles_n * a.splits;
   const int quad = warp & 3, half = (warp - 2) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   const int c0 = C::kPair ? 32 * half : 64 * half, c1 = C::kPair ? 64 + 32 * half : 64 * half + 32;
+  const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
   uint32_t n = 0;
   // a block's sums of 32 columns, added up
   const auto take = [&](float (&to)[32], uint32_t buf, int col) {
@@ -194,10 +200,10 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
   const auto taken = [&](uint32_t buf) {
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bars + kAccEmpty + buf);
+    if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
   };
-  for (int i = blockIdx.x; i < units; i += gridDim.x) {
-    const Unit u = unit_at<C::kCols>(a, i);
+  for (int i = blockIdx.x / 2; i < units; i += gridDim.x / 2) {
+    const Unit u = unit_at<C::kCols>(a, i, rank);
     float x0[32], x1[32], dh[OP == DenseOp::kDglu ? 32 : 1];
 #pragma unroll
     for (int e = 0; e < 32; ++e) x0[e] = x1[e] = 0.f;
@@ -273,38 +279,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + kAccFull + i, 1);
-      ptx::mbar_init(bars + kAccEmpty + i, kEpiWarps);
+      ptx::mbar_init(bars + kAccEmpty + i, 2 * kEpiWarps);
     }
     ptx::mbar_init(bars + kDone, 1);
     s_abort = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 1) {
-    ptx::tmem_alloc(&tmem_slot, kTmem);
-    ptx::tmem_relinquish();
-  }
+  if (warp == 1) ptx::tmem_alloc_pair<2>(&tmem_slot, kTmem);
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::pair_sync<2>();  // both CTAs' barriers are there
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  if (warp == 0) produce<OP>(a.d, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, lane);
-  else if (warp == 1) issue<OP>(a.d, sm, bars, tmem, abort_flag);
-  else finish<OP, ACT>(a, bars, tmem, abort_flag, warp, lane);
+  const uint32_t tmem = tmem_slot, rank = ptx::pair_rank<2>();
+  if (warp == 0) produce<OP>(a.d, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
+  else if (warp == 1 && rank == 0) issue<OP>(a.d, sm, bars, tmem, abort_flag);
+  else if (warp > 1) finish<OP, ACT>(a, bars, tmem, abort_flag, rank, warp, lane);
   ptx::tc_fence_before();
   __syncthreads();
+  // nothing of one CTA's reaches into the other any more, the last commit too
+  if (warp == 1 && rank == 1 && lane == 0) bounded_drain(bars + kDone, 0, kWaitNs / 4);
+  __syncwarp();
+  ptx::pair_sync<2>();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, kTmem);
+    ptx::tmem_dealloc_pair<2>(tmem, kTmem);
   }
 }
 
-__global__ void __launch_bounds__(256) k_split(const float* x, Planes to) {
+// The planes of up to four matrices in one launch; first[i]: matrix i's first block.
+struct SplitArgs {
+  const float* x[4];
+  Planes to[4];
+  int first[5];
+};
+constexpr int kSplitRun = 4;  // float4s a thread
+__global__ void __launch_bounds__(256) k_split(const SplitArgs a) {
+  int m = 0;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m += (int)blockIdx.x >= a.first[i];
+  const Planes to = a.to[m];
+  const float4* const x = reinterpret_cast<const float4*>(a.x[m]);
   const int per_row = (int)(to.cols / 4);
-  const long long n = to.rows * per_row;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(x) + i);
-    const long long row = i / per_row;
-    store_planes(to, row, 4 * (int)(i - row * per_row), v.x, v.y, v.z, v.w);
+  const long long n = to.rows * per_row, i0 = (long long)((int)blockIdx.x - a.first[m]) * (256 * kSplitRun) + threadIdx.x;
+  float4 v[kSplitRun];
+#pragma unroll
+  for (int k = 0; k < kSplitRun; ++k)
+    if (i0 + 256 * k < n) v[k] = __ldcs(x + i0 + 256 * k);
+#pragma unroll
+  for (int k = 0; k < kSplitRun; ++k) {
+    const long long i = i0 + 256 * k;
+    if (i >= n) break;
+    const long long row = n >> 32 ? i / per_row : (long long)((uint32_t)i / (uint32_t)per_row);
+    store_planes(to, row, 4 * (int)(i - row * per_row), v[k].x, v[k].y, v[k].z, v[k].w);
   }
 }
 
@@ -313,25 +339,35 @@ cudaError_t run(const CUtensorMap (&m)[4], Dense32Args a, int num_sms, cudaStrea
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(done, (const void*)k_dense32<OP, ACT>, kDynamic);
   if (e != cudaSuccess) return e;
-  a.d.tiles_m = (a.d.M + kTile - 1) / kTile;
+  a.d.tiles_m = (a.d.M + 2 * kTile - 1) / (2 * kTile);
   a.d.tiles_n = (a.d.N + Cfg<OP>::kCols - 1) / Cfg<OP>::kCols;
-  const int units = a.d.tiles_m * a.d.tiles_n * a.d.splits;
-  k_dense32<OP, ACT><<<units < num_sms ? units : num_sms, kThreads, kDynamic, st>>>(m[0], m[1], m[2], m[3], a);
-  return cudaGetLastError();
+  const int units = a.d.tiles_m * a.d.tiles_n * a.d.splits, places = num_sms / 2;
+  return launch_pairs(2, false, k_dense32<OP, ACT>, (units < places ? units : places) * 2, kThreads, kDynamic, st, m[0], m[1],
+                      m[2], m[3], a);
 }
 
 }  // namespace
 
-cudaError_t launch_split(const float* x, const Planes& to, cudaStream_t st) {
-  const long long blocks = (to.rows * (to.cols / 4) + 255) / 256;
-  k_split<<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, st>>>(x, to);
+cudaError_t launch_split(const SplitList& l, cudaStream_t st) {
+  SplitArgs a{};
+  long long blocks = 0;
+  for (int i = 0; i < 4; ++i) {
+    a.first[i] = (int)blocks;
+    if (i >= l.n) continue;
+    a.x[i] = static_cast<const float*>(l.x[i]);
+    a.to[i] = l.to[i];
+    blocks += (l.to[i].rows * (l.to[i].cols / 4) + 256 * kSplitRun - 1) / (256 * kSplitRun);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  }
+  for (int i = l.n; i < 5; ++i) a.first[i] = INT32_MAX;
+  k_split<<<(unsigned)blocks, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-// Parts of the summed axis that give every SM work: each at least four blocks deep.
+// Parts of the summed axis that give every pair of SMs work: each at least four blocks deep.
 int dense32_splits(int M, int N, int kblocks, int num_sms) {
-  const long long tiles = (long long)((M + kTile - 1) / kTile) * ((N + kTileN - 1) / kTileN);
-  long long s = num_sms / tiles;
+  const long long tiles = (long long)((M + 2 * kTile - 1) / (2 * kTile)) * ((N + kTileN - 1) / kTileN);
+  long long s = num_sms / 2 / tiles;
   if (s > kblocks / 4) s = kblocks / 4;
   return s < 1 ? 1 : (int)s;
 }

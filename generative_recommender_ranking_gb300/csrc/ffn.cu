@@ -137,9 +137,7 @@ cudaError_t ffn32_fwd(int act, long long R, long long W, long long H, const void
   cudaError_t e = ws.take(dev, off_part + (s > 1 ? (size_t)s * R * W * 4 : 0));
   if (e != cudaSuccess) return e;
   px = placed(px, ws), pi = placed(pi, ws), po = placed(po, ws), ph = placed(ph, ws);
-  e = launch_split(static_cast<const float*>(x), px, st);
-  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_in), pi, st);
-  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_out), po, st);
+  e = launch_split({3, {x, w_in, w_out}, {px, pi, po}}, st);
   CUtensorMap m[4];
   if (e == cudaSuccess && !(encode_planes(&m[0], px) && encode_planes(&m[1], pi))) e = cudaErrorInvalidValue;
   Dense32Args d{};
@@ -173,10 +171,7 @@ cudaError_t ffn32_bwd(int act, long long R, long long W, long long H, const void
   if (e != cudaSuccess) return e;
   px = placed(px, ws), pdy = placed(pdy, ws), pi = placed(pi, ws), po = placed(po, ws), ph = placed(ph, ws), pp = placed(pp, ws);
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws.p) + off_part);
-  e = launch_split(static_cast<const float*>(x), px, st);
-  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(dy), pdy, st);
-  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_in), pi, st);
-  if (e == cudaSuccess) e = launch_split(static_cast<const float*>(w_out), po, st);
+  e = launch_split({4, {x, w_in, w_out, dy}, {px, pi, po, pdy}}, st);
   CUtensorMap m[4];
   if (e == cudaSuccess &&
       !(encode_planes(&m[0], px) && encode_planes(&m[1], pi) && encode_planes(&m[2], pdy) && encode_planes(&m[3], po)))
