@@ -23,6 +23,7 @@ struct DenseArgs {
   int tiles_m, tiles_n, splits;
   int act;              // rec_attn_activation
   int wide;             // the outputs' rows start on 32-byte boundaries
+  int follows;          // behind a kernel of the same call: launched before that one has ended
   void* out;            // kGlu: h; kOut, kDx: the result; kDglu: p; kDw: the result (one split)
   void* out2;           // kDglu: h
   float* part;          // kDw: [splits][M][N] sums of parts (more than one split)
@@ -55,6 +56,7 @@ int dense32_splits(int M, int N, int kblocks, int num_sms);
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&maps)[4], DenseArgs a, int num_sms, cudaStream_t st);
 // kDw: parts of the summed axis.
 int dense_splits(int M, int N, int kblocks, int num_sms);
+// (launched behind the kernel that wrote the parts, before that one has ended)
 cudaError_t launch_dense_sum(const float* part, void* out, long long n, int splits, int dtype, cudaStream_t st);
 
 }  // namespace recattn

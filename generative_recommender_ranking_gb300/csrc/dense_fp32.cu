@@ -178,6 +178,32 @@ __device__ __forceinline__ void store_planes(const Planes& to, long long row, in
   for (int p = 0; p < 3; ++p, at += to.plane())
     *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(v[p][0], v[p][1]), pack_bf16(v[p][2], v[p][3]));
 }
+// 32 columns, `left` of which there are; wide: from a 32-byte boundary on (whole sectors are written: four
+// columns at a time took three times the traffic).
+__device__ __forceinline__ void store_planes(const Planes& to, long long row, int col, const float (&x)[32], int left, bool wide) {
+  if (wide && left >= 32) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 16) {
+      uint32_t w[3][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float a[3], b[3];
+        split3(x[c + 2 * e], a[0], a[1], a[2]);
+        split3(x[c + 2 * e + 1], b[0], b[1], b[2]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) w[p][e] = pack_bf16(a[p], b[p]);
+      }
+      char* at = static_cast<char*>(to.p) + (row * to.ld + col + c) * 2;
+#pragma unroll
+      for (int p = 0; p < 3; ++p, at += to.plane())
+        ptx::st_global_v8(at, w[p][0], w[p][1], w[p][2], w[p][3], w[p][4], w[p][5], w[p][6], w[p][7]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; c += 4)
+      if (c < left) store_planes(to, row, col + c, x[c], x[c + 1], x[c + 2], x[c + 3]);
+  }
+}
 
 template <DenseOp OP, int ACT>
 __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, uint32_t rank, int warp,
@@ -227,25 +253,24 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
     const long long row = u.m0 + quad * 32 + lane;
     if (row >= a.M) continue;
     if constexpr (C::kPair) {
-      const int col = u.n0 + 32 * half;
+      // in place: x0 becomes du, x1 h and dh dg
+      const int col = u.n0 + 32 * half, left = a.N - col;
+      const bool wide = a.N % 16 == 0;
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        float h[4], dg[4], du[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float slope;
-          const float act = act32<ACT>(x0[e + k], slope);
-          h[k] = act * x1[e + k];
-          if constexpr (OP == DenseOp::kDglu) {
-            dg[k] = dh[e + k] * x1[e + k] * slope;
-            du[k] = dh[e + k] * act;
-          }
-        }
-        if (col + e >= a.N) break;
-        store_planes(aa.h, row, col + e, h[0], h[1], h[2], h[3]);
+      for (int e = 0; e < 32; ++e) {
+        float slope;
+        const float act = act32<ACT>(x0[e], slope), up = x1[e];
+        x1[e] = act * up;
         if constexpr (OP == DenseOp::kDglu) {
-          store_planes(aa.p, row, col + e, dg[0], dg[1], dg[2], dg[3]);
-          store_planes(aa.p, row, a.N + col + e, du[0], du[1], du[2], du[3]);
+          x0[e] = dh[e] * act;
+          dh[e] = dh[e] * up * slope;
+        }
+      }
+      if (left > 0) {
+        store_planes(aa.h, row, col, x1, left, wide);
+        if constexpr (OP == DenseOp::kDglu) {
+          store_planes(aa.p, row, col, dh, left, wide);
+          store_planes(aa.p, row, a.N + col, x0, left, wide);
         }
       }
     } else {
@@ -291,6 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::pair_sync<2>();  // both CTAs' barriers are there
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot, rank = ptx::pair_rank<2>();
+  ptx::successor_may_start();
+  ptx::predecessor_done();
   if (warp == 0) produce<OP>(a.d, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
   else if (warp == 1 && rank == 0) issue<OP>(a.d, sm, bars, tmem, abort_flag);
   else if (warp > 1) finish<OP, ACT>(a, bars, tmem, abort_flag, rank, warp, lane);
@@ -314,6 +341,7 @@ struct SplitArgs {
 };
 constexpr int kSplitRun = 4;  // float4s a thread
 __global__ void __launch_bounds__(256) k_split(const SplitArgs a) {
+  ptx::successor_may_start();
   int m = 0;
 #pragma unroll
   for (int i = 1; i < 4; ++i) m += (int)blockIdx.x >= a.first[i];
@@ -342,7 +370,7 @@ cudaError_t run(const CUtensorMap (&m)[4], Dense32Args a, int num_sms, cudaStrea
   a.d.tiles_m = (a.d.M + 2 * kTile - 1) / (2 * kTile);
   a.d.tiles_n = (a.d.N + Cfg<OP>::kCols - 1) / Cfg<OP>::kCols;
   const int units = a.d.tiles_m * a.d.tiles_n * a.d.splits, places = num_sms / 2;
-  return launch_pairs(2, false, k_dense32<OP, ACT>, (units < places ? units : places) * 2, kThreads, kDynamic, st, m[0], m[1],
+  return launch_pairs(2, true, k_dense32<OP, ACT>, (units < places ? units : places) * 2, kThreads, kDynamic, st, m[0], m[1],
                       m[2], m[3], a);
 }
 

@@ -318,6 +318,8 @@ __global__ void __launch_bounds__(Cfg<OP, BN, CG>::kThreads, 1)
   if (CG == 2) ptx::pair_sync<CG>();  // both CTAs' barriers are there
   ptx::tc_fence_after();
   const uint32_t rank = ptx::pair_rank<CG>();
+  ptx::successor_may_start();
+  if (a.follows) ptx::predecessor_done();
   const uint32_t tmem = tmem_slot;
   if (warp == 0) produce<OP, BN, CG>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
   else if (warp == 1 && rank == 0) issue<OP, BN, CG>(a, sm, bars, tmem, abort_flag);
@@ -339,6 +341,8 @@ __global__ void __launch_bounds__(Cfg<OP, BN, CG>::kThreads, 1)
 template <bool BF16>
 __global__ void k_dense_sum(const float* part, void* out, long long n, int splits) {
   const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  ptx::successor_may_start();
+  ptx::predecessor_done();
   if (i >= n) return;
   float4 s = *reinterpret_cast<const float4*>(part + i);
   for (int k = 1; k < splits; ++k) {
@@ -359,7 +363,7 @@ cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;
   const int places = num_sms / CG;
-  return launch_pairs(CG, false, k_dense<OP, BN, CG, ACT>, (int)(units < places ? units : places) * CG, C::kThreads, C::kDynamic,
+  return launch_pairs(CG, a.follows != 0, k_dense<OP, BN, CG, ACT>, (int)(units < places ? units : places) * CG, C::kThreads, C::kDynamic,
                       st, m[0], m[1], m[2], m[3], a);
 }
 
@@ -402,9 +406,8 @@ int dense_splits(int M, int N, int kblocks, int num_sms) {
 
 cudaError_t launch_dense_sum(const float* part, void* out, long long n, int splits, int dtype, cudaStream_t st) {
   const unsigned blocks = (unsigned)((n / 4 + 255) / 256);
-  if (dtype == REC_ATTN_BF16) k_dense_sum<true><<<blocks, 256, 0, st>>>(part, out, n, splits);
-  else k_dense_sum<false><<<blocks, 256, 0, st>>>(part, out, n, splits);
-  return cudaGetLastError();
+  return launch_pairs(1, true, dtype == REC_ATTN_BF16 ? k_dense_sum<true> : k_dense_sum<false>, (int)blocks, 256, 0, st, part,
+                      out, n, splits);
 }
 
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {

@@ -72,7 +72,7 @@ cudaError_t dense(DenseOp op, const DenseArgs& a, int sms, cudaStream_t st, bool
 struct PlaneLayout {
   size_t bytes = 0;
   Planes add(long long rows, long long cols) {  // p: the offset, until the workspace is there
-    Planes a{reinterpret_cast<void*>(bytes), rows, cols, (cols + 7) / 8 * 8};
+    Planes a{reinterpret_cast<void*>(bytes), rows, cols, (cols + 15) / 16 * 16};  // rows of whole 32-byte sectors
     bytes += ws_up(3 * a.plane());
     return a;
   }
@@ -234,6 +234,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
   a.kblocks = blocks64(hidden);
   a.out = y;
   a.wide = wide_rows(y, width);
+  a.follows = 1;
   if (e == cudaSuccess)
     e = dense(DenseOp::kOut, a, sms, st,
               encode_dense(&m[0], ws.p, rows, hidden) && encode_dense(&m[1], w_out, width, hidden), m);
@@ -291,6 +292,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
             encode_dense(&m[0], x, rows, width) && encode_dense(&m[1], w_in, 2 * hidden, width) &&
                 encode_dense(&m[2], dy, rows, width) && encode_dense(&m[3], w_out, width, hidden),
             m);
+  a.follows = 1;
   if (e == cudaSuccess && dx) {
     a.N = W;
     a.kblocks = blocks64(2 * hidden);
@@ -328,7 +330,7 @@ bool scaled_tiles_ok(long long rows, long long cols) {  // a launch's tiles are 
 
 // The product of one scaled layer.
 cudaError_t scaled(bool gated, const void* a, const float* a_scale, long long rows, const void* b, const float* b_scale,
-                   long long cols, long long depth, int act, void* out, float* out_scale, int sms, cudaStream_t st) {
+                   long long cols, long long depth, int act, void* out, float* out_scale, bool follows, int sms, cudaStream_t st) {
   CUtensorMap ma, mb;
   if (!encode_scaled(&ma, a, rows, depth) || !encode_scaled(&mb, b, gated ? 2 * cols : cols, depth))
     return cudaErrorInvalidValue;
@@ -342,6 +344,7 @@ cudaError_t scaled(bool gated, const void* a, const float* a_scale, long long ro
   s.wide = wide_rows(out, cols);
   s.out = out;
   s.out_scale = out_scale;
+  s.follows = follows;
   s.status = dense_status();
   return launch_scaled(gated, ma, mb, s, sms, st);
 }
@@ -387,7 +390,7 @@ REC_ATTN_API rec_attn_status rec_attn_scaled_matmul(int64_t rows, int64_t cols, 
   if (rows <= kFewRows)
     return from_cuda(launch_few(true, false, {(int)rows, (int)cols, (int)depth, a, a_scale, b, b_scale, 0, y, nullptr, 0,
                                               dense_status()}, sms, st));
-  return from_cuda(scaled(false, a, a_scale, rows, b, b_scale, cols, depth, 0, y, nullptr, sms, st));
+  return from_cuda(scaled(false, a, a_scale, rows, b, b_scale, cols, depth, 0, y, nullptr, false, sms, st));
 }
 
 REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t rows, int64_t width, int64_t hidden,
@@ -426,8 +429,8 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t
     if (e == cudaSuccess) e = launch_few(true, true, {R, H, W, xq, xs, w_in, w_in_scale, activation, hq, hs, 1, word}, sms, st);
     if (e == cudaSuccess) e = launch_few(true, false, {R, W, H, hq, hs, w_out, w_out_scale, 0, y, nullptr, 1, word}, sms, st);
   } else {
-    if (e == cudaSuccess) e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, sms, st);
-    if (e == cudaSuccess) e = scaled(false, hq, hs, rows, w_out, w_out_scale, width, hidden, 0, y, nullptr, sms, st);
+    if (e == cudaSuccess) e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, true, sms, st);
+    if (e == cudaSuccess) e = scaled(false, hq, hs, rows, w_out, w_out_scale, width, hidden, 0, y, nullptr, true, sms, st);
   }
   const cudaError_t ef = ws.give_back();
   return from_cuda(e != cudaSuccess ? e : ef);

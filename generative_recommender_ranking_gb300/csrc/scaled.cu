@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::pair_sync<2>();  // both CTAs' barriers are there
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot, rank = ptx::pair_rank<2>();
+  ptx::successor_may_start();
+  if (a.follows) ptx::predecessor_done();
   if (warp < 4) {
     ptx::fewer_registers<kFewRegs>();
     if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, rank, lane);
@@ -410,7 +412,7 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int 
   a.tiles_m = (a.M + 2 * kTile - 1) / (2 * kTile);
   a.tiles_n = (a.N + tn - 1) / tn;
   const int tiles = a.tiles_m * a.tiles_n, places = num_sms / 2;
-  return launch_pairs(2, false, k_scaled<GATED, ACT>, (tiles < places ? tiles : places) * 2, kThreads, kDynamic, st, ma, mb, a);
+  return launch_pairs(2, a.follows != 0, k_scaled<GATED, ACT>, (tiles < places ? tiles : places) * 2, kThreads, kDynamic, st, ma, mb, a);
 }
 
 }  // namespace

@@ -27,6 +27,7 @@ struct ScaledArgs {
   const float* b_scale;    // [blocks of B's rows][kblocks]
   int act;                 // gated
   int wide;                // the outputs' rows start on 32-byte boundaries
+  int follows;             // behind a kernel of the same call: launched before that one has ended
   void* out;               // bf16 [M][N]; gated: e4m3
   float* out_scale;        // gated: [M][N / 128]
   int* status;
