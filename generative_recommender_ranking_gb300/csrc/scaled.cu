@@ -29,84 +29,87 @@ namespace recattn {
 namespace {
 
 // ------------------------------------------------------------------ quantizer
-// Eight values of a row.
+// Sixteen neighbouring values of a row (widths are multiples of 16): 16 bytes of e4m3.
 template <typename E>
-struct Eight;
+struct Run;
 template <>
-struct Eight<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const void* x, long long i) { v = __ldcs(static_cast<const uint4*>(x) + i); }
-  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+struct Run<__nv_bfloat16> {
+  uint4 v[2];
   __device__ __forceinline__ float at(int k) const {
-    const uint32_t w = k < 2 ? v.x : k < 4 ? v.y : k < 6 ? v.z : v.w;
+    const uint4 h = v[k >> 3];
+    const uint32_t w = (k & 7) < 2 ? h.x : (k & 7) < 4 ? h.y : (k & 7) < 6 ? h.z : h.w;
     return __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
   }
 };
 template <>
-struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* x, long long i) {
-    a = __ldcs(static_cast<const float4*>(x) + 2 * i);
-    b = __ldcs(static_cast<const float4*>(x) + 2 * i + 1);
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+struct Run<float> {
+  uint4 v[4];
   __device__ __forceinline__ float at(int k) const {
-    const float4 h = k < 4 ? a : b;
-    return (k & 3) == 0 ? h.x : (k & 3) == 1 ? h.y : (k & 3) == 2 ? h.z : h.w;
+    const uint4 h = v[k >> 2];
+    return __uint_as_float((k & 3) == 0 ? h.x : (k & 3) == 1 ? h.y : (k & 3) == 2 ? h.z : h.w);
   }
 };
+template <typename E>
+__device__ __forceinline__ void load_run(Run<E>& r, const void* x, long long i, bool in) {
+  constexpr int kN = sizeof(Run<E>) / 16;
+#pragma unroll
+  for (int k = 0; k < kN; ++k) r.v[k] = in ? __ldcs(static_cast<const uint4*>(x) + i * kN + k) : make_uint4(0, 0, 0, 0);
+}
 // The largest finite size; fine: there are no others.
 template <typename E>
-__device__ __forceinline__ float largest(const Eight<E>& x, bool& fine) {
+__device__ __forceinline__ float largest(const Run<E>& x, bool& fine) {
   float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = largest_or_nan(m, x.at(k));
+  for (int k = 0; k < 16; ++k) m = largest_or_nan(m, x.at(k));
   fine = m <= kFloatMax;
   if (!fine) {
     m = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, finite_size(x.at(k)));
+    for (int k = 0; k < 16; ++k) m = fmaxf(m, finite_size(x.at(k)));
   }
   return m;
 }
 template <typename E>
-__device__ __forceinline__ uint2 quantized(const Eight<E>& x, float inv, bool fine) {
-  return make_uint2(pack_e4m3(x.at(0) * inv, x.at(1) * inv, x.at(2) * inv, x.at(3) * inv, fine),
-                    pack_e4m3(x.at(4) * inv, x.at(5) * inv, x.at(6) * inv, x.at(7) * inv, fine));
+__device__ __forceinline__ uint4 quantized(const Run<E>& x, float inv, bool fine) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    w[k] = pack_e4m3(x.at(4 * k) * inv, x.at(4 * k + 1) * inv, x.at(4 * k + 2) * inv, x.at(4 * k + 3) * inv, fine);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kQuantThreads = 256, kQuantRun = 4;
+constexpr int kQuantThreads = 256, kRunBf16 = 4, kRunFp32 = 2;
 
-// A scale per row and 128 columns: 16 lanes a block, four blocks of theirs in flight.
-template <typename E>
+// A scale per row and 128 columns: 8 lanes a block, RUN blocks of theirs in flight.  HBM-bound: 320016
+// rows of 512 bf16 take 76 us (6.5 TB/s).
+template <typename E, int RUN>
 __global__ void __launch_bounds__(kQuantThreads) k_quantize_rows(QuantArgs a) {
   ptx::successor_may_start();
-  const int lane = threadIdx.x & 15, chunks = a.width / 8;
-  const long long units = a.rows * a.blocks, groups = (long long)gridDim.x * (kQuantThreads / 16);
-  const long long first = (long long)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
-  for (long long u0 = first; u0 - (threadIdx.x >> 4 & 1) < units; u0 += groups * kQuantRun) {  // (a warp's halves together)
-    Eight<E> x[kQuantRun];
-    long long at[kQuantRun];
+  const int lane = threadIdx.x & 7, runs = a.width / 16;
+  const long long units = a.rows * a.blocks, groups = (long long)gridDim.x * (kQuantThreads / 8);
+  const long long first = (long long)blockIdx.x * (kQuantThreads / 8) + (threadIdx.x >> 3);
+  for (long long u0 = first; u0 - (threadIdx.x >> 3 & 3) < units; u0 += groups * RUN) {  // (a warp's groups together)
+    Run<E> x[RUN];
+    long long at[RUN];
 #pragma unroll
-    for (int j = 0; j < kQuantRun; ++j) {
+    for (int j = 0; j < RUN; ++j) {
       const long long u = u0 + j * groups;
       const long long row = units >> 32 ? u / a.blocks : (long long)((uint32_t)u / (uint32_t)a.blocks);
-      const int c = (int)(u - row * a.blocks) * 16 + lane;
-      const bool in = u < units && c < chunks;
-      at[j] = in ? row * chunks + c : -1;
-      if (in) x[j].load(a.x, at[j]);
-      else x[j].zero();
+      const int c = (int)(u - row * a.blocks) * 8 + lane;
+      const bool in = u < units && c < runs;
+      at[j] = in ? row * runs + c : -1;
+      load_run(x[j], a.x, at[j], in);
     }
 #pragma unroll
-    for (int j = 0; j < kQuantRun; ++j) {
+    for (int j = 0; j < RUN; ++j) {
       bool fine;
       float top = largest(x[j], fine);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       float inv;
       const float scale = block_scale(top, inv);
       if (at[j] >= 0) {
-        reinterpret_cast<uint2*>(a.q)[at[j]] = quantized(x[j], inv, fine);
+        reinterpret_cast<uint4*>(a.q)[at[j]] = quantized(x[j], inv, fine);
         if (lane == 0) a.scale[u0 + j * groups] = scale;
       }
     }
@@ -117,18 +120,15 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize_rows(QuantArgs a) {
 template <typename E>
 __global__ void __launch_bounds__(kQuantThreads) k_quantize_blocks(QuantArgs a) {
   __shared__ float s_top[kQuantThreads / 32];
-  const int chunks = a.width / 8, c = (int)(blockIdx.x % a.blocks) * 16 + (threadIdx.x & 15);
-  const long long row0 = (long long)(blockIdx.x / a.blocks) * kScaleBlock + (threadIdx.x >> 4);
-  Eight<E> x[8];
+  const int runs = a.width / 16, c = (int)(blockIdx.x % a.blocks) * 8 + (threadIdx.x & 7);
+  const long long row0 = (long long)(blockIdx.x / a.blocks) * kScaleBlock + (threadIdx.x >> 3);
+  Run<E> x[4];
   float top = 0.f;
   bool all_fine = true;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (row0 + 16 * j < a.rows && c < chunks) x[j].load(a.x, (row0 + 16 * j) * chunks + c);
-    else x[j].zero();
-  }
+  for (int j = 0; j < 4; ++j) load_run(x[j], a.x, (row0 + 32 * j) * runs + c, row0 + 32 * j < a.rows && c < runs);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     bool fine;
     top = fmaxf(top, largest(x[j], fine));
     all_fine = all_fine && fine;
@@ -143,9 +143,9 @@ __global__ void __launch_bounds__(kQuantThreads) k_quantize_blocks(QuantArgs a) 
   const float scale = block_scale(top, inv);
   if (threadIdx.x == 0) a.scale[blockIdx.x] = scale;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (row0 + 16 * j < a.rows && c < chunks)
-      reinterpret_cast<uint2*>(a.q)[(row0 + 16 * j) * chunks + c] = quantized(x[j], inv, all_fine);
+  for (int j = 0; j < 4; ++j)
+    if (row0 + 32 * j < a.rows && c < runs)
+      reinterpret_cast<uint4*>(a.q)[(row0 + 32 * j) * runs + c] = quantized(x[j], inv, all_fine);
 }
 
 // ------------------------------------------------------------------ product
@@ -420,11 +420,11 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int 
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, int block_rows, int num_sms, cudaStream_t st) {
   const bool bf16 = dtype == REC_ATTN_BF16;
   if (block_rows == 1) {
-    const long long units = a.rows * a.blocks, run = kQuantThreads / 16 * kQuantRun;
-    const long long blocks = (units + run - 1) / run;
+    const int run = bf16 ? kRunBf16 : kRunFp32;
+    const long long units = a.rows * a.blocks, per = kQuantThreads / 8 * run, blocks = (units + per - 1) / per;
     const unsigned grid = (unsigned)(blocks < 32LL * num_sms ? blocks : 32LL * num_sms);
-    if (bf16) k_quantize_rows<__nv_bfloat16><<<grid, kQuantThreads, 0, st>>>(a);
-    else k_quantize_rows<float><<<grid, kQuantThreads, 0, st>>>(a);
+    if (bf16) k_quantize_rows<__nv_bfloat16, kRunBf16><<<grid, kQuantThreads, 0, st>>>(a);
+    else k_quantize_rows<float, kRunFp32><<<grid, kQuantThreads, 0, st>>>(a);
   } else {
     const unsigned grid = (unsigned)((a.rows + kScaleBlock - 1) / kScaleBlock * a.blocks);
     if (bf16) k_quantize_blocks<__nv_bfloat16><<<grid, kQuantThreads, 0, st>>>(a);
