@@ -37,7 +37,7 @@ template <bool GATED, int TOKENS>
 struct Cfg {
   static constexpr int kMats = GATED ? 2 : 1;
   static constexpr int kStage = kMats * kMat + TOKENS * 128;
-  static constexpr int kStages = 212 * 1024 / kStage < 12 ? 212 * 1024 / kStage : 12;
+  static constexpr int kStages = 108 * 1024 / kStage;  // two CTAs an SM
   static constexpr int kDynamic = kStages * kStage + 1024;
   static_assert(kStages * kStage >= kMats * TOKENS * 128 * 4, "the CTA's sums fit the ring");
 };
@@ -201,7 +201,7 @@ __device__ void collect(const FewArgs& a, float* s_sum, uint64_t* bars, uint32_t
 }
 
 template <bool E4M3, bool GATED, int ACT, int TOKENS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     k_few(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, const FewArgs a) {
   using C = Cfg<GATED, TOKENS>;
   extern __shared__ uint8_t smem_raw[];
@@ -314,7 +314,7 @@ cudaError_t launch_few(bool e4m3, bool gated, FewArgs a, int num_sms, cudaStream
   if (few_is_thin(e4m3, gated, a)) return launch_thin(e4m3, gated, a, st);
   a.kblocks = e4m3 ? (a.K + 127) / 128 : (a.K + 63) / 64;
   a.cluster = 1;
-  while (a.cluster < 8 && 2 * a.cluster <= a.kblocks && 2LL * a.cluster * ((a.N + 127) / 128) <= num_sms) a.cluster *= 2;
+  while (a.cluster < 8 && 2 * a.cluster <= a.kblocks && a.cluster * ((a.N + 127LL) / 128) <= num_sms) a.cluster *= 2;
   return e4m3 ? by_kind<true>(gated, a, st) : by_kind<false>(gated, a, st);
 }
 
