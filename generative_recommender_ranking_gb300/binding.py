@@ -174,13 +174,17 @@ def _ptr(x) -> int | None:
     return x.data_ptr()  # torch.Tensor
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
+    """The raw handle of a stream, or of the current one of the current device (`device`, where the
+    caller knows it)."""
     if stream is None:
         import torch
         # the raw handle of torch.cuda.current_stream(), without building the stream object
         # (a few microseconds, which a small call would notice)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -368,7 +372,7 @@ def _rows(fn: str, x, **others):
 def _here(x) -> bool:
     """Whether a tensor is on the current device."""
     import torch
-    return x.is_cuda and x.get_device() == torch.cuda.current_device()
+    return x.is_cuda and x.get_device() == torch._C._cuda_getDevice()
 
 
 def _gains(fn: str, x, types, **gains):
@@ -410,11 +414,11 @@ def rec_attn_layernorm_bwd(x, weight, dy, dx, dweight=None, dbias=None, types=No
 
 
 def _matrices(fn: str, x, *shaped):
-    """Contiguous matrices of x's device: (tensor or None, shape, dtype) each."""
+    """Contiguous matrices of x's device: (tensor, shape, dtype) each."""
     device = x.get_device()
     for o, shape, dtype in shaped:
-        if o is not None and not (o.dtype == dtype and o.shape == shape and o.get_device() == device
-                                  and o.is_contiguous()):
+        if not (o is not None and o.dtype == dtype and o.shape == shape and o.get_device() == device
+                and o.is_contiguous()):
             raise RecAttnError(fn, ERR_INVALID_ARG)
 
 
@@ -426,7 +430,7 @@ def _activation(fn: str, name: str) -> int:
 
 
 def _hidden(fn: str, w_out) -> int:
-    shape = w_out.shape
+    shape = () if w_out is None else w_out.shape
     if len(shape) != 2:
         raise RecAttnError(fn, ERR_INVALID_ARG)
     return shape[1]
@@ -440,8 +444,8 @@ def rec_attn_ffn_fwd(x, w_in, w_out, y, activation: str = "silu", stream=None) -
     dtype, rows, width = _rows(fn, x, y=y)
     hidden = _hidden(fn, w_out)
     _matrices(fn, x, (w_in, (2 * hidden, width), x.dtype), (w_out, (width, hidden), x.dtype))
-    _check(fn, L.rec_attn_ffn_fwd(dtype, _activation(fn, activation), rows, width, hidden, _ptr(x), _ptr(w_in),
-                                  _ptr(w_out), _ptr(y), _stream(stream)))
+    _check(fn, L.rec_attn_ffn_fwd(dtype, _activation(fn, activation), rows, width, hidden, x.data_ptr(), w_in.data_ptr(),
+                                  w_out.data_ptr(), y.data_ptr(), _stream(stream, x.get_device())))
 
 
 def rec_attn_ffn_bwd(x, w_in, w_out, dy, dx=None, dw_in=None, dw_out=None, activation: str = "silu",
@@ -452,10 +456,11 @@ def rec_attn_ffn_bwd(x, w_in, w_out, dy, dx=None, dw_in=None, dw_out=None, activ
     dtype, rows, width = _rows(fn, x, dy=dy)
     hidden = _hidden(fn, w_out)
     w_in_s, w_out_s = ((2 * hidden, width), x.dtype), ((width, hidden), x.dtype)
-    _matrices(fn, x, (w_in, *w_in_s), (w_out, *w_out_s), (dx, (rows, width), x.dtype), (dw_in, *w_in_s),
-              (dw_out, *w_out_s))
-    _check(fn, L.rec_attn_ffn_bwd(dtype, _activation(fn, activation), rows, width, hidden, _ptr(x), _ptr(w_in),
-                                  _ptr(w_out), _ptr(dy), _ptr(dx), _ptr(dw_in), _ptr(dw_out), _stream(stream)))
+    _matrices(fn, x, (w_in, *w_in_s), (w_out, *w_out_s))
+    _matrices(fn, x, *(o for o in ((dx, (rows, width), x.dtype), (dw_in, *w_in_s), (dw_out, *w_out_s)) if o[0] is not None))
+    _check(fn, L.rec_attn_ffn_bwd(dtype, _activation(fn, activation), rows, width, hidden, x.data_ptr(), w_in.data_ptr(),
+                                  w_out.data_ptr(), dy.data_ptr(), _ptr(dx), _ptr(dw_in), _ptr(dw_out),
+                                  _stream(stream, x.get_device())))
 
 
 def _scale_shape(shape, block_rows):
@@ -477,8 +482,8 @@ def rec_attn_scaled_quantize(x, q, scale, block_rows: int = 1, stream=None) -> N
     if block_rows not in (1, 128):
         raise RecAttnError(fn, ERR_INVALID_ARG)
     _matrices(fn, x, (q, (rows, width), torch.float8_e4m3fn), (scale, _scale_shape(x.shape, block_rows), torch.float32))
-    _check(fn, L.rec_attn_scaled_quantize(dtype, int(block_rows), rows, width, _ptr(x), _ptr(q), _ptr(scale),
-                                          _stream(stream)))
+    _check(fn, L.rec_attn_scaled_quantize(dtype, int(block_rows), rows, width, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                          _stream(stream, x.get_device())))
 
 
 def rec_attn_scaled_matmul(a, a_scale, b, b_scale, y, stream=None) -> None:
@@ -488,13 +493,13 @@ def rec_attn_scaled_matmul(a, a_scale, b, b_scale, y, stream=None) -> None:
     L, fn = lib(), "rec_attn_scaled_matmul"
     f8, f32 = torch.float8_e4m3fn, torch.float32
     _on_device(fn, a)
-    if b.dim() != 2:
+    if b is None or len(b.shape) != 2:
         raise RecAttnError(fn, ERR_INVALID_ARG)
     (rows, depth), cols = a.shape, b.shape[0]
     _matrices(fn, a, (a, (rows, depth), f8), (b, (cols, depth), f8), (a_scale, _scale_shape(a.shape, 1), f32),
               (b_scale, _scale_shape(b.shape, 128), f32), (y, (rows, cols), torch.bfloat16))
-    _check(fn, L.rec_attn_scaled_matmul(rows, cols, depth, _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(y),
-                                        _stream(stream)))
+    _check(fn, L.rec_attn_scaled_matmul(rows, cols, depth, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
+                                        b_scale.data_ptr(), y.data_ptr(), _stream(stream, a.get_device())))
 
 
 def rec_attn_ffn_scaled_fwd(x, w_in, w_in_scale, w_out, w_out_scale, y, activation: str = "silu", stream=None) -> None:
@@ -508,8 +513,9 @@ def rec_attn_ffn_scaled_fwd(x, w_in, w_in_scale, w_out, w_out_scale, y, activati
     _matrices(fn, x, (x, (rows, width), torch.bfloat16), (w_in, (2 * hidden, width), f8), (w_out, (width, hidden), f8),
               (w_in_scale, _scale_shape((2 * hidden, width), 128), f32),
               (w_out_scale, _scale_shape((width, hidden), 128), f32))
-    _check(fn, L.rec_attn_ffn_scaled_fwd(_activation(fn, activation), rows, width, hidden, _ptr(x), _ptr(w_in),
-                                         _ptr(w_in_scale), _ptr(w_out), _ptr(w_out_scale), _ptr(y), _stream(stream)))
+    _check(fn, L.rec_attn_ffn_scaled_fwd(_activation(fn, activation), rows, width, hidden, x.data_ptr(), w_in.data_ptr(),
+                                         w_in_scale.data_ptr(), w_out.data_ptr(), w_out_scale.data_ptr(), y.data_ptr(),
+                                         _stream(stream, x.get_device())))
 
 
 def rec_attn_dense_device_status(stream=None) -> int:
