@@ -32,26 +32,52 @@ __device__ __forceinline__ f32x2 fma_pairs(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
-// act(g), and its derivative.  silu: g / (1 + e^-g).  gelu: g Phi(g), Phi by the complementary error
-// function, which keeps its relative accuracy where Phi is small.
+// The hardware's 2^x and 1 / x (off by 2^-22 and 2^-23; results and operands below the normal numbers are zero).
+__device__ __forceinline__ float exp2_hw(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_hw(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Phi(g) of the normal distribution, and e^(-g^2/2): for z = |g| / sqrt(2), erfc(z) = t (a1 + t (a2 + t (a3 + t
+// (a4 + t a5)))) e^(-z^2), t = 1 / (1 + p z), off by 1.5e-7 (Abramowitz and Stegun, 7.1.26); the side below zero
+// is half of it, so it keeps its relative accuracy where Phi is small, and shares its exponential with the slope.
+__device__ __forceinline__ float normal_cdf(float g, float& density) {
+  const float t = rcp_hw(fmaf(0.70710678f * 0.3275911f, fabsf(g), 1.f));
+  density = exp2_hw(-0.72134752f * g * g);  // log2(e) / 2
+  float s = fmaf(t, 1.061405429f, -1.453152027f);
+  s = fmaf(t, s, 1.421413741f);
+  s = fmaf(t, s, -0.284496736f);
+  s = fmaf(t, s, 0.254829592f);
+  s = 0.5f * t * s * density;
+  return g > 0.f ? 1.f - s : s;
+}
+
+// act(g), and its derivative, for results in 16 bits and fewer.  silu: g / (1 + e^-g).  gelu: g Phi(g).
 template <int ACT>
 __device__ __forceinline__ float act_value(float g) {
-  if (ACT == REC_ATTN_SILU) return __fdividef(g, 1.f + __expf(-g));
-  return 0.5f * g * erfcf(-0.70710678f * g);
+  if (ACT == REC_ATTN_SILU) return g * rcp_hw(1.f + exp2_hw(-1.44269504f * g));
+  float density;
+  return g * normal_cdf(g, density);
 }
 template <int ACT>
 __device__ __forceinline__ float act_both(float g, float& slope) {
   if (ACT == REC_ATTN_SILU) {
-    const float p = __fdividef(1.f, 1.f + __expf(-g)), v = g * p;
+    const float p = rcp_hw(1.f + exp2_hw(-1.44269504f * g)), v = g * p;
     slope = fmaf(v, 1.f - p, p);
     return v;
   }
-  const float p = 0.5f * erfcf(-0.70710678f * g);
-  slope = fmaf(g, 0.39894228f * __expf(-0.5f * g * g), p);
+  float density;
+  const float p = normal_cdf(g, density);
+  slope = fmaf(g, 0.39894228f * density, p);
   return g * p;
 }
-
-// The same for fp32 results: the library's exponential and division keep its last bits.
+// The same for fp32 results: Phi by the complementary error function, and the library's exponential and division keep its last bits.
 template <int ACT>
 __device__ __forceinline__ float act32(float g, float& slope) {
   if (ACT == REC_ATTN_SILU) {
