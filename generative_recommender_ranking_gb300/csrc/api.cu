@@ -119,13 +119,13 @@ bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, i
   return r == CUDA_SUCCESS;
 }
 
-// 3-D map over the three bf16 planes of an fp32 matrix; box = 64 columns x 64 rows of one.
-bool encode_planes(CUtensorMap* m, const Planes& a) {
+// 3-D map over the three bf16 planes of an fp32 matrix; box = 64 columns x `box_rows` rows of each.
+bool encode_planes(CUtensorMap* m, const Planes& a, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows, 3};
   cuuint64_t strides[2] = {(cuuint64_t)a.ld * 2, (cuuint64_t)a.plane()};
-  cuuint32_t box[3] = {64, 64, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 3};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

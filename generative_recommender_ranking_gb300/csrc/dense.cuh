@@ -30,8 +30,9 @@ struct DenseArgs {
   int* status;
 };
 
-// A row-major [rows][cols] bf16 operand as a TMA map; box = 64 columns x 64 rows.
-bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols);
+// A row-major [rows][cols] bf16 operand as a TMA map: boxes of 64 columns x 128 rows, or 64 x 64 where the
+// summed axis runs over its rows (mn_major).
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major);
 int* dense_status();
 
 // fp32 operands (dense_fp32.cu): a matrix as three bf16 planes whose sum it is, rows `ld` apart.
@@ -50,7 +51,8 @@ struct SplitList {
   Planes to[4];
 };
 cudaError_t launch_split(const SplitList& l, cudaStream_t st);
-bool encode_planes(CUtensorMap* m, const Planes& a);
+// (a K-major A: boxes of 128 rows, other operands 64)
+bool encode_planes(CUtensorMap* m, const Planes& a, int box_rows);
 cudaError_t launch_dense32(DenseOp op, const CUtensorMap (&maps)[4], Dense32Args a, int num_sms, cudaStream_t st);
 int dense32_splits(int M, int N, int kblocks, int num_sms);
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&maps)[4], DenseArgs a, int num_sms, cudaStream_t st);

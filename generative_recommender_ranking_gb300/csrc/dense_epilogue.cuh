@@ -21,6 +21,9 @@ __device__ __forceinline__ f32x2 pair_of(float a, float b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ f32x2 pair_of_bits(uint32_t a, uint32_t b) {
+  return pair_of(__uint_as_float(a), __uint_as_float(b));
+}
 __device__ __forceinline__ float2 values_of(f32x2 v) {
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
@@ -30,6 +33,21 @@ __device__ __forceinline__ f32x2 fma_pairs(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+__device__ __forceinline__ f32x2 mul_pairs(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add_pairs(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(f32x2 v) {
+  const float2 f = values_of(v);
+  return pack_bf16(f.x, f.y);
 }
 
 // The hardware's 2^x and 1 / x (off by 2^-22 and 2^-23; results and operands below the normal numbers are zero).
@@ -44,38 +62,49 @@ __device__ __forceinline__ float rcp_hw(float x) {
   return r;
 }
 
+__device__ __forceinline__ f32x2 exp2_hw(f32x2 x) {
+  const float2 v = values_of(x);
+  return pair_of(exp2_hw(v.x), exp2_hw(v.y));
+}
+__device__ __forceinline__ f32x2 rcp_hw(f32x2 x) {
+  const float2 v = values_of(x);
+  return pair_of(rcp_hw(v.x), rcp_hw(v.y));
+}
+__device__ __forceinline__ f32x2 both(float v) { return pair_of(v, v); }
+
 // Phi(g) of the normal distribution, and e^(-g^2/2): for z = |g| / sqrt(2), erfc(z) = t (a1 + t (a2 + t (a3 + t
 // (a4 + t a5)))) e^(-z^2), t = 1 / (1 + p z), off by 1.5e-7 (Abramowitz and Stegun, 7.1.26); the side below zero
 // is half of it, so it keeps its relative accuracy where Phi is small, and shares its exponential with the slope.
-__device__ __forceinline__ float normal_cdf(float g, float& density) {
-  const float t = rcp_hw(fmaf(0.70710678f * 0.3275911f, fabsf(g), 1.f));
-  density = exp2_hw(-0.72134752f * g * g);  // log2(e) / 2
-  float s = fmaf(t, 1.061405429f, -1.453152027f);
-  s = fmaf(t, s, 1.421413741f);
-  s = fmaf(t, s, -0.284496736f);
-  s = fmaf(t, s, 0.254829592f);
-  s = 0.5f * t * s * density;
-  return g > 0.f ? 1.f - s : s;
+__device__ __forceinline__ f32x2 normal_cdf(f32x2 g, f32x2& density) {
+  const f32x2 t = rcp_hw(fma_pairs(both(0.70710678f * 0.3275911f), g & 0x7fffffff7fffffffull, both(1.f)));
+  density = exp2_hw(mul_pairs(mul_pairs(g, g), both(-0.72134752f)));  // log2(e) / 2
+  f32x2 s = fma_pairs(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+  s = fma_pairs(t, s, both(0.5f * 1.421413741f));
+  s = fma_pairs(t, s, both(0.5f * -0.284496736f));
+  s = fma_pairs(t, s, both(0.5f * 0.254829592f));
+  s = mul_pairs(mul_pairs(t, s), density);
+  const float2 v = values_of(g), w = values_of(s);
+  return pair_of(v.x > 0.f ? 1.f - w.x : w.x, v.y > 0.f ? 1.f - w.y : w.y);
 }
 
-// act(g), and its derivative, for results in 16 bits and fewer.  silu: g / (1 + e^-g).  gelu: g Phi(g).
+// act(g) of two values, and its derivative, for results in 16 bits and fewer.  silu: g / (1 + e^-g).  gelu: g Phi(g).
 template <int ACT>
-__device__ __forceinline__ float act_value(float g) {
-  if (ACT == REC_ATTN_SILU) return g * rcp_hw(1.f + exp2_hw(-1.44269504f * g));
-  float density;
-  return g * normal_cdf(g, density);
+__device__ __forceinline__ f32x2 act_value(f32x2 g) {
+  if (ACT == REC_ATTN_SILU) return mul_pairs(g, rcp_hw(add_pairs(exp2_hw(mul_pairs(g, both(-1.44269504f))), both(1.f))));
+  f32x2 density;
+  return mul_pairs(g, normal_cdf(g, density));
 }
 template <int ACT>
-__device__ __forceinline__ float act_both(float g, float& slope) {
+__device__ __forceinline__ f32x2 act_both(f32x2 g, f32x2& slope) {
   if (ACT == REC_ATTN_SILU) {
-    const float p = rcp_hw(1.f + exp2_hw(-1.44269504f * g)), v = g * p;
-    slope = fmaf(v, 1.f - p, p);
+    const f32x2 p = rcp_hw(add_pairs(exp2_hw(mul_pairs(g, both(-1.44269504f))), both(1.f))), v = mul_pairs(g, p);
+    slope = fma_pairs(v, fma_pairs(p, both(-1.f), both(1.f)), p);
     return v;
   }
-  float density;
-  const float p = normal_cdf(g, density);
-  slope = fmaf(g, 0.39894228f * density, p);
-  return g * p;
+  f32x2 density;
+  const f32x2 p = normal_cdf(g, density);
+  slope = fma_pairs(g, mul_pairs(density, both(0.39894228f)), p);
+  return mul_pairs(g, p);
 }
 // The same for fp32 results: Phi by the complementary error function, and the library's exponential and division keep its last bits.
 template <int ACT>

@@ -58,11 +58,12 @@ __device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i, uint32_t rank
   return u;
 }
 
-// 64 rows (columns) of one plane at mn0, block kb of the summed axis.
+// The three planes of 64 columns (MN) or 64 or 128 rows (the map's box) at mn0, block kb of the summed axis, one
+// after the other.
 template <bool MN>
-__device__ __forceinline__ void load_slab(uint8_t* dst, const CUtensorMap* map, int mn0, int kb, int plane, uint32_t bar) {
-  if (MN) ptx::tma_load_3d_pair(dst, map, mn0, kb * kBK, plane, bar);
-  else ptx::tma_load_3d_pair(dst, map, kb * kBK, mn0, plane, bar);
+__device__ __forceinline__ void load_planes(uint8_t* dst, const CUtensorMap* map, int mn0, int kb, uint32_t bar) {
+  if (MN) ptx::tma_load_3d_pair(dst, map, mn0, kb * kBK, 0, bar);
+  else ptx::tma_load_3d_pair(dst, map, kb * kBK, mn0, 0, bar);
 }
 
 template <DenseOp OP>
@@ -84,18 +85,14 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
         // (the first CTA's barrier counts the bytes of both; dh has 64 columns, 32 rows of B from each)
         if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * kStage);
         const int nb = C::kPair ? (rank ? a.N : 0) + u.n0 : u.n0 + 64 * (int)rank;  // gated: the gate's rows, up's
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          uint8_t *sa = s + p * kPlane, *sb = s + 3 * kPlane + p * kSlab;
-          if (grad) {
-            load_slab<false>(sa, ma2, u.m0, kb + first, p, bar);
-            load_slab<false>(sa + kSlab, ma2, u.m0 + 64, kb + first, p, bar);
-            load_slab<true>(sb, mb2, u.n0 + 32 * (int)rank, kb + first, p, bar);
-          } else {
-            load_slab<C::kAMn>(sa, ma, u.m0, kb, p, bar);
-            load_slab<C::kAMn>(sa + kSlab, ma, u.m0 + 64, kb, p, bar);
-            load_slab<C::kBMn>(sb, mb, nb, kb, p, bar);
-          }
+        uint8_t* const sb = s + 3 * kPlane;
+        if (grad) {
+          load_planes<false>(s, ma2, u.m0, kb + first, bar);
+          load_planes<true>(sb, mb2, u.n0 + 32 * (int)rank, kb + first, bar);
+        } else {
+          load_planes<C::kAMn>(s, ma, u.m0, kb, bar);
+          if (C::kAMn) load_planes<true>(s + 3 * kSlab, ma, u.m0 + 64, kb, bar);
+          load_planes<C::kBMn>(sb, mb, nb, kb, bar);
         }
       }
       __syncwarp();
@@ -113,14 +110,16 @@ out:
 template <bool AMN, bool BMN, int N>
 __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s) {
   const uint32_t idesc = ptx::idesc_bf16_f32(2 * kTile, N, AMN, BMN);
-  const uint64_t da = ptx::smem_desc_sw128(s, AMN ? kSlab : 16, 1024);
+  // A's planes: 128 rows each, or (MN) 64 columns of each and then the other 64
+  constexpr int kStepA = AMN ? kSlab : kPlane;
+  const uint64_t da = ptx::smem_desc_sw128(s, AMN ? 3 * kSlab : 16, 1024);
   const uint64_t db = ptx::smem_desc_sw128(s + 3 * kPlane, BMN ? kSlab : 16, 1024);
   constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};
 #pragma unroll
   for (int j = 0; j < 6; ++j)
 #pragma unroll
     for (int k = 0; k < kBK / 16; ++k)
-      ptx::umma_pair<2, false>(acc, ptx::smem_desc_at(da, kA[j] * kPlane + k * (AMN ? 2048 : 32)),
+      ptx::umma_pair<2, false>(acc, ptx::smem_desc_at(da, kA[j] * kStepA + k * (AMN ? 2048 : 32)),
                                ptx::smem_desc_at(db, kB[j] * kSlab + k * (BMN ? 2048 : 32)), idesc, j + k > 0);
 }
 

@@ -32,6 +32,7 @@ constexpr int kSlab = 64 * 128;              // 64 rows of 128 bytes
 
 template <DenseOp OP, int BN, int CG>
 struct Cfg {
+  static_assert(BN == 256 && CG == 2, "a CTA loads 128 rows of either operand");
   static constexpr bool kPair = OP == DenseOp::kGlu || OP == DenseOp::kDglu;  // gate and up columns
   static constexpr bool kAMn = OP == DenseOp::kDw, kBMn = OP == DenseOp::kDx || OP == DenseOp::kDw;
   static constexpr int kTileN = kPair ? BN / 2 : BN;  // columns of the result
@@ -68,12 +69,15 @@ __device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i, uint32_t rank
 }
 
 // ------------------------------------------------------------------ loads
-// `rows` (a multiple of 64) rows of one operand at mn0, block kb of the summed axis.
+// 128 rows of one operand at mn0 (MN: `rows` columns of it, a multiple of 64), block kb of the summed axis.  One
+// copy where a box can hold them: the loading warp needs about 100 cycles a copy (measured: 394 for a block's
+// four copies of 64 rows, which bounded the kernels at 570 cycles a block).
 template <bool MN, int CG>
 __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn0, int rows, int kb, uint32_t bar) {
-  for (int i = 0; i < rows / 64; ++i) {
-    if (MN) ptx::tma_load_2d_pair<CG>(dst + i * kSlab, map, mn0 + 64 * i, kb * kBK, bar);
-    else ptx::tma_load_2d_pair<CG>(dst + i * kSlab, map, kb * kBK, mn0 + 64 * i, bar);
+  if (MN) {
+    for (int i = 0; i < rows / 64; ++i) ptx::tma_load_2d_pair<CG>(dst + i * kSlab, map, mn0 + 64 * i, kb * kBK, bar);
+  } else {
+    ptx::tma_load_2d_pair<CG>(dst, map, kb * kBK, mn0, bar);
   }
 }
 
@@ -100,11 +104,8 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
           load_operand<true, CG>(s + 2 * kSlab, mb2, u.n0 + (int)rank * (C::kBRows / 2), C::kBRows / 2, kb + first, bar);
         } else {
           load_operand<C::kAMn, CG>(s, ma, u.m0, kTile, kb, bar);
-          if (C::kPair && CG == 2) {  // the gate's columns are the first CTA's rows of B, up's the second's
+          if (C::kPair) {  // the gate's columns are the first CTA's rows of B, up's the second's
             load_operand<false, CG>(s + 2 * kSlab, mb, (rank ? a.N : 0) + u.n0, C::kBRows, kb, bar);
-          } else if (C::kPair) {
-            load_operand<false, CG>(s + 2 * kSlab, mb, u.n0, BN / 2, kb, bar);
-            load_operand<false, CG>(s + 2 * kSlab + BN * 64, mb, a.N + u.n0, BN / 2, kb, bar);
           } else {
             load_operand<C::kBMn, CG>(s + 2 * kSlab, mb, u.n0 + (int)rank * C::kBRows, C::kBRows, kb, bar);
           }
@@ -225,19 +226,12 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         if (c + 16 >= kCols) give_back(empty + 8 * buf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float dg[2], du[2], h[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float dh = __uint_as_float(d[2 * e + k]), up = __uint_as_float(gu[32 + c + 2 * e + k]);
-            float slope;
-            const float act = act_both<ACT>(__uint_as_float(gu[c + 2 * e + k]), slope);
-            dg[k] = dh * up * slope;
-            du[k] = dh * act;
-            h[k] = act * up;
-          }
-          wg[e] = pack_bf16(dg[0], dg[1]);
-          wu[e] = pack_bf16(du[0], du[1]);
-          wh[e] = pack_bf16(h[0], h[1]);
+          const f32x2 dh = pair_of_bits(d[2 * e], d[2 * e + 1]), up = pair_of_bits(gu[32 + c + 2 * e], gu[33 + c + 2 * e]);
+          f32x2 slope;
+          const f32x2 act = act_both<ACT>(pair_of_bits(gu[c + 2 * e], gu[c + 2 * e + 1]), slope);
+          wg[e] = pack_bf16(mul_pairs(mul_pairs(dh, up), slope));
+          wu[e] = pack_bf16(mul_pairs(dh, act));
+          wh[e] = pack_bf16(mul_pairs(act, up));
         }
         const int col = u.n0 + part * kCols + c, left = a.N - col;
         if (row < a.M && left > 0) {
@@ -259,8 +253,8 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         if (c + kStep >= kCols) give_back(empty + 8 * buf);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          w[e] = pack_bf16(act_value<ACT>(__uint_as_float(gu[2 * e])) * __uint_as_float(gu[16 + 2 * e]),
-                           act_value<ACT>(__uint_as_float(gu[2 * e + 1])) * __uint_as_float(gu[16 + 2 * e + 1]));
+          w[e] = pack_bf16(mul_pairs(act_value<ACT>(pair_of_bits(gu[2 * e], gu[2 * e + 1])),
+                                     pair_of_bits(gu[16 + 2 * e], gu[17 + 2 * e])));
         if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
       } else {
         uint32_t r[32];
@@ -369,8 +363,8 @@ cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_
 
 }  // namespace
 
-bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols) {
-  return encode_map(m, base, rows, cols, 64);
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major) {
+  return encode_map(m, base, rows, cols, mn_major ? 64 : kTile);
 }
 
 // Asked once per device (the first call may be captured: the question belongs to no stream).

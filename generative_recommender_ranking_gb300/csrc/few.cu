@@ -253,10 +253,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (GATED) u = sum_of(u, a.cluster > 1 ? remote_float4(at + TOKENS * 32, r) : at[TOKENS * 32]);
     }
     if (GATED) {
-      v.x = act_value<ACT>(v.x) * u.x;
-      v.y = act_value<ACT>(v.y) * u.y;
-      v.z = act_value<ACT>(v.z) * u.z;
-      v.w = act_value<ACT>(v.w) * u.w;
+      const float2 a0 = values_of(mul_pairs(act_value<ACT>(pair_of(v.x, v.y)), pair_of(u.x, u.y)));
+      const float2 a1 = values_of(mul_pairs(act_value<ACT>(pair_of(v.z, v.w)), pair_of(u.z, u.w)));
+      v = make_float4(a0.x, a0.y, a1.x, a1.y);
     }
     const long long o = (long long)t * a.N + col;
     if constexpr (E4M3 && GATED) {

@@ -87,7 +87,7 @@ Planes placed(const Planes& a, const Workspace& ws) {
 cudaError_t plain32(DenseOp op, const Planes& a, const Planes& b, long long M, long long N, long long depth, int s,
                     float* part, void* out, int sms, cudaStream_t st) {
   CUtensorMap m[4];
-  if (!encode_planes(&m[0], a) || !encode_planes(&m[1], b)) return cudaErrorInvalidValue;
+  if (!encode_planes(&m[0], a, op == DenseOp::kDw ? 64 : 128) || !encode_planes(&m[1], b, 64)) return cudaErrorInvalidValue;
   Dense32Args d{};
   d.d.M = (int)M;
   d.d.N = (int)N;
@@ -139,7 +139,7 @@ cudaError_t ffn32_fwd(int act, long long R, long long W, long long H, const void
   px = placed(px, ws), pi = placed(pi, ws), po = placed(po, ws), ph = placed(ph, ws);
   e = launch_split({3, {x, w_in, w_out}, {px, pi, po}}, st);
   CUtensorMap m[4];
-  if (e == cudaSuccess && !(encode_planes(&m[0], px) && encode_planes(&m[1], pi))) e = cudaErrorInvalidValue;
+  if (e == cudaSuccess && !(encode_planes(&m[0], px, 128) && encode_planes(&m[1], pi, 64))) e = cudaErrorInvalidValue;
   Dense32Args d{};
   d.d.M = (int)R;
   d.d.N = (int)H;
@@ -174,7 +174,8 @@ cudaError_t ffn32_bwd(int act, long long R, long long W, long long H, const void
   e = launch_split({4, {x, w_in, w_out, dy}, {px, pi, po, pdy}}, st);
   CUtensorMap m[4];
   if (e == cudaSuccess &&
-      !(encode_planes(&m[0], px) && encode_planes(&m[1], pi) && encode_planes(&m[2], pdy) && encode_planes(&m[3], po)))
+      !(encode_planes(&m[0], px, 128) && encode_planes(&m[1], pi, 64) && encode_planes(&m[2], pdy, 128) &&
+        encode_planes(&m[3], po, 64)))
     e = cudaErrorInvalidValue;
   Dense32Args d{};
   d.d.M = (int)R;
@@ -229,7 +230,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
   a.out = ws.p;
   a.wide = wide_rows(ws.p, hidden);
   e = dense(DenseOp::kGlu, a, sms, st,
-            encode_dense(&m[0], x, rows, width) && encode_dense(&m[1], w_in, 2 * hidden, width), m);
+            encode_dense(&m[0], x, rows, width, false) && encode_dense(&m[1], w_in, 2 * hidden, width, false), m);
   a.N = (int)width;
   a.kblocks = blocks64(hidden);
   a.out = y;
@@ -237,7 +238,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
   a.follows = 1;
   if (e == cudaSuccess)
     e = dense(DenseOp::kOut, a, sms, st,
-              encode_dense(&m[0], ws.p, rows, hidden) && encode_dense(&m[1], w_out, width, hidden), m);
+              encode_dense(&m[0], ws.p, rows, hidden, false) && encode_dense(&m[1], w_out, width, hidden, false), m);
   const cudaError_t ef = ws.give_back();
   return from_cuda(e != cudaSuccess ? e : ef);
 }
@@ -289,8 +290,8 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
   a.out2 = h;
   a.wide = wide_rows(p, hidden);
   e = dense(DenseOp::kDglu, a, sms, st,
-            encode_dense(&m[0], x, rows, width) && encode_dense(&m[1], w_in, 2 * hidden, width) &&
-                encode_dense(&m[2], dy, rows, width) && encode_dense(&m[3], w_out, width, hidden),
+            encode_dense(&m[0], x, rows, width, false) && encode_dense(&m[1], w_in, 2 * hidden, width, false) &&
+                encode_dense(&m[2], dy, rows, width, false) && encode_dense(&m[3], w_out, width, hidden, true),
             m);
   a.follows = 1;
   if (e == cudaSuccess && dx) {
@@ -299,7 +300,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     a.out = dx;
     a.wide = wide_rows(dx, width);
     e = dense(DenseOp::kDx, a, sms, st,
-              encode_dense(&m[0], p, rows, 2 * hidden) && encode_dense(&m[1], w_in, 2 * hidden, width), m);
+              encode_dense(&m[0], p, rows, 2 * hidden, false) && encode_dense(&m[1], w_in, 2 * hidden, width, true), m);
   }
   a.kblocks = kr;
   for (int i = 0; i < 2; ++i) {
@@ -311,8 +312,8 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     a.out = dw;
     a.wide = wide_rows(dw, a.N);
     e = dense(DenseOp::kDw, a, sms, st,
-              (i ? encode_dense(&m[0], dy, rows, width) && encode_dense(&m[1], h, rows, hidden)
-                 : encode_dense(&m[0], p, rows, 2 * hidden) && encode_dense(&m[1], x, rows, width)),
+              (i ? encode_dense(&m[0], dy, rows, width, true) && encode_dense(&m[1], h, rows, hidden, true)
+                 : encode_dense(&m[0], p, rows, 2 * hidden, true) && encode_dense(&m[1], x, rows, width, true)),
               m);
     if (e == cudaSuccess && a.splits > 1) e = launch_dense_sum(a.part, dw, (long long)a.M * a.N, a.splits, dtype, st);
   }

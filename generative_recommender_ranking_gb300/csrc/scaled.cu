@@ -291,19 +291,14 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
           sums[16 * c + e] = fma_pairs(pair_of(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f, sums[16 * c + e]);
       }
     }
-    float acc[64];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float2 v = values_of(sums[e]);
-      acc[2 * e] = v.x;
-      acc[2 * e + 1] = v.y;
-    }
     if constexpr (GATED) {
-      float top = 0.f;
+      float acc[32], top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        acc[e] = act_value<ACT>(acc[e]) * acc[32 + e];
-        top = largest_or_nan(top, acc[e]);
+      for (int e = 0; e < 16; ++e) {
+        const float2 v = values_of(mul_pairs(act_value<ACT>(sums[e]), sums[16 + e]));
+        acc[2 * e] = v.x;
+        acc[2 * e + 1] = v.y;
+        top = largest_or_nan(largest_or_nan(top, v.x), v.y);
       }
       const bool fine = top <= kFloatMax;
       if (!fine) {
@@ -336,7 +331,7 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
         const int col = col0 + 16 * c;
         uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(acc[16 * c + 2 * e], acc[16 * c + 2 * e + 1]);
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(sums[8 * c + e]);
         if (in && col < a.N) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, a.N - col, a.wide);
       }
     }

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_thin(const FewArgs a) {
     if (GATED) u += s_sum[k][4 + at][from];
   }
   if (row >= a.rows || n0 + col >= a.N) return;
-  if (GATED) v = act_value<ACT>(v) * u;
+  if (GATED) v = values_of(act_value<ACT>(pair_of(v, v))).x * u;
   static_cast<__nv_bfloat16*>(a.out)[(long long)row * a.N + n0 + col] = __float2bfloat16_rn(v);
 }
 
