@@ -1,9 +1,10 @@
-// dense_epilogue.cuh -- what the epilogues of the matrix products share: the gate's activation and
-// the stores of result rows.
+// dense_device.cuh -- what the kernels of the matrix products share: the gate's activation, the stores
+// of result rows and the walk over the tiles.
 #pragma once
 
 #include <cuda_bf16.h>
 
+#include "dense.cuh"
 #include "ptx_sm103.cuh"
 #include "rec_attn_internal.cuh"
 
@@ -66,9 +67,16 @@ __device__ __forceinline__ f32x2 exp2_hw(f32x2 x) {
   const float2 v = values_of(x);
   return pair_of(exp2_hw(v.x), exp2_hw(v.y));
 }
+// Of two values from 1 to 2^62, by the reciprocal of their product (the special-function unit, at an eighth of
+// the others' rate, bounds the epilogues).
 __device__ __forceinline__ f32x2 rcp_hw(f32x2 x) {
   const float2 v = values_of(x);
-  return pair_of(rcp_hw(v.x), rcp_hw(v.y));
+  const float r = rcp_hw(v.x * v.y);
+  return mul_pairs(pair_of(v.y, v.x), pair_of(r, r));
+}
+__device__ __forceinline__ f32x2 min_pairs(f32x2 a, float most) {  // (NaN: most)
+  const float2 v = values_of(a);
+  return pair_of(fminf(v.x, most), fminf(v.y, most));
 }
 __device__ __forceinline__ f32x2 both(float v) { return pair_of(v, v); }
 
@@ -76,7 +84,7 @@ __device__ __forceinline__ f32x2 both(float v) { return pair_of(v, v); }
 // (a4 + t a5)))) e^(-z^2), t = 1 / (1 + p z), off by 1.5e-7 (Abramowitz and Stegun, 7.1.26); the side below zero
 // is half of it, so it keeps its relative accuracy where Phi is small, and shares its exponential with the slope.
 __device__ __forceinline__ f32x2 normal_cdf(f32x2 g, f32x2& density) {
-  const f32x2 t = rcp_hw(fma_pairs(both(0.70710678f * 0.3275911f), g & 0x7fffffff7fffffffull, both(1.f)));
+  const f32x2 t = rcp_hw(fma_pairs(both(0.70710678f * 0.3275911f), min_pairs(g & 0x7fffffff7fffffffull, 1e18f), both(1.f)));
   density = exp2_hw(mul_pairs(mul_pairs(g, g), both(-0.72134752f)));  // log2(e) / 2
   f32x2 s = fma_pairs(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
   s = fma_pairs(t, s, both(0.5f * 1.421413741f));
@@ -87,17 +95,22 @@ __device__ __forceinline__ f32x2 normal_cdf(f32x2 g, f32x2& density) {
   return pair_of(v.x > 0.f ? 1.f - w.x : w.x, v.y > 0.f ? 1.f - w.y : w.y);
 }
 
+// 1 / (1 + e^-g); below -41 it stays at 2^-60.
+__device__ __forceinline__ f32x2 logistic(f32x2 g) {
+  return rcp_hw(add_pairs(exp2_hw(min_pairs(mul_pairs(g, both(-1.44269504f)), 60.f)), both(1.f)));
+}
+
 // act(g) of two values, and its derivative, for results in 16 bits and fewer.  silu: g / (1 + e^-g).  gelu: g Phi(g).
 template <int ACT>
 __device__ __forceinline__ f32x2 act_value(f32x2 g) {
-  if (ACT == REC_ATTN_SILU) return mul_pairs(g, rcp_hw(add_pairs(exp2_hw(mul_pairs(g, both(-1.44269504f))), both(1.f))));
+  if (ACT == REC_ATTN_SILU) return mul_pairs(g, logistic(g));
   f32x2 density;
   return mul_pairs(g, normal_cdf(g, density));
 }
 template <int ACT>
 __device__ __forceinline__ f32x2 act_both(f32x2 g, f32x2& slope) {
   if (ACT == REC_ATTN_SILU) {
-    const f32x2 p = rcp_hw(add_pairs(exp2_hw(mul_pairs(g, both(-1.44269504f))), both(1.f))), v = mul_pairs(g, p);
+    const f32x2 p = logistic(g), v = mul_pairs(g, p);
     slope = fma_pairs(v, fma_pairs(p, both(-1.f), both(1.f)), p);
     return v;
   }
@@ -145,12 +158,66 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&
   }
 }
 
-// Tiles of tm x tn in bands of 16 row tiles: the CTAs at work together share a band's rows and the
-// columns' weights in the L2.  Row and column tile of tile t.
-__device__ __forceinline__ int2 band_tile(int t, int tiles_m, int tiles_n) {
-  const int band = t / (16 * tiles_n), in = t - band * 16 * tiles_n;
-  const int rows = min(16, tiles_m - band * 16);
-  return make_int2(band * 16 + in % rows, in / rows);
-}
+// Tiles in bands of 16 row tiles, row tiles fastest: the CTAs at work together share a band's rows and the
+// columns' weights in the L2.  A walk from tile t on in equal steps, without a division at each.
+struct TileWalk {
+  int tiles_m, band_size, band, in;  // in: tiles of the band before this one
+  __device__ __forceinline__ TileWalk(int t, int rows, int columns) : tiles_m(rows), band_size(16 * columns) {
+    band = t / band_size;
+    in = t - band * band_size;
+  }
+  __device__ __forceinline__ void advance(int step) {
+    in += step;
+    while (in >= band_size) {
+      in -= band_size;
+      ++band;
+    }
+  }
+  __device__ __forceinline__ int2 at() const {  // row and column tile
+    const int rows = tiles_m - 16 * band;
+    return rows >= 16 ? make_int2(band * 16 + (in & 15), in >> 4) : make_int2(band * 16 + in % rows, in / rows);
+  }
+};
+
+struct Unit {
+  int m0, n0, kb0, kb1, split;
+};
+
+// A pair's units in turn; m0: this CTA's first row.  (Parts of the summed axis: all tiles of one, then of the
+// next; the first a.kblocks % a.splits parts have a block more.)
+template <int TN>
+struct Units {
+  const DenseArgs& a;
+  int i, n, step, tiles, split;
+  uint32_t rank;
+  TileWalk walk;
+  __device__ __forceinline__ Units(const DenseArgs& args, uint32_t r)
+      : a(args), i((int)blockIdx.x / 2), n(args.tiles_m * args.tiles_n * args.splits), step((int)gridDim.x / 2),
+        tiles(args.tiles_m * args.tiles_n), split(0), rank(r), walk(i, args.tiles_m, args.tiles_n) {
+    settle();
+  }
+  __device__ __forceinline__ bool left() const { return i < n; }
+  __device__ __forceinline__ void next() {
+    i += step;
+    walk.advance(step);
+    settle();
+  }
+  __device__ __forceinline__ void settle() {  // a walk past the tiles goes on in the next part
+    if (a.splits == 1 || i < (split + 1) * tiles || i >= n) return;
+    split = i / tiles;
+    walk = TileWalk(i - split * tiles, a.tiles_m, a.tiles_n);
+  }
+  __device__ __forceinline__ Unit get() const {
+    const int2 at = walk.at();
+    const int q = a.kblocks / a.splits, more = a.kblocks - q * a.splits;
+    Unit u;
+    u.split = split;
+    u.m0 = (at.x * 2 + (int)rank) * kTile;
+    u.n0 = at.y * TN;
+    u.kb0 = split * q + min(split, more);
+    u.kb1 = u.kb0 + q + (split < more ? 1 : 0);
+    return u;
+  }
+};
 
 }  // namespace recattn

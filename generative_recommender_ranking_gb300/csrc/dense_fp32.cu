@@ -14,7 +14,7 @@
 #include <atomic>
 
 #include "dense.cuh"
-#include "dense_epilogue.cuh"
+#include "dense_device.cuh"
 #include "launchers.cuh"
 #include "ptx_sm103.cuh"
 #include "wait.cuh"
@@ -41,23 +41,6 @@ struct Cfg {
   static constexpr int kCols = kPair ? 64 : 128;  // of the result
 };
 
-struct Unit {
-  int m0, n0, kb0, kb1, split;
-};
-// Work of pair i; m0: this CTA's first row.
-template <int TN>
-__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i, uint32_t rank) {
-  const int tiles = a.tiles_m * a.tiles_n;
-  Unit u;
-  u.split = i / tiles;
-  const int2 at = band_tile(i - u.split * tiles, a.tiles_m, a.tiles_n);
-  u.m0 = (2 * at.x + (int)rank) * kTile;
-  u.n0 = at.y * TN;
-  u.kb0 = (int)((long long)a.kblocks * u.split / a.splits);
-  u.kb1 = (int)((long long)a.kblocks * (u.split + 1) / a.splits);
-  return u;
-}
-
 // The three planes of 64 columns (MN) or 64 or 128 rows (the map's box) at mn0, block kb of the summed axis, one
 // after the other.
 template <bool MN>
@@ -70,10 +53,9 @@ template <DenseOp OP>
 __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* ma2,
                         const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, uint32_t rank, int lane) {
   using C = Cfg<OP>;
-  const int units = a.tiles_m * a.tiles_n * a.splits;
   uint32_t n = 0;
-  for (int i = blockIdx.x / 2; i < units; i += gridDim.x / 2) {
-    const Unit u = unit_at<C::kCols>(a, i, rank);
+  for (Units<C::kCols> units(a, rank); units.left(); units.next()) {
+    const Unit u = units.get();
     const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
     for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
@@ -126,13 +108,12 @@ __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s) {
 template <DenseOp OP>
 __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
   using C = Cfg<OP>;
-  const int units = a.tiles_m * a.tiles_n * a.splits;
   const uint32_t s0 = ptx::smem_u32(sm);
   const bool el = ptx::elect_one();
   constexpr uint32_t rank = 0;  // the first CTA issues for both
   uint32_t n = 0;
-  for (int i = blockIdx.x / 2; i < units; i += gridDim.x / 2) {
-    const Unit u = unit_at<C::kCols>(a, i, rank);
+  for (Units<C::kCols> units(a, rank); units.left(); units.next()) {
+    const Unit u = units.get();
     for (int kb = OP == DenseOp::kDglu ? -a.kblocks : u.kb0; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
       const uint32_t buf = n & 1;
@@ -209,7 +190,6 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
                        int lane) {
   using C = Cfg<OP>;
   const DenseArgs& a = aa.d;
-  const int units = a.tiles_m * a.tiles_n * a.splits;
   const int quad = warp & 3, half = (warp - 2) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   const int c0 = C::kPair ? 32 * half : 64 * half, c1 = C::kPair ? 64 + 32 * half : 64 * half + 32;
@@ -227,8 +207,8 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
   };
-  for (int i = blockIdx.x / 2; i < units; i += gridDim.x / 2) {
-    const Unit u = unit_at<C::kCols>(a, i, rank);
+  for (Units<C::kCols> units(a, rank); units.left(); units.next()) {
+    const Unit u = units.get();
     float x0[32], x1[32], dh[OP == DenseOp::kDglu ? 32 : 1];
 #pragma unroll
     for (int e = 0; e < 32; ++e) x0[e] = x1[e] = 0.f;

@@ -15,7 +15,7 @@
 #include <atomic>
 
 #include "dense.cuh"
-#include "dense_epilogue.cuh"
+#include "dense_device.cuh"
 #include "launchers.cuh"
 #include "ptx_sm103.cuh"
 #include "wait.cuh"
@@ -38,6 +38,11 @@ struct Cfg {
   static constexpr int kTileN = kPair ? BN / 2 : BN;  // columns of the result
   // Warps of the epilogue: 16 where it computes the activation (of kDglu 901 us with 8)
   static constexpr int kEpiWarps = kPair ? 16 : 8, kThreads = 128 + 32 * kEpiWarps;
+  // kDglu: registers a thread, as the block is launched, and then of the loading and issuing warpgroup and of
+  // the four that hold g, u and dh
+  static constexpr bool kSplitRegs = OP == DenseOp::kDglu;
+  static constexpr int kRegs = 96, kFewRegs = 32, kSumRegs = 112;
+  static_assert(128 * kFewRegs + 512 * kSumRegs <= 640 * kRegs, "the split is the block's own");
   static constexpr int kTileM = kTile * CG;
   static constexpr int kBRows = BN / CG;               // of B in this CTA
   static constexpr int kStage = 2 * kSlab + kBRows * 128;
@@ -48,25 +53,6 @@ struct Cfg {
 
 // Barriers
 enum { kFull = 0, kEmpty = 8, kAccFull = 16, kAccEmpty = 18, kGuEmpty = 20, kDone = 21, kBars = 22 };
-
-struct Unit {
-  int m0, n0, kb0, kb1, split;
-};
-
-// Work of pair (CTA) i; m0: this CTA's first row.
-template <int TN, int CG>
-__device__ __forceinline__ Unit unit_at(const DenseArgs& a, int i, uint32_t rank) {
-  const int tiles = a.tiles_m * a.tiles_n;
-  Unit u;
-  u.split = i / tiles;
-  const int t = i - u.split * tiles;
-  const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
-  u.m0 = (at.x * CG + (int)rank) * kTile;
-  u.n0 = at.y * TN;
-  u.kb0 = (int)((long long)a.kblocks * u.split / a.splits);
-  u.kb1 = (int)((long long)a.kblocks * (u.split + 1) / a.splits);
-  return u;
-}
 
 // ------------------------------------------------------------------ loads
 // 128 rows of one operand at mn0 (MN: `rows` columns of it, a multiple of 64), block kb of the summed axis.  One
@@ -85,10 +71,9 @@ template <DenseOp OP, int BN, int CG>
 __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* ma2,
                         const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, uint32_t rank, int lane) {
   using C = Cfg<OP, BN, CG>;
-  const int units = a.tiles_m * a.tiles_n * a.splits;
   uint32_t n = 0;
-  for (int i = blockIdx.x / CG; i < units; i += gridDim.x / CG) {
-    const Unit u = unit_at<C::kTileN, CG>(a, i, rank);
+  for (Units<C::kTileN> units(a, rank); units.left(); units.next()) {
+    const Unit u = units.get();
     const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
     for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
       const int st = n % C::kStages;
@@ -144,13 +129,12 @@ __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s, bool fresh) 
 template <DenseOp OP, int BN, int CG>
 __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
   using C = Cfg<OP, BN, CG>;
-  const int units = a.tiles_m * a.tiles_n * a.splits;
   const uint32_t s0 = ptx::smem_u32(sm);
   const bool el = ptx::elect_one();
   constexpr uint32_t rank = 0;  // the first CTA issues for both
   uint32_t n = 0, it = 0;
-  for (int i = blockIdx.x / CG; i < units; i += gridDim.x / CG, ++it) {
-    const Unit u = unit_at<C::kTileN, CG>(a, i, rank);
+  for (Units<C::kTileN> units(a, rank); units.left(); units.next(), ++it) {
+    const Unit u = units.get();
     const uint32_t buf = it & 1, round = (it >> 1) & 1;
     if (!bounded_wait_warp(bars + kAccEmpty + buf, round ^ 1, abort_flag, a.status, kWaitNs)) goto out;
     ptx::tc_fence_after();
@@ -195,14 +179,13 @@ template <DenseOp OP, int BN, int CG, int ACT>
 __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, uint32_t rank, int warp,
                        int lane) {
   using C = Cfg<OP, BN, CG>;
-  const int units = a.tiles_m * a.tiles_n * a.splits;
   const int quad = warp & 3, part = (warp - 4) >> 2;
   constexpr int kCols = C::kTileN * 4 / C::kEpiWarps;  // of the result, a warp's share
   constexpr int kStep = C::kPair ? 16 : 32;
   const uint32_t empty = ptx::first_of_pair<CG>(bars + kAccEmpty), gu_empty = ptx::first_of_pair<CG>(bars + kGuEmpty);
   uint32_t it = 0;
-  for (int i = blockIdx.x / CG; i < units; i += gridDim.x / CG, ++it) {
-    const Unit u = unit_at<C::kTileN, CG>(a, i, rank);
+  for (Units<C::kTileN> units(a, rank); units.left(); units.next(), ++it) {
+    const Unit u = units.get();
     const uint32_t buf = it & 1, round = (it >> 1) & 1;
     if (!bounded_wait_warp(bars + kAccFull + buf, round, abort_flag, a.status, kWaitNs)) return;
     ptx::tc_fence_after();
@@ -315,9 +298,14 @@ __global__ void __launch_bounds__(Cfg<OP, BN, CG>::kThreads, 1)
   ptx::successor_may_start();
   if (a.follows) ptx::predecessor_done();
   const uint32_t tmem = tmem_slot;
-  if (warp == 0) produce<OP, BN, CG>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
-  else if (warp == 1 && rank == 0) issue<OP, BN, CG>(a, sm, bars, tmem, abort_flag);
-  else if (warp >= 4) finish<OP, BN, CG, ACT>(a, bars, tmem, abort_flag, rank, warp, lane);
+  if (warp < 4) {
+    if (C::kSplitRegs) ptx::fewer_registers<C::kFewRegs>();
+    if (warp == 0) produce<OP, BN, CG>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
+    else if (warp == 1 && rank == 0) issue<OP, BN, CG>(a, sm, bars, tmem, abort_flag);
+  } else {
+    if (C::kSplitRegs) ptx::more_registers<C::kSumRegs>();
+    finish<OP, BN, CG, ACT>(a, bars, tmem, abort_flag, rank, warp, lane);
+  }
   ptx::tc_fence_before();
   __syncthreads();
   if (CG == 2) {  // nothing of one CTA's reaches into the other any more, the last commit too
@@ -353,6 +341,7 @@ cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN, CG, ACT>, C::kDynamic);
   if (e != cudaSuccess) return e;
+  if (C::kSplitRegs && !launched_with(k_dense<OP, BN, CG, ACT>, C::kRegs)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + C::kTileM - 1) / C::kTileM;
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;

@@ -13,7 +13,7 @@
 #include <atomic>
 
 #include "dense.cuh"
-#include "dense_epilogue.cuh"
+#include "dense_device.cuh"
 #include "few.cuh"
 #include "launchers.cuh"
 #include "ptx_sm103.cuh"

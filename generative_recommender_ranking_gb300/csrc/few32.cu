@@ -3,7 +3,7 @@
 // Every weight is used once for each row, so the weights' bytes bound the time: a lane multiplies four
 // neighbouring values of a weight row with each token row; a block's eight warps share the summed axis
 // and are added up in their order.  (Past eight rows the tensor cores take over, dense_fp32.cu.)
-#include "dense_epilogue.cuh"
+#include "dense_device.cuh"
 #include "few.cuh"
 #include "launchers.cuh"
 

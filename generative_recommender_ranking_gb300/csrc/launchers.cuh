@@ -2,6 +2,8 @@
 #pragma once
 
 #include <atomic>
+#include <map>
+#include <mutex>
 
 #include <cuda.h>
 
@@ -58,6 +60,23 @@ cudaError_t launch_pairs(int cluster, bool early, void (*fn)(P...), int blocks, 
   }
   cfg.attrs = at;
   return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
+// Whether a kernel's threads are launched with so many registers (asked once a kernel: one that splits more
+// among its warpgroups than it was launched with would wait for them forever).
+template <typename... P>
+bool launched_with(void (*fn)(P...), int regs) {
+  static std::mutex mu;
+  static std::map<void (*)(P...), int> known;
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = known.find(fn);
+  if (it == known.end()) {
+    cudaFuncAttributes at{};
+    const OutsideCapture now;
+    if (cudaFuncGetAttributes(&at, fn) != cudaSuccess) return false;
+    it = known.emplace(fn, at.numRegs).first;
+  }
+  return it->second == regs;
 }
 
 // prologue_ok (may be null) is recorded on st once the RoPE prologue, on another stream,

@@ -17,7 +17,7 @@
 #include <atomic>
 
 #include "dense.cuh"
-#include "dense_epilogue.cuh"
+#include "dense_device.cuh"
 #include "launchers.cuh"
 #include "ptx_sm103.cuh"
 #include "quantize.cuh"
@@ -163,13 +163,13 @@ constexpr uint32_t kTmem = 512;               // two buffers of a block's sums
 
 enum { kFull = 0, kEmpty = 6, kAccFull = 12, kAccEmpty = 14, kParts = 16, kDone = 17, kBars = 18 };
 
-// Tile t's first row in this CTA and column of the result.
+// A pair's tile: this CTA's first row and the column tile.
 struct Tile {
   long long m0;
-  int n;  // column tile
+  int n;
 };
-__device__ __forceinline__ Tile tile_at(const ScaledArgs& a, int t, uint32_t rank) {
-  const int2 at = band_tile(t, a.tiles_m, a.tiles_n);
+__device__ __forceinline__ Tile tile_at(const TileWalk& walk, uint32_t rank) {
+  const int2 at = walk.at();
   return {((long long)at.x * 2 + rank) * kTile, at.y};
 }
 
@@ -178,8 +178,9 @@ __device__ void produce(const ScaledArgs& a, const CUtensorMap* ma, const CUtens
                         volatile int* abort_flag, uint32_t rank, int lane) {
   const int tiles = a.tiles_m * a.tiles_n;
   uint32_t n = 0;
-  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
-    const Tile at = tile_at(a, t, rank);
+  TileWalk walk(blockIdx.x / 2, a.tiles_m, a.tiles_n);
+  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, walk.advance(gridDim.x / 2)) {
+    const Tile at = tile_at(walk, rank);
     // gated: the gate's columns are the first CTA's rows of B, up's the second's
     const int nb = GATED ? at.n * (kBN / 2) + (rank ? a.N : 0) : at.n * kBN + (int)rank * (kBN / 2);
     for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
@@ -255,8 +256,9 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
   const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
   const bool aligned = (a.kblocks & 3) == 0;  // (a.a_scale is on a 16-byte boundary)
   uint32_t n = 0, it = 0;
-  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, ++it) {
-    const Tile at = tile_at(a, t, rank);
+  TileWalk walk(blockIdx.x / 2, a.tiles_m, a.tiles_n);
+  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, walk.advance(gridDim.x / 2), ++it) {
+    const Tile at = tile_at(walk, rank);
     const long long row = at.m0 + quad * 32 + lane;
     const bool in = row < a.M;
     const float* sa = a.a_scale + (in ? row : 0) * a.kblocks;
@@ -397,13 +399,7 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int 
   const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED, ACT>, kDynamic);
   if (e != cudaSuccess) return e;
   const int tn = GATED ? kBN / 2 : kBN;
-  // (a block launched with fewer registers than the split counts on would wait for them forever)
-  static const int regs = [] {
-    cudaFuncAttributes at{};
-    const OutsideCapture now;
-    return cudaFuncGetAttributes(&at, k_scaled<GATED, ACT>) == cudaSuccess ? at.numRegs : 0;
-  }();
-  if (regs != kRegs) return cudaErrorInvalidConfiguration;
+  if (!launched_with(k_scaled<GATED, ACT>, kRegs)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + 2 * kTile - 1) / (2 * kTile);
   a.tiles_n = (a.N + tn - 1) / tn;
   const int tiles = a.tiles_m * a.tiles_n, places = num_sms / 2;

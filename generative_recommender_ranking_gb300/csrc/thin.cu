@@ -11,7 +11,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
-#include "dense_epilogue.cuh"
+#include "dense_device.cuh"
 #include "few.cuh"
 #include "launchers.cuh"
 
