@@ -24,9 +24,9 @@ struct DenseArgs {
   int act;              // rec_attn_activation
   int wide;             // the outputs' rows start on 32-byte boundaries
   int follows;          // behind a kernel of the same call: launched before that one has ended
-  void* out;            // kGlu: h; kOut, kDx: the result; kDglu: p; kDw: the result (one split)
+  void* out;            // kGlu: h; kOut, kDx: the result; kDglu: p; kDw: the result (of one split)
   void* out2;           // kDglu: h
-  float* part;          // kDw: [splits][M][N] sums of parts (more than one split)
+  float* part;          // kOut, kDx, kDw: [splits][M][N] sums of parts (more than one split)
   int* status;
 };
 
@@ -56,8 +56,9 @@ bool encode_planes(CUtensorMap* m, const Planes& a, int box_rows);
 cudaError_t launch_dense32(DenseOp op, const CUtensorMap (&maps)[4], Dense32Args a, int num_sms, cudaStream_t st);
 int dense32_splits(int M, int N, int kblocks, int num_sms);
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&maps)[4], DenseArgs a, int num_sms, cudaStream_t st);
-// kDw: parts of the summed axis.
-int dense_splits(int M, int N, int kblocks, int num_sms);
+// Parts of the summed axis for a product in tiles of 256 x 256; block_us: what one of its blocks takes.
+constexpr double kBlockUs = 0.4, kScaledBlockUs = 0.5;
+int dense_splits(int M, int N, int kblocks, double block_us, int num_sms);
 // (launched behind the kernel that wrote the parts, before that one has ended)
 cudaError_t launch_dense_sum(const float* part, void* out, long long n, int splits, int dtype, cudaStream_t st);
 

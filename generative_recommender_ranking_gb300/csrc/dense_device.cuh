@@ -184,15 +184,15 @@ struct Unit {
 };
 
 // A pair's units in turn; m0: this CTA's first row.  (Parts of the summed axis: all tiles of one, then of the
-// next; the first a.kblocks % a.splits parts have a block more.)
-template <int TN>
+// next; the first a.kblocks % a.splits parts have a block more.  PARTS false: there is one.)
+template <int TN, typename Args, bool PARTS = true>
 struct Units {
-  const DenseArgs& a;
+  const Args& a;
   int i, n, step, tiles, split;
   uint32_t rank;
   TileWalk walk;
-  __device__ __forceinline__ Units(const DenseArgs& args, uint32_t r)
-      : a(args), i((int)blockIdx.x / 2), n(args.tiles_m * args.tiles_n * args.splits), step((int)gridDim.x / 2),
+  __device__ __forceinline__ Units(const Args& args, uint32_t r)
+      : a(args), i((int)blockIdx.x / 2), n(args.tiles_m * args.tiles_n * (PARTS ? args.splits : 1)), step((int)gridDim.x / 2),
         tiles(args.tiles_m * args.tiles_n), split(0), rank(r), walk(i, args.tiles_m, args.tiles_n) {
     settle();
   }
@@ -203,17 +203,20 @@ struct Units {
     settle();
   }
   __device__ __forceinline__ void settle() {  // a walk past the tiles goes on in the next part
-    if (a.splits == 1 || i < (split + 1) * tiles || i >= n) return;
+    if (!PARTS || a.splits == 1 || i < (split + 1) * tiles || i >= n) return;
     split = i / tiles;
     walk = TileWalk(i - split * tiles, a.tiles_m, a.tiles_n);
   }
   __device__ __forceinline__ Unit get() const {
     const int2 at = walk.at();
-    const int q = a.kblocks / a.splits, more = a.kblocks - q * a.splits;
     Unit u;
     u.split = split;
     u.m0 = (at.x * 2 + (int)rank) * kTile;
     u.n0 = at.y * TN;
+    u.kb0 = 0;
+    u.kb1 = a.kblocks;
+    if (!PARTS) return u;
+    const int q = a.kblocks / a.splits, more = a.kblocks - q * a.splits;
     u.kb0 = split * q + min(split, more);
     u.kb1 = u.kb0 + q + (split < more ? 1 : 0);
     return u;

@@ -54,7 +54,7 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
                         const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, uint32_t rank, int lane) {
   using C = Cfg<OP>;
   uint32_t n = 0;
-  for (Units<C::kCols> units(a, rank); units.left(); units.next()) {
+  for (Units<C::kCols, DenseArgs> units(a, rank); units.left(); units.next()) {
     const Unit u = units.get();
     const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
     for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
@@ -112,7 +112,7 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
   const bool el = ptx::elect_one();
   constexpr uint32_t rank = 0;  // the first CTA issues for both
   uint32_t n = 0;
-  for (Units<C::kCols> units(a, rank); units.left(); units.next()) {
+  for (Units<C::kCols, DenseArgs> units(a, rank); units.left(); units.next()) {
     const Unit u = units.get();
     for (int kb = OP == DenseOp::kDglu ? -a.kblocks : u.kb0; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
@@ -207,7 +207,7 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
   };
-  for (Units<C::kCols> units(a, rank); units.left(); units.next()) {
+  for (Units<C::kCols, DenseArgs> units(a, rank); units.left(); units.next()) {
     const Unit u = units.get();
     float x0[32], x1[32], dh[OP == DenseOp::kDglu ? 32 : 1];
 #pragma unroll

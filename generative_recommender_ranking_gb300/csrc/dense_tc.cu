@@ -9,8 +9,8 @@
 //  - kDglu: nothing of the forward is kept; g and u are summed again (256 columns) beside
 //    dh = dy w_out (128 columns).  dh has two buffers and goes first: while it is summed for the
 //    next tile the epilogue reads this tile's g and u, which have one.
-//  - kDw sums over the rows; the rows are split into parts so that all SMs have work, the parts'
-//    sums are added in a fixed order (k_dense_sum).
+//  - kDw sums over the rows; they (of kOut and kDx the summed axis, where tiles are few) are split into
+//    parts so that all SMs have work, and the parts' sums are added in a fixed order (k_dense_sum).
 // Sums are fp32; h and p are rounded to bf16 once, as operands of the next product.
 #include <atomic>
 
@@ -72,7 +72,7 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
                         const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, uint32_t rank, int lane) {
   using C = Cfg<OP, BN, CG>;
   uint32_t n = 0;
-  for (Units<C::kTileN> units(a, rank); units.left(); units.next()) {
+  for (Units<C::kTileN, DenseArgs> units(a, rank); units.left(); units.next()) {
     const Unit u = units.get();
     const int first = OP == DenseOp::kDglu ? a.kblocks : 0;  // blocks of dy and w_out before those of x and w_in
     for (int kb = u.kb0 - first; kb < u.kb1; ++kb, ++n) {
@@ -133,7 +133,7 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
   const bool el = ptx::elect_one();
   constexpr uint32_t rank = 0;  // the first CTA issues for both
   uint32_t n = 0, it = 0;
-  for (Units<C::kTileN> units(a, rank); units.left(); units.next(), ++it) {
+  for (Units<C::kTileN, DenseArgs> units(a, rank); units.left(); units.next(), ++it) {
     const Unit u = units.get();
     const uint32_t buf = it & 1, round = (it >> 1) & 1;
     if (!bounded_wait_warp(bars + kAccEmpty + buf, round ^ 1, abort_flag, a.status, kWaitNs)) goto out;
@@ -184,7 +184,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
   constexpr int kStep = C::kPair ? 16 : 32;
   const uint32_t empty = ptx::first_of_pair<CG>(bars + kAccEmpty), gu_empty = ptx::first_of_pair<CG>(bars + kGuEmpty);
   uint32_t it = 0;
-  for (Units<C::kTileN> units(a, rank); units.left(); units.next(), ++it) {
+  for (Units<C::kTileN, DenseArgs> units(a, rank); units.left(); units.next(), ++it) {
     const Unit u = units.get();
     const uint32_t buf = it & 1, round = (it >> 1) & 1;
     if (!bounded_wait_warp(bars + kAccFull + buf, round, abort_flag, a.status, kWaitNs)) return;
@@ -243,7 +243,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         uint32_t r[32];
         ptx::tmem_ld32(lanes + buf * BN + c, r);
         if (c + kStep >= kCols) give_back(empty + 8 * buf);
-        if (OP == DenseOp::kDw && a.splits > 1) {
+        if (a.splits > 1) {
           if (in) {
             float4* dst = reinterpret_cast<float4*>(a.part + ((long long)u.split * a.M + row) * a.N + col);
 #pragma unroll
@@ -370,15 +370,15 @@ int* dense_status() {
   return static_cast<int*>(p);
 }
 
-// The parts that take the least time: rounds of the pairs of SMs times a part's blocks (0.4 us each), and the
-// parts' sums written and read.
-int dense_splits(int M, int N, int kblocks, int num_sms) {
+// The parts that take the least time: rounds of the pairs of SMs times a part's blocks, and the parts' sums
+// written and read.
+int dense_splits(int M, int N, int kblocks, double block_us, int num_sms) {
   const long long tiles = (long long)((M + 255) / 256) * ((N + 255) / 256), places = num_sms / 2;
   int best = 1;
   double least = 1e300;
   for (int s = 1; s <= 64 && s <= kblocks; ++s) {
     const long long rounds = (tiles * s + places - 1) / places;
-    const double us = rounds * (0.4 * ((kblocks + s - 1) / s) + 1) + (s > 1 ? s * 8e-6 / 5 * M * N + 3 : 0);
+    const double us = rounds * (block_us * ((kblocks + s - 1) / s) + 1) + (s > 1 ? s * 8e-6 / 5 * M * N + 3 : 0);
     if (us < least) {
       least = us;
       best = s;

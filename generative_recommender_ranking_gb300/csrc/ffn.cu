@@ -68,6 +68,13 @@ cudaError_t dense(DenseOp op, const DenseArgs& a, int sms, cudaStream_t st, bool
   return encoded ? launch_dense(op, m, a, sms, st) : cudaErrorInvalidValue;
 }
 
+// A product whose summed axis may be in parts.
+cudaError_t summed(DenseOp op, const DenseArgs& a, int sms, cudaStream_t st, bool encoded, const CUtensorMap (&m)[4]) {
+  const cudaError_t e = dense(op, a, sms, st, encoded, m);
+  return e == cudaSuccess && a.splits > 1
+             ? launch_dense_sum(a.part, a.out, (long long)a.M * a.N, a.splits, REC_ATTN_BF16, st) : e;
+}
+
 // fp32 matrices as bf16 planes, laid out one after the other in a workspace.
 struct PlaneLayout {
   size_t bytes = 0;
@@ -216,8 +223,10 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
   if (rows <= (bf16 ? kFewRows : kFewRows32))
     return from_cuda(ffn_few(bf16, activation, rows, width, hidden, x, w_in, w_out, y, dev, sms, st));
   if (!bf16) return from_cuda(ffn32_fwd(activation, rows, width, hidden, x, w_in, w_out, y, dev, sms, st));
+  const int s_out = dense_splits((int)rows, (int)width, blocks64(hidden), kBlockUs, sms);
+  const size_t off_part = ws_up(rows * hidden * es);
   Workspace ws(st);
-  e = ws.take(dev, rows * hidden * es);
+  e = ws.take(dev, off_part + (s_out > 1 ? 4 * (size_t)s_out * rows * width : 0));
   if (e != cudaSuccess) return from_cuda(e);
   CUtensorMap m[4];
   DenseArgs a{};
@@ -233,12 +242,14 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_fwd(int32_t dtype, int32_t activation,
             encode_dense(&m[0], x, rows, width, false) && encode_dense(&m[1], w_in, 2 * hidden, width, false), m);
   a.N = (int)width;
   a.kblocks = blocks64(hidden);
+  a.splits = s_out;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws.p) + off_part);
   a.out = y;
   a.wide = wide_rows(y, width);
   a.follows = 1;
   if (e == cudaSuccess)
-    e = dense(DenseOp::kOut, a, sms, st,
-              encode_dense(&m[0], ws.p, rows, hidden, false) && encode_dense(&m[1], w_out, width, hidden, false), m);
+    e = summed(DenseOp::kOut, a, sms, st,
+               encode_dense(&m[0], ws.p, rows, hidden, false) && encode_dense(&m[1], w_out, width, hidden, false), m);
   const cudaError_t ef = ws.give_back();
   return from_cuda(e != cudaSuccess ? e : ef);
 }
@@ -269,8 +280,10 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
   if (dtype == REC_ATTN_FP32)
     return from_cuda(ffn32_bwd(activation, rows, width, hidden, x, w_in, w_out, dy, dx, dw_in, dw_out, dev, sms, st));
   const int kr = blocks64(rows), W = (int)width, H = (int)hidden;
-  const int si = dw_in ? dense_splits(2 * H, W, kr, sms) : 1, so = dw_out ? dense_splits(W, H, kr, sms) : 1;
-  const size_t n_part = std::max(si > 1 ? (size_t)si * 2 * H * W : 0, so > 1 ? (size_t)so * H * W : 0);
+  const int sx = dx ? dense_splits((int)rows, W, blocks64(2 * hidden), kBlockUs, sms) : 1;
+  const int si = dw_in ? dense_splits(2 * H, W, kr, kBlockUs, sms) : 1, so = dw_out ? dense_splits(W, H, kr, kBlockUs, sms) : 1;
+  const size_t n_part = std::max({sx > 1 ? (size_t)sx * rows * W : 0, si > 1 ? (size_t)si * 2 * H * W : 0,
+                                  so > 1 ? (size_t)so * H * W : 0});
   const size_t off_h = ws_up(rows * 2 * hidden * es), off_part = off_h + ws_up(rows * hidden * es);
   Workspace ws(st);
   e = ws.take(dev, off_part + 4 * n_part);
@@ -299,8 +312,9 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     a.kblocks = blocks64(2 * hidden);
     a.out = dx;
     a.wide = wide_rows(dx, width);
-    e = dense(DenseOp::kDx, a, sms, st,
-              encode_dense(&m[0], p, rows, 2 * hidden, false) && encode_dense(&m[1], w_in, 2 * hidden, width, true), m);
+    a.splits = sx;
+    e = summed(DenseOp::kDx, a, sms, st,
+               encode_dense(&m[0], p, rows, 2 * hidden, false) && encode_dense(&m[1], w_in, 2 * hidden, width, true), m);
   }
   a.kblocks = kr;
   for (int i = 0; i < 2; ++i) {
@@ -311,11 +325,10 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     a.splits = i ? so : si;
     a.out = dw;
     a.wide = wide_rows(dw, a.N);
-    e = dense(DenseOp::kDw, a, sms, st,
-              (i ? encode_dense(&m[0], dy, rows, width, true) && encode_dense(&m[1], h, rows, hidden, true)
-                 : encode_dense(&m[0], p, rows, 2 * hidden, true) && encode_dense(&m[1], x, rows, width, true)),
-              m);
-    if (e == cudaSuccess && a.splits > 1) e = launch_dense_sum(a.part, dw, (long long)a.M * a.N, a.splits, dtype, st);
+    e = summed(DenseOp::kDw, a, sms, st,
+               (i ? encode_dense(&m[0], dy, rows, width, true) && encode_dense(&m[1], h, rows, hidden, true)
+                  : encode_dense(&m[0], p, rows, 2 * hidden, true) && encode_dense(&m[1], x, rows, width, true)),
+               m);
   }
   const cudaError_t ef = ws.give_back();
   return from_cuda(e != cudaSuccess ? e : ef);
@@ -331,7 +344,8 @@ bool scaled_tiles_ok(long long rows, long long cols) {  // a launch's tiles are 
 
 // The product of one scaled layer.
 cudaError_t scaled(bool gated, const void* a, const float* a_scale, long long rows, const void* b, const float* b_scale,
-                   long long cols, long long depth, int act, void* out, float* out_scale, bool follows, int sms, cudaStream_t st) {
+                   long long cols, long long depth, int act, void* out, float* out_scale, bool follows, int splits, float* part, int sms,
+                   cudaStream_t st) {
   CUtensorMap ma, mb;
   if (!encode_scaled(&ma, a, rows, depth) || !encode_scaled(&mb, b, gated ? 2 * cols : cols, depth))
     return cudaErrorInvalidValue;
@@ -346,8 +360,11 @@ cudaError_t scaled(bool gated, const void* a, const float* a_scale, long long ro
   s.out = out;
   s.out_scale = out_scale;
   s.follows = follows;
+  s.splits = splits;
+  s.part = part;
   s.status = dense_status();
-  return launch_scaled(gated, ma, mb, s, sms, st);
+  const cudaError_t e = launch_scaled(gated, ma, mb, s, sms, st);
+  return e == cudaSuccess && splits > 1 ? launch_dense_sum(part, out, rows * cols, splits, REC_ATTN_BF16, st) : e;
 }
 
 }  // namespace
@@ -391,7 +408,13 @@ REC_ATTN_API rec_attn_status rec_attn_scaled_matmul(int64_t rows, int64_t cols, 
   if (rows <= kFewRows)
     return from_cuda(launch_few(true, false, {(int)rows, (int)cols, (int)depth, a, a_scale, b, b_scale, 0, y, nullptr, 0,
                                               dense_status()}, sms, st));
-  return from_cuda(scaled(false, a, a_scale, rows, b, b_scale, cols, depth, 0, y, nullptr, false, sms, st));
+  const int s = dense_splits((int)rows, (int)cols, (int)kb, kScaledBlockUs, sms);
+  Workspace ws(st);
+  cudaError_t ew = s > 1 ? ws.take(dev, 4 * (size_t)s * rows * cols) : cudaSuccess;
+  if (ew == cudaSuccess)
+    ew = scaled(false, a, a_scale, rows, b, b_scale, cols, depth, 0, y, nullptr, false, s, static_cast<float*>(ws.p), sms, st);
+  const cudaError_t ef = ws.give_back();
+  return from_cuda(ew != cudaSuccess ? ew : ef);
 }
 
 REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t rows, int64_t width, int64_t hidden,
@@ -416,8 +439,10 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool few = rows <= kFewRows;
   const size_t off_xs = ws_up(n), off_h = off_xs + ws_up(4 * rows * kw), off_hs = off_h + ws_up(rows * hidden);
+  const int s = few ? 1 : dense_splits((int)rows, (int)width, (int)kh, kScaledBlockUs, sms);
+  const size_t off_part = off_hs + ws_up(4 * rows * kh);
   Workspace ws(st);
-  e = ws.take(dev, off_hs + 4 * rows * kh);
+  e = ws.take(dev, off_part + (s > 1 ? 4 * (size_t)s * n : 0));
   if (e != cudaSuccess) return from_cuda(e);
   uint8_t* const xq = static_cast<uint8_t*>(ws.p);
   float* const xs = reinterpret_cast<float*>(xq + off_xs);
@@ -430,8 +455,10 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t
     if (e == cudaSuccess) e = launch_few(true, true, {R, H, W, xq, xs, w_in, w_in_scale, activation, hq, hs, 1, word}, sms, st);
     if (e == cudaSuccess) e = launch_few(true, false, {R, W, H, hq, hs, w_out, w_out_scale, 0, y, nullptr, 1, word}, sms, st);
   } else {
-    if (e == cudaSuccess) e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, true, sms, st);
-    if (e == cudaSuccess) e = scaled(false, hq, hs, rows, w_out, w_out_scale, width, hidden, 0, y, nullptr, true, sms, st);
+    if (e == cudaSuccess) e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, true, 1, nullptr, sms, st);
+    if (e == cudaSuccess)
+      e = scaled(false, hq, hs, rows, w_out, w_out_scale, width, hidden, 0, y, nullptr, true, s,
+                 reinterpret_cast<float*>(xq + off_part), sms, st);
   }
   const cudaError_t ef = ws.give_back();
   return from_cuda(e != cudaSuccess ? e : ef);

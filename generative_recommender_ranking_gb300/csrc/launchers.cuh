@@ -69,14 +69,16 @@ bool launched_with(void (*fn)(P...), int regs) {
   static std::mutex mu;
   static std::map<void (*)(P...), int> known;
   std::lock_guard<std::mutex> lk(mu);
-  auto it = known.find(fn);
-  if (it == known.end()) {
-    cudaFuncAttributes at{};
-    const OutsideCapture now;
-    if (cudaFuncGetAttributes(&at, fn) != cudaSuccess) return false;
-    it = known.emplace(fn, at.numRegs).first;
+  const auto it = known.find(fn);
+  if (it != known.end()) return it->second == regs;
+  cudaFuncAttributes at{};
+  const OutsideCapture now;
+  if (cudaFuncGetAttributes(&at, fn) != cudaSuccess) return false;
+  try {
+    known[fn] = at.numRegs;
+  } catch (...) {  // asked again by the next call
   }
-  return it->second == regs;
+  return at.numRegs == regs;
 }
 
 // prologue_ok (may be null) is recorded on st once the RoPE prologue, on another stream,

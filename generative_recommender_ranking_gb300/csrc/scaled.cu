@@ -163,34 +163,26 @@ constexpr uint32_t kTmem = 512;               // two buffers of a block's sums
 
 enum { kFull = 0, kEmpty = 6, kAccFull = 12, kAccEmpty = 14, kParts = 16, kDone = 17, kBars = 18 };
 
-// A pair's tile: this CTA's first row and the column tile.
-struct Tile {
-  long long m0;
-  int n;
-};
-__device__ __forceinline__ Tile tile_at(const TileWalk& walk, uint32_t rank) {
-  const int2 at = walk.at();
-  return {((long long)at.x * 2 + rank) * kTile, at.y};
-}
+// A pair's tiles (parts of their summed axis) in turn; n0: the first column of the result.
+template <bool GATED, bool PARTS>
+using Work = Units<GATED ? kBN / 2 : kBN, ScaledArgs, PARTS>;
 
-template <bool GATED>
+template <bool GATED, bool PARTS>
 __device__ void produce(const ScaledArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, uint8_t* sm, uint64_t* bars,
                         volatile int* abort_flag, uint32_t rank, int lane) {
-  const int tiles = a.tiles_m * a.tiles_n;
   uint32_t n = 0;
-  TileWalk walk(blockIdx.x / 2, a.tiles_m, a.tiles_n);
-  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, walk.advance(gridDim.x / 2)) {
-    const Tile at = tile_at(walk, rank);
+  for (Work<GATED, PARTS> work(a, rank); work.left(); work.next()) {
+    const Unit u = work.get();
     // gated: the gate's columns are the first CTA's rows of B, up's the second's
-    const int nb = GATED ? at.n * (kBN / 2) + (rank ? a.N : 0) : at.n * kBN + (int)rank * (kBN / 2);
-    for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
+    const int nb = u.n0 + (rank ? (GATED ? a.N : kBN / 2) : 0);
+    for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
       if (!bounded_wait_warp(bars + kEmpty + st, ((n / kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (ptx::elect_one()) {
         uint8_t* s = sm + st * kStage;
         const uint32_t bar = ptx::first_of_pair<2>(bars + kFull + st);
         if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * kStage);  // the bytes of both CTAs
-        ptx::tma_load_2d_pair<2>(s, ma, kb * 128, (int)at.m0, bar);
+        ptx::tma_load_2d_pair<2>(s, ma, kb * 128, u.m0, bar);
         ptx::tma_load_2d_pair<2>(s + kSlab, mb, kb * 128, nb, bar);
       }
       __syncwarp();
@@ -205,14 +197,15 @@ out:
 }
 
 // The first CTA issues for both.
+template <bool GATED, bool PARTS>
 __device__ __forceinline__ void issue(const ScaledArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem,
                                       volatile int* abort_flag) {
-  const int tiles = a.tiles_m * a.tiles_n;
   const uint32_t s0 = ptx::smem_u32(sm), idesc = ptx::idesc_e4m3_f32(2 * kTile, kBN);
   const bool el = ptx::elect_one();
   uint32_t n = 0;
-  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
-    for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
+  for (Work<GATED, PARTS> work(a, 0); work.left(); work.next()) {
+    const Unit u = work.get();
+    for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
       const uint32_t buf = n & 1;
       if (!bounded_wait_warp(bars + kAccEmpty + buf, ((n >> 1) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
@@ -247,23 +240,21 @@ __device__ __forceinline__ float4 next_scales(const float* s, int n, bool aligne
 
 // Sixteen warps: a thread has one row and a quarter of the tile's columns (gated: 32 gate columns and
 // the 32 up columns that belong to them).
-template <bool GATED, int ACT>
+template <bool GATED, int ACT, bool PARTS>
 __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, float* s_top,
                        uint32_t rank, int warp, int lane) {
-  const int tiles = a.tiles_m * a.tiles_n;
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
   const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
   const bool aligned = (a.kblocks & 3) == 0;  // (a.a_scale is on a 16-byte boundary)
   uint32_t n = 0, it = 0;
-  TileWalk walk(blockIdx.x / 2, a.tiles_m, a.tiles_n);
-  for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2, walk.advance(gridDim.x / 2), ++it) {
-    const Tile at = tile_at(walk, rank);
-    const long long row = at.m0 + quad * 32 + lane;
+  for (Work<GATED, PARTS> work(a, rank); work.left(); work.next(), ++it) {
+    const Unit u = work.get();
+    const long long row = u.m0 + quad * 32 + lane;
     const bool in = row < a.M;
     const float* sa = a.a_scale + (in ? row : 0) * a.kblocks;
     // the scales of this thread's first and second 32 columns' block
-    const int nb = GATED ? at.n : 2 * at.n + (part >> 1);
+    const int nb = u.n0 / 128 + (GATED ? 0 : part >> 1);
     const bool nb_in = GATED || (long long)nb * 128 < a.N;
     const float* sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
     const float* sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
@@ -271,8 +262,8 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
     f32x2 sums[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) sums[e] = 0ull;
-    for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
-      if ((kb & 3) == 0) s4 = next_scales(sa + kb, a.kblocks - kb, aligned);
+    for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
+      if ((kb & 3) == 0 || (PARTS && kb == u.kb0)) s4 = next_scales(sa + (kb & ~3), a.kblocks - (kb & ~3), aligned);
       const float sk = (kb & 2) ? (kb & 1 ? s4.w : s4.z) : (kb & 1 ? s4.y : s4.x);
       const float f0 = sk * __ldg(sb0 + kb), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
       const uint32_t buf = n & 1;
@@ -322,25 +313,32 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           w[e] = pack_e4m3(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv, fine);
-        ptx::st_global_v8(static_cast<uint8_t*>(a.out) + row * a.N + at.n * 128 + part * 32, w[0], w[1], w[2], w[3], w[4],
+        ptx::st_global_v8(static_cast<uint8_t*>(a.out) + row * a.N + u.n0 + part * 32, w[0], w[1], w[2], w[3], w[4],
                           w[5], w[6], w[7]);
-        if (part == 0) a.out_scale[row * (a.N / 128) + at.n] = scale;
+        if (part == 0) a.out_scale[row * (a.N / 128) + u.n0 / 128] = scale;
       }
     } else {
-      const int col0 = at.n * kBN + part * 64;
+      const int col0 = u.n0 + part * 64;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int col = col0 + 16 * c;
-        uint32_t w[8];
+        if constexpr (PARTS) {
+          ulonglong2* const dst = reinterpret_cast<ulonglong2*>(a.part + ((long long)u.split * a.M + row) * a.N + col);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(sums[8 * c + e]);
-        if (in && col < a.N) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, a.N - col, a.wide);
+          for (int e = 0; e < 4; ++e)
+            if (in && col + 4 * e < a.N) dst[e] = make_ulonglong2(sums[8 * c + 2 * e], sums[8 * c + 2 * e + 1]);
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = pack_bf16(sums[8 * c + e]);
+          if (in && col < a.N) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, a.N - col, a.wide);
+        }
       }
     }
   }
 }
 
-template <bool GATED, int ACT>
+template <bool GATED, int ACT, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     k_scaled(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const ScaledArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -375,11 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.follows) ptx::predecessor_done();
   if (warp < 4) {
     ptx::fewer_registers<kFewRegs>();
-    if (warp == 0) produce<GATED>(a, &ma, &mb, sm, bars, abort_flag, rank, lane);
-    else if (warp == 1 && rank == 0) issue(a, sm, bars, tmem, abort_flag);
+    if (warp == 0) produce<GATED, PARTS>(a, &ma, &mb, sm, bars, abort_flag, rank, lane);
+    else if (warp == 1 && rank == 0) issue<GATED, PARTS>(a, sm, bars, tmem, abort_flag);
   } else {
     ptx::more_registers<kSumRegs>();
-    finish<GATED, ACT>(a, bars, tmem, abort_flag, s_top, rank, warp, lane);
+    finish<GATED, ACT, PARTS>(a, bars, tmem, abort_flag, s_top, rank, warp, lane);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -393,17 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool GATED, int ACT>
+template <bool GATED, int ACT, bool PARTS>
 cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED, ACT>, kDynamic);
+  const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED, ACT, PARTS>, kDynamic);
   if (e != cudaSuccess) return e;
   const int tn = GATED ? kBN / 2 : kBN;
-  if (!launched_with(k_scaled<GATED, ACT>, kRegs)) return cudaErrorInvalidConfiguration;
+  if (!launched_with(k_scaled<GATED, ACT, PARTS>, kRegs)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + 2 * kTile - 1) / (2 * kTile);
   a.tiles_n = (a.N + tn - 1) / tn;
-  const int tiles = a.tiles_m * a.tiles_n, places = num_sms / 2;
-  return launch_pairs(2, a.follows != 0, k_scaled<GATED, ACT>, (tiles < places ? tiles : places) * 2, kThreads, kDynamic, st, ma, mb, a);
+  const int tiles = a.tiles_m * a.tiles_n * (PARTS ? a.splits : 1), places = num_sms / 2;
+  return launch_pairs(2, a.follows != 0, k_scaled<GATED, ACT, PARTS>, (tiles < places ? tiles : places) * 2, kThreads, kDynamic, st, ma, mb, a);
 }
 
 }  // namespace
@@ -426,9 +424,9 @@ cudaError_t launch_quantize(const QuantArgs& a, int dtype, int block_rows, int n
 
 cudaError_t launch_scaled(bool gated, const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int num_sms,
                           cudaStream_t st) {
-  if (!gated) return run<false, 0>(ma, mb, a, num_sms, st);
-  return a.act == REC_ATTN_SILU ? run<true, REC_ATTN_SILU>(ma, mb, a, num_sms, st)
-                                : run<true, REC_ATTN_GELU>(ma, mb, a, num_sms, st);
+  if (!gated) return a.splits > 1 ? run<false, 0, true>(ma, mb, a, num_sms, st) : run<false, 0, false>(ma, mb, a, num_sms, st);
+  return a.act == REC_ATTN_SILU ? run<true, REC_ATTN_SILU, false>(ma, mb, a, num_sms, st)
+                                : run<true, REC_ATTN_GELU, false>(ma, mb, a, num_sms, st);
 }
 
 }  // namespace recattn

@@ -22,7 +22,7 @@ cudaError_t launch_quantize(const QuantArgs& a, int dtype, int block_rows, int n
 struct ScaledArgs {
   int M, N;                // of the result; gated: N = hidden, B has 2 N rows
   int kblocks;             // blocks of 128 along the summed axis
-  int tiles_m, tiles_n;
+  int tiles_m, tiles_n, splits;
   const float* a_scale;    // [M][kblocks]
   const float* b_scale;    // [blocks of B's rows][kblocks]
   int act;                 // gated
@@ -30,6 +30,7 @@ struct ScaledArgs {
   int follows;             // behind a kernel of the same call: launched before that one has ended
   void* out;               // bf16 [M][N]; gated: e4m3
   float* out_scale;        // gated: [M][N / 128]
+  float* part;             // [splits][M][N] sums of parts of the summed axis (more than one; not gated)
   int* status;
 };
 bool encode_scaled(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows = 128);

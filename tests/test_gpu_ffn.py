@@ -95,7 +95,8 @@ def run(x, dy, w_in, w_out, act, wanted=("dx", "dw_in", "dw_out")):
 
 
 SHAPES = [(1, 8, 8), (1, 512, 1024), (5, 64, 128), (127, 72, 136), (128, 128, 128), (129, 200, 72), (300, 520, 264),
-          (77, 1408, 8), (513, 256, 1000), (2000, 64, 64), (1031, 512, 1024)]
+          (77, 1408, 8), (513, 256, 1000), (2000, 64, 64), (1031, 512, 1024),
+          (90, 520, 2056), (260, 264, 4096)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])

@@ -129,7 +129,7 @@ def within(got, value, tol, name):
 PRODUCTS = [(1, 8, 16), (1, 512, 512), (3, 136, 144), (7, 4096, 256), (128, 256, 128), (129, 264, 1040), (300, 72, 2064),
             (1000, 1000, 400), (2049, 128, 640), (16, 2048, 1024), (33, 520, 4096), (8, 24, 272), (9, 136, 400),
             (17, 1160, 144), (24, 520, 1040), (25, 264, 656), (31, 2056, 528), (32, 1000, 2064), (64, 264, 400),
-            (65, 136, 1040)]
+            (65, 136, 1040), (100, 520, 4112), (300, 264, 8208)]
 
 
 @pytest.mark.parametrize("any_scale", [False, True])
@@ -151,7 +151,7 @@ def test_matmul(rows, cols, depth, any_scale):
 
 
 FFN = [(1, 16, 128), (1, 512, 1024), (5, 144, 256), (129, 512, 128), (300, 1040, 384), (1031, 512, 1024), (20, 4096, 512), (8, 272, 128), (9, 400, 640), (25, 144, 256),
-       (32, 1040, 384), (33, 272, 256), (64, 144, 640), (65, 400, 128)]
+       (32, 1040, 384), (33, 272, 256), (64, 144, 640), (65, 400, 128), (100, 528, 2048), (280, 272, 4096)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
