@@ -4,7 +4,7 @@
 // such sums is, to 2^-24 of it, that of six pairs: hi lo, mid mid, lo hi, hi mid, mid hi, hi hi (in
 // this order, small ones first).  bf16 MMAs at a sixth of their rate are still five times CUDA cores.
 // The tensor cores cut each addition's result off (measured: 2^-24 of the sum for each 16 products,
-// always towards zero), so they sum no more than a block of 64; eight warps add the blocks up in
+// always towards zero), so they sum no more than a block of 64; sixteen warps add the blocks up in
 // fp32 registers, rounded to nearest.
 // A pair of CTAs has a tile of 256 x 128 (gated: 64 gate and 64 up columns; the backward's dh 64); a
 // ring of three 64-deep stages holds all six planes, so each is loaded once.  h and p are written as
@@ -27,7 +27,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBK = 64, kSlab = 64 * 128;    // 64 rows of 128 bytes
 constexpr int kPlane = 2 * kSlab;            // 128 rows of one plane
 constexpr int kStage = 3 * (kPlane + kSlab), kStages = 3;  // 128 rows of A and this CTA's 64 of B
-constexpr int kThreads = 320, kEpiWarps = 8;
+constexpr int kEpiWarps = 16, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kRun = 16;                     // columns that a thread takes up at a time
 constexpr int kDynamic = kStages * kStage + 1024;
 constexpr uint32_t kTmem = 256;              // two buffers of a block's sums
 constexpr int kTileN = 128;
@@ -158,30 +159,42 @@ __device__ __forceinline__ void store_planes(const Planes& to, long long row, in
   for (int p = 0; p < 3; ++p, at += to.plane())
     *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(v[p][0], v[p][1]), pack_bf16(v[p][2], v[p][3]));
 }
-// 32 columns, `left` of which there are; wide: from a 32-byte boundary on (whole sectors are written: four
+// kRun columns, `left` of which there are; wide: from a 32-byte boundary on (whole sectors are written: four
 // columns at a time took three times the traffic).
-__device__ __forceinline__ void store_planes(const Planes& to, long long row, int col, const float (&x)[32], int left, bool wide) {
-  if (wide && left >= 32) {
+__device__ __forceinline__ void store_planes(const Planes& to, long long row, int col, const float (&x)[kRun], int left,
+                                             bool wide) {
+  if (wide && left >= kRun) {
+    uint32_t w[3][8];
 #pragma unroll
-    for (int c = 0; c < 32; c += 16) {
-      uint32_t w[3][8];
+    for (int e = 0; e < 8; ++e) {
+      float a[3], b[3];
+      split3(x[2 * e], a[0], a[1], a[2]);
+      split3(x[2 * e + 1], b[0], b[1], b[2]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float a[3], b[3];
-        split3(x[c + 2 * e], a[0], a[1], a[2]);
-        split3(x[c + 2 * e + 1], b[0], b[1], b[2]);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) w[p][e] = pack_bf16(a[p], b[p]);
-      }
-      char* at = static_cast<char*>(to.p) + (row * to.ld + col + c) * 2;
-#pragma unroll
-      for (int p = 0; p < 3; ++p, at += to.plane())
-        ptx::st_global_v8(at, w[p][0], w[p][1], w[p][2], w[p][3], w[p][4], w[p][5], w[p][6], w[p][7]);
+      for (int p = 0; p < 3; ++p) w[p][e] = pack_bf16(a[p], b[p]);
     }
+    char* at = static_cast<char*>(to.p) + (row * to.ld + col) * 2;
+#pragma unroll
+    for (int p = 0; p < 3; ++p, at += to.plane())
+      ptx::st_global_v8(at, w[p][0], w[p][1], w[p][2], w[p][3], w[p][4], w[p][5], w[p][6], w[p][7]);
   } else {
 #pragma unroll
-    for (int c = 0; c < 32; c += 4)
+    for (int c = 0; c < kRun; c += 4)
       if (c < left) store_planes(to, row, col + c, x[c], x[c + 1], x[c + 2], x[c + 3]);
+  }
+}
+// The same in fp32.
+__device__ __forceinline__ void store_floats(float* dst, const float (&x)[kRun], int left, bool wide) {
+  if (wide && left >= kRun) {
+#pragma unroll
+    for (int c = 0; c < kRun; c += 8)
+      ptx::st_global_v8(dst + c, __float_as_uint(x[c]), __float_as_uint(x[c + 1]), __float_as_uint(x[c + 2]),
+                        __float_as_uint(x[c + 3]), __float_as_uint(x[c + 4]), __float_as_uint(x[c + 5]),
+                        __float_as_uint(x[c + 6]), __float_as_uint(x[c + 7]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < kRun; c += 4)
+      if (c < left) *reinterpret_cast<float4*>(dst + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
   }
 }
 
@@ -190,17 +203,18 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
                        int lane) {
   using C = Cfg<OP>;
   const DenseArgs& a = aa.d;
-  const int quad = warp & 3, half = (warp - 2) >> 2;
+  const int quad = warp & 3, part = (warp - 2) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-  const int c0 = C::kPair ? 32 * half : 64 * half, c1 = C::kPair ? 64 + 32 * half : 64 * half + 32;
+  // its columns of the tile: two runs (gated: of the gate's and of up's)
+  const int c0 = C::kPair ? kRun * part : 2 * kRun * part, c1 = C::kPair ? 64 + c0 : c0 + kRun;
   const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
   uint32_t n = 0;
-  // a block's sums of 32 columns, added up
-  const auto take = [&](float (&to)[32], uint32_t buf, int col) {
-    uint32_t r[32];
-    ptx::tmem_ld32(lanes + buf * kTileN + col, r);
+  // a block's sums of a run, added up
+  const auto take = [&](float (&to)[kRun], uint32_t buf, int col) {
+    uint32_t r[kRun];
+    ptx::tmem_ld16(lanes + buf * kTileN + col, r);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) to[e] += __uint_as_float(r[e]);
+    for (int e = 0; e < kRun; ++e) to[e] += __uint_as_float(r[e]);
   };
   const auto taken = [&](uint32_t buf) {
     ptx::tc_fence_before();
@@ -209,16 +223,16 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
   };
   for (Units<C::kCols, DenseArgs> units(a, rank); units.left(); units.next()) {
     const Unit u = units.get();
-    float x0[32], x1[32], dh[OP == DenseOp::kDglu ? 32 : 1];
+    float x0[kRun], x1[kRun], dh[OP == DenseOp::kDglu ? kRun : 1];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x0[e] = x1[e] = 0.f;
+    for (int e = 0; e < kRun; ++e) x0[e] = x1[e] = 0.f;
     if constexpr (OP == DenseOp::kDglu) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) dh[e] = 0.f;
+      for (int e = 0; e < kRun; ++e) dh[e] = 0.f;
       for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
         if (!bounded_wait_warp(bars + kAccFull + (n & 1), (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
         ptx::tc_fence_after();
-        take(dh, n & 1, 32 * half);
+        take(dh, n & 1, c0);
         taken(n & 1);
       }
     }
@@ -233,10 +247,10 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
     if (row >= a.M) continue;
     if constexpr (C::kPair) {
       // in place: x0 becomes du, x1 h and dh dg
-      const int col = u.n0 + 32 * half, left = a.N - col;
+      const int col = u.n0 + c0, left = a.N - col;
       const bool wide = a.N % 16 == 0;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
+      for (int e = 0; e < kRun; ++e) {
         float slope;
         const float act = act32<ACT>(x0[e], slope), up = x1[e];
         x1[e] = act * up;
@@ -254,13 +268,9 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
       }
     } else {
       float* const out = (a.splits > 1 ? a.part + (long long)u.split * a.M * a.N : static_cast<float*>(a.out)) + row * a.N;
-#pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        if (u.n0 + c0 + e < a.N)
-          *reinterpret_cast<float4*>(out + u.n0 + c0 + e) = make_float4(x0[e], x0[e + 1], x0[e + 2], x0[e + 3]);
-        if (u.n0 + c1 + e < a.N)
-          *reinterpret_cast<float4*>(out + u.n0 + c1 + e) = make_float4(x1[e], x1[e + 1], x1[e + 2], x1[e + 3]);
-      }
+      const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+      if (u.n0 + c0 < a.N) store_floats(out + u.n0 + c0, x0, a.N - u.n0 - c0, wide);
+      if (u.n0 + c1 < a.N) store_floats(out + u.n0 + c1, x1, a.N - u.n0 - c1, wide);
     }
   }
 }
