@@ -1,8 +1,9 @@
 // dense_tc.cu -- the matrix products of the gated feed-forward block on the sm_103a tensor cores.
 //
 // y = (act(x Wg') * (x Wu')) w_out' over packed token rows, and its gradients (dense.cuh lists the
-// five products).  One persistent CTA per SM takes tiles of 128 rows; a TMA warp keeps a ring of
-// 64-deep operand blocks full, one warp issues tcgen05 MMAs into TMEM, eight or sixteen warps read a
+// five products).  A persistent pair of CTAs takes tiles of 256 x 256 (cta_group::2: each CTA loads its 128
+// rows of A and half of B, two thirds of what two single CTAs would); a TMA warp keeps a ring of 64-deep
+// operand blocks full, one warp of the first CTA issues tcgen05 MMAs into TMEM, eight or sixteen warps read a
 // finished tile out while the next one is summed.
 //  - kGlu: a tile's 256 columns are 128 gate and the 128 up columns that belong to them, so the
 //    activation and the product happen in the epilogue and neither projection reaches memory.
@@ -11,7 +12,13 @@
 //    next tile the epilogue reads this tile's g and u, which have one.
 //  - kDw sums over the rows; they (of kOut and kDx the summed axis, where tiles are few) are split into
 //    parts so that all SMs have work, and the parts' sums are added in a fixed order (k_dense_sum).
-// Sums are fp32; h and p are rounded to bf16 once, as operands of the next product.
+// Sums are fp32 in TMEM (each addition cut, 2^-24 of the sum for every 16 products: measured 3e-5 over 32768,
+// under the 2^-9 of the results' rounding); h and p are rounded to bf16 once, as operands of the next product.
+// 320016 rows of 512 x 1024 (us under ncu, rate): kGlu 348-363 (1.9 PFLOP/s, tensor pipe 85%), kOut 183-190 (1.8),
+// kDglu 660-685 (1.5; its epilogue, 8 of a tile's 10 thousand cycles, bounds it: three stores and the activation's
+// exponential and reciprocal), kDx 348-367 (1.9), kDw 354-373 and 189-197 (1.9 and 1.7).  In a loop the
+// board's power cap takes another fifth.  Single CTAs of 128 x 256: kGlu 438, kOut 231, kDx 424, kDw 544.  Clusters of two
+// pairs with A multicast between them, and fetching A into the L2 ahead, gained nothing.
 #include <atomic>
 
 #include "dense.cuh"

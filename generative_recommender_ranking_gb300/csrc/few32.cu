@@ -2,7 +2,9 @@
 //
 // Every weight is used once for each row, so the weights' bytes bound the time: a lane multiplies four
 // neighbouring values of a weight row with each token row; a block's eight warps share the summed axis
-// and are added up in their order.  (Past eight rows the tensor cores take over, dense_fp32.cu.)
+// and are added up in their order.  Past eight rows the tensor cores take over
+// (dense_fp32.cu): on 4096 x 4096 they take 174 us for any number of rows up to 200, this way 16 rows a block 111 us for
+// nine rows and 32 a block 477 for 24.
 #include "dense_device.cuh"
 #include "few.cuh"
 #include "launchers.cuh"

@@ -410,9 +410,16 @@ rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows, int64_t widt
  * Sums are fp32.  The gated product h, and in the backward p, are rounded to dtype once as
  * operands of the next product, and outputs are rounded once.  The backward computes g and u
  * again from x: nothing of the forward is kept.  Equal calls give equal bits.
- * Workspace from the library pool on `stream`: forward rows * hidden elements; backward
- * 3 * rows * hidden elements, and fp32 sums of parts of the rows, at most twice the SMs times 128
- * KB and a copy of the weights' gradients.
+ * bf16: operands of the tensor cores; outputs are off by about 2.4e-3 (relative), their own rounding
+ * being 1.7e-3 of that.  fp32: three bf16 values stand for each operand and six of their products are
+ * summed, in blocks of 64 that are added up in fp32: off by 3e-7.  x, dy and the weights must be
+ * finite for a finite result; a value that is not reaches its own row of y and dx, and dw_in and dw_out.
+ * silu's logistic function stays at 2^-60 below -41 (bf16).
+ * Workspace from the library pool on `stream`, in bytes: forward, bf16 2 * rows * hidden, fp32 6 times
+ * the elements of x, both weights and h (up to 8 rows: 4 * rows * hidden); backward, bf16 6 * rows *
+ * hidden, fp32 6 times the elements of x, dy, both weights and p and h (3 * rows * hidden); and where
+ * results have few tiles of 256 x 256, fp32 sums of parts of their summed axis, up to 64 times the
+ * result.
  * Asynchronous; both calls may be captured into a CUDA graph.
  * Errors: INVALID_ARG, UNSUPPORTED (too large), OOM, CUDA; a wait that ran out is reported by
  * rec_attn_dense_device_status.
@@ -448,7 +455,8 @@ rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation, int64_t rows
  *   (w_in_scale [2 * hidden / 128][ceil(width / 128)], w_out_scale [ceil(width / 128)]
  *   [hidden / 128]): x and the gated product h are quantized as above with a scale for 128 values
  *   of a row.  width a multiple of 16, hidden of 128.  Workspace from the library pool on
- *   `stream`: rows * (width + hidden) * (1 + 1 / 32) bytes.
+ *   `stream`: rows * (width + hidden) * (1 + 1 / 32) bytes, and as rec_attn_scaled_matmul's fp32 sums
+ *   of parts of y's summed axis where y has few tiles of 256 x 256 (up to 64 times y's elements).
  *
  * All device, contiguous, 16-byte aligned; outputs overlap nothing.  Asynchronous; the calls may
  * be captured into a CUDA graph.  Equal calls give equal bits.
