@@ -44,7 +44,8 @@ rec_attn_status check_ffn(int32_t dtype, int32_t act, int64_t rows, int64_t widt
   if (rows < 0 || width < 1 || hidden < 1 || width % unit || hidden % unit) return REC_ATTN_ERR_INVALID_ARG;
   if (rows > kMaxRows || width > kMaxWidth || hidden > kMaxWidth) return REC_ATTN_ERR_UNSUPPORTED;
   // a launch's tiles are counted in 32 bits
-  if (((rows + kTile - 1) / kTile) * ((2 * std::max(hidden, width) + kTile - 1) / kTile) > INT32_MAX / 2) return REC_ATTN_ERR_UNSUPPORTED;
+  if (((rows + kTile - 1) / kTile) * ((2 * std::max(hidden, width) + kTile - 1) / kTile) > INT32_MAX / 2)
+    return REC_ATTN_ERR_UNSUPPORTED;
   return REC_ATTN_OK;
 }
 
@@ -268,6 +269,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
   const Range all[7] = {{rows > 0 ? dx : nullptr, nx}, {dw_in, ni}, {dw_out, no}, {rows > 0 ? x : nullptr, nx},
                         {w_in, ni}, {w_out, no}, {rows > 0 ? dy : nullptr, nx}};
   if (clash(all, 3, 7)) return REC_ATTN_ERR_INVALID_ARG;
+  if (!(rows > 0 && dx) && !dw_in && !dw_out) return REC_ATTN_OK;  // nothing wanted
   int dev = -1, sms = 0;
   cudaError_t e = device_and_sms(&dev, &sms);
   if (e != cudaSuccess) return from_cuda(e);
@@ -344,8 +346,8 @@ bool scaled_tiles_ok(long long rows, long long cols) {  // a launch's tiles are 
 
 // The product of one scaled layer.
 cudaError_t scaled(bool gated, const void* a, const float* a_scale, long long rows, const void* b, const float* b_scale,
-                   long long cols, long long depth, int act, void* out, float* out_scale, bool follows, int splits, float* part, int sms,
-                   cudaStream_t st) {
+                   long long cols, long long depth, int act, void* out, float* out_scale, bool follows, int splits,
+                   float* part, int sms, cudaStream_t st) {
   CUtensorMap ma, mb;
   if (!encode_scaled(&ma, a, rows, depth) || !encode_scaled(&mb, b, gated ? 2 * cols : cols, depth))
     return cudaErrorInvalidValue;
@@ -373,7 +375,7 @@ REC_ATTN_API rec_attn_status rec_attn_scaled_quantize(int32_t dtype, int32_t blo
                                                       const void* x, void* q, float* scale, void* stream) {
   if (dtype != REC_ATTN_BF16 && dtype != REC_ATTN_FP32) return REC_ATTN_ERR_INVALID_ARG;
   if ((block_rows != 1 && block_rows != kScaleBlock) || rows < 0 || width < 1 || width % 16) return REC_ATTN_ERR_INVALID_ARG;
-  if (rows > kMaxRows || width > kMaxWidth || !scaled_tiles_ok(rows, width)) return REC_ATTN_ERR_UNSUPPORTED;
+  if (rows > kMaxRows || width > 2 * kMaxWidth || !scaled_tiles_ok(rows, width)) return REC_ATTN_ERR_UNSUPPORTED;
   if (rows == 0) return REC_ATTN_OK;
   if (!x || !q || !scale || misaligned(x) || misaligned(q) || misaligned(scale)) return REC_ATTN_ERR_INVALID_ARG;
   const size_t n_scale = 4 * (size_t)((rows + block_rows - 1) / block_rows * blocks128(width));
@@ -452,10 +454,13 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t
   if (few) {
     const int R = (int)rows, W = (int)width, H = (int)hidden;
     int* const word = dense_status();
-    if (e == cudaSuccess) e = launch_few(true, true, {R, H, W, xq, xs, w_in, w_in_scale, activation, hq, hs, 1, word}, sms, st);
-    if (e == cudaSuccess) e = launch_few(true, false, {R, W, H, hq, hs, w_out, w_out_scale, 0, y, nullptr, 1, word}, sms, st);
+    if (e == cudaSuccess)
+      e = launch_few(true, true, {R, H, W, xq, xs, w_in, w_in_scale, activation, hq, hs, 1, word}, sms, st);
+    if (e == cudaSuccess)
+      e = launch_few(true, false, {R, W, H, hq, hs, w_out, w_out_scale, 0, y, nullptr, 1, word}, sms, st);
   } else {
-    if (e == cudaSuccess) e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, true, 1, nullptr, sms, st);
+    if (e == cudaSuccess)
+      e = scaled(true, xq, xs, rows, w_in, w_in_scale, hidden, width, activation, hq, hs, true, 1, nullptr, sms, st);
     if (e == cudaSuccess)
       e = scaled(false, hq, hs, rows, w_out, w_out_scale, width, hidden, 0, y, nullptr, true, s,
                  reinterpret_cast<float*>(xq + off_part), sms, st);

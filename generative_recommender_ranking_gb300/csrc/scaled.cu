@@ -238,10 +238,10 @@ out:
 }
 
 // A row's scales of four blocks (n are left): every thread of a warp reads another row, 32 sectors, so they
-// are read together.
+// are read together.  (Plain loads: the kernel may have started before they were written.)
 __device__ __forceinline__ float4 next_scales(const float* s, int n, bool aligned) {
-  if (aligned) return __ldg(reinterpret_cast<const float4*>(s));
-  return make_float4(__ldg(s), n > 1 ? __ldg(s + 1) : 0.f, n > 2 ? __ldg(s + 2) : 0.f, n > 3 ? __ldg(s + 3) : 0.f);
+  if (aligned) return *reinterpret_cast<const float4*>(s);
+  return make_float4(s[0], n > 1 ? s[1] : 0.f, n > 2 ? s[2] : 0.f, n > 3 ? s[3] : 0.f);
 }
 
 // Sixteen warps: a thread has one row and a quarter of the tile's columns (gated: 32 gate columns and

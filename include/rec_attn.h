@@ -443,7 +443,7 @@ rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation, int64_t rows
  *   A block's scale is the least power of two, from 2^-126 up, that brings its largest finite
  *   value to at most 448 (1 for a block without any but zeros): x / scale is exact, and q is the
  *   nearest e4m3 value, ties to even.  A value that is not finite becomes NaN.
- *   width a multiple of 16, at most 65536.
+ *   width a multiple of 16, at most 131072.
  *
  * rec_attn_scaled_matmul -- y[m][n] = sum over blocks k of a_scale[m][k] b_scale[n / 128][k]
  *   times the sum over the block of a[m][.] b[n][.]: a [rows][depth] with a scale for each row's

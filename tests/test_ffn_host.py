@@ -56,7 +56,7 @@ def test_scaled_refusals(L):
                 dict(x=None), dict(q=None), dict(s=None), dict(x=X + 8), dict(q=Y + 1), dict(s=DX + 4), dict(q=X),
                 dict(s=X + 16), dict(s=Y)):
         assert q(**bad) == INV, bad
-    assert q(width=65552) == UNS and q(rows=1 << 31) == UNS
+    assert q(width=131088) == UNS and q(rows=1 << 31) == UNS
     assert q(rows=0, x=None) == bd.OK
     m = lambda rows=4, cols=64, depth=64, a=X, sa=WI, b=WO, sb=DX, y=Y: L.rec_attn_scaled_matmul(rows, cols, depth, a, sa, b,
                                                                                                 sb, y, None)

@@ -276,3 +276,108 @@ def test_with_the_attention_and_the_layer_norm():
     torch.cuda.synchronize()
     # x, both weights and h are off by at most 2^-4 each: three of them in g, u and h = act(g) u, one more in w_out
     assert (ys.double() - y.double()).norm() <= 6 * 2.0**-4 * y.double().norm()
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import torch
+import test_gpu_ffn_calls as t
+run, tensors = {case}
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = run(tensors)
+g.replay()
+torch.cuda.synchronize()
+assert t.same(out, run(tensors))
+"""
+
+
+@pytest.mark.parametrize("case", [
+    "t.train, t.inputs(300, 136, 264, t.BF)", "t.train, t.inputs(3, 512, 1024, t.BF)", "t.train, t.inputs(40, 512, 1024, t.BF)",
+    "t.train, t.inputs(150, 132, 68, t.F32)", "t.train, t.inputs(2, 132, 68, t.F32)", "t.quantize_and_product, t.raw(300)",
+    "t.quantize_and_product, t.raw(3)", "t.quantize_and_product, t.raw(40)"])
+def test_first_call_of_a_process_is_captured(case):
+    import os
+    import subprocess
+    import sys
+    code = FIRST.format(root=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), case=case)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def raw(rows):
+    """Rows and weights that nothing of the library has touched."""
+    g = torch.Generator().manual_seed(rows)
+    return [torch.randn(s, generator=g).to(BF).cuda() for s in ((rows, 256), (512, 256), (256, 256))]
+
+
+def quantize_and_product(t):
+    def q(m, br):
+        v, sc = torch.empty(m.shape, dtype=F8, device="cuda"), torch.empty(-(-m.shape[0] // br), m.shape[1] // 128, device="cuda")
+        bd.rec_attn_scaled_quantize(m, v, sc, block_rows=br)
+        return v, sc
+
+    x, wi, wo = t
+    a, b, c = q(x, 1), q(wi, 128), q(wo, 128)
+    y, z = torch.empty_like(x), torch.empty(x.shape[0], 512, dtype=BF, device="cuda")
+    bd.rec_attn_scaled_matmul(*a, *b, z)
+    bd.rec_attn_ffn_scaled_fwd(x, *b, *c, y)
+    return [z, y]
+
+
+def test_a_few_rows_of_many_blocks():
+    """Long summed axes for few rows (a cluster's CTAs go round their stages), and more columns than SMs."""
+    for rows, width, hidden in ((2, 8192, 128), (20, 8192, 128), (60, 8192, 136), (33, 128, 40000), (5, 136, 40000)):
+        t = inputs(rows, width, hidden, BF, seed=rows)
+        y = torch.empty_like(t[0])
+        bd.rec_attn_ffn_fwd(t[0], t[2], t[3], y)
+        torch.cuda.synchronize()
+        assert bd.rec_attn_dense_device_status() == bd.OK
+        within(y, reference(*t, "silu", 2.0**-8)["y"], "y")
+    for rows, cols, depth in ((3, 128, 40000), (40, 128, 40000), (64, 40000, 272), (7, 40000, 272), (200, 40, 131072)):
+        g = torch.Generator().manual_seed(rows)
+        a, asc = quantize(torch.randn(rows, depth, generator=g).cuda(), 1)
+        b, bsc = quantize(torch.randn(cols, depth, generator=g).cuda(), 128)
+        y = torch.full((rows, cols), float("nan"), dtype=BF, device="cuda")
+        bd.rec_attn_scaled_matmul(a, asc, b, bsc, y)
+        torch.cuda.synchronize()
+        assert bd.rec_attn_dense_device_status() == bd.OK
+        A, B = held(a, asc, 1), held(b, bsc, 128)
+        want = A @ B.T
+        assert ((y.double() - want).abs() <= 2.0**-8 * want.abs() + sums(depth) * (A.abs() @ B.abs().T) + 1e-30).all()
+
+
+def test_largest_widths():
+    """65536 wide, and e4m3 131072: few rows, and past a tile."""
+    for rows in (3, 70, 300):
+        t = inputs(rows, 65536, 64, BF, seed=rows)
+        out = train(t)
+        torch.cuda.synchronize()
+        ref = reference(*t, "silu", 2.0**-8)
+        for n, got in zip(("y", "dx", "dw_in", "dw_out"), out):
+            within(got, ref[n], n)
+        t = inputs(rows, 64, 65536, BF, seed=rows)
+        out = train(t)
+        torch.cuda.synchronize()
+        ref = reference(*t, "silu", 2.0**-8)
+        for n, got in zip(("y", "dx", "dw_in", "dw_out"), out):
+            within(got, ref[n], n)
+
+
+def test_binding_refuses_on_the_device():
+    x, dy, wi, wo = inputs(4, 64, 128, BF)
+    y = torch.empty_like(x)
+    for bad in ((x.float(), wi, wo, y), (x, wi.float(), wo, y), (x, wi[:128], wo, y), (x, wi, wo.T, y), (x, wi, wo, y[:2]),
+                (x.T, wi, wo, y), (x, wi.cpu(), wo, y), (x, wi, wo, x), (x[:, ::2], wi, wo, y), (x, None, wo, y)):
+        with pytest.raises(bd.RecAttnError) as e:
+            bd.rec_attn_ffn_fwd(*bad)
+        assert e.value.code == bd.ERR_INVALID_ARG
+    with pytest.raises(bd.RecAttnError):
+        bd.rec_attn_ffn_fwd(x, wi, wo, y, activation="relu")
+    with pytest.raises(bd.RecAttnError):
+        bd.rec_attn_ffn_bwd(x, wi, wo, dy, dx=dy)
+    with pytest.raises(bd.RecAttnError):
+        bd.rec_attn_scaled_quantize(x, torch.empty(4, 64, dtype=torch.uint8, device="cuda"), torch.empty(4, 1, device="cuda"))
+    assert bd.rec_attn_dense_device_status() == bd.OK
