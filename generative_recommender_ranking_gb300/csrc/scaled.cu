@@ -11,10 +11,9 @@
 // an instruction) while the next block is summed.  So the scales may be any fp32, and no sum of more than
 // 128 products is the tensor cores' own.  The gated form takes 128 gate and 128 up columns as a tile and writes
 // their product in e4m3 with its scales.
-// 16387 x 8192 x 4096: 504 us (2.2 PFLOP/s; without taking sums up 3.5).  A block takes 1140 cycles where its MMAs
-// take 540: the buffers' round trip (commit, the warps' waking, two reads of 32 columns, their multiply-adds,
-// the arrival at the first CTA) bounds it; two issuing warps with half a tile each changed nothing, and more
-// buffers do not fit TMEM.  The gated form on 320016 rows of 512 x 1024: 457 us, half of it the tile's
+// 16387 x 8192 x 4096: 472 us (2.3 PFLOP/s; without taking sums up 3.5).  A block takes 1060 cycles where its MMAs
+// take 540: the sixteen warps bound it (waking, two reads of 32 columns, their multiply-adds, the next block's
+// scales), so that two issuing warps with half a tile each changed nothing; more buffers do not fit TMEM.  The gated form on 320016 rows of 512 x 1024: 457 us, half of it the tile's
 // epilogue (the special-function unit).  Sixteen warps of 112 registers read 32 columns at a time; eight
 // warps of 168, or 16 columns at a time: 562 and 603 us against 508.
 #include <cuda_bf16.h>
@@ -249,31 +248,53 @@ __device__ __forceinline__ float4 next_scales(const float* s, int n, bool aligne
 template <bool GATED, int ACT, bool PARTS>
 __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, float* s_top,
                        uint32_t rank, int warp, int lane) {
+  // Scales are read a block, and over a tile's end, ahead: 16387 x 8192 x 4096 500 -> 472 us (487 without the
+  // step over the end).  Not in the gated form, whose registers it exceeds (a block of 512 to 1024 columns on 320016
+  // rows 737 -> 757 us), nor for parts, where it spills.
+  constexpr bool kEarly = !GATED && !PARTS;
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
   const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
   const bool aligned = (a.kblocks & 3) == 0;  // (a.a_scale is on a 16-byte boundary)
-  uint32_t n = 0, it = 0;
-  for (Work<GATED, PARTS> work(a, rank); work.left(); work.next(), ++it) {
-    const Unit u = work.get();
+  Work<GATED, PARTS> work(a, rank);
+  // the tile, this thread's row of it, and the scales of the row and of its first and second 32 columns' block
+  Unit u;
+  bool in;
+  const float *sa, *sb0, *sb1;
+  float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+  float b0 = 0.f;
+  auto begin = [&] {
+    u = work.get();
     const long long row = u.m0 + quad * 32 + lane;
-    const bool in = row < a.M;
-    const float* sa = a.a_scale + (in ? row : 0) * a.kblocks;
-    // the scales of this thread's first and second 32 columns' block
+    in = row < a.M;
+    sa = a.a_scale + (in ? row : 0) * a.kblocks;
     const int nb = u.n0 / 128 + (GATED ? 0 : part >> 1);
     const bool nb_in = GATED || (long long)nb * 128 < a.N;
-    const float* sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
-    const float* sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
-    float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
+    sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
+    if (kEarly && u.kb0 < u.kb1) {
+      s4 = next_scales(sa + (u.kb0 & ~3), a.kblocks - (u.kb0 & ~3), aligned);
+      b0 = __ldg(sb0 + u.kb0);
+    }
+  };
+  uint32_t n = 0;
+  if (kEarly && work.left()) begin();
+  for (uint32_t it = 0; work.left(); ++it) {
+    if (!kEarly) begin();
     f32x2 sums[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) sums[e] = 0ull;
     for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
-      if ((kb & 3) == 0 || (PARTS && kb == u.kb0)) s4 = next_scales(sa + (kb & ~3), a.kblocks - (kb & ~3), aligned);
+      if (!kEarly && ((kb & 3) == 0 || (PARTS && kb == u.kb0)))
+        s4 = next_scales(sa + (kb & ~3), a.kblocks - (kb & ~3), aligned);
       const float sk = (kb & 2) ? (kb & 1 ? s4.w : s4.z) : (kb & 1 ? s4.y : s4.x);
-      const float f0 = sk * __ldg(sb0 + kb), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
+      const float f0 = sk * (kEarly ? b0 : __ldg(sb0 + kb)), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
+      if (kEarly && kb + 1 < u.kb1) {
+        b0 = __ldg(sb0 + kb + 1);
+        if ((kb & 3) == 3) s4 = next_scales(sa + kb + 1, a.kblocks - kb - 1, aligned);
+      }
       const uint32_t buf = n & 1;
-      if (!bounded_wait_warp(bars + kAccFull + buf, (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
+      if (!bounded_wait_voted(bars + kAccFull + buf, (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
       ptx::tc_fence_after();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -289,6 +310,13 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
         for (int e = 0; e < 16; ++e)
           sums[16 * c + e] = fma_pairs(pair_of(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f, sums[16 * c + e]);
       }
+    }
+    const Unit at = u;
+    const bool here = in;
+    const long long row = at.m0 + quad * 32 + lane;
+    if (kEarly) {  // the next tile's first scales travel while this tile is written
+      work.next();
+      if (work.left()) begin();
     }
     if constexpr (GATED) {
       float acc[32], top = 0.f;
@@ -310,37 +338,38 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       s[part * 128] = top;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bars + kParts);
-      if (!bounded_wait_warp(bars + kParts, it & 1, abort_flag, a.status, kWaitNs)) return;
+      if (!bounded_wait_voted(bars + kParts, it & 1, abort_flag, a.status, kWaitNs)) return;
       top = fmaxf(fmaxf(s[0], s[128]), fmaxf(s[256], s[384]));
       float inv;
       const float scale = block_scale(top, inv);
-      if (in) {
+      if (here) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           w[e] = pack_e4m3(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv, fine);
-        ptx::st_global_v8(static_cast<uint8_t*>(a.out) + row * a.N + u.n0 + part * 32, w[0], w[1], w[2], w[3], w[4],
+        ptx::st_global_v8(static_cast<uint8_t*>(a.out) + row * a.N + at.n0 + part * 32, w[0], w[1], w[2], w[3], w[4],
                           w[5], w[6], w[7]);
-        if (part == 0) a.out_scale[row * (a.N / 128) + u.n0 / 128] = scale;
+        if (part == 0) a.out_scale[row * (a.N / 128) + at.n0 / 128] = scale;
       }
     } else {
-      const int col0 = u.n0 + part * 64;
+      const int col0 = at.n0 + part * 64;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int col = col0 + 16 * c;
         if constexpr (PARTS) {
-          ulonglong2* const dst = reinterpret_cast<ulonglong2*>(a.part + ((long long)u.split * a.M + row) * a.N + col);
+          ulonglong2* const dst = reinterpret_cast<ulonglong2*>(a.part + ((long long)at.split * a.M + row) * a.N + col);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (in && col + 4 * e < a.N) dst[e] = make_ulonglong2(sums[8 * c + 2 * e], sums[8 * c + 2 * e + 1]);
+            if (here && col + 4 * e < a.N) dst[e] = make_ulonglong2(sums[8 * c + 2 * e], sums[8 * c + 2 * e + 1]);
         } else {
           uint32_t w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = pack_bf16(sums[8 * c + e]);
-          if (in && col < a.N) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, a.N - col, a.wide);
+          if (here && col < a.N) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, a.N - col, a.wide);
         }
       }
     }
+    if (!kEarly) work.next();
   }
 }
 

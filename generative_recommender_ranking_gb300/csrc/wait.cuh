@@ -38,6 +38,26 @@ __device__ __forceinline__ bool bounded_wait_warp(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same with a vote at every look at the barrier, for a warp whose every block waits: it is not split and joined
+// around the looks (the e4m3 product of 16387 x 8192 x 4096 507 -> 501 us; no difference in the bf16 and fp32
+// products).  The phase may not end before this warp has answered it: a lane looks again after it has seen it.
+__device__ __forceinline__ bool bounded_wait_voted(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                   uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > limit_ns)) {
+      *abort_flag = 1;
+      set_status(status, REC_ATTN_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // Wait for a copy (or matrix instructions) of the thread's own to finish before the CTA reuses what they
 // write, or leaves.  Bounded too; it waits in earnest only after an abort.
 __device__ __forceinline__ void bounded_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
