@@ -95,9 +95,19 @@ __device__ __forceinline__ f32x2 normal_cdf(f32x2 g, f32x2& density) {
   return pair_of(v.x > 0.f ? 1.f - w.x : w.x, v.y > 0.f ? 1.f - w.y : w.y);
 }
 
-// 1 / (1 + e^-g); below -41 it stays at 2^-60.
+// a b + c, from 0 to 1.
+__device__ __forceinline__ float fma_sat(float a, float b, float c) {
+  float r;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 1 / (1 + e^-g) less 2^-60, where it would stay from -41.6 down: a gate that is closed by a large value has the
+// weight 0 and no gradient, whatever its size.  (From -34 up that is less than half a bf16 step of it; the exact form
+// from e^-|g| takes five more instructions: 320016 rows through an e4m3 block of 512 x 1024 750 us against 724.)
 __device__ __forceinline__ f32x2 logistic(f32x2 g) {
-  return rcp_hw(add_pairs(exp2_hw(min_pairs(mul_pairs(g, both(-1.44269504f)), 60.f)), both(1.f)));
+  const float2 v = values_of(add_pairs(exp2_hw(min_pairs(mul_pairs(g, both(-1.44269504f)), 60.f)), both(1.f)));
+  const float r = rcp_hw(v.x * v.y), floor = -0x1.00002p-60f;  // (2^-60 and the reciprocal's error)
+  return pair_of(fma_sat(r, v.y, floor), fma_sat(r, v.x, floor));
 }
 
 // act(g) of two values, and its derivative, for results in 16 bits and fewer.  silu: g / (1 + e^-g).  gelu: g Phi(g).

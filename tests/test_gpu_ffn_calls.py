@@ -381,3 +381,48 @@ def test_binding_refuses_on_the_device():
     with pytest.raises(bd.RecAttnError):
         bd.rec_attn_scaled_quantize(x, torch.empty(4, 64, dtype=torch.uint8, device="cuda"), torch.empty(4, 1, device="cuda"))
     assert bd.rec_attn_dense_device_status() == bd.OK
+
+
+@pytest.mark.parametrize("size", [64.0, 1e9, 2.0**127])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows", [3, 24, 150])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_closed_gates(rows, act, dtype, size):
+    """Hidden columns whose gate is far below zero, down to the types' lowest power of two: they add nothing, neither
+    to y nor to dx (act and its slope are below 64 e^-64 there), and their weights have no gradient; the others are
+    as if they were alone."""
+    closed, hidden = 40, 264
+    x, dy, wi, wo = inputs(rows, 136, hidden, dtype, 11)
+    x[:, 0] = 1
+    wi[:closed] = 0
+    wi[:closed, 0] = -size
+    y, dx, dwi, dwo = train((x, dy, wi, wo), act)
+    assert same([], [])
+    rest = torch.arange(2 * hidden, device="cuda") % hidden >= closed
+    ref = reference(x, dy, wi[rest], wo[:, closed:], act, 2.0**-8 if dtype == BF else 2.0**-24)
+    for got, name in ((y, "y"), (dx, "dx"), (dwi[rest], "dw_in"), (dwo[:, closed:], "dw_out")):
+        within(got, ref[name], name)
+    for got in (dwi[~rest], dwo[:, :closed]):
+        assert got.double().abs().max() < 1e-20
+
+
+@pytest.mark.parametrize("size", [64.0, 1e9, 2.0**127])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows", [3, 24, 150])
+def test_closed_gates_scaled(rows, act, size):
+    """As if the up projections of the closed columns were zero."""
+    closed, hidden, width = 128, 256, 144
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn(rows, width, generator=g).to(BF).cuda()
+    x[:, 0] = 1
+    wi = (torch.randn(2 * hidden, width, generator=g) / 12).cuda()
+    wi[:closed] = 0
+    wi[:closed, 0] = -size
+    wo = quantize((torch.randn(width, hidden, generator=g) / 16).cuda(), 128)
+    out = []
+    for up in (1, 0):
+        wi[hidden : hidden + closed] *= up
+        y = torch.full_like(x, 7)
+        bd.rec_attn_ffn_scaled_fwd(x, *quantize(wi, 128), *wo, y, activation=act)
+        out.append(y)
+    assert same(out[:1], out[1:])
