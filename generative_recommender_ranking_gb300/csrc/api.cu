@@ -106,11 +106,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 2-D map over a [T][H*d] bf16 tensor; box = 64 columns x `rows` rows, 128-byte swizzle.
-bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, int rows) {
+bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, int rows, long long ld) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)T};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : cols) * 2};
   cuuint32_t box[2] = {64, (cuuint32_t)rows};
   cuuint32_t es[2] = {1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,

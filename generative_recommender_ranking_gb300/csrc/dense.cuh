@@ -22,6 +22,9 @@ struct DenseArgs {
   int kblocks;          // blocks of 64 along the summed axis
   int tiles_m, tiles_n, splits;
   int act;              // rec_attn_activation
+  int pad;              // columns between the halves of p and behind the rows of p and h (0 or 8: hidden
+                        // an odd multiple of 8), so that they start on 32-byte boundaries
+  int cut;              // kDx, kDw of such a p: hidden
   int wide;             // the outputs' rows start on 32-byte boundaries
   int follows;          // behind a kernel of the same call: launched before that one has ended
   void* out;            // kGlu: h; kOut, kDx: the result; kDglu: p; kDw: the result (of one split)
@@ -32,7 +35,8 @@ struct DenseArgs {
 
 // A row-major [rows][cols] bf16 operand as a TMA map: boxes of 64 columns x 128 rows, or 64 x 64 where the
 // summed axis runs over its rows (mn_major).
-bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major);
+// ld: from a row to the next, if that is not cols.
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major, long long ld = 0);
 int* dense_status();
 
 // fp32 operands (dense_fp32.cu): a matrix as three bf16 planes whose sum it is, rows `ld` apart.

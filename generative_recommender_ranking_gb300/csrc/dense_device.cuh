@@ -143,13 +143,20 @@ __device__ __forceinline__ float act32(float g, float& slope) {
 }
 
 // 32 columns of a row in bf16; `left` columns of the result remain from the first on (a multiple of
-// 8).  wide: the row starts on a 32-byte boundary, whole sectors are written.
+// 8).  wide: the row starts on a 32-byte boundary.  Whole sectors are written, of other rows (every second one, where
+// the width is an odd multiple of 8) between the first and the last 16 bytes: dx of 40000 x 520 with hidden 1024
+// 239 -> 234 us, and twice as much where more is stored.
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&w)[16], int left, bool wide) {
-  if (wide && left >= 32) {
+  char* const at = reinterpret_cast<char*>(dst);
+  if (left >= 32 && (wide || (reinterpret_cast<uintptr_t>(dst) & 31) == 0)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      ptx::st_global_v8(reinterpret_cast<char*>(dst) + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3],
-                        w[8 * c + 4], w[8 * c + 5], w[8 * c + 6], w[8 * c + 7]);
+      ptx::st_global_v8(at + 32 * c, w[8 * c], w[8 * c + 1], w[8 * c + 2], w[8 * c + 3], w[8 * c + 4], w[8 * c + 5],
+                        w[8 * c + 6], w[8 * c + 7]);
+  } else if (left >= 32) {
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    ptx::st_global_v8(at + 16, w[4], w[5], w[6], w[7], w[8], w[9], w[10], w[11]);
+    *reinterpret_cast<uint4*>(at + 48) = make_uint4(w[12], w[13], w[14], w[15]);
   } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -159,7 +166,7 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&
 
 // 16 columns.
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&w)[8], int left, bool wide) {
-  if (wide && left >= 16) {
+  if (left >= 16 && (wide || (reinterpret_cast<uintptr_t>(dst) & 31) == 0)) {
     ptx::st_global_v8(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
   } else {
 #pragma unroll

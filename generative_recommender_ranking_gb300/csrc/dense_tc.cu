@@ -91,7 +91,12 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
         const bool grad = OP == DenseOp::kDglu && kb < 0;
         // (the first CTA's barrier counts the bytes of both)
         if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, CG * (grad ? 2 * kSlab + C::kBRows * 64 : C::kStage));
-        if (grad) {
+        // kDx where p's halves do not adjoin: its second half and the up projection have maps of their own
+        const int half = OP == DenseOp::kDx && a.pad ? (a.cut + kBK - 1) / kBK : INT32_MAX;
+        if (OP == DenseOp::kDx && kb >= half) {
+          load_operand<false, CG>(s, ma2, u.m0, kTile, kb - half, bar);
+          load_operand<true, CG>(s + 2 * kSlab, mb2, u.n0 + (int)rank * C::kBRows, C::kBRows, kb - half, bar);
+        } else if (grad) {
           load_operand<false, CG>(s, ma2, u.m0, kTile, kb + first, bar);
           load_operand<true, CG>(s + 2 * kSlab, mb2, u.n0 + (int)rank * (C::kBRows / 2), C::kBRows / 2, kb + first, bar);
         } else {
@@ -197,7 +202,8 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
     if (!bounded_wait_warp(bars + kAccFull + buf, round, abort_flag, a.status, kWaitNs)) return;
     ptx::tc_fence_after();
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
-    const long long row = u.m0 + quad * 32 + lane;
+    long long row = u.m0 + quad * 32 + lane;
+    if (OP == DenseOp::kDw && a.pad && row >= a.cut) row = row < a.cut + a.pad ? a.M : row - a.pad;  // (between: none)
     const auto give_back = [&](uint32_t bar) {
       ptx::tc_fence_before();
       __syncwarp();
@@ -225,10 +231,11 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         }
         const int col = u.n0 + part * kCols + c, left = a.N - col;
         if (row < a.M && left > 0) {
-          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + row * 2 * a.N + col;
+          const int ld = a.N + a.pad;
+          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + row * 2 * ld + col;
           store_bf16(p, wg, left, a.wide);
-          store_bf16(p + a.N, wu, left, a.wide);
-          store_bf16(static_cast<__nv_bfloat16*>(a.out2) + row * a.N + col, wh, left, a.wide);
+          store_bf16(p + ld, wu, left, a.wide);
+          store_bf16(static_cast<__nv_bfloat16*>(a.out2) + row * ld + col, wh, left, a.wide);
         }
       }
       continue;
@@ -245,7 +252,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         for (int e = 0; e < 8; ++e)
           w[e] = pack_bf16(mul_pairs(act_value<ACT>(pair_of_bits(gu[2 * e], gu[2 * e + 1])),
                                      pair_of_bits(gu[16 + 2 * e], gu[17 + 2 * e])));
-        if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * a.N + col, w, left, a.wide);
+        if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * (a.N + a.pad) + col, w, left, a.wide);
       } else {
         uint32_t r[32];
         ptx::tmem_ld32(lanes + buf * BN + c, r);
@@ -349,7 +356,7 @@ cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_
   const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN, CG, ACT>, C::kDynamic);
   if (e != cudaSuccess) return e;
   if (C::kSplitRegs && !launched_with(k_dense<OP, BN, CG, ACT>, C::kRegs)) return cudaErrorInvalidConfiguration;
-  a.tiles_m = (a.M + C::kTileM - 1) / C::kTileM;
+  a.tiles_m = (a.M + (OP == DenseOp::kDw ? a.pad : 0) + C::kTileM - 1) / C::kTileM;
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;
   const int places = num_sms / CG;
@@ -359,8 +366,8 @@ cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_
 
 }  // namespace
 
-bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major) {
-  return encode_map(m, base, rows, cols, mn_major ? 64 : kTile);
+bool encode_dense(CUtensorMap* m, const void* base, long long rows, long long cols, bool mn_major, long long ld) {
+  return encode_map(m, base, rows, cols, mn_major ? 64 : kTile, ld);
 }
 
 // Asked once per device (the first call may be captured: the question belongs to no stream).

@@ -215,7 +215,8 @@ rec_attn_status from_cuda(cudaError_t e);
 cudaError_t pool_for(int device, cudaMemPool_t* out);  // the library's memory pool of a device
 bool overlaps(const void* a, size_t na, const void* b, size_t nb);
 cudaError_t device_and_sms(int* dev, int* sms);  // the current device
-bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, int rows = kTile);
+bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, int rows = kTile,
+                long long ld = 0);
 // 1 when the plan's items run over many key tiles (AttnArgs::long_items).
 int long_items(const rec_attn_params& p, int batch, long long n_tiles);
 
