@@ -120,10 +120,10 @@ bool encode_map(CUtensorMap* m, const void* base, long long T, long long cols, i
 }
 
 // 3-D map over the three bf16 planes of an fp32 matrix; box = 64 columns x `box_rows` rows of each.
-bool encode_planes(CUtensorMap* m, const Planes& a, int box_rows) {
+bool encode_planes(CUtensorMap* m, const Planes& a, int box_rows, long long rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows, 3};
+  cuuint64_t dims[3] = {(cuuint64_t)a.cols, (cuuint64_t)(rows ? rows : a.rows), 3};
   cuuint64_t strides[2] = {(cuuint64_t)a.ld * 2, (cuuint64_t)a.plane()};
   cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 3};
   cuuint32_t es[3] = {1, 1, 1};

@@ -22,8 +22,8 @@ struct DenseArgs {
   int kblocks;          // blocks of 64 along the summed axis
   int tiles_m, tiles_n, splits;
   int act;              // rec_attn_activation
-  int pad;              // columns between the halves of p and behind the rows of p and h (0 or 8: hidden
-                        // an odd multiple of 8), so that they start on 32-byte boundaries
+  int pad;              // columns between the halves of p and behind the rows of p and h (hidden not a
+                        // multiple of 16), so that they start on 32-byte boundaries
   int cut;              // kDx, kDw of such a p: hidden
   int wide;             // the outputs' rows start on 32-byte boundaries
   int follows;          // behind a kernel of the same call: launched before that one has ended
@@ -56,7 +56,8 @@ struct SplitList {
 };
 cudaError_t launch_split(const SplitList& l, cudaStream_t st);
 // (a K-major A: boxes of 128 rows, other operands 64)
-bool encode_planes(CUtensorMap* m, const Planes& a, int box_rows);
+// (rows: of a part of the matrix that starts at a.p)
+bool encode_planes(CUtensorMap* m, const Planes& a, int box_rows, long long rows = 0);
 cudaError_t launch_dense32(DenseOp op, const CUtensorMap (&maps)[4], Dense32Args a, int num_sms, cudaStream_t st);
 int dense32_splits(int M, int N, int kblocks, int num_sms);
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&maps)[4], DenseArgs a, int num_sms, cudaStream_t st);

@@ -71,7 +71,12 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
         if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * kStage);
         const int nb = C::kPair ? (rank ? a.N : 0) + u.n0 : u.n0 + 64 * (int)rank;  // gated: the gate's rows, up's
         uint8_t* const sb = s + 3 * kPlane;
-        if (grad) {
+        // kDx where p's halves do not adjoin: its second half and the up projection have maps of their own
+        const int half = OP == DenseOp::kDx && a.pad ? (a.cut + kBK - 1) / kBK : INT32_MAX;
+        if (OP == DenseOp::kDx && kb >= half) {
+          load_planes<false>(s, ma2, u.m0, kb - half, bar);
+          load_planes<true>(sb, mb2, nb, kb - half, bar);
+        } else if (grad) {
           load_planes<false>(s, ma2, u.m0, kb + first, bar);
           load_planes<true>(sb, mb2, u.n0 + 32 * (int)rank, kb + first, bar);
         } else {
@@ -161,11 +166,10 @@ __device__ __forceinline__ void store_planes(const Planes& to, long long row, in
   for (int p = 0; p < 3; ++p, at += to.plane())
     *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(v[p][0], v[p][1]), pack_bf16(v[p][2], v[p][3]));
 }
-// kRun columns, `left` of which there are; wide: from a 32-byte boundary on (whole sectors are written: four
+// kRun columns from a 32-byte boundary on, `left` of which there are (whole sectors are written: four
 // columns at a time took three times the traffic).
-__device__ __forceinline__ void store_planes(const Planes& to, long long row, int col, const float (&x)[kRun], int left,
-                                             bool wide) {
-  if (wide && left >= kRun) {
+__device__ __forceinline__ void store_planes(const Planes& to, long long row, int col, const float (&x)[kRun], int left) {
+  if (left >= kRun) {
     uint32_t w[3][8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -245,12 +249,12 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
       take(x1, n & 1, c1);
       taken(n & 1);
     }
-    const long long row = u.m0 + quad * 32 + lane;
+    long long row = u.m0 + quad * 32 + lane;
+    if (OP == DenseOp::kDw && a.pad && row >= a.cut) row = row < a.cut + a.pad ? a.M : row - a.pad;  // (between: none)
     if (row >= a.M) continue;
     if constexpr (C::kPair) {
       // in place: x0 becomes du, x1 h and dh dg
       const int col = u.n0 + c0, left = a.N - col;
-      const bool wide = a.N % 16 == 0;
 #pragma unroll
       for (int e = 0; e < kRun; ++e) {
         float slope;
@@ -262,10 +266,10 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
         }
       }
       if (left > 0) {
-        store_planes(aa.h, row, col, x1, left, wide);
+        store_planes(aa.h, row, col, x1, left);
         if constexpr (OP == DenseOp::kDglu) {
-          store_planes(aa.p, row, col, dh, left, wide);
-          store_planes(aa.p, row, a.N + col, x0, left, wide);
+          store_planes(aa.p, row, col, dh, left);
+          store_planes(aa.p, row, a.N + a.pad + col, x0, left);
         }
       }
     } else {
@@ -358,7 +362,7 @@ cudaError_t run(const CUtensorMap (&m)[4], Dense32Args a, int num_sms, cudaStrea
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(done, (const void*)k_dense32<OP, ACT>, kDynamic);
   if (e != cudaSuccess) return e;
-  a.d.tiles_m = (a.d.M + 2 * kTile - 1) / (2 * kTile);
+  a.d.tiles_m = (a.d.M + (OP == DenseOp::kDw ? a.d.pad : 0) + 2 * kTile - 1) / (2 * kTile);
   a.d.tiles_n = (a.d.N + Cfg<OP>::kCols - 1) / Cfg<OP>::kCols;
   const int units = a.d.tiles_m * a.d.tiles_n * a.d.splits, places = num_sms / 2;
   return launch_pairs(2, true, k_dense32<OP, ACT>, (units < places ? units : places) * 2, kThreads, kDynamic, st, m[0], m[1],

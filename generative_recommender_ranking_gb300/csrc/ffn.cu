@@ -54,6 +54,7 @@ rec_attn_status check_ffn(int32_t dtype, int32_t act, int64_t rows, int64_t widt
 long long row_pad(long long hidden) { return (16 - hidden % 16) % 16; }
 
 int blocks64(int64_t n) { return (int)((n + 63) / 64); }
+int blocks_of_p(int64_t hidden) { return row_pad(hidden) ? 2 * blocks64(hidden) : blocks64(2 * hidden); }
 
 // A workspace of the library's pool, given back in stream order.
 struct Workspace {
@@ -95,15 +96,28 @@ Planes placed(const Planes& a, const Workspace& ws) {
   return b;
 }
 
-// out = a b' over `depth`, the sums of parts of it (s > 1) in part.
+// out = a b' over `depth`, the sums of parts of it (s > 1) in part.  cut: the columns of a half of a, and rows of
+// a half of b, where a's halves do not adjoin.
 cudaError_t plain32(DenseOp op, const Planes& a, const Planes& b, long long M, long long N, long long depth, int s,
-                    float* part, void* out, int sms, cudaStream_t st) {
+                    float* part, void* out, int sms, cudaStream_t st, long long cut = 0) {
   CUtensorMap m[4];
-  if (!encode_planes(&m[0], a, op == DenseOp::kDw ? 64 : 128) || !encode_planes(&m[1], b, 64)) return cudaErrorInvalidValue;
   Dense32Args d{};
+  d.d.cut = (int)cut;
+  d.d.pad = cut ? (int)row_pad(cut) : 0;
+  if (op == DenseOp::kDx && d.d.pad) {
+    Planes ha = a, hb = b;
+    ha.cols = cut;
+    bool ok = encode_planes(&m[0], ha, 128) && encode_planes(&m[1], hb, 64, cut);
+    ha.p = static_cast<char*>(a.p) + (cut + d.d.pad) * 2;
+    hb.p = static_cast<char*>(b.p) + cut * b.ld * 2;
+    ok = ok && encode_planes(&m[2], ha, 128) && encode_planes(&m[3], hb, 64, cut);
+    if (!ok) return cudaErrorInvalidValue;
+  } else if (!encode_planes(&m[0], a, op == DenseOp::kDw ? 64 : 128) || !encode_planes(&m[1], b, 64)) {
+    return cudaErrorInvalidValue;
+  }
   d.d.M = (int)M;
   d.d.N = (int)N;
-  d.d.kblocks = blocks64(depth);
+  d.d.kblocks = op == DenseOp::kDx ? blocks_of_p(cut) : blocks64(depth);
   d.d.splits = s;
   d.d.part = part;
   d.d.out = out;
@@ -170,8 +184,8 @@ cudaError_t ffn32_fwd(int act, long long R, long long W, long long H, const void
 cudaError_t ffn32_bwd(int act, long long R, long long W, long long H, const void* x, const void* w_in, const void* w_out,
                       const void* dy, void* dx, void* dw_in, void* dw_out, int dev, int sms, cudaStream_t st) {
   PlaneLayout l;
-  Planes px = l.add(R, W), pdy = l.add(R, W), pi = l.add(2 * H, W), po = l.add(W, H), ph = l.add(R, H), pp = l.add(R, 2 * H);
-  const int sx = dense32_splits((int)R, (int)W, blocks64(2 * H), sms);
+  Planes px = l.add(R, W), pdy = l.add(R, W), pi = l.add(2 * H, W), po = l.add(W, H), ph = l.add(R, H), pp = l.add(R, 2 * (H + row_pad(H)));
+  const int sx = dense32_splits((int)R, (int)W, blocks_of_p(H), sms);
   const int si = dense32_splits((int)(2 * H), (int)W, blocks64(R), sms), so = dense32_splits((int)W, (int)H, blocks64(R), sms);
   size_t n_part = 0;
   if (dx && sx > 1) n_part = (size_t)sx * R * W;
@@ -196,11 +210,12 @@ cudaError_t ffn32_bwd(int act, long long R, long long W, long long H, const void
   d.d.splits = 1;
   d.d.act = act;
   d.d.status = dense_status();
+  d.d.pad = (int)row_pad(H);
   d.h = ph;
   d.p = pp;
   if (e == cudaSuccess) e = launch_dense32(DenseOp::kDglu, m, d, sms, st);
-  if (e == cudaSuccess && dx) e = plain32(DenseOp::kDx, pp, pi, R, W, 2 * H, sx, part, dx, sms, st);
-  if (e == cudaSuccess && dw_in) e = plain32(DenseOp::kDw, pp, px, 2 * H, W, R, si, part, dw_in, sms, st);
+  if (e == cudaSuccess && dx) e = plain32(DenseOp::kDx, pp, pi, R, W, 2 * H, sx, part, dx, sms, st, H);
+  if (e == cudaSuccess && dw_in) e = plain32(DenseOp::kDw, pp, px, 2 * H, W, R, si, part, dw_in, sms, st, H);
   if (e == cudaSuccess && dw_out) e = plain32(DenseOp::kDw, pdy, ph, W, H, R, so, part, dw_out, sms, st);
   const cudaError_t ef = ws.give_back();
   return e != cudaSuccess ? e : ef;
@@ -289,7 +304,7 @@ REC_ATTN_API rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation,
     return from_cuda(ffn32_bwd(activation, rows, width, hidden, x, w_in, w_out, dy, dx, dw_in, dw_out, dev, sms, st));
   const int kr = blocks64(rows), W = (int)width, H = (int)hidden;
   const long long pad = row_pad(hidden), ld = hidden + pad;
-  const int kp = pad ? 2 * blocks64(hidden) : blocks64(2 * hidden);  // of p, a row
+  const int kp = blocks_of_p(hidden);
   const int sx = dx ? dense_splits((int)rows, W, kp, kBlockUs, sms) : 1;
   const int si = dw_in ? dense_splits(2 * H, W, kr, kBlockUs, sms) : 1, so = dw_out ? dense_splits(W, H, kr, kBlockUs, sms) : 1;
   const size_t n_part = std::max({sx > 1 ? (size_t)sx * rows * W : 0, si > 1 ? (size_t)si * 2 * H * W : 0,
