@@ -189,14 +189,22 @@ __device__ __forceinline__ void store_planes(const Planes& to, long long row, in
       if (c < left) store_planes(to, row, col + c, x[c], x[c + 1], x[c + 2], x[c + 3]);
   }
 }
-// The same in fp32.
-__device__ __forceinline__ void store_floats(float* dst, const float (&x)[kRun], int left, bool wide) {
-  if (wide && left >= kRun) {
+__device__ __forceinline__ void store8(float* dst, const float* x) {
+  ptx::st_global_v8(dst, __float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]),
+                    __float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+}
+// The same in fp32; a row that starts between two sectors' borders has them whole but for the first and last (8000 x 516
+// with hidden 1024: 136 -> 133 us).
+__device__ __forceinline__ void store_floats(float* dst, const float (&x)[kRun], int left) {
+  const bool off = (reinterpret_cast<uintptr_t>(dst) & 31) != 0;
+  if (left >= kRun && !off) {
 #pragma unroll
-    for (int c = 0; c < kRun; c += 8)
-      ptx::st_global_v8(dst + c, __float_as_uint(x[c]), __float_as_uint(x[c + 1]), __float_as_uint(x[c + 2]),
-                        __float_as_uint(x[c + 3]), __float_as_uint(x[c + 4]), __float_as_uint(x[c + 5]),
-                        __float_as_uint(x[c + 6]), __float_as_uint(x[c + 7]));
+    for (int c = 0; c < kRun; c += 8) store8(dst + c, x + c);
+  } else if (left >= kRun) {
+    *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+    for (int c = 4; c + 8 < kRun; c += 8) store8(dst + c, x + c);
+    *reinterpret_cast<float4*>(dst + kRun - 4) = make_float4(x[kRun - 4], x[kRun - 3], x[kRun - 2], x[kRun - 1]);
   } else {
 #pragma unroll
     for (int c = 0; c < kRun; c += 4)
@@ -274,9 +282,8 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
       }
     } else {
       float* const out = (a.splits > 1 ? a.part + (long long)u.split * a.M * a.N : static_cast<float*>(a.out)) + row * a.N;
-      const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-      if (u.n0 + c0 < a.N) store_floats(out + u.n0 + c0, x0, a.N - u.n0 - c0, wide);
-      if (u.n0 + c1 < a.N) store_floats(out + u.n0 + c1, x1, a.N - u.n0 - c1, wide);
+      if (u.n0 + c0 < a.N) store_floats(out + u.n0 + c0, x0, a.N - u.n0 - c0);
+      if (u.n0 + c1 < a.N) store_floats(out + u.n0 + c1, x1, a.N - u.n0 - c1);
     }
   }
 }
