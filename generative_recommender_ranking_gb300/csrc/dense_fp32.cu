@@ -32,10 +32,11 @@ constexpr int kStage = 3 * (kPlane + kSlab), kStages = 3;  // 128 rows of A and 
 constexpr int kEpiWarps = 16, kThreads = 64 + 32 * kEpiWarps;
 constexpr int kRun = 16;                     // columns that a thread takes up at a time
 constexpr int kDynamic = kStages * kStage + 1024;
-constexpr uint32_t kTmem = 256;              // two buffers of a block's sums
 constexpr int kTileN = 128;
+constexpr int kBufs = 4;  // buffers of a block's sums: all of TMEM (40000 rows, 512 x 1024, forward 492 us with two, 457)
+constexpr uint32_t kTmem = kBufs * kTileN;
 
-enum { kFull = 0, kEmpty = 3, kAccFull = 6, kAccEmpty = 8, kDone = 10, kBars = 11 };
+enum { kFull = 0, kEmpty = 3, kAccFull = 6, kAccEmpty = 10, kDone = 14, kBars = 15 };
 
 template <DenseOp OP>
 struct Cfg {
@@ -124,8 +125,8 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
     const Unit u = units.get();
     for (int kb = OP == DenseOp::kDglu ? -a.kblocks : u.kb0; kb < u.kb1; ++kb, ++n) {
       const int st = n % kStages;
-      const uint32_t buf = n & 1;
-      if (!bounded_wait_warp(bars + kAccEmpty + buf, ((n >> 1) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
+      const uint32_t buf = n % kBufs;
+      if (!bounded_wait_warp(bars + kAccEmpty + buf, ((n / kBufs) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (!bounded_wait_warp(bars + kFull + st, (n / kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
       ptx::tc_fence_after();
       if (el) {
@@ -244,18 +245,18 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
 #pragma unroll
       for (int e = 0; e < kRun; ++e) dh[e] = 0.f;
       for (int kb = 0; kb < a.kblocks; ++kb, ++n) {
-        if (!bounded_wait_warp(bars + kAccFull + (n & 1), (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
+        if (!bounded_wait_warp(bars + kAccFull + n % kBufs, (n / kBufs) & 1, abort_flag, a.status, kWaitNs)) return;
         ptx::tc_fence_after();
-        take(dh, n & 1, c0);
-        taken(n & 1);
+        take(dh, n % kBufs, c0);
+        taken(n % kBufs);
       }
     }
     for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
-      if (!bounded_wait_warp(bars + kAccFull + (n & 1), (n >> 1) & 1, abort_flag, a.status, kWaitNs)) return;
+      if (!bounded_wait_warp(bars + kAccFull + n % kBufs, (n / kBufs) & 1, abort_flag, a.status, kWaitNs)) return;
       ptx::tc_fence_after();
-      take(x0, n & 1, c0);
-      take(x1, n & 1, c1);
-      taken(n & 1);
+      take(x0, n % kBufs, c0);
+      take(x1, n % kBufs, c1);
+      taken(n % kBufs);
     }
     long long row = u.m0 + quad * 32 + lane;
     if (OP == DenseOp::kDw && a.pad && row >= a.cut) row = row < a.cut + a.pad ? a.M : row - a.pad;  // (between: none)
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bars + kFull + i, 1);
       ptx::mbar_init(bars + kEmpty + i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       ptx::mbar_init(bars + kAccFull + i, 1);
       ptx::mbar_init(bars + kAccEmpty + i, 2 * kEpiWarps);
     }
