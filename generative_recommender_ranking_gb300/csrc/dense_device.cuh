@@ -129,7 +129,8 @@ __device__ __forceinline__ f32x2 act_both(f32x2 g, f32x2& slope) {
   slope = fma_pairs(g, mul_pairs(density, both(0.39894228f)), p);
   return mul_pairs(g, p);
 }
-// The same for fp32 results: Phi by the complementary error function, and the library's exponential and division keep its last bits.
+// The same for fp32 results: Phi by the complementary error function, and the library's exponential and division keep
+// its last bits.
 template <int ACT>
 __device__ __forceinline__ float act32(float g, float& slope) {
   if (ACT == REC_ATTN_SILU) {

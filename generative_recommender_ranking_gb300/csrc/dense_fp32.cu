@@ -8,9 +8,9 @@
 // fp32 registers, rounded to nearest.
 // A pair of CTAs has a tile of 256 x 128 (gated: 64 gate and 64 up columns; the backward's dh 64); a
 // ring of three 64-deep stages holds all six planes, so each is loaded once.  h and p are written as
-// planes.  1850 rows of 512 x 1024, forward and backward, 149 us (elementary fp32 operations 454): 22 R W H
+// planes.  1850 rows of 512 x 1024, forward and backward, 148 us (elementary fp32 operations 454): 22 R W H
 // multiplied by six is 68 us at the bf16 rate; the rest is eleven kernels of one or two tiles a pair, each with the
-// filling of its ring and an epilogue at its end.  7680 rows: tensor pipe 47 to 69%.
+// filling of its ring and an epilogue at its end.  7680 rows: tensor pipe 50 to 69%.
 #include <cuda_bf16.h>
 
 #include <atomic>

@@ -360,8 +360,8 @@ cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;
   const int places = num_sms / CG;
-  return launch_pairs(CG, a.follows != 0, k_dense<OP, BN, CG, ACT>, (int)(units < places ? units : places) * CG, C::kThreads, C::kDynamic,
-                      st, m[0], m[1], m[2], m[3], a);
+  return launch_pairs(CG, a.follows != 0, k_dense<OP, BN, CG, ACT>, (int)(units < places ? units : places) * CG,
+                      C::kThreads, C::kDynamic, st, m[0], m[1], m[2], m[3], a);
 }
 
 }  // namespace

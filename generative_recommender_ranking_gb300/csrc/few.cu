@@ -50,7 +50,10 @@ __device__ __forceinline__ float4 remote_float4(const void* p, int rank) {
   uint32_t at;
   float4 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ float4 sum_of(float4 a, float4 b) {
@@ -178,7 +181,8 @@ __device__ void collect(const FewArgs& a, float* s_sum, uint64_t* bars, uint32_t
           ptx::tmem_ld16(lanes + (buf * C::kMats + m) * TOKENS + c, r);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            acc[m][c + e] = fmaf(__uint_as_float(r[e]), sw[m] * __shfl_sync(0xffffffffu, sx[(c + e) / 32], (c + e) & 31), acc[m][c + e]);
+            acc[m][c + e] = fmaf(__uint_as_float(r[e]),
+                                 sw[m] * __shfl_sync(0xffffffffu, sx[(c + e) / 32], (c + e) & 31), acc[m][c + e]);
         }
       }
       ptx::tc_fence_before();
@@ -269,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
       float inv;
       const float scale = block_scale(top, inv);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + o) = pack_e4m3(v.x * inv, v.y * inv, v.z * inv, v.w * inv, fine);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + o) =
+          pack_e4m3(v.x * inv, v.y * inv, v.z * inv, v.w * inv, fine);
       if (lane == 0) a.out_scale[(long long)t * (a.N / 128) + n0 / 128] = scale;
     } else if (col < a.N) {
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));

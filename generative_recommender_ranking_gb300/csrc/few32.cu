@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_few32(const FewArgs a) {
       for (int m = 0; m < kMats; ++m)
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          acc[m][c][r] = fmaf(xv.x, wv[m][c].x, fmaf(xv.y, wv[m][c].y, fmaf(xv.z, wv[m][c].z, fmaf(xv.w, wv[m][c].w, acc[m][c][r]))));
+          acc[m][c][r] = fmaf(xv.x, wv[m][c].x,
+                              fmaf(xv.y, wv[m][c].y, fmaf(xv.z, wv[m][c].z, fmaf(xv.w, wv[m][c].w, acc[m][c][r]))));
     }
   }
 #pragma unroll

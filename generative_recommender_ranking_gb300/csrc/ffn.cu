@@ -184,7 +184,8 @@ cudaError_t ffn32_fwd(int act, long long R, long long W, long long H, const void
 cudaError_t ffn32_bwd(int act, long long R, long long W, long long H, const void* x, const void* w_in, const void* w_out,
                       const void* dy, void* dx, void* dw_in, void* dw_out, int dev, int sms, cudaStream_t st) {
   PlaneLayout l;
-  Planes px = l.add(R, W), pdy = l.add(R, W), pi = l.add(2 * H, W), po = l.add(W, H), ph = l.add(R, H), pp = l.add(R, 2 * (H + row_pad(H)));
+  Planes px = l.add(R, W), pdy = l.add(R, W), pi = l.add(2 * H, W), po = l.add(W, H), ph = l.add(R, H);
+  Planes pp = l.add(R, 2 * (H + row_pad(H)));
   const int sx = dense32_splits((int)R, (int)W, blocks_of_p(H), sms);
   const int si = dense32_splits((int)(2 * H), (int)W, blocks64(R), sms), so = dense32_splits((int)W, (int)H, blocks64(R), sms);
   size_t n_part = 0;

@@ -13,9 +13,10 @@
 // their product in e4m3 with its scales.
 // 16387 x 8192 x 4096: 472 us (2.3 PFLOP/s; without taking sums up 3.5).  A block takes 1060 cycles where its MMAs
 // take 540: the sixteen warps bound it (waking, two reads of 32 columns, their multiply-adds, the next block's
-// scales), so that two issuing warps with half a tile each changed nothing; more buffers do not fit TMEM.  The gated form on 320016 rows of 512 x 1024: 457 us, half of it the tile's
-// epilogue (the special-function unit).  Sixteen warps of 112 registers read 32 columns at a time; eight
-// warps of 168, or 16 columns at a time: 562 and 603 us against 508.
+// scales), so that two issuing warps with half a tile each changed nothing; more buffers do not fit TMEM.  The
+// gated form on 320016 rows of 512 x 1024: 463 us under ncu, half of it the tile's epilogue.  Sixteen warps of 112
+// registers read 32 columns at a time; eight warps of 168, or 16 columns at a time: 562 and 603 us where these
+// took 508.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -436,7 +437,8 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int 
   a.tiles_m = (a.M + 2 * kTile - 1) / (2 * kTile);
   a.tiles_n = (a.N + tn - 1) / tn;
   const int tiles = a.tiles_m * a.tiles_n * (PARTS ? a.splits : 1), places = num_sms / 2;
-  return launch_pairs(2, a.follows != 0, k_scaled<GATED, ACT, PARTS>, (tiles < places ? tiles : places) * 2, kThreads, kDynamic, st, ma, mb, a);
+  return launch_pairs(2, a.follows != 0, k_scaled<GATED, ACT, PARTS>, (tiles < places ? tiles : places) * 2, kThreads,
+                      kDynamic, st, ma, mb, a);
 }
 
 }  // namespace

@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_thin(const FewArgs a) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int k = c * kChunk + (4 * i + t) * kPer;
-          to[m][r][i] = n < a.N && k < a.K ? __ldcs(reinterpret_cast<const uint4*>(row + (long long)k * kSize)) : make_uint4(0, 0, 0, 0);
+          to[m][r][i] = n < a.N && k < a.K ? __ldcs(reinterpret_cast<const uint4*>(row + (long long)k * kSize))
+                                           : make_uint4(0, 0, 0, 0);
         }
       }
   };
