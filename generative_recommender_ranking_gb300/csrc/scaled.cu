@@ -167,7 +167,7 @@ static_assert(128 * kFewRegs + 32 * kEpiWarps * kSumRegs <= kThreads * kRegs, "t
 constexpr int kDynamic = kStages * kStage + 1024;
 constexpr uint32_t kTmem = 512;               // two buffers of a block's sums
 
-enum { kFull = 0, kEmpty = 6, kAccFull = 12, kAccEmpty = 14, kParts = 16, kDone = 17, kBars = 18 };
+enum { kFull = 0, kEmpty = 6, kAccFull = 12, kAccEmpty = 14, kParts = 16, kDone = 20, kBars = 21 };
 
 // A pair's tiles (parts of their summed axis) in turn; n0: the first column of the result.
 template <bool GATED, bool PARTS>
@@ -338,8 +338,8 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       float* s = s_top + (it & 1) * 512 + quad * 32 + lane;
       s[part * 128] = top;
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars + kParts);
-      if (!bounded_wait_voted(bars + kParts, it & 1, abort_flag, a.status, kWaitNs)) return;
+      if (lane == 0) ptx::mbar_arrive(bars + kParts + quad);
+      if (!bounded_wait_voted(bars + kParts + quad, it & 1, abort_flag, a.status, kWaitNs)) return;
       top = fmaxf(fmaxf(s[0], s[128]), fmaxf(s[256], s[384]));
       float inv;
       const float scale = block_scale(top, inv);
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bars + kAccFull + i, 1);
       ptx::mbar_init(bars + kAccEmpty + i, 2 * kEpiWarps);
     }
-    ptx::mbar_init(bars + kParts, kEpiWarps);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(bars + kParts + i, kEpiWarps / 4);
     ptx::mbar_init(bars + kDone, 1);
     s_abort = 0;
     ptx::fence_barrier_init();
