@@ -14,7 +14,7 @@
 // 16387 x 8192 x 4096: 472 us (2.3 PFLOP/s; without taking sums up 3.5).  A block takes 1060 cycles where its MMAs
 // take 540: the sixteen warps bound it (waking, two reads of 32 columns, their multiply-adds, the next block's
 // scales), so that two issuing warps with half a tile each changed nothing; more buffers do not fit TMEM.  The
-// gated form on 320016 rows of 512 x 1024: 463 us under ncu, half of it the tile's epilogue.  Sixteen warps of 112
+// gated form on 320016 rows of 512 x 1024: 414 us under ncu, half of it the tile's epilogue.  Sixteen warps of 112
 // registers read 32 columns at a time; eight warps of 168, or 16 columns at a time: 562 and 603 us where these
 // took 508.
 #include <cuda_bf16.h>
@@ -250,9 +250,10 @@ template <bool GATED, int ACT, bool PARTS>
 __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, float* s_top,
                        uint32_t rank, int warp, int lane) {
   // Scales are read a block, and over a tile's end, ahead: 16387 x 8192 x 4096 500 -> 472 us (487 without the
-  // step over the end).  Not in the gated form, whose registers it exceeds (a block of 512 to 1024 columns on 320016
-  // rows 737 -> 757 us), nor for parts, where it spills.
-  constexpr bool kEarly = !GATED && !PARTS;
+  // step over the end).  The gated form has no registers for each block's (a block of 512 to 1024 columns on 320016
+  // rows 737 -> 757 us); it reads a tile's first when the sums of the one before are done with (717 -> 685).  Parts
+  // read none ahead (spills).
+  constexpr bool kEarly = !GATED && !PARTS, kFirst = !PARTS;
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
   const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
@@ -273,20 +274,18 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
     const bool nb_in = GATED || (long long)nb * 128 < a.N;
     sb0 = a.b_scale + (long long)(nb_in ? nb : 0) * a.kblocks;
     sb1 = GATED ? a.b_scale + (long long)(a.N / 128 + nb) * a.kblocks : sb0;
-    if (kEarly && u.kb0 < u.kb1) {
-      s4 = next_scales(sa + (u.kb0 & ~3), a.kblocks - (u.kb0 & ~3), aligned);
-      b0 = __ldg(sb0 + u.kb0);
-    }
+    if (kFirst && u.kb0 < u.kb1) s4 = next_scales(sa + (u.kb0 & ~3), a.kblocks - (u.kb0 & ~3), aligned);
+    if (kEarly && u.kb0 < u.kb1) b0 = __ldg(sb0 + u.kb0);
   };
   uint32_t n = 0;
-  if (kEarly && work.left()) begin();
+  if (kFirst && work.left()) begin();
   for (uint32_t it = 0; work.left(); ++it) {
-    if (!kEarly) begin();
+    if (!kFirst) begin();
     f32x2 sums[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) sums[e] = 0ull;
     for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
-      if (!kEarly && ((kb & 3) == 0 || (PARTS && kb == u.kb0)))
+      if (!kEarly && (PARTS ? (kb & 3) == 0 || kb == u.kb0 : (kb & 3) == 0 && kb > 0))
         s4 = next_scales(sa + (kb & ~3), a.kblocks - (kb & ~3), aligned);
       const float sk = (kb & 2) ? (kb & 1 ? s4.w : s4.z) : (kb & 1 ? s4.y : s4.x);
       const float f0 = sk * (kEarly ? b0 : __ldg(sb0 + kb)), f1 = GATED ? sk * __ldg(sb1 + kb) : f0;
@@ -339,6 +338,8 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
       s[part * 128] = top;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bars + kParts + quad);
+      work.next();
+      if (work.left()) begin();
       if (!bounded_wait_voted(bars + kParts + quad, it & 1, abort_flag, a.status, kWaitNs)) return;
       top = fmaxf(fmaxf(s[0], s[128]), fmaxf(s[256], s[384]));
       float inv;
@@ -370,7 +371,7 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
         }
       }
     }
-    if (!kEarly) work.next();
+    if (!kFirst) work.next();
   }
 }
 
