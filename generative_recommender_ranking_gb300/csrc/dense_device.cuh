@@ -104,8 +104,10 @@ __device__ __forceinline__ float fma_sat(float a, float b, float c) {
 // 1 / (1 + e^-g) less 2^-60, where it would stay from -41.6 down: a gate that is closed by a large value has the
 // weight 0 and no gradient, whatever its size.  (From -34 up that is less than half a bf16 step of it; the exact form
 // from e^-|g| takes five more instructions: 320016 rows through an e4m3 block of 512 x 1024 750 us against 724.)
-__device__ __forceinline__ f32x2 logistic(f32x2 g) {
-  const float2 v = values_of(add_pairs(exp2_hw(min_pairs(mul_pairs(g, both(-1.44269504f)), 60.f)), both(1.f)));
+// e: e^-g, up to 2^60.
+__device__ __forceinline__ f32x2 logistic(f32x2 g, f32x2& e) {
+  e = exp2_hw(min_pairs(mul_pairs(g, both(-1.44269504f)), 60.f));
+  const float2 v = values_of(add_pairs(e, both(1.f)));
   const float r = rcp_hw(v.x * v.y), floor = -0x1.00002p-60f;  // (2^-60 and the reciprocal's error)
   return pair_of(fma_sat(r, v.y, floor), fma_sat(r, v.x, floor));
 }
@@ -113,15 +115,20 @@ __device__ __forceinline__ f32x2 logistic(f32x2 g) {
 // act(g) of two values, and its derivative, for results in 16 bits and fewer.  silu: g / (1 + e^-g).  gelu: g Phi(g).
 template <int ACT>
 __device__ __forceinline__ f32x2 act_value(f32x2 g) {
-  if (ACT == REC_ATTN_SILU) return mul_pairs(g, logistic(g));
+  if (ACT == REC_ATTN_SILU) {
+    f32x2 e;
+    return mul_pairs(g, logistic(g, e));
+  }
   f32x2 density;
   return mul_pairs(g, normal_cdf(g, density));
 }
 template <int ACT>
 __device__ __forceinline__ f32x2 act_both(f32x2 g, f32x2& slope) {
   if (ACT == REC_ATTN_SILU) {
-    const f32x2 p = logistic(g), v = mul_pairs(g, p);
-    slope = fma_pairs(v, fma_pairs(p, both(-1.f), both(1.f)), p);
+    // 1 - p as e^-g p: p of an open gate may be 2^-24 short of one, which a large g would make a slope of its own
+    f32x2 e;
+    const f32x2 p = logistic(g, e), v = mul_pairs(g, p);
+    slope = fma_pairs(v, mul_pairs(e, p), p);
     return v;
   }
   f32x2 density;
