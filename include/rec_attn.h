@@ -414,7 +414,8 @@ rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows, int64_t widt
  * being 1.7e-3 of that.  fp32: three bf16 values stand for each operand and six of their products are
  * summed, in blocks of 64 that are added up in fp32: off by 3e-7.  x, dy and the weights must be
  * finite for a finite result; a value that is not reaches its own row of y and dx, and dw_in and dw_out.
- * bf16: silu's logistic function is cut by 2^-60, so it is zero from -41 down.
+ * bf16 (and e4m3): silu's logistic function is cut by 2^-60, so it is zero from -41 down; gelu's Phi is off by 8e-7 at
+ * most and below zero by 4e-4 of itself, and zero from -13.2 down.
  * Workspace from the library pool on `stream`, in bytes (hidden rounded up to 16): forward, bf16 2 * rows * hidden, fp32 6 times
  * the elements of x, both weights and h (up to 8 rows: 4 * rows * hidden); backward, bf16 6 * rows *
  * hidden, fp32 6 times the elements of x, dy, both weights and p and h (3 * rows * hidden); and where
