@@ -150,7 +150,7 @@ out:
 // one that is not finite is in hi alone.)
 __device__ __forceinline__ void split3(float x, float& hi, float& mid, float& lo) {
   hi = __bfloat162float(__float2bfloat16_rn(x));
-  if (!(fabsf(hi) <= 3.402823466e38f)) hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  if (!(fabsf(hi) <= 3.402823466e38f) && fabsf(x) <= 3.402823466e38f) hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
   const float r = x - hi;
   const bool fine = fabsf(r) <= 3.402823466e38f;
   mid = fine ? __bfloat162float(__float2bfloat16_rn(r)) : 0.f;
