@@ -131,6 +131,8 @@ def lib() -> ctypes.CDLL:
         L.rec_attn_ffn_scaled_fwd.restype = ctypes.c_int
         L.rec_attn_dense_device_status.argtypes = [ctypes.POINTER(i32), vp]
         L.rec_attn_dense_device_status.restype = ctypes.c_int
+        L.rec_attn_check_dense_wait_timeout.argtypes = [ctypes.c_uint32, vp]
+        L.rec_attn_check_dense_wait_timeout.restype = ctypes.c_int
         L.rec_attn_fwd_compress.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
         L.rec_attn_fwd_compress.restype = ctypes.c_int
         L.rec_attn_cache_create.argtypes = [ctypes.POINTER(RecAttnParams), i32, vp, vp, vp, vp, vp,
@@ -519,10 +521,16 @@ def rec_attn_ffn_scaled_fwd(x, w_in, w_in_scale, w_out, w_out_scale, y, activati
 
 
 def rec_attn_dense_device_status(stream=None) -> int:
-    """Status word of the feed-forward and scaled calls on the current device."""
+    """Status word of the feed-forward and scaled calls on the current device: the first error since one
+    was last reported."""
     s = ctypes.c_int32()
     _check("rec_attn_dense_device_status", lib().rec_attn_dense_device_status(ctypes.byref(s), _stream(stream)))
     return int(s.value)
+
+
+def rec_attn_check_dense_wait_timeout(limit_ms: int = 50, stream=None) -> None:
+    """Run the kernels' bounded wait on a barrier nothing arrives at, into that status word."""
+    _check("rec_attn_check_dense_wait_timeout", lib().rec_attn_check_dense_wait_timeout(int(limit_ms), _stream(stream)))
 
 
 def rec_attn_fwd_compress(plan: Plan, q, k, v, hist_begin, hist_len, segments, x_out, t_out, ty_out,

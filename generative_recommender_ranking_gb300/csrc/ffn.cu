@@ -508,6 +508,17 @@ REC_ATTN_API rec_attn_status rec_attn_dense_device_status(int32_t* status_out, v
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(&s, word, sizeof s, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && s != REC_ATTN_OK) {  // reported: later calls start anew (while it was set, no other error was kept)
+    e = cudaMemsetAsync(word, 0, sizeof s, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
   if (e == cudaSuccess) *status_out = s;
   return from_cuda(e);
+}
+
+REC_ATTN_API rec_attn_status rec_attn_check_dense_wait_timeout(uint32_t limit_ms, void* stream) {
+  if (limit_ms < 1 || limit_ms > 10000) return REC_ATTN_ERR_INVALID_ARG;
+  int* const word = dense_status();
+  if (!word) return REC_ATTN_ERR_CUDA;
+  return from_cuda(launch_wait_timeout(word, limit_ms * 1000000ull, static_cast<cudaStream_t>(stream)));
 }

@@ -473,11 +473,18 @@ rec_attn_status rec_attn_ffn_scaled_fwd(int32_t activation, int64_t rows, int64_
 
 /*
  * rec_attn_dense_device_status -- the first error (rec_attn_status) that a kernel of the
- * feed-forward and scaled calls recorded on the current device: OK, or TIMEOUT when a kernel's
- * bounded wait ran out (its outputs are then not complete).  Synchronizes `stream`.
+ * feed-forward and scaled calls recorded on the current device since one was last reported: OK, or
+ * TIMEOUT when a kernel's bounded wait ran out (its outputs are then not complete).  Reporting an
+ * error clears it, so that later calls are told by themselves.  The calls of all streams of the
+ * device share the word; `stream` is synchronized: the calls enqueued on it before are finished.
  * Errors: INVALID_ARG, CUDA.
+ *
+ * rec_attn_check_dense_wait_timeout -- self-check of that report: rec_attn_check_wait_timeout's wait
+ * (limit_ms 1..10000) on the current device's word of these calls, which then holds TIMEOUT if it
+ * held no error.  Asynchronous.  Errors: INVALID_ARG, CUDA.
  */
 rec_attn_status rec_attn_dense_device_status(int32_t* status_out, void* stream);
+rec_attn_status rec_attn_check_dense_wait_timeout(uint32_t limit_ms, void* stream);
 
 /*
  * rec_attn_fwd_compress -- rec_attn_fwd whose output is written already compressed:
