@@ -45,11 +45,11 @@ struct Cfg {
   static constexpr int kTileN = kPair ? BN / 2 : BN;  // columns of the result
   // Warps of the epilogue: 16 where it computes the activation (of kDglu 901 us with 8)
   static constexpr int kEpiWarps = kPair ? 16 : 8, kThreads = 128 + 32 * kEpiWarps;
-  // kDglu: registers a thread, as the block is launched, and then of the loading and issuing warpgroup and of
-  // the four that hold g, u and dh
+  // Registers a thread, as the block is launched (what an SM has for it); kDglu: then of the loading and issuing
+  // warpgroup and of the four that hold g, u and dh
   static constexpr bool kSplitRegs = OP == DenseOp::kDglu;
-  static constexpr int kRegs = 96, kFewRegs = 32, kSumRegs = 112;
-  static_assert(128 * kFewRegs + 512 * kSumRegs <= 640 * kRegs, "the split is the block's own");
+  static constexpr int kRegs = 65536 / kThreads / 8 * 8, kFewRegs = 32, kSumRegs = 112;
+  static_assert(!kSplitRegs || 128 * kFewRegs + 512 * kSumRegs <= kThreads * kRegs, "the split is the block's own");
   static constexpr int kTileM = kTile * CG;
   static constexpr int kBRows = BN / CG;               // of B in this CTA
   static constexpr int kStage = 2 * kSlab + kBRows * 128;
@@ -278,7 +278,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
 }
 
 template <DenseOp OP, int BN, int CG, int ACT>
-__global__ void __launch_bounds__(Cfg<OP, BN, CG>::kThreads, 1)
+__global__ void __maxnreg__((Cfg<OP, BN, CG>::kRegs))
     k_dense(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
             const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2, const DenseArgs a) {
   using C = Cfg<OP, BN, CG>;
@@ -355,7 +355,8 @@ cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN, CG, ACT>, C::kDynamic);
   if (e != cudaSuccess) return e;
-  if (C::kSplitRegs && !launched_with(k_dense<OP, BN, CG, ACT>, C::kRegs)) return cudaErrorInvalidConfiguration;
+  static std::atomic<int> regs{0};
+  if (C::kSplitRegs && !launched_with(regs, (const void*)k_dense<OP, BN, CG, ACT>, C::kRegs)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + (OP == DenseOp::kDw ? a.pad : 0) + C::kTileM - 1) / C::kTileM;
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;

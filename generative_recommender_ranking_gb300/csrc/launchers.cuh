@@ -2,8 +2,6 @@
 #pragma once
 
 #include <atomic>
-#include <map>
-#include <mutex>
 
 #include <cuda.h>
 
@@ -62,23 +60,18 @@ cudaError_t launch_pairs(int cluster, bool early, void (*fn)(P...), int blocks, 
   return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
 
-// Whether a kernel's threads are launched with so many registers (asked once a kernel: one that splits more
-// among its warpgroups than it was launched with would wait for them forever).
-template <typename... P>
-bool launched_with(void (*fn)(P...), int regs) {
-  static std::mutex mu;
-  static std::map<void (*)(P...), int> known;
-  std::lock_guard<std::mutex> lk(mu);
-  const auto it = known.find(fn);
-  if (it != known.end()) return it->second == regs;
-  cudaFuncAttributes at{};
-  const OutsideCapture now;
-  if (cudaFuncGetAttributes(&at, fn) != cudaSuccess) return false;
-  try {
-    known[fn] = at.numRegs;
-  } catch (...) {  // asked again by the next call
+// Whether a kernel's threads are launched with so many registers (asked once, kept in `known`): one that splits more
+// among its warpgroups than it was launched with would wait for them forever.  The kernels ask for theirs by
+// __maxnreg__, so this says no only if a compiler gives them fewer.
+inline bool launched_with(std::atomic<int>& known, const void* fn, int regs) {
+  int n = known.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaFuncAttributes at{};
+    const OutsideCapture now;
+    if (cudaFuncGetAttributes(&at, fn) != cudaSuccess) return false;
+    known.store(n = at.numRegs, std::memory_order_relaxed);
   }
-  return at.numRegs == regs;
+  return n == regs;
 }
 
 // prologue_ok (may be null) is recorded on st once the RoPE prologue, on another stream,

@@ -376,7 +376,7 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
 }
 
 template <bool GATED, int ACT, bool PARTS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __maxnreg__(kRegs)
     k_scaled(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const ScaledArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kBars];
@@ -434,7 +434,8 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, ScaledArgs a, int 
   const cudaError_t e = allow_smem(done, (const void*)k_scaled<GATED, ACT, PARTS>, kDynamic);
   if (e != cudaSuccess) return e;
   const int tn = GATED ? kBN / 2 : kBN;
-  if (!launched_with(k_scaled<GATED, ACT, PARTS>, kRegs)) return cudaErrorInvalidConfiguration;
+  static std::atomic<int> regs{0};
+  if (!launched_with(regs, (const void*)k_scaled<GATED, ACT, PARTS>, kRegs)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + 2 * kTile - 1) / (2 * kTile);
   a.tiles_n = (a.N + tn - 1) / tn;
   const int tiles = a.tiles_m * a.tiles_n * (PARTS ? a.splits : 1), places = num_sms / 2;
