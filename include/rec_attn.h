@@ -419,8 +419,8 @@ rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows, int64_t widt
  * Workspace from the library pool on `stream`, in bytes (hidden rounded up to 16): forward, bf16 2 * rows * hidden, fp32 6 times
  * the elements of x, both weights and h (up to 8 rows: 4 * rows * hidden); backward, bf16 6 * rows *
  * hidden, fp32 6 times the elements of x, dy, both weights and p and h (3 * rows * hidden); and where
- * results have few tiles of 256 x 256, fp32 sums of parts of their summed axis, up to 64 times the
- * result.
+ * results have few tiles of 256 x 256 (fp32: 256 x 128), fp32 sums of parts of their summed axis: up to
+ * 64 (fp32: half the number of SMs) times the elements of the largest result that is summed so, 4 bytes each.
  * Asynchronous; both calls may be captured into a CUDA graph.
  * Errors: INVALID_ARG, UNSUPPORTED (too large), OOM, CUDA; a wait that ran out is reported by
  * rec_attn_dense_device_status.
