@@ -66,7 +66,7 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
       if (!bounded_wait_warp(bars + kEmpty + st, ((n / kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (ptx::elect_one()) {
         uint8_t* s = sm + st * kStage;
-        const uint32_t bar = ptx::first_of_pair<2>(bars + kFull + st);
+        const uint32_t bar = ptx::first_of_pair(bars + kFull + st);
         const bool grad = OP == DenseOp::kDglu && kb < 0;
         // (the first CTA's barrier counts the bytes of both; dh has 64 columns, 32 rows of B from each)
         if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * kStage);
@@ -110,7 +110,7 @@ __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s) {
   for (int j = 0; j < 6; ++j)
 #pragma unroll
     for (int k = 0; k < kBK / 16; ++k)
-      ptx::umma_pair<2, false>(acc, ptx::smem_desc_at(da, kA[j] * kStepA + k * (AMN ? 2048 : 32)),
+      ptx::umma_pair<false>(acc, ptx::smem_desc_at(da, kA[j] * kStepA + k * (AMN ? 2048 : 32)),
                                ptx::smem_desc_at(db, kB[j] * kSlab + k * (BMN ? 2048 : 32)), idesc, j + k > 0);
 }
 
@@ -132,15 +132,15 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
       if (el) {
         if (OP == DenseOp::kDglu && kb < 0) block_mma<false, true, 64>(tmem + buf * kTileN, s0 + st * kStage);
         else block_mma<C::kAMn, C::kBMn, kTileN>(tmem + buf * kTileN, s0 + st * kStage);
-        ptx::umma_commit_pair<2>(bars + kEmpty + st);
-        ptx::umma_commit_pair<2>(bars + kAccFull + buf);
+        ptx::umma_commit_pair(bars + kEmpty + st);
+        ptx::umma_commit_pair(bars + kAccFull + buf);
       }
       __syncwarp();
     }
   }
 out:
   if (el) {
-    ptx::umma_commit_pair<2>(bars + kDone);
+    ptx::umma_commit_pair(bars + kDone);
     bounded_drain(bars + kDone, 0, kWaitNs / 4);
   }
   __syncwarp();
@@ -222,7 +222,7 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   // its columns of the tile: two runs (gated: of the gate's and of up's)
   const int c0 = C::kPair ? kRun * part : 2 * kRun * part, c1 = C::kPair ? 64 + c0 : c0 + kRun;
-  const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
+  const uint32_t empty = ptx::first_of_pair(bars + kAccEmpty);
   uint32_t n = 0;
   // a block's sums of a run, added up
   const auto take = [&](float (&to)[kRun], uint32_t buf, int col) {
@@ -234,7 +234,7 @@ __device__ void finish(const Dense32Args& aa, uint64_t* bars, uint32_t tmem, vol
   const auto taken = [&](uint32_t buf) {
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
+    if (lane == 0) ptx::mbar_arrive_pair(empty + 8 * buf);
   };
   for (Units<C::kCols, DenseArgs> units(a, rank); units.left(); units.next()) {
     const Unit u = units.get();
@@ -313,12 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 1) ptx::tmem_alloc_pair<2>(&tmem_slot, kTmem);
+  if (warp == 1) ptx::tmem_alloc_pair(&tmem_slot, kTmem);
   ptx::tc_fence_before();
   __syncthreads();
-  ptx::pair_sync<2>();  // both CTAs' barriers are there
+  ptx::cluster_sync();  // both CTAs' barriers are there
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_slot, rank = ptx::pair_rank<2>();
+  const uint32_t tmem = tmem_slot, rank = ptx::cluster_rank();
   ptx::successor_may_start();
   ptx::predecessor_done();
   if (warp == 0) produce<OP>(a.d, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
@@ -329,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // nothing of one CTA's reaches into the other any more, the last commit too
   if (warp == 1 && rank == 1 && lane == 0) bounded_drain(bars + kDone, 0, kWaitNs / 4);
   __syncwarp();
-  ptx::pair_sync<2>();
+  ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc_pair<2>(tmem, kTmem);
+    ptx::tmem_dealloc_pair(tmem, kTmem);
   }
 }
 

@@ -36,13 +36,13 @@ __device__ int g_dense_status;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kBK = 64;                      // a block along the summed axis: 128 bytes
 constexpr int kSlab = 64 * 128;              // 64 rows of 128 bytes
+constexpr int kBN = 256;                     // columns of B a tile; a CTA loads 128 rows of either operand
 
-template <DenseOp OP, int BN, int CG>
+template <DenseOp OP>
 struct Cfg {
-  static_assert(BN == 256 && CG == 2, "a CTA loads 128 rows of either operand");
   static constexpr bool kPair = OP == DenseOp::kGlu || OP == DenseOp::kDglu;  // gate and up columns
   static constexpr bool kAMn = OP == DenseOp::kDw, kBMn = OP == DenseOp::kDx || OP == DenseOp::kDw;
-  static constexpr int kTileN = kPair ? BN / 2 : BN;  // columns of the result
+  static constexpr int kTileN = kPair ? kBN / 2 : kBN;  // columns of the result
   // Warps of the epilogue: 16 where it computes the activation (of kDglu 901 us with 8)
   static constexpr int kEpiWarps = kPair ? 16 : 8, kThreads = 128 + 32 * kEpiWarps;
   // Registers a thread, as the block is launched (what an SM has for it); kDglu: then of the loading and issuing
@@ -50,12 +50,12 @@ struct Cfg {
   static constexpr bool kSplitRegs = OP == DenseOp::kDglu;
   static constexpr int kRegs = 65536 / kThreads / 8 * 8, kFewRegs = 32, kSumRegs = 112;
   static_assert(!kSplitRegs || 128 * kFewRegs + 512 * kSumRegs <= kThreads * kRegs, "the split is the block's own");
-  static constexpr int kTileM = kTile * CG;
-  static constexpr int kBRows = BN / CG;               // of B in this CTA
+  static constexpr int kTileM = 2 * kTile;
+  static constexpr int kBRows = kBN / 2;               // of B in this CTA
   static constexpr int kStage = 2 * kSlab + kBRows * 128;
   static constexpr int kStages = 6 * 32 * 1024 / kStage;
   static constexpr int kDynamic = kStages * kStage + 1024;
-  static constexpr uint32_t kTmem = 2 * BN;  // kDglu: g, u and two buffers of dh
+  static constexpr uint32_t kTmem = 2 * kBN;  // kDglu: g, u and two buffers of dh
 };
 
 // Barriers
@@ -65,19 +65,19 @@ enum { kFull = 0, kEmpty = 8, kAccFull = 16, kAccEmpty = 18, kGuEmpty = 20, kDon
 // 128 rows of one operand at mn0 (MN: `rows` columns of it, a multiple of 64), block kb of the summed axis.  One
 // copy where a box can hold them: the loading warp needs about 100 cycles a copy (measured: 394 for a block's
 // four copies of 64 rows, which bounded the kernels at 570 cycles a block).
-template <bool MN, int CG>
+template <bool MN>
 __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int mn0, int rows, int kb, uint32_t bar) {
   if (MN) {
-    for (int i = 0; i < rows / 64; ++i) ptx::tma_load_2d_pair<CG>(dst + i * kSlab, map, mn0 + 64 * i, kb * kBK, bar);
+    for (int i = 0; i < rows / 64; ++i) ptx::tma_load_2d_pair(dst + i * kSlab, map, mn0 + 64 * i, kb * kBK, bar);
   } else {
-    ptx::tma_load_2d_pair<CG>(dst, map, kb * kBK, mn0, bar);
+    ptx::tma_load_2d_pair(dst, map, kb * kBK, mn0, bar);
   }
 }
 
-template <DenseOp OP, int BN, int CG>
+template <DenseOp OP>
 __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* ma2,
                         const CUtensorMap* mb2, uint8_t* sm, uint64_t* bars, volatile int* abort_flag, uint32_t rank, int lane) {
-  using C = Cfg<OP, BN, CG>;
+  using C = Cfg<OP>;
   uint32_t n = 0;
   for (Units<C::kTileN, DenseArgs> units(a, rank); units.left(); units.next()) {
     const Unit u = units.get();
@@ -87,24 +87,24 @@ __device__ void produce(const DenseArgs& a, const CUtensorMap* ma, const CUtenso
       if (!bounded_wait_warp(bars + kEmpty + st, ((n / C::kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (ptx::elect_one()) {
         uint8_t* s = sm + st * C::kStage;
-        const uint32_t bar = ptx::first_of_pair<CG>(bars + kFull + st);
+        const uint32_t bar = ptx::first_of_pair(bars + kFull + st);
         const bool grad = OP == DenseOp::kDglu && kb < 0;
         // (the first CTA's barrier counts the bytes of both)
-        if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, CG * (grad ? 2 * kSlab + C::kBRows * 64 : C::kStage));
+        if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * (grad ? 2 * kSlab + C::kBRows * 64 : C::kStage));
         // kDx where p's halves do not adjoin: its second half and the up projection have maps of their own
         const int half = OP == DenseOp::kDx && a.pad ? (a.cut + kBK - 1) / kBK : INT32_MAX;
         if (OP == DenseOp::kDx && kb >= half) {
-          load_operand<false, CG>(s, ma2, u.m0, kTile, kb - half, bar);
-          load_operand<true, CG>(s + 2 * kSlab, mb2, u.n0 + (int)rank * C::kBRows, C::kBRows, kb - half, bar);
+          load_operand<false>(s, ma2, u.m0, kTile, kb - half, bar);
+          load_operand<true>(s + 2 * kSlab, mb2, u.n0 + (int)rank * C::kBRows, C::kBRows, kb - half, bar);
         } else if (grad) {
-          load_operand<false, CG>(s, ma2, u.m0, kTile, kb + first, bar);
-          load_operand<true, CG>(s + 2 * kSlab, mb2, u.n0 + (int)rank * (C::kBRows / 2), C::kBRows / 2, kb + first, bar);
+          load_operand<false>(s, ma2, u.m0, kTile, kb + first, bar);
+          load_operand<true>(s + 2 * kSlab, mb2, u.n0 + (int)rank * (C::kBRows / 2), C::kBRows / 2, kb + first, bar);
         } else {
-          load_operand<C::kAMn, CG>(s, ma, u.m0, kTile, kb, bar);
+          load_operand<C::kAMn>(s, ma, u.m0, kTile, kb, bar);
           if (C::kPair) {  // the gate's columns are the first CTA's rows of B, up's the second's
-            load_operand<false, CG>(s + 2 * kSlab, mb, (rank ? a.N : 0) + u.n0, C::kBRows, kb, bar);
+            load_operand<false>(s + 2 * kSlab, mb, (rank ? a.N : 0) + u.n0, C::kBRows, kb, bar);
           } else {
-            load_operand<C::kBMn, CG>(s + 2 * kSlab, mb, u.n0 + (int)rank * C::kBRows, C::kBRows, kb, bar);
+            load_operand<C::kBMn>(s + 2 * kSlab, mb, u.n0 + (int)rank * C::kBRows, C::kBRows, kb, bar);
           }
         }
       }
@@ -130,17 +130,17 @@ __device__ __forceinline__ uint64_t step(uint64_t desc, int k) {
   return ptx::smem_desc_at(desc, k * (MN ? 16 * 128 : 32));
 }
 
-template <bool AMN, bool BMN, int N, int CG>
+template <bool AMN, bool BMN, int N>
 __device__ __forceinline__ void block_mma(uint32_t acc, uint32_t s, bool fresh) {
-  const uint32_t idesc = ptx::idesc_bf16_f32(kTile * CG, N, AMN, BMN);
+  const uint32_t idesc = ptx::idesc_bf16_f32(2 * kTile, N, AMN, BMN);
   const uint64_t da = operand<AMN>(s), db = operand<BMN>(s + 2 * kSlab);
 #pragma unroll
-  for (int k = 0; k < kBK / 16; ++k) ptx::umma_pair<CG, false>(acc, step<AMN>(da, k), step<BMN>(db, k), idesc, !fresh || k > 0);
+  for (int k = 0; k < kBK / 16; ++k) ptx::umma_pair<false>(acc, step<AMN>(da, k), step<BMN>(db, k), idesc, !fresh || k > 0);
 }
 
-template <DenseOp OP, int BN, int CG>
+template <DenseOp OP>
 __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tmem, volatile int* abort_flag) {
-  using C = Cfg<OP, BN, CG>;
+  using C = Cfg<OP>;
   const uint32_t s0 = ptx::smem_u32(sm);
   const bool el = ptx::elect_one();
   constexpr uint32_t rank = 0;  // the first CTA issues for both
@@ -156,45 +156,45 @@ __device__ void issue(const DenseArgs& a, uint8_t* sm, uint64_t* bars, uint32_t 
         if (!bounded_wait_warp(bars + kFull + st, (n / C::kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
         ptx::tc_fence_after();
         if (el) {
-          block_mma<false, true, BN / 2, CG>(tmem + BN + buf * (BN / 2), s0 + st * C::kStage, kb == 0);
-          ptx::umma_commit_pair<CG>(bars + kEmpty + st);
+          block_mma<false, true, kBN / 2>(tmem + kBN + buf * (kBN / 2), s0 + st * C::kStage, kb == 0);
+          ptx::umma_commit_pair(bars + kEmpty + st);
         }
         __syncwarp();
       }
       if (!bounded_wait_warp(bars + kGuEmpty, (it & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       ptx::tc_fence_after();
     }
-    const uint32_t acc = OP == DenseOp::kDglu ? tmem : tmem + buf * BN;
+    const uint32_t acc = OP == DenseOp::kDglu ? tmem : tmem + buf * kBN;
     for (int kb = u.kb0; kb < u.kb1; ++kb, ++n) {
       const int st = n % C::kStages;
       if (!bounded_wait_warp(bars + kFull + st, (n / C::kStages) & 1, abort_flag, a.status, kWaitNs)) goto out;
       ptx::tc_fence_after();
       if (el) {
-        block_mma<C::kAMn, C::kBMn, BN, CG>(acc, s0 + st * C::kStage, kb == u.kb0);
-        ptx::umma_commit_pair<CG>(bars + kEmpty + st);
+        block_mma<C::kAMn, C::kBMn, kBN>(acc, s0 + st * C::kStage, kb == u.kb0);
+        ptx::umma_commit_pair(bars + kEmpty + st);
       }
       __syncwarp();
     }
-    if (el) ptx::umma_commit_pair<CG>(bars + kAccFull + buf);
+    if (el) ptx::umma_commit_pair(bars + kAccFull + buf);
     __syncwarp();
   }
 out:
   if (el) {
-    ptx::umma_commit_pair<CG>(bars + kDone);
+    ptx::umma_commit_pair(bars + kDone);
     bounded_drain(bars + kDone, 0, kWaitNs / 4);
   }
   __syncwarp();
 }
 
 // ------------------------------------------------------------------ epilogues
-template <DenseOp OP, int BN, int CG, int ACT>
+template <DenseOp OP, int ACT>
 __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volatile int* abort_flag, uint32_t rank, int warp,
                        int lane) {
-  using C = Cfg<OP, BN, CG>;
+  using C = Cfg<OP>;
   const int quad = warp & 3, part = (warp - 4) >> 2;
   constexpr int kCols = C::kTileN * 4 / C::kEpiWarps;  // of the result, a warp's share
   constexpr int kStep = C::kPair ? 16 : 32;
-  const uint32_t empty = ptx::first_of_pair<CG>(bars + kAccEmpty), gu_empty = ptx::first_of_pair<CG>(bars + kGuEmpty);
+  const uint32_t empty = ptx::first_of_pair(bars + kAccEmpty), gu_empty = ptx::first_of_pair(bars + kGuEmpty);
   uint32_t it = 0;
   for (Units<C::kTileN, DenseArgs> units(a, rank); units.left(); units.next(), ++it) {
     const Unit u = units.get();
@@ -207,18 +207,18 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
     const auto give_back = [&](uint32_t bar) {
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_pair<CG>(bar);
+      if (lane == 0) ptx::mbar_arrive_pair(bar);
     };
     if constexpr (OP == DenseOp::kDglu) {
       // g and u of all of the warp's columns leave their only buffer at once, so that the next tile's can be
       // summed into it; dh, which has two, is read 16 columns at a time.
       uint32_t gu[64];
-      ptx::tmem_ld2x32(lanes, lanes + BN / 2, gu);
+      ptx::tmem_ld2x32(lanes, lanes + kBN / 2, gu);
       give_back(gu_empty);
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
         uint32_t d[16], wg[8], wu[8], wh[8];
-        ptx::tmem_ld16(lanes + BN + buf * (BN / 2) + c, d);
+        ptx::tmem_ld16(lanes + kBN + buf * (kBN / 2) + c, d);
         if (c + 16 >= kCols) give_back(empty + 8 * buf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -246,7 +246,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
       const bool in = row < a.M && left > 0;
       if constexpr (OP == DenseOp::kGlu) {
         uint32_t gu[32], w[8];
-        ptx::tmem_ld2x16(lanes + buf * BN + c, lanes + buf * BN + BN / 2 + c, gu);
+        ptx::tmem_ld2x16(lanes + buf * kBN + c, lanes + buf * kBN + kBN / 2 + c, gu);
         if (c + kStep >= kCols) give_back(empty + 8 * buf);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -255,7 +255,7 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
         if (in) store_bf16(static_cast<__nv_bfloat16*>(a.out) + row * (a.N + a.pad) + col, w, left, a.wide);
       } else {
         uint32_t r[32];
-        ptx::tmem_ld32(lanes + buf * BN + c, r);
+        ptx::tmem_ld32(lanes + buf * kBN + c, r);
         if (c + kStep >= kCols) give_back(empty + 8 * buf);
         if (a.splits > 1) {
           if (in) {
@@ -277,11 +277,11 @@ __device__ void finish(const DenseArgs& a, uint64_t* bars, uint32_t tmem, volati
   }
 }
 
-template <DenseOp OP, int BN, int CG, int ACT>
-__global__ void __maxnreg__((Cfg<OP, BN, CG>::kRegs))
+template <DenseOp OP, int ACT>
+__global__ void __maxnreg__((Cfg<OP>::kRegs))
     k_dense(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
             const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2, const DenseArgs a) {
-  using C = Cfg<OP, BN, CG>;
+  using C = Cfg<OP>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ int s_abort;
@@ -296,40 +296,39 @@ __global__ void __maxnreg__((Cfg<OP, BN, CG>::kRegs))
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars + kAccFull + i, 1);
-      ptx::mbar_init(bars + kAccEmpty + i, CG * C::kEpiWarps);
+      ptx::mbar_init(bars + kAccEmpty + i, 2 * C::kEpiWarps);
     }
-    ptx::mbar_init(bars + kGuEmpty, CG * C::kEpiWarps);
+    ptx::mbar_init(bars + kGuEmpty, 2 * C::kEpiWarps);
     ptx::mbar_init(bars + kDone, 1);
     s_abort = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 1) ptx::tmem_alloc_pair<CG>(&tmem_slot, C::kTmem);
+  if (warp == 1) ptx::tmem_alloc_pair(&tmem_slot, C::kTmem);
   ptx::tc_fence_before();
   __syncthreads();
-  if (CG == 2) ptx::pair_sync<CG>();  // both CTAs' barriers are there
+  ptx::cluster_sync();  // both CTAs' barriers are there
   ptx::tc_fence_after();
-  const uint32_t rank = ptx::pair_rank<CG>();
+  const uint32_t rank = ptx::cluster_rank();
   ptx::successor_may_start();
   if (a.follows) ptx::predecessor_done();
   const uint32_t tmem = tmem_slot;
   if (warp < 4) {
     if (C::kSplitRegs) ptx::fewer_registers<C::kFewRegs>();
-    if (warp == 0) produce<OP, BN, CG>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
-    else if (warp == 1 && rank == 0) issue<OP, BN, CG>(a, sm, bars, tmem, abort_flag);
+    if (warp == 0) produce<OP>(a, &ma, &mb, &ma2, &mb2, sm, bars, abort_flag, rank, lane);
+    else if (warp == 1 && rank == 0) issue<OP>(a, sm, bars, tmem, abort_flag);
   } else {
     if (C::kSplitRegs) ptx::more_registers<C::kSumRegs>();
-    finish<OP, BN, CG, ACT>(a, bars, tmem, abort_flag, rank, warp, lane);
+    finish<OP, ACT>(a, bars, tmem, abort_flag, rank, warp, lane);
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (CG == 2) {  // nothing of one CTA's reaches into the other any more, the last commit too
-    if (warp == 1 && rank == 1 && lane == 0) bounded_drain(bars + kDone, 0, kWaitNs / 4);
-    __syncwarp();
-    ptx::pair_sync<CG>();
-  }
+  // nothing of one CTA's reaches into the other any more, the last commit too
+  if (warp == 1 && rank == 1 && lane == 0) bounded_drain(bars + kDone, 0, kWaitNs / 4);
+  __syncwarp();
+  ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc_pair<CG>(tmem, C::kTmem);
+    ptx::tmem_dealloc_pair(tmem, C::kTmem);
   }
 }
 
@@ -349,19 +348,19 @@ __global__ void k_dense_sum(const float* part, void* out, long long n, int split
   else reinterpret_cast<float4*>(out)[i / 4] = s;
 }
 
-template <DenseOp OP, int BN, int CG, int ACT>
+template <DenseOp OP, int ACT>
 cudaError_t run(const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
-  using C = Cfg<OP, BN, CG>;
+  using C = Cfg<OP>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, BN, CG, ACT>, C::kDynamic);
+  const cudaError_t e = allow_smem(done, (const void*)k_dense<OP, ACT>, C::kDynamic);
   if (e != cudaSuccess) return e;
   static std::atomic<int> regs{0};
-  if (C::kSplitRegs && !launched_with(regs, (const void*)k_dense<OP, BN, CG, ACT>, C::kRegs)) return cudaErrorInvalidConfiguration;
+  if (C::kSplitRegs && !launched_with(regs, (const void*)k_dense<OP, ACT>, C::kRegs)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + (OP == DenseOp::kDw ? a.pad : 0) + C::kTileM - 1) / C::kTileM;
   a.tiles_n = (a.N + C::kTileN - 1) / C::kTileN;
   const long long units = (long long)a.tiles_m * a.tiles_n * a.splits;
-  const int places = num_sms / CG;
-  return launch_pairs(CG, a.follows != 0, k_dense<OP, BN, CG, ACT>, (int)(units < places ? units : places) * CG,
+  const int places = num_sms / 2;
+  return launch_pairs(2, a.follows != 0, k_dense<OP, ACT>, (int)(units < places ? units : places) * 2,
                       C::kThreads, C::kDynamic, st, m[0], m[1], m[2], m[3], a);
 }
 
@@ -411,14 +410,14 @@ cudaError_t launch_dense_sum(const float* part, void* out, long long n, int spli
 cudaError_t launch_dense(DenseOp op, const CUtensorMap (&m)[4], DenseArgs a, int num_sms, cudaStream_t st) {
   switch (op) {
     case DenseOp::kGlu:
-      return a.act == REC_ATTN_SILU ? run<DenseOp::kGlu, 256, 2, REC_ATTN_SILU>(m, a, num_sms, st)
-                                    : run<DenseOp::kGlu, 256, 2, REC_ATTN_GELU>(m, a, num_sms, st);
+      return a.act == REC_ATTN_SILU ? run<DenseOp::kGlu, REC_ATTN_SILU>(m, a, num_sms, st)
+                                    : run<DenseOp::kGlu, REC_ATTN_GELU>(m, a, num_sms, st);
     case DenseOp::kDglu:
-      return a.act == REC_ATTN_SILU ? run<DenseOp::kDglu, 256, 2, REC_ATTN_SILU>(m, a, num_sms, st)
-                                    : run<DenseOp::kDglu, 256, 2, REC_ATTN_GELU>(m, a, num_sms, st);
-    case DenseOp::kOut: return run<DenseOp::kOut, 256, 2, 0>(m, a, num_sms, st);
-    case DenseOp::kDx: return run<DenseOp::kDx, 256, 2, 0>(m, a, num_sms, st);
-    case DenseOp::kDw: return run<DenseOp::kDw, 256, 2, 0>(m, a, num_sms, st);
+      return a.act == REC_ATTN_SILU ? run<DenseOp::kDglu, REC_ATTN_SILU>(m, a, num_sms, st)
+                                    : run<DenseOp::kDglu, REC_ATTN_GELU>(m, a, num_sms, st);
+    case DenseOp::kOut: return run<DenseOp::kOut, 0>(m, a, num_sms, st);
+    case DenseOp::kDx: return run<DenseOp::kDx, 0>(m, a, num_sms, st);
+    case DenseOp::kDw: return run<DenseOp::kDw, 0>(m, a, num_sms, st);
   }
   return cudaErrorInvalidValue;
 }

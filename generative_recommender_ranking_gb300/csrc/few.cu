@@ -130,8 +130,8 @@ __device__ void issue(const FewArgs& a, uint8_t* sm, uint64_t* bars, uint32_t tm
         const uint64_t dw = ptx::smem_desc_sw128(s + m * kMat, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          ptx::umma_pair<1, E4M3>(tmem + (buf * C::kMats + m) * TOKENS, ptx::smem_desc_at(dw, 32 * k),
-                                  ptx::smem_desc_at(dx, 32 * k), idesc, k > 0 || (!E4M3 && n > 0));
+          (E4M3 ? ptx::umma_f8 : ptx::umma_f16)(tmem + (buf * C::kMats + m) * TOKENS, ptx::smem_desc_at(dw, 32 * k),
+                                                ptx::smem_desc_at(dx, 32 * k), idesc, k > 0 || (!E4M3 && n > 0));
       }
       ptx::umma_commit(bars + kEmpty + st);
       if (E4M3 || n == blocks - 1) ptx::umma_commit(bars + kAccFull + buf);
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = a.cluster > 1 ? (int)ptx::pair_rank<2>() : 0, n0 = (int)(blockIdx.x / a.cluster) * 128;
+  const int rank = a.cluster > 1 ? (int)ptx::cluster_rank() : 0, n0 = (int)(blockIdx.x / a.cluster) * 128;
   const int kb0 = a.kblocks * rank / a.cluster, kb1 = a.kblocks * (rank + 1) / a.cluster;
   const Loader<E4M3, GATED, TOKENS> in{a, &mw, &mx, sm, bars, n0, kb0};
   if (threadIdx.x == 0) {
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   else if (warp == 1) issue<E4M3, GATED, TOKENS>(a, sm, bars, tmem, abort_flag, kb1 - kb0);
   else collect<E4M3, GATED, TOKENS>(a, s_sum, bars, tmem, abort_flag, n0, kb0, kb1, warp, lane);
   __syncthreads();
-  if (a.cluster > 1) ptx::pair_sync<2>();
+  if (a.cluster > 1) ptx::cluster_sync();
   // a warp per token row: 128 columns, four a lane
   const int col = n0 + 4 * lane;
   for (int t = rank + a.cluster * warp; t < a.rows; t += a.cluster * (kThreads / 32)) {
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (a.cluster > 1) ptx::pair_sync<2>();  // no CTA leaves while another reads its sums
+  if (a.cluster > 1) ptx::cluster_sync();  // no CTA leaves while another reads its sums
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmem);

@@ -186,10 +186,10 @@ __device__ void produce(const ScaledArgs& a, const CUtensorMap* ma, const CUtens
       if (!bounded_wait_warp(bars + kEmpty + st, ((n / kStages) & 1) ^ 1, abort_flag, a.status, kWaitNs)) goto out;
       if (ptx::elect_one()) {
         uint8_t* s = sm + st * kStage;
-        const uint32_t bar = ptx::first_of_pair<2>(bars + kFull + st);
+        const uint32_t bar = ptx::first_of_pair(bars + kFull + st);
         if (rank == 0) ptx::mbar_arrive_expect_tx(bars + kFull + st, 2 * kStage);  // the bytes of both CTAs
-        ptx::tma_load_2d_pair<2>(s, ma, kb * 128, u.m0, bar);
-        ptx::tma_load_2d_pair<2>(s + kSlab, mb, kb * 128, nb, bar);
+        ptx::tma_load_2d_pair(s, ma, kb * 128, u.m0, bar);
+        ptx::tma_load_2d_pair(s + kSlab, mb, kb * 128, nb, bar);
       }
       __syncwarp();
     }
@@ -222,16 +222,16 @@ __device__ __forceinline__ void issue(const ScaledArgs& a, uint8_t* sm, uint64_t
         const uint64_t db = ptx::smem_desc_sw128(s0 + st * kStage + kSlab, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          ptx::umma_pair<2, true>(tmem + buf * kBN, ptx::smem_desc_at(da, 32 * k), ptx::smem_desc_at(db, 32 * k), idesc, k > 0);
-        ptx::umma_commit_pair<2>(bars + kEmpty + st);
-        ptx::umma_commit_pair<2>(bars + kAccFull + buf);
+          ptx::umma_pair<true>(tmem + buf * kBN, ptx::smem_desc_at(da, 32 * k), ptx::smem_desc_at(db, 32 * k), idesc, k > 0);
+        ptx::umma_commit_pair(bars + kEmpty + st);
+        ptx::umma_commit_pair(bars + kAccFull + buf);
       }
       __syncwarp();
     }
   }
 out:
   if (el) {
-    ptx::umma_commit_pair<2>(bars + kDone);
+    ptx::umma_commit_pair(bars + kDone);
     bounded_drain(bars + kDone, 0, kWaitNs / 4);
   }
   __syncwarp();
@@ -256,7 +256,7 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
   constexpr bool kEarly = !GATED && !PARTS, kFirst = !PARTS;
   const int quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (GATED ? 32 : 64) * part;
-  const uint32_t empty = ptx::first_of_pair<2>(bars + kAccEmpty);
+  const uint32_t empty = ptx::first_of_pair(bars + kAccEmpty);
   const bool aligned = (a.kblocks & 3) == 0;  // (a.a_scale is on a 16-byte boundary)
   Work<GATED, PARTS> work(a, rank);
   // the tile, this thread's row of it, and the scales of the row and of its first and second 32 columns' block
@@ -303,7 +303,7 @@ __device__ void finish(const ScaledArgs& a, uint64_t* bars, uint32_t tmem, volat
         if (c == 1) {  // the buffer goes back before its last columns are added
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_pair<2>(empty + 8 * buf);
+          if (lane == 0) ptx::mbar_arrive_pair(empty + 8 * buf);
         }
         const f32x2 f = GATED && c ? pair_of(f1, f1) : pair_of(f0, f0);
 #pragma unroll
@@ -400,12 +400,12 @@ __global__ void __maxnreg__(kRegs)
     s_abort = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 1) ptx::tmem_alloc_pair<2>(&tmem_slot, kTmem);
+  if (warp == 1) ptx::tmem_alloc_pair(&tmem_slot, kTmem);
   ptx::tc_fence_before();
   __syncthreads();
-  ptx::pair_sync<2>();  // both CTAs' barriers are there
+  ptx::cluster_sync();  // both CTAs' barriers are there
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_slot, rank = ptx::pair_rank<2>();
+  const uint32_t tmem = tmem_slot, rank = ptx::cluster_rank();
   ptx::successor_may_start();
   if (a.follows) ptx::predecessor_done();
   if (warp < 4) {
@@ -421,10 +421,10 @@ __global__ void __maxnreg__(kRegs)
   // nothing of one CTA's reaches into the other any more, the last commit too
   if (warp == 1 && rank == 1 && lane == 0) bounded_drain(bars + kDone, 0, kWaitNs / 4);
   __syncwarp();
-  ptx::pair_sync<2>();
+  ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc_pair<2>(tmem, kTmem);
+    ptx::tmem_dealloc_pair(tmem, kTmem);
   }
 }
 
