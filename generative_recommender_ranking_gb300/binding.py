@@ -362,10 +362,13 @@ def _dtypes() -> dict:
 def _rows(fn: str, x, **others):
     """(dtype, rows, width) of a contiguous [rows, width] tensor of the current device; the
     others must match it."""
+    if x is None:
+        raise RecAttnError(fn, ERR_INVALID_ARG)
     dtype, shape = (_DTYPES or _dtypes()).get(x.dtype), x.shape
     ok = len(shape) == 2 and dtype is not None and x.is_contiguous() and _here(x)
     for o in others.values():
-        ok = ok and o.dtype == x.dtype and o.shape == shape and o.get_device() == x.get_device() and o.is_contiguous()
+        ok = (ok and o is not None and o.dtype == x.dtype and o.shape == shape and o.get_device() == x.get_device()
+              and o.is_contiguous())
     if not ok:
         raise RecAttnError(fn, ERR_INVALID_ARG)
     return dtype, shape[0], shape[1]
@@ -470,7 +473,7 @@ def _scale_shape(shape, block_rows):
 
 
 def _on_device(fn: str, x) -> None:
-    if not (len(x.shape) == 2 and x.is_contiguous() and _here(x)):
+    if not (x is not None and len(x.shape) == 2 and x.is_contiguous() and _here(x)):
         raise RecAttnError(fn, ERR_INVALID_ARG)
 
 
