@@ -8,7 +8,7 @@
 // fp32 registers, rounded to nearest.
 // A pair of CTAs has a tile of 256 x 128 (gated: 64 gate and 64 up columns; the backward's dh 64); a
 // ring of three 64-deep stages holds all six planes, so each is loaded once.  h and p are written as
-// planes.  1850 rows of 512 x 1024, forward and backward, 148 us (elementary fp32 operations 454): 22 R W H
+// planes.  (kDglu spills 4 and 8 bytes at 96 registers a thread.)  1850 rows of 512 x 1024, forward and backward, 148 us (elementary fp32 operations 454): 22 R W H
 // multiplied by six is 68 us at the bf16 rate; the rest is eleven kernels of one or two tiles a pair, each with the
 // filling of its ring and an epilogue at its end.  7680 rows: tensor pipe 50 to 69%.
 #include <cuda_bf16.h>
@@ -395,7 +395,10 @@ cudaError_t launch_split(const SplitList& l, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Parts of the summed axis that give every pair of SMs work: each at least four blocks deep.
+// Parts of the summed axis that give every pair of SMs work: each at least four blocks deep.  (At least one, two, four,
+// eight and sixteen blocks, us on the device: forward of 500 rows of 128 x 4096 32.3, 26.7, 25.7, 27.6, 33.4; of 200 rows of
+// 512 x 1024 26.1, 25.2, 26.3, 29.0, 33.8; with backward, 200 rows of 128 x 4096 86.6, 73.6, 68.8, 71.6, 82.5, 4000 rows of
+// 256 x 256 88.0, 86.1, 78.2, 82.2, 99.8, 1850 of 512 x 1024 137, 137, 137, 138, 162.)
 int dense32_splits(int M, int N, int kblocks, int num_sms) {
   const long long tiles = (long long)((M + 2 * kTile - 1) / (2 * kTile)) * ((N + kTileN - 1) / kTileN);
   long long s = num_sms / 2 / tiles;

@@ -10,7 +10,8 @@
 // The first weights of a product that follows another are fetched before that one has ended.
 // 24 rows of 4096 x 8192, both products: 41 us (4.9 TB/s), e4m3 30.5 with the quantizer (3.3 TB/s): about 6 us of
 // each kernel are its launch, its first copies' latency and the join; 67 and 134 MB take 15 and 26 us alone.  One
-// CTA an SM with 180 KB: 43; mma.sync from registers (thin.cu) with 24 rows: 61 and 59.
+// CTA an SM with 180 KB: 43; mma.sync from registers (thin.cu) with 24 rows: 61 and 59.  (The gated e4m3 form for more than
+// 32 rows holds 128 sums a thread and spills 28 bytes at 168 registers.)
 #include <cuda_bf16.h>
 
 #include <atomic>

@@ -3,8 +3,12 @@
 // Every weight is used once for each row, so the weights' bytes bound the time: a lane multiplies four
 // neighbouring values of a weight row with each token row; a block's eight warps share the summed axis
 // and are added up in their order.  Past eight rows the tensor cores take over
-// (dense_fp32.cu): on 4096 x 4096 they take 174 us for any number of rows up to 200, this way 16 rows a block 111 us for
+// (dense_fp32.cu): on 4096 x 4096 they take 168 us for nine rows and 170 for 64, this way 16 rows a block 111 us for
 // nine rows and 32 a block 477 for 24.
+// Both products, us on the device with the weights not in the L2: 512 x 1024, one, two, four and eight rows, 5.2, 5.3,
+// 8.7 and 10.6; 4096 x 4096 39.0, 39.1, 70.6 and 84.0 (201 MB: 30 at the copy's rate); 4096 x 8192 71, 72, 126 and 179 (403
+// MB: 59).  One row reads 5.0 and 4.2 TB/s under ncu; eight 2.6 and 1.6: two blocks an SM (94 to 124 registers a thread)
+// have too few loads on their way, and the warps wait for them.
 #include "dense_device.cuh"
 #include "few.cuh"
 #include "launchers.cuh"
