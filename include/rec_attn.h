@@ -412,7 +412,8 @@ rec_attn_status rec_attn_layernorm_bwd(int32_t dtype, int64_t rows, int64_t widt
  * again from x: nothing of the forward is kept.  Equal calls give equal bits.
  * bf16: operands of the tensor cores; outputs are off by about 2.4e-3 (relative), their own rounding
  * being 1.7e-3 of that.  fp32: three bf16 values stand for each operand and six of their products are
- * summed, in blocks of 64 that are added up in fp32: off by 3e-7.  x, dy and the weights must be
+ * summed, in blocks of 64 that are added up in fp32: off by 3e-7 (operands below 2^-109, h and p among them, keep
+ * 2^-133, which is fewer bits).  x, dy and the weights must be
  * finite for a finite result; a value that is not reaches its own row of y and dx, and dw_in and dw_out.
  * bf16 (and e4m3): silu's logistic function is cut by 2^-60, so it is zero from -41 down; gelu's Phi is off by 8e-7 at
  * most and below zero by 4e-4 of itself, and zero from -13.2 down.
@@ -449,7 +450,7 @@ rec_attn_status rec_attn_ffn_bwd(int32_t dtype, int32_t activation, int64_t rows
  * rec_attn_scaled_matmul -- y[m][n] = sum over blocks k of a_scale[m][k] b_scale[n / 128][k]
  *   times the sum over the block of a[m][.] b[n][.]: a [rows][depth] with a scale for each row's
  *   128 values, b [cols][depth] with one for each 128 x 128, any finite scales whose products are
- *   finite; y bf16 [rows][cols].  cols a multiple of 8, depth of 16, both at most 131072.  A
+ *   finite (their product is rounded to fp32: below 2^-126 it has fewer bits); y bf16 [rows][cols].  cols a multiple of 8, depth of 16, both at most 131072.  A
  *   block is summed by the tensor cores, the blocks in fp32; y is rounded once.
  *
  * rec_attn_ffn_scaled_fwd -- rec_attn_ffn_fwd for bf16 rows x and e4m3 weights

@@ -116,3 +116,24 @@ def test_fp32_precision_of_few_rows(built, rows, act):
         bd.rec_attn_ffn_fwd(x, wi, wo, y, activation=act)
         ref = block(lambda a, b: a @ b.T, x.double(), dy.double(), wi.double(), wo.double(), act)
         assert off(y, ref[0]) < BOUND
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F32], ids=["bf16", "fp32"])
+def test_small_gradients(built, dtype):
+    """The backward is linear in dy, and powers of two move no rounding: 2^-60 dy gives 2^-60 of each gradient, bit for
+    bit.  At 2^-108 fp32's last plane meets the end of bf16's range: p is of size one (times that), so 2^-133 is 2^-25 of it
+    and of dy; two operands and three products give less than 2^-22."""
+    x, dy, wi, wo = inputs(200, 136, 264, dtype, 3)
+
+    def gradients(e):
+        o = [torch.full_like(t, 7) for t in (x, wi, wo)]
+        bd.rec_attn_ffn_bwd(x, wi, wo, (dy.double() * 2.0**e).to(dtype), *o)
+        torch.cuda.synchronize()
+        return [t.double() * 2.0**-e for t in o]
+
+    full = gradients(0)
+    for got, want in zip(gradients(-60), full):
+        assert torch.equal(got, want)
+    for got, want in zip(gradients(-108), full):
+        assert off(got, want) < 2.0**-22
