@@ -44,6 +44,7 @@ struct Cfg {
   static constexpr int kStages = 108 * 1024 / kStage;  // two CTAs an SM
   static constexpr int kDynamic = kStages * kStage + 1024;
   static_assert(kStages * kStage >= kMats * TOKENS * 128 * 4, "the CTA's sums fit the ring");
+  static_assert(3 * kDynamic > 228 * 1024, "no more CTAs an SM than TMEM has columns for");
 };
 
 // Four floats of another CTA's shared memory, at this one's place `p`.
@@ -236,6 +237,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     ptx::fence_barrier_init();
     for (int j = 0; j < min(kb1 - kb0, C::kStages); ++j) in.weights(j);
   }
+  // (Before TMEM is taken: a successor's CTA on this SM may take its 256 columns first and wait for this kernel, but shared
+  // memory holds two CTAs of these kernels an SM at most, whose columns are 512 together.)
   ptx::successor_may_start();
   if (warp == 1) {
     ptx::tmem_alloc(&tmem_slot, kTmem);
